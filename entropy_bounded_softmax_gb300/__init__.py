@@ -19,7 +19,12 @@ from __future__ import annotations
 
 from . import _lib
 from ._lib import (CONSTANTS, cs_attention_softmax, cs_attention_softmax_ex,
-                   cs_biencoder_attention, cs_biencoder_attention_ex,
+                   cs_attention_shape, cs_biencoder_attention,
+                   cs_biencoder_attention_ex,
+                   cs_check_fused_attention_args,
+                   cs_check_fused_attention_backward_args,
+                   cs_fused_attention, cs_fused_attention_backward,
+                   cs_fused_attention_backward_workspace,
                    cs_check_biencoder_args, cs_plan_biencoder_host,
                    cs_check_args, cs_check_attention_args,
                    cs_check_backward_args, cs_constrained_softmax,
@@ -52,6 +57,10 @@ __all__ = [
     "biencoder_attention", "cs_biencoder_attention",
     "cs_biencoder_attention_ex", "cs_plan_biencoder_host",
     "cs_check_biencoder_args",
+    "fused_attention", "fused_attention_backward", "FusedAttentionFunction",
+    "cs_attention_shape", "cs_fused_attention", "cs_fused_attention_backward",
+    "cs_fused_attention_backward_workspace", "cs_check_fused_attention_args",
+    "cs_check_fused_attention_backward_args",
 ]
 
 # Defaults of section 2.1's signature.
@@ -316,6 +325,158 @@ def biencoder_attention(query, keys, values, scale=None,
     return res if len(res) > 1 else out
 
 
+def _heads_like(x):
+    """An uninitialised tensor of x's shape: in x's memory order where that is
+    one of a whole tensor's (so a [B, S, H, D] projection seen as
+    [B, H, S, D] keeps its order), else contiguous."""
+    import torch
+    return torch.empty_like(x)
+
+
+def _check_heads(name, x, shape=None, device=None) -> None:
+    import torch
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if x.dim() != 4:
+        raise ValueError(f"{name} must be 4-D [batch, heads, length, d_head]")
+    if device is not None and x.device != device:
+        raise ValueError(f"{name} must be on the query's device")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if x.numel() == 0:
+        return
+    st = x.stride()
+    if x.shape[3] > 1 and st[3] != 1:
+        raise ValueError(f"{name}'s head dimension must be contiguous")
+    if (x.data_ptr() % 16 or any(n > 1 and (s <= 0 or s % 8)
+                                 for n, s in zip(x.shape[:3], st[:3]))):
+        raise ValueError(f"{name}'s base must be 16-byte aligned and its "
+                         "batch, head and position strides positive multiples "
+                         "of 8 elements")
+
+
+def _attention_shape(query, keys, values, mask, causal, scale):
+    """The checked inputs of fused attention: (shape, mask pointer)."""
+    import math
+    import torch
+    _check_heads("query", query)
+    B, H, Sq, D = query.shape
+    _check_heads("keys", keys, device=query.device)
+    Hk, Sk = keys.shape[1], keys.shape[2]
+    if keys.shape[0] != B or keys.shape[3] != D:
+        raise ValueError("keys must be [batch, kv_heads, key_len, d_head] "
+                         "with the query's batch and d_head")
+    _check_heads("values", values, keys.shape, query.device)
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError("the query's heads must be a multiple of the keys'")
+    if D < 8 or D > 128 or D % 8:
+        raise ValueError("d_head must be a multiple of 8 in 8..128")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if not (scale > 0.0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
+    m_ptr, m_stride = None, Sk
+    if mask is not None:
+        if (not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool
+                or mask.device != query.device
+                or tuple(mask.shape) != (B, Sk)):
+            raise ValueError("mask must be a bool [batch, key_len] tensor on "
+                             "the query's device")
+        if ((Sk > 1 and mask.stride(1) != 1)
+                or (B > 1 and mask.stride(0) < Sk)):
+            raise ValueError("mask's rows must be contiguous and not overlap")
+        if mask.numel():
+            m_ptr, m_stride = mask.data_ptr(), mask.stride(0)
+    shape = cs_attention_shape(B, H, Hk, Sq, Sk, D, int(bool(causal)),
+                               float(scale), query.stride()[:3],
+                               keys.stride()[:3], values.stride()[:3])
+    shape.mask_stride = m_stride
+    return shape, m_ptr
+
+
+def _check_lse(lse, query) -> None:
+    import torch
+    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32
+            or lse.shape != query.shape[:3] or lse.device != query.device
+            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [batch, heads, "
+                         "query_len] tensor on the query's device")
+
+
+def fused_attention(query, keys, values, mask=None, causal: bool = False,
+                    scale=None, out=None, return_lse: bool = False):
+    """softmax(scale query keys^T) values over CUDA bf16 tensors, without the
+    scores in memory: query [B, H, Sq, D], keys and values [B, Hk, Sk, D],
+    H a multiple of Hk (head h reads key head h // (H // Hk)), D a multiple
+    of 8 up to 128.
+
+    ``mask`` is None or a bool [B, Sk] tensor, False for keys that no query
+    attends (padding; what they hold has no effect); ``causal`` keeps keys
+    j <= i + Sk - Sq for query i; ``scale`` defaults to 1/sqrt(D).  A query
+    without keys gets zeros.  Any strides that are multiples of 8 elements
+    over a contiguous head dimension are taken, [B, S, H, D] storage seen as
+    [B, H, S, D] among them.  Returns the output [B, H, Sq, D] in bf16, in
+    the query's memory order (or ``out``), and with ``return_lse`` the log of
+    the softmax's sums [B, H, Sq] in fp32 (-inf without keys), which
+    :func:`fused_attention_backward` takes.  Asynchronous on the current
+    stream; NaN or infinite scores propagate and are reported by
+    :func:`get_error`.
+    """
+    import torch
+    shape, m_ptr = _attention_shape(query, keys, values, mask, causal, scale)
+    if out is None:
+        out = _heads_like(query)
+    else:
+        _check_heads("out", out, query.shape, query.device)
+    shape.o_stride = out.stride()[:3]
+    lse = None
+    if return_lse:
+        lse = torch.empty(query.shape[:3], dtype=torch.float32,
+                          device=query.device)
+    with _on_device(query.device):
+        st = cs_fused_attention(
+            query.data_ptr(), keys.data_ptr(), values.data_ptr(),
+            out.data_ptr(), lse.data_ptr() if return_lse else None, m_ptr,
+            shape, _stream_handle(query.device))
+    if st != 0:
+        raise CsError(st, "cs_fused_attention")
+    return (out, lse) if return_lse else out
+
+
+def fused_attention_backward(query, keys, values, out, lse, grad_output,
+                             mask=None, causal: bool = False, scale=None):
+    """Gradients of :func:`fused_attention` with respect to query, keys and
+    values, given ``grad_output``, that of its output, and its ``out`` and
+    ``lse`` (``return_lse=True``).  The probabilities are recomputed; every
+    sum has a fixed order, so repeated calls give the same bits.  Returns
+    bf16 gradients in the memory order of their tensors; removed keys get
+    zeros.  Asynchronous on the current stream.
+    """
+    import torch
+    shape, m_ptr = _attention_shape(query, keys, values, mask, causal, scale)
+    _check_heads("out", out, query.shape, query.device)
+    _check_heads("grad_output", grad_output, query.shape, query.device)
+    _check_lse(lse, query)
+    grads = [_heads_like(x) for x in (query, keys, values)]
+    shape.o_stride = out.stride()[:3]
+    shape.go_stride = grad_output.stride()[:3]
+    shape.dq_stride, shape.dk_stride, shape.dv_stride = (
+        g.stride()[:3] for g in grads)
+    size = cs_fused_attention_backward_workspace(shape)
+    work = torch.empty(max(size, 0), dtype=torch.uint8, device=query.device)
+    with _on_device(query.device):
+        st = cs_fused_attention_backward(
+            query.data_ptr(), keys.data_ptr(), values.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), grad_output.data_ptr(),
+            *(g.data_ptr() for g in grads), m_ptr, shape, work.data_ptr(),
+            size, _stream_handle(query.device))
+    if st != 0:
+        raise CsError(st, "cs_fused_attention_backward")
+    return tuple(grads)
+
+
 def plan_attention(batch: int, heads: int, seq_len: int, aligned: bool = True,
                    variant: str = "auto", param: int = 0,
                    threads: int = 0) -> dict:
@@ -357,11 +518,51 @@ def _autograd_function():
     return ConstrainedSoftmaxFunction
 
 
+def _fused_attention_function():
+    import torch
+
+    def strided(x):
+        """x itself where the kernels take its strides, else a copy."""
+        ok = (x.dim() == 4 and x.stride(3) == 1 and x.data_ptr() % 16 == 0
+              and all(n <= 1 or (s > 0 and s % 8 == 0)
+                      for n, s in zip(x.shape[:3], x.stride()[:3])))
+        return x if ok else x.contiguous()
+
+    class FusedAttentionFunction(torch.autograd.Function):
+        """Autograd wrapper of :func:`fused_attention`: ``apply(query, keys,
+        values, mask, causal, scale)``; query, keys and values receive
+        gradients.  Inputs whose strides the kernels do not take (expanded
+        ones, for example) are copied."""
+
+        @staticmethod
+        def forward(ctx, query, keys, values, mask=None, causal=False,
+                    scale=None):
+            query, keys, values = (strided(x) for x in (query, keys, values))
+            out, lse = fused_attention(query, keys, values, mask, causal,
+                                       scale, return_lse=True)
+            ctx.save_for_backward(query, keys, values, out, lse, mask)
+            ctx.causal, ctx.scale = causal, scale
+            return out
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_output):
+            query, keys, values, out, lse, mask = ctx.saved_tensors
+            grads = fused_attention_backward(
+                query, keys, values, out, lse, strided(grad_output), mask,
+                ctx.causal, ctx.scale)
+            return (*grads, None, None, None)
+
+    return FusedAttentionFunction
+
+
 def __getattr__(name):
-    # The autograd class needs torch; it is built on first use so that the
-    # package imports without torch (the C ABI tests run without it).
-    if name == "ConstrainedSoftmaxFunction":
-        cls = _autograd_function()
+    # The autograd classes need torch; they are built on first use so that
+    # the package imports without torch (the C ABI tests run without it).
+    make = {"ConstrainedSoftmaxFunction": _autograd_function,
+            "FusedAttentionFunction": _fused_attention_function}.get(name)
+    if make is not None:
+        cls = make()
         globals()[name] = cls
         return cls
     raise AttributeError(name)

@@ -49,6 +49,31 @@ class cs_plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+_STRIDES = ctypes.c_int64 * 3
+
+
+class cs_attention_shape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("query_len", ctypes.c_int32),
+        ("key_len", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride", _STRIDES),
+        ("k_stride", _STRIDES),
+        ("v_stride", _STRIDES),
+        ("o_stride", _STRIDES),
+        ("go_stride", _STRIDES),
+        ("dq_stride", _STRIDES),
+        ("dk_stride", _STRIDES),
+        ("dv_stride", _STRIDES),
+        ("mask_stride", ctypes.c_int64),
+    ]
+
+
 def _header_constants() -> dict[str, int]:
     """The #define'd integer constants of the public header."""
     out = {}
@@ -125,6 +150,19 @@ _SIGNATURES = {
     "cs_check_biencoder_args": (_I32, [_VP, _VP, _VP, _VP, _I32, _I32, _I32,
                                        _I32, _I32, _F32, _F32, _F32, _F32,
                                        _I32, _VP, _VP]),
+    "cs_fused_attention": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP,
+                                  ctypes.POINTER(cs_attention_shape), _VP]),
+    "cs_fused_attention_backward": (
+        _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+               ctypes.POINTER(cs_attention_shape), _VP, _I64, _VP]),
+    "cs_fused_attention_backward_workspace": (
+        _I64, [ctypes.POINTER(cs_attention_shape)]),
+    "cs_check_fused_attention_args": (
+        _I32, [_VP, _VP, _VP, _VP, _VP, _VP,
+               ctypes.POINTER(cs_attention_shape)]),
+    "cs_check_fused_attention_backward_args": (
+        _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+               ctypes.POINTER(cs_attention_shape), _VP, _I64]),
     "cs_probe_ex2": (_I32, [_VP, _I32, ctypes.POINTER(_I64), _VP]),
     "cs_probe_ex2_sink_floats": (_I32, []),
     "cs_test_wait_timeout": (_I32, [_I64, _VP]),
@@ -346,6 +384,42 @@ def cs_check_biencoder_args(query, keys, values, output, batch_size,
         query, keys, values, output, batch_size, query_len, context_len,
         d_head, num_heads, scale, entropy_bound, t_min, t_max, max_iter,
         attn_out, t_out)
+
+
+def cs_fused_attention(query, keys, values, out, lse, mask, shape,
+                       stream) -> int:
+    return load().cs_fused_attention(query, keys, values, out, lse, mask,
+                                     ctypes.byref(shape), stream)
+
+
+def cs_fused_attention_backward(query, keys, values, out, lse, grad_out,
+                                grad_query, grad_keys, grad_values, mask,
+                                shape, workspace, workspace_bytes,
+                                stream) -> int:
+    return load().cs_fused_attention_backward(
+        query, keys, values, out, lse, grad_out, grad_query, grad_keys,
+        grad_values, mask, ctypes.byref(shape), workspace, workspace_bytes,
+        stream)
+
+
+def cs_fused_attention_backward_workspace(shape) -> int:
+    return load().cs_fused_attention_backward_workspace(ctypes.byref(shape))
+
+
+def cs_check_fused_attention_args(query, keys, values, out, lse, mask,
+                                  shape) -> int:
+    return load().cs_check_fused_attention_args(query, keys, values, out, lse,
+                                                mask, ctypes.byref(shape))
+
+
+def cs_check_fused_attention_backward_args(query, keys, values, out, lse,
+                                           grad_out, grad_query, grad_keys,
+                                           grad_values, mask, shape,
+                                           workspace,
+                                           workspace_bytes) -> int:
+    return load().cs_check_fused_attention_backward_args(
+        query, keys, values, out, lse, grad_out, grad_query, grad_keys,
+        grad_values, mask, ctypes.byref(shape), workspace, workspace_bytes)
 
 
 def cs_probe_ex2(sink, iters, stream) -> tuple[int, int]:

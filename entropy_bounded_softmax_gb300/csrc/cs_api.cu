@@ -558,6 +558,107 @@ cs_status forward(const void* logits, bool in_bf16, float* out, int64_t batch,
     return CS_OK;
 }
 
+// ------------------------------------------------------------ fused attention
+// Sizes and strides of one [batch, heads, length, d_head] bf16 tensor: the
+// bytes from its first to past its last element, or -1 when a stride is
+// refused (negative, not a multiple of 8 elements, or 0 over more than one
+// element; strides of dimensions of one element are not looked at).
+int64_t heads_extent(const cs_attention_shape& s, int32_t heads, int32_t length,
+                     const int64_t* stride) {
+    const int64_t dim[3] = {s.batch, heads, length};
+    int64_t last = s.d_head;
+    for (int i = 0; i < 3; ++i) {
+        if (dim[i] == 0) return 0;
+    }
+    for (int i = 0; i < 3; ++i) {
+        if (dim[i] == 1) continue;
+        // The tensor copies take strides below 2^40 bytes.
+        if (stride[i] <= 0 || stride[i] % 8 != 0 || stride[i] >= (int64_t(1) << 39))
+            return -1;
+        last += (dim[i] - 1) * stride[i];
+        if (last > (int64_t(1) << 60)) return -1;
+    }
+    return 2 * last;
+}
+
+cs_status check_attention_shape(const cs_attention_shape* s) {
+    if (!s) return CS_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->heads < 1 || s->kv_heads < 1 || s->query_len < 0 ||
+        s->key_len < 0 || s->d_head < 1 || s->heads % s->kv_heads != 0)
+        return CS_ERR_DIM_MISMATCH;
+    if (s->d_head > cs::kFattnMaxDHead) return CS_ERR_OOM;
+    if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
+    if (s->causal != 0 && s->causal != 1) return CS_ERR_INVALID_ARG;
+    if (!isfinite(s->scale) || !(s->scale > 0.0f)) return CS_ERR_INVALID_ARG;
+    // Rows and tiles are counted in 32 bits.
+    if (s->query_len > (1 << 30) || s->key_len > (1 << 30) ||
+        static_cast<int64_t>(s->batch) * s->heads > kMaxGridX)
+        return CS_ERR_DIM_MISMATCH;
+    const int64_t bh = static_cast<int64_t>(s->batch) * s->heads;
+    if (bh * ceil_div(s->query_len, 128) > kMaxGridX ||
+        bh * ceil_div(s->key_len, 128) > kMaxGridX)
+        return CS_ERR_DIM_MISMATCH;
+    return CS_OK;
+}
+
+// One tensor of a call: where it is, how far it reaches, whether the call
+// writes it.
+struct Span {
+    const void* data;
+    int64_t bytes;
+    int align;
+    bool written;
+};
+
+// Every span present, aligned, and no written one overlapping another.
+cs_status check_spans(const Span* x, int n) {
+    for (int i = 0; i < n; ++i) {
+        if (x[i].bytes < 0) return CS_ERR_INVALID_ARG;
+        if (x[i].bytes == 0) continue;
+        if (!x[i].data || reinterpret_cast<uintptr_t>(x[i].data) % x[i].align)
+            return CS_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if ((x[i].written || x[j].written) &&
+                ranges_overlap(x[i].data, x[i].bytes, x[j].data, x[j].bytes))
+                return CS_ERR_INVALID_ARG;
+    }
+    return CS_OK;
+}
+
+int64_t mask_extent(const cs_attention_shape& s, const uint8_t* mask) {
+    if (!mask || s.batch == 0 || s.key_len == 0) return 0;
+    if (s.batch > 1 && s.mask_stride < s.key_len) return -1;
+    return s.key_len + (s.batch > 1 ? (s.batch - 1) * s.mask_stride : 0);
+}
+
+cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
+                             unsigned int* err) {
+    cs::FattnTask t{};
+    t.mask = mask;
+    t.mask_stride = s.mask_stride;
+    t.err = err;
+    for (int i = 0; i < 3; ++i) {
+        t.q_stride[i] = s.q_stride[i];
+        t.k_stride[i] = s.k_stride[i];
+        t.v_stride[i] = s.v_stride[i];
+        t.o_stride[i] = s.o_stride[i];
+        t.go_stride[i] = s.go_stride[i];
+        t.dq_stride[i] = s.dq_stride[i];
+        t.dk_stride[i] = s.dk_stride[i];
+        t.dv_stride[i] = s.dv_stride[i];
+    }
+    t.batch = s.batch;
+    t.heads = s.heads;
+    t.kv_heads = s.kv_heads;
+    t.query_len = s.query_len;
+    t.key_len = s.key_len;
+    t.d_head = s.d_head;
+    t.causal = s.causal;
+    t.scale = s.scale;
+    t.wait_limit_cycles = cs::kWaitLimitCycles;
+    return t;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1084,6 +1185,119 @@ cs_status cs_biencoder_attention(const float* query,
                                      context_len, d_head, num_heads, scale,
                                      entropy_bound, 0.01f, 10.0f, 20, nullptr,
                                      nullptr, nullptr, stream);
+}
+
+cs_status cs_check_fused_attention_args(const uint16_t* query,
+                                        const uint16_t* keys,
+                                        const uint16_t* values,
+                                        const uint16_t* out, const float* lse,
+                                        const uint8_t* mask,
+                                        const cs_attention_shape* shape) {
+    const cs_status st = check_attention_shape(shape);
+    if (st != CS_OK) return st;
+    const cs_attention_shape& s = *shape;
+    const int64_t rows = static_cast<int64_t>(s.batch) * s.heads * s.query_len;
+    const Span spans[6] = {
+        {query, heads_extent(s, s.heads, s.query_len, s.q_stride), 16, false},
+        {keys, heads_extent(s, s.kv_heads, s.key_len, s.k_stride), 16, false},
+        {values, heads_extent(s, s.kv_heads, s.key_len, s.v_stride), 16, false},
+        {mask, mask_extent(s, mask), 1, false},
+        {out, heads_extent(s, s.heads, s.query_len, s.o_stride), 16, true},
+        {lse, lse ? rows * 4 : 0, 4, true}};
+    return check_spans(spans, 6);
+}
+
+cs_status cs_fused_attention(const uint16_t* query, const uint16_t* keys,
+                             const uint16_t* values, uint16_t* out,
+                             float* lse, const uint8_t* mask,
+                             const cs_attention_shape* shape, void* stream) {
+    cs_status st = cs_check_fused_attention_args(query, keys, values, out, lse,
+                                                 mask, shape);
+    if (st != CS_OK) return st;
+    if (shape->batch == 0 || shape->query_len == 0) return CS_OK;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != CS_OK) return st;
+    cs::FattnTask t = attention_task(*shape, mask, d->err);
+    t.q = query;
+    t.k = keys;
+    t.v = values;
+    t.out = out;
+    t.lse = lse;
+    if (cs::launch_fattn_forward(t, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return CS_ERR_CUDA;
+    }
+    return CS_OK;
+}
+
+int64_t cs_fused_attention_backward_workspace(const cs_attention_shape* shape) {
+    if (check_attention_shape(shape) != CS_OK) return -1;
+    return 4 * cs::fattn_workspace_floats(shape->batch, shape->heads,
+                                          shape->query_len);
+}
+
+cs_status cs_check_fused_attention_backward_args(
+    const uint16_t* query, const uint16_t* keys, const uint16_t* values,
+    const uint16_t* out, const float* lse, const uint16_t* grad_out,
+    const uint16_t* grad_query, const uint16_t* grad_keys,
+    const uint16_t* grad_values, const uint8_t* mask,
+    const cs_attention_shape* shape, const void* workspace,
+    int64_t workspace_bytes) {
+    const cs_status st = check_attention_shape(shape);
+    if (st != CS_OK) return st;
+    const cs_attention_shape& s = *shape;
+    const int64_t rows = static_cast<int64_t>(s.batch) * s.heads * s.query_len;
+    const int64_t need = cs_fused_attention_backward_workspace(shape);
+    if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
+    const Span spans[11] = {
+        {query, heads_extent(s, s.heads, s.query_len, s.q_stride), 16, false},
+        {keys, heads_extent(s, s.kv_heads, s.key_len, s.k_stride), 16, false},
+        {values, heads_extent(s, s.kv_heads, s.key_len, s.v_stride), 16, false},
+        {out, heads_extent(s, s.heads, s.query_len, s.o_stride), 16, false},
+        {grad_out, heads_extent(s, s.heads, s.query_len, s.go_stride), 16, false},
+        {lse, rows * 4, 4, false},
+        {mask, mask_extent(s, mask), 1, false},
+        {grad_query, heads_extent(s, s.heads, s.query_len, s.dq_stride), 16, true},
+        {grad_keys, heads_extent(s, s.kv_heads, s.key_len, s.dk_stride), 16, true},
+        {grad_values, heads_extent(s, s.kv_heads, s.key_len, s.dv_stride), 16, true},
+        {workspace, need, 16, true}};
+    return check_spans(spans, 11);
+}
+
+cs_status cs_fused_attention_backward(
+    const uint16_t* query, const uint16_t* keys, const uint16_t* values,
+    const uint16_t* out, const float* lse, const uint16_t* grad_out,
+    uint16_t* grad_query, uint16_t* grad_keys, uint16_t* grad_values,
+    const uint8_t* mask, const cs_attention_shape* shape, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+    cs_status st = cs_check_fused_attention_backward_args(
+        query, keys, values, out, lse, grad_out, grad_query, grad_keys,
+        grad_values, mask, shape, workspace, workspace_bytes);
+    if (st != CS_OK) return st;
+    if (shape->batch == 0 || (shape->query_len == 0 && shape->key_len == 0))
+        return CS_OK;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != CS_OK) return st;
+    cs::FattnTask t = attention_task(*shape, mask, d->err);
+    t.q = query;
+    t.k = keys;
+    t.v = values;
+    t.out = const_cast<uint16_t*>(out);
+    t.lse = const_cast<float*>(lse);
+    t.go = grad_out;
+    t.dq = grad_query;
+    t.dk = grad_keys;
+    t.dv = grad_values;
+    t.rows = static_cast<float*>(workspace);
+    if (cs::launch_fattn_backward(t, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return CS_ERR_CUDA;
+    }
+    return CS_OK;
 }
 
 int32_t cs_probe_ex2_sink_floats(void) {

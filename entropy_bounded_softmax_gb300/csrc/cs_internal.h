@@ -314,6 +314,45 @@ inline int64_t pv_smem_bytes(int K, int D) {
 cudaError_t launch_bienc_pv(const PvTask& task, int sm_count,
                             cudaStream_t stream);
 
+// One fused_attention launch (forward or backward): bf16 tensors [batch,
+// heads, length, d_head] with element strides of the first three dimensions.
+struct FattnTask {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* out;           // backward: the forward's, read only
+    float* lse;              // [batch, heads, query_len]; forward: may be null
+    const uint16_t* go;      // backward: gradient of out
+    uint16_t* dq;
+    uint16_t* dk;
+    uint16_t* dv;
+    float* rows;             // backward: workspace, see fattn_workspace_floats
+    const uint8_t* mask;     // [batch, key_len], nonzero keeps; may be null
+    int64_t mask_stride;
+    unsigned int* err;       // device error word
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+    int64_t go_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+    int32_t batch, heads, kv_heads, query_len, key_len, d_head;
+    int32_t causal;
+    float scale;
+    uint64_t wait_limit_cycles;
+};
+
+constexpr int kFattnMaxDHead = 128;
+
+// The backward's workspace: for every query row the log2 of its normaliser
+// and <grad_out, out>, two arrays of batch * heads rows of query_len rounded
+// up to whole tiles of 128.
+inline int64_t fattn_rows_padded(int32_t query_len) {
+    return (static_cast<int64_t>(query_len) + 127) / 128 * 128;
+}
+inline int64_t fattn_workspace_floats(int32_t batch, int32_t heads, int32_t query_len) {
+    return 2 * static_cast<int64_t>(batch) * heads * fattn_rows_padded(query_len);
+}
+
+cudaError_t launch_fattn_forward(const FattnTask& task, cudaStream_t stream);
+cudaError_t launch_fattn_backward(const FattnTask& task, cudaStream_t stream);
+
 cudaError_t launch_rowgroup(const RowTask& task, int lanes_per_row,
                             int elems_per_lane, cudaStream_t stream);
 cudaError_t launch_cluster(const RowTask& task, int cluster_size,

@@ -48,11 +48,10 @@
 // neighbours.  Every wait is bounded; after a timeout the CTA records it,
 // raises a shared abort flag, and every role skips its remaining waits and
 // work.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <string.h>
 
 #include "cs_tcgen05.cuh"
+#include "cs_tensormap.h"
 
 namespace cs {
 namespace {
@@ -340,23 +339,6 @@ bienc_pv_kernel(PvTask t, const __grid_constant__ CUtensorMap tmap, int use_tma)
     __syncthreads();
     if (warp == kPvMmaWarp) tmem_dealloc(tmem, kPvTmemCols);
     if (*abort_flag && threadIdx.x == 0) raise_error(t.err, kBitTimeout);
-}
-
-// cuTensorMapEncodeTiled, from the CUDA driver through the runtime (no link
-// against the driver library); null if unavailable.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
 }
 
 }  // namespace

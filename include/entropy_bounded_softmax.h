@@ -489,6 +489,114 @@ cs_status cs_check_biencoder_args(const float* query,
                                   const float* attn_out, const float* t_out);
 
 /*
+ * Fused attention of language-model shapes, for training: the scores never
+ * reach memory.  bf16 tensors (bit patterns, uint16_t), each
+ * [batch, heads or kv_heads, length, d_head] with the head dimension
+ * contiguous and the element strides of the other three given.
+ */
+typedef struct cs_attention_shape {
+    int32_t batch;      /* >= 0                                             */
+    int32_t heads;      /* query heads, a positive multiple of kv_heads     */
+    int32_t kv_heads;   /* key and value heads; head h reads key head
+                           h / (heads / kv_heads)                           */
+    int32_t query_len;  /* >= 0                                             */
+    int32_t key_len;    /* >= 0                                             */
+    int32_t d_head;     /* 8..128, a multiple of 8                          */
+    int32_t causal;     /* 1: query i keeps keys j <= i + key_len - query_len
+                           (the last query sees every key); 0: all keys     */
+    float scale;        /* of the scores; positive and finite               */
+    int64_t q_stride[3];   /* batch, head, position; non-negative           */
+    int64_t k_stride[3];   /* multiples of 8 elements (a dimension of size  */
+    int64_t v_stride[3];   /* 1 may have any); an input's may not be 0      */
+    int64_t o_stride[3];   /* where the dimension has more than one element */
+    int64_t go_stride[3];  /* backward: grad_out                            */
+    int64_t dq_stride[3];  /* backward: the gradients                       */
+    int64_t dk_stride[3];
+    int64_t dv_stride[3];
+    int64_t mask_stride;   /* bytes between the mask's rows, >= key_len     */
+} cs_attention_shape;
+
+/*
+ * cs_fused_attention -- for every batch b, head h and query i, over the keys
+ * j that neither the mask nor `causal` removes:
+ *
+ *   s_j = scale * (query_i . key_j)
+ *   lse_i = ln sum_j e^(s_j)
+ *   out_i = sum_j e^(s_j - lse_i) value_j
+ *
+ * query, keys, values, out   device pointers, 16-byte aligned; out is written
+ *          completely and must not overlap the inputs or lse.
+ * lse      optional device pointer, [batch, heads, query_len] fp32,
+ *          contiguous: what the backward takes.
+ * mask     optional device pointer, [batch, key_len] bytes: 0 removes the
+ *          key for every query of the sequence (padding).  What removed keys
+ *          and values hold has no effect, NaN included.
+ * A query whose keys are all removed gets zeros and lse = -inf.
+ *
+ * Scores, maxima, sums and outputs are accumulated in fp32; the weights are
+ * rounded to bf16, the tensor cores' operand type, for the product with the
+ * values, and out is rounded once.  NaN or infinite scores of kept keys
+ * propagate by IEEE arithmetic and OR CS_ERR_NAN_INPUT into the error word.
+ * A value that is NaN or infinite propagates to every query of its block of
+ * 128 keys, those that only `causal` keeps from it included (0 times it is
+ * NaN).
+ *
+ * The tensor cores take the products (tcgen05.mma); see cs_check_* for what
+ * is refused.  Ownership, execution and errors: as cs_constrained_softmax.
+ */
+cs_status cs_fused_attention(const uint16_t* query, const uint16_t* keys,
+                             const uint16_t* values, uint16_t* out,
+                             float* lse, const uint8_t* mask,
+                             const cs_attention_shape* shape, void* stream);
+
+/*
+ * cs_fused_attention_backward -- the gradients of a loss with respect to
+ * query, keys and values, given grad_out, that of out, and the forward's out
+ * and lse.  The probabilities are recomputed from lse:
+ *
+ *   P_ij = e^(s_ij - lse_i),  dS_ij = P_ij (grad_out_i . value_j
+ *                                           - grad_out_i . out_i)
+ *   grad_query_i = scale sum_j dS_ij key_j
+ *   grad_key_j   = scale sum_i dS_ij query_i
+ *   grad_value_j = sum_i P_ij grad_out_i
+ *
+ * the last two summed over the heads that share the key head.  Every element
+ * of the three gradients is written; removed keys and queries without keys
+ * get zeros.  Sums are fp32 with a fixed order (repeated calls give the same
+ * bits); P and dS are rounded to bf16 for the products, the gradients once.
+ *
+ * workspace  device pointer, 16-byte aligned, at least
+ *          cs_fused_attention_backward_workspace(shape) bytes: the caller's,
+ *          written and read by this call only, free after it on the stream.
+ * The gradients must not overlap each other, the inputs or the workspace.
+ * Everything else: as cs_fused_attention.
+ */
+cs_status cs_fused_attention_backward(
+    const uint16_t* query, const uint16_t* keys, const uint16_t* values,
+    const uint16_t* out, const float* lse, const uint16_t* grad_out,
+    uint16_t* grad_query, uint16_t* grad_keys, uint16_t* grad_values,
+    const uint8_t* mask, const cs_attention_shape* shape, void* workspace,
+    int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the backward needs; negative for a malformed shape. */
+int64_t cs_fused_attention_backward_workspace(const cs_attention_shape* shape);
+
+/* Host-only argument checks (no CUDA call). */
+cs_status cs_check_fused_attention_args(const uint16_t* query,
+                                        const uint16_t* keys,
+                                        const uint16_t* values,
+                                        const uint16_t* out, const float* lse,
+                                        const uint8_t* mask,
+                                        const cs_attention_shape* shape);
+cs_status cs_check_fused_attention_backward_args(
+    const uint16_t* query, const uint16_t* keys, const uint16_t* values,
+    const uint16_t* out, const float* lse, const uint16_t* grad_out,
+    const uint16_t* grad_query, const uint16_t* grad_keys,
+    const uint16_t* grad_values, const uint8_t* mask,
+    const cs_attention_shape* shape, const void* workspace,
+    int64_t workspace_bytes);
+
+/*
  * Throughput probe of the ex2 unit, the unit this operation is bound by.
  * Launches one kernel over all SMs in which every thread runs `iters`
  * rounds of 8 independent ex2.approx.ftz.f32 chains; *ex2_count receives
