@@ -25,6 +25,9 @@ from ._lib import (CONSTANTS, cs_attention_softmax, cs_attention_softmax_ex,
                    cs_check_fused_attention_backward_args,
                    cs_fused_attention, cs_fused_attention_backward,
                    cs_fused_attention_backward_workspace,
+                   cs_check_paged_attention_args, cs_paged_attention,
+                   cs_paged_attention_chunk, cs_paged_attention_workspace,
+                   cs_paged_shape,
                    cs_check_biencoder_args, cs_plan_biencoder_host,
                    cs_check_args, cs_check_attention_args,
                    cs_check_backward_args, cs_constrained_softmax,
@@ -61,6 +64,9 @@ __all__ = [
     "cs_attention_shape", "cs_fused_attention", "cs_fused_attention_backward",
     "cs_fused_attention_backward_workspace", "cs_check_fused_attention_args",
     "cs_check_fused_attention_backward_args",
+    "paged_attention", "cs_paged_shape", "cs_paged_attention",
+    "cs_paged_attention_workspace", "cs_paged_attention_chunk",
+    "cs_check_paged_attention_args",
 ]
 
 # Defaults of section 2.1's signature.
@@ -74,7 +80,7 @@ VARIANTS = {"auto": CONSTANTS["CS_VARIANT_AUTO"],
             "cluster": CONSTANTS["CS_VARIANT_CLUSTER"]}
 ERROR_BITS = {name: 1 << CONSTANTS[f"CS_ERR_{name}"]
               for name in ("NAN_INPUT", "INF_INPUT", "ENTROPY_OVERFLOW",
-                           "TIMEOUT")}
+                           "TIMEOUT", "BAD_PAGE")}
 
 
 class CsError(RuntimeError):
@@ -475,6 +481,107 @@ def fused_attention_backward(query, keys, values, out, lse, grad_output,
     if st != 0:
         raise CsError(st, "cs_fused_attention_backward")
     return tuple(grads)
+
+
+def _check_rows(name, x, dim, dtype, device) -> None:
+    import torch
+    if (not isinstance(x, torch.Tensor) or x.device.type != "cuda"
+            or (device is not None and x.device != device)):
+        raise ValueError(f"{name} must be a CUDA tensor on one device with "
+                         "the others")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if x.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    if x.numel() == 0:
+        return
+    st = x.stride()
+    if (st[-1] != 1 or x.data_ptr() % 16
+            or any(n > 1 and s % 8 for n, s in zip(x.shape[:-1], st))):
+        raise ValueError(f"{name}'s last dimension must be contiguous, its "
+                         "base 16-byte aligned and its other strides "
+                         "multiples of 8 elements")
+
+
+def paged_attention(query, key_pages, value_pages, page_table, lengths,
+                    scale=None, out=None, return_lse: bool = False):
+    """Attention of one new token per sequence over a paged key-value cache:
+    softmax(scale query keys^T) values over the sequence's tokens.
+
+    ``query`` [B, H, D]; ``key_pages`` and ``value_pages``
+    [pages, page_size, Hk, D], H a multiple of Hk, D a multiple of 8 up to
+    256, all bf16 or all fp16 on one CUDA device; ``page_table`` int32
+    [B, n]: token j of sequence b is in slot j % page_size of page
+    ``page_table[b, j // page_size]``; ``lengths`` int32 [B].  Table entries
+    and slots past a length are not read.  ``scale`` defaults to 1/sqrt(D).
+    Returns [B, H, D] (or ``out``), zeros for a length of 0, and with
+    ``return_lse`` the log of the softmax's sums [B, H] in fp32.
+    Asynchronous on the current stream; lengths and page numbers out of
+    range are left out and reported by :func:`get_error`, and so are NaN or
+    infinite scores, which propagate.
+    """
+    import math
+    import torch
+    dtype = query.dtype if isinstance(query, torch.Tensor) else None
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("query must be a bfloat16 or float16 tensor")
+    dev = query.device
+    _check_rows("query", query, 3, dtype, None)
+    _check_rows("key_pages", key_pages, 4, dtype, dev)
+    _check_rows("value_pages", value_pages, 4, dtype, dev)
+    B, H, D = query.shape
+    pages, page_size, Hk, _ = key_pages.shape
+    if key_pages.shape[3] != D or value_pages.shape != key_pages.shape:
+        raise ValueError("key_pages and value_pages must both be "
+                         "[pages, page_size, kv_heads, d_head] with the "
+                         "query's d_head")
+    if H < 1 or Hk < 1 or H % Hk or page_size < 1:
+        raise ValueError("the query's heads must be a multiple of the "
+                         "pages', and page_size positive")
+    if D < 8 or D > 256 or D % 8:
+        raise ValueError("d_head must be a multiple of 8 in 8..256")
+    for name, x, dim in (("page_table", page_table, 2),
+                         ("lengths", lengths, 1)):
+        if (not isinstance(x, torch.Tensor) or x.dtype != torch.int32
+                or x.device != dev or x.dim() != dim or x.shape[0] != B
+                or (x.shape[-1] > 1 and x.stride(-1) != 1)):
+            raise ValueError(f"{name} must be an int32 tensor of the batch's "
+                             "rows, contiguous along its last dimension, on "
+                             "the query's device")
+    if B > 1 and page_table.stride(0) < page_table.shape[1]:
+        raise ValueError("page_table's rows must not overlap")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if not (scale > 0.0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
+    if out is None:
+        out = torch.empty((B, H, D), dtype=dtype, device=dev)
+    else:
+        _check_rows("out", out, 3, dtype, dev)
+        if out.shape != query.shape:
+            raise ValueError("out must be shaped like query")
+    lse = None
+    if return_lse:
+        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+    shape = cs_paged_shape(
+        B, H, Hk, D, page_size, pages, page_table.shape[1],
+        int(dtype == torch.float16), float(scale), query.stride()[:2],
+        out.stride()[:2], key_pages.stride()[:3], value_pages.stride()[:3],
+        page_table.stride(0))
+    size = cs_paged_attention_workspace(shape)
+    work = None
+    if size > 0:
+        work = torch.empty(size, dtype=torch.uint8, device=dev)
+    with _on_device(dev):
+        st = cs_paged_attention(
+            query.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
+            page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+            lse.data_ptr() if return_lse else None, shape,
+            work.data_ptr() if work is not None else None, max(size, 0),
+            _stream_handle(dev))
+    if st != 0:
+        raise CsError(st, "cs_paged_attention")
+    return (out, lse) if return_lse else out
 
 
 def plan_attention(batch: int, heads: int, seq_len: int, aligned: bool = True,

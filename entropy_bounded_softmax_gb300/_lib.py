@@ -74,6 +74,25 @@ class cs_attention_shape(ctypes.Structure):
     ]
 
 
+class cs_paged_shape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("fp16", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("o_stride", ctypes.c_int64 * 2),
+        ("k_stride", _STRIDES),
+        ("v_stride", _STRIDES),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
 def _header_constants() -> dict[str, int]:
     """The #define'd integer constants of the public header."""
     out = {}
@@ -163,6 +182,14 @@ _SIGNATURES = {
     "cs_check_fused_attention_backward_args": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                ctypes.POINTER(cs_attention_shape), _VP, _I64]),
+    "cs_paged_attention": (
+        _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
+               ctypes.POINTER(cs_paged_shape), _VP, _I64, _VP]),
+    "cs_paged_attention_workspace": (_I64, [ctypes.POINTER(cs_paged_shape)]),
+    "cs_paged_attention_chunk": (_I32, [ctypes.POINTER(cs_paged_shape)]),
+    "cs_check_paged_attention_args": (
+        _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
+               ctypes.POINTER(cs_paged_shape), _VP, _I64]),
     "cs_probe_ex2": (_I32, [_VP, _I32, ctypes.POINTER(_I64), _VP]),
     "cs_probe_ex2_sink_floats": (_I32, []),
     "cs_test_wait_timeout": (_I32, [_I64, _VP]),
@@ -420,6 +447,30 @@ def cs_check_fused_attention_backward_args(query, keys, values, out, lse,
     return load().cs_check_fused_attention_backward_args(
         query, keys, values, out, lse, grad_out, grad_query, grad_keys,
         grad_values, mask, ctypes.byref(shape), workspace, workspace_bytes)
+
+
+def cs_paged_attention(query, key_pages, value_pages, page_table, lengths,
+                       out, lse, shape, workspace, workspace_bytes,
+                       stream) -> int:
+    return load().cs_paged_attention(
+        query, key_pages, value_pages, page_table, lengths, out, lse,
+        ctypes.byref(shape), workspace, workspace_bytes, stream)
+
+
+def cs_paged_attention_workspace(shape) -> int:
+    return load().cs_paged_attention_workspace(ctypes.byref(shape))
+
+
+def cs_paged_attention_chunk(shape) -> int:
+    return load().cs_paged_attention_chunk(ctypes.byref(shape))
+
+
+def cs_check_paged_attention_args(query, key_pages, value_pages, page_table,
+                                  lengths, out, lse, shape, workspace,
+                                  workspace_bytes) -> int:
+    return load().cs_check_paged_attention_args(
+        query, key_pages, value_pages, page_table, lengths, out, lse,
+        ctypes.byref(shape), workspace, workspace_bytes)
 
 
 def cs_probe_ex2(sink, iters, stream) -> tuple[int, int]:

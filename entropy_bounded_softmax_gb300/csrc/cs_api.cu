@@ -575,6 +575,7 @@ int64_t heads_extent(const cs_attention_shape& s, int32_t heads, int32_t length,
         // The tensor copies take strides below 2^40 bytes.
         if (stride[i] <= 0 || stride[i] % 8 != 0 || stride[i] >= (int64_t(1) << 39))
             return -1;
+        if (stride[i] > (int64_t(1) << 60) / dim[i]) return -1;
         last += (dim[i] - 1) * stride[i];
         if (last > (int64_t(1) << 60)) return -1;
     }
@@ -657,6 +658,65 @@ cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
     t.scale = s.scale;
     t.wait_limit_cycles = cs::kWaitLimitCycles;
     return t;
+}
+
+// ------------------------------------------------------------ paged attention
+constexpr int32_t kPagedMaxTokens = 1 << 30;
+// CTAs the chunks of full-length sequences should make: four for each of the
+// two resident on 152 SMs.
+constexpr int64_t kPagedTargetCtas = 4 * 2 * 152;
+
+cs_status check_paged_shape(const cs_paged_shape* s) {
+    if (!s) return CS_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->heads < 1 || s->kv_heads < 1 || s->d_head < 1 ||
+        s->heads % s->kv_heads != 0 || s->page_size < 1 || s->num_pages < 0 ||
+        s->max_pages < 0)
+        return CS_ERR_DIM_MISMATCH;
+    if (s->d_head > cs::kPagedMaxDHead) return CS_ERR_OOM;
+    if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
+    if (s->fp16 != 0 && s->fp16 != 1) return CS_ERR_INVALID_ARG;
+    if (!isfinite(s->scale) || !(s->scale > 0.0f)) return CS_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(s->max_pages) * s->page_size > kPagedMaxTokens ||
+        static_cast<int64_t>(s->batch) * s->heads > kMaxGridX)
+        return CS_ERR_DIM_MISMATCH;
+    return CS_OK;
+}
+
+int32_t paged_head_tiles(const cs_paged_shape& s) {
+    return static_cast<int32_t>(ceil_div(s.heads / s.kv_heads, 16));
+}
+
+int32_t paged_chunk(const cs_paged_shape& s) {
+    const int64_t most = static_cast<int64_t>(s.max_pages) * s.page_size;
+    const int64_t work = static_cast<int64_t>(s.batch) * s.kv_heads *
+                         paged_head_tiles(s) * most;
+    int64_t c = ceil_div(ceil_div(work, kPagedTargetCtas), 64) * 64;
+    if (c < 128) c = 128;
+    if (c > 4096) c = 4096;
+    return static_cast<int32_t>(c);
+}
+
+int64_t paged_chunks(const cs_paged_shape& s) {
+    const int64_t n = ceil_div(static_cast<int64_t>(s.max_pages) * s.page_size,
+                               paged_chunk(s));
+    return n > 0 ? n : 1;
+}
+
+// The bytes of a strided tensor with a contiguous last dimension of d, from
+// its first to past its last element; -1 for a refused stride.
+int64_t strided_extent(const int64_t* dim, const int64_t* stride, int n, int32_t d) {
+    int64_t last = d;
+    for (int i = 0; i < n; ++i)
+        if (dim[i] == 0) return 0;
+    for (int i = 0; i < n; ++i) {
+        if (dim[i] == 1) continue;
+        if (stride[i] < 0 || stride[i] % 8 != 0 || stride[i] > (int64_t(1) << 40))
+            return -1;
+        if (stride[i] > (int64_t(1) << 60) / dim[i]) return -1;
+        last += (dim[i] - 1) * stride[i];
+        if (last > (int64_t(1) << 60)) return -1;
+    }
+    return 2 * last;
 }
 
 }  // namespace
@@ -1300,6 +1360,112 @@ cs_status cs_fused_attention_backward(
     return CS_OK;
 }
 
+int32_t cs_paged_attention_chunk(const cs_paged_shape* shape) {
+    if (check_paged_shape(shape) != CS_OK) return -1;
+    return paged_chunk(*shape);
+}
+
+int64_t cs_paged_attention_workspace(const cs_paged_shape* shape) {
+    if (check_paged_shape(shape) != CS_OK) return -1;
+    const int64_t chunks = paged_chunks(*shape);
+    if (chunks == 1) return 0;
+    // The (maximum, sum) pairs, then the outputs, 16-byte aligned.
+    const int64_t parts = static_cast<int64_t>(shape->batch) * shape->heads * chunks;
+    return ceil_div(parts, 2) * 16 + parts * shape->d_head * 4;
+}
+
+cs_status cs_check_paged_attention_args(
+    const uint16_t* query, const uint16_t* key_pages,
+    const uint16_t* value_pages, const int32_t* page_table,
+    const int32_t* lengths, const uint16_t* out, const float* lse,
+    const cs_paged_shape* shape, const void* workspace,
+    int64_t workspace_bytes) {
+    const cs_status st = check_paged_shape(shape);
+    if (st != CS_OK) return st;
+    const cs_paged_shape& s = *shape;
+    if (s.batch == 0) return CS_OK;
+    const int64_t grid = paged_chunks(s) * s.batch * s.kv_heads * paged_head_tiles(s);
+    if (grid > kMaxGridX) return CS_ERR_DIM_MISMATCH;
+    const int64_t need = cs_paged_attention_workspace(shape);
+    if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
+    if (s.batch > 1 && s.table_stride < s.max_pages) return CS_ERR_INVALID_ARG;
+    if (s.o_stride[0] == 0 && s.batch > 1) return CS_ERR_INVALID_ARG;
+    if (s.o_stride[1] == 0 && s.heads > 1) return CS_ERR_INVALID_ARG;
+    const int64_t rows[2] = {s.batch, s.heads};
+    const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
+    const int64_t table = s.max_pages == 0 ? 0
+        : 4 * ((s.batch > 1 ? (s.batch - 1) * s.table_stride : 0) + s.max_pages);
+    const Span spans[8] = {
+        {query, strided_extent(rows, s.q_stride, 2, s.d_head), 16, false},
+        {key_pages, strided_extent(pages, s.k_stride, 3, s.d_head), 16, false},
+        {value_pages, strided_extent(pages, s.v_stride, 3, s.d_head), 16, false},
+        {page_table, table, 4, false},
+        {lengths, 4 * static_cast<int64_t>(s.batch), 4, false},
+        {out, strided_extent(rows, s.o_stride, 2, s.d_head), 16, true},
+        {lse, lse ? 4 * static_cast<int64_t>(s.batch) * s.heads : 0, 4, true},
+        {workspace, need, 16, true}};
+    return check_spans(spans, 8);
+}
+
+cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
+                             const uint16_t* value_pages,
+                             const int32_t* page_table,
+                             const int32_t* lengths, uint16_t* out,
+                             float* lse, const cs_paged_shape* shape,
+                             void* workspace, int64_t workspace_bytes,
+                             void* stream) {
+    cs_status st = cs_check_paged_attention_args(
+        query, key_pages, value_pages, page_table, lengths, out, lse, shape,
+        workspace, workspace_bytes);
+    if (st != CS_OK) return st;
+    const cs_paged_shape& s = *shape;
+    if (s.batch == 0) return CS_OK;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != CS_OK) return st;
+    cs::PagedTask t{};
+    t.q = query;
+    t.k_pages = key_pages;
+    t.v_pages = value_pages;
+    t.page_table = page_table;
+    t.lengths = lengths;
+    t.out = out;
+    t.lse = lse;
+    t.err = d->err;
+    for (int i = 0; i < 2; ++i) {
+        t.q_stride[i] = s.q_stride[i];
+        t.o_stride[i] = s.o_stride[i];
+    }
+    for (int i = 0; i < 3; ++i) {
+        t.k_stride[i] = s.k_stride[i];
+        t.v_stride[i] = s.v_stride[i];
+    }
+    t.table_stride = s.table_stride;
+    t.batch = s.batch;
+    t.heads = s.heads;
+    t.kv_heads = s.kv_heads;
+    t.d_head = s.d_head;
+    t.page_size = s.page_size;
+    t.num_pages = s.num_pages;
+    t.max_pages = s.max_pages;
+    t.head_tiles = paged_head_tiles(s);
+    t.chunk_tokens = paged_chunk(s);
+    t.chunks = static_cast<int32_t>(paged_chunks(s));
+    t.fp16 = s.fp16;
+    t.scale = s.scale;
+    if (t.chunks > 1) {
+        const int64_t parts = static_cast<int64_t>(s.batch) * s.heads * t.chunks;
+        t.part_stats = static_cast<float2*>(workspace);
+        t.part_out = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                              ceil_div(parts, 2) * 16);
+    }
+    if (cs::launch_paged(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return CS_ERR_CUDA;
+    }
+    return CS_OK;
+}
+
 int32_t cs_probe_ex2_sink_floats(void) {
     DeviceInfo* d = nullptr;
     if (device_info(&d) != CS_OK) return -1;
@@ -1354,6 +1520,7 @@ const char* cs_status_string(cs_status status) {
         case CS_ERR_INVALID_ARG: return "invalid argument";
         case CS_ERR_CUDA: return "CUDA error";
         case CS_ERR_TIMEOUT: return "device wait timed out";
+        case CS_ERR_BAD_PAGE: return "page or length out of range";
         default: return "unknown status";
     }
 }

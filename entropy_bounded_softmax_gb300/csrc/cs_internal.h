@@ -15,6 +15,7 @@ constexpr unsigned int kBitNan = 1u << CS_ERR_NAN_INPUT;
 constexpr unsigned int kBitInf = 1u << CS_ERR_INF_INPUT;
 constexpr unsigned int kBitOverflow = 1u << CS_ERR_ENTROPY_OVERFLOW;
 constexpr unsigned int kBitTimeout = 1u << CS_ERR_TIMEOUT;
+constexpr unsigned int kBitBadPage = 1u << CS_ERR_BAD_PAGE;
 
 // Default limit of every bounded device wait, in SM cycles: 2^31 cycles,
 // about 1 s at GB300's 2.07 GHz maximum clock.
@@ -352,6 +353,33 @@ inline int64_t fattn_workspace_floats(int32_t batch, int32_t heads, int32_t quer
 
 cudaError_t launch_fattn_forward(const FattnTask& task, cudaStream_t stream);
 cudaError_t launch_fattn_backward(const FattnTask& task, cudaStream_t stream);
+
+// One paged_attention launch: a new token for each of `batch` sequences.
+struct PagedTask {
+    const uint16_t* q;         // [batch, heads, d_head], bf16 or (fp16) fp16
+    const uint16_t* k_pages;   // [num_pages, page_size, kv_heads, d_head]
+    const uint16_t* v_pages;
+    const int32_t* page_table; // [batch, max_pages]
+    const int32_t* lengths;    // [batch]
+    uint16_t* out;             // [batch, heads, d_head]
+    float* lse;                // [batch, heads] or null
+    float2* part_stats;        // workspace: [batch, heads, chunks] (max, sum)
+    float* part_out;           // [batch, heads, chunks, d_head]
+    unsigned int* err;         // device error word
+    int64_t q_stride[2], o_stride[2], k_stride[3], v_stride[3];
+    int64_t table_stride;
+    int32_t batch, heads, kv_heads, d_head;
+    int32_t page_size, num_pages, max_pages;
+    int32_t head_tiles;        // tiles of 16 query heads to a key head
+    int32_t chunk_tokens;      // tokens of a chunk
+    int32_t chunks;            // chunks of the longest sequence
+    int32_t fp16;
+    float scale;
+};
+
+constexpr int kPagedMaxDHead = 256;
+
+cudaError_t launch_paged(const PagedTask& task, cudaStream_t stream);
 
 cudaError_t launch_rowgroup(const RowTask& task, int lanes_per_row,
                             int elems_per_lane, cudaStream_t stream);

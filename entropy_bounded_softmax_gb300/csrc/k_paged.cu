@@ -1,0 +1,471 @@
+// Attention of one new token per sequence over a paged key-value cache.  For
+// sequence b, query head h and its key head hk, over tokens j < lengths[b]
+// (token j in slot j % page_size of page table[b][j / page_size]):
+//   s_j = scale q . k_j,  out = sum e^(s_j - m) v_j / sum e^(s_j - m).
+//
+// Every key and value is read once and used for the query heads that share
+// its head: bound by the cache's bytes.  The tokens are cut into chunks of
+// fixed length; a CTA takes one chunk of one (sequence, key head), up to 16
+// query heads of it.  Its four warps walk the chunk's tiles of 16 tokens,
+// each with a ring of its own that asynchronous copies keep full (no barrier
+// between warps until the end), a running maximum and sum, and two products
+// on m16n8k16 tensor-core instructions with the query heads along M: scores
+// = Q K^T and out += P V.  The instruction's rate does not matter here (a
+// head group of 16 or less leaves tcgen05's 128 rows empty, and the bytes
+// take longer).  The warps' sums are joined in shared memory; a sequence of
+// one chunk is finished there, the others' parts (maximum, sum, unnormalised
+// output) go to the workspace and a second small kernel joins them.  Chunks
+// past a sequence's end return at once.
+//
+// The weights enter the second product as two halves of the cache's type,
+// the nearest value and the nearest to the rest, so that their rounding
+// (2^-16 in bf16) stays below the result's.  They carry a factor 2^8: fp16
+// has no exponents below 2^-24, and the largest weight, 2^8 to 2^14 with a
+// lagging maximum, leaves 2^-32 of it.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "cs_device.cuh"
+
+namespace cs {
+namespace {
+
+using namespace csd;
+
+constexpr int kPgWarps = 4;
+constexpr int kPgThreads = 32 * kPgWarps;
+constexpr int kPgTile = 16;            // tokens
+constexpr int kPgStages = 3;
+constexpr float kWeightBits = 8.0f;    // log2 of the weights' common factor
+constexpr float kLagBits = 6.0f;       // how far the maximum may lag
+
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// The cache's element types: the tensor-core product and the two halves of a
+// pair of weights.
+struct PgBF16 {
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4],
+                                               uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&x);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return make_float2(InBF16::lo(u), InBF16::hi(u));
+    }
+};
+
+struct PgFP16 {
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4],
+                                               uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+            "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const __half2 x = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&x);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    }
+};
+
+template <int DP>
+struct PgSmem {
+    static constexpr int kRow = DP * 2;                       // bytes of a token's row
+    static constexpr int kHalf = kPgTile * kRow;              // a tile's keys, or values
+    static constexpr int kWarp = kPgStages * 2 * kHalf;
+    static constexpr int kRing = kPgWarps * kWarp;
+    // The ring's space holds the warps' outputs at the end: 16 rows of DP + 4
+    // floats each.
+    static constexpr int kOutRow = DP + 4;
+    static constexpr int kStats = kRing;                      // [warps][16] float2
+    static constexpr int kLive = kStats + kPgWarps * 16 * 8;  // [warps][stages] bits
+    static constexpr int kBytes = kLive + kPgWarps * kPgStages * 4;
+    static_assert(kPgWarps * 16 * kOutRow * 4 <= kRing, "outputs fit the ring");
+};
+
+// A sequence's length, and whether it is one the table can hold.
+__device__ __forceinline__ int length_of(const PagedTask& t, int b, bool& bad) {
+    const int n = t.lengths[b];
+    const int most = t.max_pages * t.page_size;
+    bad = n < 0 || n > most;
+    return n < 0 ? 0 : min(n, most);
+}
+
+// Writes elements d .. d + 7 of one head's output, and with d = 0 its lse,
+// from the joined maximum (in base 2), sum and unnormalised output.
+template <class T>
+__device__ __forceinline__ void paged_finish(const PagedTask& t, int b, int h, int d,
+                                             const float (&acc)[8], float top, float sum) {
+    if (d < t.d_head) {
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+        uint4 w;
+        w.x = T::pack(acc[0] * inv, acc[1] * inv);
+        w.y = T::pack(acc[2] * inv, acc[3] * inv);
+        w.z = T::pack(acc[4] * inv, acc[5] * inv);
+        w.w = T::pack(acc[6] * inv, acc[7] * inv);
+        *reinterpret_cast<uint4*>(t.out + b * t.o_stride[0] + h * t.o_stride[1] + d) = w;
+    }
+    if (d == 0) {
+        if (t.lse)
+            t.lse[static_cast<int64_t>(b) * t.heads + h] =
+                sum == 0.0f ? -INFINITY : (top + log2f(sum) - kWeightBits) * kLn2;
+        if (!isfinite(sum)) raise_error(t.err, kBitNan);
+    }
+}
+
+template <int DP, class T>
+__global__ void __launch_bounds__(kPgThreads)
+paged_kernel(const PagedTask t) {
+    using L = PgSmem<DP>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Head tiles are the fastest index (they share the chunk's keys through
+    // L2), then key heads (their rows are neighbours in a page), then chunks.
+    int64_t x = blockIdx.x;
+    const int ht = static_cast<int>(x % t.head_tiles);
+    x /= t.head_tiles;
+    const int hk = static_cast<int>(x % t.kv_heads);
+    x /= t.kv_heads;
+    const int chunk = static_cast<int>(x % t.chunks);
+    const int b = static_cast<int>(x / t.chunks);
+    bool bad;
+    const int len = length_of(t, b, bad);
+    if (bad && chunk == 0 && threadIdx.x == 0) raise_error(t.err, kBitBadPage);
+    const int t0 = chunk * t.chunk_tokens;
+    if (t0 >= len && chunk > 0) return;
+    const int t1 = min(len, t0 + t.chunk_tokens);
+    const int group = t.heads / t.kv_heads;
+    const int h0 = hk * group + 16 * ht;                 // first query head
+    const int nh = min(16, group - 16 * ht);             // query heads here
+
+    unsigned char* ring = smem + warp * L::kWarp;
+    volatile uint32_t* live =
+        reinterpret_cast<uint32_t*>(smem + L::kLive) + warp * kPgStages;
+    const int tiles = (t1 - t0 + kPgTile - 1) / kPgTile;
+    const int mine = tiles > warp ? (tiles - warp + kPgWarps - 1) / kPgWarps : 0;
+
+    // The page and slot of token (lane % 16) of this warp's tile i, -1 past
+    // the chunk, -2 for an entry that is no page; looked up one tile ahead.
+    auto locate = [&](int i, int& page, int& slot) {
+        const int tok = t0 + (warp + i * kPgWarps) * kPgTile + (lane & 15);
+        page = -1;
+        slot = 0;
+        if (i < mine && tok < t1) {
+            const int e = tok / t.page_size;
+            slot = tok - e * t.page_size;
+            page = t.page_table[b * t.table_stride + e];
+            if (page < 0 || page >= t.num_pages) page = -2;
+        }
+    };
+    const uint16_t* kbase = t.k_pages + hk * t.k_stride[2];
+    const uint16_t* vbase = t.v_pages + hk * t.v_stride[2];
+    // Starts the copies of tile i into stage st: kUnits 16-byte units a row,
+    // so 32 / kUnits rows at a time; zeros past d_head and for tokens that
+    // are not there.
+    constexpr int kUnits = DP / 8;
+    auto issue = [&](int st, int page, int slot) {
+        unsigned char* dk = ring + st * 2 * L::kHalf;
+        unsigned char* dv = dk + L::kHalf;
+        const uint32_t here = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+        if (lane == 0) live[st] = here;
+        if (__any_sync(0xffffffffu, page == -2) && lane == 0) raise_error(t.err, kBitBadPage);
+#pragma unroll
+        for (int n = 0; n < kPgTile * kUnits / 32; ++n) {
+            const int e = n * 32 + lane;
+            const int r = e / kUnits, u = e % kUnits;
+            const int pg = __shfl_sync(0xffffffffu, page, r);
+            const int sl = __shfl_sync(0xffffffffu, slot, r);
+            const bool copy = pg >= 0 && 8 * u < t.d_head;
+            const uint32_t bytes = copy ? 16u : 0u;   // 0: any address, not read
+            const uint16_t* ks = kbase + pg * t.k_stride[0] + sl * t.k_stride[1] + 8 * u;
+            const uint16_t* vs = vbase + pg * t.v_stride[0] + sl * t.v_stride[1] + 8 * u;
+            const int at = r * L::kRow + ((u ^ (r & 7)) << 4);
+            cp_async16_zfill(dk + at, copy ? ks : t.q, bytes);
+            cp_async16_zfill(dv + at, copy ? vs : t.q, bytes);
+        }
+    };
+
+    int page, slot;
+    locate(0, page, slot);
+#pragma unroll
+    for (int i = 0; i < kPgStages - 1; ++i) {
+        if (i < mine) issue(i, page, slot);
+        cp_async_commit();
+        locate(i + 1, page, slot);
+    }
+
+    // Query fragments: rows lane / 4 and lane / 4 + 8, columns 2 (lane % 4)
+    // and 8 more of each 16.
+    const int g = lane >> 2, c2 = 2 * (lane & 3);
+    uint32_t q[DP / 16][4];
+#pragma unroll
+    for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = g + 8 * (i & 1), col = 16 * ks + c2 + 8 * (i >> 1);
+            q[ks][i] = 0u;
+            if (row < nh && col < t.d_head)
+                q[ks][i] = *reinterpret_cast<const uint32_t*>(
+                    t.q + b * t.q_stride[0] + (h0 + row) * t.q_stride[1] + col);
+        }
+
+    const float c = t.scale * kLog2e;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float o[DP / 8][4];
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
+
+    const int mat = lane >> 3, r8 = lane & 7;
+    for (int i = 0; i < mine; ++i) {
+        const int st = i % kPgStages;
+        cp_async_wait_group<kPgStages - 2>();
+        __syncwarp();
+        // Stage (i - 1) % kPgStages was read before the __syncwarp.
+        if (i + kPgStages - 1 < mine) issue((i + kPgStages - 1) % kPgStages, page, slot);
+        cp_async_commit();
+        locate(i + kPgStages, page, slot);
+
+        const uint32_t sk = smem_addr(ring + st * 2 * L::kHalf), sv = sk + L::kHalf;
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+            const int row = (mat >> 1) * 8 + r8;
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) {
+                uint32_t k[4];
+                ldmatrix4(k, sk + row * L::kRow + (((2 * ks + (mat & 1)) ^ r8) << 4));
+                T::mma(s[0], q[ks], k[0], k[1]);
+                T::mma(s[1], q[ks], k[2], k[3]);
+            }
+        }
+        const uint32_t here = live[st];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = 8 * n + c2 + (k & 1);
+                s[n][k] = (here >> tok) & 1u ? s[n][k] * c : -INFINITY;
+            }
+        float top[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]),
+                           fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            top[r] = fmaxf(top[r], m[r]);
+        }
+        // m = -inf and a finite top: an infinite difference, above the lag.
+        if (__any_sync(0xffffffffu, top[0] - m[0] > kLagBits || top[1] - m[1] > kLagBits)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float f = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top[r]);
+                m[r] = top[r];
+                l[r] *= f;
+#pragma unroll
+                for (int n = 0; n < DP / 8; ++n) {
+                    o[n][2 * r] *= f;
+                    o[n][2 * r + 1] *= f;
+                }
+            }
+        }
+        float p[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float base = m[r] == -INFINITY ? 0.0f : m[r] - kWeightBits;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    p[n][2 * r + k] = ex2(s[n][2 * r + k] - base);
+                    l[r] += p[n][2 * r + k];
+                }
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = p[k >> 1][2 * (k & 1)], z = p[k >> 1][2 * (k & 1) + 1];
+            hi[k] = T::pack(a, z);
+            const float2 w = T::unpack(hi[k]);
+            lo[k] = T::pack(a - w.x, z - w.y);
+        }
+        {
+            const int row = (mat & 1) * 8 + r8;
+#pragma unroll
+            for (int n2 = 0; n2 < DP / 16; ++n2) {
+                uint32_t v[4];
+                ldmatrix4_trans(v, sv + row * L::kRow + (((2 * n2 + (mat >> 1)) ^ r8) << 4));
+                T::mma(o[2 * n2], hi, v[0], v[1]);
+                T::mma(o[2 * n2], lo, v[0], v[1]);
+                T::mma(o[2 * n2 + 1], hi, v[2], v[3]);
+                T::mma(o[2 * n2 + 1], lo, v[2], v[3]);
+            }
+        }
+    }
+    cp_async_wait_all();
+
+    // Join the warps: rows g and g + 8 of each, the row's sum over its four
+    // lanes first.
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    __syncthreads();   // every ring is read
+    float* outs = reinterpret_cast<float*>(smem);
+    float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        if ((lane & 3) == 0) stats[warp * 16 + row] = make_float2(m[r], l[r]);
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n)
+            *reinterpret_cast<float2*>(outs + (warp * 16 + row) * L::kOutRow + 8 * n + c2) =
+                make_float2(o[n][2 * r], o[n][2 * r + 1]);
+    }
+    __syncthreads();
+    const bool whole = len <= t.chunk_tokens;
+    for (int e = threadIdx.x; e < nh * (DP / 8); e += kPgThreads) {
+        const int row = e / (DP / 8), d = 8 * (e % (DP / 8));
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kPgWarps; ++w) top = fmaxf(top, stats[w * 16 + row].x);
+        float sum = 0.0f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kPgWarps; ++w) {
+            const float2 st = stats[w * 16 + row];
+            const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
+            sum = fmaf(st.y, f, sum);
+            const float4* a = reinterpret_cast<const float4*>(
+                outs + (w * 16 + row) * L::kOutRow + d);
+            const float4 a0 = a[0], a1 = a[1];
+            const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+        }
+        const int64_t bh = static_cast<int64_t>(b) * t.heads + h0 + row;
+        if (whole) {
+            paged_finish<T>(t, b, h0 + row, d, acc, top, sum);
+        } else {
+            const int64_t part = bh * t.chunks + chunk;
+            if (d == 0) t.part_stats[part] = make_float2(top, sum);
+            if (d < t.d_head) {
+                float4* w = reinterpret_cast<float4*>(t.part_out + part * t.d_head + d);
+                w[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                w[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            }
+        }
+    }
+}
+
+// Joins a head's chunks, one CTA a (sequence, head): every warp takes the
+// largest maximum and the sum over all chunks, then the CTA's threads, DP / 8
+// of them to a row, add the chunks' outputs.
+template <int DP, class T>
+__global__ void __launch_bounds__(kPgThreads)
+paged_join_kernel(const PagedTask t) {
+    constexpr int kUnits = DP / 8, kRows = kPgThreads / kUnits;
+    __shared__ float part[kRows][DP + 4];
+    const int b = static_cast<int>(blockIdx.x / t.heads);
+    const int h = static_cast<int>(blockIdx.x % t.heads);
+    bool bad;
+    const int len = length_of(t, b, bad);
+    if (len <= t.chunk_tokens) return;   // finished by its only chunk
+    const int n = (len + t.chunk_tokens - 1) / t.chunk_tokens;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * t.chunks;
+    const int lane = threadIdx.x & 31;
+    float top = -INFINITY, sum = 0.0f;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, t.part_stats[first + i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = lane; i < n; i += 32) {
+        const float2 st = t.part_stats[first + i];
+        sum = fmaf(st.y, st.x == -INFINITY ? 0.0f : ex2(st.x - top), sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int row = threadIdx.x / kUnits, d = 8 * (threadIdx.x % kUnits);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (d < t.d_head) {
+        for (int i = row; i < n; i += kRows) {
+            const float x = t.part_stats[first + i].x;
+            const float f = x == -INFINITY ? 0.0f : ex2(x - top);
+            const float4* a = reinterpret_cast<const float4*>(
+                t.part_out + (first + i) * t.d_head + d);
+            const float4 a0 = a[0], a1 = a[1];
+            const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[row][d + k] = acc[k];
+    __syncthreads();
+    if (threadIdx.x >= kUnits) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        acc[k] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) acc[k] += part[r][d + k];
+    }
+    paged_finish<T>(t, b, h, d, acc, top, sum);
+}
+
+template <int DP, class T>
+cudaError_t launch(const PagedTask& t, int slot, cudaStream_t stream) {
+    const void* kern = reinterpret_cast<const void*>(paged_kernel<DP, T>);
+    cudaError_t e = ensure_smem_attribute(kern, slot, PgSmem<DP>::kBytes, false);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(t.batch) * t.chunks * t.kv_heads * t.head_tiles;
+    paged_kernel<DP, T><<<static_cast<unsigned>(grid), kPgThreads, PgSmem<DP>::kBytes,
+                          stream>>>(t);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || t.chunks == 1) return e;
+    paged_join_kernel<DP, T><<<static_cast<unsigned>(t.batch * t.heads), kPgThreads, 0,
+                               stream>>>(t);
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_type(const PagedTask& t, int slot, cudaStream_t stream) {
+    if (t.d_head <= 64) return launch<64, T>(t, slot, stream);
+    if (t.d_head <= 128) return launch<128, T>(t, slot + 1, stream);
+    return launch<256, T>(t, slot + 2, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged(const PagedTask& task, cudaStream_t stream) {
+    return task.fp16 ? launch_type<PgFP16>(task, 62, stream)
+                     : launch_type<PgBF16>(task, 65, stream);
+}
+
+}  // namespace cs

@@ -45,7 +45,7 @@ extern "C" {
 #endif
 
 /* Status codes.  0-7 keep the numbering of section 5.1 (enum BurtError);
- * 8-10 are new.  4 (spectral overflow) and 5 (capacity full) belong to other
+ * 8-11 are new.  4 (spectral overflow) and 5 (capacity full) belong to other
  * kernels of that page and are never returned here. */
 typedef int32_t cs_status;
 #define CS_OK 0
@@ -57,6 +57,8 @@ typedef int32_t cs_status;
 #define CS_ERR_INVALID_ARG 8      /* null/overlapping pointers, bad params  */
 #define CS_ERR_CUDA 9             /* a CUDA call failed (launch, attribute)  */
 #define CS_ERR_TIMEOUT 10         /* a bounded device wait gave up (async)  */
+#define CS_ERR_BAD_PAGE 11        /* a cache length or page number out of
+                                     range (asynchronous)                   */
 
 /* Kernel variants (cs_options.variant, cs_plan.variant). */
 #define CS_VARIANT_AUTO 0
@@ -225,7 +227,7 @@ cs_status cs_check_args_bf16(const uint16_t* logits, const float* out,
  * Reads and clears the calling thread's current device's error word, then
  * synchronises `stream`.  *code_mask receives a bitmask of (1 << code) for
  * every asynchronous condition since the last call: CS_ERR_NAN_INPUT,
- * CS_ERR_INF_INPUT, CS_ERR_ENTROPY_OVERFLOW, CS_ERR_TIMEOUT.  The read and
+ * CS_ERR_INF_INPUT, CS_ERR_ENTROPY_OVERFLOW, CS_ERR_TIMEOUT, CS_ERR_BAD_PAGE.  The read and
  * the clear are one atomic exchange, made by a one-thread kernel on `stream`
  * after the work enqueued on it before this call.  The word is shared by
  * every launch on the device: a launch on another stream that runs
@@ -594,6 +596,82 @@ cs_status cs_check_fused_attention_backward_args(
     const uint16_t* grad_query, const uint16_t* grad_keys,
     const uint16_t* grad_values, const uint8_t* mask,
     const cs_attention_shape* shape, const void* workspace,
+    int64_t workspace_bytes);
+
+/*
+ * Attention of one new token per sequence over a key-value cache in pages,
+ * for serving.  The cache's pages are [num_pages, page_size, kv_heads,
+ * d_head] with the head dimension contiguous; token j of sequence b lies in
+ * slot j % page_size of page page_table[b][j / page_size].
+ */
+typedef struct cs_paged_shape {
+    int32_t batch;      /* sequences, >= 0                                  */
+    int32_t heads;      /* query heads, a positive multiple of kv_heads     */
+    int32_t kv_heads;   /* head h reads key head h / (heads / kv_heads)     */
+    int32_t d_head;     /* 8..256, a multiple of 8                          */
+    int32_t page_size;  /* tokens of a page, >= 1                           */
+    int32_t num_pages;  /* pages of the cache, >= 0                         */
+    int32_t max_pages;  /* entries of a page-table row, >= 0; at most 2^30
+                           tokens a row                                     */
+    int32_t fp16;       /* 0: query, pages and out are bf16; 1: fp16        */
+    float scale;        /* of the scores; positive and finite               */
+    int64_t q_stride[2];   /* batch, head; elements, non-negative           */
+    int64_t o_stride[2];   /* multiples of 8                                */
+    int64_t k_stride[3];   /* page, slot, head                              */
+    int64_t v_stride[3];
+    int64_t table_stride;  /* entries between page-table rows, >= max_pages */
+} cs_paged_shape;
+
+/*
+ * cs_paged_attention -- for every sequence b and query head h, over the
+ * tokens j < lengths[b]:
+ *
+ *   s_j = scale * (query . key_j),  lse = ln sum_j e^(s_j)
+ *   out = sum_j e^(s_j - lse) value_j
+ *
+ * query    device pointer, [batch, heads, d_head]; out the same, written
+ *          completely, overlapping nothing else of the call.
+ * key_pages, value_pages  device pointers.  All four 16-byte aligned.
+ * page_table  device pointer, int32.  Entries past a sequence's length are
+ *          not read, nor are a page's slots past it.
+ * lengths  device pointer, [batch] int32: tokens in the cache, the new one's
+ *          included when it has been written there.  0 gives zeros and
+ *          lse = -inf.
+ * lse      optional device pointer, [batch, heads] fp32, contiguous.
+ * workspace  device pointer, 16-byte aligned, at least
+ *          cs_paged_attention_workspace(shape) bytes (NULL when that is 0):
+ *          the caller's, used by this call only, free after it on the stream.
+ *
+ * A length that is negative or past the table's row is taken as 0 or the
+ * row's tokens, and a token whose page number is outside 0..num_pages-1 is
+ * left out; both OR CS_ERR_BAD_PAGE into the error word.  Sums are fp32 in a
+ * fixed order (repeated calls give the same bits, whatever else runs).  NaN
+ * or infinite scores propagate by IEEE arithmetic and OR CS_ERR_NAN_INPUT
+ * into the error word.  Ownership, execution and errors: as
+ * cs_constrained_softmax.
+ */
+cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
+                             const uint16_t* value_pages,
+                             const int32_t* page_table,
+                             const int32_t* lengths, uint16_t* out,
+                             float* lse, const cs_paged_shape* shape,
+                             void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of workspace the call needs (0 when no row of the table is longer
+ * than a chunk); negative for a malformed shape.  Host-only. */
+int64_t cs_paged_attention_workspace(const cs_paged_shape* shape);
+
+/* Tokens of the chunks a sequence is cut into; negative for a malformed
+ * shape.  Host-only. */
+int32_t cs_paged_attention_chunk(const cs_paged_shape* shape);
+
+/* Host-only argument check (no CUDA call). */
+cs_status cs_check_paged_attention_args(
+    const uint16_t* query, const uint16_t* key_pages,
+    const uint16_t* value_pages, const int32_t* page_table,
+    const int32_t* lengths, const uint16_t* out, const float* lse,
+    const cs_paged_shape* shape, const void* workspace,
     int64_t workspace_bytes);
 
 /*
