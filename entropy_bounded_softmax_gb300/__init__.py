@@ -17,6 +17,8 @@ raise if the library is missing or the tensors are not on a CUDA device.
 """
 from __future__ import annotations
 
+import contextlib
+
 from . import _lib
 from ._lib import (CONSTANTS, cs_attention_softmax, cs_attention_softmax_ex,
                    cs_attention_shape, cs_biencoder_attention,
@@ -83,6 +85,9 @@ ERROR_BITS = {name: 1 << CONSTANTS[f"CS_ERR_{name}"]
                            "TIMEOUT", "BAD_PAGE")}
 
 
+_STAY = contextlib.nullcontext()
+
+
 class CsError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -103,10 +108,9 @@ def _stream_handle(device) -> int:
 def _on_device(device):
     """A context that makes `device` current: none when it already is (the
     common case, and the cheapest: the call is on every step's path)."""
-    import contextlib
     import torch
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _STAY
     return torch.cuda.device(device)
 
 
@@ -331,84 +335,77 @@ def biencoder_attention(query, keys, values, scale=None,
     return res if len(res) > 1 else out
 
 
-def _heads_like(x):
-    """An uninitialised tensor of x's shape: in x's memory order where that is
-    one of a whole tensor's (so a [B, S, H, D] projection seen as
-    [B, H, S, D] keeps its order), else contiguous."""
+def _heads(name, x, shape, device):
+    """The strides and the address of a [batch, heads, length, d_head] bf16
+    tensor, checked: on the CUDA device of that index, of the given shape, in
+    strides that the tensor copies take."""
     import torch
-    return torch.empty_like(x)
-
-
-def _check_heads(name, x, shape=None, device=None) -> None:
-    import torch
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
-    if x.dim() != 4:
-        raise ValueError(f"{name} must be 4-D [batch, heads, length, d_head]")
-    if device is not None and x.device != device:
+    if x.get_device() != device:
         raise ValueError(f"{name} must be on the query's device")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if x.numel() == 0:
-        return
     st = x.stride()
-    if x.shape[3] > 1 and st[3] != 1:
-        raise ValueError(f"{name}'s head dimension must be contiguous")
-    if (x.data_ptr() % 16 or any(n > 1 and (s <= 0 or s % 8)
-                                 for n, s in zip(x.shape[:3], st[:3]))):
-        raise ValueError(f"{name}'s base must be 16-byte aligned and its "
-                         "batch, head and position strides positive multiples "
-                         "of 8 elements")
+    ptr = x.data_ptr()
+    s0, s1, s2, s3 = st
+    if (s3 != 1 or (ptr | 2 * (s0 | s1 | s2)) & 15
+            or s0 <= 0 or s1 <= 0 or s2 <= 0) and x.numel():
+        # Strides of dimensions of one element do not matter.
+        if s3 != 1:
+            raise ValueError(f"{name}'s head dimension must be contiguous")
+        if ptr & 15 or any(n > 1 and (s <= 0 or s % 8)
+                           for n, s in zip(shape[:3], st)):
+            raise ValueError(f"{name}'s base must be 16-byte aligned and its "
+                             "batch, head and position strides positive "
+                             "multiples of 8 elements")
+    return st, ptr
 
 
-def _attention_shape(query, keys, values, mask, causal, scale):
-    """The checked inputs of fused attention: (shape, mask pointer)."""
+def _attention_inputs(query, keys, values, mask, scale):
+    """The checked inputs of fused attention: the query's device index, the
+    two shapes, the scale, and (strides, address) of query, keys, values and
+    the mask's row stride and address."""
     import math
     import torch
-    _check_heads("query", query)
-    B, H, Sq, D = query.shape
-    _check_heads("keys", keys, device=query.device)
-    Hk, Sk = keys.shape[1], keys.shape[2]
-    if keys.shape[0] != B or keys.shape[3] != D:
+    for name, x in (("query", query), ("keys", keys)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.dim() != 4:
+            raise ValueError(f"{name} must be 4-D [batch, heads, length, "
+                             "d_head]")
+    dev = query.get_device()
+    qs, ks = query.shape, keys.shape
+    B, H, _, D = qs
+    Hk, Sk = ks[1], ks[2]
+    if ks[0] != B or ks[3] != D:
         raise ValueError("keys must be [batch, kv_heads, key_len, d_head] "
                          "with the query's batch and d_head")
-    _check_heads("values", values, keys.shape, query.device)
     if Hk < 1 or H < 1 or H % Hk:
         raise ValueError("the query's heads must be a multiple of the keys'")
     if D < 8 or D > 128 or D % 8:
         raise ValueError("d_head must be a multiple of 8 in 8..128")
+    q = _heads("query", query, qs, dev)
+    k = _heads("keys", keys, ks, dev)
+    v = _heads("values", values, ks, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    if not (scale > 0.0 and math.isfinite(scale)):
+    elif not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
-    m_ptr, m_stride = None, Sk
+    m = (Sk, None)
     if mask is not None:
         if (not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool
-                or mask.device != query.device
-                or tuple(mask.shape) != (B, Sk)):
+                or mask.device != query.device or mask.shape != (B, Sk)):
             raise ValueError("mask must be a bool [batch, key_len] tensor on "
                              "the query's device")
-        if ((Sk > 1 and mask.stride(1) != 1)
-                or (B > 1 and mask.stride(0) < Sk)):
+        s0, s1 = mask.stride()
+        if (Sk > 1 and s1 != 1) or (B > 1 and s0 < Sk):
             raise ValueError("mask's rows must be contiguous and not overlap")
         if mask.numel():
-            m_ptr, m_stride = mask.data_ptr(), mask.stride(0)
-    shape = cs_attention_shape(B, H, Hk, Sq, Sk, D, int(bool(causal)),
-                               float(scale), query.stride()[:3],
-                               keys.stride()[:3], values.stride()[:3])
-    shape.mask_stride = m_stride
-    return shape, m_ptr
-
-
-def _check_lse(lse, query) -> None:
-    import torch
-    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32
-            or lse.shape != query.shape[:3] or lse.device != query.device
-            or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [batch, heads, "
-                         "query_len] tensor on the query's device")
+            m = (s0, mask.data_ptr())
+    return dev, qs, ks, scale, q, k, v, m
 
 
 def fused_attention(query, keys, values, mask=None, causal: bool = False,
@@ -431,21 +428,23 @@ def fused_attention(query, keys, values, mask=None, causal: bool = False,
     :func:`get_error`.
     """
     import torch
-    shape, m_ptr = _attention_shape(query, keys, values, mask, causal, scale)
+    dev, qs, ks, scale, q, k, v, m = _attention_inputs(query, keys, values,
+                                                       mask, scale)
+    B, H, Sq, D = qs
     if out is None:
-        out = _heads_like(query)
-    else:
-        _check_heads("out", out, query.shape, query.device)
-    shape.o_stride = out.stride()[:3]
+        out = torch.empty_like(query)
+    o = _heads("out", out, qs, dev)
     lse = None
     if return_lse:
-        lse = torch.empty(query.shape[:3], dtype=torch.float32,
+        lse = torch.empty((B, H, Sq), dtype=torch.float32,
                           device=query.device)
+    shape = _lib.pack_attention_shape(
+        B, H, ks[1], Sq, ks[2], D, 1 if causal else 0, scale, q[0], k[0],
+        v[0], o[0], mask_stride=m[0])
     with _on_device(query.device):
-        st = cs_fused_attention(
-            query.data_ptr(), keys.data_ptr(), values.data_ptr(),
-            out.data_ptr(), lse.data_ptr() if return_lse else None, m_ptr,
-            shape, _stream_handle(query.device))
+        st = cs_fused_attention(q[1], k[1], v[1], o[1],
+                                lse.data_ptr() if return_lse else None, m[1],
+                                shape, _stream_handle(query.device))
     if st != 0:
         raise CsError(st, "cs_fused_attention")
     return (out, lse) if return_lse else out
@@ -461,46 +460,72 @@ def fused_attention_backward(query, keys, values, out, lse, grad_output,
     zeros.  Asynchronous on the current stream.
     """
     import torch
-    shape, m_ptr = _attention_shape(query, keys, values, mask, causal, scale)
-    _check_heads("out", out, query.shape, query.device)
-    _check_heads("grad_output", grad_output, query.shape, query.device)
-    _check_lse(lse, query)
-    grads = [_heads_like(x) for x in (query, keys, values)]
-    shape.o_stride = out.stride()[:3]
-    shape.go_stride = grad_output.stride()[:3]
-    shape.dq_stride, shape.dk_stride, shape.dv_stride = (
-        g.stride()[:3] for g in grads)
+    dev, qs, ks, scale, q, k, v, m = _attention_inputs(query, keys, values,
+                                                       mask, scale)
+    B, H, Sq, D = qs
+    o = _heads("out", out, qs, dev)
+    go = _heads("grad_output", grad_output, qs, dev)
+    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32
+            or lse.shape != qs[:3] or lse.get_device() != dev
+            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [batch, heads, "
+                         "query_len] tensor on the query's device")
+    grads = (torch.empty_like(query), torch.empty_like(keys),
+             torch.empty_like(values))
+    dq, dk, dv = (_heads("gradient", g, s, dev)
+                  for g, s in zip(grads, (qs, ks, ks)))
+    shape = _lib.pack_attention_shape(
+        B, H, ks[1], Sq, ks[2], D, 1 if causal else 0, scale, q[0], k[0],
+        v[0], o[0], go[0], dq[0], dk[0], dv[0], m[0])
     size = cs_fused_attention_backward_workspace(shape)
     work = torch.empty(max(size, 0), dtype=torch.uint8, device=query.device)
     with _on_device(query.device):
         st = cs_fused_attention_backward(
-            query.data_ptr(), keys.data_ptr(), values.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), grad_output.data_ptr(),
-            *(g.data_ptr() for g in grads), m_ptr, shape, work.data_ptr(),
-            size, _stream_handle(query.device))
+            q[1], k[1], v[1], o[1], lse.data_ptr(), go[1], dq[1], dk[1],
+            dv[1], m[1], shape, work.data_ptr(), size,
+            _stream_handle(query.device))
     if st != 0:
         raise CsError(st, "cs_fused_attention_backward")
-    return tuple(grads)
+    return grads
 
 
-def _check_rows(name, x, dim, dtype, device) -> None:
+def _rows(name, x, shape, dtype, device):
+    """The strides and the address of a strided tensor with a contiguous last
+    dimension, checked: on the CUDA device of that index, of the given shape
+    and type, 16-byte aligned rows."""
     import torch
-    if (not isinstance(x, torch.Tensor) or x.device.type != "cuda"
-            or (device is not None and x.device != device)):
+    if (not isinstance(x, torch.Tensor) or not x.is_cuda
+            or x.get_device() != device):
         raise ValueError(f"{name} must be a CUDA tensor on one device with "
                          "the others")
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if x.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions")
-    if x.numel() == 0:
-        return
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
     st = x.stride()
-    if (st[-1] != 1 or x.data_ptr() % 16
-            or any(n > 1 and s % 8 for n, s in zip(x.shape[:-1], st))):
+    ptr = x.data_ptr()
+    if x.numel() and (st[-1] != 1 or ptr & 15 or any(
+            n > 1 and s & 7 for n, s in zip(shape[:-1], st))):
         raise ValueError(f"{name}'s last dimension must be contiguous, its "
                          "base 16-byte aligned and its other strides "
                          "multiples of 8 elements")
+    return st, ptr
+
+
+def _index_rows(name, x, dim, rows, device):
+    """The strides and the address of an int32 tensor of page numbers or
+    lengths, checked."""
+    import torch
+    if (not isinstance(x, torch.Tensor) or x.dtype is not torch.int32
+            or x.get_device() != device or x.dim() != dim
+            or x.shape[0] != rows):
+        raise ValueError(f"{name} must be an int32 tensor of the batch's "
+                         "rows on the query's device")
+    st = x.stride()
+    if x.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last "
+                         "dimension")
+    return st, x.data_ptr()
 
 
 def paged_attention(query, key_pages, value_pages, page_table, lengths,
@@ -522,16 +547,19 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
     """
     import math
     import torch
-    dtype = query.dtype if isinstance(query, torch.Tensor) else None
-    if dtype not in (torch.bfloat16, torch.float16):
+    for name, x, dim in (("query", query, 3), ("key_pages", key_pages, 4)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.dim() != dim:
+            raise ValueError(f"{name} must have {dim} dimensions")
+    dtype = query.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError("query must be a bfloat16 or float16 tensor")
-    dev = query.device
-    _check_rows("query", query, 3, dtype, None)
-    _check_rows("key_pages", key_pages, 4, dtype, dev)
-    _check_rows("value_pages", value_pages, 4, dtype, dev)
-    B, H, D = query.shape
-    pages, page_size, Hk, _ = key_pages.shape
-    if key_pages.shape[3] != D or value_pages.shape != key_pages.shape:
+    dev = query.get_device()
+    qs, ps = query.shape, key_pages.shape
+    B, H, D = qs
+    pages, page_size, Hk, _ = ps
+    if ps[3] != D:
         raise ValueError("key_pages and value_pages must both be "
                          "[pages, page_size, kv_heads, d_head] with the "
                          "query's d_head")
@@ -540,45 +568,38 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
                          "pages', and page_size positive")
     if D < 8 or D > 256 or D % 8:
         raise ValueError("d_head must be a multiple of 8 in 8..256")
-    for name, x, dim in (("page_table", page_table, 2),
-                         ("lengths", lengths, 1)):
-        if (not isinstance(x, torch.Tensor) or x.dtype != torch.int32
-                or x.device != dev or x.dim() != dim or x.shape[0] != B
-                or (x.shape[-1] > 1 and x.stride(-1) != 1)):
-            raise ValueError(f"{name} must be an int32 tensor of the batch's "
-                             "rows, contiguous along its last dimension, on "
-                             "the query's device")
-    if B > 1 and page_table.stride(0) < page_table.shape[1]:
+    q = _rows("query", query, qs, dtype, dev)
+    k = _rows("key_pages", key_pages, ps, dtype, dev)
+    v = _rows("value_pages", value_pages, ps, dtype, dev)
+    table = _index_rows("page_table", page_table, 2, B, dev)
+    count = _index_rows("lengths", lengths, 1, B, dev)
+    most = page_table.shape[1]
+    if B > 1 and table[0][0] < most:
         raise ValueError("page_table's rows must not overlap")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    if not (scale > 0.0 and math.isfinite(scale)):
+    elif not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
     if out is None:
-        out = torch.empty((B, H, D), dtype=dtype, device=dev)
-    else:
-        _check_rows("out", out, 3, dtype, dev)
-        if out.shape != query.shape:
-            raise ValueError("out must be shaped like query")
+        out = torch.empty((B, H, D), dtype=dtype, device=query.device)
+    o = _rows("out", out, qs, dtype, dev)
     lse = None
     if return_lse:
-        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
-    shape = cs_paged_shape(
-        B, H, Hk, D, page_size, pages, page_table.shape[1],
-        int(dtype == torch.float16), float(scale), query.stride()[:2],
-        out.stride()[:2], key_pages.stride()[:3], value_pages.stride()[:3],
-        page_table.stride(0))
+        lse = torch.empty((B, H), dtype=torch.float32, device=query.device)
+    shape = _lib.pack_paged_shape(
+        B, H, Hk, D, page_size, pages, most,
+        1 if dtype is torch.float16 else 0, scale, q[0], o[0], k[0], v[0],
+        table[0][0])
     size = cs_paged_attention_workspace(shape)
     work = None
     if size > 0:
-        work = torch.empty(size, dtype=torch.uint8, device=dev)
-    with _on_device(dev):
+        work = torch.empty(size, dtype=torch.uint8, device=query.device)
+    with _on_device(query.device):
         st = cs_paged_attention(
-            query.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
-            page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+            q[1], k[1], v[1], table[1], count[1], o[1],
             lse.data_ptr() if return_lse else None, shape,
             work.data_ptr() if work is not None else None, max(size, 0),
-            _stream_handle(dev))
+            _stream_handle(query.device))
     if st != 0:
         raise CsError(st, "cs_paged_attention")
     return (out, lse) if return_lse else out

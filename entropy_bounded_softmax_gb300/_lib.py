@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -93,6 +94,38 @@ class cs_paged_shape(ctypes.Structure):
     ]
 
 
+_PACK_ATTENTION = struct.Struct("=7if25q")
+_PACK_PAGED = struct.Struct("=8ifxxxx11q")
+_NONE3 = (0, 0, 0)
+
+
+def pack_attention_shape(batch, heads, kv_heads, query_len, key_len, d_head,
+                         causal, scale, q, k, v, o, go=_NONE3, dq=_NONE3,
+                         dk=_NONE3, dv=_NONE3, mask_stride=0) -> bytes:
+    """The bytes of a cs_attention_shape, which every function that takes one
+    also takes; q .. dv: element strides, the first three of each are used.
+    (Filling the ctypes struct costs more than the launch.)"""
+    return _PACK_ATTENTION.pack(
+        batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
+        q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
+        o[0], o[1], o[2], go[0], go[1], go[2], dq[0], dq[1], dq[2],
+        dk[0], dk[1], dk[2], dv[0], dv[1], dv[2], mask_stride)
+
+
+def pack_paged_shape(batch, heads, kv_heads, d_head, page_size, num_pages,
+                     max_pages, fp16, scale, q, o, k, v,
+                     table_stride) -> bytes:
+    """The bytes of a cs_paged_shape (as pack_attention_shape)."""
+    return _PACK_PAGED.pack(
+        batch, heads, kv_heads, d_head, page_size, num_pages, max_pages,
+        fp16, scale, q[0], q[1], o[0], o[1], k[0], k[1], k[2],
+        v[0], v[1], v[2], table_stride)
+
+
+def _shape_ref(shape):
+    return shape if type(shape) is bytes else ctypes.byref(shape)
+
+
 def _header_constants() -> dict[str, int]:
     """The #define'd integer constants of the public header."""
     out = {}
@@ -170,26 +203,26 @@ _SIGNATURES = {
                                        _I32, _I32, _F32, _F32, _F32, _F32,
                                        _I32, _VP, _VP]),
     "cs_fused_attention": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP,
-                                  ctypes.POINTER(cs_attention_shape), _VP]),
+                                  _VP, _VP]),
     "cs_fused_attention_backward": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
-               ctypes.POINTER(cs_attention_shape), _VP, _I64, _VP]),
+               _VP, _VP, _I64, _VP]),
     "cs_fused_attention_backward_workspace": (
-        _I64, [ctypes.POINTER(cs_attention_shape)]),
+        _I64, [_VP]),
     "cs_check_fused_attention_args": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP,
-               ctypes.POINTER(cs_attention_shape)]),
+               _VP]),
     "cs_check_fused_attention_backward_args": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
-               ctypes.POINTER(cs_attention_shape), _VP, _I64]),
+               _VP, _VP, _I64]),
     "cs_paged_attention": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
-               ctypes.POINTER(cs_paged_shape), _VP, _I64, _VP]),
-    "cs_paged_attention_workspace": (_I64, [ctypes.POINTER(cs_paged_shape)]),
-    "cs_paged_attention_chunk": (_I32, [ctypes.POINTER(cs_paged_shape)]),
+               _VP, _VP, _I64, _VP]),
+    "cs_paged_attention_workspace": (_I64, [_VP]),
+    "cs_paged_attention_chunk": (_I32, [_VP]),
     "cs_check_paged_attention_args": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
-               ctypes.POINTER(cs_paged_shape), _VP, _I64]),
+               _VP, _VP, _I64]),
     "cs_probe_ex2": (_I32, [_VP, _I32, ctypes.POINTER(_I64), _VP]),
     "cs_probe_ex2_sink_floats": (_I32, []),
     "cs_test_wait_timeout": (_I32, [_I64, _VP]),
@@ -416,7 +449,7 @@ def cs_check_biencoder_args(query, keys, values, output, batch_size,
 def cs_fused_attention(query, keys, values, out, lse, mask, shape,
                        stream) -> int:
     return load().cs_fused_attention(query, keys, values, out, lse, mask,
-                                     ctypes.byref(shape), stream)
+                                     _shape_ref(shape), stream)
 
 
 def cs_fused_attention_backward(query, keys, values, out, lse, grad_out,
@@ -425,18 +458,18 @@ def cs_fused_attention_backward(query, keys, values, out, lse, grad_out,
                                 stream) -> int:
     return load().cs_fused_attention_backward(
         query, keys, values, out, lse, grad_out, grad_query, grad_keys,
-        grad_values, mask, ctypes.byref(shape), workspace, workspace_bytes,
+        grad_values, mask, _shape_ref(shape), workspace, workspace_bytes,
         stream)
 
 
 def cs_fused_attention_backward_workspace(shape) -> int:
-    return load().cs_fused_attention_backward_workspace(ctypes.byref(shape))
+    return load().cs_fused_attention_backward_workspace(_shape_ref(shape))
 
 
 def cs_check_fused_attention_args(query, keys, values, out, lse, mask,
                                   shape) -> int:
     return load().cs_check_fused_attention_args(query, keys, values, out, lse,
-                                                mask, ctypes.byref(shape))
+                                                mask, _shape_ref(shape))
 
 
 def cs_check_fused_attention_backward_args(query, keys, values, out, lse,
@@ -446,7 +479,7 @@ def cs_check_fused_attention_backward_args(query, keys, values, out, lse,
                                            workspace_bytes) -> int:
     return load().cs_check_fused_attention_backward_args(
         query, keys, values, out, lse, grad_out, grad_query, grad_keys,
-        grad_values, mask, ctypes.byref(shape), workspace, workspace_bytes)
+        grad_values, mask, _shape_ref(shape), workspace, workspace_bytes)
 
 
 def cs_paged_attention(query, key_pages, value_pages, page_table, lengths,
@@ -454,15 +487,15 @@ def cs_paged_attention(query, key_pages, value_pages, page_table, lengths,
                        stream) -> int:
     return load().cs_paged_attention(
         query, key_pages, value_pages, page_table, lengths, out, lse,
-        ctypes.byref(shape), workspace, workspace_bytes, stream)
+        _shape_ref(shape), workspace, workspace_bytes, stream)
 
 
 def cs_paged_attention_workspace(shape) -> int:
-    return load().cs_paged_attention_workspace(ctypes.byref(shape))
+    return load().cs_paged_attention_workspace(_shape_ref(shape))
 
 
 def cs_paged_attention_chunk(shape) -> int:
-    return load().cs_paged_attention_chunk(ctypes.byref(shape))
+    return load().cs_paged_attention_chunk(_shape_ref(shape))
 
 
 def cs_check_paged_attention_args(query, key_pages, value_pages, page_table,
@@ -470,7 +503,7 @@ def cs_check_paged_attention_args(query, key_pages, value_pages, page_table,
                                   workspace_bytes) -> int:
     return load().cs_check_paged_attention_args(
         query, key_pages, value_pages, page_table, lengths, out, lse,
-        ctypes.byref(shape), workspace, workspace_bytes)
+        _shape_ref(shape), workspace, workspace_bytes)
 
 
 def cs_probe_ex2(sink, iters, stream) -> tuple[int, int]:

@@ -8,25 +8,32 @@
 // Two launches of one kernel, so that every sum stays in one CTA's tensor
 // memory: no atomics, the same bits every time, no fp32 copy of a gradient
 // in memory.  They recompute P twice (seven products instead of five).
-//   queries (KV = false)  128 query rows a CTA, over blocks of 64 keys:
+//   queries (KV = false)  128 query rows a CTA, over blocks of 128 keys:
 //       S = Q K^T, G V^T, dq += dS K.  Before its blocks it takes delta of
 //       its rows and leaves delta and lse, in base 2 and padded to whole
 //       tiles, in the workspace for the second launch;
-//   keys (KV = true)      128 key rows a CTA, over blocks of 64 queries of
+//   keys (KV = true)      128 key rows a CTA, over blocks of 128 queries of
 //       every head of its group: S^T = K Q^T, V G^T, dv += P^T G,
 //       dk += dS^T Q.
 // In both the fixed tiles' rows are the lanes of tensor memory, and the
-// weights, rounded to bf16 in the columns their scores had, are the next
-// product's A operand there.  Roles:
-//   warps 0-3, 4-7  the elementwise part of even and odd blocks, one row a
-//                   thread, 64 columns of S and of G V^T in registers;
-//   warp 8          issues the products: block i's sums, then block i + 2's
-//                   scores into the columns that block i has left, so that
-//                   the products of one block run under the elementwise
-//                   part of the other;
-//   warp 9          tensor copies: the two fixed tiles, then the blocks;
-//   warp 10         queries with a key mask only: a block's kept keys as
-//                   bits, and zeros over the removed keys' rows of K.
+// weights, rounded to bf16 in columns their scores had, are the next
+// product's A operand there.  Products of 128 columns, because one of 64
+// reads its A tile from shared memory twice as often and is bound by that.
+//
+// Tensor memory holds two sums, S and G V^T (keys), or one sum, S and two of
+// G V^T (queries).  The elementwise part has two phases, P from S and dS from
+// P and G V^T, and the products are issued so that each phase runs under
+// products that do not wait for it:
+//   keys     dv(i), S(i+1), dk(i), G V^T(i+1): P(i+1) under dk(i) and
+//            G V^T(i+1), dS(i) under dv(i) and S(i+1);
+//   queries  S(i+1), G V^T(i+1), dq(i): P(i) and dS(i) under the first two.
+// Roles:
+//   warps 0-7   the elementwise part, a row and 64 of its columns a thread
+//               (warps w and w + 4 share the rows of lanes 32 (w % 4) ..);
+//   warp 8      issues the products;
+//   warp 9      tensor copies: the two fixed tiles, then the blocks;
+//   warp 10     queries with a key mask only: a block's kept keys as bits,
+//               and zeros over the removed keys' rows of K.
 //
 // P and dS are rounded to bf16, the operand type next to bf16 values (a sum
 // over many rows averages those roundings); everything else stays fp32.
@@ -45,26 +52,40 @@ constexpr int kBwdMmaWarp = 8;
 constexpr int kBwdLoadWarp = 9;
 constexpr int kBwdMaskWarp = 10;
 constexpr uint32_t kBwdTmemCols = 512;
-constexpr uint32_t kBarCompute = 1;
-constexpr int kBlk = 64;                       // rows of a streamed block
+constexpr uint32_t kBarElementwise = 1;
+constexpr uint32_t kElementwise = 256;         // threads
 
+// The first streamed tensor (K, or Q) is read by a block's first and last
+// product, the second (V, or G) by the ones between: three stages and two.
 template <int DP>
 struct BwdSmem {
     static constexpr int kTile = 128 * DP * 2;
-    static constexpr int kBlock = kBlk * DP * 2;
-    static constexpr int kStages = 4;
+    static constexpr int kStages1 = 3, kStages2 = 2, kStagesR = 2;
     static constexpr int kA1 = 0;              // Q, or K
     static constexpr int kA2 = kA1 + kTile;    // G, or V
-    static constexpr int kB = kA2 + kTile;     // [kStages] of K, V or of Q, G
-    static constexpr int kStage = 2 * kBlock;
-    static constexpr int kRows = kB + kStages * kStage;   // [kStages][2][64] lse, delta
-    static constexpr int kDelta = kRows + kStages * 2 * kBlk * 4;   // [128]
-    static constexpr int kBars = kDelta + 128 * 4;
-    static constexpr int kNumBars = 1 + 3 * kStages + 2 + 2 + 1 + 1;
-    static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages][2]
-    static constexpr int kFlags = kWords + kStages * 8;
-    static constexpr int kBytes = kFlags + 16 + 1024;
+    static constexpr int kB1 = kA2 + kTile;
+    static constexpr int kB2 = kB1 + kStages1 * kTile;
+    static constexpr int kRows = kB2 + kStages2 * kTile;  // [kStagesR][2][128] lse, delta
+    static constexpr int kBars = kRows + kStagesR * 2 * 128 * 4;
+    static constexpr int kNumBars =
+        1 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 6 + 2;
+    static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages1][4]
+    static constexpr int kFlags = kWords + kStages1 * 16;
+    static constexpr int kBytes = kFlags + 16;
 };
+
+// D[128 x DP] (+)= W[128 x 128] . B[128 x DP], W bf16 in tensor memory, the
+// two halves of its columns 64 columns of 32 bits apart; B a tile.
+template <int DP>
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t w, uint32_t b,
+                                            bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16(128, DP, true);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        mma_bf16_ts(d, w + 64 * (ks >> 2) + 8 * (ks & 3),
+                    smem_desc_mn_sw128(b + ks * 2048, 128 * 128, 1024), idesc,
+                    accumulate || ks > 0);
+}
 
 template <int DP, bool KV>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -73,20 +94,27 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                  const __grid_constant__ CUtensorMap map_b1,
                  const __grid_constant__ CUtensorMap map_b2) {
     using L = BwdSmem<DP>;
-    constexpr int NS = L::kStages;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    constexpr int N1 = L::kStages1, N2 = L::kStages2, NR = L::kStagesR;
+    // The tiles need 1024-byte alignment, and fill the shared memory that a
+    // CTA can have up to a few hundred bytes; there are no static variables.
+    extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t* a_full = bars;                   // the fixed tiles landed
-    uint64_t* b_full = a_full + 1;             // [NS] ring stage landed
-    uint64_t* b_empty = b_full + NS;           // [NS] products that read it completed
-    uint64_t* b_masked = b_empty + NS;         // [NS] removed rows zeroed, bits written
-    uint64_t* s_full = b_masked + NS;          // [2] scores of an even, odd block
-    uint64_t* w_full = s_full + 2;             // [2] its weights
-    uint64_t* sums_full = w_full + 2;          // every sum completed
+    uint64_t* b1_full = a_full + 1;            // [N1] ring stage landed
+    uint64_t* b1_empty = b1_full + N1;         // [N1] products that read it completed
+    uint64_t* b1_masked = b1_empty + N1;       // [N1] removed rows zeroed, bits written
+    uint64_t* b2_full = b1_masked + N1;        // [N2]
+    uint64_t* b2_empty = b2_full + N2;
+    uint64_t* r_full = b2_empty + N2;          // [NR] keys: lse and delta landed
+    uint64_t* r_empty = r_full + NR;
+    uint64_t* s_full = r_empty + NR;           // a block's scores
+    uint64_t* s_read = s_full + 1;             // queries: in registers
+    uint64_t* g_full = s_read + 1;             // [2] its G V^T, by buffer
+    uint64_t* p_full = g_full + 2;             // keys: its P
+    uint64_t* d_full = p_full + 1;             // its dS
+    uint64_t* sums_full = d_full + 1;          // every sum completed
     uint64_t* drained = sums_full + 1;
     float* rows_s = reinterpret_cast<float*>(smem + L::kRows);
-    float* delta_s = reinterpret_cast<float*>(smem + L::kDelta);
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
@@ -111,15 +139,25 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
 
     if (threadIdx.x == 0) {
         mbar_init(a_full, 1u);
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&b_full[i], 1u);
-            mbar_init(&b_empty[i], 1u);
-            mbar_init(&b_masked[i], 1u);
+        for (int i = 0; i < N1; ++i) {
+            mbar_init(&b1_full[i], 1u);
+            mbar_init(&b1_empty[i], 1u);
+            mbar_init(&b1_masked[i], 1u);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1u);
-            mbar_init(&w_full[i], 4u);
+        for (int i = 0; i < N2; ++i) {
+            mbar_init(&b2_full[i], 1u);
+            mbar_init(&b2_empty[i], 1u);
         }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&r_full[i], 1u);
+            mbar_init(&r_empty[i], 8u);
+        }
+        mbar_init(s_full, 1u);
+        mbar_init(s_read, 8u);
+        mbar_init(&g_full[0], 1u);
+        mbar_init(&g_full[1], 1u);
+        mbar_init(p_full, 8u);
+        mbar_init(d_full, 8u);
         mbar_init(sums_full, 1u);
         mbar_init(drained, 1u);
         flags[0] = 0u;
@@ -143,29 +181,33 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     if (KV) {
         // Queries with a kept key in the tile: i >= a0 - off under causal.
         const int lo = t.causal ? max(0, a0 - off) : 0;
-        first = lo / kBlk;
+        first = lo >> 7;
         if (lo < t.query_len && a0 < key_hi && last >= key_lo)
-            per = (t.query_len + kBlk - 1) / kBlk - first;
+            per = ((t.query_len + 127) >> 7) - first;
     } else {
         const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
-        first = key_lo / kBlk;
-        if (hi > key_lo) per = (hi + kBlk - 1) / kBlk - first;
+        first = key_lo >> 7;
+        if (hi > key_lo) per = ((hi + 127) >> 7) - first;
     }
     const int blocks = KV ? per * group : per;
     // Block i's head on the streamed side and its first row there.
     auto block_head = [&](int i) { return KV ? ha * group + i / per : ha / group; };
-    auto block_row = [&](int i) { return kBlk * (first + (KV ? i % per : i)); };
+    auto block_row = [&](int i) { return (first + (KV ? i % per : i)) << 7; };
     const uint32_t acc1 = tmem;                // dq, or dv
-    const uint32_t acc2 = tmem + DP;           // dk
-    auto t_scores = [&](int s) { return tmem + 256 + 128 * s; };
-    auto t_grads = [&](int s) { return tmem + 256 + 128 * s + kBlk; };
+    const uint32_t acc2 = tmem + DP;           // keys: dk
+    const uint32_t t_s = tmem + (KV ? 256 : 128);
+    // G V^T of block i: keys: one buffer; queries: two, because a block's may
+    // complete before every warp has waited for the one before.
+    auto g_buf = [&](int i) { return KV ? 1 : i & 1; };
+    auto g_phase = [&](int i) { return KV ? i : i >> 1; };
+    auto t_g = [&](int i) { return tmem + 256 + 128 * g_buf(i); };
 
     if (warp < 8) {
         // ----------------------------------------------------- elementwise
-        const int wg = warp >> 2;
+        const int half = warp >> 2;
         const int quarter = warp & 3;
         const int a = a0 + 32 * quarter + lane;          // this thread's row
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t at = (static_cast<uint32_t>(quarter * 32) << 16) + 64 * half;
         const float c = t.scale * kLog2e;
         float row_lse = 0.0f, row_delta = 0.0f;
         if (!KV) {
@@ -190,7 +232,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 }
 #pragma unroll
                 for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                if (u == 0) delta_s[r] = d;
+                if (u == 0) rows_s[r] = d;
             }
             // An empty row, and a row past the last, gets lse = +inf: P = 0.
             row_lse = INFINITY;
@@ -198,84 +240,112 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 const float x = t.lse[static_cast<int64_t>(bh) * t.query_len + a];
                 if (x != -INFINITY) row_lse = x * kLog2e;
             }
-            named_barrier(kBarCompute, 256);
-            row_delta = delta_s[a - a0];
-            if (wg == 0) {
+            named_barrier(kBarElementwise, kElementwise);
+            row_delta = rows_s[a - a0];
+            if (half == 0) {
                 ws_lse[bh * padded + a] = row_lse;
                 ws_delta[bh * padded + a] = row_delta;
             }
         }
         bool ok = true;
-        for (int i = wg; i < blocks; i += 2) {
-            const int st = i % NS;
-            ok = warp_wait(&s_full[wg], i >> 1, limit);
-            if (KV && ok) ok = warp_wait(&b_full[st], i / NS, limit);
-            if (!KV && mask && ok) ok = warp_wait(&b_masked[st], i / NS, limit);
+        for (int i = 0; i < blocks; ++i) {
+            const int st = i % NR;
+            const int b0 = block_row(i) + 64 * half;     // first of this thread's columns
+            const float4* lse4 = reinterpret_cast<const float4*>(rows_s + 256 * st + 64 * half);
+            const float4* delta4 = lse4 + 32;
+            if (KV) ok = warp_wait(&r_full[st], i / NR, limit);
+            if (!KV && mask) ok = warp_wait(&b1_masked[i % N1], i / N1, limit);
+            if (ok) ok = warp_wait(s_full, i, limit);
             if (!ok) break;
             tc_fence_after_sync();
-            const int b0 = block_row(i);
-            uint32_t s[64], g[64];
-            tmem_ld32_async(t_scores(wg) + lanes, s);
-            tmem_ld32_async(t_scores(wg) + lanes + 32, s + 32);
-            tmem_ld32_async(t_grads(wg) + lanes, g);
-            tmem_ld32_async(t_grads(wg) + lanes + 32, g + 32);
+            uint32_t s[64];
+            tmem_ld32_async(t_s + at, s);
+            tmem_ld32_async(t_s + at + 32, s + 32);
             tmem_wait_ld<64>(s);
-            tmem_wait_ld<64>(g);
+            if (!KV) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_read);
+            }
             if (KV) {
                 // Columns are queries.  Rows of removed keys are not treated
                 // here: their sums are replaced by zeros at the end.
-                const float4* lse4 = reinterpret_cast<const float4*>(rows_s + 2 * kBlk * st);
-                const float4* delta4 = lse4 + kBlk / 4;
                 // Causal: query b0 + k keeps this key from column `from` on.
                 const int from = t.causal ? a - off - b0 : 0;
                 const bool edge = t.causal && a0 + 32 * quarter + 31 - off > b0;
+                uint32_t w[32];
 #pragma unroll
-                for (int k4 = 0; k4 < kBlk / 4; ++k4) {
-                    const float4 le = lse4[k4], de = delta4[k4];
+                for (int k4 = 0; k4 < 16; ++k4) {
+                    const float4 le = lse4[k4];
                     const float ls[4] = {le.x, le.y, le.z, le.w};
-                    const float ds[4] = {de.x, de.y, de.z, de.w};
-                    float p[4], d[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const int k = 4 * k4 + x;
-                        p[x] = ex2(fmaf(__uint_as_float(s[k]), c, -ls[x]));
-                        d[x] = p[x] * (__uint_as_float(g[k]) - ds[x]);
-                        if (edge && k < from) p[x] = d[x] = 0.0f;
+                        float p = ex2(fmaf(__uint_as_float(s[k]), c, -ls[x]));
+                        if (edge && k < from) p = 0.0f;
+                        s[k] = __float_as_uint(p);
                     }
-                    s[2 * k4] = pack_bf16(p[0], p[1]);
-                    s[2 * k4 + 1] = pack_bf16(p[2], p[3]);
-                    g[2 * k4] = pack_bf16(d[0], d[1]);
-                    g[2 * k4 + 1] = pack_bf16(d[2], d[3]);
+                    w[2 * k4] = pack_bf16(__uint_as_float(s[4 * k4]),
+                                          __uint_as_float(s[4 * k4 + 1]));
+                    w[2 * k4 + 1] = pack_bf16(__uint_as_float(s[4 * k4 + 2]),
+                                              __uint_as_float(s[4 * k4 + 3]));
                 }
-                tmem_st32(t_scores(wg) + lanes, s);
+                tmem_st32(t_s + at, w);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
             } else {
                 // Columns are keys.
                 const int limit_row = t.causal ? min(t.key_len, a + off + 1) : t.key_len;
                 const int limit_warp =
                     t.causal ? min(t.key_len, a0 + 32 * quarter + off + 1) : t.key_len;
                 uint2 kept = make_uint2(~0u, ~0u);
-                if (mask) kept = *reinterpret_cast<const uint2*>(words + 2 * st);
-                const bool edge = limit_warp < b0 + kBlk || (kept.x & kept.y) != ~0u;
-                const uint32_t bits[2] = {kept.x & bits_below(limit_row, b0),
-                                          kept.y & bits_below(limit_row, b0 + 32)};
+                if (mask) kept = *reinterpret_cast<const uint2*>(words + 4 * (i % N1) + 2 * half);
+                const bool edge = limit_warp < b0 + 64 || (kept.x & kept.y) != ~0u;
 #pragma unroll
-                for (int k2 = 0; k2 < kBlk / 2; ++k2) {
-                    float d[2];
+                for (int k = 0; k < 64; ++k)
+                    s[k] = __float_as_uint(ex2(fmaf(__uint_as_float(s[k]), c, -row_lse)));
+                if (edge) {
+                    const uint32_t bits[2] = {kept.x & bits_below(limit_row, b0),
+                                              kept.y & bits_below(limit_row, b0 + 32)};
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int k = 2 * k2 + x;
-                        const float p = ex2(fmaf(__uint_as_float(s[k]), c, -row_lse));
-                        d[x] = p * (__uint_as_float(g[k]) - row_delta);
-                        if (edge && !((bits[k >> 5] >> (k & 31)) & 1u)) d[x] = 0.0f;
-                    }
-                    g[k2] = pack_bf16(d[0], d[1]);
+                    for (int k = 0; k < 64; ++k)
+                        if (!((bits[k >> 5] >> (k & 31)) & 1u)) s[k] = 0u;
                 }
             }
-            tmem_st32(t_grads(wg) + lanes, g);
+            ok = warp_wait(&g_full[g_buf(i)], g_phase(i), limit);
+            if (!ok) break;
+            tc_fence_after_sync();
+            uint32_t g[64];
+            tmem_ld32_async(t_g(i) + at, g);
+            tmem_ld32_async(t_g(i) + at + 32, g + 32);
+            tmem_wait_ld<64>(g);
+            // dS; 0 where P is 0, whatever G V^T holds there (a removed
+            // value's NaN, a causally removed query's infinity).
+#pragma unroll
+            for (int k4 = 0; k4 < 16; ++k4) {
+                float4 de = make_float4(row_delta, row_delta, row_delta, row_delta);
+                if (KV) de = delta4[k4];
+                const float ds[4] = {de.x, de.y, de.z, de.w};
+                float d[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float p = __uint_as_float(s[4 * k4 + x]);
+                    d[x] = p * (__uint_as_float(g[4 * k4 + x]) - ds[x]);
+                    if (p == 0.0f) d[x] = 0.0f;
+                }
+                g[2 * k4] = pack_bf16(d[0], d[1]);
+                g[2 * k4 + 1] = pack_bf16(d[2], d[3]);
+            }
+            tmem_st32(t_g(i) + at, g);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&w_full[wg]);
+            if (lane == 0) {
+                mbar_arrive(d_full);
+                if (KV) mbar_arrive(&r_empty[st]);
+            }
         }
         if (ok && blocks > 0) ok = warp_wait(sums_full, 0, limit);
         if (ok) {
@@ -283,16 +353,17 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             // The rows' sums: keys: dv by the first four warps, dk by the
             // others; queries: half of dq's columns each.
             constexpr int kCols = KV ? DP : DP / 2;
-            const int c0 = KV ? 0 : wg * kCols;
-            const uint32_t from = (KV && wg == 1 ? acc2 : acc1) + lanes + c0;
+            const int c0 = KV ? 0 : half * kCols;
+            const uint32_t from = (KV && half == 1 ? acc2 : acc1) +
+                                  (static_cast<uint32_t>(quarter * 32) << 16) + c0;
             uint16_t* row;
-            if (KV && wg == 0)
+            if (KV && half == 0)
                 row = t.dv + b * t.dv_stride[0] + ha * t.dv_stride[1] + a * t.dv_stride[2];
             else if (KV)
                 row = t.dk + b * t.dk_stride[0] + ha * t.dk_stride[1] + a * t.dk_stride[2];
             else
                 row = t.dq + b * t.dq_stride[0] + ha * t.dq_stride[1] + a * t.dq_stride[2];
-            const float f = KV && wg == 0 ? 1.0f : t.scale;
+            const float f = KV && half == 0 ? 1.0f : t.scale;
             const bool live = a < fixed_len;
             const bool zero = blocks == 0 || (KV && mask && live && mask[a] == 0);
 #pragma unroll
@@ -312,42 +383,60 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     } else if (warp == kBwdMmaWarp) {
         // ----------------------------------------------------- MMA issuer
         const uint32_t a1 = smem_addr(smem + L::kA1), a2 = smem_addr(smem + L::kA2);
-        const uint32_t b1 = smem_addr(smem + L::kB), b2 = b1 + L::kBlock;
+        const uint32_t b1 = smem_addr(smem + L::kB1), b2 = smem_addr(smem + L::kB2);
+        auto tile1 = [&](int i) { return b1 + (i % N1) * L::kTile; };
+        auto tile2 = [&](int i) { return b2 + (i % N2) * L::kTile; };
+        uint64_t* ready1 = !KV && mask ? b1_masked : b1_full;
+        // S of block i, G V^T of block i, once their tiles are there.
         auto scores = [&](int i) {
+            if (!warp_wait(&ready1[i % N1], i / N1, limit)) return false;
             if (lane == 0) {
-                const uint32_t st = (i % NS) * L::kStage;
-                mma_tiles<kBlk, DP>(t_scores(i & 1), a1, b1 + st);
-                mma_tiles<kBlk, DP>(t_grads(i & 1), a2, b2 + st);
-                mma_commit(&s_full[i & 1]);
+                mma_tiles<128, DP>(t_s, a1, tile1(i));
+                mma_commit(s_full);
             }
             __syncwarp();
+            return true;
         };
-        bool ok = blocks == 0 || warp_wait(a_full, 0, limit);
-        uint64_t* ready = !KV && mask ? b_masked : b_full;
-        for (int i = 0; i < 2 && i < blocks && ok; ++i) {
-            ok = warp_wait(&ready[i % NS], i / NS, limit);
-            if (ok) scores(i);
-        }
+        auto grads = [&](int i) {
+            if (!warp_wait(&b2_full[i % N2], i / N2, limit)) return false;
+            if (lane == 0) {
+                mma_tiles<128, DP>(t_g(i), a2, tile2(i));
+                mma_commit(&g_full[g_buf(i)]);
+                if (!KV) mma_commit(&b2_empty[i % N2]);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = blocks == 0 ||
+                  (warp_wait(a_full, 0, limit) && scores(0) && grads(0));
         for (int i = 0; i < blocks && ok; ++i) {
-            ok = warp_wait(&w_full[i & 1], i >> 1, limit);
+            const bool more = i + 1 < blocks;
+            if (KV) {
+                ok = warp_wait(p_full, i, limit);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (lane == 0) {
+                    mma_weights<DP>(acc1, t_s, tile2(i), i > 0);
+                    mma_commit(&b2_empty[i % N2]);
+                }
+                __syncwarp();
+                if (more) ok = scores(i + 1);
+            } else if (more) {
+                ok = warp_wait(s_read, i, limit);
+                if (!ok) break;
+                tc_fence_after_sync();
+                ok = scores(i + 1) && grads(i + 1);
+            }
+            if (ok) ok = warp_wait(d_full, i, limit);
             if (!ok) break;
             tc_fence_after_sync();
             if (lane == 0) {
-                const uint32_t st = (i % NS) * L::kStage;
-                if (KV) {
-                    mma_weights<kBlk, DP>(acc1, t_scores(i & 1), b2 + st, i > 0);
-                    mma_weights<kBlk, DP>(acc2, t_grads(i & 1), b1 + st, i > 0);
-                } else {
-                    mma_weights<kBlk, DP>(acc1, t_grads(i & 1), b1 + st, i > 0);
-                }
-                mma_commit(&b_empty[i % NS]);
-                if (i == blocks - 1) mma_commit(sums_full);
+                mma_weights<DP>(KV ? acc2 : acc1, t_g(i), tile1(i), i > 0);
+                mma_commit(&b1_empty[i % N1]);
+                if (!more) mma_commit(sums_full);
             }
             __syncwarp();
-            if (i + 2 < blocks) {
-                ok = warp_wait(&ready[(i + 2) % NS], (i + 2) / NS, limit);
-                if (ok) scores(i + 2);
-            }
+            if (KV && more) ok = grads(i + 1);
         }
         // No product may be in flight when the tensor memory is freed.
         if (lane == 0) {
@@ -357,48 +446,60 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         __syncwarp();
     } else if (warp == kBwdLoadWarp) {
         // --------------------------------------------------------- loader
-        int issued = 0;
+        int issued1 = 0, issued2 = 0;
         for (int i = 0; i < blocks; ++i) {
-            const int st = i % NS;
-            if (i >= NS && !warp_wait(&b_empty[st], i / NS - 1, limit)) break;
+            const int s1 = i % N1, s2 = i % N2, sr = i % NR;
+            const int hb = block_head(i), row = block_row(i);
+            if (i >= N1 && !warp_wait(&b1_empty[s1], i / N1 - 1, limit)) break;
             if (lane == 0) {
                 if (i == 0) {
                     mbar_arrive_expect_tx(a_full, 2 * L::kTile);
                     load_tile<128, DP>(smem + L::kA1, &map_a1, a0, ha, b, a_full);
-                    load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, a_full);
                 }
-                unsigned char* at = smem + L::kB + st * L::kStage;
-                const int hb = block_head(i), row = block_row(i);
-                mbar_arrive_expect_tx(&b_full[st], L::kStage + (KV ? 2 * kBlk * 4 : 0));
-                load_tile<kBlk, DP>(at, &map_b1, row, hb, b, &b_full[st]);
-                load_tile<kBlk, DP>(at + L::kBlock, &map_b2, row, hb, b, &b_full[st]);
-                if (KV) {
-                    const int64_t r = (static_cast<int64_t>(b) * t.heads + hb) * padded + row;
-                    bulk_load(rows_s + 2 * kBlk * st, ws_lse + r, kBlk * 4, &b_full[st]);
-                    bulk_load(rows_s + 2 * kBlk * st + kBlk, ws_delta + r, kBlk * 4,
-                              &b_full[st]);
-                }
+                mbar_arrive_expect_tx(&b1_full[s1], L::kTile);
+                load_tile<128, DP>(smem + L::kB1 + s1 * L::kTile, &map_b1, row, hb, b,
+                                   &b1_full[s1]);
+                if (i == 0) load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, a_full);
             }
             __syncwarp();
-            issued = i + 1;
+            issued1 = i + 1;
+            if (KV && i >= NR && !warp_wait(&r_empty[sr], i / NR - 1, limit)) break;
+            if (i >= N2 && !warp_wait(&b2_empty[s2], i / N2 - 1, limit)) break;
+            if (lane == 0) {
+                if (KV) {
+                    const int64_t r = (static_cast<int64_t>(b) * t.heads + hb) * padded + row;
+                    mbar_arrive_expect_tx(&r_full[sr], 2 * 128 * 4);
+                    bulk_load(rows_s + 256 * sr, ws_lse + r, 128 * 4, &r_full[sr]);
+                    bulk_load(rows_s + 256 * sr + 128, ws_delta + r, 128 * 4, &r_full[sr]);
+                }
+                mbar_arrive_expect_tx(&b2_full[s2], L::kTile);
+                load_tile<128, DP>(smem + L::kB2 + s2 * L::kTile, &map_b2, row, hb, b,
+                                   &b2_full[s2]);
+            }
+            __syncwarp();
+            issued2 = i + 1;
         }
         // After an abort copies may still be in flight: none may land in
         // shared memory after the CTA exits (bounded waits).
-        if (*limit.abort_flag && lane == 0 && issued > 0) {
+        if (*limit.abort_flag && lane == 0 && issued1 > 0) {
             mbar_wait<false>(a_full, 0u, t.wait_limit_cycles);
-            for (int i = max(0, issued - NS); i < issued; ++i)
-                mbar_wait<false>(&b_full[i % NS], (i / NS) & 1, t.wait_limit_cycles);
+            for (int i = max(0, issued1 - N1); i < issued1; ++i)
+                mbar_wait<false>(&b1_full[i % N1], (i / N1) & 1, t.wait_limit_cycles);
+            for (int i = max(0, issued2 - N2); i < issued2; ++i) {
+                mbar_wait<false>(&b2_full[i % N2], (i / N2) & 1, t.wait_limit_cycles);
+                if (KV) mbar_wait<false>(&r_full[i % NR], (i / NR) & 1, t.wait_limit_cycles);
+            }
         }
         __syncwarp();
     } else if (!KV && warp == kBwdMaskWarp && mask) {
         // ------------------------------------------------------ key masks
         for (int i = 0; i < blocks; ++i) {
-            const int st = i % NS;
-            if (!warp_wait(&b_full[st], i / NS, limit)) break;
-            mask_tile<kBlk, DP>(mask, t.key_len, block_row(i), smem + L::kB + st * L::kStage,
-                                words + 2 * st, lane);
+            const int st = i % N1;
+            if (!warp_wait(&b1_full[st], i / N1, limit)) break;
+            mask_tile<128, DP>(mask, t.key_len, block_row(i), smem + L::kB1 + st * L::kTile,
+                               words + 4 * st, lane);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b_masked[st]);
+            if (lane == 0) mbar_arrive(&b1_masked[st]);
         }
     }
     tc_fence_before_sync();
@@ -410,15 +511,15 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
 template <int DP, bool KV>
 cudaError_t launch_bwd(const FattnTask& t, int slot, cudaStream_t stream) {
     const void* kern = reinterpret_cast<const void*>(fattn_bwd_kernel<DP, KV>);
-    const int smem = BwdSmem<DP>::kBytes;
+    constexpr int smem = BwdSmem<DP>::kBytes;
+    static_assert(smem <= 232448, "the shared memory of a CTA");
     cudaError_t e = ensure_smem_attribute(kern, slot, smem, false);
     if (e != cudaSuccess) return e;
-    constexpr int RQ = KV ? kBlk : 128, RK = KV ? 128 : kBlk;
     CUtensorMap mq, mg, mk, mv;
-    if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, RQ) ||
-        !encode_heads_map(&mg, t.go, t, t.heads, t.query_len, t.go_stride, RQ) ||
-        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, RK) ||
-        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, RK))
+    if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, 128) ||
+        !encode_heads_map(&mg, t.go, t, t.heads, t.query_len, t.go_stride, 128) ||
+        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, 128) ||
+        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, 128))
         return cudaErrorInvalidValue;
     const int64_t length = KV ? t.key_len : t.query_len;
     const int64_t heads = KV ? t.kv_heads : t.heads;

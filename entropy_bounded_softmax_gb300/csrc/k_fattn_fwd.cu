@@ -60,6 +60,17 @@ struct FwdSmem {
     static constexpr int kBytes = kFlags + 16 + 1024;     // and alignment slack
 };
 
+// D[128 x DP] (+)= P[128 x R] . B[R x DP], P bf16 in tensor memory, B a tile.
+template <int R, int DP>
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t p, uint32_t b,
+                                            bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16(128, DP, true);
+#pragma unroll
+    for (int ks = 0; ks < R / 16; ++ks)
+        mma_bf16_ts(d, p + 8 * ks, smem_desc_mn_sw128(b + ks * 2048, R * 128, 1024), idesc,
+                    accumulate || ks > 0);
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
