@@ -61,15 +61,44 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const void* tmap, 
         tma_load_4d(dst + p * R * 128, tmap, 64 * p, row, head, batch, bar);
 }
 
-// D[128 x N] = A[128 x DP] . B[N x DP]^T on two tiles.
+// The largest of three (NaN operands are passed over, as by fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// What 16 rows of a panel add to a descriptor's address.
+constexpr uint32_t kDescRows16 = 16 * 128 / 16;
+
+// D[128 x N] = A . B^T on a tile of 128 rows and one of N (their descriptors).
 template <int N, int DP>
-__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint64_t a, uint64_t b, bool leader) {
     constexpr uint32_t idesc = idesc_bf16(128, N, false);
 #pragma unroll
     for (int ks = 0; ks < DP / 16; ++ks)
-        mma_bf16_ss(d, smem_desc_sw128(a + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 1024),
-                    smem_desc_sw128(b + (ks >> 2) * (N * 128) + (ks & 3) * 32, 1024),
-                    idesc, ks > 0);
+        mma_bf16_ss(d, a + (ks >> 2) * (128 * 128 / 16) + (ks & 3) * (32 / 16),
+                    b + (ks >> 2) * (N * 128 / 16) + (ks & 3) * (32 / 16), idesc, ks > 0, leader);
+}
+
+// D[128 x DP] (+)= W[128 x N] . B[N x DP] (N a multiple of 16), W bf16 in
+// tensor memory from column w, B from the row of a tile that b, its MN-major
+// descriptor, names.
+template <int DP, int N>
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t w, uint64_t b,
+                                            bool accumulate, bool leader) {
+    constexpr uint32_t idesc = idesc_bf16(128, DP, true);
+#pragma unroll
+    for (int ks = 0; ks < N / 16; ++ks)
+        mma_bf16_ts(d, w + 8 * ks, b + ks * kDescRows16, idesc, accumulate || ks > 0, leader);
+}
+
+// The descriptors of a tile at shared address a: as an operand of mma_tiles,
+// and, of R rows, as B of mma_weights.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t a) { return smem_desc_sw128(a, 1024); }
+template <int R>
+__device__ __forceinline__ uint64_t weights_desc(uint32_t a) {
+    return smem_desc_mn_sw128(a, R * 128, 1024);
 }
 
 // Bits of the 32 columns from `base` that lie below `limit`.
@@ -78,30 +107,28 @@ __device__ __forceinline__ uint32_t bits_below(int limit, int base) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// The first and one past the last nonzero byte of row[0, n), by the whole
-// CTA; an empty row gives lo >= hi.  lo_hi: two shared ints; includes two
-// __syncthreads.
-__device__ __forceinline__ void block_nonzero_range(const uint8_t* row, int n, int* lo_hi,
-                                                    int& lo, int& hi) {
-    if (threadIdx.x == 0) {
-        lo_hi[0] = n;
-        lo_hi[1] = 0;
-    }
-    __syncthreads();
+// The first and one past the last nonzero byte of row[0, n), by one warp; an
+// empty row gives lo >= hi.
+__device__ __forceinline__ void warp_nonzero_range(const uint8_t* row, int n, int lane, int& lo,
+                                                   int& hi) {
     int first = n, past = 0;
-    const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15);
-    const int h = head < n ? head : n;
+    const int lead = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15);
+    const int h = lead < n ? lead : n;
     const int vecs = (n - h) >> 4;
+    const int tail = h + 16 * vecs;
     auto one = [&](int i) {
         if (row[i]) {
             first = min(first, i);
             past = max(past, i + 1);
         }
     };
-    for (int i = threadIdx.x; i < h; i += blockDim.x) one(i);
-    for (int i = h + 16 * vecs + threadIdx.x; i < n; i += blockDim.x) one(i);
-    for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + h) + v);
+    // Fewer than 16 bytes before and after the aligned units.
+    if (lane < h) one(lane);
+    if (tail + lane < n) one(tail + lane);
+    const uint4* units = reinterpret_cast<const uint4*>(row + h);
+#pragma unroll 4
+    for (int v = lane; v < vecs; v += 32) {
+        const uint4 x = __ldg(units + v);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -112,15 +139,8 @@ __device__ __forceinline__ void block_nonzero_range(const uint8_t* row, int n, i
             }
         }
     }
-    first = __reduce_min_sync(0xffffffffu, first);
-    past = __reduce_max_sync(0xffffffffu, past);
-    if ((threadIdx.x & 31) == 0) {
-        atomicMin(&lo_hi[0], first);
-        atomicMax(&lo_hi[1], past);
-    }
-    __syncthreads();
-    lo = lo_hi[0];
-    hi = lo_hi[1];
+    lo = __reduce_min_sync(0xffffffffu, first);
+    hi = __reduce_max_sync(0xffffffffu, past);
 }
 
 // The kept keys among the R (a multiple of 32) from `key`, one bit each, and
@@ -148,21 +168,39 @@ __device__ __forceinline__ void mask_tile(const uint8_t* row, int keys, int key,
     fence_proxy_async_smem();
 }
 
-// 32 fp32 columns c0 .. c0 + 31 times f, rounded to bf16, into a row of d
-// elements (d % 8 == 0, the row 16-byte aligned).
-__device__ __forceinline__ void store_row32(uint16_t* row, int d, int c0, const uint32_t* v,
-                                            float f) {
+// 32 fp32 columns c0 .. c0 + 31 times f, rounded to bf16, into row r of a
+// 128-row tile as the tensor copies lay it out (so that the 32 lanes' 16-byte
+// stores, each to a row of its own, fall in different banks).
+__device__ __forceinline__ void stage_row32(unsigned char* tile, int r, int c0,
+                                            const uint32_t* v, float f) {
+    unsigned char* row = tile + (c0 >> 6) * (128 * 128) + r * 128;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        if (c0 + 8 * u < d) {
-            uint32_t w[4];
+        uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16(__uint_as_float(v[8 * u + 2 * i]) * f,
-                                 __uint_as_float(v[8 * u + 2 * i + 1]) * f);
-            *reinterpret_cast<uint4*>(row + c0 + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack_bf16(__uint_as_float(v[8 * u + 2 * i]) * f,
+                             __uint_as_float(v[8 * u + 2 * i + 1]) * f);
+        *reinterpret_cast<uint4*>(row + ((((c0 >> 3) & 7) + u) ^ (r & 7)) * 16) =
+            make_uint4(w[0], w[1], w[2], w[3]);
     }
+}
+
+// Copies panels p0 .. p1 - 1 of rows r0 .. r0 + 31 of a staged tile, which
+// this warp has written, to the tensor's rows from `row` on (a map with boxes
+// of 32 rows; rows and head elements outside the tensor are not written), and
+// waits until the tile has been read.
+__device__ __forceinline__ void store_rows32(const unsigned char* tile, int r0, int p0, int p1,
+                                             const void* tmap, int row, int head, int batch,
+                                             int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        for (int p = p0; p < p1; ++p)
+            tma_store_4d(tmap, tile + p * (128 * 128) + r0 * 128, 64 * p, row, head, batch);
+        bulk_store_wait_read();
+    }
+    __syncwarp();
 }
 
 }  // namespace csd

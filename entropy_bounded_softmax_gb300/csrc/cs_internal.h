@@ -341,8 +341,8 @@ struct FattnTask {
 
 constexpr int kFattnMaxDHead = 128;
 
-// The backward's workspace: for every query row the log2 of its normaliser
-// and <grad_out, out>, two arrays of batch * heads rows of query_len rounded
+// The backward's workspace: for every query row minus the log2 of its
+// normaliser and minus <grad_out, out>, two arrays of batch * heads rows of query_len rounded
 // up to whole tiles of 128.
 inline int64_t fattn_rows_padded(int32_t query_len) {
     return (static_cast<int64_t>(query_len) + 127) / 128 * 128;

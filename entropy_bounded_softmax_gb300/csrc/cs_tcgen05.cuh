@@ -158,26 +158,46 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
          | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] . B[smem], K = 16, issued by one thread.
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"
+                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+
+// D[tmem] (+)= A[smem] . B[smem], K = 16.  Called by the whole warp, issued by
+// the lane where `leader` is true: the operands are then the same in every
+// lane and stay in uniform registers, where a branch around the call would
+// move each of them there for every instruction (an issuing thread that did
+// so took 97 to 150 cycles an instruction of 64).
 __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc,
                                             uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+                                            bool accumulate, bool leader) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
         :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc),
-           "r"(accumulate ? 1u : 0u) : "memory");
+           "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u) : "memory");
 }
 
 // The same with A in tensor memory: row m in lane m, two bf16 to a column.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
                                             uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+                                            bool accumulate, bool leader) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
         :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc),
-           "r"(accumulate ? 1u : 0u) : "memory");
+           "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u) : "memory");
+}
+
+// mma_commit by the leader of a warp that issues as mma_bf16_ss.
+__device__ __forceinline__ void mma_commit(uint64_t* bar, bool leader) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+        :: "r"(smem_addr(bar)), "r"(leader ? 1u : 0u) : "memory");
 }
 
 // 32 consecutive columns of this thread's lane, without the wait: the
@@ -225,6 +245,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
            "r"(r[30]), "r"(r[31]) : "memory");
 }
 
+// 16 registers into 16 consecutive columns, as tmem_st32.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, "
+        "%9, %10, %11, %12, %13, %14, %15, %16};"
+        :: "r"(taddr),
+           "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+           "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+           "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+           "r"(r[15]) : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -237,6 +270,27 @@ __device__ __forceinline__ void tma_load_4d(void* sdst, const void* tmap, int x,
         " [%0], [%1, {%2, %3, %4, %5}], [%6];"
         :: "r"(smem_addr(sdst)), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w),
            "r"(smem_addr(bar)) : "memory");
+}
+
+// The same from shared into global memory (elements outside the tensor are
+// not written); bulk_store_wait_read() commits this thread's stores and waits
+// until their source has been read.
+__device__ __forceinline__ void tma_store_4d(const void* tmap, const void* ssrc, int x, int y,
+                                             int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group"
+        " [%0, {%1, %2, %3, %4}], [%5];"
+        :: "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(ssrc)) : "memory");
+}
+
+__device__ __forceinline__ void bulk_store_wait_read() {
+    asm volatile("cp.async.bulk.commit_group;\n"
+                 "cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// Fetches a tensor map ahead of its first use.
+__device__ __forceinline__ void prefetch_tmap(const void* tmap) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(tmap) : "memory");
 }
 
 // Untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned).

@@ -8,17 +8,19 @@
 // Two launches of one kernel, so that every sum stays in one CTA's tensor
 // memory: no atomics, the same bits every time, no fp32 copy of a gradient
 // in memory.  They recompute P twice (seven products instead of five).
-//   queries (KV = false)  128 query rows a CTA, over blocks of 128 keys:
+//   queries (KV = false)  128 query rows a CTA, over blocks of keys:
 //       S = Q K^T, G V^T, dq += dS K.  Before its blocks it takes delta of
-//       its rows and leaves delta and lse, in base 2 and padded to whole
+//       its rows and leaves -delta and -lse, in base 2 and padded to whole
 //       tiles, in the workspace for the second launch;
-//   keys (KV = true)      128 key rows a CTA, over blocks of 128 queries of
+//   keys (KV = true)      128 key rows a CTA, over blocks of queries of
 //       every head of its group: S^T = K Q^T, V G^T, dv += P^T G,
 //       dk += dS^T Q.
 // In both the fixed tiles' rows are the lanes of tensor memory, and the
 // weights, rounded to bf16 in columns their scores had, are the next
-// product's A operand there.  Products of 128 columns, because one of 64
-// reads its A tile from shared memory twice as often and is bound by that.
+// product's A operand there.  Blocks are 128 rows for d_head > 64: a product
+// of 64 columns reads its A tile from shared memory twice as often and is
+// bound by that.  For d_head <= 64 they are 64 rows, so that two CTAs fit an
+// SM and the start and the end of one run under the other's work.
 //
 // Tensor memory holds two sums, S and G V^T (keys), or one sum, S and two of
 // G V^T (queries).  The elementwise part has two phases, P from S and dS from
@@ -28,7 +30,7 @@
 //            G V^T(i+1), dS(i) under dv(i) and S(i+1);
 //   queries  S(i+1), G V^T(i+1), dq(i): P(i) and dS(i) under the first two.
 // Roles:
-//   warps 0-7   the elementwise part, a row and 64 of its columns a thread
+//   warps 0-7   the elementwise part, a row and half its columns a thread
 //               (warps w and w + 4 share the rows of lanes 32 (w % 4) ..);
 //   warp 8      issues the products;
 //   warp 9      tensor copies: the two fixed tiles, then the blocks;
@@ -51,21 +53,25 @@ constexpr int kBwdThreads = 352;
 constexpr int kBwdMmaWarp = 8;
 constexpr int kBwdLoadWarp = 9;
 constexpr int kBwdMaskWarp = 10;
-constexpr uint32_t kBwdTmemCols = 512;
 constexpr uint32_t kBarElementwise = 1;
 constexpr uint32_t kElementwise = 256;         // threads
 
 // The first streamed tensor (K, or Q) is read by a block's first and last
 // product, the second (V, or G) by the ones between: three stages and two.
 template <int DP>
-struct BwdSmem {
+struct BwdPlan {
+    static constexpr int kBlk = DP == 64 ? 64 : 128;      // rows of a block
+    static constexpr int kCtasPerSm = DP == 64 ? 2 : 1;
+    static constexpr uint32_t kTmemCols = DP == 64 ? 256 : 512;
+    static constexpr int kCols = kBlk / 2;                // columns of a thread
     static constexpr int kTile = 128 * DP * 2;
+    static constexpr int kBlock = kBlk * DP * 2;
     static constexpr int kStages1 = 3, kStages2 = 2, kStagesR = 2;
     static constexpr int kA1 = 0;              // Q, or K
     static constexpr int kA2 = kA1 + kTile;    // G, or V
     static constexpr int kB1 = kA2 + kTile;
-    static constexpr int kB2 = kB1 + kStages1 * kTile;
-    static constexpr int kRows = kB2 + kStages2 * kTile;  // [kStagesR][2][128] lse, delta
+    static constexpr int kB2 = kB1 + kStages1 * kBlock;
+    static constexpr int kRows = kB2 + kStages2 * kBlock;  // [kStagesR][2][128] lse, delta
     static constexpr int kBars = kRows + kStagesR * 2 * 128 * 4;
     static constexpr int kNumBars =
         1 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 6 + 2;
@@ -74,27 +80,36 @@ struct BwdSmem {
     static constexpr int kBytes = kFlags + 16;
 };
 
-// D[128 x DP] (+)= W[128 x 128] . B[128 x DP], W bf16 in tensor memory, the
-// two halves of its columns 64 columns of 32 bits apart; B a tile.
-template <int DP>
-__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t w, uint32_t b,
-                                            bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16(128, DP, true);
+__device__ __forceinline__ float2 pair(const uint32_t* x, int k) {
+    return make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+}
+
+// Zeros for the columns whose bit is not set.
+template <int N>
+__device__ __forceinline__ void clear_removed(uint32_t (&x)[N], const uint32_t (&kept)[N / 32]) {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-        mma_bf16_ts(d, w + 64 * (ks >> 2) + 8 * (ks & 3),
-                    smem_desc_mn_sw128(b + ks * 2048, 128 * 128, 1024), idesc,
-                    accumulate || ks > 0);
+    for (int k = 0; k < N; ++k)
+        if (!((kept[k >> 5] >> (k & 31)) & 1u)) x[k] = 0u;
+}
+
+__device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&w)[32]) {
+    tmem_st32(at, w);
+}
+__device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&w)[16]) {
+    tmem_st16(at, w);
 }
 
 template <int DP, bool KV>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, BwdPlan<DP>::kCtasPerSm)
 fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                  const __grid_constant__ CUtensorMap map_a2,
                  const __grid_constant__ CUtensorMap map_b1,
-                 const __grid_constant__ CUtensorMap map_b2) {
-    using L = BwdSmem<DP>;
+                 const __grid_constant__ CUtensorMap map_b2,
+                 const __grid_constant__ CUtensorMap map_d1,
+                 const __grid_constant__ CUtensorMap map_d2) {
+    using L = BwdPlan<DP>;
     constexpr int N1 = L::kStages1, N2 = L::kStages2, NR = L::kStagesR;
+    constexpr int BLK = L::kBlk, CO = L::kCols;
     // The tiles need 1024-byte alignment, and fill the shared memory that a
     // CTA can have up to a few hundred bytes; there are no static variables.
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -106,14 +121,14 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     uint64_t* b2_full = b1_masked + N1;        // [N2]
     uint64_t* b2_empty = b2_full + N2;
     uint64_t* r_full = b2_empty + N2;          // [NR] keys: lse and delta landed
-    uint64_t* r_empty = r_full + NR;
-    uint64_t* s_full = r_empty + NR;           // a block's scores
-    uint64_t* s_read = s_full + 1;             // queries: in registers
-    uint64_t* g_full = s_read + 1;             // [2] its G V^T, by buffer
-    uint64_t* p_full = g_full + 2;             // keys: its P
-    uint64_t* d_full = p_full + 1;             // its dS
-    uint64_t* sums_full = d_full + 1;          // every sum completed
+    uint64_t* s_full = r_full + NR;            // a block's scores
+    uint64_t* g_full = s_full + 1;             // [2] its G V^T, by buffer
+    uint64_t* sums_full = g_full + 2;          // every sum completed
     uint64_t* drained = sums_full + 1;
+    uint64_t* r_empty = drained + 1;           // [NR] from eight warps, as those below
+    uint64_t* s_read = r_empty + NR;           // queries: the scores are in registers
+    uint64_t* p_full = s_read + 1;             // keys: the block's P
+    uint64_t* d_full = p_full + 1;             // its dS
     float* rows_s = reinterpret_cast<float*>(smem + L::kRows);
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
@@ -137,43 +152,32 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     float* ws_lse = t.rows;
     float* ws_delta = t.rows + static_cast<int64_t>(t.batch) * t.heads * padded;
 
-    if (threadIdx.x == 0) {
-        mbar_init(a_full, 1u);
-        for (int i = 0; i < N1; ++i) {
-            mbar_init(&b1_full[i], 1u);
-            mbar_init(&b1_empty[i], 1u);
-            mbar_init(&b1_masked[i], 1u);
-        }
-        for (int i = 0; i < N2; ++i) {
-            mbar_init(&b2_full[i], 1u);
-            mbar_init(&b2_empty[i], 1u);
-        }
-        for (int i = 0; i < NR; ++i) {
-            mbar_init(&r_full[i], 1u);
-            mbar_init(&r_empty[i], 8u);
-        }
-        mbar_init(s_full, 1u);
-        mbar_init(s_read, 8u);
-        mbar_init(&g_full[0], 1u);
-        mbar_init(&g_full[1], 1u);
-        mbar_init(p_full, 8u);
-        mbar_init(d_full, 8u);
-        mbar_init(sums_full, 1u);
-        mbar_init(drained, 1u);
-        flags[0] = 0u;
+    // The loader initialises the barriers, and starts its first copies before
+    // the others have set up.
+    if (warp == kBwdLoadWarp) {
+        static_assert(L::kNumBars <= 32, "a lane a barrier");
+        if (lane < L::kNumBars) mbar_init(bars + lane, bars + lane < r_empty ? 1u : 8u);
+        if (lane == 0) flags[0] = 0u;
         fence_mbar_init();
+        __syncwarp();
+        if (lane == 0) {
+            if (t.query_len > 0 && t.key_len > 0) {   // (an empty tensor has no map)
+                prefetch_tmap(&map_b1);
+                prefetch_tmap(&map_b2);
+            }
+            mbar_arrive_expect_tx(a_full, 2 * L::kTile);
+            load_tile<128, DP>(smem + L::kA1, &map_a1, a0, ha, b, a_full);
+            load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, a_full);
+            prefetch_tmap(&map_d1);
+            prefetch_tmap(&map_d2);
+        }
+        __syncwarp();
+    } else if (warp == kBwdMmaWarp) {
+        tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
     }
-    if (warp == kBwdMmaWarp)
-        tmem_alloc(const_cast<uint32_t*>(flags) + 1, kBwdTmemCols);
     const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
     int key_lo = 0, key_hi = t.key_len;
-    if (mask)
-        block_nonzero_range(mask, t.key_len,
-                            reinterpret_cast<int*>(smem + L::kFlags) + 2, key_lo, key_hi);
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = flags[1];
+    if (mask) warp_nonzero_range(mask, t.key_len, lane, key_lo, key_hi);
 
     // Blocks first .. first + per - 1 of the streamed side, for each head.
     int first = 0, per = 0;
@@ -181,35 +185,70 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     if (KV) {
         // Queries with a kept key in the tile: i >= a0 - off under causal.
         const int lo = t.causal ? max(0, a0 - off) : 0;
-        first = lo >> 7;
+        first = lo / BLK;
         if (lo < t.query_len && a0 < key_hi && last >= key_lo)
-            per = ((t.query_len + 127) >> 7) - first;
+            per = (t.query_len + BLK - 1) / BLK - first;
     } else {
         const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
-        first = key_lo >> 7;
-        if (hi > key_lo) per = ((hi + 127) >> 7) - first;
+        first = key_lo / BLK;
+        if (hi > key_lo) per = (hi + BLK - 1) / BLK - first;
     }
     const int blocks = KV ? per * group : per;
     // Block i's head on the streamed side and its first row there.
     auto block_head = [&](int i) { return KV ? ha * group + i / per : ha / group; };
-    auto block_row = [&](int i) { return (first + (KV ? i % per : i)) << 7; };
+    auto block_row = [&](int i) { return BLK * (first + (KV ? i % per : i)); };
+    auto load1 = [&](int i) {
+        uint64_t* bar = &b1_full[i % N1];
+        mbar_arrive_expect_tx(bar, L::kBlock);
+        load_tile<BLK, DP>(smem + L::kB1 + (i % N1) * L::kBlock, &map_b1, block_row(i),
+                           block_head(i), b, bar);
+    };
+    auto load2 = [&](int i) {
+        uint64_t* bar = &b2_full[i % N2];
+        mbar_arrive_expect_tx(bar, L::kBlock);
+        load_tile<BLK, DP>(smem + L::kB2 + (i % N2) * L::kBlock, &map_b2, block_row(i),
+                           block_head(i), b, bar);
+    };
+    auto load_rows = [&](int i) {
+        const int64_t r =
+            (static_cast<int64_t>(b) * t.heads + block_head(i)) * padded + block_row(i);
+        uint64_t* bar = &r_full[i % NR];
+        float* at = rows_s + 2 * BLK * (i % NR);
+        mbar_arrive_expect_tx(bar, 2 * BLK * 4);
+        bulk_load(at, ws_lse + r, BLK * 4, bar);
+        bulk_load(at + BLK, ws_delta + r, BLK * 4, bar);
+    };
+    const int early1 = min(blocks, N1), early2 = min(blocks, N2);
+    static_assert(N2 == NR, "the row values' ring is as deep as the second tensor's");
+    if (warp == kBwdLoadWarp && lane == 0) {
+        for (int i = 0; i < early1; ++i) {
+            load1(i);
+            if (KV && i < NR) load_rows(i);
+            if (i < N2) load2(i);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = flags[1];
     const uint32_t acc1 = tmem;                // dq, or dv
     const uint32_t acc2 = tmem + DP;           // keys: dk
-    const uint32_t t_s = tmem + (KV ? 256 : 128);
+    const uint32_t t_s = tmem + (KV ? 2 : 1) * DP;
     // G V^T of block i: keys: one buffer; queries: two, because a block's may
     // complete before every warp has waited for the one before.
-    auto g_buf = [&](int i) { return KV ? 1 : i & 1; };
+    auto g_buf = [&](int i) { return KV ? 0 : i & 1; };
     auto g_phase = [&](int i) { return KV ? i : i >> 1; };
-    auto t_g = [&](int i) { return tmem + 256 + 128 * g_buf(i); };
+    auto t_g = [&](int i) { return t_s + BLK * (KV ? 1 : 1 + (i & 1)); };
 
     if (warp < 8) {
         // ----------------------------------------------------- elementwise
         const int half = warp >> 2;
         const int quarter = warp & 3;
         const int a = a0 + 32 * quarter + lane;          // this thread's row
-        const uint32_t at = (static_cast<uint32_t>(quarter * 32) << 16) + 64 * half;
+        const uint32_t at = (static_cast<uint32_t>(quarter * 32) << 16) + CO * half;
         const float c = t.scale * kLog2e;
-        float row_lse = 0.0f, row_delta = 0.0f;
+        const float2 c2 = make_float2(c, c);
+        float row_lse = 0.0f, row_delta = 0.0f;   // queries: -lse, -delta
         if (!KV) {
             // delta: DP / 8 lanes a row, 16 bytes of out and of g each.
             constexpr int LR = DP / 8;
@@ -234,14 +273,14 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
                 if (u == 0) rows_s[r] = d;
             }
-            // An empty row, and a row past the last, gets lse = +inf: P = 0.
-            row_lse = INFINITY;
+            // An empty row, and a row past the last, gets -lse = -inf: P = 0.
+            row_lse = -INFINITY;
             if (a < t.query_len) {
                 const float x = t.lse[static_cast<int64_t>(bh) * t.query_len + a];
-                if (x != -INFINITY) row_lse = x * kLog2e;
+                if (x != -INFINITY) row_lse = -x * kLog2e;
             }
             named_barrier(kBarElementwise, kElementwise);
-            row_delta = rows_s[a - a0];
+            row_delta = -rows_s[a - a0];
             if (half == 0) {
                 ws_lse[bh * padded + a] = row_lse;
                 ws_delta[bh * padded + a] = row_delta;
@@ -250,95 +289,111 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         bool ok = true;
         for (int i = 0; i < blocks; ++i) {
             const int st = i % NR;
-            const int b0 = block_row(i) + 64 * half;     // first of this thread's columns
-            const float4* lse4 = reinterpret_cast<const float4*>(rows_s + 256 * st + 64 * half);
-            const float4* delta4 = lse4 + 32;
+            const int b0 = block_row(i) + CO * half;     // first of this thread's columns
+            // -lse and -delta of this thread's columns (keys).
+            const float4* lse4 = reinterpret_cast<const float4*>(rows_s + 2 * BLK * st + CO * half);
+            const float4* delta4 = lse4 + BLK / 4;
             if (KV) ok = warp_wait(&r_full[st], i / NR, limit);
             if (!KV && mask) ok = warp_wait(&b1_masked[i % N1], i / N1, limit);
             if (ok) ok = warp_wait(s_full, i, limit);
             if (!ok) break;
             tc_fence_after_sync();
-            uint32_t s[64];
-            tmem_ld32_async(t_s + at, s);
-            tmem_ld32_async(t_s + at + 32, s + 32);
-            tmem_wait_ld<64>(s);
+            uint32_t s[CO];
+#pragma unroll
+            for (int u = 0; u < CO / 32; ++u) tmem_ld32_async(t_s + at + 32 * u, s + 32 * u);
+            tmem_wait_ld<CO>(s);
             if (!KV) {
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_read);
             }
+            // P from S: 2^(s c - lse), packed pairs.
+            uint32_t kept[CO / 32];
+#pragma unroll
+            for (int u = 0; u < CO / 32; ++u) kept[u] = ~0u;
+            bool edge;
             if (KV) {
                 // Columns are queries.  Rows of removed keys are not treated
                 // here: their sums are replaced by zeros at the end.
-                // Causal: query b0 + k keeps this key from column `from` on.
-                const int from = t.causal ? a - off - b0 : 0;
-                const bool edge = t.causal && a0 + 32 * quarter + 31 - off > b0;
-                uint32_t w[32];
+                // Causal: query b0 + k keeps this key from k = a - off - b0 on.
+                edge = t.causal && a0 + 32 * quarter + 31 - off > b0;
+                if (edge) {
 #pragma unroll
-                for (int k4 = 0; k4 < 16; ++k4) {
-                    const float4 le = lse4[k4];
-                    const float ls[4] = {le.x, le.y, le.z, le.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int k = 4 * k4 + x;
-                        float p = ex2(fmaf(__uint_as_float(s[k]), c, -ls[x]));
-                        if (edge && k < from) p = 0.0f;
-                        s[k] = __float_as_uint(p);
-                    }
-                    w[2 * k4] = pack_bf16(__uint_as_float(s[4 * k4]),
-                                          __uint_as_float(s[4 * k4 + 1]));
-                    w[2 * k4 + 1] = pack_bf16(__uint_as_float(s[4 * k4 + 2]),
-                                              __uint_as_float(s[4 * k4 + 3]));
+                    for (int u = 0; u < CO / 32; ++u) kept[u] = ~bits_below(a - off, b0 + 32 * u);
                 }
-                tmem_st32(t_s + at, w);
+            } else {
+                // Columns are keys.
+                const int limit_warp =
+                    t.causal ? min(t.key_len, a0 + 32 * quarter + off + 1) : t.key_len;
+                edge = limit_warp < b0 + CO;
+                if (mask) {
+#pragma unroll
+                    for (int u = 0; u < CO / 32; ++u) {
+                        kept[u] = words[4 * (i % N1) + CO / 32 * half + u];
+                        edge = edge || kept[u] != ~0u;
+                    }
+                }
+                if (edge) {
+                    const int limit_row = t.causal ? min(t.key_len, a + off + 1) : t.key_len;
+#pragma unroll
+                    for (int u = 0; u < CO / 32; ++u) kept[u] &= bits_below(limit_row, b0 + 32 * u);
+                }
+            }
+#pragma unroll
+            for (int k4 = 0; k4 < CO / 4; ++k4) {
+                float4 le = make_float4(row_lse, row_lse, row_lse, row_lse);
+                if (KV) le = lse4[k4];
+                const float2 y0 = fma2(pair(s, 4 * k4), c2, make_float2(le.x, le.y));
+                const float2 y1 = fma2(pair(s, 4 * k4 + 2), c2, make_float2(le.z, le.w));
+                s[4 * k4] = __float_as_uint(ex2(y0.x));
+                s[4 * k4 + 1] = __float_as_uint(ex2(y0.y));
+                s[4 * k4 + 2] = __float_as_uint(ex2(y1.x));
+                s[4 * k4 + 3] = __float_as_uint(ex2(y1.y));
+            }
+            if (edge) clear_removed(s, kept);
+            if (KV) {
+                uint32_t w[CO / 2];
+#pragma unroll
+                for (int k = 0; k < CO / 2; ++k) {
+                    const float2 p = pair(s, 2 * k);
+                    w[k] = pack_bf16(p.x, p.y);
+                }
+                store_weights(t_s + at, w);
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
-            } else {
-                // Columns are keys.
-                const int limit_row = t.causal ? min(t.key_len, a + off + 1) : t.key_len;
-                const int limit_warp =
-                    t.causal ? min(t.key_len, a0 + 32 * quarter + off + 1) : t.key_len;
-                uint2 kept = make_uint2(~0u, ~0u);
-                if (mask) kept = *reinterpret_cast<const uint2*>(words + 4 * (i % N1) + 2 * half);
-                const bool edge = limit_warp < b0 + 64 || (kept.x & kept.y) != ~0u;
-#pragma unroll
-                for (int k = 0; k < 64; ++k)
-                    s[k] = __float_as_uint(ex2(fmaf(__uint_as_float(s[k]), c, -row_lse)));
-                if (edge) {
-                    const uint32_t bits[2] = {kept.x & bits_below(limit_row, b0),
-                                              kept.y & bits_below(limit_row, b0 + 32)};
-#pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!((bits[k >> 5] >> (k & 31)) & 1u)) s[k] = 0u;
-                }
             }
             ok = warp_wait(&g_full[g_buf(i)], g_phase(i), limit);
             if (!ok) break;
             tc_fence_after_sync();
-            uint32_t g[64];
-            tmem_ld32_async(t_g(i) + at, g);
-            tmem_ld32_async(t_g(i) + at + 32, g + 32);
-            tmem_wait_ld<64>(g);
-            // dS; 0 where P is 0, whatever G V^T holds there (a removed
-            // value's NaN, a causally removed query's infinity).
+            uint32_t g[CO];
 #pragma unroll
-            for (int k4 = 0; k4 < 16; ++k4) {
+            for (int u = 0; u < CO / 32; ++u) tmem_ld32_async(t_g(i) + at + 32 * u, g + 32 * u);
+            tmem_wait_ld<CO>(g);
+            // dS = P (G V^T - delta), packed pairs; exactly 0 for removed
+            // pairs, whatever G V^T holds there (padding's NaN).
+#pragma unroll
+            for (int k4 = 0; k4 < CO / 4; ++k4) {
                 float4 de = make_float4(row_delta, row_delta, row_delta, row_delta);
                 if (KV) de = delta4[k4];
-                const float ds[4] = {de.x, de.y, de.z, de.w};
-                float d[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float p = __uint_as_float(s[4 * k4 + x]);
-                    d[x] = p * (__uint_as_float(g[4 * k4 + x]) - ds[x]);
-                    if (p == 0.0f) d[x] = 0.0f;
-                }
-                g[2 * k4] = pack_bf16(d[0], d[1]);
-                g[2 * k4 + 1] = pack_bf16(d[2], d[3]);
+                const float2 d0 = mul2(pair(s, 4 * k4),
+                                       add2(pair(g, 4 * k4), make_float2(de.x, de.y)));
+                const float2 d1 = mul2(pair(s, 4 * k4 + 2),
+                                       add2(pair(g, 4 * k4 + 2), make_float2(de.z, de.w)));
+                g[4 * k4] = __float_as_uint(d0.x);
+                g[4 * k4 + 1] = __float_as_uint(d0.y);
+                g[4 * k4 + 2] = __float_as_uint(d1.x);
+                g[4 * k4 + 3] = __float_as_uint(d1.y);
             }
-            tmem_st32(t_g(i) + at, g);
+            if (edge) clear_removed(g, kept);
+            uint32_t w[CO / 2];
+#pragma unroll
+            for (int k = 0; k < CO / 2; ++k) {
+                const float2 d = pair(g, 2 * k);
+                w[k] = pack_bf16(d.x, d.y);
+            }
+            store_weights(t_g(i) + at, w);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
@@ -347,65 +402,65 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 if (KV) mbar_arrive(&r_empty[st]);
             }
         }
-        if (ok && blocks > 0) ok = warp_wait(sums_full, 0, limit);
-        if (ok) {
+        // The rows' sums, staged over the fixed tiles once those are read (or,
+        // without blocks, have landed): keys: dv by the first four warps, dk
+        // by the others; queries: a panel of 64 columns of dq each.
+        if (ok) ok = blocks > 0 ? warp_wait(sums_full, 0, limit) : warp_wait(a_full, 0, limit);
+        const int row0 = a0 + 32 * quarter;
+        constexpr int kPanels = DP / 64;
+        const int p0 = KV || kPanels == 1 ? 0 : half, p1 = KV ? kPanels : p0 + 1;
+        if (ok && row0 < fixed_len && (KV || kPanels == 2 || half == 0)) {
             tc_fence_after_sync();
-            // The rows' sums: keys: dv by the first four warps, dk by the
-            // others; queries: half of dq's columns each.
-            constexpr int kCols = KV ? DP : DP / 2;
-            const int c0 = KV ? 0 : half * kCols;
             const uint32_t from = (KV && half == 1 ? acc2 : acc1) +
-                                  (static_cast<uint32_t>(quarter * 32) << 16) + c0;
-            uint16_t* row;
-            if (KV && half == 0)
-                row = t.dv + b * t.dv_stride[0] + ha * t.dv_stride[1] + a * t.dv_stride[2];
-            else if (KV)
-                row = t.dk + b * t.dk_stride[0] + ha * t.dk_stride[1] + a * t.dk_stride[2];
-            else
-                row = t.dq + b * t.dq_stride[0] + ha * t.dq_stride[1] + a * t.dq_stride[2];
+                                  (static_cast<uint32_t>(quarter * 32) << 16);
+            unsigned char* stage = smem + (KV && half == 1 ? L::kA2 : L::kA1);
             const float f = KV && half == 0 ? 1.0f : t.scale;
-            const bool live = a < fixed_len;
-            const bool zero = blocks == 0 || (KV && mask && live && mask[a] == 0);
-#pragma unroll
-            for (int u = 0; u < kCols / 32; ++u) {
+            const bool zero =
+                blocks == 0 || (KV && mask && a < fixed_len && mask[a] == 0);
+#pragma unroll 1
+            for (int c0 = 64 * p0; c0 < 64 * p1; c0 += 32) {
                 uint32_t x[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = 0u;
                 if (blocks > 0) {
-                    tmem_ld32_async(from + 32 * u, x);
+                    tmem_ld32_async(from + c0, x);
                     tmem_wait_ld<32>(x);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] = zero ? 0u : x[k];
-                if (live) store_row32(row, t.d_head, c0 + 32 * u, x, f);
+                stage_row32(stage, 32 * quarter + lane, c0, x, f);
             }
+            store_rows32(stage, 32 * quarter, p0, p1, KV && half == 1 ? &map_d2 : &map_d1, row0,
+                         ha, b, lane);
         }
     } else if (warp == kBwdMmaWarp) {
         // ----------------------------------------------------- MMA issuer
-        const uint32_t a1 = smem_addr(smem + L::kA1), a2 = smem_addr(smem + L::kA2);
+        const bool leader = elect_lane();
+        constexpr uint32_t step = L::kBlock / 16;
         const uint32_t b1 = smem_addr(smem + L::kB1), b2 = smem_addr(smem + L::kB2);
-        auto tile1 = [&](int i) { return b1 + (i % N1) * L::kTile; };
-        auto tile2 = [&](int i) { return b2 + (i % N2) * L::kTile; };
+        const uint64_t a1_t = tile_desc(smem_addr(smem + L::kA1));
+        const uint64_t a2_t = tile_desc(smem_addr(smem + L::kA2));
+        const uint64_t b1_t = tile_desc(b1), b1_w = weights_desc<BLK>(b1);
+        const uint64_t b2_t = tile_desc(b2), b2_w = weights_desc<BLK>(b2);
         uint64_t* ready1 = !KV && mask ? b1_masked : b1_full;
         // S of block i, G V^T of block i, once their tiles are there.
         auto scores = [&](int i) {
             if (!warp_wait(&ready1[i % N1], i / N1, limit)) return false;
-            if (lane == 0) {
-                mma_tiles<128, DP>(t_s, a1, tile1(i));
-                mma_commit(s_full);
-            }
-            __syncwarp();
+            mma_tiles<BLK, DP>(t_s, a1_t, b1_t + (i % N1) * step, leader);
+            mma_commit(s_full, leader);
             return true;
         };
         auto grads = [&](int i) {
             if (!warp_wait(&b2_full[i % N2], i / N2, limit)) return false;
-            if (lane == 0) {
-                mma_tiles<128, DP>(t_g(i), a2, tile2(i));
-                mma_commit(&g_full[g_buf(i)]);
-                if (!KV) mma_commit(&b2_empty[i % N2]);
-            }
-            __syncwarp();
+            mma_tiles<BLK, DP>(t_g(i), a2_t, b2_t + (i % N2) * step, leader);
+            mma_commit(&g_full[g_buf(i)], leader);
+            if (!KV) mma_commit(&b2_empty[i % N2], leader);
             return true;
+        };
+        // A sum's product; each half's weights are where its scores were.
+        auto sums = [&](uint32_t d, uint32_t w, uint64_t b, bool accumulate) {
+            mma_weights<DP, CO>(d, w, b, accumulate, leader);
+            mma_weights<DP, CO>(d, w + CO, b + CO / 16 * kDescRows16, true, leader);
         };
         bool ok = blocks == 0 ||
                   (warp_wait(a_full, 0, limit) && scores(0) && grads(0));
@@ -415,11 +470,8 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 ok = warp_wait(p_full, i, limit);
                 if (!ok) break;
                 tc_fence_after_sync();
-                if (lane == 0) {
-                    mma_weights<DP>(acc1, t_s, tile2(i), i > 0);
-                    mma_commit(&b2_empty[i % N2]);
-                }
-                __syncwarp();
+                sums(acc1, t_s, b2_w + (i % N2) * step, i > 0);
+                mma_commit(&b2_empty[i % N2], leader);
                 if (more) ok = scores(i + 1);
             } else if (more) {
                 ok = warp_wait(s_read, i, limit);
@@ -430,59 +482,37 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             if (ok) ok = warp_wait(d_full, i, limit);
             if (!ok) break;
             tc_fence_after_sync();
-            if (lane == 0) {
-                mma_weights<DP>(KV ? acc2 : acc1, t_g(i), tile1(i), i > 0);
-                mma_commit(&b1_empty[i % N1]);
-                if (!more) mma_commit(sums_full);
-            }
-            __syncwarp();
+            sums(KV ? acc2 : acc1, t_g(i), b1_w + (i % N1) * step, i > 0);
+            mma_commit(&b1_empty[i % N1], leader);
+            if (!more) mma_commit(sums_full, leader);
             if (KV && more) ok = grads(i + 1);
         }
         // No product may be in flight when the tensor memory is freed.
-        if (lane == 0) {
-            mma_commit(drained);
-            mbar_wait<false>(drained, 0u, t.wait_limit_cycles);
-        }
+        mma_commit(drained, leader);
+        mbar_wait<false>(drained, 0u, t.wait_limit_cycles);
         __syncwarp();
     } else if (warp == kBwdLoadWarp) {
         // --------------------------------------------------------- loader
-        int issued1 = 0, issued2 = 0;
-        for (int i = 0; i < blocks; ++i) {
-            const int s1 = i % N1, s2 = i % N2, sr = i % NR;
-            const int hb = block_head(i), row = block_row(i);
-            if (i >= N1 && !warp_wait(&b1_empty[s1], i / N1 - 1, limit)) break;
-            if (lane == 0) {
-                if (i == 0) {
-                    mbar_arrive_expect_tx(a_full, 2 * L::kTile);
-                    load_tile<128, DP>(smem + L::kA1, &map_a1, a0, ha, b, a_full);
-                }
-                mbar_arrive_expect_tx(&b1_full[s1], L::kTile);
-                load_tile<128, DP>(smem + L::kB1 + s1 * L::kTile, &map_b1, row, hb, b,
-                                   &b1_full[s1]);
-                if (i == 0) load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, a_full);
+        int issued1 = early1, issued2 = early2;
+        for (int i = early2; i < blocks; ++i) {
+            if (i >= early1) {
+                if (!warp_wait(&b1_empty[i % N1], i / N1 - 1, limit)) break;
+                if (lane == 0) load1(i);
+                issued1 = i + 1;
             }
-            __syncwarp();
-            issued1 = i + 1;
-            if (KV && i >= NR && !warp_wait(&r_empty[sr], i / NR - 1, limit)) break;
-            if (i >= N2 && !warp_wait(&b2_empty[s2], i / N2 - 1, limit)) break;
+            if (KV && !warp_wait(&r_empty[i % NR], i / NR - 1, limit)) break;
+            if (!warp_wait(&b2_empty[i % N2], i / N2 - 1, limit)) break;
             if (lane == 0) {
-                if (KV) {
-                    const int64_t r = (static_cast<int64_t>(b) * t.heads + hb) * padded + row;
-                    mbar_arrive_expect_tx(&r_full[sr], 2 * 128 * 4);
-                    bulk_load(rows_s + 256 * sr, ws_lse + r, 128 * 4, &r_full[sr]);
-                    bulk_load(rows_s + 256 * sr + 128, ws_delta + r, 128 * 4, &r_full[sr]);
-                }
-                mbar_arrive_expect_tx(&b2_full[s2], L::kTile);
-                load_tile<128, DP>(smem + L::kB2 + s2 * L::kTile, &map_b2, row, hb, b,
-                                   &b2_full[s2]);
+                if (KV) load_rows(i);
+                load2(i);
             }
-            __syncwarp();
             issued2 = i + 1;
         }
-        // After an abort copies may still be in flight: none may land in
-        // shared memory after the CTA exits (bounded waits).
-        if (*limit.abort_flag && lane == 0 && issued1 > 0) {
-            mbar_wait<false>(a_full, 0u, t.wait_limit_cycles);
+        // A copy may still be in flight after an abort, or the fixed tiles'
+        // without blocks: none may land in shared memory after the CTA exits
+        // (bounded waits).
+        mbar_wait<false>(a_full, 0u, t.wait_limit_cycles);
+        if (*limit.abort_flag) {
             for (int i = max(0, issued1 - N1); i < issued1; ++i)
                 mbar_wait<false>(&b1_full[i % N1], (i / N1) & 1, t.wait_limit_cycles);
             for (int i = max(0, issued2 - N2); i < issued2; ++i) {
@@ -496,7 +526,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         for (int i = 0; i < blocks; ++i) {
             const int st = i % N1;
             if (!warp_wait(&b1_full[st], i / N1, limit)) break;
-            mask_tile<128, DP>(mask, t.key_len, block_row(i), smem + L::kB1 + st * L::kTile,
+            mask_tile<BLK, DP>(mask, t.key_len, block_row(i), smem + L::kB1 + st * L::kBlock,
                                words + 4 * st, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&b1_masked[st]);
@@ -504,29 +534,34 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kBwdMmaWarp) tmem_dealloc(tmem, kBwdTmemCols);
+    if (warp == kBwdMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
 template <int DP, bool KV>
 cudaError_t launch_bwd(const FattnTask& t, int slot, cudaStream_t stream) {
     const void* kern = reinterpret_cast<const void*>(fattn_bwd_kernel<DP, KV>);
-    constexpr int smem = BwdSmem<DP>::kBytes;
+    constexpr int smem = BwdPlan<DP>::kBytes;
     static_assert(smem <= 232448, "the shared memory of a CTA");
     cudaError_t e = ensure_smem_attribute(kern, slot, smem, false);
     if (e != cudaSuccess) return e;
-    CUtensorMap mq, mg, mk, mv;
-    if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, 128) ||
-        !encode_heads_map(&mg, t.go, t, t.heads, t.query_len, t.go_stride, 128) ||
-        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, 128) ||
-        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, 128))
+    constexpr int kBlk = BwdPlan<DP>::kBlk;
+    constexpr int RQ = KV ? kBlk : 128, RK = KV ? 128 : kBlk;
+    CUtensorMap mq, mg, mk, mv, md1, md2;
+    if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, RQ) ||
+        !encode_heads_map(&mg, t.go, t, t.heads, t.query_len, t.go_stride, RQ) ||
+        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, RK) ||
+        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, RK) ||
+        !(KV ? encode_heads_map(&md1, t.dv, t, t.kv_heads, t.key_len, t.dv_stride, 32) &&
+                   encode_heads_map(&md2, t.dk, t, t.kv_heads, t.key_len, t.dk_stride, 32)
+             : encode_heads_map(&md1, t.dq, t, t.heads, t.query_len, t.dq_stride, 32)))
         return cudaErrorInvalidValue;
     const int64_t length = KV ? t.key_len : t.query_len;
     const int64_t heads = KV ? t.kv_heads : t.heads;
     const int64_t grid = (length + 127) / 128 * t.batch * heads;
     if (grid == 0) return cudaSuccess;
     fattn_bwd_kernel<DP, KV><<<static_cast<unsigned>(grid), kBwdThreads, smem, stream>>>(
-        t, KV ? mk : mq, KV ? mv : mg, KV ? mq : mk, KV ? mg : mv);
+        t, KV ? mk : mq, KV ? mv : mg, KV ? mq : mk, KV ? mg : mv, md1, KV ? md2 : md1);
     return cudaGetLastError();
 }
 

@@ -4,20 +4,27 @@
 // in one pass over the keys with the running m and l of a softmax: the
 // scores never leave the SM.
 //
-// A CTA takes 256 query rows of one head as two tiles of 128 and walks the
-// keys in blocks of 128.  Tensor memory holds both tiles' scores (128
-// columns each) and outputs (DP columns each); a tile's weights overwrite
-// its scores as bf16 and are the next product's A operand there.  Roles, one
-// mbarrier hand-off each:
-//   warps 0-3, 4-7  softmax of tile 0 and 1, one row a thread: the row's 128
-//                   scores to registers, the maximum, 2^(s c - m c) and the
-//                   sum, the weights back to tensor memory;
-//   warp 8          issues the products: for each block and tile P V, then
-//                   the next block's Q K^T into the columns P V has read, so
-//                   that one tile's products run under the other's softmax;
-//   warp 9          tensor copies of Q, and of K and V into rings;
-//   warp 10         with a key mask only: a block's kept keys as bits, and
-//                   zeros over the removed keys' rows of V.
+// A CTA takes tiles of 128 query rows of one head, and walks the keys in
+// blocks.  Tensor memory holds each tile's scores (a block's columns) and
+// output (DP columns); a tile's weights overwrite its scores as bf16 and are
+// the next product's A operand there.  Several tiles must be under way on an
+// SM, so that one's products run under the others' softmax:
+//   d_head > 64   two tiles in one CTA, blocks of 128 keys: it reads K and V
+//                 from shared memory and from L2 once for both, and their
+//                 traffic is what bounds it;
+//   d_head <= 64  three CTAs of one tile on an SM, blocks of 64 keys (128
+//                 columns of tensor memory and 80 registers a thread each):
+//                 the start and the end of one, microseconds that short
+//                 sequences feel, run under the others' work.
+// Roles of a CTA of T tiles, one mbarrier hand-off each:
+//   4 T warps  softmax, one row a thread: the maximum of the row's scores,
+//              2^(s c - m c) and the sum, the weights back to tensor memory;
+//              at the end the output, through shared memory, by tensor copies;
+//   MMA warp   issues the products: for each block and tile P V, then the
+//              next block's Q K^T into the columns P V has read;
+//   loader     tensor copies of Q, and of K and V into rings;
+//   mask warp  with a key mask only: a block's kept keys as bits, and zeros
+//              over the removed keys' rows of V.
 //
 // The weights are rounded to bf16, the type the tensor cores take next to
 // bf16 values; their sum is taken in fp32 before that.  m may lag the true
@@ -35,62 +42,69 @@ namespace {
 
 using namespace csd;
 
-constexpr int kFwdThreads = 384;
-// Registers a thread: 168 at launch; the softmax warps, whose row of scores is
-// 128 of them, take what the others give up: 256 x 208 + 128 x 72 <= 384 x 168.
-constexpr int kFwdRegsSoftmax = 208;
-constexpr int kFwdRegsOther = 72;
-constexpr int kFwdMmaWarp = 8;
-constexpr int kFwdLoadWarp = 9;
-constexpr int kFwdMaskWarp = 10;
-constexpr uint32_t kFwdTmemCols = 512;
 constexpr float kRescaleBits = 8.0f;
 
 template <int DP>
-struct FwdSmem {
-    static constexpr int kTile = 128 * DP * 2;
+struct FwdPlan {
+    static constexpr int kTiles = DP == 64 ? 1 : 2;
+    static constexpr int kBlk = DP == 64 ? 64 : 128;      // keys of a block
+    static constexpr int kCtasPerSm = DP == 64 ? 3 : 1;
+    static constexpr uint32_t kTmemCols = DP == 64 ? 128 : 512;
+    static constexpr int kMmaWarp = 4 * kTiles;
+    static constexpr int kLoadWarp = kMmaWarp + 1;
+    static constexpr int kMaskWarp = kMmaWarp + 2;
+    static constexpr int kThreads = 32 * (kMmaWarp + 4);
+    // Scores a softmax thread holds: the whole row, or, with 80 registers, 32
+    // at a time, read from tensor memory once for the maximum and once for
+    // the weights.
+    static constexpr int kChunk = DP == 64 ? 32 : 128;
+    // Registers a thread with two tiles: 168 at launch; the softmax warps
+    // take what the others give up: 256 x 208 + 128 x 72 <= 384 x 168.
+    static constexpr int kRegsSoftmax = 208;
+    static constexpr int kRegsOther = 72;
+    // Shared memory.
+    static constexpr int kTile = 128 * DP * 2;            // of Q
+    static constexpr int kBlock = kBlk * DP * 2;          // of K or V
     static constexpr int kStages = DP == 64 ? 3 : 2;      // of K and of V
     static constexpr int kQ = 0;
-    static constexpr int kK = kQ + 2 * kTile;
-    static constexpr int kV = kK + kStages * kTile;
-    static constexpr int kBars = kV + kStages * kTile;
-    static constexpr int kNumBars = 2 + 5 * kStages + 2 + 2 + 2 + 1;
+    static constexpr int kK = kQ + kTiles * kTile;
+    static constexpr int kV = kK + kStages * kBlock;
+    static constexpr int kBars = kV + kStages * kBlock;
+    static constexpr int kNumBars = 5 * kStages + 4 * kTiles + 1;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages][4]
-    static constexpr int kFlags = kWords + kStages * 16;  // abort, tmem, lo, hi
+    static constexpr int kFlags = kWords + kStages * 16;  // abort, tmem
     static constexpr int kBytes = kFlags + 16 + 1024;     // and alignment slack
 };
 
-// D[128 x DP] (+)= P[128 x R] . B[R x DP], P bf16 in tensor memory, B a tile.
-template <int R, int DP>
-__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t p, uint32_t b,
-                                            bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16(128, DP, true);
+// -inf for the columns whose bit is not set.
+template <int N>
+__device__ __forceinline__ void remove_columns(uint32_t (&s)[N], const uint32_t* kept) {
 #pragma unroll
-    for (int ks = 0; ks < R / 16; ++ks)
-        mma_bf16_ts(d, p + 8 * ks, smem_desc_mn_sw128(b + ks * 2048, R * 128, 1024), idesc,
-                    accumulate || ks > 0);
+    for (int k = 0; k < N; ++k)
+        if (!((kept[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(FwdPlan<DP>::kThreads, FwdPlan<DP>::kCtasPerSm)
 fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                  const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v) {
-    using L = FwdSmem<DP>;
-    constexpr int NS = L::kStages;
+                 const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ CUtensorMap map_o) {
+    using L = FwdPlan<DP>;
+    constexpr int NS = L::kStages, T = L::kTiles, BLK = L::kBlk, CH = L::kChunk;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-    uint64_t* q_full = bars;                  // [2] tile's queries landed
-    uint64_t* k_full = q_full + 2;            // [NS] ring stage landed
+    uint64_t* k_full = bars;                  // [NS] ring stage landed
     uint64_t* k_empty = k_full + NS;          // [NS] products that read it completed
     uint64_t* v_full = k_empty + NS;
     uint64_t* v_empty = v_full + NS;
     uint64_t* v_masked = v_empty + NS;        // [NS] removed rows zeroed, bits written
-    uint64_t* s_full = v_masked + NS;         // [2] tile's scores of a block
-    uint64_t* p_full = s_full + 2;            // [2] tile's weights of a block
-    uint64_t* o_full = p_full + 2;            // [2] the block's P V completed
-    uint64_t* drained = o_full + 2;
+    uint64_t* q_full = v_masked + NS;         // [T] tile's queries landed
+    uint64_t* s_full = q_full + T;            // [T] tile's scores of a block
+    uint64_t* o_full = s_full + T;            // [T] the block's P V completed
+    uint64_t* drained = o_full + T;
+    uint64_t* p_full = drained + 1;           // [T] tile's weights, from four warps
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
@@ -98,67 +112,89 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int BH = t.batch * t.heads;
-    const int q_tiles = (t.query_len + 255) / 256;
+    const int q_tiles = (t.query_len + 128 * T - 1) / (128 * T);
     // Under the causal mask later rows keep more keys: longest first.
     const int qt = t.causal ? q_tiles - 1 - static_cast<int>(blockIdx.x / BH)
                             : static_cast<int>(blockIdx.x / BH);
     const int bh = static_cast<int>(blockIdx.x % BH);
     const int b = bh / t.heads, h = bh - b * t.heads;
     const int hk = h / (t.heads / t.kv_heads);
-    const int q0 = 256 * qt;
+    const int q0 = 128 * T * qt;
     const int off = t.key_len - t.query_len;   // row i keeps keys j <= i + off
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1u);
-            mbar_init(&s_full[i], 1u);
-            mbar_init(&p_full[i], 4u);
-            mbar_init(&o_full[i], 1u);
-        }
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&k_full[i], 1u);
-            mbar_init(&k_empty[i], 1u);
-            mbar_init(&v_full[i], 1u);
-            mbar_init(&v_empty[i], 1u);
-            mbar_init(&v_masked[i], 1u);
-        }
-        mbar_init(drained, 1u);
-        flags[0] = 0u;
+    // The loader initialises the barriers, and starts its first copies before
+    // the others have set up.
+    if (warp == L::kLoadWarp) {
+        if (lane < L::kNumBars) mbar_init(bars + lane, bars + lane < p_full ? 1u : 4u);
+        if (lane == 0) flags[0] = 0u;
+        static_assert(L::kNumBars <= 32, "a lane a barrier");
         fence_mbar_init();
+        __syncwarp();
+        if (lane == 0) {
+            if (t.key_len > 0) {   // (an empty tensor has no map)
+                prefetch_tmap(&map_k);
+                prefetch_tmap(&map_v);
+            }
+            for (int i = 0; i < T; ++i) {
+                if (q0 + 128 * i >= t.query_len) break;
+                mbar_arrive_expect_tx(&q_full[i], L::kTile);
+                load_tile<128, DP>(smem + L::kQ + i * L::kTile, &map_q, q0 + 128 * i, h, b,
+                                   &q_full[i]);
+            }
+            prefetch_tmap(&map_o);
+        }
+        __syncwarp();
+    } else if (warp == L::kMmaWarp) {
+        tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
     }
-    if (warp == kFwdMmaWarp)
-        tmem_alloc(const_cast<uint32_t*>(flags) + 1, kFwdTmemCols);
     const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
     int key_lo = 0, key_hi = t.key_len;
-    if (mask)
-        block_nonzero_range(mask, t.key_len,
-                            reinterpret_cast<int*>(smem + L::kFlags) + 2, key_lo, key_hi);
+    if (mask) warp_nonzero_range(mask, t.key_len, lane, key_lo, key_hi);
+
+    // Blocks j0, j0 + 1, ..: n[i] of them for tile i, none for a tile without
+    // rows or without kept keys.
+    const int j0 = key_lo / BLK;
+    int n[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        const int last = min(q0 + 128 * (i + 1), t.query_len) - 1;
+        const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
+        n[i] = last >= q0 + 128 * i && hi > key_lo ? (hi + BLK - 1) / BLK - j0 : 0;
+    }
+    const int blocks = max(n[0], n[1]);
+    auto load_k = [&](int j) {
+        const int st = j % NS;
+        mbar_arrive_expect_tx(&k_full[st], L::kBlock);
+        load_tile<BLK, DP>(smem + L::kK + st * L::kBlock, &map_k, (j0 + j) * BLK, hk, b,
+                           &k_full[st]);
+    };
+    auto load_v = [&](int j) {
+        const int st = j % NS;
+        mbar_arrive_expect_tx(&v_full[st], L::kBlock);
+        load_tile<BLK, DP>(smem + L::kV + st * L::kBlock, &map_v, (j0 + j) * BLK, hk, b,
+                           &v_full[st]);
+    };
+    const int early = min(blocks, NS);
+    if (warp == L::kLoadWarp && lane == 0) {
+        for (int j = 0; j < early; ++j) {
+            load_k(j);
+            load_v(j);
+        }
+    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = flags[1];
 
-    // Blocks j0, j0 + 1, ..: n[i] of them for tile i, none for a tile without
-    // rows or without kept keys.
-    const int j0 = key_lo >> 7;
-    int n[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int last = min(q0 + 128 * (i + 1), t.query_len) - 1;
-        const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
-        n[i] = last >= q0 + 128 * i && hi > key_lo ? ((hi + 127) >> 7) - j0 : 0;
-    }
-    const int blocks = max(n[0], n[1]);
-
-    if (warp < 8) {
+    if (warp < 4 * T) {
         // -------------------------------------------------------- softmax
-        take_registers<kFwdRegsSoftmax>();
+        if (T == 2) take_registers<L::kRegsSoftmax>();
         const int tile = warp >> 2;
         const int row0 = q0 + 128 * tile + 32 * (warp & 3);
         const int i = row0 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128 * tile;
-        const uint32_t to = tmem + lanes + 256 + DP * tile;
+        const uint32_t ts = tmem + lanes + BLK * tile;
+        const uint32_t to = tmem + lanes + BLK * T + DP * tile;
         const float c = t.scale * kLog2e;
         // Keys below these limits are kept in every row of the warp, and in
         // this thread's.
@@ -172,28 +208,37 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             if (ok && mask) ok = warp_wait(&v_masked[j % NS], j / NS, limit);
             if (!ok) break;
             tc_fence_after_sync();
-            uint32_t s[128];
+            const int key = (j0 + j) * BLK;
+            bool edge = warp_limit < key + BLK;
+            uint32_t kept[BLK / 32];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) tmem_ld32_async(ts + 32 * u, s + 32 * u);
-            tmem_wait_ld<128>(s);
-            const int key = (j0 + j) << 7;
-            uint4 kept = make_uint4(~0u, ~0u, ~0u, ~0u);
-            if (mask) kept = *reinterpret_cast<const uint4*>(words + 4 * (j % NS));
-            if (warp_limit < key + 128 || (kept.x & kept.y & kept.z & kept.w) != ~0u) {
-                const uint32_t bits[4] = {kept.x & bits_below(row_limit, key),
-                                          kept.y & bits_below(row_limit, key + 32),
-                                          kept.z & bits_below(row_limit, key + 64),
-                                          kept.w & bits_below(row_limit, key + 96)};
-#pragma unroll
-                for (int k = 0; k < 128; ++k)
-                    if (!((bits[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
+            for (int u = 0; u < BLK / 32; ++u) {
+                kept[u] = mask ? words[4 * (j % NS) + u] : ~0u;
+                edge = edge || kept[u] != ~0u;
             }
-            float mx[4];
+            if (edge) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
+                for (int u = 0; u < BLK / 32; ++u) kept[u] &= bits_below(row_limit, key + 32 * u);
+            }
+            uint32_t s[CH];
+            auto load = [&](int x) {
 #pragma unroll
-            for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
-            const float top = fmaxf(fmaxf(m, fmaxf(mx[0], mx[1])), fmaxf(mx[2], mx[3]));
+                for (int u = 0; u < CH / 32; ++u) tmem_ld32_async(ts + CH * x + 32 * u, s + 32 * u);
+                tmem_wait_ld<CH>(s);
+                if (edge) remove_columns(s, kept + CH / 32 * x);
+            };
+            float mx[4] = {m, m, m, m};
+#pragma unroll
+            for (int x = 0; x < BLK / CH; ++x) {
+                load(x);
+#pragma unroll
+                for (int k = 0; k < CH; k += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mx[y] = max3(mx[y], __uint_as_float(s[k + 2 * y]),
+                                     __uint_as_float(s[k + 2 * y + 1]));
+            }
+            const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
             if (j == 0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, (top - m) * c > kRescaleBits)) {
@@ -203,7 +248,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 ok = warp_wait(&o_full[tile], j - 1, limit);
                 if (!ok) break;
                 tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < DP / 32; ++u) {
                     uint32_t o[32];
                     tmem_ld32_async(to + 32 * u, o);
@@ -218,15 +263,21 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-                const float2 y = fma2(make_float2(__uint_as_float(s[2 * k]),
-                                                  __uint_as_float(s[2 * k + 1])), c2, mc2);
-                const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                sum[k & 1] = add2(sum[k & 1], e);
-                s[k] = pack_bf16(e.x, e.y);
+            for (int x = 0; x < BLK / CH; ++x) {
+                if (CH < BLK) load(x);
+#pragma unroll
+                for (int k = 0; k < CH / 2; ++k) {
+                    const float2 y = fma2(make_float2(__uint_as_float(s[2 * k]),
+                                                      __uint_as_float(s[2 * k + 1])), c2, mc2);
+                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                    sum[k & 1] = add2(sum[k & 1], e);
+                    s[k] = pack_bf16(e.x, e.y);
+                }
+                // (Over columns that this thread has read for good.)
+                if (CH == 32) tmem_st16(ts + 16 * x, s);
+#pragma unroll
+                for (int u = 0; u < CH / 64; ++u) tmem_st32(ts + CH / 2 * x + 32 * u, s + 32 * u);
             }
-            tmem_st32(ts, s);
-            tmem_st32(ts + 32, s + 32);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
@@ -234,13 +285,16 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
         }
+        // The tile's queries are read (or, without blocks, have landed) before
+        // the output is staged over them.
         if (ok && nt > 0) ok = warp_wait(&o_full[tile], nt - 1, limit);
-        if (ok) {
+        if (ok && nt == 0 && row0 < t.query_len) ok = warp_wait(&q_full[tile], 0, limit);
+        if (ok && row0 < t.query_len) {
             tc_fence_after_sync();
-            const bool live = i < t.query_len;
             const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
-            uint16_t* row = t.out + b * t.o_stride[0] + h * t.o_stride[1] + i * t.o_stride[2];
-#pragma unroll
+            unsigned char* stage = smem + L::kQ + tile * L::kTile;
+            const int r = 32 * (warp & 3);
+#pragma unroll 1
             for (int u = 0; u < DP / 32; ++u) {
                 uint32_t o[32];
 #pragma unroll
@@ -249,139 +303,123 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                     tmem_ld32_async(to + 32 * u, o);
                     tmem_wait_ld<32>(o);
                 }
-                if (live) store_row32(row, t.d_head, 32 * u, o, inv);
+                stage_row32(stage, r + lane, 32 * u, o, inv);
             }
-            if (live && t.lse)
-                t.lse[static_cast<int64_t>(bh) * t.query_len + i] =
-                    l == 0.0f ? -INFINITY : (m * c + log2f(l)) * kLn2;
-            if (live && !isfinite(l)) raise_error(t.err, kBitNan);
+            store_rows32(stage, r, 0, DP / 64, &map_o, row0, h, b, lane);
+            if (i < t.query_len) {
+                if (t.lse)
+                    t.lse[static_cast<int64_t>(bh) * t.query_len + i] =
+                        l == 0.0f ? -INFINITY : (m * c + log2f(l)) * kLn2;
+                if (!isfinite(l)) raise_error(t.err, kBitNan);
+            }
         }
-    } else if (give_registers<kFwdRegsOther>(); warp == kFwdMmaWarp) {
-        // ----------------------------------------------------- MMA issuer
-        const uint32_t q = smem_addr(smem + L::kQ);
-        const uint32_t k = smem_addr(smem + L::kK);
-        const uint32_t v = smem_addr(smem + L::kV);
-        auto scores = [&](int i, int j) {
-            if (lane == 0) {
-                mma_tiles<128, DP>(tmem + 128 * i, q + i * L::kTile, k + (j % NS) * L::kTile);
-                mma_commit(&s_full[i]);
-            }
-        };
-        bool ok = true;
-        if (blocks > 0) {
-            ok = warp_wait(&k_full[0], 0, limit);
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (n[i] == 0) continue;
-                ok = warp_wait(&q_full[i], 0, limit);
-                if (ok) scores(i, 0);
-            }
-            if (ok && lane == 0) mma_commit(&k_empty[0]);
-            __syncwarp();
-        }
-        uint64_t* v_ready = mask ? v_masked : v_full;
-        for (int j = 0; j < blocks && ok; ++j) {
-            ok = warp_wait(&v_ready[j % NS], j / NS, limit);
-            if (ok && j + 1 < blocks) ok = warp_wait(&k_full[(j + 1) % NS], (j + 1) / NS, limit);
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (j >= n[i]) continue;
-                ok = warp_wait(&p_full[i], j, limit);
-                if (!ok) break;
-                tc_fence_after_sync();
-                if (lane == 0) {
-                    mma_weights<128, DP>(tmem + 256 + DP * i, tmem + 128 * i,
-                                         v + (j % NS) * L::kTile, j > 0);
-                    mma_commit(&o_full[i]);
+    } else {
+        if (T == 2) give_registers<L::kRegsOther>();
+        if (warp == L::kMmaWarp) {
+            // ------------------------------------------------- MMA issuer
+            const bool leader = elect_lane();
+            const uint64_t q = tile_desc(smem_addr(smem + L::kQ));
+            const uint64_t k = tile_desc(smem_addr(smem + L::kK));
+            const uint64_t v = weights_desc<BLK>(smem_addr(smem + L::kV));
+            constexpr uint32_t tile = L::kTile / 16, step = L::kBlock / 16;
+            auto scores = [&](int i, int stage) {
+                mma_tiles<BLK, DP>(tmem + BLK * i, q + i * tile, k + stage * step, leader);
+                mma_commit(&s_full[i], leader);
+            };
+            bool ok = true;
+            if (blocks > 0) {
+                ok = warp_wait(&k_full[0], 0, limit);
+                for (int i = 0; i < T && ok; ++i) {
+                    if (n[i] == 0) continue;
+                    ok = warp_wait(&q_full[i], 0, limit);
+                    if (ok) scores(i, 0);
                 }
-                if (j + 1 < n[i]) scores(i, j + 1);
-                __syncwarp();
+                if (ok) mma_commit(&k_empty[0], leader);
             }
-            if (ok && lane == 0) {
-                mma_commit(&v_empty[j % NS]);
-                if (j + 1 < blocks) mma_commit(&k_empty[(j + 1) % NS]);
+            uint64_t* v_ready = mask ? v_masked : v_full;
+            for (int j = 0; j < blocks && ok; ++j) {
+                const int st = j % NS, st1 = (j + 1) % NS;
+                ok = warp_wait(&v_ready[st], j / NS, limit);
+                for (int i = 0; i < T && ok; ++i) {
+                    if (j >= n[i]) continue;
+                    ok = warp_wait(&p_full[i], j, limit);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    mma_weights<DP, BLK>(tmem + BLK * T + DP * i, tmem + BLK * i, v + st * step,
+                                         j > 0, leader);
+                    mma_commit(&o_full[i], leader);
+                    if (j + 1 < n[i]) {
+                        ok = warp_wait(&k_full[st1], (j + 1) / NS, limit);
+                        if (ok) scores(i, st1);
+                    }
+                }
+                if (ok) {
+                    mma_commit(&v_empty[st], leader);
+                    if (j + 1 < blocks) mma_commit(&k_empty[st1], leader);
+                }
             }
-            __syncwarp();
-        }
-        // No product may be in flight when the tensor memory is freed.
-        if (lane == 0) {
-            mma_commit(drained);
+            // No product may be in flight when the tensor memory is freed.
+            mma_commit(drained, leader);
             mbar_wait<false>(drained, 0u, t.wait_limit_cycles);
-        }
-        __syncwarp();
-    } else if (warp == kFwdLoadWarp) {
-        // --------------------------------------------------------- loader
-        bool ok = true;
-        int issued = 0;
-        for (int j = 0; j < blocks; ++j) {
-            const int st = j % NS;
-            if (j >= NS) ok = warp_wait(&k_empty[st], j / NS - 1, limit);
-            if (!ok) break;
-            if (lane == 0) {
-                if (j == 0 && n[0] > 0) {
-                    mbar_arrive_expect_tx(&q_full[0], L::kTile);
-                    load_tile<128, DP>(smem + L::kQ, &map_q, q0, h, b, &q_full[0]);
-                }
-                mbar_arrive_expect_tx(&k_full[st], L::kTile);
-                load_tile<128, DP>(smem + L::kK + st * L::kTile, &map_k, (j0 + j) << 7, hk, b,
-                                   &k_full[st]);
-                if (j == 0 && n[1] > 0) {
-                    mbar_arrive_expect_tx(&q_full[1], L::kTile);
-                    load_tile<128, DP>(smem + L::kQ + L::kTile, &map_q, q0 + 128, h, b,
-                                       &q_full[1]);
-                }
-            }
             __syncwarp();
-            if (j >= NS) ok = warp_wait(&v_empty[st], j / NS - 1, limit);
-            if (lane == 0 && ok) {
-                mbar_arrive_expect_tx(&v_full[st], L::kTile);
-                load_tile<128, DP>(smem + L::kV + st * L::kTile, &map_v, (j0 + j) << 7, hk, b,
-                                   &v_full[st]);
+        } else if (warp == L::kLoadWarp) {
+            // ----------------------------------------------------- loader
+            int k_issued = early, v_issued = early;
+            for (int j = early; j < blocks; ++j) {
+                if (!warp_wait(&k_empty[j % NS], j / NS - 1, limit)) break;
+                if (lane == 0) load_k(j);
+                k_issued = j + 1;
+                if (!warp_wait(&v_empty[j % NS], j / NS - 1, limit)) break;
+                if (lane == 0) load_v(j);
+                v_issued = j + 1;
             }
-            __syncwarp();
-            issued = j + 1;
-            if (!ok) break;
-        }
-        // After an abort copies may still be in flight: none may land in
-        // shared memory after the CTA exits (bounded waits).
-        if (*limit.abort_flag && lane == 0) {
-            for (int i = 0; i < 2; ++i)
-                if (n[i] > 0) mbar_wait<false>(&q_full[i], 0u, t.wait_limit_cycles);
-            for (int j = max(0, issued - NS); j < issued; ++j) {
-                mbar_wait<false>(&k_full[j % NS], (j / NS) & 1, t.wait_limit_cycles);
-                if (ok || j + 1 < issued)
+            // A copy may still be in flight after an abort, or that of a tile
+            // without blocks: none may land in shared memory after the CTA
+            // exits (bounded waits).
+            for (int i = 0; i < T; ++i)
+                if (q0 + 128 * i < t.query_len) mbar_wait<false>(&q_full[i], 0u, t.wait_limit_cycles);
+            if (*limit.abort_flag) {
+                for (int j = max(0, k_issued - NS); j < k_issued; ++j)
+                    mbar_wait<false>(&k_full[j % NS], (j / NS) & 1, t.wait_limit_cycles);
+                for (int j = max(0, v_issued - NS); j < v_issued; ++j)
                     mbar_wait<false>(&v_full[j % NS], (j / NS) & 1, t.wait_limit_cycles);
             }
-        }
-        __syncwarp();
-    } else if (warp == kFwdMaskWarp && mask) {
-        // ------------------------------------------------------ key masks
-        for (int j = 0; j < blocks; ++j) {
-            const int st = j % NS;
-            if (!warp_wait(&v_full[st], j / NS, limit)) break;
-            mask_tile<128, DP>(mask, t.key_len, (j0 + j) << 7, smem + L::kV + st * L::kTile,
-                               words + 4 * st, lane);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&v_masked[st]);
+        } else if (warp == L::kMaskWarp && mask) {
+            // -------------------------------------------------- key masks
+            for (int j = 0; j < blocks; ++j) {
+                const int st = j % NS;
+                if (!warp_wait(&v_full[st], j / NS, limit)) break;
+                mask_tile<BLK, DP>(mask, t.key_len, (j0 + j) * BLK, smem + L::kV + st * L::kBlock,
+                                   words + 4 * st, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_masked[st]);
+            }
         }
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kFwdMmaWarp) tmem_dealloc(tmem, kFwdTmemCols);
+    if (warp == L::kMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
 template <int DP>
 cudaError_t launch_fwd(const FattnTask& t, int slot, cudaStream_t stream) {
+    using L = FwdPlan<DP>;
     const void* kern = reinterpret_cast<const void*>(fattn_fwd_kernel<DP>);
-    cudaError_t e = ensure_smem_attribute(kern, slot, FwdSmem<DP>::kBytes, false);
+    cudaError_t e = ensure_smem_attribute(kern, slot, L::kBytes, false);
     if (e != cudaSuccess) return e;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, 128) ||
-        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, 128) ||
-        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, 128))
+        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, L::kBlk) ||
+        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, L::kBlk) ||
+        !encode_heads_map(&mo, t.out, t, t.heads, t.query_len, t.o_stride, 32))
         return cudaErrorInvalidValue;
-    const int64_t grid = static_cast<int64_t>((t.query_len + 255) / 256) * t.batch * t.heads;
-    fattn_fwd_kernel<DP><<<static_cast<unsigned>(grid), kFwdThreads, FwdSmem<DP>::kBytes,
-                           stream>>>(t, mq, mk, mv);
+    constexpr int kRows = 128 * L::kTiles;
+    const int64_t grid =
+        static_cast<int64_t>((t.query_len + kRows - 1) / kRows) * t.batch * t.heads;
+    fattn_fwd_kernel<DP><<<static_cast<unsigned>(grid), L::kThreads, L::kBytes, stream>>>(
+        t, mq, mk, mv, mo);
     return cudaGetLastError();
 }
 
