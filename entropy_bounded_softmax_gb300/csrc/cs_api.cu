@@ -591,13 +591,9 @@ cs_status check_attention_shape(const cs_attention_shape* s) {
     if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
     if (s->causal != 0 && s->causal != 1) return CS_ERR_INVALID_ARG;
     if (!isfinite(s->scale) || !(s->scale > 0.0f)) return CS_ERR_INVALID_ARG;
-    // Rows and tiles are counted in 32 bits.
-    if (s->query_len > (1 << 30) || s->key_len > (1 << 30) ||
-        static_cast<int64_t>(s->batch) * s->heads > kMaxGridX)
-        return CS_ERR_DIM_MISMATCH;
-    const int64_t bh = static_cast<int64_t>(s->batch) * s->heads;
-    if (bh * ceil_div(s->query_len, 128) > kMaxGridX ||
-        bh * ceil_div(s->key_len, 128) > kMaxGridX)
+    if (s->heads > cs::kFattnMaxHeads || s->batch > cs::kFattnMaxBatch ||
+        ceil_div(s->query_len, 128) > cs::kFattnMaxTiles ||
+        ceil_div(s->key_len, 128) > cs::kFattnMaxTiles)
         return CS_ERR_DIM_MISMATCH;
     return CS_OK;
 }
@@ -656,6 +652,7 @@ cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
     t.d_head = s.d_head;
     t.causal = s.causal;
     t.scale = s.scale;
+    t.inv_group = static_cast<float>(static_cast<double>(s.kv_heads) / s.heads);
     t.wait_limit_cycles = cs::kWaitLimitCycles;
     return t;
 }

@@ -39,6 +39,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, int phase, const WaitLi
     return __all_sync(0xffffffffu, ok);
 }
 
+// The key head of query head h (an integer division costs the start of a CTA
+// a hundred cycles): exact for h < 2^20, whose (h + 1/2) / group lies at least
+// 1 / (2 group) from an integer, further than the roundings reach.
+__device__ __forceinline__ int head_of(int h, float inv_group) {
+    return static_cast<int>((static_cast<float>(h) + 0.5f) * inv_group);
+}
+
 // Raises, or lowers, the registers of every thread of this warpgroup (four
 // warps, all of which call it) to N, a multiple of 8.  Raising waits for
 // registers that the block was launched with and has given up.

@@ -336,10 +336,15 @@ struct FattnTask {
     int32_t batch, heads, kv_heads, query_len, key_len, d_head;
     int32_t causal;
     float scale;
+    float inv_group;         // kv_heads / heads
     uint64_t wait_limit_cycles;
 };
 
 constexpr int kFattnMaxDHead = 128;
+// Heads, sequences and tiles of 128 rows are the launch's three dimensions.
+constexpr int kFattnMaxHeads = 1 << 20;
+constexpr int kFattnMaxBatch = 65535;
+constexpr int kFattnMaxTiles = 65535;
 
 // The backward's workspace: for every query row minus the log2 of its
 // normaliser and minus <grad_out, out>, two arrays of batch * heads rows of query_len rounded

@@ -136,18 +136,15 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int group = t.heads / t.kv_heads;
     const int fixed_len = KV ? t.key_len : t.query_len;
-    const int fixed_heads = KV ? t.kv_heads : t.heads;
-    const int BH = t.batch * fixed_heads;
-    const int tiles = (fixed_len + 127) / 128;
     // Under the causal mask late queries keep the most keys and early keys
     // have the most queries: longest first in both.
-    const int order = static_cast<int>(blockIdx.x / BH);
-    const int a0 = 128 * (!KV && t.causal ? tiles - 1 - order : order);
-    const int bh = static_cast<int>(blockIdx.x % BH);
-    const int b = bh / fixed_heads, ha = bh - b * fixed_heads;
+    const int ha = blockIdx.x, b = blockIdx.y;     // the fixed tiles' head
+    const int a0 = 128 * static_cast<int>(!KV && t.causal ? gridDim.z - 1 - blockIdx.z
+                                                          : blockIdx.z);
     const int off = t.key_len - t.query_len;   // query i keeps keys j <= i + off
+    const int group = KV ? t.heads / t.kv_heads : 1;
+    const int hk = KV ? ha : head_of(ha, t.inv_group);
     const int64_t padded = (static_cast<int64_t>(t.query_len) + 127) / 128 * 128;
     float* ws_lse = t.rows;
     float* ws_delta = t.rows + static_cast<int64_t>(t.batch) * t.heads * padded;
@@ -194,37 +191,50 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         if (hi > key_lo) per = (hi + BLK - 1) / BLK - first;
     }
     const int blocks = KV ? per * group : per;
-    // Block i's head on the streamed side and its first row there.
-    auto block_head = [&](int i) { return KV ? ha * group + i / per : ha / group; };
-    auto block_row = [&](int i) { return BLK * (first + (KV ? i % per : i)); };
-    auto load1 = [&](int i) {
+    // A block's head on the streamed side and its first row there, walked in
+    // order (each walker keeps its own: a division by `per` for every block
+    // would cost more than its elementwise part's shorter phase).
+    struct Place {
+        int head, row;
+    };
+    const Place begin{KV ? ha * group : hk, BLK * first};
+    auto advance = [&](Place& x) {
+        x.row += BLK;
+        if (KV && x.row >= BLK * (first + per)) {
+            x.row = BLK * first;
+            ++x.head;
+        }
+    };
+    auto load1 = [&](int i, Place& at) {
         uint64_t* bar = &b1_full[i % N1];
         mbar_arrive_expect_tx(bar, L::kBlock);
-        load_tile<BLK, DP>(smem + L::kB1 + (i % N1) * L::kBlock, &map_b1, block_row(i),
-                           block_head(i), b, bar);
+        load_tile<BLK, DP>(smem + L::kB1 + (i % N1) * L::kBlock, &map_b1, at.row, at.head, b,
+                           bar);
+        advance(at);
     };
-    auto load2 = [&](int i) {
+    // The second tensor's block, and for keys its queries' lse and delta.
+    auto load2 = [&](int i, Place& at) {
+        if (KV) {
+            const int64_t r = (static_cast<int64_t>(b) * t.heads + at.head) * padded + at.row;
+            uint64_t* bar = &r_full[i % NR];
+            float* rows = rows_s + 2 * BLK * (i % NR);
+            mbar_arrive_expect_tx(bar, 2 * BLK * 4);
+            bulk_load(rows, ws_lse + r, BLK * 4, bar);
+            bulk_load(rows + BLK, ws_delta + r, BLK * 4, bar);
+        }
         uint64_t* bar = &b2_full[i % N2];
         mbar_arrive_expect_tx(bar, L::kBlock);
-        load_tile<BLK, DP>(smem + L::kB2 + (i % N2) * L::kBlock, &map_b2, block_row(i),
-                           block_head(i), b, bar);
+        load_tile<BLK, DP>(smem + L::kB2 + (i % N2) * L::kBlock, &map_b2, at.row, at.head, b,
+                           bar);
+        advance(at);
     };
-    auto load_rows = [&](int i) {
-        const int64_t r =
-            (static_cast<int64_t>(b) * t.heads + block_head(i)) * padded + block_row(i);
-        uint64_t* bar = &r_full[i % NR];
-        float* at = rows_s + 2 * BLK * (i % NR);
-        mbar_arrive_expect_tx(bar, 2 * BLK * 4);
-        bulk_load(at, ws_lse + r, BLK * 4, bar);
-        bulk_load(at + BLK, ws_delta + r, BLK * 4, bar);
-    };
+    Place at1 = begin, at2 = begin;            // the loader's
     const int early1 = min(blocks, N1), early2 = min(blocks, N2);
     static_assert(N2 == NR, "the row values' ring is as deep as the second tensor's");
     if (warp == kBwdLoadWarp && lane == 0) {
         for (int i = 0; i < early1; ++i) {
-            load1(i);
-            if (KV && i < NR) load_rows(i);
-            if (i < N2) load2(i);
+            load1(i, at1);
+            if (i < N2) load2(i, at2);
         }
     }
     tc_fence_before_sync();
@@ -250,6 +260,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         const float2 c2 = make_float2(c, c);
         float row_lse = 0.0f, row_delta = 0.0f;   // queries: -lse, -delta
         if (!KV) {
+            const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
             // delta: DP / 8 lanes a row, 16 bytes of out and of g each.
             constexpr int LR = DP / 8;
             const int u = lane % LR;
@@ -276,20 +287,22 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             // An empty row, and a row past the last, gets -lse = -inf: P = 0.
             row_lse = -INFINITY;
             if (a < t.query_len) {
-                const float x = t.lse[static_cast<int64_t>(bh) * t.query_len + a];
+                const float x = t.lse[row * t.query_len + a];
                 if (x != -INFINITY) row_lse = -x * kLog2e;
             }
             named_barrier(kBarElementwise, kElementwise);
             row_delta = -rows_s[a - a0];
             if (half == 0) {
-                ws_lse[bh * padded + a] = row_lse;
-                ws_delta[bh * padded + a] = row_delta;
+                ws_lse[row * padded + a] = row_lse;
+                ws_delta[row * padded + a] = row_delta;
             }
         }
         bool ok = true;
+        Place place = begin;
         for (int i = 0; i < blocks; ++i) {
             const int st = i % NR;
-            const int b0 = block_row(i) + CO * half;     // first of this thread's columns
+            const int b0 = place.row + CO * half;        // first of this thread's columns
+            advance(place);
             // -lse and -delta of this thread's columns (keys).
             const float4* lse4 = reinterpret_cast<const float4*>(rows_s + 2 * BLK * st + CO * half);
             const float4* delta4 = lse4 + BLK / 4;
@@ -497,15 +510,12 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         for (int i = early2; i < blocks; ++i) {
             if (i >= early1) {
                 if (!warp_wait(&b1_empty[i % N1], i / N1 - 1, limit)) break;
-                if (lane == 0) load1(i);
+                if (lane == 0) load1(i, at1);
                 issued1 = i + 1;
             }
             if (KV && !warp_wait(&r_empty[i % NR], i / NR - 1, limit)) break;
             if (!warp_wait(&b2_empty[i % N2], i / N2 - 1, limit)) break;
-            if (lane == 0) {
-                if (KV) load_rows(i);
-                load2(i);
-            }
+            if (lane == 0) load2(i, at2);
             issued2 = i + 1;
         }
         // A copy may still be in flight after an abort, or the fixed tiles'
@@ -526,7 +536,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         for (int i = 0; i < blocks; ++i) {
             const int st = i % N1;
             if (!warp_wait(&b1_full[st], i / N1, limit)) break;
-            mask_tile<BLK, DP>(mask, t.key_len, block_row(i), smem + L::kB1 + st * L::kBlock,
+            mask_tile<BLK, DP>(mask, t.key_len, BLK * (first + i), smem + L::kB1 + st * L::kBlock,
                                words + 4 * st, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&b1_masked[st]);
@@ -556,11 +566,10 @@ cudaError_t launch_bwd(const FattnTask& t, int slot, cudaStream_t stream) {
                    encode_heads_map(&md2, t.dk, t, t.kv_heads, t.key_len, t.dk_stride, 32)
              : encode_heads_map(&md1, t.dq, t, t.heads, t.query_len, t.dq_stride, 32)))
         return cudaErrorInvalidValue;
-    const int64_t length = KV ? t.key_len : t.query_len;
-    const int64_t heads = KV ? t.kv_heads : t.heads;
-    const int64_t grid = (length + 127) / 128 * t.batch * heads;
-    if (grid == 0) return cudaSuccess;
-    fattn_bwd_kernel<DP, KV><<<static_cast<unsigned>(grid), kBwdThreads, smem, stream>>>(
+    const int length = KV ? t.key_len : t.query_len;
+    if (length == 0) return cudaSuccess;
+    const dim3 grid(KV ? t.kv_heads : t.heads, t.batch, (length + 127) / 128);
+    fattn_bwd_kernel<DP, KV><<<grid, kBwdThreads, smem, stream>>>(
         t, KV ? mk : mq, KV ? mv : mg, KV ? mq : mk, KV ? mg : mv, md1, KV ? md2 : md1);
     return cudaGetLastError();
 }

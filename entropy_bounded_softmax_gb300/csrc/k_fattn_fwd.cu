@@ -5,23 +5,24 @@
 // scores never leave the SM.
 //
 // A CTA takes tiles of 128 query rows of one head, and walks the keys in
-// blocks.  Tensor memory holds each tile's scores (a block's columns) and
-// output (DP columns); a tile's weights overwrite its scores as bf16 and are
-// the next product's A operand there.  Several tiles must be under way on an
-// SM, so that one's products run under the others' softmax:
-//   d_head > 64   two tiles in one CTA, blocks of 128 keys: it reads K and V
-//                 from shared memory and from L2 once for both, and their
-//                 traffic is what bounds it;
-//   d_head <= 64  three CTAs of one tile on an SM, blocks of 64 keys (128
-//                 columns of tensor memory and 80 registers a thread each):
-//                 the start and the end of one, microseconds that short
-//                 sequences feel, run under the others' work.
+// blocks.  Tensor memory holds two buffers of scores (a block's columns each)
+// and each tile's output (DP columns); a tile's weights overwrite its scores
+// as bf16 and are the next product's A operand there.
+//   d_head > 64   two tiles in one CTA, blocks of 128 keys, a buffer a tile,
+//                 so that one tile's products run under the other's softmax.
+//                 K and V are read from shared memory and from L2 once for
+//                 both: that traffic bounds it;
+//   d_head <= 64  two CTAs of one tile on an SM, blocks of 64 keys, the
+//                 buffers for two blocks of it, so that its softmax need not
+//                 wait for products; the start and the end of one CTA,
+//                 microseconds that short sequences feel, run under the
+//                 other's work.
 // Roles of a CTA of T tiles, one mbarrier hand-off each:
 //   4 T warps  softmax, one row a thread: the maximum of the row's scores,
 //              2^(s c - m c) and the sum, the weights back to tensor memory;
 //              at the end the output, through shared memory, by tensor copies;
-//   MMA warp   issues the products: for each block and tile P V, then the
-//              next block's Q K^T into the columns P V has read;
+//   MMA warp   issues the products: for each block and tile P V, then a
+//              coming block's Q K^T into the columns P V has read;
 //   loader     tensor copies of Q, and of K and V into rings;
 //   mask warp  with a key mask only: a block's kept keys as bits, and zeros
 //              over the removed keys' rows of V.
@@ -48,16 +49,14 @@ template <int DP>
 struct FwdPlan {
     static constexpr int kTiles = DP == 64 ? 1 : 2;
     static constexpr int kBlk = DP == 64 ? 64 : 128;      // keys of a block
-    static constexpr int kCtasPerSm = DP == 64 ? 3 : 1;
-    static constexpr uint32_t kTmemCols = DP == 64 ? 128 : 512;
+    static constexpr int kCtasPerSm = DP == 64 ? 2 : 1;
+    static constexpr uint32_t kTmemCols = DP == 64 ? 256 : 512;
+    // Blocks whose scores are computed ahead of the first block's weights.
+    static constexpr int kAhead = 2 / kTiles;
     static constexpr int kMmaWarp = 4 * kTiles;
     static constexpr int kLoadWarp = kMmaWarp + 1;
     static constexpr int kMaskWarp = kMmaWarp + 2;
     static constexpr int kThreads = 32 * (kMmaWarp + 4);
-    // Scores a softmax thread holds: the whole row, or, with 80 registers, 32
-    // at a time, read from tensor memory once for the maximum and once for
-    // the weights.
-    static constexpr int kChunk = DP == 64 ? 32 : 128;
     // Registers a thread with two tiles: 168 at launch; the softmax warps
     // take what the others give up: 256 x 208 + 128 x 72 <= 384 x 168.
     static constexpr int kRegsSoftmax = 208;
@@ -70,7 +69,7 @@ struct FwdPlan {
     static constexpr int kK = kQ + kTiles * kTile;
     static constexpr int kV = kK + kStages * kBlock;
     static constexpr int kBars = kV + kStages * kBlock;
-    static constexpr int kNumBars = 5 * kStages + 4 * kTiles + 1;
+    static constexpr int kNumBars = 5 * kStages + 2 * kTiles + 4 + 1;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages][4]
     static constexpr int kFlags = kWords + kStages * 16;  // abort, tmem
     static constexpr int kBytes = kFlags + 16 + 1024;     // and alignment slack
@@ -91,7 +90,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                  const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ CUtensorMap map_o) {
     using L = FwdPlan<DP>;
-    constexpr int NS = L::kStages, T = L::kTiles, BLK = L::kBlk, CH = L::kChunk;
+    constexpr int NS = L::kStages, T = L::kTiles, BLK = L::kBlk, AHEAD = L::kAhead;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -101,24 +100,21 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     uint64_t* v_empty = v_full + NS;
     uint64_t* v_masked = v_empty + NS;        // [NS] removed rows zeroed, bits written
     uint64_t* q_full = v_masked + NS;         // [T] tile's queries landed
-    uint64_t* s_full = q_full + T;            // [T] tile's scores of a block
-    uint64_t* o_full = s_full + T;            // [T] the block's P V completed
+    uint64_t* s_full = q_full + T;            // [2] a buffer's scores
+    uint64_t* o_full = s_full + 2;            // [T] the block's P V completed
     uint64_t* drained = o_full + T;
-    uint64_t* p_full = drained + 1;           // [T] tile's weights, from four warps
+    uint64_t* p_full = drained + 1;           // [2] a buffer's weights, from four warps
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int BH = t.batch * t.heads;
-    const int q_tiles = (t.query_len + 128 * T - 1) / (128 * T);
     // Under the causal mask later rows keep more keys: longest first.
-    const int qt = t.causal ? q_tiles - 1 - static_cast<int>(blockIdx.x / BH)
-                            : static_cast<int>(blockIdx.x / BH);
-    const int bh = static_cast<int>(blockIdx.x % BH);
-    const int b = bh / t.heads, h = bh - b * t.heads;
-    const int hk = h / (t.heads / t.kv_heads);
+    const int h = blockIdx.x, b = blockIdx.y;
+    const int qt = t.causal ? static_cast<int>(gridDim.z - 1 - blockIdx.z)
+                            : static_cast<int>(blockIdx.z);
+    const int hk = head_of(h, t.inv_group);
     const int q0 = 128 * T * qt;
     const int off = t.key_len - t.query_len;   // row i keeps keys j <= i + off
 
@@ -174,6 +170,9 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         load_tile<BLK, DP>(smem + L::kV + st * L::kBlock, &map_v, (j0 + j) * BLK, hk, b,
                            &v_full[st]);
     };
+    // The buffer and the phase of its barriers for tile i's block j.
+    auto buffer = [&](int i, int j) { return T == 2 ? i : j & 1; };
+    auto phase = [&](int j) { return T == 2 ? j : j >> 1; };
     const int early = min(blocks, NS);
     if (warp == L::kLoadWarp && lane == 0) {
         for (int j = 0; j < early; ++j) {
@@ -193,8 +192,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         const int row0 = q0 + 128 * tile + 32 * (warp & 3);
         const int i = row0 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + BLK * tile;
-        const uint32_t to = tmem + lanes + BLK * T + DP * tile;
+        const uint32_t to = tmem + lanes + 2 * BLK + DP * tile;
         const float c = t.scale * kLog2e;
         // Keys below these limits are kept in every row of the warp, and in
         // this thread's.
@@ -204,7 +202,9 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         bool ok = true;
         const int nt = n[tile];
         for (int j = 0; j < nt; ++j) {
-            ok = warp_wait(&s_full[tile], j, limit);
+            const int buf = buffer(tile, j);
+            const uint32_t ts = tmem + lanes + BLK * buf;
+            ok = warp_wait(&s_full[buf], phase(j), limit);
             if (ok && mask) ok = warp_wait(&v_masked[j % NS], j / NS, limit);
             if (!ok) break;
             tc_fence_after_sync();
@@ -220,24 +220,18 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
                 for (int u = 0; u < BLK / 32; ++u) kept[u] &= bits_below(row_limit, key + 32 * u);
             }
-            uint32_t s[CH];
-            auto load = [&](int x) {
+            uint32_t s[BLK];
 #pragma unroll
-                for (int u = 0; u < CH / 32; ++u) tmem_ld32_async(ts + CH * x + 32 * u, s + 32 * u);
-                tmem_wait_ld<CH>(s);
-                if (edge) remove_columns(s, kept + CH / 32 * x);
-            };
+            for (int u = 0; u < BLK / 32; ++u) tmem_ld32_async(ts + 32 * u, s + 32 * u);
+            tmem_wait_ld<BLK>(s);
+            if (edge) remove_columns(s, kept);
             float mx[4] = {m, m, m, m};
 #pragma unroll
-            for (int x = 0; x < BLK / CH; ++x) {
-                load(x);
+            for (int k = 0; k < BLK; k += 8)
 #pragma unroll
-                for (int k = 0; k < CH; k += 8)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        mx[y] = max3(mx[y], __uint_as_float(s[k + 2 * y]),
-                                     __uint_as_float(s[k + 2 * y + 1]));
-            }
+                for (int y = 0; y < 4; ++y)
+                    mx[y] = max3(mx[y], __uint_as_float(s[k + 2 * y]),
+                                 __uint_as_float(s[k + 2 * y + 1]));
             const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
             if (j == 0) {
                 m = top;
@@ -263,30 +257,27 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int x = 0; x < BLK / CH; ++x) {
-                if (CH < BLK) load(x);
-#pragma unroll
-                for (int k = 0; k < CH / 2; ++k) {
-                    const float2 y = fma2(make_float2(__uint_as_float(s[2 * k]),
-                                                      __uint_as_float(s[2 * k + 1])), c2, mc2);
-                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                    sum[k & 1] = add2(sum[k & 1], e);
-                    s[k] = pack_bf16(e.x, e.y);
-                }
-                // (Over columns that this thread has read for good.)
-                if (CH == 32) tmem_st16(ts + 16 * x, s);
-#pragma unroll
-                for (int u = 0; u < CH / 64; ++u) tmem_st32(ts + CH / 2 * x + 32 * u, s + 32 * u);
+            for (int k = 0; k < BLK / 2; ++k) {
+                const float2 y = fma2(make_float2(__uint_as_float(s[2 * k]),
+                                                  __uint_as_float(s[2 * k + 1])), c2, mc2);
+                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                sum[k & 1] = add2(sum[k & 1], e);
+                s[k] = pack_bf16(e.x, e.y);
             }
+#pragma unroll
+            for (int u = 0; u < BLK / 64; ++u) tmem_st32(ts + 32 * u, s + 32 * u);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[tile]);
+            if (lane == 0) mbar_arrive(&p_full[buf]);
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
         }
         // The tile's queries are read (or, without blocks, have landed) before
         // the output is staged over them.
+        // (A barrier tells a phase from the one before only: with two buffers
+        // the last two products may both be under way.)
+        if (ok && nt > 1) ok = warp_wait(&o_full[tile], nt - 2, limit);
         if (ok && nt > 0) ok = warp_wait(&o_full[tile], nt - 1, limit);
         if (ok && nt == 0 && row0 < t.query_len) ok = warp_wait(&q_full[tile], 0, limit);
         if (ok && row0 < t.query_len) {
@@ -294,6 +285,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
             unsigned char* stage = smem + L::kQ + tile * L::kTile;
             const int r = 32 * (warp & 3);
+            const int64_t row = (static_cast<int64_t>(b) * t.heads + h) * t.query_len + i;
 #pragma unroll 1
             for (int u = 0; u < DP / 32; ++u) {
                 uint32_t o[32];
@@ -308,7 +300,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             store_rows32(stage, r, 0, DP / 64, &map_o, row0, h, b, lane);
             if (i < t.query_len) {
                 if (t.lse)
-                    t.lse[static_cast<int64_t>(bh) * t.query_len + i] =
+                    t.lse[row] =
                         l == 0.0f ? -INFINITY : (m * c + log2f(l)) * kLn2;
                 if (!isfinite(l)) raise_error(t.err, kBitNan);
             }
@@ -322,40 +314,42 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             const uint64_t k = tile_desc(smem_addr(smem + L::kK));
             const uint64_t v = weights_desc<BLK>(smem_addr(smem + L::kV));
             constexpr uint32_t tile = L::kTile / 16, step = L::kBlock / 16;
-            auto scores = [&](int i, int stage) {
-                mma_tiles<BLK, DP>(tmem + BLK * i, q + i * tile, k + stage * step, leader);
-                mma_commit(&s_full[i], leader);
+            auto scores = [&](int i, int j) {
+                const int buf = buffer(i, j);
+                mma_tiles<BLK, DP>(tmem + BLK * buf, q + i * tile, k + (j % NS) * step, leader);
+                mma_commit(&s_full[buf], leader);
             };
             bool ok = true;
-            if (blocks > 0) {
-                ok = warp_wait(&k_full[0], 0, limit);
+            for (int j = 0; j < AHEAD && j < blocks && ok; ++j) {
+                ok = warp_wait(&k_full[j], 0, limit);
                 for (int i = 0; i < T && ok; ++i) {
-                    if (n[i] == 0) continue;
+                    if (j >= n[i]) continue;
                     ok = warp_wait(&q_full[i], 0, limit);
-                    if (ok) scores(i, 0);
+                    if (ok) scores(i, j);
                 }
-                if (ok) mma_commit(&k_empty[0], leader);
+                if (ok) mma_commit(&k_empty[j], leader);
             }
             uint64_t* v_ready = mask ? v_masked : v_full;
             for (int j = 0; j < blocks && ok; ++j) {
-                const int st = j % NS, st1 = (j + 1) % NS;
+                const int st = j % NS, ja = j + AHEAD;
                 ok = warp_wait(&v_ready[st], j / NS, limit);
                 for (int i = 0; i < T && ok; ++i) {
                     if (j >= n[i]) continue;
-                    ok = warp_wait(&p_full[i], j, limit);
+                    const int buf = buffer(i, j);
+                    ok = warp_wait(&p_full[buf], phase(j), limit);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    mma_weights<DP, BLK>(tmem + BLK * T + DP * i, tmem + BLK * i, v + st * step,
+                    mma_weights<DP, BLK>(tmem + 2 * BLK + DP * i, tmem + BLK * buf, v + st * step,
                                          j > 0, leader);
                     mma_commit(&o_full[i], leader);
-                    if (j + 1 < n[i]) {
-                        ok = warp_wait(&k_full[st1], (j + 1) / NS, limit);
-                        if (ok) scores(i, st1);
+                    if (ja < n[i]) {
+                        ok = warp_wait(&k_full[ja % NS], ja / NS, limit);
+                        if (ok) scores(i, ja);
                     }
                 }
                 if (ok) {
                     mma_commit(&v_empty[st], leader);
-                    if (j + 1 < blocks) mma_commit(&k_empty[st1], leader);
+                    if (ja < blocks) mma_commit(&k_empty[ja % NS], leader);
                 }
             }
             // No product may be in flight when the tensor memory is freed.
@@ -416,9 +410,8 @@ cudaError_t launch_fwd(const FattnTask& t, int slot, cudaStream_t stream) {
         !encode_heads_map(&mo, t.out, t, t.heads, t.query_len, t.o_stride, 32))
         return cudaErrorInvalidValue;
     constexpr int kRows = 128 * L::kTiles;
-    const int64_t grid =
-        static_cast<int64_t>((t.query_len + kRows - 1) / kRows) * t.batch * t.heads;
-    fattn_fwd_kernel<DP><<<static_cast<unsigned>(grid), L::kThreads, L::kBytes, stream>>>(
+    const dim3 grid(t.heads, t.batch, (t.query_len + kRows - 1) / kRows);
+    fattn_fwd_kernel<DP><<<grid, L::kThreads, L::kBytes, stream>>>(
         t, mq, mk, mv, mo);
     return cudaGetLastError();
 }

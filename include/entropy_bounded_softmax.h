@@ -497,12 +497,13 @@ cs_status cs_check_biencoder_args(const float* query,
  * contiguous and the element strides of the other three given.
  */
 typedef struct cs_attention_shape {
-    int32_t batch;      /* >= 0                                             */
-    int32_t heads;      /* query heads, a positive multiple of kv_heads     */
+    int32_t batch;      /* 0..65535                                         */
+    int32_t heads;      /* query heads, a positive multiple of kv_heads, at
+                           most 2^20                                        */
     int32_t kv_heads;   /* key and value heads; head h reads key head
                            h / (heads / kv_heads)                           */
-    int32_t query_len;  /* >= 0                                             */
-    int32_t key_len;    /* >= 0                                             */
+    int32_t query_len;  /* 0..8388480 (65535 tiles of 128)                  */
+    int32_t key_len;    /* the same                                         */
     int32_t d_head;     /* 8..128, a multiple of 8                          */
     int32_t causal;     /* 1: query i keeps keys j <= i + key_len - query_len
                            (the last query sees every key); 0: all keys     */
