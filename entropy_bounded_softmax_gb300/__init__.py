@@ -28,7 +28,7 @@ from ._lib import (CONSTANTS, cs_attention_softmax, cs_attention_softmax_ex,
                    cs_fused_attention, cs_fused_attention_backward,
                    cs_fused_attention_backward_workspace,
                    cs_check_paged_attention_args, cs_paged_attention,
-                   cs_paged_attention_chunk, cs_paged_attention_workspace,
+                   cs_paged_attention_workspace,
                    cs_paged_shape,
                    cs_check_biencoder_args, cs_plan_biencoder_host,
                    cs_check_args, cs_check_attention_args,
@@ -67,7 +67,7 @@ __all__ = [
     "cs_fused_attention_backward_workspace", "cs_check_fused_attention_args",
     "cs_check_fused_attention_backward_args",
     "paged_attention", "cs_paged_shape", "cs_paged_attention",
-    "cs_paged_attention_workspace", "cs_paged_attention_chunk",
+    "cs_paged_attention_workspace",
     "cs_check_paged_attention_args",
 ]
 

@@ -219,7 +219,6 @@ _SIGNATURES = {
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
                _VP, _VP, _I64, _VP]),
     "cs_paged_attention_workspace": (_I64, [_VP]),
-    "cs_paged_attention_chunk": (_I32, [_VP]),
     "cs_check_paged_attention_args": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
                _VP, _VP, _I64]),
@@ -492,10 +491,6 @@ def cs_paged_attention(query, key_pages, value_pages, page_table, lengths,
 
 def cs_paged_attention_workspace(shape) -> int:
     return load().cs_paged_attention_workspace(_shape_ref(shape))
-
-
-def cs_paged_attention_chunk(shape) -> int:
-    return load().cs_paged_attention_chunk(_shape_ref(shape))
 
 
 def cs_check_paged_attention_args(query, key_pages, value_pages, page_table,

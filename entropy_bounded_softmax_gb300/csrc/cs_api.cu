@@ -659,9 +659,8 @@ cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
 
 // ------------------------------------------------------------ paged attention
 constexpr int32_t kPagedMaxTokens = 1 << 30;
-// CTAs the chunks of full-length sequences should make: four for each of the
-// two resident on 152 SMs.
-constexpr int64_t kPagedTargetCtas = 4 * 2 * 152;
+constexpr int64_t kPagedStep = 64;      // tokens
+constexpr int64_t kPagedWholeSteps = 4;
 
 cs_status check_paged_shape(const cs_paged_shape* s) {
     if (!s) return CS_ERR_INVALID_ARG;
@@ -674,7 +673,7 @@ cs_status check_paged_shape(const cs_paged_shape* s) {
     if (s->fp16 != 0 && s->fp16 != 1) return CS_ERR_INVALID_ARG;
     if (!isfinite(s->scale) || !(s->scale > 0.0f)) return CS_ERR_INVALID_ARG;
     if (static_cast<int64_t>(s->max_pages) * s->page_size > kPagedMaxTokens ||
-        static_cast<int64_t>(s->batch) * s->heads > kMaxGridX)
+        s->batch > cs::kFattnMaxBatch || s->heads > cs::kFattnMaxHeads)
         return CS_ERR_DIM_MISMATCH;
     return CS_OK;
 }
@@ -683,20 +682,27 @@ int32_t paged_head_tiles(const cs_paged_shape& s) {
     return static_cast<int32_t>(ceil_div(s.heads / s.kv_heads, 16));
 }
 
-int32_t paged_chunk(const cs_paged_shape& s) {
-    const int64_t most = static_cast<int64_t>(s.max_pages) * s.page_size;
-    const int64_t work = static_cast<int64_t>(s.batch) * s.kv_heads *
-                         paged_head_tiles(s) * most;
-    int64_t c = ceil_div(ceil_div(work, kPagedTargetCtas), 64) * 64;
-    if (c < 128) c = 128;
-    if (c > 4096) c = 4096;
-    return static_cast<int32_t>(c);
+// The most steps a sequence can have, and the rows of one.
+int64_t paged_steps(const cs_paged_shape& s) {
+    return ceil_div(static_cast<int64_t>(s.max_pages) * s.page_size, kPagedStep);
+}
+int64_t paged_rows(const cs_paged_shape& s) {
+    return static_cast<int64_t>(s.kv_heads) * paged_head_tiles(s);
 }
 
-int64_t paged_chunks(const cs_paged_shape& s) {
-    const int64_t n = ceil_div(static_cast<int64_t>(s.max_pages) * s.page_size,
-                               paged_chunk(s));
-    return n > 0 ? n : 1;
+// Groups of CTAs that the steps are dealt to: as many as 152 SMs hold at once
+// (4, 2 or 1 CTAs each by the shared memory of their rings), because a CTA's
+// start and end cost it microseconds of streaming.  One sequence of 131072
+// tokens, 8 key heads, cut for 304 CTAs: 82 us, for 608: 88, for 1216: 96.
+// 0: no sequence is longer than kPagedWholeSteps, and every row of a sequence
+// is one CTA's.
+int64_t paged_groups(const cs_paged_shape& s) {
+    if (paged_steps(s) <= kPagedWholeSteps) return 0;
+    const int64_t ctas = 152 * (s.d_head <= 64 ? 4 : s.d_head <= 128 ? 2 : 1);
+    int64_t n = ctas / paged_rows(s);
+    if (n < 1) n = 1;
+    const int64_t total = paged_steps(s) * s.batch;
+    return n < total ? n : total;
 }
 
 // The bytes of a strided tensor with a contiguous last dimension of d, from
@@ -1357,18 +1363,11 @@ cs_status cs_fused_attention_backward(
     return CS_OK;
 }
 
-int32_t cs_paged_attention_chunk(const cs_paged_shape* shape) {
-    if (check_paged_shape(shape) != CS_OK) return -1;
-    return paged_chunk(*shape);
-}
-
 int64_t cs_paged_attention_workspace(const cs_paged_shape* shape) {
     if (check_paged_shape(shape) != CS_OK) return -1;
-    const int64_t chunks = paged_chunks(*shape);
-    if (chunks == 1) return 0;
-    // The (maximum, sum) pairs, then the outputs, 16-byte aligned.
-    const int64_t parts = static_cast<int64_t>(shape->batch) * shape->heads * chunks;
-    return ceil_div(parts, 2) * 16 + parts * shape->d_head * 4;
+    // Two parts a CTA, of 16 heads: the (maximum, sum) pairs, the outputs.
+    const int64_t heads = paged_groups(*shape) * paged_rows(*shape) * 2 * 16;
+    return heads * 8 + heads * shape->d_head * 4;
 }
 
 cs_status cs_check_paged_attention_args(
@@ -1381,8 +1380,9 @@ cs_status cs_check_paged_attention_args(
     if (st != CS_OK) return st;
     const cs_paged_shape& s = *shape;
     if (s.batch == 0) return CS_OK;
-    const int64_t grid = paged_chunks(s) * s.batch * s.kv_heads * paged_head_tiles(s);
-    if (grid > kMaxGridX) return CS_ERR_DIM_MISMATCH;
+    // Steps and CTAs are counted in 32 bits.
+    if (paged_steps(s) * s.batch > (1 << 30) || paged_rows(s) * s.batch > (1 << 30))
+        return CS_ERR_DIM_MISMATCH;
     const int64_t need = cs_paged_attention_workspace(shape);
     if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
     if (s.batch > 1 && s.table_stride < s.max_pages) return CS_ERR_INVALID_ARG;
@@ -1446,15 +1446,14 @@ cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
     t.num_pages = s.num_pages;
     t.max_pages = s.max_pages;
     t.head_tiles = paged_head_tiles(s);
-    t.chunk_tokens = paged_chunk(s);
-    t.chunks = static_cast<int32_t>(paged_chunks(s));
+    t.groups = static_cast<int32_t>(paged_groups(s));
+    t.split = t.groups > 0;
     t.fp16 = s.fp16;
     t.scale = s.scale;
-    if (t.chunks > 1) {
-        const int64_t parts = static_cast<int64_t>(s.batch) * s.heads * t.chunks;
+    if (t.split) {
         t.part_stats = static_cast<float2*>(workspace);
-        t.part_out = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                              ceil_div(parts, 2) * 16);
+        t.part_out = reinterpret_cast<float*>(t.part_stats +
+                                              paged_groups(s) * paged_rows(s) * 2 * 16);
     }
     if (cs::launch_paged(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();

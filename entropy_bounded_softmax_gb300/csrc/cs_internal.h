@@ -368,16 +368,16 @@ struct PagedTask {
     const int32_t* lengths;    // [batch]
     uint16_t* out;             // [batch, heads, d_head]
     float* lse;                // [batch, heads] or null
-    float2* part_stats;        // workspace: [batch, heads, chunks] (max, sum)
-    float* part_out;           // [batch, heads, chunks, d_head]
+    float2* part_stats;        // workspace: [groups, rows, 2, 16] (max, sum)
+    float* part_out;           // [groups, rows, 2, 16, d_head]
     unsigned int* err;         // device error word
     int64_t q_stride[2], o_stride[2], k_stride[3], v_stride[3];
     int64_t table_stride;
     int32_t batch, heads, kv_heads, d_head;
     int32_t page_size, num_pages, max_pages;
     int32_t head_tiles;        // tiles of 16 query heads to a key head
-    int32_t chunk_tokens;      // tokens of a chunk
-    int32_t chunks;            // chunks of the longest sequence
+    int32_t split;             // 1: the sequences' steps are dealt to groups of
+    int32_t groups;            // kv_heads * head_tiles CTAs, this many
     int32_t fp16;
     float scale;
 };

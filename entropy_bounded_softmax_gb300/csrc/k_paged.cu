@@ -4,18 +4,25 @@
 //   s_j = scale q . k_j,  out = sum e^(s_j - m) v_j / sum e^(s_j - m).
 //
 // Every key and value is read once and used for the query heads that share
-// its head: bound by the cache's bytes.  The tokens are cut into chunks of
-// fixed length; a CTA takes one chunk of one (sequence, key head), up to 16
-// query heads of it.  Its four warps walk the chunk's tiles of 16 tokens,
-// each with a ring of its own that asynchronous copies keep full (no barrier
-// between warps until the end), a running maximum and sum, and two products
-// on m16n8k16 tensor-core instructions with the query heads along M: scores
-// = Q K^T and out += P V.  The instruction's rate does not matter here (a
-// head group of 16 or less leaves tcgen05's 128 rows empty, and the bytes
-// take longer).  The warps' sums are joined in shared memory; a sequence of
-// one chunk is finished there, the others' parts (maximum, sum, unnormalised
-// output) go to the workspace and a second small kernel joins them.  Chunks
-// past a sequence's end return at once.
+// its head: bound by the cache's bytes.  A sequence's tokens are steps of 64.
+// The steps of the batch, one sequence after the other, are dealt to groups
+// of CTAs in equal shares, so that a batch of any lengths keeps every SM
+// streaming to the end.  A group has a CTA for every row, a key head's tile
+// of up to 16 query heads: its CTAs walk the same pages at the same time,
+// where the rows of all heads are neighbours (one sequence of 131072 tokens:
+// 83 us so, 87 with each CTA on a stretch of its own).  A CTA takes its
+// share's sequences one after the other.  Its four warps walk a part's tiles
+// of 16 tokens, each with a ring of its own that asynchronous copies keep
+// full (no barrier between warps until the part's end), a running maximum and
+// sum, and two products on m16n8k16 tensor-core instructions with the query
+// heads along M: scores = Q K^T and out += P V.  The instruction's rate does
+// not matter here (a group of 16 heads or less leaves tcgen05's 128 rows
+// empty, and the bytes take longer).  The warps' sums are joined in shared
+// memory; a sequence that lies in one share is finished there, the others'
+// parts (maximum, sum, unnormalised output) go to the workspace and a second
+// small kernel, launched to overlap the first's end, joins them.  Where no
+// sequence can be longer than four steps every CTA takes one whole row of one
+// sequence, and there is no second kernel.
 //
 // The weights enter the second product as two halves of the cache's type,
 // the nearest value and the nearest to the rest, so that their rounding
@@ -36,6 +43,7 @@ using namespace csd;
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgTile = 16;            // tokens
+constexpr int kPgStep = kPgTile * kPgWarps;
 constexpr int kPgStages = 3;
 constexpr float kWeightBits = 8.0f;    // log2 of the weights' common factor
 constexpr float kLagBits = 6.0f;       // how far the maximum may lag
@@ -46,6 +54,16 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+// The next kernel on the stream, launched to overlap this one, may start once
+// every CTA has called the first or ended; the second waits until the kernel
+// before has ended and its writes are visible.
+__device__ __forceinline__ void allow_next_kernel() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -101,13 +119,15 @@ struct PgSmem {
     static constexpr int kHalf = kPgTile * kRow;              // a tile's keys, or values
     static constexpr int kWarp = kPgStages * 2 * kHalf;
     static constexpr int kRing = kPgWarps * kWarp;
-    // The ring's space holds the warps' outputs at the end: 16 rows of DP + 4
-    // floats each.
-    static constexpr int kOutRow = DP + 4;
+    // At a part's end a warp's output, 16 rows of DP floats, takes exactly the
+    // space of its ring's last stage, while the next part's first tiles land
+    // in the others.
+    static constexpr int kOut = (kPgStages - 1) * 2 * kHalf;
     static constexpr int kStats = kRing;                      // [warps][16] float2
     static constexpr int kLive = kStats + kPgWarps * 16 * 8;  // [warps][stages] bits
-    static constexpr int kBytes = kLive + kPgWarps * kPgStages * 4;
-    static_assert(kPgWarps * 16 * kOutRow * 4 <= kRing, "outputs fit the ring");
+    static constexpr int kScan = kLive + kPgWarps * kPgStages * 4;   // [kPgWarps + 4]
+    static constexpr int kBytes = kScan + (kPgWarps + 4) * 4;
+    static_assert(16 * DP * 4 <= 2 * kHalf, "an output fits a stage");
 };
 
 // A sequence's length, and whether it is one the table can hold.
@@ -140,57 +160,166 @@ __device__ __forceinline__ void paged_finish(const PagedTask& t, int b, int h, i
     }
 }
 
+__device__ __forceinline__ int steps_of(int len) { return (len + kPgStep - 1) / kPgStep; }
+
+// The steps of the sequences before `upto`, by the whole CTA; scan: kPgWarps
+// shared ints.
+__device__ __forceinline__ int steps_before(const PagedTask& t, int upto, int* scan) {
+    int n = 0;
+    bool bad;
+    for (int b = threadIdx.x; b < upto; b += kPgThreads) n += steps_of(length_of(t, b, bad));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) scan[threadIdx.x >> 5] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) n += scan[w];
+    __syncthreads();
+    return n;
+}
+
+// Steps of a group's share.
+__device__ __forceinline__ int share_of(const PagedTask& t, int total) {
+    const int n = (total + t.groups - 1) / t.groups;
+    return n > 0 ? n : 1;
+}
+
+// The sum of n over the threads before this one and over all of the CTA; scan:
+// kPgWarps shared ints, free again after the caller's next __syncthreads.
+__device__ __forceinline__ void block_scan(int n, int* scan, int& before, int& all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int up = n;   // inclusive sum of the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += x;
+    }
+    if (lane == 31) scan[warp] = up;
+    __syncthreads();
+    before = up - n;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
+    }
+}
+
+// A group's steps g0 .. g1 - 1 of the batch's, the sequence that holds g0 and
+// its first step, by a whole CTA; false without steps.  scan: kPgWarps + 2
+// shared ints.
+__device__ __forceinline__ bool deal(const PagedTask& t, int grp, int* scan, int& g0, int& g1,
+                                     int& b, int& base) {
+    const bool once = t.batch <= kPgThreads;   // one walk over the lengths is enough
+    int total = once ? 0 : steps_before(t, t.batch, scan);
+    int done = 0;
+    for (int b0 = 0; b0 < t.batch; b0 += kPgThreads) {
+        const int i = b0 + threadIdx.x;
+        bool bad;
+        const int n = i < t.batch ? steps_of(length_of(t, i, bad)) : 0;
+        int first, all;
+        block_scan(n, scan, first, all);
+        if (once) total = all;
+        const int share = share_of(t, total);
+        g0 = grp * share;
+        g1 = min(total, g0 + share);
+        if (g0 >= g1) return false;
+        first += done;
+        if (first <= g0 && g0 < first + n) {
+            scan[kPgWarps] = i;
+            scan[kPgWarps + 1] = first;
+        }
+        done += all;
+        __syncthreads();
+        if (done > g0) break;
+    }
+    b = scan[kPgWarps];
+    base = scan[kPgWarps + 1];
+    return true;
+}
+
+// Tokens t0 .. t1 - 1 of sequence b: all of them, or part `place` of the
+// workspace.
+struct Part {
+    int b, t0, t1;
+    bool whole;
+    int place;
+};
+
+// CTAs an SM: what the rings' shared memory allows.
 template <int DP, class T>
-__global__ void __launch_bounds__(kPgThreads)
+__global__ void __launch_bounds__(kPgThreads, DP == 64 ? 4 : DP == 128 ? 2 : 1)
 paged_kernel(const PagedTask t) {
     using L = PgSmem<DP>;
     extern __shared__ __align__(128) unsigned char smem[];
+    allow_next_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Head tiles are the fastest index (they share the chunk's keys through
-    // L2), then key heads (their rows are neighbours in a page), then chunks.
-    int64_t x = blockIdx.x;
-    const int ht = static_cast<int>(x % t.head_tiles);
-    x /= t.head_tiles;
-    const int hk = static_cast<int>(x % t.kv_heads);
-    x /= t.kv_heads;
-    const int chunk = static_cast<int>(x % t.chunks);
-    const int b = static_cast<int>(x / t.chunks);
-    bool bad;
-    const int len = length_of(t, b, bad);
-    if (bad && chunk == 0 && threadIdx.x == 0) raise_error(t.err, kBitBadPage);
-    const int t0 = chunk * t.chunk_tokens;
-    if (t0 >= len && chunk > 0) return;
-    const int t1 = min(len, t0 + t.chunk_tokens);
+    const int cta = blockIdx.x;
+    const int rows = t.kv_heads * t.head_tiles;   // of a sequence
+    const int grp = cta / rows, row = cta - grp * rows;
+    const int hk = row / t.head_tiles, ht = row - hk * t.head_tiles;
     const int group = t.heads / t.kv_heads;
-    const int h0 = hk * group + 16 * ht;                 // first query head
-    const int nh = min(16, group - 16 * ht);             // query heads here
+    const int h0 = hk * group + 16 * ht;          // first query head
+    const int nh = min(16, group - 16 * ht);      // query heads here
+    bool bad;
+
+    // The walk over this CTA's parts: step g of g0 .. g1 - 1, in sequence b
+    // whose first step is base.
+    int g = 0, g0 = 0, g1 = 1, b = grp, base = 0;
+    bool any = true;
+    if (t.split) any = deal(t, grp, reinterpret_cast<int*>(smem + L::kScan), g0, g1, b, base);
+    int len = any ? length_of(t, b, bad) : 0, steps = steps_of(len);
+    g = g0;
+    auto next = [&](Part& p) {
+        if (!any || g >= g1) return false;
+        int s0 = 0, s1 = steps;
+        if (t.split) {
+            while (g >= base + steps) {   // (sequences without tokens too)
+                base += steps;
+                len = length_of(t, ++b, bad);
+                steps = steps_of(len);
+            }
+            s0 = g - base;
+            s1 = min(steps, s0 + g1 - g);
+        }
+        p.b = b;
+        p.t0 = s0 * kPgStep;
+        p.t1 = min(len, s1 * kPgStep);
+        p.whole = s0 == 0 && s1 == steps;
+        p.place = 2 * cta + (g > g0);
+        g += t.split ? s1 - s0 : 1;
+        return true;
+    };
 
     unsigned char* ring = smem + warp * L::kWarp;
     volatile uint32_t* live =
         reinterpret_cast<uint32_t*>(smem + L::kLive) + warp * kPgStages;
-    const int tiles = (t1 - t0 + kPgTile - 1) / kPgTile;
-    const int mine = tiles > warp ? (tiles - warp + kPgWarps - 1) / kPgWarps : 0;
-
+    // A part's tiles that are this warp's.
+    auto tiles_of = [&](const Part& p) {
+        const int tiles = (p.t1 - p.t0 + kPgTile - 1) / kPgTile;
+        return tiles > warp ? (tiles - warp + kPgWarps - 1) / kPgWarps : 0;
+    };
     // The page and slot of token (lane % 16) of this warp's tile i, -1 past
-    // the chunk, -2 for an entry that is no page; looked up one tile ahead.
-    auto locate = [&](int i, int& page, int& slot) {
-        const int tok = t0 + (warp + i * kPgWarps) * kPgTile + (lane & 15);
+    // the part, -2 for an entry that is no page; looked up one tile ahead.
+    int page, slot;
+    auto locate = [&](const Part& p, int i) {
+        const int tok = p.t0 + (warp + i * kPgWarps) * kPgTile + (lane & 15);
         page = -1;
         slot = 0;
-        if (i < mine && tok < t1) {
+        if (tok < p.t1) {
             const int e = tok / t.page_size;
             slot = tok - e * t.page_size;
-            page = t.page_table[b * t.table_stride + e];
+            page = t.page_table[p.b * t.table_stride + e];
             if (page < 0 || page >= t.num_pages) page = -2;
         }
     };
+    // Starts the copies of the tile that was looked up into stage st: kUnits
+    // 16-byte units a row, so 32 / kUnits rows at a time; zeros past d_head
+    // and for tokens that are not there.
+    constexpr int kUnits = DP / 8;
     const uint16_t* kbase = t.k_pages + hk * t.k_stride[2];
     const uint16_t* vbase = t.v_pages + hk * t.v_stride[2];
-    // Starts the copies of tile i into stage st: kUnits 16-byte units a row,
-    // so 32 / kUnits rows at a time; zeros past d_head and for tokens that
-    // are not there.
-    constexpr int kUnits = DP / 8;
-    auto issue = [&](int st, int page, int slot) {
+    auto issue = [&](int st) {
         unsigned char* dk = ring + st * 2 * L::kHalf;
         unsigned char* dv = dk + L::kHalf;
         const uint32_t here = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
@@ -212,214 +341,264 @@ paged_kernel(const PagedTask t) {
         }
     };
 
-    int page, slot;
-    locate(0, page, slot);
+    // A part's first tiles; then the next to look up is kPgStages - 1.
+    auto begin = [&](const Part& p) {
+        const int mine = tiles_of(p);
+        locate(p, 0);
 #pragma unroll
-    for (int i = 0; i < kPgStages - 1; ++i) {
-        if (i < mine) issue(i, page, slot);
-        cp_async_commit();
-        locate(i + 1, page, slot);
-    }
-
-    // Query fragments: rows lane / 4 and lane / 4 + 8, columns 2 (lane % 4)
-    // and 8 more of each 16.
-    const int g = lane >> 2, c2 = 2 * (lane & 3);
-    uint32_t q[DP / 16][4];
-#pragma unroll
-    for (int ks = 0; ks < DP / 16; ++ks)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = g + 8 * (i & 1), col = 16 * ks + c2 + 8 * (i >> 1);
-            q[ks][i] = 0u;
-            if (row < nh && col < t.d_head)
-                q[ks][i] = *reinterpret_cast<const uint32_t*>(
-                    t.q + b * t.q_stride[0] + (h0 + row) * t.q_stride[1] + col);
+        for (int i = 0; i < kPgStages - 1; ++i) {
+            if (i < mine) issue(i);
+            cp_async_commit();
+            locate(p, i + 1);
         }
+    };
+    // Unit n (8 floats) of row r of warp w's output, at the end of a part:
+    // units permuted within a row by its number, so that the rows' stores
+    // fall in different banks.
+    auto out_of = [&](int w, int r, int n) {
+        return reinterpret_cast<float4*>(smem + w * L::kWarp + L::kOut + r * DP * 4 +
+                                         ((n ^ (r & 7)) << 5));
+    };
+    float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
 
-    const float c = t.scale * kLog2e;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float o[DP / 8][4];
+    Part now, then;
+    bool more = next(now);
+    if (more) begin(now);
+    while (more) {
+        const int mine = tiles_of(now);
+        // Query fragments: rows lane / 4 and lane / 4 + 8, columns 2 (lane % 4)
+        // and 8 more of each 16.
+        const int gr = lane >> 2, c2 = 2 * (lane & 3);
+        uint32_t q[DP / 16][4];
 #pragma unroll
-    for (int n = 0; n < DP / 8; ++n)
+        for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-
-    const int mat = lane >> 3, r8 = lane & 7;
-    for (int i = 0; i < mine; ++i) {
-        const int st = i % kPgStages;
-        cp_async_wait_group<kPgStages - 2>();
-        __syncwarp();
-        // Stage (i - 1) % kPgStages was read before the __syncwarp.
-        if (i + kPgStages - 1 < mine) issue((i + kPgStages - 1) % kPgStages, page, slot);
-        cp_async_commit();
-        locate(i + kPgStages, page, slot);
-
-        const uint32_t sk = smem_addr(ring + st * 2 * L::kHalf), sv = sk + L::kHalf;
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
-            const int row = (mat >> 1) * 8 + r8;
-#pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) {
-                uint32_t k[4];
-                ldmatrix4(k, sk + row * L::kRow + (((2 * ks + (mat & 1)) ^ r8) << 4));
-                T::mma(s[0], q[ks], k[0], k[1]);
-                T::mma(s[1], q[ks], k[2], k[3]);
+            for (int i = 0; i < 4; ++i) {
+                const int row = gr + 8 * (i & 1), col = 16 * ks + c2 + 8 * (i >> 1);
+                q[ks][i] = 0u;
+                if (row < nh && col < t.d_head)
+                    q[ks][i] = *reinterpret_cast<const uint32_t*>(
+                        t.q + now.b * t.q_stride[0] + (h0 + row) * t.q_stride[1] + col);
             }
-        }
-        const uint32_t here = live[st];
+
+        const float c = t.scale * kLog2e;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float o[DP / 8][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < DP / 8; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int tok = 8 * n + c2 + (k & 1);
-                s[n][k] = (here >> tok) & 1u ? s[n][k] * c : -INFINITY;
-            }
-        float top[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]),
-                           fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            top[r] = fmaxf(top[r], m[r]);
-        }
-        // m = -inf and a finite top: an infinite difference, above the lag.
-        if (__any_sync(0xffffffffu, top[0] - m[0] > kLagBits || top[1] - m[1] > kLagBits)) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float f = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top[r]);
-                m[r] = top[r];
-                l[r] *= f;
-#pragma unroll
-                for (int n = 0; n < DP / 8; ++n) {
-                    o[n][2 * r] *= f;
-                    o[n][2 * r + 1] *= f;
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
+
+        const int mat = lane >> 3, r8 = lane & 7;
+        for (int i = 0; i < mine; ++i) {
+            const int st = i % kPgStages;
+            cp_async_wait_group<kPgStages - 2>();
+            __syncwarp();
+            // Stage (i - 1) % kPgStages was read before the __syncwarp.
+            if (i + kPgStages - 1 < mine) issue((i + kPgStages - 1) % kPgStages);
+            cp_async_commit();
+            locate(now, i + kPgStages);
+
+            const uint32_t sk = smem_addr(ring + st * 2 * L::kHalf), sv = sk + L::kHalf;
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            {
+                const int row = (mat >> 1) * 8 + r8;
+    #pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    uint32_t k[4];
+                    ldmatrix4(k, sk + row * L::kRow + (((2 * ks + (mat & 1)) ^ r8) << 4));
+                    T::mma(s[0], q[ks], k[0], k[1]);
+                    T::mma(s[1], q[ks], k[2], k[3]);
                 }
             }
-        }
-        float p[2][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float base = m[r] == -INFINITY ? 0.0f : m[r] - kWeightBits;
-#pragma unroll
+            const uint32_t here = live[st];
+    #pragma unroll
             for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    p[n][2 * r + k] = ex2(s[n][2 * r + k] - base);
-                    l[r] += p[n][2 * r + k];
+    #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tok = 8 * n + c2 + (k & 1);
+                    s[n][k] = (here >> tok) & 1u ? s[n][k] * c : -INFINITY;
                 }
-        }
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float a = p[k >> 1][2 * (k & 1)], z = p[k >> 1][2 * (k & 1) + 1];
-            hi[k] = T::pack(a, z);
-            const float2 w = T::unpack(hi[k]);
-            lo[k] = T::pack(a - w.x, z - w.y);
-        }
-        {
-            const int row = (mat & 1) * 8 + r8;
-#pragma unroll
-            for (int n2 = 0; n2 < DP / 16; ++n2) {
-                uint32_t v[4];
-                ldmatrix4_trans(v, sv + row * L::kRow + (((2 * n2 + (mat >> 1)) ^ r8) << 4));
-                T::mma(o[2 * n2], hi, v[0], v[1]);
-                T::mma(o[2 * n2], lo, v[0], v[1]);
-                T::mma(o[2 * n2 + 1], hi, v[2], v[3]);
-                T::mma(o[2 * n2 + 1], lo, v[2], v[3]);
+            float top[2];
+    #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]),
+                               fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                top[r] = fmaxf(top[r], m[r]);
+            }
+            // m = -inf and a finite top: an infinite difference, above the lag.
+            if (__any_sync(0xffffffffu, top[0] - m[0] > kLagBits || top[1] - m[1] > kLagBits)) {
+    #pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float f = m[r] == -INFINITY ? 0.0f : ex2(m[r] - top[r]);
+                    m[r] = top[r];
+                    l[r] *= f;
+    #pragma unroll
+                    for (int n = 0; n < DP / 8; ++n) {
+                        o[n][2 * r] *= f;
+                        o[n][2 * r + 1] *= f;
+                    }
+                }
+            }
+            float p[2][4];
+    #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float base = m[r] == -INFINITY ? 0.0f : m[r] - kWeightBits;
+    #pragma unroll
+                for (int n = 0; n < 2; ++n)
+    #pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        p[n][2 * r + k] = ex2(s[n][2 * r + k] - base);
+                        l[r] += p[n][2 * r + k];
+                    }
+            }
+            uint32_t hi[4], lo[4];
+    #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float a = p[k >> 1][2 * (k & 1)], z = p[k >> 1][2 * (k & 1) + 1];
+                hi[k] = T::pack(a, z);
+                const float2 w = T::unpack(hi[k]);
+                lo[k] = T::pack(a - w.x, z - w.y);
+            }
+            {
+                const int row = (mat & 1) * 8 + r8;
+    #pragma unroll
+                for (int n2 = 0; n2 < DP / 16; ++n2) {
+                    uint32_t v[4];
+                    ldmatrix4_trans(v, sv + row * L::kRow + (((2 * n2 + (mat >> 1)) ^ r8) << 4));
+                    T::mma(o[2 * n2], hi, v[0], v[1]);
+                    T::mma(o[2 * n2], lo, v[0], v[1]);
+                    T::mma(o[2 * n2 + 1], hi, v[2], v[3]);
+                    T::mma(o[2 * n2 + 1], lo, v[2], v[3]);
+                }
             }
         }
+
+        // The next part's first tiles come while this one's warps are joined.
+        __syncwarp();
+        more = next(then);
+        if (more) begin(then);
+
+        // Join the warps: rows gr and gr + 8 of each, the row's sum over its
+        // four lanes first.
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            const int row = gr + 8 * r;
+            if ((lane & 3) == 0) stats[warp * 16 + row] = make_float2(m[r], l[r]);
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n)
+                reinterpret_cast<float2*>(out_of(warp, row, n))[lane & 3] =
+                    make_float2(o[n][2 * r], o[n][2 * r + 1]);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < nh * (DP / 8); e += kPgThreads) {
+            const int row = e / (DP / 8), d = 8 * (e % (DP / 8));
+            float top = -INFINITY;
+    #pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) top = fmaxf(top, stats[w * 16 + row].x);
+            float sum = 0.0f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    #pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) {
+                const float2 st = stats[w * 16 + row];
+                const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
+                sum = fmaf(st.y, f, sum);
+                const float4* a = out_of(w, row, d >> 3);
+                const float4 a0 = a[0], a1 = a[1];
+                const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    #pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+            }
+            if (now.whole) {
+                paged_finish<T>(t, now.b, h0 + row, d, acc, top, sum);
+            } else {
+                const int64_t at = static_cast<int64_t>(now.place) * 16 + row;
+                if (d == 0) t.part_stats[at] = make_float2(top, sum);
+                if (d < t.d_head) {
+                    float4* w = reinterpret_cast<float4*>(t.part_out + at * t.d_head + d);
+                    w[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    w[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                }
+            }
+        }
+        __syncthreads();   // the next part's later tiles take the outputs' space
+        now = then;
     }
     cp_async_wait_all();
 
-    // Join the warps: rows g and g + 8 of each, the row's sum over its four
-    // lanes first.
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-    __syncthreads();   // every ring is read
-    float* outs = reinterpret_cast<float*>(smem);
-    float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = g + 8 * r;
-        if ((lane & 3) == 0) stats[warp * 16 + row] = make_float2(m[r], l[r]);
-#pragma unroll
-        for (int n = 0; n < DP / 8; ++n)
-            *reinterpret_cast<float2*>(outs + (warp * 16 + row) * L::kOutRow + 8 * n + c2) =
-                make_float2(o[n][2 * r], o[n][2 * r + 1]);
-    }
-    __syncthreads();
-    const bool whole = len <= t.chunk_tokens;
-    for (int e = threadIdx.x; e < nh * (DP / 8); e += kPgThreads) {
-        const int row = e / (DP / 8), d = 8 * (e % (DP / 8));
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kPgWarps; ++w) top = fmaxf(top, stats[w * 16 + row].x);
-        float sum = 0.0f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kPgWarps; ++w) {
-            const float2 st = stats[w * 16 + row];
-            const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
-            sum = fmaf(st.y, f, sum);
-            const float4* a = reinterpret_cast<const float4*>(
-                outs + (w * 16 + row) * L::kOutRow + d);
-            const float4 a0 = a[0], a1 = a[1];
-            const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], f, acc[k]);
-        }
-        const int64_t bh = static_cast<int64_t>(b) * t.heads + h0 + row;
-        if (whole) {
-            paged_finish<T>(t, b, h0 + row, d, acc, top, sum);
-        } else {
-            const int64_t part = bh * t.chunks + chunk;
-            if (d == 0) t.part_stats[part] = make_float2(top, sum);
-            if (d < t.d_head) {
-                float4* w = reinterpret_cast<float4*>(t.part_out + part * t.d_head + d);
-                w[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                w[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-            }
+    // Sequences without tokens have no steps: their rows are zeros, written
+    // by the CTAs in turn; so is what is wrong with a length reported.
+    for (int i = t.split ? cta : grp; i < t.batch; i += gridDim.x) {
+        const int n = length_of(t, i, bad);
+        if (bad && threadIdx.x == 0) raise_error(t.err, kBitBadPage);
+        if (n == 0 && t.split) {
+            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int e = threadIdx.x; e < t.heads * (DP / 8); e += kPgThreads)
+                paged_finish<T>(t, i, e / (DP / 8), 8 * (e % (DP / 8)), zero, 0.0f, 0.0f);
         }
     }
 }
 
-// Joins a head's chunks, one CTA a (sequence, head): every warp takes the
-// largest maximum and the sum over all chunks, then the CTA's threads, DP / 8
-// of them to a row, add the chunks' outputs.
+// Joins a sequence's parts, one CTA a (sequence, head): every warp takes the
+// largest maximum and the sum over all parts, then the CTA's threads, DP / 8
+// of them to a part, add the parts' outputs.  Launched while the parts are
+// still computed (it waits for them here), so that its start costs nothing.
 template <int DP, class T>
 __global__ void __launch_bounds__(kPgThreads)
 paged_join_kernel(const PagedTask t) {
     constexpr int kUnits = DP / 8, kRows = kPgThreads / kUnits;
     __shared__ float part[kRows][DP + 4];
-    const int b = static_cast<int>(blockIdx.x / t.heads);
-    const int h = static_cast<int>(blockIdx.x % t.heads);
+    __shared__ int scan[kPgWarps];
+    const int b = blockIdx.y, h = blockIdx.x;
     bool bad;
-    const int len = length_of(t, b, bad);
-    if (len <= t.chunk_tokens) return;   // finished by its only chunk
-    const int n = (len + t.chunk_tokens - 1) / t.chunk_tokens;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * t.chunks;
+    const int steps = steps_of(length_of(t, b, bad));
+    if (steps == 0) return;
+    const int share = share_of(t, steps_before(t, t.batch, scan));
+    const int begin = steps_before(t, b, scan);
+    const int c0 = begin / share, c1 = (begin + steps - 1) / share;
+    if (c0 == c1) return;   // finished by the only group that had it
+    const int group = t.heads / t.kv_heads;
+    const int hk = h / group, hh = h - hk * group;
+    const int rows = t.kv_heads * t.head_tiles, row = hk * t.head_tiles + hh / 16;
+    const int n = c1 - c0 + 1;
+    // Part i: group c0 + i's first, but group c0's last where it had others
+    // before.
+    const int late = begin > c0 * share ? 1 : 0;
+    auto place = [&](int i) {
+        return static_cast<int64_t>(2 * ((c0 + i) * rows + row) + (i == 0 ? late : 0)) * 16 +
+               hh % 16;
+    };
     const int lane = threadIdx.x & 31;
+    wait_for_previous_kernel();
     float top = -INFINITY, sum = 0.0f;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, t.part_stats[first + i].x);
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) {
+        const float2 st = t.part_stats[place(i)];
+        const float m = fmaxf(top, st.x);
+        // (Both maxima -inf: nothing to rescale.)
+        const float f = top == -INFINITY ? 0.0f : ex2(top - m);
+        const float g = st.x == -INFINITY ? 0.0f : ex2(st.x - m);
+        sum = fmaf(sum, f, st.y * g);
+        top = m;
+    }
+    const float mine = top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = lane; i < n; i += 32) {
-        const float2 st = t.part_stats[first + i];
-        sum = fmaf(st.y, st.x == -INFINITY ? 0.0f : ex2(st.x - top), sum);
-    }
+    sum = mine == -INFINITY ? sum : sum * ex2(mine - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int row = threadIdx.x / kUnits, d = 8 * (threadIdx.x % kUnits);
+    const int line = threadIdx.x / kUnits, d = 8 * (threadIdx.x % kUnits);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (d < t.d_head) {
-        for (int i = row; i < n; i += kRows) {
-            const float x = t.part_stats[first + i].x;
+#pragma unroll 4
+        for (int i = line; i < n; i += kRows) {
+            const float x = t.part_stats[place(i)].x;
             const float f = x == -INFINITY ? 0.0f : ex2(x - top);
             const float4* a = reinterpret_cast<const float4*>(
-                t.part_out + (first + i) * t.d_head + d);
+                t.part_out + place(i) * t.d_head + d);
             const float4 a0 = a[0], a1 = a[1];
             const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
@@ -427,7 +606,7 @@ paged_join_kernel(const PagedTask t) {
         }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) part[row][d + k] = acc[k];
+    for (int k = 0; k < 8; ++k) part[line][d + k] = acc[k];
     __syncthreads();
     if (threadIdx.x >= kUnits) return;
 #pragma unroll
@@ -444,14 +623,20 @@ cudaError_t launch(const PagedTask& t, int slot, cudaStream_t stream) {
     const void* kern = reinterpret_cast<const void*>(paged_kernel<DP, T>);
     cudaError_t e = ensure_smem_attribute(kern, slot, PgSmem<DP>::kBytes, false);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(t.batch) * t.chunks * t.kv_heads * t.head_tiles;
-    paged_kernel<DP, T><<<static_cast<unsigned>(grid), kPgThreads, PgSmem<DP>::kBytes,
-                          stream>>>(t);
+    const int grid = (t.split ? t.groups : t.batch) * t.kv_heads * t.head_tiles;
+    paged_kernel<DP, T><<<grid, kPgThreads, PgSmem<DP>::kBytes, stream>>>(t);
     e = cudaGetLastError();
-    if (e != cudaSuccess || t.chunks == 1) return e;
-    paged_join_kernel<DP, T><<<static_cast<unsigned>(t.batch * t.heads), kPgThreads, 0,
-                               stream>>>(t);
-    return cudaGetLastError();
+    if (e != cudaSuccess || !t.split) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(t.heads, t.batch);
+    cfg.blockDim = dim3(kPgThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<DP, T>, t);
 }
 
 template <class T>

@@ -613,7 +613,7 @@ typedef struct cs_paged_shape {
     int32_t page_size;  /* tokens of a page, >= 1                           */
     int32_t num_pages;  /* pages of the cache, >= 0                         */
     int32_t max_pages;  /* entries of a page-table row, >= 0; at most 2^30
-                           tokens a row                                     */
+                           tokens a row, 2^36 over the batch               */
     int32_t fp16;       /* 0: query, pages and out are bf16; 1: fp16        */
     float scale;        /* of the scores; positive and finite               */
     int64_t q_stride[2];   /* batch, head; elements, non-negative           */
@@ -646,8 +646,8 @@ typedef struct cs_paged_shape {
  * A length that is negative or past the table's row is taken as 0 or the
  * row's tokens, and a token whose page number is outside 0..num_pages-1 is
  * left out; both OR CS_ERR_BAD_PAGE into the error word.  Sums are fp32 in a
- * fixed order (repeated calls give the same bits, whatever else runs).  NaN
- * or infinite scores propagate by IEEE arithmetic and OR CS_ERR_NAN_INPUT
+ * fixed order, which depends on the batch's lengths (repeated calls give the
+ * same bits, whatever else runs).  NaN or infinite scores propagate by IEEE arithmetic and OR CS_ERR_NAN_INPUT
  * into the error word.  Ownership, execution and errors: as
  * cs_constrained_softmax.
  */
@@ -659,13 +659,9 @@ cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
                              void* workspace, int64_t workspace_bytes,
                              void* stream);
 
-/* Bytes of workspace the call needs (0 when no row of the table is longer
- * than a chunk); negative for a malformed shape.  Host-only. */
+/* Bytes of workspace the call needs (0 when no row of the table holds more
+ * than 256 tokens); negative for a malformed shape.  Host-only. */
 int64_t cs_paged_attention_workspace(const cs_paged_shape* shape);
-
-/* Tokens of the chunks a sequence is cut into; negative for a malformed
- * shape.  Host-only. */
-int32_t cs_paged_attention_chunk(const cs_paged_shape* shape);
 
 /* Host-only argument check (no CUDA call). */
 cs_status cs_check_paged_attention_args(

@@ -114,11 +114,20 @@ def test_against_definition(case, dtype):
     check(cache(*case, dtype=dtype))
 
 
-def test_chunks_are_joined():
-    """Many chunks of one sequence: the plan cuts, and the parts join."""
-    args = cache([4111, 300, 128], 8, 2, 64, 16)
-    shape = cs.cs_paged_shape(3, 8, 2, 64, 16, args[1].shape[0],
+def test_rows_are_split_and_joined():
+    """More CTAs than rows: the rows' steps are dealt out, and the parts
+    join; a batch of short sequences needs no workspace."""
+    args = cache([4111, 300, 0, 128], 8, 2, 64, 16)
+    shape = cs.cs_paged_shape(4, 8, 2, 64, 16, args[1].shape[0],
                               args[3].shape[1], 0, 1.0)
-    assert cs.cs_paged_attention_chunk(shape) < 300
     assert cs.cs_paged_attention_workspace(shape) > 0
     check(args)
+    shape.max_pages = 16
+    assert cs.cs_paged_attention_workspace(shape) == 0
+
+
+def test_many_sequences():
+    """More sequences than a CTA has threads, some without tokens: the walk
+    over the lengths takes several rounds."""
+    lengths = [(37 * b) % 400 for b in range(300)]
+    check(cache(lengths, 2, 1, 64, 16))
