@@ -86,6 +86,7 @@ ERROR_BITS = {name: 1 << CONSTANTS[f"CS_ERR_{name}"]
 
 
 _STAY = contextlib.nullcontext()
+_INF = float("inf")
 
 
 class CsError(RuntimeError):
@@ -335,11 +336,20 @@ def biencoder_attention(query, keys, values, scale=None,
     return res if len(res) > 1 else out
 
 
-def _heads(name, x, shape, device):
+def _heads(name, x, shape, device, torch):
     """The strides and the address of a [batch, heads, length, d_head] bf16
     tensor, checked: on the CUDA device of that index, of the given shape, in
     strides that the tensor copies take."""
-    import torch
+    if isinstance(x, torch.Tensor):
+        st = x.stride()
+        ptr = x.data_ptr()
+        if (x.dtype is torch.bfloat16 and x.get_device() == device
+                and x.shape == shape):
+            s0, s1, s2, s3 = st
+            if (s3 == 1 and s0 > 0 and s1 > 0 and s2 > 0
+                    and not (ptr | 2 * (s0 | s1 | s2)) & 15):
+                return st, ptr
+    # The refusals, and the shapes whose strides do not all matter.
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dtype is not torch.bfloat16:
@@ -348,13 +358,8 @@ def _heads(name, x, shape, device):
         raise ValueError(f"{name} must be on the query's device")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    st = x.stride()
-    ptr = x.data_ptr()
-    s0, s1, s2, s3 = st
-    if (s3 != 1 or (ptr | 2 * (s0 | s1 | s2)) & 15
-            or s0 <= 0 or s1 <= 0 or s2 <= 0) and x.numel():
-        # Strides of dimensions of one element do not matter.
-        if s3 != 1:
+    if x.numel():
+        if st[3] != 1:
             raise ValueError(f"{name}'s head dimension must be contiguous")
         if ptr & 15 or any(n > 1 and (s <= 0 or s % 8)
                            for n, s in zip(shape[:3], st)):
@@ -364,12 +369,10 @@ def _heads(name, x, shape, device):
     return st, ptr
 
 
-def _attention_inputs(query, keys, values, mask, scale):
+def _attention_inputs(query, keys, values, mask, scale, torch):
     """The checked inputs of fused attention: the query's device index, the
     two shapes, the scale, and (strides, address) of query, keys, values and
     the mask's row stride and address."""
-    import math
-    import torch
     for name, x in (("query", query), ("keys", keys)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -387,12 +390,12 @@ def _attention_inputs(query, keys, values, mask, scale):
         raise ValueError("the query's heads must be a multiple of the keys'")
     if D < 8 or D > 128 or D % 8:
         raise ValueError("d_head must be a multiple of 8 in 8..128")
-    q = _heads("query", query, qs, dev)
-    k = _heads("keys", keys, ks, dev)
-    v = _heads("values", values, ks, dev)
+    q = _heads("query", query, qs, dev, torch)
+    k = _heads("keys", keys, ks, dev, torch)
+    v = _heads("values", values, ks, dev, torch)
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    elif not (scale > 0.0 and math.isfinite(scale)):
+        scale = D ** -0.5
+    elif not 0.0 < scale < _INF:
         raise ValueError("scale must be positive and finite")
     m = (Sk, None)
     if mask is not None:
@@ -429,18 +432,20 @@ def fused_attention(query, keys, values, mask=None, causal: bool = False,
     """
     import torch
     dev, qs, ks, scale, q, k, v, m = _attention_inputs(query, keys, values,
-                                                       mask, scale)
+                                                       mask, scale, torch)
     B, H, Sq, D = qs
     if out is None:
         out = torch.empty_like(query)
-    o = _heads("out", out, qs, dev)
+        o = out.stride(), out.data_ptr()
+    else:
+        o = _heads("out", out, qs, dev, torch)
     lse = None
     if return_lse:
         lse = torch.empty((B, H, Sq), dtype=torch.float32,
                           device=query.device)
     shape = _lib.pack_attention_shape(
         B, H, ks[1], Sq, ks[2], D, 1 if causal else 0, scale, q[0], k[0],
-        v[0], o[0], mask_stride=m[0])
+        v[0], o[0], m[0])
     with _on_device(query.device):
         st = cs_fused_attention(q[1], k[1], v[1], o[1],
                                 lse.data_ptr() if return_lse else None, m[1],
@@ -461,39 +466,36 @@ def fused_attention_backward(query, keys, values, out, lse, grad_output,
     """
     import torch
     dev, qs, ks, scale, q, k, v, m = _attention_inputs(query, keys, values,
-                                                       mask, scale)
+                                                       mask, scale, torch)
     B, H, Sq, D = qs
-    o = _heads("out", out, qs, dev)
-    go = _heads("grad_output", grad_output, qs, dev)
-    if (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32
+    o = _heads("out", out, qs, dev, torch)
+    go = _heads("grad_output", grad_output, qs, dev, torch)
+    if (not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32
             or lse.shape != qs[:3] or lse.get_device() != dev
             or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [batch, heads, "
                          "query_len] tensor on the query's device")
-    grads = (torch.empty_like(query), torch.empty_like(keys),
-             torch.empty_like(values))
-    dq, dk, dv = (_heads("gradient", g, s, dev)
-                  for g, s in zip(grads, (qs, ks, ks)))
-    shape = _lib.pack_attention_shape(
+    dq, dk, dv = (torch.empty_like(query), torch.empty_like(keys),
+                  torch.empty_like(values))
+    shape = _lib.pack_attention_backward_shape(
         B, H, ks[1], Sq, ks[2], D, 1 if causal else 0, scale, q[0], k[0],
-        v[0], o[0], go[0], dq[0], dk[0], dv[0], m[0])
+        v[0], o[0], go[0], dq.stride(), dk.stride(), dv.stride(), m[0])
     size = cs_fused_attention_backward_workspace(shape)
     work = torch.empty(max(size, 0), dtype=torch.uint8, device=query.device)
     with _on_device(query.device):
         st = cs_fused_attention_backward(
-            q[1], k[1], v[1], o[1], lse.data_ptr(), go[1], dq[1], dk[1],
-            dv[1], m[1], shape, work.data_ptr(), size,
+            q[1], k[1], v[1], o[1], lse.data_ptr(), go[1], dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), m[1], shape, work.data_ptr(), size,
             _stream_handle(query.device))
     if st != 0:
         raise CsError(st, "cs_fused_attention_backward")
-    return grads
+    return dq, dk, dv
 
 
-def _rows(name, x, shape, dtype, device):
+def _rows(name, x, shape, dtype, device, torch):
     """The strides and the address of a strided tensor with a contiguous last
     dimension, checked: on the CUDA device of that index, of the given shape
     and type, 16-byte aligned rows."""
-    import torch
     if (not isinstance(x, torch.Tensor) or not x.is_cuda
             or x.get_device() != device):
         raise ValueError(f"{name} must be a CUDA tensor on one device with "
@@ -504,18 +506,18 @@ def _rows(name, x, shape, dtype, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     st = x.stride()
     ptr = x.data_ptr()
-    if x.numel() and (st[-1] != 1 or ptr & 15 or any(
-            n > 1 and s & 7 for n, s in zip(shape[:-1], st))):
+    if (st[-1] != 1 or ptr & 15 or sum(s & 7 for s in st[:-1])) and (
+            x.numel() and (st[-1] != 1 or ptr & 15 or any(
+                n > 1 and s & 7 for n, s in zip(shape[:-1], st)))):
         raise ValueError(f"{name}'s last dimension must be contiguous, its "
                          "base 16-byte aligned and its other strides "
                          "multiples of 8 elements")
     return st, ptr
 
 
-def _index_rows(name, x, dim, rows, device):
+def _index_rows(name, x, dim, rows, device, torch):
     """The strides and the address of an int32 tensor of page numbers or
     lengths, checked."""
-    import torch
     if (not isinstance(x, torch.Tensor) or x.dtype is not torch.int32
             or x.get_device() != device or x.dim() != dim
             or x.shape[0] != rows):
@@ -545,7 +547,6 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
     range are left out and reported by :func:`get_error`, and so are NaN or
     infinite scores, which propagate.
     """
-    import math
     import torch
     for name, x, dim in (("query", query, 3), ("key_pages", key_pages, 4)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -568,21 +569,23 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
                          "pages', and page_size positive")
     if D < 8 or D > 256 or D % 8:
         raise ValueError("d_head must be a multiple of 8 in 8..256")
-    q = _rows("query", query, qs, dtype, dev)
-    k = _rows("key_pages", key_pages, ps, dtype, dev)
-    v = _rows("value_pages", value_pages, ps, dtype, dev)
-    table = _index_rows("page_table", page_table, 2, B, dev)
-    count = _index_rows("lengths", lengths, 1, B, dev)
+    q = _rows("query", query, qs, dtype, dev, torch)
+    k = _rows("key_pages", key_pages, ps, dtype, dev, torch)
+    v = _rows("value_pages", value_pages, ps, dtype, dev, torch)
+    table = _index_rows("page_table", page_table, 2, B, dev, torch)
+    count = _index_rows("lengths", lengths, 1, B, dev, torch)
     most = page_table.shape[1]
     if B > 1 and table[0][0] < most:
         raise ValueError("page_table's rows must not overlap")
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    elif not (scale > 0.0 and math.isfinite(scale)):
+        scale = D ** -0.5
+    elif not 0.0 < scale < _INF:
         raise ValueError("scale must be positive and finite")
     if out is None:
         out = torch.empty((B, H, D), dtype=dtype, device=query.device)
-    o = _rows("out", out, qs, dtype, dev)
+        o = out.stride(), out.data_ptr()
+    else:
+        o = _rows("out", out, qs, dtype, dev, torch)
     lse = None
     if return_lse:
         lse = torch.empty((B, H), dtype=torch.float32, device=query.device)

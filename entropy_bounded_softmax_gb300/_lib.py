@@ -94,18 +94,27 @@ class cs_paged_shape(ctypes.Structure):
     ]
 
 
-_PACK_ATTENTION = struct.Struct("=7if25q")
+_PACK_ATTENTION = struct.Struct("=7if12q96xq")     # without gradients
+_PACK_ATTENTION_BACKWARD = struct.Struct("=7if25q")
 _PACK_PAGED = struct.Struct("=8ifxxxx11q")
-_NONE3 = (0, 0, 0)
 
 
 def pack_attention_shape(batch, heads, kv_heads, query_len, key_len, d_head,
-                         causal, scale, q, k, v, o, go=_NONE3, dq=_NONE3,
-                         dk=_NONE3, dv=_NONE3, mask_stride=0) -> bytes:
+                         causal, scale, q, k, v, o, mask_stride=0) -> bytes:
     """The bytes of a cs_attention_shape, which every function that takes one
-    also takes; q .. dv: element strides, the first three of each are used.
+    also takes; q .. o: element strides, the first three of each are used.
     (Filling the ctypes struct costs more than the launch.)"""
     return _PACK_ATTENTION.pack(
+        batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
+        q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
+        o[0], o[1], o[2], mask_stride)
+
+
+def pack_attention_backward_shape(batch, heads, kv_heads, query_len, key_len,
+                                  d_head, causal, scale, q, k, v, o, go, dq,
+                                  dk, dv, mask_stride=0) -> bytes:
+    """The same with the strides of the gradients."""
+    return _PACK_ATTENTION_BACKWARD.pack(
         batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
         q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
         o[0], o[1], o[2], go[0], go[1], go[2], dq[0], dq[1], dq[2],

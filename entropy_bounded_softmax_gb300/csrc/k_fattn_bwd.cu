@@ -74,7 +74,7 @@ struct BwdPlan {
     static constexpr int kRows = kB2 + kStages2 * kBlock;  // [kStagesR][2][128] lse, delta
     static constexpr int kBars = kRows + kStagesR * 2 * 128 * 4;
     static constexpr int kNumBars =
-        1 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 6 + 2;
+        1 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 7 + 2;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages1][4]
     static constexpr int kFlags = kWords + kStages1 * 16;
     static constexpr int kBytes = kFlags + 16;
@@ -128,7 +128,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     uint64_t* r_empty = drained + 1;           // [NR] from eight warps, as those below
     uint64_t* s_read = r_empty + NR;           // queries: the scores are in registers
     uint64_t* p_full = s_read + 1;             // keys: the block's P
-    uint64_t* d_full = p_full + 1;             // its dS
+    uint64_t* d_full = p_full + 1;             // [2] its dS, by buffer
     float* rows_s = reinterpret_cast<float*>(smem + L::kRows);
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
@@ -244,8 +244,10 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     const uint32_t acc1 = tmem;                // dq, or dv
     const uint32_t acc2 = tmem + DP;           // keys: dk
     const uint32_t t_s = tmem + (KV ? 2 : 1) * DP;
-    // G V^T of block i: keys: one buffer; queries: two, because a block's may
-    // complete before every warp has waited for the one before.
+    // G V^T of block i, and the dS over it: keys: one buffer; queries: two with
+    // barriers of their own, because there a block's G V^T may complete, and a
+    // fast warp's dS be written, before every warp is done with the block
+    // before.
     auto g_buf = [&](int i) { return KV ? 0 : i & 1; };
     auto g_phase = [&](int i) { return KV ? i : i >> 1; };
     auto t_g = [&](int i) { return t_s + BLK * (KV ? 1 : 1 + (i & 1)); };
@@ -411,7 +413,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(d_full);
+                mbar_arrive(&d_full[g_buf(i)]);
                 if (KV) mbar_arrive(&r_empty[st]);
             }
         }
@@ -492,7 +494,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 tc_fence_after_sync();
                 ok = scores(i + 1) && grads(i + 1);
             }
-            if (ok) ok = warp_wait(d_full, i, limit);
+            if (ok) ok = warp_wait(&d_full[g_buf(i)], g_phase(i), limit);
             if (!ok) break;
             tc_fence_after_sync();
             sums(KV ? acc2 : acc1, t_g(i), b1_w + (i % N1) * step, i > 0);
@@ -548,36 +550,50 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
-template <int DP, bool KV>
-cudaError_t launch_bwd(const FattnTask& t, int slot, cudaStream_t stream) {
-    const void* kern = reinterpret_cast<const void*>(fattn_bwd_kernel<DP, KV>);
-    constexpr int smem = BwdPlan<DP>::kBytes;
-    static_assert(smem <= 232448, "the shared memory of a CTA");
-    cudaError_t e = ensure_smem_attribute(kern, slot, smem, false);
-    if (e != cudaSuccess) return e;
-    constexpr int kBlk = BwdPlan<DP>::kBlk;
-    constexpr int RQ = KV ? kBlk : 128, RK = KV ? 128 : kBlk;
-    CUtensorMap mq, mg, mk, mv, md1, md2;
-    if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, RQ) ||
-        !encode_heads_map(&mg, t.go, t, t.heads, t.query_len, t.go_stride, RQ) ||
-        !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, RK) ||
-        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, RK) ||
-        !(KV ? encode_heads_map(&md1, t.dv, t, t.kv_heads, t.key_len, t.dv_stride, 32) &&
-                   encode_heads_map(&md2, t.dk, t, t.kv_heads, t.key_len, t.dk_stride, 32)
-             : encode_heads_map(&md1, t.dq, t, t.heads, t.query_len, t.dq_stride, 32)))
-        return cudaErrorInvalidValue;
-    const int length = KV ? t.key_len : t.query_len;
-    if (length == 0) return cudaSuccess;
-    const dim3 grid(KV ? t.kv_heads : t.heads, t.batch, (length + 127) / 128);
-    fattn_bwd_kernel<DP, KV><<<grid, kBwdThreads, smem, stream>>>(
-        t, KV ? mk : mq, KV ? mv : mg, KV ? mq : mk, KV ? mg : mv, md1, KV ? md2 : md1);
-    return cudaGetLastError();
-}
+// The maps of the four inputs for one box height.
+struct InputMaps {
+    CUtensorMap q, g, k, v;
+    bool encode(const FattnTask& t, int rows) {
+        return encode_heads_map(&q, t.q, t, t.heads, t.query_len, t.q_stride, rows) &&
+               encode_heads_map(&g, t.go, t, t.heads, t.query_len, t.go_stride, rows) &&
+               encode_heads_map(&k, t.k, t, t.kv_heads, t.key_len, t.k_stride, rows) &&
+               encode_heads_map(&v, t.v, t, t.kv_heads, t.key_len, t.v_stride, rows);
+    }
+};
 
 template <int DP>
 cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
-    const cudaError_t e = launch_bwd<DP, false>(t, slot, stream);
-    return e == cudaSuccess ? launch_bwd<DP, true>(t, slot + 1, stream) : e;
+    using L = BwdPlan<DP>;
+    constexpr int smem = L::kBytes;
+    static_assert(smem <= 232448, "the shared memory of a CTA");
+    cudaError_t e = ensure_smem_attribute(
+        reinterpret_cast<const void*>(fattn_bwd_kernel<DP, false>), slot, smem, false);
+    if (e == cudaSuccess)
+        e = ensure_smem_attribute(reinterpret_cast<const void*>(fattn_bwd_kernel<DP, true>),
+                                  slot + 1, smem, false);
+    if (e != cudaSuccess) return e;
+    // Fixed tiles of 128 rows, streamed blocks of kBlk.
+    InputMaps fixed, streamed;
+    CUtensorMap dq, dk, dv;
+    if (!fixed.encode(t, 128) || (L::kBlk != 128 && !streamed.encode(t, L::kBlk)) ||
+        !encode_heads_map(&dq, t.dq, t, t.heads, t.query_len, t.dq_stride, 32) ||
+        !encode_heads_map(&dk, t.dk, t, t.kv_heads, t.key_len, t.dk_stride, 32) ||
+        !encode_heads_map(&dv, t.dv, t, t.kv_heads, t.key_len, t.dv_stride, 32))
+        return cudaErrorInvalidValue;
+    const InputMaps& blocks = L::kBlk == 128 ? fixed : streamed;
+    if (t.query_len > 0) {
+        const dim3 grid(t.heads, t.batch, (t.query_len + 127) / 128);
+        fattn_bwd_kernel<DP, false><<<grid, kBwdThreads, smem, stream>>>(
+            t, fixed.q, fixed.g, blocks.k, blocks.v, dq, dq);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && t.key_len > 0) {
+        const dim3 grid(t.kv_heads, t.batch, (t.key_len + 127) / 128);
+        fattn_bwd_kernel<DP, true><<<grid, kBwdThreads, smem, stream>>>(
+            t, fixed.k, fixed.v, blocks.q, blocks.g, dv, dk);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 }  // namespace

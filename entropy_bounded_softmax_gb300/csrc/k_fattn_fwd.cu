@@ -69,7 +69,7 @@ struct FwdPlan {
     static constexpr int kK = kQ + kTiles * kTile;
     static constexpr int kV = kK + kStages * kBlock;
     static constexpr int kBars = kV + kStages * kBlock;
-    static constexpr int kNumBars = 5 * kStages + 2 * kTiles + 4 + 1;
+    static constexpr int kNumBars = 5 * kStages + 3 * kTiles + 4 + 1;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages][4]
     static constexpr int kFlags = kWords + kStages * 16;  // abort, tmem
     static constexpr int kBytes = kFlags + 16 + 1024;     // and alignment slack
@@ -102,7 +102,8 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     uint64_t* q_full = v_masked + NS;         // [T] tile's queries landed
     uint64_t* s_full = q_full + T;            // [2] a buffer's scores
     uint64_t* o_full = s_full + 2;            // [T] the block's P V completed
-    uint64_t* drained = o_full + T;
+    uint64_t* o_done = o_full + T;            // [T] the tile's last P V completed
+    uint64_t* drained = o_done + T;
     uint64_t* p_full = drained + 1;           // [2] a buffer's weights, from four warps
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
@@ -239,6 +240,8 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 const float f = m == -INFINITY ? 0.0f : ex2((m - top) * c);
                 m = top;
                 l *= f;
+                // The product of block j - 2 has completed (block j's scores
+                // were issued after it), that of block j has not begun.
                 ok = warp_wait(&o_full[tile], j - 1, limit);
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -275,10 +278,9 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         }
         // The tile's queries are read (or, without blocks, have landed) before
         // the output is staged over them.
-        // (A barrier tells a phase from the one before only: with two buffers
-        // the last two products may both be under way.)
-        if (ok && nt > 1) ok = warp_wait(&o_full[tile], nt - 2, limit);
-        if (ok && nt > 0) ok = warp_wait(&o_full[tile], nt - 1, limit);
+        // (Not by o_full: a barrier tells a phase from the one before it only,
+        // and none, one or both of the last two products may have completed.)
+        if (ok && nt > 0) ok = warp_wait(&o_done[tile], 0, limit);
         if (ok && nt == 0 && row0 < t.query_len) ok = warp_wait(&q_full[tile], 0, limit);
         if (ok && row0 < t.query_len) {
             tc_fence_after_sync();
@@ -342,6 +344,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                     mma_weights<DP, BLK>(tmem + 2 * BLK + DP * i, tmem + BLK * buf, v + st * step,
                                          j > 0, leader);
                     mma_commit(&o_full[i], leader);
+                    if (j + 1 == n[i]) mma_commit(&o_done[i], leader);
                     if (ja < n[i]) {
                         ok = warp_wait(&k_full[ja % NS], ja / NS, limit);
                         if (ok) scores(i, ja);

@@ -100,3 +100,31 @@ def test_sequence_major_storage(case):
     assert torch.equal(out, same[0])
     for a, b in zip(grads, same[2]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("case", [
+    (1, 4, 2, 300, 700, 64, True, "holes"),
+    (1, 4, 2, 300, 700, 128, True, "holes"),
+    (3, 8, 4, 700, 700, 64, True, None),
+    (3, 8, 4, 700, 700, 128, True, None),
+], ids=str)
+def test_repeated_calls_agree(case):
+    """Hundreds of launches beside another stream's work: the same bits, and
+    no wait that gives up (the warps' order differs from launch to launch)."""
+    q, k, v, g, mask, causal = inputs(case, 5)
+    out, lse, grads = check(q, k, v, g, mask, causal)
+    noise = torch.randn(2048, 2048, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(150):
+        if i % 3 == 0:
+            with torch.cuda.stream(side):
+                noise = noise @ noise * 1e-3
+        o, l = cs.fused_attention(q, k, v, mask, causal, return_lse=True)
+        d = cs.fused_attention_backward(q, k, v, o, l, g, mask, causal)
+        for a, b in zip((o, l, *d), (out, lse, *grads)):
+            differ += (a.view(torch.int16) != b.view(torch.int16)).sum()
+    torch.cuda.synchronize()
+    assert int(differ) == 0
+    assert cs.get_error() == set()
