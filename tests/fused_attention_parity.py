@@ -10,7 +10,9 @@ a dot product of D terms errs by at most (D + 8) 2^-23 of the sum of its
 terms' magnitudes (accumulation in any order, one bit spare for a truncating
 accumulator), 2^x by 2^-21, and the running sums are bounded below by
 2^-18 of the sum of magnitudes (n <= 4096 terms of half a step, mostly
-cancelling; 64 n would be needed to exceed it)."""
+cancelling; 64 n would be needed to exceed it).  Numbers below 2^-126 are
+flushed to zero, by 2^x and as operands: a P or dS errs by up to 2^-126
+whatever its size, which shows only where nothing larger is summed."""
 import math
 
 import torch
@@ -18,6 +20,7 @@ import torch
 HALF = 2.0 ** -8     # half a step of bf16
 F32 = 2.0 ** -23
 SUMS = 2.0 ** -18
+FLUSH = 2.0 ** -126
 
 
 def kept_pairs(mask, causal, B, Sq, Sk):
@@ -82,7 +85,9 @@ def gradients(f, out, g):
     # fp32 errors of dS: P's relative one, and those of the two dot products.
     dot = (f.D + 8) * F32 * (g.abs() @ f.v.abs().mT
                              + (g * o).abs().sum(-1, keepdim=True))
-    eS = dS.abs() * f.es[..., None] + f.P * dot
+    # P flushed shows as much as G V^T - delta is large, dS flushed once more.
+    eS = (dS.abs() * f.es[..., None] + f.P * dot
+          + FLUSH * ((dP - delta).abs() + 1))
 
     def fold(x):
         return x.reshape(B, Hk, f.group, *x.shape[2:]).sum(2)
@@ -99,7 +104,7 @@ def gradients(f, out, g):
     fold_or = fold
     dk, dv = fold(dS.mT @ f.q), fold(f.P.mT @ g)
     tk = tol(dk, dS.mT, eS.mT, f.q) * f.scale
-    tv = tol(dv, f.P.mT, (f.P * f.es[..., None]).mT, g)
+    tv = tol(dv, f.P.mT, (f.P * f.es[..., None] + 2 * FLUSH).mT, g)
     return (dq * f.scale, dk * f.scale, dv), (tq, tk, tv)
 
 
