@@ -118,33 +118,43 @@ __device__ __forceinline__ uint32_t bits_below(int limit, int base) {
 // empty row gives lo >= hi.
 __device__ __forceinline__ void warp_nonzero_range(const uint8_t* row, int n, int lane, int& lo,
                                                    int& hi) {
-    int first = n, past = 0;
+    // Fewer than 16 bytes before and after the aligned 16-byte units; all
+    // loads of a round are under way before the first is used.
     const int lead = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15);
     const int h = lead < n ? lead : n;
     const int vecs = (n - h) >> 4;
     const int tail = h + 16 * vecs;
-    auto one = [&](int i) {
-        if (row[i]) {
-            first = min(first, i);
-            past = max(past, i + 1);
-        }
-    };
-    // Fewer than 16 bytes before and after the aligned units.
-    if (lane < h) one(lane);
-    if (tail + lane < n) one(tail + lane);
+    const uint8_t before = lane < h ? row[lane] : 0;
+    const uint8_t after = tail + lane < n ? row[tail + lane] : 0;
+    int first = n, past = 0;
     const uint4* units = reinterpret_cast<const uint4*>(row + h);
-#pragma unroll 4
-    for (int v = lane; v < vecs; v += 32) {
-        const uint4 x = __ldg(units + v);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int v0 = lane; v0 < vecs; v0 += 4 * 32) {
+        uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (w[i]) {
-                const int at = h + 16 * v + 4 * i;
-                first = min(first, at + ((__ffs(static_cast<int>(w[i])) - 1) >> 3));
-                past = max(past, at + 4 - (__clz(static_cast<int>(w[i])) >> 3));
+        for (int k = 0; k < 4; ++k) {
+            const int v = v0 + 32 * k;
+            x[k] = v < vecs ? __ldg(units + v) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (w[i]) {
+                    const int at = h + 16 * (v0 + 32 * k) + 4 * i;
+                    first = min(first, at + ((__ffs(static_cast<int>(w[i])) - 1) >> 3));
+                    past = max(past, at + 4 - (__clz(static_cast<int>(w[i])) >> 3));
+                }
             }
         }
+    }
+    if (before) {
+        first = min(first, lane);
+        past = max(past, lane + 1);
+    }
+    if (after) {
+        first = min(first, tail + lane);
+        past = max(past, tail + lane + 1);
     }
     lo = __reduce_min_sync(0xffffffffu, first);
     hi = __reduce_max_sync(0xffffffffu, past);

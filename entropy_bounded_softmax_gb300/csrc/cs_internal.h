@@ -405,4 +405,23 @@ cudaError_t launch_take_error(unsigned int* err, unsigned int* taken,
 cudaError_t ensure_smem_attribute(const void* func, int slot, int bytes,
                                   bool cluster);
 
+// Launches a kernel that may start before the one before it on the stream has
+// ended: it calls csd::wait_for_previous_kernel() before it uses what that one
+// writes, and in every CTA.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int smem_bytes,
+                              cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace cs

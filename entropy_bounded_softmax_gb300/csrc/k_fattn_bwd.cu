@@ -14,7 +14,9 @@
 //       tiles, in the workspace for the second launch;
 //   keys (KV = true)      128 key rows a CTA, over blocks of queries of
 //       every head of its group: S^T = K Q^T, V G^T, dv += P^T G,
-//       dk += dS^T Q.
+//       dk += dS^T Q.  It starts while the first still runs, and waits for it
+//       where it needs the workspace: its start, and what is left of the
+//       device's SMs at the first's end, cost nothing.
 // In both the fixed tiles' rows are the lanes of tensor memory, and the
 // weights, rounded to bf16 in columns their scores had, are the next
 // product's A operand there.  Blocks are 128 rows for d_head > 64: a product
@@ -74,7 +76,7 @@ struct BwdPlan {
     static constexpr int kRows = kB2 + kStages2 * kBlock;  // [kStagesR][2][128] lse, delta
     static constexpr int kBars = kRows + kStagesR * 2 * 128 * 4;
     static constexpr int kNumBars =
-        1 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 7 + 2;
+        2 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 7 + 2;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages1][4]
     static constexpr int kFlags = kWords + kStages1 * 16;
     static constexpr int kBytes = kFlags + 16;
@@ -114,8 +116,8 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     // CTA can have up to a few hundred bytes; there are no static variables.
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-    uint64_t* a_full = bars;                   // the fixed tiles landed
-    uint64_t* b1_full = a_full + 1;            // [N1] ring stage landed
+    uint64_t* a_full = bars;                   // [2] a fixed tile landed
+    uint64_t* b1_full = a_full + 2;            // [N1] ring stage landed
     uint64_t* b1_empty = b1_full + N1;         // [N1] products that read it completed
     uint64_t* b1_masked = b1_empty + N1;       // [N1] removed rows zeroed, bits written
     uint64_t* b2_full = b1_masked + N1;        // [N2]
@@ -133,6 +135,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
+    if (!KV) allow_next_kernel();
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -162,15 +165,36 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 prefetch_tmap(&map_b1);
                 prefetch_tmap(&map_b2);
             }
-            mbar_arrive_expect_tx(a_full, 2 * L::kTile);
-            load_tile<128, DP>(smem + L::kA1, &map_a1, a0, ha, b, a_full);
-            load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, a_full);
-            prefetch_tmap(&map_d1);
-            prefetch_tmap(&map_d2);
+            mbar_arrive_expect_tx(&a_full[0], L::kTile);
+            load_tile<128, DP>(smem + L::kA1, &map_a1, a0, ha, b, &a_full[0]);
         }
         __syncwarp();
     } else if (warp == kBwdMmaWarp) {
         tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
+    }
+    // Queries: the rows of out and g that delta is taken from, and lse, on their
+    // way before anything is waited for: DP / 8 lanes a row, 16 bytes of each,
+    // 16 rows a warp.  (Taken one after the other, after the set-up, they cost
+    // 8000 cycles, a third of a short sequence's CTA.)
+    constexpr int LR = DP / 8, kSteps = 16 * LR / 32;
+    uint4 x[kSteps], y[kSteps];
+    float lse = -INFINITY;
+    const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
+    if (!KV && warp < 8) {
+        const int u = lane % LR;
+#pragma unroll
+        for (int n = 0; n < kSteps; ++n) {
+            const int i = a0 + 16 * warp + lane / LR + n * (32 / LR);
+            x[n] = y[n] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < t.query_len && 8 * u < t.d_head) {
+                x[n] = *reinterpret_cast<const uint4*>(
+                    t.out + b * t.o_stride[0] + ha * t.o_stride[1] + i * t.o_stride[2] + 8 * u);
+                y[n] = *reinterpret_cast<const uint4*>(
+                    t.go + b * t.go_stride[0] + ha * t.go_stride[1] + i * t.go_stride[2] + 8 * u);
+            }
+        }
+        const int a = a0 + 32 * (warp & 3) + lane;
+        if (a < t.query_len) lse = t.lse[row * t.query_len + a];
     }
     const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
     int key_lo = 0, key_hi = t.key_len;
@@ -212,30 +236,37 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                            bar);
         advance(at);
     };
-    // The second tensor's block, and for keys its queries' lse and delta.
+    // Keys: lse and delta of a block's queries.
+    auto load_rows = [&](int i, Place& at) {
+        const int64_t r = (static_cast<int64_t>(b) * t.heads + at.head) * padded + at.row;
+        uint64_t* bar = &r_full[i % NR];
+        float* rows = rows_s + 2 * BLK * (i % NR);
+        mbar_arrive_expect_tx(bar, 2 * BLK * 4);
+        bulk_load(rows, ws_lse + r, BLK * 4, bar);
+        bulk_load(rows + BLK, ws_delta + r, BLK * 4, bar);
+        advance(at);
+    };
     auto load2 = [&](int i, Place& at) {
-        if (KV) {
-            const int64_t r = (static_cast<int64_t>(b) * t.heads + at.head) * padded + at.row;
-            uint64_t* bar = &r_full[i % NR];
-            float* rows = rows_s + 2 * BLK * (i % NR);
-            mbar_arrive_expect_tx(bar, 2 * BLK * 4);
-            bulk_load(rows, ws_lse + r, BLK * 4, bar);
-            bulk_load(rows + BLK, ws_delta + r, BLK * 4, bar);
-        }
         uint64_t* bar = &b2_full[i % N2];
         mbar_arrive_expect_tx(bar, L::kBlock);
         load_tile<BLK, DP>(smem + L::kB2 + (i % N2) * L::kBlock, &map_b2, at.row, at.head, b,
                            bar);
         advance(at);
     };
-    Place at1 = begin, at2 = begin;            // the loader's
+    Place at1 = begin, at2 = begin, at_r = begin;   // the loader's
     const int early1 = min(blocks, N1), early2 = min(blocks, N2);
     static_assert(N2 == NR, "the row values' ring is as deep as the second tensor's");
     if (warp == kBwdLoadWarp && lane == 0) {
+        // In the order of their use: the first S, the first G V^T, the rest.
+        if (early1 > 0) load1(0, at1);
+        mbar_arrive_expect_tx(&a_full[1], L::kTile);
+        load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, &a_full[1]);
         for (int i = 0; i < early1; ++i) {
-            load1(i, at1);
             if (i < N2) load2(i, at2);
+            if (i + 1 < early1) load1(i + 1, at1);
         }
+        prefetch_tmap(&map_d1);
+        prefetch_tmap(&map_d2);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -262,36 +293,23 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         const float2 c2 = make_float2(c, c);
         float row_lse = 0.0f, row_delta = 0.0f;   // queries: -lse, -delta
         if (!KV) {
-            const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
-            // delta: DP / 8 lanes a row, 16 bytes of out and of g each.
-            constexpr int LR = DP / 8;
-            const int u = lane % LR;
-#pragma unroll 4
-            for (int r = 16 * warp + lane / LR; r < 16 * warp + 16; r += 32 / LR) {
-                const int i = a0 + r;
-                float d = 0.0f;
-                if (i < t.query_len && 8 * u < t.d_head) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(
-                        t.out + b * t.o_stride[0] + ha * t.o_stride[1] + i * t.o_stride[2] + 8 * u);
-                    const uint4 y = *reinterpret_cast<const uint4*>(
-                        t.go + b * t.go_stride[0] + ha * t.go_stride[1] + i * t.go_stride[2] + 8 * u);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            // delta from the rows loaded at the start.
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        d = fmaf(InBF16::lo(xs[k]), InBF16::lo(ys[k]), d);
-                        d = fmaf(InBF16::hi(xs[k]), InBF16::hi(ys[k]), d);
-                    }
+            for (int n = 0; n < kSteps; ++n) {
+                const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+                const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+                float d = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    d = fmaf(InBF16::lo(xs[k]), InBF16::lo(ys[k]), d);
+                    d = fmaf(InBF16::hi(xs[k]), InBF16::hi(ys[k]), d);
                 }
 #pragma unroll
                 for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                if (u == 0) rows_s[r] = d;
+                if (lane % LR == 0) rows_s[16 * warp + lane / LR + n * (32 / LR)] = d;
             }
             // An empty row, and a row past the last, gets -lse = -inf: P = 0.
-            row_lse = -INFINITY;
-            if (a < t.query_len) {
-                const float x = t.lse[row * t.query_len + a];
-                if (x != -INFINITY) row_lse = -x * kLog2e;
-            }
+            row_lse = lse == -INFINITY ? lse : -lse * kLog2e;
             named_barrier(kBarElementwise, kElementwise);
             row_delta = -rows_s[a - a0];
             if (half == 0) {
@@ -420,7 +438,9 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // The rows' sums, staged over the fixed tiles once those are read (or,
         // without blocks, have landed): keys: dv by the first four warps, dk
         // by the others; queries: a panel of 64 columns of dq each.
-        if (ok) ok = blocks > 0 ? warp_wait(sums_full, 0, limit) : warp_wait(a_full, 0, limit);
+        if (ok && blocks > 0) ok = warp_wait(sums_full, 0, limit);
+        if (ok && blocks == 0)
+            ok = warp_wait(&a_full[0], 0, limit) && warp_wait(&a_full[1], 0, limit);
         const int row0 = a0 + 32 * quarter;
         constexpr int kPanels = DP / 64;
         const int p0 = KV || kPanels == 1 ? 0 : half, p1 = KV ? kPanels : p0 + 1;
@@ -478,7 +498,8 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             mma_weights<DP, CO>(d, w + CO, b + CO / 16 * kDescRows16, true, leader);
         };
         bool ok = blocks == 0 ||
-                  (warp_wait(a_full, 0, limit) && scores(0) && grads(0));
+                  (warp_wait(&a_full[0], 0, limit) && scores(0) &&
+                   warp_wait(&a_full[1], 0, limit) && grads(0));
         for (int i = 0; i < blocks && ok; ++i) {
             const bool more = i + 1 < blocks;
             if (KV) {
@@ -508,6 +529,11 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         __syncwarp();
     } else if (warp == kBwdLoadWarp) {
         // --------------------------------------------------------- loader
+        if (KV && lane == 0) {
+            wait_for_previous_kernel();   // it writes the workspace
+            for (int i = 0; i < early2; ++i) load_rows(i, at_r);
+        }
+        __syncwarp();
         int issued1 = early1, issued2 = early2;
         for (int i = early2; i < blocks; ++i) {
             if (i >= early1) {
@@ -517,13 +543,16 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             }
             if (KV && !warp_wait(&r_empty[i % NR], i / NR - 1, limit)) break;
             if (!warp_wait(&b2_empty[i % N2], i / N2 - 1, limit)) break;
-            if (lane == 0) load2(i, at2);
+            if (lane == 0) {
+                if (KV) load_rows(i, at_r);
+                load2(i, at2);
+            }
             issued2 = i + 1;
         }
         // A copy may still be in flight after an abort, or the fixed tiles'
         // without blocks: none may land in shared memory after the CTA exits
         // (bounded waits).
-        mbar_wait<false>(a_full, 0u, t.wait_limit_cycles);
+        for (int i = 0; i < 2; ++i) mbar_wait<false>(&a_full[i], 0u, t.wait_limit_cycles);
         if (*limit.abort_flag) {
             for (int i = max(0, issued1 - N1); i < issued1; ++i)
                 mbar_wait<false>(&b1_full[i % N1], (i / N1) & 1, t.wait_limit_cycles);
@@ -589,9 +618,8 @@ cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
     }
     if (e == cudaSuccess && t.key_len > 0) {
         const dim3 grid(t.kv_heads, t.batch, (t.key_len + 127) / 128);
-        fattn_bwd_kernel<DP, true><<<grid, kBwdThreads, smem, stream>>>(
-            t, fixed.k, fixed.v, blocks.q, blocks.g, dv, dk);
-        e = cudaGetLastError();
+        e = launch_overlapped(fattn_bwd_kernel<DP, true>, grid, kBwdThreads, smem, stream, t,
+                              fixed.k, fixed.v, blocks.q, blocks.g, dv, dk);
     }
     return e;
 }

@@ -119,6 +119,12 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     const int q0 = 128 * T * qt;
     const int off = t.key_len - t.query_len;   // row i keeps keys j <= i + off
 
+    auto load_q = [&](int i) {
+        if (q0 + 128 * i >= t.query_len) return;
+        mbar_arrive_expect_tx(&q_full[i], L::kTile);
+        load_tile<128, DP>(smem + L::kQ + i * L::kTile, &map_q, q0 + 128 * i, h, b, &q_full[i]);
+    };
+
     // The loader initialises the barriers, and starts its first copies before
     // the others have set up.
     if (warp == L::kLoadWarp) {
@@ -132,13 +138,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 prefetch_tmap(&map_k);
                 prefetch_tmap(&map_v);
             }
-            for (int i = 0; i < T; ++i) {
-                if (q0 + 128 * i >= t.query_len) break;
-                mbar_arrive_expect_tx(&q_full[i], L::kTile);
-                load_tile<128, DP>(smem + L::kQ + i * L::kTile, &map_q, q0 + 128 * i, h, b,
-                                   &q_full[i]);
-            }
-            prefetch_tmap(&map_o);
+            load_q(0);
         }
         __syncwarp();
     } else if (warp == L::kMmaWarp) {
@@ -176,10 +176,14 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     auto phase = [&](int j) { return T == 2 ? j : j >> 1; };
     const int early = min(blocks, NS);
     if (warp == L::kLoadWarp && lane == 0) {
+        // In the order of their use.
         for (int j = 0; j < early; ++j) {
             load_k(j);
+            if (j == 0 && T == 2) load_q(1);
             load_v(j);
         }
+        if (early == 0 && T == 2) load_q(1);
+        prefetch_tmap(&map_o);
     }
     tc_fence_before_sync();
     __syncthreads();

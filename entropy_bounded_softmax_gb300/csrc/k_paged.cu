@@ -56,16 +56,6 @@ __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
-// The next kernel on the stream, launched to overlap this one, may start once
-// every CTA has called the first or ended; the second waits until the kernel
-// before has ended and its writes are visible.
-__device__ __forceinline__ void allow_next_kernel() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous_kernel() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -555,11 +545,12 @@ paged_join_kernel(const PagedTask t) {
     const int b = blockIdx.y, h = blockIdx.x;
     bool bad;
     const int steps = steps_of(length_of(t, b, bad));
-    if (steps == 0) return;
     const int share = share_of(t, steps_before(t, t.batch, scan));
     const int begin = steps_before(t, b, scan);
     const int c0 = begin / share, c1 = (begin + steps - 1) / share;
-    if (c0 == c1) return;   // finished by the only group that had it
+    wait_for_previous_kernel();
+    // Without steps, or finished by the only group that had it.
+    if (steps == 0 || c0 == c1) return;
     const int group = t.heads / t.kv_heads;
     const int hk = h / group, hh = h - hk * group;
     const int rows = t.kv_heads * t.head_tiles, row = hk * t.head_tiles + hh / 16;
@@ -572,7 +563,6 @@ paged_join_kernel(const PagedTask t) {
                hh % 16;
     };
     const int lane = threadIdx.x & 31;
-    wait_for_previous_kernel();
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 4
     for (int i = lane; i < n; i += 32) {
@@ -627,16 +617,8 @@ cudaError_t launch(const PagedTask& t, int slot, cudaStream_t stream) {
     paged_kernel<DP, T><<<grid, kPgThreads, PgSmem<DP>::kBytes, stream>>>(t);
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.split) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(t.heads, t.batch);
-    cfg.blockDim = dim3(kPgThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<DP, T>, t);
+    return launch_overlapped(paged_join_kernel<DP, T>, dim3(t.heads, t.batch), kPgThreads, 0,
+                             stream, t);
 }
 
 template <class T>
