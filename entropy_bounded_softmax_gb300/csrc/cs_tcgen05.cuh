@@ -272,22 +272,6 @@ __device__ __forceinline__ void tma_load_4d(void* sdst, const void* tmap, int x,
            "r"(smem_addr(bar)) : "memory");
 }
 
-// The same from shared into global memory (elements outside the tensor are
-// not written); bulk_store_wait_read() commits this thread's stores and waits
-// until their source has been read.
-__device__ __forceinline__ void tma_store_4d(const void* tmap, const void* ssrc, int x, int y,
-                                             int z, int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group"
-        " [%0, {%1, %2, %3, %4}], [%5];"
-        :: "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(ssrc)) : "memory");
-}
-
-__device__ __forceinline__ void bulk_store_wait_read() {
-    asm volatile("cp.async.bulk.commit_group;\n"
-                 "cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
 // Fetches a tensor map ahead of its first use.
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(tmap) : "memory");

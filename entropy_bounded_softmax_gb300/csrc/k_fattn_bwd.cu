@@ -73,10 +73,14 @@ struct BwdPlan {
     static constexpr int kA2 = kA1 + kTile;    // G, or V
     static constexpr int kB1 = kA2 + kTile;
     static constexpr int kB2 = kB1 + kStages1 * kBlock;
-    static constexpr int kRows = kB2 + kStages2 * kBlock;  // [kStagesR][2][128] lse, delta
+    // Queries: the tile of out, before the first blocks: where shared memory
+    // is full, over the last stage of the first ring.
+    static constexpr int kOut = DP == 64 ? kB2 + kStages2 * kBlock
+                                         : kB1 + (kStages1 - 1) * kBlock;
+    static constexpr int kRows = kB2 + kStages2 * kBlock + (DP == 64 ? kTile : 0);  // [kStagesR][2][128] lse, delta
     static constexpr int kBars = kRows + kStagesR * 2 * 128 * 4;
     static constexpr int kNumBars =
-        2 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 7 + 2;
+        3 + 3 * kStages1 + 2 * kStages2 + 2 * kStagesR + 8 + 2;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages1][4]
     static constexpr int kFlags = kWords + kStages1 * 16;
     static constexpr int kBytes = kFlags + 16;
@@ -107,8 +111,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                  const __grid_constant__ CUtensorMap map_a2,
                  const __grid_constant__ CUtensorMap map_b1,
                  const __grid_constant__ CUtensorMap map_b2,
-                 const __grid_constant__ CUtensorMap map_d1,
-                 const __grid_constant__ CUtensorMap map_d2) {
+                 const __grid_constant__ CUtensorMap map_o) {
     using L = BwdPlan<DP>;
     constexpr int N1 = L::kStages1, N2 = L::kStages2, NR = L::kStagesR;
     constexpr int BLK = L::kBlk, CO = L::kCols;
@@ -117,7 +120,8 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t* a_full = bars;                   // [2] a fixed tile landed
-    uint64_t* b1_full = a_full + 2;            // [N1] ring stage landed
+    uint64_t* o_full = a_full + 2;             // queries: the tile of out landed
+    uint64_t* b1_full = o_full + 1;            // [N1] ring stage landed
     uint64_t* b1_empty = b1_full + N1;         // [N1] products that read it completed
     uint64_t* b1_masked = b1_empty + N1;       // [N1] removed rows zeroed, bits written
     uint64_t* b2_full = b1_masked + N1;        // [N2]
@@ -128,7 +132,8 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     uint64_t* sums_full = g_full + 2;          // every sum completed
     uint64_t* drained = sums_full + 1;
     uint64_t* r_empty = drained + 1;           // [NR] from eight warps, as those below
-    uint64_t* s_read = r_empty + NR;           // queries: the scores are in registers
+    uint64_t* o_read = r_empty + NR;           // queries: the tile of out is read
+    uint64_t* s_read = o_read + 1;             // queries: the scores are in registers
     uint64_t* p_full = s_read + 1;             // keys: the block's P
     uint64_t* d_full = p_full + 1;             // [2] its dS, by buffer
     float* rows_s = reinterpret_cast<float*>(smem + L::kRows);
@@ -171,30 +176,6 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         __syncwarp();
     } else if (warp == kBwdMmaWarp) {
         tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
-    }
-    // Queries: the rows of out and g that delta is taken from, and lse, on their
-    // way before anything is waited for: DP / 8 lanes a row, 16 bytes of each,
-    // 16 rows a warp.  (Taken one after the other, after the set-up, they cost
-    // 8000 cycles, a third of a short sequence's CTA.)
-    constexpr int LR = DP / 8, kSteps = 16 * LR / 32;
-    uint4 x[kSteps], y[kSteps];
-    float lse = -INFINITY;
-    const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
-    if (!KV && warp < 8) {
-        const int u = lane % LR;
-#pragma unroll
-        for (int n = 0; n < kSteps; ++n) {
-            const int i = a0 + 16 * warp + lane / LR + n * (32 / LR);
-            x[n] = y[n] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < t.query_len && 8 * u < t.d_head) {
-                x[n] = *reinterpret_cast<const uint4*>(
-                    t.out + b * t.o_stride[0] + ha * t.o_stride[1] + i * t.o_stride[2] + 8 * u);
-                y[n] = *reinterpret_cast<const uint4*>(
-                    t.go + b * t.go_stride[0] + ha * t.go_stride[1] + i * t.go_stride[2] + 8 * u);
-            }
-        }
-        const int a = a0 + 32 * (warp & 3) + lane;
-        if (a < t.query_len) lse = t.lse[row * t.query_len + a];
     }
     const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
     int key_lo = 0, key_hi = t.key_len;
@@ -254,19 +235,17 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         advance(at);
     };
     Place at1 = begin, at2 = begin, at_r = begin;   // the loader's
-    const int early1 = min(blocks, N1), early2 = min(blocks, N2);
     static_assert(N2 == NR, "the row values' ring is as deep as the second tensor's");
     if (warp == kBwdLoadWarp && lane == 0) {
-        // In the order of their use: the first S, the first G V^T, the rest.
-        if (early1 > 0) load1(0, at1);
+        // In the order of their use: the first S, the first G V^T.
+        if (blocks > 0) load1(0, at1);
         mbar_arrive_expect_tx(&a_full[1], L::kTile);
         load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, &a_full[1]);
-        for (int i = 0; i < early1; ++i) {
-            if (i < N2) load2(i, at2);
-            if (i + 1 < early1) load1(i + 1, at1);
+        if (!KV) {
+            mbar_arrive_expect_tx(o_full, L::kTile);
+            load_tile<128, DP>(smem + L::kOut, &map_o, a0, ha, b, o_full);
         }
-        prefetch_tmap(&map_d1);
-        prefetch_tmap(&map_d2);
+        if (blocks > 0) load2(0, at2);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -292,22 +271,44 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         const float c = t.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
         float row_lse = 0.0f, row_delta = 0.0f;   // queries: -lse, -delta
+        bool ok = true;
         if (!KV) {
-            // delta from the rows loaded at the start.
+            // delta: DP / 8 lanes a row, 16 bytes of out and of g each, 16 rows
+            // a warp, from the tiles that the tensor copies brought.  (Loads of
+            // out's rows took 2 to 10 thousand cycles, a third of a short
+            // sequence's CTA.)  A wait that gives up leaves delta wrong and the
+            // barrier below matched; the next wait gives up too.
+            constexpr int LR = DP / 8, kSteps = 16 * LR / 32;
+            const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
+            const float lse = a < t.query_len ? t.lse[row * t.query_len + a] : -INFINITY;
+            warp_wait(&a_full[1], 0, limit);
+            warp_wait(o_full, 0, limit);
+            const int u = lane % LR, r0 = 16 * warp + lane / LR;
+            float d[kSteps];
 #pragma unroll
             for (int n = 0; n < kSteps; ++n) {
-                const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-                const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
-                float d = 0.0f;
+                const int r = r0 + n * (32 / LR);
+                const int at = (u >> 3) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+                const uint4 x = *reinterpret_cast<const uint4*>(smem + L::kOut + at);
+                const uint4 y = *reinterpret_cast<const uint4*>(smem + L::kA2 + at);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    d = fmaf(InBF16::lo(xs[k]), InBF16::lo(ys[k]), d);
-                    d = fmaf(InBF16::hi(xs[k]), InBF16::hi(ys[k]), d);
-                }
-#pragma unroll
-                for (int o = LR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                if (lane % LR == 0) rows_s[16 * warp + lane / LR + n * (32 / LR)] = d;
+                for (int k = 0; k < 4; ++k)
+                    sum = fma2(make_float2(InBF16::lo(xs[k]), InBF16::hi(xs[k])),
+                               make_float2(InBF16::lo(ys[k]), InBF16::hi(ys[k])), sum);
+                d[n] = sum.x + sum.y;
             }
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int n = 0; n < kSteps; ++n) d[n] += __shfl_xor_sync(0xffffffffu, d[n], o);
+#pragma unroll
+            for (int n = 0; n < kSteps; ++n)
+                if (u == 0) rows_s[r0 + n * (32 / LR)] = d[n];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_read);
             // An empty row, and a row past the last, gets -lse = -inf: P = 0.
             row_lse = lse == -INFINITY ? lse : -lse * kLog2e;
             named_barrier(kBarElementwise, kElementwise);
@@ -317,7 +318,6 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 ws_delta[row * padded + a] = row_delta;
             }
         }
-        bool ok = true;
         Place place = begin;
         for (int i = 0; i < blocks; ++i) {
             const int st = i % NR;
@@ -465,8 +465,11 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 for (int k = 0; k < 32; ++k) x[k] = zero ? 0u : x[k];
                 stage_row32(stage, 32 * quarter + lane, c0, x, f);
             }
-            store_rows32(stage, 32 * quarter, p0, p1, KV && half == 1 ? &map_d2 : &map_d1, row0,
-                         ha, b, lane);
+            uint16_t* to = KV ? (half == 1 ? t.dk : t.dv) : t.dq;
+            const int64_t* stride = KV ? (half == 1 ? t.dk_stride : t.dv_stride) : t.dq_stride;
+            store_rows32<KV ? kPanels : 1>(
+                stage, 32 * quarter, p0, to + b * stride[0] + ha * stride[1] + row0 * stride[2],
+                stride[2], fixed_len - row0, t.d_head, lane);
         }
     } else if (warp == kBwdMmaWarp) {
         // ----------------------------------------------------- MMA issuer
@@ -531,18 +534,23 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // --------------------------------------------------------- loader
         if (KV && lane == 0) {
             wait_for_previous_kernel();   // it writes the workspace
-            for (int i = 0; i < early2; ++i) load_rows(i, at_r);
+            if (blocks > 0) load_rows(0, at_r);
         }
         __syncwarp();
-        int issued1 = early1, issued2 = early2;
-        for (int i = early2; i < blocks; ++i) {
-            if (i >= early1) {
-                if (!warp_wait(&b1_empty[i % N1], i / N1 - 1, limit)) break;
-                if (lane == 0) load1(i, at1);
-                issued1 = i + 1;
+        // The rest once the first blocks are there: while CTAs start together
+        // L2 is what bounds them (288 KB each took 9000 cycles to come).
+        int issued1 = min(blocks, 1), issued2 = issued1;
+        if (blocks > 1) warp_wait(&b2_full[0], 0, limit);
+        for (int i = 1; i < blocks; ++i) {
+            if (i >= N1 && !warp_wait(&b1_empty[i % N1], i / N1 - 1, limit)) break;
+            // The first copy over the tile of out.
+            if (!KV && DP == 128 && i == N1 - 1 && !warp_wait(o_read, 0, limit)) break;
+            if (lane == 0) load1(i, at1);
+            issued1 = i + 1;
+            if (i >= N2) {
+                if (KV && !warp_wait(&r_empty[i % NR], i / NR - 1, limit)) break;
+                if (!warp_wait(&b2_empty[i % N2], i / N2 - 1, limit)) break;
             }
-            if (KV && !warp_wait(&r_empty[i % NR], i / NR - 1, limit)) break;
-            if (!warp_wait(&b2_empty[i % N2], i / N2 - 1, limit)) break;
             if (lane == 0) {
                 if (KV) load_rows(i, at_r);
                 load2(i, at2);
@@ -553,6 +561,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // without blocks: none may land in shared memory after the CTA exits
         // (bounded waits).
         for (int i = 0; i < 2; ++i) mbar_wait<false>(&a_full[i], 0u, t.wait_limit_cycles);
+        if (!KV) mbar_wait<false>(o_full, 0u, t.wait_limit_cycles);
         if (*limit.abort_flag) {
             for (int i = max(0, issued1 - N1); i < issued1; ++i)
                 mbar_wait<false>(&b1_full[i % N1], (i / N1) & 1, t.wait_limit_cycles);
@@ -603,23 +612,21 @@ cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Fixed tiles of 128 rows, streamed blocks of kBlk.
     InputMaps fixed, streamed;
-    CUtensorMap dq, dk, dv;
+    CUtensorMap out;
     if (!fixed.encode(t, 128) || (L::kBlk != 128 && !streamed.encode(t, L::kBlk)) ||
-        !encode_heads_map(&dq, t.dq, t, t.heads, t.query_len, t.dq_stride, 32) ||
-        !encode_heads_map(&dk, t.dk, t, t.kv_heads, t.key_len, t.dk_stride, 32) ||
-        !encode_heads_map(&dv, t.dv, t, t.kv_heads, t.key_len, t.dv_stride, 32))
+        !encode_heads_map(&out, t.out, t, t.heads, t.query_len, t.o_stride, 128))
         return cudaErrorInvalidValue;
     const InputMaps& blocks = L::kBlk == 128 ? fixed : streamed;
     if (t.query_len > 0) {
         const dim3 grid(t.heads, t.batch, (t.query_len + 127) / 128);
         fattn_bwd_kernel<DP, false><<<grid, kBwdThreads, smem, stream>>>(
-            t, fixed.q, fixed.g, blocks.k, blocks.v, dq, dq);
+            t, fixed.q, fixed.g, blocks.k, blocks.v, out);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && t.key_len > 0) {
         const dim3 grid(t.kv_heads, t.batch, (t.key_len + 127) / 128);
         e = launch_overlapped(fattn_bwd_kernel<DP, true>, grid, kBwdThreads, smem, stream, t,
-                              fixed.k, fixed.v, blocks.q, blocks.g, dv, dk);
+                              fixed.k, fixed.v, blocks.q, blocks.g, out);
     }
     return e;
 }

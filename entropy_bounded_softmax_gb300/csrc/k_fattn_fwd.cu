@@ -20,7 +20,7 @@
 // Roles of a CTA of T tiles, one mbarrier hand-off each:
 //   4 T warps  softmax, one row a thread: the maximum of the row's scores,
 //              2^(s c - m c) and the sum, the weights back to tensor memory;
-//              at the end the output, through shared memory, by tensor copies;
+//              at the end the output, through shared memory;
 //   MMA warp   issues the products: for each block and tile P V, then a
 //              coming block's Q K^T into the columns P V has read;
 //   loader     tensor copies of Q, and of K and V into rings;
@@ -87,8 +87,7 @@ template <int DP>
 __global__ void __launch_bounds__(FwdPlan<DP>::kThreads, FwdPlan<DP>::kCtasPerSm)
 fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                  const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v,
-                 const __grid_constant__ CUtensorMap map_o) {
+                 const __grid_constant__ CUtensorMap map_v) {
     using L = FwdPlan<DP>;
     constexpr int NS = L::kStages, T = L::kTiles, BLK = L::kBlk, AHEAD = L::kAhead;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -183,7 +182,6 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             load_v(j);
         }
         if (early == 0 && T == 2) load_q(1);
-        prefetch_tmap(&map_o);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -303,7 +301,10 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 }
                 stage_row32(stage, r + lane, 32 * u, o, inv);
             }
-            store_rows32(stage, r, 0, DP / 64, &map_o, row0, h, b, lane);
+            store_rows32<DP / 64>(
+                stage, r, 0,
+                t.out + b * t.o_stride[0] + h * t.o_stride[1] + row0 * t.o_stride[2],
+                t.o_stride[2], t.query_len - row0, t.d_head, lane);
             if (i < t.query_len) {
                 if (t.lse)
                     t.lse[row] =
@@ -410,16 +411,15 @@ cudaError_t launch_fwd(const FattnTask& t, int slot, cudaStream_t stream) {
     const void* kern = reinterpret_cast<const void*>(fattn_fwd_kernel<DP>);
     cudaError_t e = ensure_smem_attribute(kern, slot, L::kBytes, false);
     if (e != cudaSuccess) return e;
-    CUtensorMap mq, mk, mv, mo;
+    CUtensorMap mq, mk, mv;
     if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, 128) ||
         !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, L::kBlk) ||
-        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, L::kBlk) ||
-        !encode_heads_map(&mo, t.out, t, t.heads, t.query_len, t.o_stride, 32))
+        !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, L::kBlk))
         return cudaErrorInvalidValue;
     constexpr int kRows = 128 * L::kTiles;
     const dim3 grid(t.heads, t.batch, (t.query_len + kRows - 1) / kRows);
     fattn_fwd_kernel<DP><<<grid, L::kThreads, L::kBytes, stream>>>(
-        t, mq, mk, mv, mo);
+        t, mq, mk, mv);
     return cudaGetLastError();
 }
 
