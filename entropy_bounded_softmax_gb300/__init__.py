@@ -86,7 +86,6 @@ ERROR_BITS = {name: 1 << CONSTANTS[f"CS_ERR_{name}"]
 
 
 _STAY = contextlib.nullcontext()
-_INF = float("inf")
 
 
 class CsError(RuntimeError):
@@ -336,43 +335,40 @@ def biencoder_attention(query, keys, values, scale=None,
     return res if len(res) > 1 else out
 
 
-def _heads(name, x, shape, device, torch):
-    """The strides and the address of a [batch, heads, length, d_head] bf16
-    tensor, checked: on the CUDA device of that index, of the given shape, in
-    strides that the tensor copies take."""
-    if isinstance(x, torch.Tensor):
-        st = x.stride()
-        ptr = x.data_ptr()
-        if (x.dtype is torch.bfloat16 and x.get_device() == device
-                and x.shape == shape):
-            s0, s1, s2, s3 = st
-            if (s3 == 1 and s0 > 0 and s1 > 0 and s2 > 0
-                    and not (ptr | 2 * (s0 | s1 | s2)) & 15):
-                return st, ptr
-    # The refusals, and the shapes whose strides do not all matter.
+def _check_heads(name, x, shape, device) -> None:
+    """Raises what is wrong with a [batch, heads, length, d_head] bf16
+    tensor of fused attention."""
+    import torch
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dtype is not torch.bfloat16:
+    if x.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
+    if x.dim() != 4:
+        raise ValueError(f"{name} must be 4-D [batch, heads, length, d_head]")
     if x.get_device() != device:
         raise ValueError(f"{name} must be on the query's device")
-    if x.shape != shape:
+    if tuple(x.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if x.numel():
-        if st[3] != 1:
-            raise ValueError(f"{name}'s head dimension must be contiguous")
-        if ptr & 15 or any(n > 1 and (s <= 0 or s % 8)
-                           for n, s in zip(shape[:3], st)):
-            raise ValueError(f"{name}'s base must be 16-byte aligned and its "
-                             "batch, head and position strides positive "
-                             "multiples of 8 elements")
-    return st, ptr
+    if not x.numel():
+        return
+    st = x.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}'s head dimension must be contiguous")
+    if x.data_ptr() & 15 or any(n > 1 and (s <= 0 or s % 8)
+                                for n, s in zip(shape[:3], st)):
+        raise ValueError(f"{name}'s base must be 16-byte aligned and its "
+                         "batch, head and position strides positive "
+                         "multiples of 8 elements")
 
 
-def _attention_inputs(query, keys, values, mask, scale, torch):
-    """The checked inputs of fused attention: the query's device index, the
-    two shapes, the scale, and (strides, address) of query, keys, values and
-    the mask's row stride and address."""
+def _check_attention(query, keys, values, mask, scale, lse, same) -> None:
+    """Raises what is wrong with the arguments of fused attention, if
+    anything is; `same`: the tensors that have to be shaped like query, by
+    name.  The calls look at the properties that they need themselves, and
+    leave strides, addresses and ranges to the library; only what either
+    refuses comes here for its message."""
+    import math
+    import torch
     for name, x in (("query", query), ("keys", keys)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -380,35 +376,70 @@ def _attention_inputs(query, keys, values, mask, scale, torch):
             raise ValueError(f"{name} must be 4-D [batch, heads, length, "
                              "d_head]")
     dev = query.get_device()
-    qs, ks = query.shape, keys.shape
-    B, H, _, D = qs
-    Hk, Sk = ks[1], ks[2]
-    if ks[0] != B or ks[3] != D:
+    B, H, Sq, D = query.shape
+    Hk, Sk = keys.shape[1], keys.shape[2]
+    if keys.shape[0] != B or keys.shape[3] != D:
         raise ValueError("keys must be [batch, kv_heads, key_len, d_head] "
                          "with the query's batch and d_head")
     if Hk < 1 or H < 1 or H % Hk:
         raise ValueError("the query's heads must be a multiple of the keys'")
     if D < 8 or D > 128 or D % 8:
         raise ValueError("d_head must be a multiple of 8 in 8..128")
-    q = _heads("query", query, qs, dev, torch)
-    k = _heads("keys", keys, ks, dev, torch)
-    v = _heads("values", values, ks, dev, torch)
-    if scale is None:
-        scale = D ** -0.5
-    elif not 0.0 < scale < _INF:
+    _check_heads("query", query, query.shape, dev)
+    _check_heads("keys", keys, keys.shape, dev)
+    _check_heads("values", values, keys.shape, dev)
+    for name, x in same.items():
+        _check_heads(name, x, query.shape, dev)
+    if scale is not None and not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
-    m = (Sk, None)
     if mask is not None:
         if (not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool
-                or mask.device != query.device or mask.shape != (B, Sk)):
+                or mask.device != query.device
+                or tuple(mask.shape) != (B, Sk)):
             raise ValueError("mask must be a bool [batch, key_len] tensor on "
                              "the query's device")
-        s0, s1 = mask.stride()
-        if (Sk > 1 and s1 != 1) or (B > 1 and s0 < Sk):
+        if ((Sk > 1 and mask.stride(1) != 1)
+                or (B > 1 and mask.stride(0) < Sk)):
             raise ValueError("mask's rows must be contiguous and not overlap")
-        if mask.numel():
-            m = (s0, mask.data_ptr())
-    return dev, qs, ks, scale, q, k, v, m
+    if lse is not None and (
+            not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32
+            or lse.shape != query.shape[:3] or lse.get_device() != dev
+            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [batch, heads, "
+                         "query_len] tensor on the query's device")
+
+
+def _attention_ok(torch, query, keys, values, mask, lse, same):
+    """Whether the properties that the library cannot see are right: types,
+    devices, shapes and contiguous last dimensions."""
+    t = torch.Tensor
+    if not (isinstance(query, t) and isinstance(keys, t)
+            and isinstance(values, t)):
+        return False
+    bf16, dev = torch.bfloat16, query.get_device()
+    shape, ks = query.shape, keys.shape
+    if (query.dtype is not bf16 or keys.dtype is not bf16
+            or values.dtype is not bf16 or dev < 0
+            or keys.get_device() != dev or values.get_device() != dev
+            or len(shape) != 4 or len(ks) != 4 or values.shape != ks
+            or ks[0] != shape[0] or ks[3] != shape[3] or shape[3] < 2
+            or query.stride(3) != 1 or keys.stride(3) != 1
+            or values.stride(3) != 1):
+        return False
+    for x in same:
+        if (not isinstance(x, t) or x.dtype is not bf16
+                or x.get_device() != dev or x.shape != shape
+                or x.stride(3) != 1):
+            return False
+    if mask is not None and (
+            not isinstance(mask, t) or mask.dtype is not torch.bool
+            or mask.get_device() != dev or mask.shape != (ks[0], ks[2])
+            or mask.stride(1) != 1):
+        return False
+    return lse is None or (
+        isinstance(lse, t) and lse.dtype is torch.float32
+        and lse.get_device() == dev and lse.shape == shape[:3]
+        and lse.is_contiguous())
 
 
 def fused_attention(query, keys, values, mask=None, causal: bool = False,
@@ -431,26 +462,30 @@ def fused_attention(query, keys, values, mask=None, causal: bool = False,
     :func:`get_error`.
     """
     import torch
-    dev, qs, ks, scale, q, k, v, m = _attention_inputs(query, keys, values,
-                                                       mask, scale, torch)
-    B, H, Sq, D = qs
+    same = () if out is None else (out,)
+    if not _attention_ok(torch, query, keys, values, mask, None, same):
+        _check_attention(query, keys, values, mask, scale, None,
+                         {} if out is None else {"out": out})
+    B, H, Sq, D = query.shape
+    _, Hk, Sk, _ = keys.shape
     if out is None:
         out = torch.empty_like(query)
-        o = out.stride(), out.data_ptr()
-    else:
-        o = _heads("out", out, qs, dev, torch)
     lse = None
     if return_lse:
         lse = torch.empty((B, H, Sq), dtype=torch.float32,
                           device=query.device)
     shape = _lib.pack_attention_shape(
-        B, H, ks[1], Sq, ks[2], D, 1 if causal else 0, scale, q[0], k[0],
-        v[0], o[0], m[0])
+        B, H, Hk, Sq, Sk, D, 1 if causal else 0,
+        D ** -0.5 if scale is None else scale, query.stride(), keys.stride(),
+        values.stride(), out.stride(), Sk if mask is None else mask.stride(0))
     with _on_device(query.device):
-        st = cs_fused_attention(q[1], k[1], v[1], o[1],
-                                lse.data_ptr() if return_lse else None, m[1],
-                                shape, _stream_handle(query.device))
+        st = cs_fused_attention(
+            query.data_ptr(), keys.data_ptr(), values.data_ptr(),
+            out.data_ptr(), lse.data_ptr() if return_lse else None,
+            None if mask is None else mask.data_ptr(), shape,
+            _stream_handle(query.device))
     if st != 0:
+        _check_attention(query, keys, values, mask, scale, lse, {"out": out})
         raise CsError(st, "cs_fused_attention")
     return (out, lse) if return_lse else out
 
@@ -465,69 +500,120 @@ def fused_attention_backward(query, keys, values, out, lse, grad_output,
     zeros.  Asynchronous on the current stream.
     """
     import torch
-    dev, qs, ks, scale, q, k, v, m = _attention_inputs(query, keys, values,
-                                                       mask, scale, torch)
-    B, H, Sq, D = qs
-    o = _heads("out", out, qs, dev, torch)
-    go = _heads("grad_output", grad_output, qs, dev, torch)
-    if (not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32
-            or lse.shape != qs[:3] or lse.get_device() != dev
-            or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [batch, heads, "
-                         "query_len] tensor on the query's device")
+    same = {"out": out, "grad_output": grad_output}
+    if lse is None or not _attention_ok(torch, query, keys, values, mask, lse,
+                                        (out, grad_output)):
+        _check_attention(query, keys, values, mask, scale,
+                         False if lse is None else lse, same)
+    B, H, Sq, D = query.shape
+    _, Hk, Sk, _ = keys.shape
     dq, dk, dv = (torch.empty_like(query), torch.empty_like(keys),
                   torch.empty_like(values))
     shape = _lib.pack_attention_backward_shape(
-        B, H, ks[1], Sq, ks[2], D, 1 if causal else 0, scale, q[0], k[0],
-        v[0], o[0], go[0], dq.stride(), dk.stride(), dv.stride(), m[0])
-    size = cs_fused_attention_backward_workspace(shape)
-    work = torch.empty(max(size, 0), dtype=torch.uint8, device=query.device)
+        B, H, Hk, Sq, Sk, D, 1 if causal else 0,
+        D ** -0.5 if scale is None else scale, query.stride(), keys.stride(),
+        values.stride(), out.stride(), grad_output.stride(), dq.stride(),
+        dk.stride(), dv.stride(), Sk if mask is None else mask.stride(0))
+    size = max(cs_fused_attention_backward_workspace(shape), 0)
+    work = torch.empty(size, dtype=torch.uint8, device=query.device)
     with _on_device(query.device):
         st = cs_fused_attention_backward(
-            q[1], k[1], v[1], o[1], lse.data_ptr(), go[1], dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), m[1], shape, work.data_ptr(), size,
-            _stream_handle(query.device))
+            query.data_ptr(), keys.data_ptr(), values.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), grad_output.data_ptr(),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            None if mask is None else mask.data_ptr(), shape, work.data_ptr(),
+            size, _stream_handle(query.device))
     if st != 0:
+        _check_attention(query, keys, values, mask, scale, lse, same)
         raise CsError(st, "cs_fused_attention_backward")
     return dq, dk, dv
 
 
-def _rows(name, x, shape, dtype, device, torch):
-    """The strides and the address of a strided tensor with a contiguous last
-    dimension, checked: on the CUDA device of that index, of the given shape
-    and type, 16-byte aligned rows."""
-    if (not isinstance(x, torch.Tensor) or not x.is_cuda
-            or x.get_device() != device):
-        raise ValueError(f"{name} must be a CUDA tensor on one device with "
-                         "the others")
-    if x.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if x.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    st = x.stride()
-    ptr = x.data_ptr()
-    if (st[-1] != 1 or ptr & 15 or sum(s & 7 for s in st[:-1])) and (
-            x.numel() and (st[-1] != 1 or ptr & 15 or any(
-                n > 1 and s & 7 for n, s in zip(shape[:-1], st)))):
-        raise ValueError(f"{name}'s last dimension must be contiguous, its "
-                         "base 16-byte aligned and its other strides "
-                         "multiples of 8 elements")
-    return st, ptr
+def _check_paged(query, key_pages, value_pages, page_table, lengths, scale,
+                 out) -> None:
+    """Raises what is wrong with the arguments of paged attention, if
+    anything is (as _check_attention)."""
+    import math
+    import torch
+    for name, x, dim in (("query", query, 3), ("key_pages", key_pages, 4)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.dim() != dim:
+            raise ValueError(f"{name} must have {dim} dimensions")
+    dev = query.device
+    if query.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("query must be a bfloat16 or float16 tensor")
+    B, H, D = query.shape
+    _, page_size, Hk, _ = key_pages.shape
+    if key_pages.shape[3] != D:
+        raise ValueError("key_pages must be [pages, page_size, kv_heads, "
+                         "d_head] with the query's d_head")
+    if H < 1 or Hk < 1 or H % Hk or page_size < 1:
+        raise ValueError("the query's heads must be a multiple of the "
+                         "pages', and page_size positive")
+    if D < 8 or D > 256 or D % 8:
+        raise ValueError("d_head must be a multiple of 8 in 8..256")
+    for name, x, shape in (("query", query, query.shape),
+                           ("key_pages", key_pages, key_pages.shape),
+                           ("value_pages", value_pages, key_pages.shape),
+                           ("out", out, query.shape)):
+        if name == "out" and x is None:
+            continue
+        if not isinstance(x, torch.Tensor) or x.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the query's "
+                             "device")
+        if x.dtype != query.dtype:
+            raise TypeError(f"{name} must be {query.dtype}")
+        if x.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}")
+        if x.numel() and (
+                x.stride(-1) != 1 or x.data_ptr() & 15
+                or any(n > 1 and s % 8
+                       for n, s in zip(shape[:-1], x.stride()))):
+            raise ValueError(f"{name}'s last dimension must be contiguous, "
+                             "its base 16-byte aligned and its other strides "
+                             "multiples of 8 elements")
+    for name, x, dim in (("page_table", page_table, 2),
+                         ("lengths", lengths, 1)):
+        if (not isinstance(x, torch.Tensor) or x.dtype != torch.int32
+                or x.device != dev or x.dim() != dim or x.shape[0] != B
+                or (x.shape[-1] > 1 and x.stride(-1) != 1)):
+            raise ValueError(f"{name} must be an int32 tensor of the batch's "
+                             "rows, contiguous along its last dimension, on "
+                             "the query's device")
+    if B > 1 and page_table.stride(0) < page_table.shape[1]:
+        raise ValueError("page_table's rows must not overlap")
+    if scale is not None and not (scale > 0.0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
 
 
-def _index_rows(name, x, dim, rows, device, torch):
-    """The strides and the address of an int32 tensor of page numbers or
-    lengths, checked."""
-    if (not isinstance(x, torch.Tensor) or x.dtype is not torch.int32
-            or x.get_device() != device or x.dim() != dim
-            or x.shape[0] != rows):
-        raise ValueError(f"{name} must be an int32 tensor of the batch's "
-                         "rows on the query's device")
-    st = x.stride()
-    if x.shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{name} must be contiguous along its last "
-                         "dimension")
-    return st, x.data_ptr()
+def _paged_ok(torch, query, key_pages, value_pages, page_table, lengths, out):
+    """Whether the properties that the library cannot see are right."""
+    t = torch.Tensor
+    if not (isinstance(query, t) and isinstance(key_pages, t)
+            and isinstance(value_pages, t) and isinstance(page_table, t)
+            and isinstance(lengths, t)):
+        return False
+    dtype, dev = query.dtype, query.get_device()
+    qs, ps = query.shape, key_pages.shape
+    i32 = torch.int32
+    return ((dtype is torch.bfloat16 or dtype is torch.float16) and dev >= 0
+            and key_pages.dtype is dtype and value_pages.dtype is dtype
+            and page_table.dtype is i32 and lengths.dtype is i32
+            and key_pages.get_device() == dev
+            and value_pages.get_device() == dev
+            and page_table.get_device() == dev and lengths.get_device() == dev
+            and len(qs) == 3 and len(ps) == 4 and value_pages.shape == ps
+            and ps[3] == qs[2] and qs[2] > 1
+            and page_table.dim() == 2 and page_table.shape[0] == qs[0]
+            and lengths.shape == qs[:1]
+            and query.stride(2) == 1 and key_pages.stride(3) == 1
+            and value_pages.stride(3) == 1 and page_table.stride(1) == 1
+            and lengths.stride(0) == 1
+            and (out is None or (
+                isinstance(out, t) and out.dtype is dtype
+                and out.get_device() == dev and out.shape == qs
+                and out.stride(2) == 1)))
 
 
 def paged_attention(query, key_pages, value_pages, page_table, lengths,
@@ -548,62 +634,35 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
     infinite scores, which propagate.
     """
     import torch
-    for name, x, dim in (("query", query, 3), ("key_pages", key_pages, 4)):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if x.dim() != dim:
-            raise ValueError(f"{name} must have {dim} dimensions")
+    given = (query, key_pages, value_pages, page_table, lengths)
+    if not _paged_ok(torch, *given, out):
+        _check_paged(*given, scale, out)
     dtype = query.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise TypeError("query must be a bfloat16 or float16 tensor")
-    dev = query.get_device()
-    qs, ps = query.shape, key_pages.shape
-    B, H, D = qs
-    pages, page_size, Hk, _ = ps
-    if ps[3] != D:
-        raise ValueError("key_pages and value_pages must both be "
-                         "[pages, page_size, kv_heads, d_head] with the "
-                         "query's d_head")
-    if H < 1 or Hk < 1 or H % Hk or page_size < 1:
-        raise ValueError("the query's heads must be a multiple of the "
-                         "pages', and page_size positive")
-    if D < 8 or D > 256 or D % 8:
-        raise ValueError("d_head must be a multiple of 8 in 8..256")
-    q = _rows("query", query, qs, dtype, dev, torch)
-    k = _rows("key_pages", key_pages, ps, dtype, dev, torch)
-    v = _rows("value_pages", value_pages, ps, dtype, dev, torch)
-    table = _index_rows("page_table", page_table, 2, B, dev, torch)
-    count = _index_rows("lengths", lengths, 1, B, dev, torch)
-    most = page_table.shape[1]
-    if B > 1 and table[0][0] < most:
-        raise ValueError("page_table's rows must not overlap")
-    if scale is None:
-        scale = D ** -0.5
-    elif not 0.0 < scale < _INF:
-        raise ValueError("scale must be positive and finite")
+    B, H, D = query.shape
+    pages, page_size, Hk, _ = key_pages.shape
     if out is None:
         out = torch.empty((B, H, D), dtype=dtype, device=query.device)
-        o = out.stride(), out.data_ptr()
-    else:
-        o = _rows("out", out, qs, dtype, dev, torch)
     lse = None
     if return_lse:
         lse = torch.empty((B, H), dtype=torch.float32, device=query.device)
     shape = _lib.pack_paged_shape(
-        B, H, Hk, D, page_size, pages, most,
-        1 if dtype is torch.float16 else 0, scale, q[0], o[0], k[0], v[0],
-        table[0][0])
-    size = cs_paged_attention_workspace(shape)
+        B, H, Hk, D, page_size, pages, page_table.shape[1],
+        1 if dtype is torch.float16 else 0,
+        D ** -0.5 if scale is None else scale, query.stride(), out.stride(),
+        key_pages.stride(), value_pages.stride(), page_table.stride(0))
+    size = max(cs_paged_attention_workspace(shape), 0)
     work = None
-    if size > 0:
+    if size:
         work = torch.empty(size, dtype=torch.uint8, device=query.device)
     with _on_device(query.device):
         st = cs_paged_attention(
-            q[1], k[1], v[1], table[1], count[1], o[1],
+            query.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
+            page_table.data_ptr(), lengths.data_ptr(), out.data_ptr(),
             lse.data_ptr() if return_lse else None, shape,
-            work.data_ptr() if work is not None else None, max(size, 0),
+            work.data_ptr() if size else None, size,
             _stream_handle(query.device))
     if st != 0:
+        _check_paged(*given, scale, out)
         raise CsError(st, "cs_paged_attention")
     return (out, lse) if return_lse else out
 
