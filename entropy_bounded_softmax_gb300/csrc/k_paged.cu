@@ -289,39 +289,45 @@ paged_kernel(const PagedTask t) {
         const int tiles = (p.t1 - p.t0 + kPgTile - 1) / kPgTile;
         return tiles > warp ? (tiles - warp + kPgWarps - 1) / kPgWarps : 0;
     };
-    // The page and slot of token (lane % 16) of this warp's tile i, -1 past
-    // the part, -2 for an entry that is no page; looked up one tile ahead.
-    int page, slot;
+    // The page and slot of token (lane % 16) of this warp's tile i; slot -1
+    // past the part.  Looked up two tiles before the copies that need them: a
+    // table's entry takes a microsecond to come when it is not in a cache.
+    struct Place {
+        int page, slot;
+    };
     auto locate = [&](const Part& p, int i) {
         const int tok = p.t0 + (warp + i * kPgWarps) * kPgTile + (lane & 15);
-        page = -1;
-        slot = 0;
+        Place at{0, -1};
         if (tok < p.t1) {
             const int e = tok / t.page_size;
-            slot = tok - e * t.page_size;
-            page = t.page_table[p.b * t.table_stride + e];
-            if (page < 0 || page >= t.num_pages) page = -2;
+            at.slot = tok - e * t.page_size;
+            at.page = t.page_table[p.b * t.table_stride + e];
         }
+        return at;
     };
-    // Starts the copies of the tile that was looked up into stage st: kUnits
+    Place soon, later;   // of the next tiles to copy
+    // Starts the copies of the tile at `where` into stage st: kUnits
     // 16-byte units a row, so 32 / kUnits rows at a time; zeros past d_head
     // and for tokens that are not there.
     constexpr int kUnits = DP / 8;
     const uint16_t* kbase = t.k_pages + hk * t.k_stride[2];
     const uint16_t* vbase = t.v_pages + hk * t.v_stride[2];
-    auto issue = [&](int st) {
+    auto issue = [&](const Place& where, int st) {
         unsigned char* dk = ring + st * 2 * L::kHalf;
         unsigned char* dv = dk + L::kHalf;
-        const uint32_t here = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+        const bool valid = where.page >= 0 && where.page < t.num_pages;
+        const int slot = valid ? where.slot : -1;
+        const uint32_t here = __ballot_sync(0xffffffffu, slot >= 0) & 0xffffu;
         if (lane == 0) live[st] = here;
-        if (__any_sync(0xffffffffu, page == -2) && lane == 0) raise_error(t.err, kBitBadPage);
+        if (__any_sync(0xffffffffu, where.slot >= 0 && !valid) && lane == 0)
+            raise_error(t.err, kBitBadPage);
 #pragma unroll
         for (int n = 0; n < kPgTile * kUnits / 32; ++n) {
             const int e = n * 32 + lane;
             const int r = e / kUnits, u = e % kUnits;
-            const int pg = __shfl_sync(0xffffffffu, page, r);
+            const int pg = __shfl_sync(0xffffffffu, where.page, r);
             const int sl = __shfl_sync(0xffffffffu, slot, r);
-            const bool copy = pg >= 0 && 8 * u < t.d_head;
+            const bool copy = sl >= 0 && 8 * u < t.d_head;
             const uint32_t bytes = copy ? 16u : 0u;   // 0: any address, not read
             const uint16_t* ks = kbase + pg * t.k_stride[0] + sl * t.k_stride[1] + 8 * u;
             const uint16_t* vs = vbase + pg * t.v_stride[0] + sl * t.v_stride[1] + 8 * u;
@@ -331,16 +337,17 @@ paged_kernel(const PagedTask t) {
         }
     };
 
-    // A part's first tiles; then the next to look up is kPgStages - 1.
+    // A part's first tiles.
     auto begin = [&](const Part& p) {
+        static_assert(kPgStages == 3, "two tiles under way, two looked up");
         const int mine = tiles_of(p);
-        locate(p, 0);
-#pragma unroll
-        for (int i = 0; i < kPgStages - 1; ++i) {
-            if (i < mine) issue(i);
-            cp_async_commit();
-            locate(p, i + 1);
-        }
+        const Place first = locate(p, 0), second = locate(p, 1);
+        soon = locate(p, 2);
+        later = locate(p, 3);
+        if (mine > 0) issue(first, 0);
+        cp_async_commit();
+        if (mine > 1) issue(second, 1);
+        cp_async_commit();
     };
     // Unit n (8 floats) of row r of warp w's output, at the end of a part:
     // units permuted within a row by its number, so that the rows' stores
@@ -385,9 +392,10 @@ paged_kernel(const PagedTask t) {
             cp_async_wait_group<kPgStages - 2>();
             __syncwarp();
             // Stage (i - 1) % kPgStages was read before the __syncwarp.
-            if (i + kPgStages - 1 < mine) issue((i + kPgStages - 1) % kPgStages);
+            if (i + kPgStages - 1 < mine) issue(soon, (i + kPgStages - 1) % kPgStages);
             cp_async_commit();
-            locate(now, i + kPgStages);
+            soon = later;
+            later = locate(now, i + kPgStages + 1);
 
             const uint32_t sk = smem_addr(ring + st * 2 * L::kHalf), sv = sk + L::kHalf;
             float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
