@@ -4,28 +4,29 @@
 // in one pass over the keys with the running m and l of a softmax: the
 // scores never leave the SM.
 //
-// A CTA takes tiles of 128 query rows of one head, and walks the keys in
-// blocks.  Tensor memory holds two buffers of scores (a block's columns each)
-// and each tile's output (DP columns); a tile's weights overwrite its scores
-// as bf16 and are the next product's A operand there.
-//   d_head > 64   two tiles in one CTA, blocks of 128 keys, a buffer a tile,
-//                 so that one tile's products run under the other's softmax.
-//                 K and V are read from shared memory and from L2 once for
-//                 both: that traffic bounds it;
-//   d_head <= 64  two CTAs of one tile on an SM, blocks of 64 keys, the
-//                 buffers for two blocks of it, so that its softmax need not
-//                 wait for products; the start and the end of one CTA,
-//                 microseconds that short sequences feel, run under the
-//                 other's work.
-// Roles of a CTA of T tiles, one mbarrier hand-off each:
-//   4 T warps  softmax, one row a thread: the maximum of the row's scores,
-//              2^(s c - m c) and the sum, the weights back to tensor memory;
-//              at the end the output, through shared memory;
-//   MMA warp   issues the products: for each block and tile P V, then a
-//              coming block's Q K^T into the columns P V has read;
-//   loader     tensor copies of Q, and of K and V into rings;
-//   mask warp  with a key mask only: a block's kept keys as bits, and zeros
-//              over the removed keys' rows of V.
+// A CTA takes two tiles of 128 query rows of one head and walks the keys in
+// blocks, so that one tile's products run under the other's softmax and both
+// use the same K and V.  Tensor memory holds each tile's scores (a block's
+// columns) and output (DP columns); a tile's weights overwrite its scores as
+// bf16 and are the next product's A operand there.
+//   d_head > 64   blocks of 128 keys, one CTA an SM.  Shared memory bounds it:
+//                 the products read 192 KB a pair of blocks and the copies
+//                 write 64, 2050 of its 3000 cycles;
+//   d_head <= 64  blocks of 64 keys, two CTAs an SM, which four tiles keep
+//                 busier (32 x 8 heads x 512: 24.6 us; two CTAs of one tile
+//                 with two score buffers 28.5, three of one tile 28.4, one of
+//                 two tiles and blocks of 128 35).
+// Roles, one mbarrier hand-off each:
+//   warps 0-3, 4-7  softmax of tile 0 and 1, one row a thread: the maximum of
+//                   the row's scores, 2^(s c - m c) and the sum, the weights
+//                   back to tensor memory; at the end the output, through
+//                   shared memory;
+//   warp 8          issues the products: for each block and tile P V, then the
+//                   next block's Q K^T into the columns P V has read (the
+//                   products of one thread execute in its order);
+//   warp 9          tensor copies of Q, and of K and V into rings;
+//   warp 10         with a key mask only: a block's kept keys as bits, and
+//                   zeros over the removed keys' rows of V.
 //
 // The weights are rounded to bf16, the type the tensor cores take next to
 // bf16 values; their sum is taken in fp32 before that.  m may lag the true
@@ -45,31 +46,33 @@ using namespace csd;
 
 constexpr float kRescaleBits = 8.0f;
 
+constexpr int kFwdThreads = 384;
+constexpr int kFwdMmaWarp = 8;
+constexpr int kFwdLoadWarp = 9;
+constexpr int kFwdMaskWarp = 10;
+
 template <int DP>
 struct FwdPlan {
-    static constexpr int kTiles = DP == 64 ? 1 : 2;
     static constexpr int kBlk = DP == 64 ? 64 : 128;      // keys of a block
     static constexpr int kCtasPerSm = DP == 64 ? 2 : 1;
     static constexpr uint32_t kTmemCols = DP == 64 ? 256 : 512;
-    // Blocks whose scores are computed ahead of the first block's weights.
-    static constexpr int kAhead = 2 / kTiles;
-    static constexpr int kMmaWarp = 4 * kTiles;
-    static constexpr int kLoadWarp = kMmaWarp + 1;
-    static constexpr int kMaskWarp = kMmaWarp + 2;
-    static constexpr int kThreads = 32 * (kMmaWarp + 4);
-    // Registers a thread with two tiles: 168 at launch; the softmax warps
-    // take what the others give up: 256 x 208 + 128 x 72 <= 384 x 168.
-    static constexpr int kRegsSoftmax = 208;
-    static constexpr int kRegsOther = 72;
+    // Registers a thread: 168 or, with two CTAs an SM, 80 at launch; the
+    // softmax warps take what the others give up: 256 x 208 + 128 x 72 <=
+    // 384 x 168, and 256 x 88 + 128 x 56 <= 384 x 80.
+    static constexpr int kRegsSoftmax = DP == 64 ? 88 : 208;
+    static constexpr int kRegsOther = DP == 64 ? 56 : 72;
+    // Scores a softmax thread holds: the whole row, or 32 at a time, read from
+    // tensor memory once for the maximum and once for the weights.
+    static constexpr int kChunk = DP == 64 ? 32 : 128;
     // Shared memory.
     static constexpr int kTile = 128 * DP * 2;            // of Q
     static constexpr int kBlock = kBlk * DP * 2;          // of K or V
-    static constexpr int kStages = DP == 64 ? 3 : 2;      // of K and of V
+    static constexpr int kStages = 2;                     // of K and of V
     static constexpr int kQ = 0;
-    static constexpr int kK = kQ + kTiles * kTile;
+    static constexpr int kK = kQ + 2 * kTile;
     static constexpr int kV = kK + kStages * kBlock;
     static constexpr int kBars = kV + kStages * kBlock;
-    static constexpr int kNumBars = 5 * kStages + 3 * kTiles + 4 + 1;
+    static constexpr int kNumBars = 5 * kStages + 4 * 2 + 1 + 2;
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages][4]
     static constexpr int kFlags = kWords + kStages * 16;  // abort, tmem
     static constexpr int kBytes = kFlags + 16 + 1024;     // and alignment slack
@@ -84,12 +87,12 @@ __device__ __forceinline__ void remove_columns(uint32_t (&s)[N], const uint32_t*
 }
 
 template <int DP>
-__global__ void __launch_bounds__(FwdPlan<DP>::kThreads, FwdPlan<DP>::kCtasPerSm)
+__global__ void __launch_bounds__(kFwdThreads, FwdPlan<DP>::kCtasPerSm)
 fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                  const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v) {
     using L = FwdPlan<DP>;
-    constexpr int NS = L::kStages, T = L::kTiles, BLK = L::kBlk, AHEAD = L::kAhead;
+    constexpr int NS = L::kStages, BLK = L::kBlk, CH = L::kChunk;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -98,12 +101,12 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     uint64_t* v_full = k_empty + NS;
     uint64_t* v_empty = v_full + NS;
     uint64_t* v_masked = v_empty + NS;        // [NS] removed rows zeroed, bits written
-    uint64_t* q_full = v_masked + NS;         // [T] tile's queries landed
-    uint64_t* s_full = q_full + T;            // [2] a buffer's scores
-    uint64_t* o_full = s_full + 2;            // [T] the block's P V completed
-    uint64_t* o_done = o_full + T;            // [T] the tile's last P V completed
-    uint64_t* drained = o_done + T;
-    uint64_t* p_full = drained + 1;           // [2] a buffer's weights, from four warps
+    uint64_t* q_full = v_masked + NS;         // [2] a tile's queries landed
+    uint64_t* s_full = q_full + 2;            // [2] its scores of a block
+    uint64_t* o_full = s_full + 2;            // [2] the block's P V completed
+    uint64_t* o_done = o_full + 2;            // [2] its last P V completed
+    uint64_t* drained = o_done + 2;
+    uint64_t* p_full = drained + 1;           // [2] its weights, from four warps
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
@@ -115,7 +118,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     const int qt = t.causal ? static_cast<int>(gridDim.z - 1 - blockIdx.z)
                             : static_cast<int>(blockIdx.z);
     const int hk = head_of(h, t.inv_group);
-    const int q0 = 128 * T * qt;
+    const int q0 = 256 * qt;
     const int off = t.key_len - t.query_len;   // row i keeps keys j <= i + off
 
     auto load_q = [&](int i) {
@@ -126,7 +129,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
 
     // The loader initialises the barriers, and starts its first copies before
     // the others have set up.
-    if (warp == L::kLoadWarp) {
+    if (warp == kFwdLoadWarp) {
         if (lane < L::kNumBars) mbar_init(bars + lane, bars + lane < p_full ? 1u : 4u);
         if (lane == 0) flags[0] = 0u;
         static_assert(L::kNumBars <= 32, "a lane a barrier");
@@ -140,7 +143,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             load_q(0);
         }
         __syncwarp();
-    } else if (warp == L::kMmaWarp) {
+    } else if (warp == kFwdMmaWarp) {
         tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
     }
     const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
@@ -152,7 +155,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     const int j0 = key_lo / BLK;
     int n[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int last = min(q0 + 128 * (i + 1), t.query_len) - 1;
         const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
         n[i] = last >= q0 + 128 * i && hi > key_lo ? (hi + BLK - 1) / BLK - j0 : 0;
@@ -170,31 +173,29 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         load_tile<BLK, DP>(smem + L::kV + st * L::kBlock, &map_v, (j0 + j) * BLK, hk, b,
                            &v_full[st]);
     };
-    // The buffer and the phase of its barriers for tile i's block j.
-    auto buffer = [&](int i, int j) { return T == 2 ? i : j & 1; };
-    auto phase = [&](int j) { return T == 2 ? j : j >> 1; };
     const int early = min(blocks, NS);
-    if (warp == L::kLoadWarp && lane == 0) {
+    if (warp == kFwdLoadWarp && lane == 0) {
         // In the order of their use.
         for (int j = 0; j < early; ++j) {
             load_k(j);
-            if (j == 0 && T == 2) load_q(1);
+            if (j == 0) load_q(1);
             load_v(j);
         }
-        if (early == 0 && T == 2) load_q(1);
+        if (early == 0) load_q(1);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = flags[1];
 
-    if (warp < 4 * T) {
+    if (warp < 8) {
         // -------------------------------------------------------- softmax
-        if (T == 2) take_registers<L::kRegsSoftmax>();
+        take_registers<L::kRegsSoftmax>();
         const int tile = warp >> 2;
         const int row0 = q0 + 128 * tile + 32 * (warp & 3);
         const int i = row0 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + BLK * tile;
         const uint32_t to = tmem + lanes + 2 * BLK + DP * tile;
         const float c = t.scale * kLog2e;
         // Keys below these limits are kept in every row of the warp, and in
@@ -205,9 +206,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         bool ok = true;
         const int nt = n[tile];
         for (int j = 0; j < nt; ++j) {
-            const int buf = buffer(tile, j);
-            const uint32_t ts = tmem + lanes + BLK * buf;
-            ok = warp_wait(&s_full[buf], phase(j), limit);
+            ok = warp_wait(&s_full[tile], j, limit);
             if (ok && mask) ok = warp_wait(&v_masked[j % NS], j / NS, limit);
             if (!ok) break;
             tc_fence_after_sync();
@@ -223,18 +222,24 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
                 for (int u = 0; u < BLK / 32; ++u) kept[u] &= bits_below(row_limit, key + 32 * u);
             }
-            uint32_t s[BLK];
+            uint32_t s[CH];
+            auto load = [&](int x) {
 #pragma unroll
-            for (int u = 0; u < BLK / 32; ++u) tmem_ld32_async(ts + 32 * u, s + 32 * u);
-            tmem_wait_ld<BLK>(s);
-            if (edge) remove_columns(s, kept);
+                for (int u = 0; u < CH / 32; ++u) tmem_ld32_async(ts + CH * x + 32 * u, s + 32 * u);
+                tmem_wait_ld<CH>(s);
+                if (edge) remove_columns(s, kept + CH / 32 * x);
+            };
             float mx[4] = {m, m, m, m};
 #pragma unroll
-            for (int k = 0; k < BLK; k += 8)
+            for (int x = 0; x < BLK / CH; ++x) {
+                load(x);
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    mx[y] = max3(mx[y], __uint_as_float(s[k + 2 * y]),
-                                 __uint_as_float(s[k + 2 * y + 1]));
+                for (int k = 0; k < CH; k += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mx[y] = max3(mx[y], __uint_as_float(s[k + 2 * y]),
+                                     __uint_as_float(s[k + 2 * y + 1]));
+            }
             const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
             if (j == 0) {
                 m = top;
@@ -242,8 +247,6 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 const float f = m == -INFINITY ? 0.0f : ex2((m - top) * c);
                 m = top;
                 l *= f;
-                // The product of block j - 2 has completed (block j's scores
-                // were issued after it), that of block j has not begun.
                 ok = warp_wait(&o_full[tile], j - 1, limit);
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -262,26 +265,30 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int k = 0; k < BLK / 2; ++k) {
-                const float2 y = fma2(make_float2(__uint_as_float(s[2 * k]),
-                                                  __uint_as_float(s[2 * k + 1])), c2, mc2);
-                const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                sum[k & 1] = add2(sum[k & 1], e);
-                s[k] = pack_bf16(e.x, e.y);
-            }
+            for (int x = 0; x < BLK / CH; ++x) {
+                if (CH < BLK) load(x);
 #pragma unroll
-            for (int u = 0; u < BLK / 64; ++u) tmem_st32(ts + 32 * u, s + 32 * u);
+                for (int k = 0; k < CH / 2; ++k) {
+                    const float2 y = fma2(make_float2(__uint_as_float(s[2 * k]),
+                                                      __uint_as_float(s[2 * k + 1])), c2, mc2);
+                    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                    sum[k & 1] = add2(sum[k & 1], e);
+                    s[k] = pack_bf16(e.x, e.y);
+                }
+                // (Over columns that this thread has read for good.)
+                if (CH == 32) tmem_st16(ts + 16 * x, s);
+#pragma unroll
+                for (int u = 0; u < CH / 64; ++u) tmem_st32(ts + CH / 2 * x + 32 * u, s + 32 * u);
+            }
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[buf]);
+            if (lane == 0) mbar_arrive(&p_full[tile]);
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
         }
         // The tile's queries are read (or, without blocks, have landed) before
         // the output is staged over them.
-        // (Not by o_full: a barrier tells a phase from the one before it only,
-        // and none, one or both of the last two products may have completed.)
         if (ok && nt > 0) ok = warp_wait(&o_done[tile], 0, limit);
         if (ok && nt == 0 && row0 < t.query_len) ok = warp_wait(&q_full[tile], 0, limit);
         if (ok && row0 < t.query_len) {
@@ -313,8 +320,8 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             }
         }
     } else {
-        if (T == 2) give_registers<L::kRegsOther>();
-        if (warp == L::kMmaWarp) {
+        give_registers<L::kRegsOther>();
+        if (warp == kFwdMmaWarp) {
             // ------------------------------------------------- MMA issuer
             const bool leader = elect_lane();
             const uint64_t q = tile_desc(smem_addr(smem + L::kQ));
@@ -322,49 +329,48 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             const uint64_t v = weights_desc<BLK>(smem_addr(smem + L::kV));
             constexpr uint32_t tile = L::kTile / 16, step = L::kBlock / 16;
             auto scores = [&](int i, int j) {
-                const int buf = buffer(i, j);
-                mma_tiles<BLK, DP>(tmem + BLK * buf, q + i * tile, k + (j % NS) * step, leader);
-                mma_commit(&s_full[buf], leader);
+                mma_tiles<BLK, DP>(tmem + BLK * i, q + i * tile, k + (j % NS) * step, leader);
+                mma_commit(&s_full[i], leader);
             };
             bool ok = true;
-            for (int j = 0; j < AHEAD && j < blocks && ok; ++j) {
-                ok = warp_wait(&k_full[j], 0, limit);
-                for (int i = 0; i < T && ok; ++i) {
-                    if (j >= n[i]) continue;
+            if (blocks > 0) {
+                ok = warp_wait(&k_full[0], 0, limit);
+                for (int i = 0; i < 2 && ok; ++i) {
+                    if (n[i] == 0) continue;
                     ok = warp_wait(&q_full[i], 0, limit);
-                    if (ok) scores(i, j);
+                    if (ok) scores(i, 0);
                 }
-                if (ok) mma_commit(&k_empty[j], leader);
+                if (ok) mma_commit(&k_empty[0], leader);
             }
             uint64_t* v_ready = mask ? v_masked : v_full;
             for (int j = 0; j < blocks && ok; ++j) {
-                const int st = j % NS, ja = j + AHEAD;
+                const int st = j % NS, next = (j + 1) % NS;
                 ok = warp_wait(&v_ready[st], j / NS, limit);
-                for (int i = 0; i < T && ok; ++i) {
+                for (int i = 0; i < 2 && ok; ++i) {
                     if (j >= n[i]) continue;
-                    const int buf = buffer(i, j);
-                    ok = warp_wait(&p_full[buf], phase(j), limit);
+                    ok = warp_wait(&p_full[i], j, limit);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    mma_weights<DP, BLK>(tmem + 2 * BLK + DP * i, tmem + BLK * buf, v + st * step,
+                    mma_weights<DP, BLK>(tmem + 2 * BLK + DP * i, tmem + BLK * i, v + st * step,
                                          j > 0, leader);
                     mma_commit(&o_full[i], leader);
-                    if (j + 1 == n[i]) mma_commit(&o_done[i], leader);
-                    if (ja < n[i]) {
-                        ok = warp_wait(&k_full[ja % NS], ja / NS, limit);
-                        if (ok) scores(i, ja);
+                    if (j + 1 == n[i]) {
+                        mma_commit(&o_done[i], leader);
+                    } else {
+                        ok = warp_wait(&k_full[next], (j + 1) / NS, limit);
+                        if (ok) scores(i, j + 1);
                     }
                 }
                 if (ok) {
                     mma_commit(&v_empty[st], leader);
-                    if (ja < blocks) mma_commit(&k_empty[ja % NS], leader);
+                    if (j + 1 < blocks) mma_commit(&k_empty[next], leader);
                 }
             }
             // No product may be in flight when the tensor memory is freed.
             mma_commit(drained, leader);
             mbar_wait<false>(drained, 0u, t.wait_limit_cycles);
             __syncwarp();
-        } else if (warp == L::kLoadWarp) {
+        } else if (warp == kFwdLoadWarp) {
             // ----------------------------------------------------- loader
             int k_issued = early, v_issued = early;
             for (int j = early; j < blocks; ++j) {
@@ -378,7 +384,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
             // A copy may still be in flight after an abort, or that of a tile
             // without blocks: none may land in shared memory after the CTA
             // exits (bounded waits).
-            for (int i = 0; i < T; ++i)
+            for (int i = 0; i < 2; ++i)
                 if (q0 + 128 * i < t.query_len) mbar_wait<false>(&q_full[i], 0u, t.wait_limit_cycles);
             if (*limit.abort_flag) {
                 for (int j = max(0, k_issued - NS); j < k_issued; ++j)
@@ -387,7 +393,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                     mbar_wait<false>(&v_full[j % NS], (j / NS) & 1, t.wait_limit_cycles);
             }
             __syncwarp();
-        } else if (warp == L::kMaskWarp && mask) {
+        } else if (warp == kFwdMaskWarp && mask) {
             // -------------------------------------------------- key masks
             for (int j = 0; j < blocks; ++j) {
                 const int st = j % NS;
@@ -401,7 +407,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == L::kMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
+    if (warp == kFwdMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
@@ -416,9 +422,8 @@ cudaError_t launch_fwd(const FattnTask& t, int slot, cudaStream_t stream) {
         !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, L::kBlk) ||
         !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, L::kBlk))
         return cudaErrorInvalidValue;
-    constexpr int kRows = 128 * L::kTiles;
-    const dim3 grid(t.heads, t.batch, (t.query_len + kRows - 1) / kRows);
-    fattn_fwd_kernel<DP><<<grid, L::kThreads, L::kBytes, stream>>>(
+    const dim3 grid(t.heads, t.batch, (t.query_len + 255) / 256);
+    fattn_fwd_kernel<DP><<<grid, kFwdThreads, L::kBytes, stream>>>(
         t, mq, mk, mv);
     return cudaGetLastError();
 }
