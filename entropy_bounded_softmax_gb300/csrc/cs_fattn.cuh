@@ -78,34 +78,44 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // What 16 rows of a panel add to a descriptor's address.
 constexpr uint32_t kDescRows16 = 16 * 128 / 16;
 
-// D[128 x N] = A . B^T on a tile of 128 rows and one of N (their descriptors).
+// D[128 x N] = A . B^T on a tile of 128 rows and one of N (their low descriptor
+// words), over the first 16 `steps` head elements: those past d_head are
+// zeros, and products with them would cost as much as others.
 template <int N, int DP>
-__device__ __forceinline__ void mma_tiles(uint32_t d, uint64_t a, uint64_t b, bool leader) {
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b, int steps,
+                                          bool leader) {
     constexpr uint32_t idesc = idesc_bf16(128, N, false);
-#pragma unroll
-    for (int ks = 0; ks < DP / 16; ++ks)
+    auto one = [&](int ks) {
         mma_bf16_ss(d, a + (ks >> 2) * (128 * 128 / 16) + (ks & 3) * (32 / 16),
                     b + (ks >> 2) * (N * 128 / 16) + (ks & 3) * (32 / 16), idesc, ks > 0, leader);
+    };
+    if (steps == DP / 16) {
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) one(ks);
+    } else {
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks) one(ks);
+    }
 }
 
-// D[128 x DP] (+)= W[128 x N] . B[N x DP] (N a multiple of 16), W bf16 in
-// tensor memory from column w, B from the row of a tile that b, its MN-major
-// descriptor, names.
-template <int DP, int N>
-__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t w, uint64_t b,
+// D[128 x 16 steps] (+)= W[128 x N] . B[N x 16 steps] (N a multiple of 16), W
+// bf16 in tensor memory from column w, B from the row of a tile that b, its
+// low descriptor word as MN-major operand, names; idesc: of that shape.
+// (Columns past 16 steps keep what they held.)
+template <int N>
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t w, uint32_t b, uint32_t idesc,
                                             bool accumulate, bool leader) {
-    constexpr uint32_t idesc = idesc_bf16(128, DP, true);
 #pragma unroll
     for (int ks = 0; ks < N / 16; ++ks)
         mma_bf16_ts(d, w + 8 * ks, b + ks * kDescRows16, idesc, accumulate || ks > 0, leader);
 }
 
-// The descriptors of a tile at shared address a: as an operand of mma_tiles,
-// and, of R rows, as B of mma_weights.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t a) { return smem_desc_sw128(a, 1024); }
+// The low descriptor words of a tile at shared address a: as an operand of
+// mma_tiles, and, of R rows, as B of mma_weights.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t a) { return desc_low(a, 0); }
 template <int R>
-__device__ __forceinline__ uint64_t weights_desc(uint32_t a) {
-    return smem_desc_mn_sw128(a, R * 128, 1024);
+__device__ __forceinline__ uint32_t weights_desc(uint32_t a) {
+    return desc_low(a, R * 128);
 }
 
 // Bits of the 32 columns from `base` that lie below `limit`.

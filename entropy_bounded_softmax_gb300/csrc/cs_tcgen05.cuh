@@ -134,19 +134,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t sbo
            (2ull << 61);
 }
 
-// Shared-memory matrix descriptor of an operand whose M or N elements are
-// contiguous ("MN-major"), in the 128-byte swizzled layout: atoms of 8 K rows
-// by 64 16-bit M or N elements (1024 bytes), lbo bytes between atoms
-// adjacent along M or N, sbo bytes between atoms adjacent along K.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo,
-                                                       uint32_t sbo) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
-           (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) |
-           (1ull << 46) |
-           (2ull << 61);
-}
-
 // Instruction descriptor of a dense kind::f16 MMA on bf16 operands with an
 // fp32 accumulator, M x N; A K-major, B K-major or (b_mn) MN-major.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
@@ -166,30 +153,42 @@ __device__ __forceinline__ bool elect_lane() {
     return r != 0;
 }
 
-// D[tmem] (+)= A[smem] . B[smem], K = 16.  Called by the whole warp, issued by
-// the lane where `leader` is true: the operands are then the same in every
-// lane and stay in uniform registers, where a branch around the call would
-// move each of them there for every instruction (an issuing thread that did
-// so took 97 to 150 cycles an instruction of 64).
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc,
-                                            uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate, bool leader) {
+// The low word of the descriptors of 128-byte swizzled operands whose 8-row
+// atoms lie 1024 bytes apart: the address, which steps by plain additions, and
+// the leading offset (bytes; K-major operands have none).  Their high word is
+// kDescHigh: the atoms' distance, this architecture's version, the swizzle.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+    return (saddr >> 4) | ((lbo ? lbo >> 4 : 1u) << 16);
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// D[tmem] (+)= A[smem] . B[smem], K = 16, of descriptors with these low words.
+// Called by the whole warp, issued by the lane where `leader` is true: the
+// operands are then the same in every lane and stay in uniform registers,
+// where a branch around the call would move each of them there for every
+// instruction (an issuing thread that did so took 97 to 150 cycles an
+// instruction of 64).
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low,
+                                            uint32_t idesc, bool accumulate, bool leader) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc),
-           "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u) : "memory");
+        "{\n .reg .pred p, q;\n .reg .b64 a, b;\n"
+        " setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
+        :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u),
+           "r"(leader ? 1u : 0u), "r"(kDescHigh) : "memory");
 }
 
 // The same with A in tensor memory: row m in lane m, two bf16 to a column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
-                                            uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate, bool leader) {
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low,
+                                            uint32_t idesc, bool accumulate, bool leader) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc),
-           "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u) : "memory");
+        "{\n .reg .pred p, q;\n .reg .b64 b;\n"
+        " setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " mov.b64 b, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
+        :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate ? 1u : 0u),
+           "r"(leader ? 1u : 0u), "r"(kDescHigh) : "memory");
 }
 
 // mma_commit by the leader of a warp that issues as mma_bf16_ss.

@@ -475,30 +475,32 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // ----------------------------------------------------- MMA issuer
         const bool leader = elect_lane();
         constexpr uint32_t step = L::kBlock / 16;
+        const int steps = (t.d_head + 15) / 16;
+        const uint32_t idesc = idesc_bf16(128, 16 * steps, true);
         const uint32_t b1 = smem_addr(smem + L::kB1), b2 = smem_addr(smem + L::kB2);
-        const uint64_t a1_t = tile_desc(smem_addr(smem + L::kA1));
-        const uint64_t a2_t = tile_desc(smem_addr(smem + L::kA2));
-        const uint64_t b1_t = tile_desc(b1), b1_w = weights_desc<BLK>(b1);
-        const uint64_t b2_t = tile_desc(b2), b2_w = weights_desc<BLK>(b2);
+        const uint32_t a1_t = tile_desc(smem_addr(smem + L::kA1));
+        const uint32_t a2_t = tile_desc(smem_addr(smem + L::kA2));
+        const uint32_t b1_t = tile_desc(b1), b1_w = weights_desc<BLK>(b1);
+        const uint32_t b2_t = tile_desc(b2), b2_w = weights_desc<BLK>(b2);
         uint64_t* ready1 = !KV && mask ? b1_masked : b1_full;
         // S of block i, G V^T of block i, once their tiles are there.
         auto scores = [&](int i) {
             if (!warp_wait(&ready1[i % N1], i / N1, limit)) return false;
-            mma_tiles<BLK, DP>(t_s, a1_t, b1_t + (i % N1) * step, leader);
+            mma_tiles<BLK, DP>(t_s, a1_t, b1_t + (i % N1) * step, steps, leader);
             mma_commit(s_full, leader);
             return true;
         };
         auto grads = [&](int i) {
             if (!warp_wait(&b2_full[i % N2], i / N2, limit)) return false;
-            mma_tiles<BLK, DP>(t_g(i), a2_t, b2_t + (i % N2) * step, leader);
+            mma_tiles<BLK, DP>(t_g(i), a2_t, b2_t + (i % N2) * step, steps, leader);
             mma_commit(&g_full[g_buf(i)], leader);
             if (!KV) mma_commit(&b2_empty[i % N2], leader);
             return true;
         };
         // A sum's product; each half's weights are where its scores were.
-        auto sums = [&](uint32_t d, uint32_t w, uint64_t b, bool accumulate) {
-            mma_weights<DP, CO>(d, w, b, accumulate, leader);
-            mma_weights<DP, CO>(d, w + CO, b + CO / 16 * kDescRows16, true, leader);
+        auto sums = [&](uint32_t d, uint32_t w, uint32_t b, bool accumulate) {
+            mma_weights<CO>(d, w, b, idesc, accumulate, leader);
+            mma_weights<CO>(d, w + CO, b + CO / 16 * kDescRows16, idesc, true, leader);
         };
         bool ok = blocks == 0 ||
                   (warp_wait(&a_full[0], 0, limit) && scores(0) &&

@@ -324,12 +324,14 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         if (warp == kFwdMmaWarp) {
             // ------------------------------------------------- MMA issuer
             const bool leader = elect_lane();
-            const uint64_t q = tile_desc(smem_addr(smem + L::kQ));
-            const uint64_t k = tile_desc(smem_addr(smem + L::kK));
-            const uint64_t v = weights_desc<BLK>(smem_addr(smem + L::kV));
+            const uint32_t q = tile_desc(smem_addr(smem + L::kQ));
+            const uint32_t k = tile_desc(smem_addr(smem + L::kK));
+            const uint32_t v = weights_desc<BLK>(smem_addr(smem + L::kV));
             constexpr uint32_t tile = L::kTile / 16, step = L::kBlock / 16;
+            const int steps = (t.d_head + 15) / 16;
+            const uint32_t idesc = idesc_bf16(128, 16 * steps, true);
             auto scores = [&](int i, int j) {
-                mma_tiles<BLK, DP>(tmem + BLK * i, q + i * tile, k + (j % NS) * step, leader);
+                mma_tiles<BLK, DP>(tmem + BLK * i, q + i * tile, k + (j % NS) * step, steps, leader);
                 mma_commit(&s_full[i], leader);
             };
             bool ok = true;
@@ -351,8 +353,8 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                     ok = warp_wait(&p_full[i], j, limit);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    mma_weights<DP, BLK>(tmem + 2 * BLK + DP * i, tmem + BLK * i, v + st * step,
-                                         j > 0, leader);
+                    mma_weights<BLK>(tmem + 2 * BLK + DP * i, tmem + BLK * i, v + st * step,
+                                     idesc, j > 0, leader);
                     mma_commit(&o_full[i], leader);
                     if (j + 1 == n[i]) {
                         mma_commit(&o_done[i], leader);
