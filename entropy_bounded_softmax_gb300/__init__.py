@@ -716,7 +716,7 @@ def _fused_attention_function():
         ok = (x.dim() == 4 and x.stride(3) == 1 and x.data_ptr() % 16 == 0
               and all(n <= 1 or (s > 0 and s % 8 == 0)
                       for n, s in zip(x.shape[:3], x.stride()[:3])))
-        return x if ok else x.contiguous()
+        return x if ok else x.clone(memory_format=torch.contiguous_format)
 
     class FusedAttentionFunction(torch.autograd.Function):
         """Autograd wrapper of :func:`fused_attention`: ``apply(query, keys,

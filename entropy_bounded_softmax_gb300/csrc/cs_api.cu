@@ -559,12 +559,33 @@ cs_status forward(const void* logits, bool in_bf16, float* out, int64_t batch,
 }
 
 // ------------------------------------------------------------ fused attention
+// Whether rows of d elements at these strides (n <= 3 dimensions, more than
+// one element each or not looked at) can share an element: unless each stride,
+// in ascending order, steps past all that the smaller ones span.  (Orders that
+// interleave without sharing any are refused with them.)
+bool overlaps_itself(const int64_t* dim, const int64_t* stride, int n, int32_t d) {
+    int64_t span = d;
+    int taken = 0;
+    for (int round = 0; round < n; ++round) {
+        int next = -1;   // the smallest stride not taken
+        for (int i = 0; i < n; ++i)
+            if (dim[i] > 1 && !(taken >> i & 1) && (next < 0 || stride[i] < stride[next]))
+                next = i;
+        if (next < 0) break;
+        taken |= 1 << next;
+        if (stride[next] < span) return true;
+        span += (dim[next] - 1) * stride[next];
+    }
+    return false;
+}
+
 // Sizes and strides of one [batch, heads, length, d_head] bf16 tensor: the
 // bytes from its first to past its last element, or -1 when a stride is
 // refused (negative, not a multiple of 8 elements, or 0 over more than one
-// element; strides of dimensions of one element are not looked at).
+// element; strides of dimensions of one element are not looked at; of a
+// written tensor also strides that may share elements).
 int64_t heads_extent(const cs_attention_shape& s, int32_t heads, int32_t length,
-                     const int64_t* stride) {
+                     const int64_t* stride, bool written = false) {
     const int64_t dim[3] = {s.batch, heads, length};
     int64_t last = s.d_head;
     for (int i = 0; i < 3; ++i) {
@@ -579,6 +600,7 @@ int64_t heads_extent(const cs_attention_shape& s, int32_t heads, int32_t length,
         last += (dim[i] - 1) * stride[i];
         if (last > (int64_t(1) << 60)) return -1;
     }
+    if (written && overlaps_itself(dim, stride, 3, s.d_head)) return -1;
     return 2 * last;
 }
 
@@ -1265,7 +1287,7 @@ cs_status cs_check_fused_attention_args(const uint16_t* query,
         {keys, heads_extent(s, s.kv_heads, s.key_len, s.k_stride), 16, false},
         {values, heads_extent(s, s.kv_heads, s.key_len, s.v_stride), 16, false},
         {mask, mask_extent(s, mask), 1, false},
-        {out, heads_extent(s, s.heads, s.query_len, s.o_stride), 16, true},
+        {out, heads_extent(s, s.heads, s.query_len, s.o_stride, true), 16, true},
         {lse, lse ? rows * 4 : 0, 4, true}};
     return check_spans(spans, 6);
 }
@@ -1322,9 +1344,9 @@ cs_status cs_check_fused_attention_backward_args(
         {grad_out, heads_extent(s, s.heads, s.query_len, s.go_stride), 16, false},
         {lse, rows * 4, 4, false},
         {mask, mask_extent(s, mask), 1, false},
-        {grad_query, heads_extent(s, s.heads, s.query_len, s.dq_stride), 16, true},
-        {grad_keys, heads_extent(s, s.kv_heads, s.key_len, s.dk_stride), 16, true},
-        {grad_values, heads_extent(s, s.kv_heads, s.key_len, s.dv_stride), 16, true},
+        {grad_query, heads_extent(s, s.heads, s.query_len, s.dq_stride, true), 16, true},
+        {grad_keys, heads_extent(s, s.kv_heads, s.key_len, s.dk_stride, true), 16, true},
+        {grad_values, heads_extent(s, s.kv_heads, s.key_len, s.dv_stride, true), 16, true},
         {workspace, need, 16, true}};
     return check_spans(spans, 11);
 }
@@ -1386,8 +1408,6 @@ cs_status cs_check_paged_attention_args(
     const int64_t need = cs_paged_attention_workspace(shape);
     if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
     if (s.batch > 1 && s.table_stride < s.max_pages) return CS_ERR_INVALID_ARG;
-    if (s.o_stride[0] == 0 && s.batch > 1) return CS_ERR_INVALID_ARG;
-    if (s.o_stride[1] == 0 && s.heads > 1) return CS_ERR_INVALID_ARG;
     const int64_t rows[2] = {s.batch, s.heads};
     const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
     const int64_t table = s.max_pages == 0 ? 0
@@ -1401,6 +1421,8 @@ cs_status cs_check_paged_attention_args(
         {out, strided_extent(rows, s.o_stride, 2, s.d_head), 16, true},
         {lse, lse ? 4 * static_cast<int64_t>(s.batch) * s.heads : 0, 4, true},
         {workspace, need, 16, true}};
+    if (spans[5].bytes > 0 && overlaps_itself(rows, s.o_stride, 2, s.d_head))
+        return CS_ERR_INVALID_ARG;
     return check_spans(spans, 8);
 }
 

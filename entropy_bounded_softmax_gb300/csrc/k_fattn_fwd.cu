@@ -11,7 +11,8 @@
 // bf16 and are the next product's A operand there.
 //   d_head > 64   blocks of 128 keys, one CTA an SM.  Shared memory bounds it:
 //                 the products read 192 KB a pair of blocks and the copies
-//                 write 64, 2050 of its 3000 cycles;
+//                 write 64, 2050 of its 3000 cycles (2 x 8 heads x 4096 of
+//                 128, causal: 52 us, 1.3 PFLOP/s);
 //   d_head <= 64  blocks of 64 keys, two CTAs an SM, which four tiles keep
 //                 busier (32 x 8 heads x 512: 24.6 us; two CTAs of one tile
 //                 with two score buffers 28.5, three of one tile 28.4, one of
@@ -294,6 +295,7 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         if (ok && row0 < t.query_len) {
             tc_fence_after_sync();
             const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
+            const bool some_empty = __any_sync(0xffffffffu, l == 0.0f);
             unsigned char* stage = smem + L::kQ + tile * L::kTile;
             const int r = 32 * (warp & 3);
             const int64_t row = (static_cast<int64_t>(b) * t.heads + h) * t.query_len + i;
@@ -305,6 +307,12 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 if (nt > 0) {
                     tmem_ld32_async(to + 32 * u, o);
                     tmem_wait_ld<32>(o);
+                }
+                // Exactly 0 without kept keys, whatever a value that only
+                // `causal` removes holds (0 times its NaN is NaN).
+                if (some_empty) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0u : o[k];
                 }
                 stage_row32(stage, r + lane, 32 * u, o, inv);
             }

@@ -24,6 +24,11 @@
 // sequence can be longer than four steps every CTA takes one whole row of one
 // sequence, and there is no second kernel.
 //
+// Measured with 8 key heads of 128 in bf16: 83 us for 32 query heads of 131072
+// tokens (6.4 TB/s of the cache, DRAM 84% busy), 41 us for 32 sequences of up
+// to 4096 tokens (4.9 TB/s; the start of the copies, 5 us, and the join, 3,
+// do not overlap with them), 4.3 us for a call of few tokens.
+//
 // The weights enter the second product as two halves of the cache's type,
 // the nearest value and the nearest to the rest, so that their rounding
 // (2^-16 in bf16) stays below the result's.  They carry a factor 2^8: fp16
@@ -223,8 +228,10 @@ __device__ __forceinline__ bool deal(const PagedTask& t, int grp, int* scan, int
         __syncthreads();
         if (done > g0) break;
     }
-    b = scan[kPgWarps];
-    base = scan[kPgWarps + 1];
+    // (In range even where the lengths were changed under the call: what it
+    // returns is then wrong, but no walk leaves the batch.)
+    b = max(0, min(scan[kPgWarps], t.batch - 1));
+    base = min(scan[kPgWarps + 1], g0);
     return true;
 }
 
@@ -265,6 +272,7 @@ paged_kernel(const PagedTask t) {
         int s0 = 0, s1 = steps;
         if (t.split) {
             while (g >= base + steps) {   // (sequences without tokens too)
+                if (b + 1 >= t.batch) return false;
                 base += steps;
                 len = length_of(t, ++b, bad);
                 steps = steps_of(len);
@@ -555,10 +563,10 @@ paged_join_kernel(const PagedTask t) {
     const int steps = steps_of(length_of(t, b, bad));
     const int share = share_of(t, steps_before(t, t.batch, scan));
     const int begin = steps_before(t, b, scan);
-    const int c0 = begin / share, c1 = (begin + steps - 1) / share;
+    const int c0 = begin / share, c1 = min((begin + steps - 1) / share, t.groups - 1);
     wait_for_previous_kernel();
     // Without steps, or finished by the only group that had it.
-    if (steps == 0 || c0 == c1) return;
+    if (steps == 0 || c0 >= c1) return;
     const int group = t.heads / t.kv_heads;
     const int hk = h / group, hh = h - hk * group;
     const int rows = t.kv_heads * t.head_tiles, row = hk * t.head_tiles + hh / 16;

@@ -528,7 +528,9 @@ typedef struct cs_attention_shape {
  *   out_i = sum_j e^(s_j - lse_i) value_j
  *
  * query, keys, values, out   device pointers, 16-byte aligned; out is written
- *          completely and must not overlap the inputs or lse.
+ *          completely and must not overlap the inputs or lse (from its first
+ *          to its last byte) or itself: each of its strides, in ascending
+ *          order, steps past what the smaller ones span.
  * lse      optional device pointer, [batch, heads, query_len] fp32,
  *          contiguous: what the backward takes.
  * mask     optional device pointer, [batch, key_len] bytes: 0 removes the
@@ -541,8 +543,9 @@ typedef struct cs_attention_shape {
  * values, and out is rounded once.  NaN or infinite scores of kept keys
  * propagate by IEEE arithmetic and OR CS_ERR_NAN_INPUT into the error word.
  * A value that is NaN or infinite propagates to every query of its block of
- * 128 keys, those that only `causal` keeps from it included (0 times it is
- * NaN).
+ * 128 keys that has keys, those that only `causal` keeps from it included (0
+ * times it is NaN); in the backward so does such a key, query or grad_out row.
+ * A query whose kept scores are all -infinite counts as one without keys.
  *
  * The tensor cores take the products (tcgen05.mma); see cs_check_* for what
  * is refused.  Ownership, execution and errors: as cs_constrained_softmax.
@@ -571,7 +574,8 @@ cs_status cs_fused_attention(const uint16_t* query, const uint16_t* keys,
  * workspace  device pointer, 16-byte aligned, at least
  *          cs_fused_attention_backward_workspace(shape) bytes: the caller's,
  *          written and read by this call only, free after it on the stream.
- * The gradients must not overlap each other, the inputs or the workspace.
+ * The gradients must not overlap each other, themselves, the inputs or the
+ * workspace (as out above).
  * Everything else: as cs_fused_attention.
  */
 cs_status cs_fused_attention_backward(
@@ -631,10 +635,11 @@ typedef struct cs_paged_shape {
  *   out = sum_j e^(s_j - lse) value_j
  *
  * query    device pointer, [batch, heads, d_head]; out the same, written
- *          completely, overlapping nothing else of the call.
+ *          completely, overlapping nothing else of the call, nor itself.
  * key_pages, value_pages  device pointers.  All four 16-byte aligned.
  * page_table  device pointer, int32.  Entries past a sequence's length are
- *          not read, nor are a page's slots past it.
+ *          not read, nor are a page's slots past it.  An infinite value may
+ *          give NaN instead of infinity (0 times it is added).
  * lengths  device pointer, [batch] int32: tokens in the cache, the new one's
  *          included when it has been written there.  0 gives zeros and
  *          lse = -inf.

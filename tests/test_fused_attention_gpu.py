@@ -383,3 +383,57 @@ def test_repeated_calls_agree(case):
     torch.cuda.synchronize()
     assert int(differ) == 0
     assert cs.get_error() == set()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_without_keys_stay_zero_beside_nan(D):
+    """Queries 0..39 keep no key; the keys and values that others of their
+    block keep hold NaN, which 0 weights would carry over to them."""
+    q, k, v, g, _, _ = inputs((1, 2, 1, 100, 60, D, True, None))
+    v[0, 0, 5] = math.nan
+    k[0, 0, 5] = math.nan
+    out, lse = cs.fused_attention(q, k, v, causal=True, return_lse=True)
+    assert (out[:, :, :40] == 0).all() and (lse[:, :, :40] == -math.inf).all()
+    dq, _, _ = cs.fused_attention_backward(q, k, v, out, lse, g, causal=True)
+    assert (dq[:, :, :40] == 0).all()
+    assert out[:, :, 45:].isnan().all()
+    assert cs.get_error() == {"NAN_INPUT"}
+
+
+def test_autograd_takes_an_odd_base():
+    """A contiguous input whose base is not 16-byte aligned is copied."""
+    q, k, v, g, _, _ = inputs((1, 2, 2, 40, 50, 64, False, None))
+    store = torch.empty(q.numel() + 1, dtype=torch.bfloat16, device="cuda")
+    odd = store[1:].view(q.shape).copy_(q).requires_grad_()
+    assert odd.data_ptr() % 16 != 0
+    out = cs.FusedAttentionFunction.apply(odd, k, v)
+    out.backward(g)
+    want, lse = cs.fused_attention(q, k, v, return_lse=True)
+    dq, _, _ = cs.fused_attention_backward(q, k, v, want, lse, g)
+    assert torch.equal(out, want) and torch.equal(odd.grad, dq)
+
+
+def test_outputs_that_overlap_themselves_are_refused():
+    q, k, v, _, _, _ = inputs((2, 4, 2, 20, 30, 64, False, None))
+    store = torch.empty(2 * 4 * 20 * 64, dtype=torch.bfloat16, device="cuda")
+    out = store.as_strided((2, 4, 20, 64), (4 * 20 * 64, 20 * 64, 32, 1))
+    with pytest.raises(cs.CsError):
+        cs.fused_attention(q, k, v, out=out)
+
+
+def test_no_queries_behind_work_that_allows_overlap():
+    """Gradients of keys without queries, in memory that the kernels before
+    still use: the call may not start before they end."""
+    k = torch.randn(1, 2, 4096, 64, device="cuda").bfloat16()
+    q = k[:, :, :0]
+    lse = torch.empty(1, 2, 0, device="cuda")
+    qp = torch.randn(4, 8, 128, device="cuda").bfloat16()
+    pages = torch.randn(4096, 16, 8, 128, device="cuda").bfloat16()
+    table = torch.arange(4096, dtype=torch.int32, device="cuda").view(4, 1024)
+    lengths = torch.full((4,), 16384, dtype=torch.int32, device="cuda")
+    want = cs.paged_attention(qp, pages, pages, table, lengths)
+    for _ in range(5):
+        got = cs.paged_attention(qp, pages, pages, table, lengths)
+        _, dk, dv = cs.fused_attention_backward(q, k, k, q, lse, q)
+        assert torch.equal(got, want)
+        assert (dk == 0).all() and (dv == 0).all()

@@ -244,3 +244,20 @@ def test_reference_gradients_by_differences(causal):
                 sides.append(loss(*y))
             slope = (sides[0] - sides[1]) / (2 * step)
             assert abs(slope - float(grad[tuple(at)])) < 1e-8
+
+
+def test_written_tensors_do_not_overlap_themselves():
+    sbhd = (64, 2 * 64, 2 * 2 * 64)            # [S, H, B, D] storage
+    assert check(shape(H=2, Hk=2, o=sbhd)) == OK
+    packed = (16 * 3 * 4 * 64, 64, 3 * 4 * 64)   # one of three in a row
+    assert check(shape(o=packed)) == OK
+    assert check(shape(o=(4096, 1024, 56))) == BAD     # rows into each other
+    assert check(shape(o=(4096, 960, 64))) == BAD      # heads
+    assert check(shape(o=(64, 64, 256))) == BAD        # the same address twice
+    assert check(shape(B=1, o=(0, 1024, 64))) == OK
+    assert check(shape(q=(4096, 960, 64))) == OK       # an input may
+    for name in ("dq", "dk", "dv"):
+        assert backward(shape(**{name: (4096, 1024, 56)})) == BAD
+    assert check_paged(paged(o=(512, 56))) == BAD
+    assert check_paged(paged(o=(448, 64))) == BAD
+    assert check_paged(paged(o=(64, 128))) == OK       # [H, B, D] storage
