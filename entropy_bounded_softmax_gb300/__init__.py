@@ -10,6 +10,11 @@ softmax of attention scores.  The backward
 with respect to the logits; :class:`ConstrainedSoftmaxFunction` joins the two
 for autograd.
 
+Attention of language models: :func:`fused_attention` (softmax(scale q k^T) v
+without the scores in memory), :func:`fused_attention_backward`, joined for
+autograd by :class:`FusedAttentionFunction`, and :func:`paged_attention` (one
+new token per sequence over a key-value cache in pages).
+
 PyTorch supplies device memory and the current stream; the computation runs
 in the hand-written CUDA kernels of ``libcsoftmax.so`` behind a C ABI
 (``include/entropy_bounded_softmax.h``).  There is no CPU path: the calls
