@@ -58,14 +58,16 @@ __device__ __forceinline__ void give_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 
-// The box copies of one R x DP tile whose first row is `row` (R: rows of the
-// map's box).
-template <int R, int DP>
+// The box copies of one R x DP tile whose first row is `row` (BOX: rows of the
+// map's box, a divisor of R).
+template <int R, int DP, int BOX = R>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const void* tmap, int row,
                                           int head, int batch, uint64_t* bar) {
 #pragma unroll
     for (int p = 0; p < DP / 64; ++p)
-        tma_load_4d(dst + p * R * 128, tmap, 64 * p, row, head, batch, bar);
+#pragma unroll
+        for (int r = 0; r < R; r += BOX)
+            tma_load_4d(dst + (p * R + r) * 128, tmap, 64 * p, row + r, head, batch, bar);
 }
 
 // The largest of three (NaN operands are passed over, as by fmaxf).

@@ -177,7 +177,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 prefetch_tmap(&map_b2);
             }
             mbar_arrive_expect_tx(&a_full[0], L::kTile);
-            load_tile<128, DP>(smem + L::kA1, &map_a1, a0, ha, b, &a_full[0]);
+            load_tile<128, DP, BLK>(smem + L::kA1, &map_a1, a0, ha, b, &a_full[0]);
         }
         __syncwarp();
     } else if (warp == kBwdMmaWarp) {
@@ -246,10 +246,10 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // In the order of their use: the first S, the first G V^T.
         if (blocks > 0) load1(0, at1);
         mbar_arrive_expect_tx(&a_full[1], L::kTile);
-        load_tile<128, DP>(smem + L::kA2, &map_a2, a0, ha, b, &a_full[1]);
+        load_tile<128, DP, BLK>(smem + L::kA2, &map_a2, a0, ha, b, &a_full[1]);
         if (!KV) {
             mbar_arrive_expect_tx(o_full, L::kTile);
-            load_tile<128, DP>(smem + L::kOut, &map_o, a0, ha, b, o_full);
+            load_tile<128, DP, BLK>(smem + L::kOut, &map_o, a0, ha, b, o_full);
         }
         if (blocks > 0) load2(0, at2);
     }
@@ -598,17 +598,6 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
-// The maps of the four inputs for one box height.
-struct InputMaps {
-    CUtensorMap q, g, k, v;
-    bool encode(const FattnTask& t, int rows) {
-        return encode_heads_map(&q, t.q, t, t.heads, t.query_len, t.q_stride, rows) &&
-               encode_heads_map(&g, t.go, t, t.heads, t.query_len, t.go_stride, rows) &&
-               encode_heads_map(&k, t.k, t, t.kv_heads, t.key_len, t.k_stride, rows) &&
-               encode_heads_map(&v, t.v, t, t.kv_heads, t.key_len, t.v_stride, rows);
-    }
-};
-
 template <int DP>
 cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
     using L = BwdPlan<DP>;
@@ -620,17 +609,20 @@ cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
         e = ensure_smem_attribute(reinterpret_cast<const void*>(fattn_bwd_kernel<DP, true>),
                                   slot + 1, smem, false);
     if (e != cudaSuccess) return e;
-    // Fixed tiles of 128 rows, streamed blocks of kBlk.
-    InputMaps fixed, streamed;
-    CUtensorMap out;
-    if (!fixed.encode(t, 128) || (L::kBlk != 128 && !streamed.encode(t, L::kBlk)) ||
-        !encode_heads_map(&out, t.out, t, t.heads, t.query_len, t.o_stride, 128))
+    // Boxes of a block's rows; fixed tiles of 128 rows are two of them where
+    // blocks are 64.
+    CUtensorMap q, g, k, v, out;
+    constexpr int kBox = L::kBlk;
+    if (!encode_heads_map(&q, t.q, t, t.heads, t.query_len, t.q_stride, kBox) ||
+        !encode_heads_map(&g, t.go, t, t.heads, t.query_len, t.go_stride, kBox) ||
+        !encode_heads_map(&k, t.k, t, t.kv_heads, t.key_len, t.k_stride, kBox) ||
+        !encode_heads_map(&v, t.v, t, t.kv_heads, t.key_len, t.v_stride, kBox) ||
+        !encode_heads_map(&out, t.out, t, t.heads, t.query_len, t.o_stride, kBox))
         return cudaErrorInvalidValue;
-    const InputMaps& blocks = L::kBlk == 128 ? fixed : streamed;
     if (t.query_len > 0) {
         const dim3 grid(t.heads, t.batch, (t.query_len + 127) / 128);
         fattn_bwd_kernel<DP, false><<<grid, kBwdThreads, smem, stream>>>(
-            t, fixed.q, fixed.g, blocks.k, blocks.v, out);
+            t, q, g, k, v, out);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && t.key_len > 0) {
@@ -640,10 +632,10 @@ cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
         // memory, has ended.
         if (t.query_len > 0) {
             e = launch_overlapped(fattn_bwd_kernel<DP, true>, grid, kBwdThreads, smem, stream, t,
-                                  fixed.k, fixed.v, blocks.q, blocks.g, out);
+                                  k, v, q, g, out);
         } else {
             fattn_bwd_kernel<DP, true><<<grid, kBwdThreads, smem, stream>>>(
-                t, fixed.k, fixed.v, blocks.q, blocks.g, out);
+                t, k, v, q, g, out);
             e = cudaGetLastError();
         }
     }
