@@ -119,8 +119,9 @@ struct PgSmem {
     // in the others.
     static constexpr int kOut = (kPgStages - 1) * 2 * kHalf;
     static constexpr int kStats = kRing;                      // [warps][16] float2
-    static constexpr int kLive = kStats + kPgWarps * 16 * 8;  // [warps][stages] bits
-    static constexpr int kScan = kLive + kPgWarps * kPgStages * 4;   // [kPgWarps + 4]
+    // [warps][2][16]: where a tile's tokens have their keys and values.
+    static constexpr int kRows = kStats + kPgWarps * 16 * 8;
+    static constexpr int kScan = kRows + kPgWarps * 2 * 16 * 16;     // [kPgWarps + 4]
     static constexpr int kBytes = kScan + (kPgWarps + 4) * 4;
     static_assert(16 * DP * 4 <= 2 * kHalf, "an output fits a stage");
 };
@@ -290,72 +291,98 @@ paged_kernel(const PagedTask t) {
     };
 
     unsigned char* ring = smem + warp * L::kWarp;
-    volatile uint32_t* live =
-        reinterpret_cast<uint32_t*>(smem + L::kLive) + warp * kPgStages;
+    ulonglong2* rows_of = reinterpret_cast<ulonglong2*>(smem + L::kRows) + warp * 2 * 16;
     // A part's tiles that are this warp's.
     auto tiles_of = [&](const Part& p) {
         const int tiles = (p.t1 - p.t0 + kPgTile - 1) / kPgTile;
         return tiles > warp ? (tiles - warp + kPgWarps - 1) / kPgWarps : 0;
     };
-    // The page and slot of token (lane % 16) of this warp's tile i; slot -1
-    // past the part.  Looked up two tiles before the copies that need them: a
-    // table's entry takes a microsecond to come when it is not in a cache.
+    // A tile's way, in this warp (lanes 16 to 31 as the 16 before): its tokens'
+    // pages are looked up (locate), a table's entry takes a microsecond to come
+    // when it is not in a cache; the addresses of their rows are left in shared
+    // memory (aim) an iteration later; its copies start (issue) in the next,
+    // and two iterations later it is used.  Every lane working out the
+    // addresses that it copies from took 980 cycles of a tile's 2000.
     struct Place {
-        int page, slot;
+        int page, slot;   // slot -1: no token
     };
-    auto locate = [&](const Part& p, int i) {
-        const int tok = p.t0 + (warp + i * kPgWarps) * kPgTile + (lane & 15);
+    // The next token to look up, its entry of the table and its slot.
+    int tok = 0, entry = 0, slot = 0;
+    const int skip = kPgStep / t.page_size, rest = kPgStep - skip * t.page_size;
+    auto locate = [&](const Part& p) {
         Place at{0, -1};
         if (tok < p.t1) {
-            const int e = tok / t.page_size;
-            at.slot = tok - e * t.page_size;
-            at.page = t.page_table[p.b * t.table_stride + e];
+            at.slot = slot;
+            at.page = t.page_table[p.b * t.table_stride + entry];
+        }
+        tok += kPgStep;
+        entry += skip;
+        slot += rest;
+        if (slot >= t.page_size) {
+            slot -= t.page_size;
+            ++entry;
         }
         return at;
     };
-    Place soon, later;   // of the next tiles to copy
-    // Starts the copies of the tile at `where` into stage st: kUnits
-    // 16-byte units a row, so 32 / kUnits rows at a time; zeros past d_head
-    // and for tokens that are not there.
-    constexpr int kUnits = DP / 8;
+    constexpr int kUnits = DP / 8;     // 16-byte units of a row
     const uint16_t* kbase = t.k_pages + hk * t.k_stride[2];
     const uint16_t* vbase = t.v_pages + hk * t.v_stride[2];
-    auto issue = [&](const Place& where, int st) {
+    // Leaves the rows' addresses in table `buf`; the tokens that are there, one
+    // bit each.  (A __syncwarp before the copies.)
+    auto aim = [&](const Place& where, int buf) {
+        const bool valid = where.slot >= 0 && where.page >= 0 && where.page < t.num_pages;
+        if (where.slot >= 0 && !valid) raise_error(t.err, kBitBadPage);
+        const uint16_t *k = t.q, *v = t.q;
+        if (valid) {
+            k = kbase + where.page * t.k_stride[0] + where.slot * t.k_stride[1];
+            v = vbase + where.page * t.v_stride[0] + where.slot * t.v_stride[1];
+        }
+        if (lane < 16)
+            rows_of[16 * buf + lane] = make_ulonglong2(reinterpret_cast<uintptr_t>(k),
+                                                       reinterpret_cast<uintptr_t>(v));
+        return __ballot_sync(0xffffffffu, valid) & 0xffffu;
+    };
+    // Starts a tile's copies into stage st: 32 / kUnits rows at a time; zeros
+    // past d_head and for tokens that are not there.
+    const int unit = lane % kUnits;
+    const bool in_head = 8 * unit < t.d_head;
+    const uint32_t at_unit = in_head ? 16 * unit : 0;
+    auto issue = [&](uint32_t there, int buf, int st) {
         unsigned char* dk = ring + st * 2 * L::kHalf;
         unsigned char* dv = dk + L::kHalf;
-        const bool valid = where.page >= 0 && where.page < t.num_pages;
-        const int slot = valid ? where.slot : -1;
-        const uint32_t here = __ballot_sync(0xffffffffu, slot >= 0) & 0xffffu;
-        if (lane == 0) live[st] = here;
-        if (__any_sync(0xffffffffu, where.slot >= 0 && !valid) && lane == 0)
-            raise_error(t.err, kBitBadPage);
 #pragma unroll
         for (int n = 0; n < kPgTile * kUnits / 32; ++n) {
-            const int e = n * 32 + lane;
-            const int r = e / kUnits, u = e % kUnits;
-            const int pg = __shfl_sync(0xffffffffu, where.page, r);
-            const int sl = __shfl_sync(0xffffffffu, slot, r);
-            const bool copy = sl >= 0 && 8 * u < t.d_head;
-            const uint32_t bytes = copy ? 16u : 0u;   // 0: any address, not read
-            const uint16_t* ks = kbase + pg * t.k_stride[0] + sl * t.k_stride[1] + 8 * u;
-            const uint16_t* vs = vbase + pg * t.v_stride[0] + sl * t.v_stride[1] + 8 * u;
-            const int at = r * L::kRow + ((u ^ (r & 7)) << 4);
-            cp_async16_zfill(dk + at, copy ? ks : t.q, bytes);
-            cp_async16_zfill(dv + at, copy ? vs : t.q, bytes);
+            const int r = n * (32 / kUnits) + lane / kUnits;
+            const ulonglong2 row = rows_of[16 * buf + r];
+            const uint32_t bytes = in_head && (there >> r & 1u) ? 16u : 0u;
+            const int at = r * L::kRow + ((unit ^ (r & 7)) << 4);
+            cp_async16_zfill(dk + at, reinterpret_cast<const void*>(row.x + at_unit), bytes);
+            cp_async16_zfill(dv + at, reinterpret_cast<const void*>(row.y + at_unit), bytes);
         }
     };
 
-    // A part's first tiles.
+    // A part's first tiles.  From then on, before tile i: its tokens that are
+    // there in here0, the next tile's in here1, and those of tile i + 2, aimed
+    // in table i % 2, in here2; tile i + 3 is `soon`.
+    uint32_t here0 = 0, here1 = 0, here2 = 0;
+    Place soon{0, -1};
     auto begin = [&](const Part& p) {
-        static_assert(kPgStages == 3, "two tiles under way, two looked up");
+        static_assert(kPgStages == 3, "two tiles under way");
         const int mine = tiles_of(p);
-        const Place first = locate(p, 0), second = locate(p, 1);
-        soon = locate(p, 2);
-        later = locate(p, 3);
-        if (mine > 0) issue(first, 0);
+        tok = p.t0 + warp * kPgTile + (lane & 15);
+        entry = tok / t.page_size;
+        slot = tok - entry * t.page_size;
+        const Place first = locate(p), second = locate(p), third = locate(p);
+        soon = locate(p);
+        here0 = aim(first, 0);
+        here1 = aim(second, 1);
+        __syncwarp();
+        if (mine > 0) issue(here0, 0, 0);
         cp_async_commit();
-        if (mine > 1) issue(second, 1);
+        if (mine > 1) issue(here1, 1, 1);
         cp_async_commit();
+        __syncwarp();
+        here2 = aim(third, 0);
     };
     // Unit n (8 floats) of row r of warp w's output, at the end of a part:
     // units permuted within a row by its number, so that the rows' stores
@@ -400,10 +427,9 @@ paged_kernel(const PagedTask t) {
             cp_async_wait_group<kPgStages - 2>();
             __syncwarp();
             // Stage (i - 1) % kPgStages was read before the __syncwarp.
-            if (i + kPgStages - 1 < mine) issue(soon, (i + kPgStages - 1) % kPgStages);
+            if (i + kPgStages - 1 < mine) issue(here2, i & 1, (i + kPgStages - 1) % kPgStages);
             cp_async_commit();
-            soon = later;
-            later = locate(now, i + kPgStages + 1);
+            const Place later = locate(now);
 
             const uint32_t sk = smem_addr(ring + st * 2 * L::kHalf), sv = sk + L::kHalf;
             float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -417,7 +443,7 @@ paged_kernel(const PagedTask t) {
                     T::mma(s[1], q[ks], k[2], k[3]);
                 }
             }
-            const uint32_t here = live[st];
+            const uint32_t here = here0;
     #pragma unroll
             for (int n = 0; n < 2; ++n)
     #pragma unroll
@@ -480,6 +506,11 @@ paged_kernel(const PagedTask t) {
                     T::mma(o[2 * n2 + 1], lo, v[2], v[3]);
                 }
             }
+            // (Table (i + 1) % 2 was read before this iteration's __syncwarp.)
+            here0 = here1;
+            here1 = here2;
+            here2 = aim(soon, (i + 1) & 1);
+            soon = later;
         }
 
         // The next part's first tiles come while this one's warps are joined.
