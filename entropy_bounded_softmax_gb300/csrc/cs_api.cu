@@ -682,7 +682,6 @@ cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
 // ------------------------------------------------------------ paged attention
 constexpr int32_t kPagedMaxTokens = 1 << 30;
 constexpr int64_t kPagedStep = 64;      // tokens
-constexpr int64_t kPagedWholeSteps = 4;
 
 cs_status check_paged_shape(const cs_paged_shape* s) {
     if (!s) return CS_ERR_INVALID_ARG;
@@ -716,10 +715,15 @@ int64_t paged_rows(const cs_paged_shape& s) {
 // (4, 2 or 1 CTAs each by the shared memory of their rings), because a CTA's
 // start and end cost it microseconds of streaming.  One sequence of 131072
 // tokens, 8 key heads, cut for 304 CTAs: 82 us, for 608: 88, for 1216: 96.
-// 0: no sequence is longer than kPagedWholeSteps, and every row of a sequence
-// is one CTA's.
+// 0: every row of a sequence is one CTA's, and there is nothing to join: where
+// no sequence can be longer than 4 steps, or than 8 with at least 128 such
+// CTAs, which keep the device busy by themselves.  Lengths up to 512 tokens,
+// from a quarter of it on: 128 CTAs 10.5 us whole and 11.5 cut (d_head 128),
+// 256 CTAs 12.3 and 15.8; 64 CTAs 10.4 and 9.7, 16 CTAs 10.1 and 7.2.  Up to
+// 1024 cut is faster with 128 CTAs, 13.6 and 17.3, and as fast with 256.
 int64_t paged_groups(const cs_paged_shape& s) {
-    if (paged_steps(s) <= kPagedWholeSteps) return 0;
+    const int64_t steps = paged_steps(s);
+    if (steps <= 4 || (steps <= 8 && s.batch * paged_rows(s) >= 128)) return 0;
     const int64_t ctas = 152 * (s.d_head <= 64 ? 4 : s.d_head <= 128 ? 2 : 1);
     int64_t n = ctas / paged_rows(s);
     if (n < 1) n = 1;

@@ -21,12 +21,12 @@
 // memory; a sequence that lies in one share is finished there, the others'
 // parts (maximum, sum, unnormalised output) go to the workspace and a second
 // small kernel, launched to overlap the first's end, joins them.  Where no
-// sequence can be longer than four steps every CTA takes one whole row of one
+// sequence can be longer than a few steps every CTA takes one whole row of one
 // sequence, and there is no second kernel.
 //
 // Measured with 8 key heads of 128 in bf16: 83 us for 32 query heads of 131072
-// tokens (6.4 TB/s of the cache, DRAM 84% busy), 41 us for 32 sequences of up
-// to 4096 tokens (4.9 TB/s; the start of the copies, 5 us, and the join, 3,
+// tokens (6.5 TB/s of the cache, DRAM 84% busy), 39 us for 32 sequences of up
+// to 4096 tokens (5.1 TB/s; the start of the copies, 5 us, and the join, 3,
 // do not overlap with them), 4.3 us for a call of few tokens.
 //
 // The weights enter the second product as two halves of the cache's type,

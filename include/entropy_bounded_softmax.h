@@ -665,7 +665,8 @@ cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
                              void* stream);
 
 /* Bytes of workspace the call needs (0 when no row of the table holds more
- * than 256 tokens); negative for a malformed shape.  Host-only. */
+ * than 256 tokens, 512 in large batches); negative for a malformed shape.
+ * Host-only. */
 int64_t cs_paged_attention_workspace(const cs_paged_shape* shape);
 
 /* Host-only argument check (no CUDA call). */

@@ -261,3 +261,15 @@ def test_written_tensors_do_not_overlap_themselves():
     assert check_paged(paged(o=(512, 56))) == BAD
     assert check_paged(paged(o=(448, 64))) == BAD
     assert check_paged(paged(o=(64, 128))) == OK       # [H, B, D] storage
+
+
+def test_paged_workspace_follows_the_cut():
+    """Rows of sequences that can have up to 512 tokens are not cut where
+    there are at least 128 of them, one a key head and sequence."""
+    def need(B, most):
+        return cs.cs_paged_attention_workspace(paged(B=B, most=most))
+
+    assert need(64, 32) == 0 and need(64, 33) > 0      # 2 key heads each
+    assert need(63, 32) > 0 and need(63, 16) == 0
+    big = paged(B=2, H=64 * 20, Hk=64, most=32)        # two tiles of 16 heads
+    assert cs.cs_paged_attention_workspace(big) == 0

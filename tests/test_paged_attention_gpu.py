@@ -373,3 +373,18 @@ def test_prompt_then_tokens(D):
             tol = 2.0 ** -7 * last.abs() + 7 * 2.0 ** -8 * c + 1e-4
             assert ((out[b].float() - last).abs() <= tol).all()
     assert cs.get_error() == set()
+
+
+def test_many_longer_sequences():
+    """As test_many_sequences, past the length up to which large batches are
+    not cut: the dealing walks over the lengths in several rounds."""
+    lengths = [(53 * b) % 700 for b in range(300)]
+    check(cache(lengths, 2, 1, 64, 16))
+
+
+@pytest.mark.parametrize("D,page", [(64, 1), (128, 7), (80, 100), (256, 64)])
+def test_page_sizes_off_the_step(D, page):
+    """Pages that divide no step of 64 tokens, one token a page, pages longer
+    than a step: entry and slot are walked without a division."""
+    check(cache([700, 1, 64, 65, 333], 4, 2, D, page))
+    check(cache([150, 0, 99], 4, 4, D, page))
