@@ -609,17 +609,37 @@ paged_join_kernel(const PagedTask t) {
         return static_cast<int64_t>(2 * ((c0 + i) * rows + row) + (i == 0 ? late : 0)) * 16 +
                hh % 16;
     };
+    // The first outputs of this thread come while the maximum is taken.
+    const int line = threadIdx.x / kUnits, d = 8 * (threadIdx.x % kUnits);
+    auto output = [&](int i) {
+        return reinterpret_cast<const float4*>(t.part_out + place(i) * t.d_head + d);
+    };
+    const bool any = d < t.d_head && line < n;
+    float4 first0 = make_float4(0.f, 0.f, 0.f, 0.f), first1 = first0;
+    float x0 = -INFINITY;
+    if (any) {
+        first0 = output(line)[0];
+        first1 = output(line)[1];
+        x0 = t.part_stats[place(line)].x;
+    }
     const int lane = threadIdx.x & 31;
     float top = -INFINITY, sum = 0.0f;
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) {
-        const float2 st = t.part_stats[place(i)];
-        const float m = fmaxf(top, st.x);
-        // (Both maxima -inf: nothing to rescale.)
-        const float f = top == -INFINITY ? 0.0f : ex2(top - m);
-        const float g = st.x == -INFINITY ? 0.0f : ex2(st.x - m);
-        sum = fmaf(sum, f, st.y * g);
-        top = m;
+    for (int i0 = lane; i0 < n; i0 += 4 * 32) {
+        float2 st[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + 32 * u;
+            st[u] = i < n ? t.part_stats[place(i)] : make_float2(-INFINITY, 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float m = fmaxf(top, st[u].x);
+            // (Both maxima -inf: nothing to rescale.)
+            const float f = top == -INFINITY ? 0.0f : ex2(top - m);
+            const float g = st[u].x == -INFINITY ? 0.0f : ex2(st[u].x - m);
+            sum = fmaf(sum, f, st[u].y * g);
+            top = m;
+        }
     }
     const float mine = top;
 #pragma unroll
@@ -627,19 +647,32 @@ paged_join_kernel(const PagedTask t) {
     sum = mine == -INFINITY ? sum : sum * ex2(mine - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int line = threadIdx.x / kUnits, d = 8 * (threadIdx.x % kUnits);
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (d < t.d_head) {
-#pragma unroll 4
-        for (int i = line; i < n; i += kRows) {
-            const float x = t.part_stats[place(i)].x;
-            const float f = x == -INFINITY ? 0.0f : ex2(x - top);
-            const float4* a = reinterpret_cast<const float4*>(
-                t.part_out + place(i) * t.d_head + d);
-            const float4 a0 = a[0], a1 = a[1];
-            const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    auto add = [&](float x, const float4& a0, const float4& a1) {
+        const float f = x == -INFINITY ? 0.0f : ex2(x - top);
+        const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+    };
+    if (any) {
+        add(x0, first0, first1);
+        // (Four at a time, all loads first; the last ones too.)
+        for (int i0 = line + kRows; i0 < n; i0 += 4 * kRows) {
+            float x[4];
+            float4 a0[4], a1[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kRows;
+                x[u] = -INFINITY;
+                a0[u] = a1[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    x[u] = t.part_stats[place(i)].x;
+                    a0[u] = output(i)[0];
+                    a1[u] = output(i)[1];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(x[u], a0[u], a1[u]);
         }
     }
 #pragma unroll
