@@ -163,52 +163,19 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     float* ws_lse = t.rows;
     float* ws_delta = t.rows + static_cast<int64_t>(t.batch) * t.heads * padded;
 
-    // The loader initialises the barriers, and starts its first copies before
-    // the others have set up.
-    if (warp == kBwdLoadWarp) {
-        static_assert(L::kNumBars <= 32, "a lane a barrier");
-        if (lane < L::kNumBars) mbar_init(bars + lane, bars + lane < r_empty ? 1u : 8u);
-        if (lane == 0) flags[0] = 0u;
-        fence_mbar_init();
-        __syncwarp();
-        if (lane == 0) {
-            if (t.query_len > 0 && t.key_len > 0) {   // (an empty tensor has no map)
-                prefetch_tmap(&map_b1);
-                prefetch_tmap(&map_b2);
-            }
-            mbar_arrive_expect_tx(&a_full[0], L::kTile);
-            load_tile<128, DP, BLK>(smem + L::kA1, &map_a1, a0, ha, b, &a_full[0]);
-        }
-        __syncwarp();
-    } else if (warp == kBwdMmaWarp) {
-        tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
-    }
-    const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
-    int key_lo = 0, key_hi = t.key_len;
-    if (mask) warp_nonzero_range(mask, t.key_len, lane, key_lo, key_hi);
-
-    // Blocks first .. first + per - 1 of the streamed side, for each head.
-    int first = 0, per = 0;
+    // Keys: the queries with a kept key in the tile, i >= a0 - off under causal.
+    const int lo = KV && t.causal ? max(0, a0 - off) : 0;
     const int last = min(a0 + 128, fixed_len) - 1;
-    if (KV) {
-        // Queries with a kept key in the tile: i >= a0 - off under causal.
-        const int lo = t.causal ? max(0, a0 - off) : 0;
-        first = lo / BLK;
-        if (lo < t.query_len && a0 < key_hi && last >= key_lo)
-            per = (t.query_len + BLK - 1) / BLK - first;
-    } else {
-        const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
-        first = key_lo / BLK;
-        if (hi > key_lo) per = (hi + BLK - 1) / BLK - first;
-    }
-    const int blocks = KV ? per * group : per;
+    // Blocks first .. first + per - 1 of the streamed side, for each head.
+    int first = lo / BLK, per = 0;
+    if (KV && lo < t.query_len) per = (t.query_len + BLK - 1) / BLK - first;
     // A block's head on the streamed side and its first row there, walked in
     // order (each walker keeps its own: a division by `per` for every block
     // would cost more than its elementwise part's shorter phase).
     struct Place {
         int head, row;
     };
-    const Place begin{KV ? ha * group : hk, BLK * first};
+    Place begin{KV ? ha * group : hk, BLK * first};
     auto advance = [&](Place& x) {
         x.row += BLK;
         if (KV && x.row >= BLK * (first + per)) {
@@ -242,16 +209,54 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     };
     Place at1 = begin, at2 = begin, at_r = begin;   // the loader's
     static_assert(N2 == NR, "the row values' ring is as deep as the second tensor's");
-    if (warp == kBwdLoadWarp && lane == 0) {
-        // In the order of their use: the first S, the first G V^T.
-        if (blocks > 0) load1(0, at1);
-        mbar_arrive_expect_tx(&a_full[1], L::kTile);
-        load_tile<128, DP, BLK>(smem + L::kA2, &map_a2, a0, ha, b, &a_full[1]);
-        if (!KV) {
-            mbar_arrive_expect_tx(o_full, L::kTile);
-            load_tile<128, DP, BLK>(smem + L::kOut, &map_o, a0, ha, b, o_full);
+
+    // The loader initialises the barriers, and starts the copies that the mask
+    // does not decide on before the others have set up and the mask is read
+    // (1700 cycles), in the order of their use: the first S, the first G V^T.
+    const bool any = KV && per > 0;   // blocks, if the tile's keys are kept
+    if (warp == kBwdLoadWarp) {
+        static_assert(L::kNumBars <= 32, "a lane a barrier");
+        if (lane < L::kNumBars) mbar_init(bars + lane, bars + lane < r_empty ? 1u : 8u);
+        if (lane == 0) flags[0] = 0u;
+        fence_mbar_init();
+        __syncwarp();
+        if (lane == 0) {
+            if (t.query_len > 0 && t.key_len > 0) {   // (an empty tensor has no map)
+                prefetch_tmap(&map_b1);
+                prefetch_tmap(&map_b2);
+            }
+            mbar_arrive_expect_tx(&a_full[0], L::kTile);
+            load_tile<128, DP, BLK>(smem + L::kA1, &map_a1, a0, ha, b, &a_full[0]);
+            if (any) load1(0, at1);
+            mbar_arrive_expect_tx(&a_full[1], L::kTile);
+            load_tile<128, DP, BLK>(smem + L::kA2, &map_a2, a0, ha, b, &a_full[1]);
+            if (any) load2(0, at2);
+            if (!KV) {
+                mbar_arrive_expect_tx(o_full, L::kTile);
+                load_tile<128, DP, BLK>(smem + L::kOut, &map_o, a0, ha, b, o_full);
+            }
         }
-        if (blocks > 0) load2(0, at2);
+        __syncwarp();
+    } else if (warp == kBwdMmaWarp) {
+        tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
+    }
+    const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
+    int key_lo = 0, key_hi = t.key_len;
+    if (mask) warp_nonzero_range(mask, t.key_len, lane, key_lo, key_hi);
+
+    if (KV) {
+        if (a0 >= key_hi || last < key_lo) per = 0;
+    } else {
+        const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
+        first = key_lo / BLK;
+        if (hi > key_lo) per = (hi + BLK - 1) / BLK - first;
+        begin.row = BLK * first;
+        at1 = at2 = begin;
+    }
+    const int blocks = KV ? per * group : per;
+    if (!KV && warp == kBwdLoadWarp && lane == 0 && blocks > 0) {
+        load1(0, at1);
+        load2(0, at2);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -571,6 +576,10 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // without blocks: none may land in shared memory after the CTA exits
         // (bounded waits).
         for (int i = 0; i < 2; ++i) mbar_wait<false>(&a_full[i], 0u, t.wait_limit_cycles);
+        if (any && blocks == 0) {
+            mbar_wait<false>(&b1_full[0], 0u, t.wait_limit_cycles);
+            mbar_wait<false>(&b2_full[0], 0u, t.wait_limit_cycles);
+        }
         if (!KV) mbar_wait<false>(o_full, 0u, t.wait_limit_cycles);
         if (*limit.abort_flag) {
             for (int i = max(0, issued1 - N1); i < issued1; ++i)
