@@ -235,4 +235,16 @@ __device__ __forceinline__ void store_rows32(const unsigned char* tile, int r0, 
     }
 }
 
+// The same with zeros, without a tile.
+template <int N>
+__device__ __forceinline__ void zero_rows32(int p0, uint16_t* out, int64_t stride, int rows,
+                                            int d, int lane) {
+#pragma unroll 1
+    for (int e = lane; e < 32 * 8 * N; e += 32) {
+        const int r = e / (8 * N), at = 64 * p0 + 8 * (e % (8 * N));
+        if (r < rows && at < d)
+            *reinterpret_cast<uint4*>(out + r * stride + at) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 }  // namespace csd

@@ -241,6 +241,17 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
     }
     const uint8_t* mask = t.mask ? t.mask + b * t.mask_stride : nullptr;
+    // An elementwise thread's row of the fixed tile, and what it needs from
+    // memory for it, loaded before the set-up's waits: lse, or whether the key
+    // is removed.
+    const int a = a0 + 32 * (warp & 3) + lane;
+    const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
+    float lse = -INFINITY;
+    bool removed = false;
+    if (warp < 8 && a < fixed_len) {
+        if (!KV) lse = t.lse[row * t.query_len + a];
+        if (KV && mask) removed = mask[a] == 0;
+    }
     int key_lo = 0, key_hi = t.key_len;
     if (mask) warp_nonzero_range(mask, t.key_len, lane, key_lo, key_hi);
 
@@ -277,7 +288,6 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         // ----------------------------------------------------- elementwise
         const int half = warp >> 2;
         const int quarter = warp & 3;
-        const int a = a0 + 32 * quarter + lane;          // this thread's row
         const uint32_t at = (static_cast<uint32_t>(quarter * 32) << 16) + CO * half;
         const float c = t.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
@@ -290,8 +300,6 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             // sequence's CTA.)  A wait that gives up leaves delta wrong and the
             // barrier below matched; the next wait gives up too.
             constexpr int LR = DP / 8, kSteps = 16 * LR / 32;
-            const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
-            const float lse = a < t.query_len ? t.lse[row * t.query_len + a] : -INFINITY;
             warp_wait(&a_full[1], 0, limit);
             warp_wait(o_full, 0, limit);
             const int u = lane % LR, r0 = 16 * warp + lane / LR;
@@ -446,43 +454,40 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                 if (KV) mbar_arrive(&r_empty[st]);
             }
         }
-        // The rows' sums, staged over the fixed tiles once those are read (or,
-        // without blocks, have landed): keys: dv by the first four warps, dk
-        // by the others; queries: a panel of 64 columns of dq each.
+        // The rows' sums, staged over the fixed tiles once those are read: keys:
+        // dv by the first four warps, dk by the others; queries: a panel of 64
+        // columns of dq each.
         if (ok && blocks > 0) ok = warp_wait(sums_full, 0, limit);
-        if (ok && blocks == 0)
-            ok = warp_wait(&a_full[0], 0, limit) && warp_wait(&a_full[1], 0, limit);
         const int row0 = a0 + 32 * quarter;
         constexpr int kPanels = DP / 64;
         const int p0 = KV || kPanels == 1 ? 0 : half, p1 = KV ? kPanels : p0 + 1;
         if (ok && row0 < fixed_len && (KV || kPanels == 2 || half == 0)) {
-            tc_fence_after_sync();
-            const uint32_t from = (KV && half == 1 ? acc2 : acc1) +
-                                  (static_cast<uint32_t>(quarter * 32) << 16);
             unsigned char* stage = smem + (KV && half == 1 ? L::kA2 : L::kA1);
-            const float f = KV && half == 0 ? 1.0f : t.scale;
-            // Exactly 0 for removed keys and for queries without keys, whatever
-            // the rows that they were multiplied with hold.
-            const bool zero = blocks == 0 || (KV ? mask && a < fixed_len && mask[a] == 0
-                                                 : row_lse == -INFINITY);
-#pragma unroll 1
-            for (int c0 = 64 * p0; c0 < 64 * p1; c0 += 32) {
-                uint32_t x[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = 0u;
-                if (blocks > 0) {
-                    tmem_ld32_async(from + c0, x);
-                    tmem_wait_ld<32>(x);
-                }
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = zero ? 0u : x[k];
-                stage_row32(stage, 32 * quarter + lane, c0, x, f);
-            }
             uint16_t* to = KV ? (half == 1 ? t.dk : t.dv) : t.dq;
             const int64_t* stride = KV ? (half == 1 ? t.dk_stride : t.dv_stride) : t.dq_stride;
-            store_rows32<KV ? kPanels : 1>(
-                stage, 32 * quarter, p0, to + b * stride[0] + ha * stride[1] + row0 * stride[2],
-                stride[2], fixed_len - row0, t.d_head, lane);
+            to += b * stride[0] + ha * stride[1] + row0 * stride[2];
+            if (blocks > 0) {
+                tc_fence_after_sync();
+                const uint32_t from = (KV && half == 1 ? acc2 : acc1) +
+                                      (static_cast<uint32_t>(quarter * 32) << 16);
+                const float f = KV && half == 0 ? 1.0f : t.scale;
+                // Exactly 0 for removed keys and for queries without keys,
+                // whatever the rows that they were multiplied with hold.
+                const bool zero = KV ? removed : row_lse == -INFINITY;
+#pragma unroll 1
+                for (int c0 = 64 * p0; c0 < 64 * p1; c0 += 32) {
+                    uint32_t x[32];
+                    tmem_ld32_async(from + c0, x);
+                    tmem_wait_ld<32>(x);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = zero ? 0u : x[k];
+                    stage_row32(stage, 32 * quarter + lane, c0, x, f);
+                }
+                store_rows32<KV ? kPanels : 1>(stage, 32 * quarter, p0, to, stride[2],
+                                               fixed_len - row0, t.d_head, lane);
+            } else {
+                zero_rows32<KV ? kPanels : 1>(p0, to, stride[2], fixed_len - row0, t.d_head, lane);
+            }
         }
     } else if (warp == kBwdMmaWarp) {
         // ----------------------------------------------------- MMA issuer
