@@ -140,23 +140,25 @@ __device__ __forceinline__ void warp_nonzero_range(const uint8_t* row, int n, in
     const uint8_t after = tail + lane < n ? row[tail + lane] : 0;
     int first = n, past = 0;
     const uint4* units = reinterpret_cast<const uint4*>(row + h);
-    for (int v0 = lane; v0 < vecs; v0 += 4 * 32) {
+    for (int v0 = 0; v0 < vecs; v0 += 4 * 32) {
         uint4 x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int v = v0 + 32 * k;
+            const int v = v0 + 32 * k + lane;
             x[k] = v < vecs ? __ldg(units + v) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (w[i]) {
-                    const int at = h + 16 * (v0 + 32 * k) + 4 * i;
-                    first = min(first, at + ((__ffs(static_cast<int>(w[i])) - 1) >> 3));
-                    past = max(past, at + 4 - (__clz(static_cast<int>(w[i])) >> 3));
-                }
+            if (v0 + 32 * k >= vecs) break;
+            // The lowest and the highest word that is not zero.
+            const uint32_t low = x[k].x ? x[k].x : x[k].y ? x[k].y : x[k].z ? x[k].z : x[k].w;
+            const uint32_t high = x[k].w ? x[k].w : x[k].z ? x[k].z : x[k].y ? x[k].y : x[k].x;
+            const int low_at = x[k].x ? 0 : x[k].y ? 4 : x[k].z ? 8 : 12;
+            const int high_at = x[k].w ? 12 : x[k].z ? 8 : x[k].y ? 4 : 0;
+            const int at = h + 16 * (v0 + 32 * k + lane);
+            if (low) {
+                first = min(first, at + low_at + ((__ffs(static_cast<int>(low)) - 1) >> 3));
+                past = max(past, at + high_at + 4 - (__clz(static_cast<int>(high)) >> 3));
             }
         }
     }
