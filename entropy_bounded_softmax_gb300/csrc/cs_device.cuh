@@ -317,6 +317,14 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
     return r;
 }
 
+// 16 bytes of (possibly remote) shared memory.
+__device__ __forceinline__ float4 cluster_load(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // Writes {a, b} into (possibly remote) shared memory and counts 8
 // transaction bytes on the (same CTA's) mbarrier when the write lands.
 __device__ __forceinline__ void push_pair(uint32_t dst, float a, float b,

@@ -337,6 +337,7 @@ struct FattnTask {
     int32_t causal;
     float scale;
     float inv_group;         // kv_heads / heads
+    int32_t split_bits;      // backward: 2^split_bits CTAs, a cluster, share a tile
     uint64_t wait_limit_cycles;
 };
 
@@ -405,22 +406,39 @@ cudaError_t launch_take_error(unsigned int* err, unsigned int* taken,
 cudaError_t ensure_smem_attribute(const void* func, int slot, int bytes,
                                   bool cluster);
 
-// Launches a kernel that may start before the one before it on the stream has
-// ended: it calls csd::wait_for_previous_kernel() before it uses what that one
+// A launch: in clusters of `cluster` CTAs along x, and, if `overlapped`, such
+// that it may start before the kernel before it on the stream has ended: the
+// kernel calls csd::wait_for_previous_kernel() before it uses what that one
 // writes, and in every CTA.
+struct LaunchShape {
+    dim3 grid;
+    int threads, smem_bytes;
+    cudaStream_t stream;
+    bool overlapped;
+    int cluster;
+};
+
 template <class... P, class... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, int smem_bytes,
-                              cudaStream_t stream, const A&... args) {
+cudaError_t launch_shaped(void (*kernel)(P...), const LaunchShape& s, const A&... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem_bytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.gridDim = s.grid;
+    cfg.blockDim = dim3(s.threads);
+    cfg.dynamicSmemBytes = s.smem_bytes;
+    cfg.stream = s.stream;
+    cudaLaunchAttribute attr[2] = {};
+    int n = 0;
+    if (s.overlapped) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (s.cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = s.cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

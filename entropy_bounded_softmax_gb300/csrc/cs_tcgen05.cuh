@@ -158,7 +158,9 @@ __device__ __forceinline__ bool elect_lane() {
 // the leading offset (bytes; K-major operands have none).  Their high word is
 // kDescHigh: the atoms' distance, this architecture's version, the swizzle.
 __device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
-    return (saddr >> 4) | ((lbo ? lbo >> 4 : 1u) << 16);
+    // (In a cluster an address has bits above the 18 that name a byte of the
+    // CTA's shared memory, which would fall into the offset.)
+    return ((saddr & 0x3ffffu) >> 4) | ((lbo ? lbo >> 4 : 1u) << 16);
 }
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 

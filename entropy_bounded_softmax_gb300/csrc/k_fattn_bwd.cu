@@ -17,6 +17,13 @@
 //       dk += dS^T Q.  It starts while the first still runs, and waits for it
 //       where it needs the workspace: its start, and what is left of the
 //       device's SMs at the first's end, cost nothing.
+// Where the tiles of a launch are too few for the device (few key heads, short
+// sequences against long ones), a tile's blocks are shared by a cluster of up
+// to eight CTAs, which leave their sums in shared memory in fp32; each adds an
+// equal share of the rows over the cluster, in the order of the ranks, so that
+// these sums have a fixed order too.  8 query heads on one key head x 4096 of
+// 128, causal: 351 us without, 126 with; 8 on 2 x 512 of 64: 39 and 26.
+//
 // In both the fixed tiles' rows are the lanes of tensor memory, and the
 // weights, rounded to bf16 in columns their scores had, are the next
 // product's A operand there.  Blocks are 128 rows for d_head > 64: a product
@@ -90,6 +97,10 @@ struct BwdPlan {
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages1][4]
     static constexpr int kFlags = kWords + kStages1 * 16;
     static constexpr int kBytes = kFlags + 16;
+    // A cluster's sums, in fp32 from the start of shared memory on.
+    static constexpr int kSums = 128 * DP * 4;
+    static_assert(2 * kSums <= kB2 + kStages2 * kBlock, "dk and dv fit");
+    static_assert(kSums <= kB1, "dq fits the fixed tiles");
 };
 
 __device__ __forceinline__ float2 pair(const uint32_t* x, int k) {
@@ -111,7 +122,9 @@ __device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&w)[1
     tmem_st16(at, w);
 }
 
-template <int DP, bool KV>
+// SPLIT: launched in clusters that share a tile (an instance of its own, so
+// that its code does not cost the others registers: 2% of 32 x 8 x 512).
+template <int DP, bool KV, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, BwdPlan<DP>::kCtasPerSm)
 fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
                  const __grid_constant__ CUtensorMap map_a2,
@@ -153,7 +166,10 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     const int fixed_len = KV ? t.key_len : t.query_len;
     // Under the causal mask late queries keep the most keys and early keys
     // have the most queries: longest first in both.
-    const int ha = blockIdx.x, b = blockIdx.y;     // the fixed tiles' head
+    // The fixed tiles' head, and this CTA's place among those of its cluster,
+    // which share the tile's blocks.
+    const int bits = SPLIT ? t.split_bits : 0;
+    const int ha = blockIdx.x >> bits, rank = blockIdx.x & ((1 << bits) - 1), b = blockIdx.y;
     const int a0 = 128 * static_cast<int>(!KV && t.causal ? gridDim.z - 1 - blockIdx.z
                                                           : blockIdx.z);
     const int off = t.key_len - t.query_len;   // query i keeps keys j <= i + off
@@ -169,13 +185,23 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     // Blocks first .. first + per - 1 of the streamed side, for each head.
     int first = lo / BLK, per = 0;
     if (KV && lo < t.query_len) per = (t.query_len + BLK - 1) / BLK - first;
+    // Of the tile's n blocks, head after head, this CTA takes from the first of
+    // its share on.
+    auto share = [&](int n, int r) {
+        return static_cast<int>(static_cast<int64_t>(n) * r >> bits);
+    };
     // A block's head on the streamed side and its first row there, walked in
     // order (each walker keeps its own: a division by `per` for every block
     // would cost more than its elementwise part's shorter phase).
     struct Place {
         int head, row;
     };
-    Place begin{KV ? ha * group : hk, BLK * first};
+    int from = share(per * group, rank), blocks = share(per * group, rank + 1) - from;
+    Place begin{KV ? ha * group : hk, BLK * (first + from)};
+    if (KV && from > 0) {
+        begin.head += from / per;
+        begin.row = BLK * (first + from % per);
+    }
     auto advance = [&](Place& x) {
         x.row += BLK;
         if (KV && x.row >= BLK * (first + per)) {
@@ -213,7 +239,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     // The loader initialises the barriers, and starts the copies that the mask
     // does not decide on before the others have set up and the mask is read
     // (1700 cycles), in the order of their use: the first S, the first G V^T.
-    const bool any = KV && per > 0;   // blocks, if the tile's keys are kept
+    const bool any = KV && blocks > 0;   // if the tile's keys are kept
     if (warp == kBwdLoadWarp) {
         static_assert(L::kNumBars <= 32, "a lane a barrier");
         if (lane < L::kNumBars) mbar_init(bars + lane, bars + lane < r_empty ? 1u : 8u);
@@ -245,11 +271,11 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     // memory for it, loaded before the set-up's waits: lse, or whether the key
     // is removed.
     const int a = a0 + 32 * (warp & 3) + lane;
-    const int64_t row = static_cast<int64_t>(b) * t.heads + ha;
+    const int64_t row_of_head = static_cast<int64_t>(b) * t.heads + ha;
     float lse = -INFINITY;
     bool removed = false;
     if (warp < 8 && a < fixed_len) {
-        if (!KV) lse = t.lse[row * t.query_len + a];
+        if (!KV) lse = t.lse[row_of_head * t.query_len + a];
         if (KV && mask) removed = mask[a] == 0;
     }
     int key_lo = 0, key_hi = t.key_len;
@@ -261,10 +287,12 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
         first = key_lo / BLK;
         if (hi > key_lo) per = (hi + BLK - 1) / BLK - first;
-        begin.row = BLK * first;
+        from = share(per, rank);
+        begin.row = BLK * (first + from);
         at1 = at2 = begin;
     }
-    const int blocks = KV ? per * group : per;
+    blocks = per > 0 ? share(per * group, rank + 1) - from : 0;
+    const bool joint = SPLIT && per > 0;   // the cluster's sums are added
     if (!KV && warp == kBwdLoadWarp && lane == 0 && blocks > 0) {
         load1(0, at1);
         load2(0, at2);
@@ -332,9 +360,9 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
             row_lse = lse == -INFINITY ? lse : -lse * kLog2e;
             named_barrier(kBarElementwise, kElementwise);
             row_delta = -rows_s[a - a0];
-            if (half == 0) {
-                ws_lse[row * padded + a] = row_lse;
-                ws_delta[row * padded + a] = row_delta;
+            if (half == 0 && rank == 0) {
+                ws_lse[row_of_head * padded + a] = row_lse;
+                ws_delta[row_of_head * padded + a] = row_delta;
             }
         }
         Place place = begin;
@@ -461,14 +489,41 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         const int row0 = a0 + 32 * quarter;
         constexpr int kPanels = DP / 64;
         const int p0 = KV || kPanels == 1 ? 0 : half, p1 = KV ? kPanels : p0 + 1;
-        if (ok && row0 < fixed_len && (KV || kPanels == 2 || half == 0)) {
+        if (joint) {
+            // In fp32, over the fixed tiles and the first ring, once all has
+            // landed and is read: rows of DP floats, their 16-byte units
+            // permuted by the row.
+            if (ok && blocks == 0)
+                ok = warp_wait(&a_full[0], 0, limit) && warp_wait(&a_full[1], 0, limit);
+            if (ok && (KV || kPanels == 2 || half == 0)) {
+                tc_fence_after_sync();
+                const uint32_t sums = (KV && half == 1 ? acc2 : acc1) +
+                                      (static_cast<uint32_t>(quarter * 32) << 16);
+                const int r = 32 * quarter + lane;
+                unsigned char* to = smem + (KV && half == 1 ? L::kSums : 0) + r * DP * 4;
+#pragma unroll 1
+                for (int c0 = 64 * p0; c0 < 64 * p1; c0 += 32) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = 0u;
+                    if (blocks > 0) {
+                        tmem_ld32_async(sums + c0, x);
+                        tmem_wait_ld<32>(x);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(to + (((c0 / 4 + k) ^ (r & 7)) << 4)) =
+                            make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                }
+            }
+        } else if (ok && row0 < fixed_len && (KV || kPanels == 2 || half == 0)) {
             unsigned char* stage = smem + (KV && half == 1 ? L::kA2 : L::kA1);
             uint16_t* to = KV ? (half == 1 ? t.dk : t.dv) : t.dq;
             const int64_t* stride = KV ? (half == 1 ? t.dk_stride : t.dv_stride) : t.dq_stride;
             to += b * stride[0] + ha * stride[1] + row0 * stride[2];
             if (blocks > 0) {
                 tc_fence_after_sync();
-                const uint32_t from = (KV && half == 1 ? acc2 : acc1) +
+                const uint32_t sums = (KV && half == 1 ? acc2 : acc1) +
                                       (static_cast<uint32_t>(quarter * 32) << 16);
                 const float f = KV && half == 0 ? 1.0f : t.scale;
                 // Exactly 0 for removed keys and for queries without keys,
@@ -477,7 +532,7 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
 #pragma unroll 1
                 for (int c0 = 64 * p0; c0 < 64 * p1; c0 += 32) {
                     uint32_t x[32];
-                    tmem_ld32_async(from + c0, x);
+                    tmem_ld32_async(sums + c0, x);
                     tmem_wait_ld<32>(x);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) x[k] = zero ? 0u : x[k];
@@ -600,11 +655,49 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
         for (int i = 0; i < blocks; ++i) {
             const int st = i % N1;
             if (!warp_wait(&b1_full[st], i / N1, limit)) break;
-            mask_tile<BLK, DP>(mask, t.key_len, BLK * (first + i), smem + L::kB1 + st * L::kBlock,
+            mask_tile<BLK, DP>(mask, t.key_len, begin.row + BLK * i, smem + L::kB1 + st * L::kBlock,
                                words + 4 * st, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&b1_masked[st]);
         }
+    }
+    if (joint) {
+        // Each CTA adds its share of the rows over the cluster, in the order
+        // of the ranks.
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        constexpr int kUnits = DP / 8;
+        const int rows = 128 >> bits;
+        for (int e = threadIdx.x; e < (KV ? 2 : 1) * rows * kUnits; e += kBwdThreads) {
+            const int u = e % kUnits, x = e / kUnits / rows;
+            const int r = rank * rows + (e / kUnits & (rows - 1)), i = a0 + r;
+            if (i >= fixed_len || 8 * u >= t.d_head) continue;
+            const bool zero = KV ? mask && mask[i] == 0
+                                 : t.lse[row_of_head * t.query_len + i] == -INFINITY;
+            const uint32_t at = smem_addr(smem) + x * L::kSums + r * DP * 4;
+            float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+#pragma unroll 2
+            for (int k = 0; k < 1 << bits; ++k) {
+                const uint32_t there = map_to_rank(at, k);
+                const float4 v0 = cluster_load(there + ((2 * u ^ (r & 7)) << 4));
+                const float4 v1 = cluster_load(there + (((2 * u + 1) ^ (r & 7)) << 4));
+                s0 = make_float4(s0.x + v0.x, s0.y + v0.y, s0.z + v0.z, s0.w + v0.w);
+                s1 = make_float4(s1.x + v1.x, s1.y + v1.y, s1.z + v1.z, s1.w + v1.w);
+            }
+            const float f = KV && x == 0 ? 1.0f : t.scale;
+            uint4 w = make_uint4(pack_bf16(s0.x * f, s0.y * f), pack_bf16(s0.z * f, s0.w * f),
+                                 pack_bf16(s1.x * f, s1.y * f), pack_bf16(s1.z * f, s1.w * f));
+            if (zero) w = make_uint4(0u, 0u, 0u, 0u);
+            uint16_t* to = KV ? (x == 1 ? t.dk : t.dv) : t.dq;
+            const int64_t* stride = KV ? (x == 1 ? t.dk_stride : t.dv_stride) : t.dq_stride;
+            *reinterpret_cast<uint4*>(to + b * stride[0] + ha * stride[1] + i * stride[2] +
+                                      8 * u) = w;
+        }
+        // No CTA ends while another reads its shared memory.
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -612,17 +705,42 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
+// log2 of the CTAs that share a tile's blocks: 1 to 8, as many as the device
+// holds at once of all tiles, with at least four blocks each (8 query heads on
+// 2 x 77: 15.1 us with one CTA a tile, 13.8 with two of four blocks).
+int split_bits(int64_t tiles, int64_t blocks, int slots) {
+    int bits = 0;
+    while (bits < 3 && (tiles << (bits + 1)) <= slots && (blocks >> (bits + 1)) >= 4) ++bits;
+    return bits;
+}
+
+// One of the two launches: its tiles of `heads` heads of `length` rows, walked
+// over up to `blocks` blocks; slots: two, for the kernel without and with
+// clusters.
+template <int DP, bool KV>
+cudaError_t launch_one(FattnTask t, int heads, int length, int64_t blocks, bool overlapped,
+                       int slot, cudaStream_t stream, const CUtensorMap& a1,
+                       const CUtensorMap& a2, const CUtensorMap& b1, const CUtensorMap& b2,
+                       const CUtensorMap& out) {
+    using L = BwdPlan<DP>;
+    static_assert(L::kBytes <= 232448, "the shared memory of a CTA");
+    const int row_tiles = (length + 127) / 128;
+    t.split_bits = split_bits(static_cast<int64_t>(heads) * t.batch * row_tiles, blocks,
+                              152 * L::kCtasPerSm);
+    const auto kernel = t.split_bits > 0 ? fattn_bwd_kernel<DP, KV, true>
+                                         : fattn_bwd_kernel<DP, KV, false>;
+    const cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel),
+                                                slot + (t.split_bits > 0), L::kBytes, false);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(heads << t.split_bits, t.batch, row_tiles);
+    return launch_shaped(
+        kernel, {grid, kBwdThreads, L::kBytes, stream, overlapped, 1 << t.split_bits}, t, a1, a2,
+        b1, b2, out);
+}
+
 template <int DP>
 cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
     using L = BwdPlan<DP>;
-    constexpr int smem = L::kBytes;
-    static_assert(smem <= 232448, "the shared memory of a CTA");
-    cudaError_t e = ensure_smem_attribute(
-        reinterpret_cast<const void*>(fattn_bwd_kernel<DP, false>), slot, smem, false);
-    if (e == cudaSuccess)
-        e = ensure_smem_attribute(reinterpret_cast<const void*>(fattn_bwd_kernel<DP, true>),
-                                  slot + 1, smem, false);
-    if (e != cudaSuccess) return e;
     // Boxes of a block's rows; fixed tiles of 128 rows are two of them where
     // blocks are 64.
     CUtensorMap q, g, k, v, out;
@@ -633,26 +751,18 @@ cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
         !encode_heads_map(&v, t.v, t, t.kv_heads, t.key_len, t.v_stride, kBox) ||
         !encode_heads_map(&out, t.out, t, t.heads, t.query_len, t.o_stride, kBox))
         return cudaErrorInvalidValue;
-    if (t.query_len > 0) {
-        const dim3 grid(t.heads, t.batch, (t.query_len + 127) / 128);
-        fattn_bwd_kernel<DP, false><<<grid, kBwdThreads, smem, stream>>>(
-            t, q, g, k, v, out);
-        e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && t.key_len > 0) {
-        const dim3 grid(t.kv_heads, t.batch, (t.key_len + 127) / 128);
-        // Overlaps the first launch only: without that one (no queries) it may
-        // not start before the stream's own work, which may use the gradients'
-        // memory, has ended.
-        if (t.query_len > 0) {
-            e = launch_overlapped(fattn_bwd_kernel<DP, true>, grid, kBwdThreads, smem, stream, t,
-                                  k, v, q, g, out);
-        } else {
-            fattn_bwd_kernel<DP, true><<<grid, kBwdThreads, smem, stream>>>(
-                t, k, v, q, g, out);
-            e = cudaGetLastError();
-        }
-    }
+    const int64_t key_blocks = (t.key_len + kBox - 1) / kBox;
+    const int64_t query_blocks = (t.query_len + kBox - 1) / kBox * (t.heads / t.kv_heads);
+    cudaError_t e = cudaSuccess;
+    if (t.query_len > 0)
+        e = launch_one<DP, false>(t, t.heads, t.query_len, key_blocks, false, slot, stream, q, g,
+                                  k, v, out);
+    // The second overlaps the first only: without that one (no queries) it may
+    // not start before the stream's own work, which may use the gradients'
+    // memory, has ended.
+    if (e == cudaSuccess && t.key_len > 0)
+        e = launch_one<DP, true>(t, t.kv_heads, t.key_len, query_blocks, t.query_len > 0, slot + 2,
+                                 stream, k, v, q, g, out);
     return e;
 }
 
@@ -660,7 +770,7 @@ cudaError_t launch_both(const FattnTask& t, int slot, cudaStream_t stream) {
 
 cudaError_t launch_fattn_backward(const FattnTask& task, cudaStream_t stream) {
     return task.d_head <= 64 ? launch_both<64>(task, 58, stream)
-                             : launch_both<128>(task, 60, stream);
+                             : launch_both<128>(task, 68, stream);
 }
 
 }  // namespace cs

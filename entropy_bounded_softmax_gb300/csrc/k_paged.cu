@@ -697,8 +697,8 @@ cudaError_t launch(const PagedTask& t, int slot, cudaStream_t stream) {
     paged_kernel<DP, T><<<grid, kPgThreads, PgSmem<DP>::kBytes, stream>>>(t);
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.split) return e;
-    return launch_overlapped(paged_join_kernel<DP, T>, dim3(t.heads, t.batch), kPgThreads, 0,
-                             stream, t);
+    return launch_shaped(paged_join_kernel<DP, T>,
+                         {dim3(t.heads, t.batch), kPgThreads, 0, stream, true, 1}, t);
 }
 
 template <class T>

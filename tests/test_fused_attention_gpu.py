@@ -437,3 +437,20 @@ def test_no_queries_behind_work_that_allows_overlap():
         _, dk, dv = cs.fused_attention_backward(q, k, k, q, lse, q)
         assert torch.equal(got, want)
         assert (dk == 0).all() and (dv == 0).all()
+
+
+@pytest.mark.parametrize("case", [
+    (1, 4, 1, 1100, 300, 64, False, None),     # keys: eight CTAs a tile
+    (1, 4, 1, 300, 1100, 128, True, None),     # both by clusters
+    (1, 6, 2, 900, 700, 128, True, "left"),    # tiles without blocks among them
+    (2, 2, 1, 150, 1500, 40, False, "holes"),
+    (1, 8, 1, 1300, 140, 96, True, "right"),   # queries without keys
+    (1, 2, 1, 1000, 1000, 64, True, "all"),    # no key at all
+], ids=str)
+def test_few_tiles(case):
+    """Tiles of gradients that several CTAs share, and join."""
+    args = inputs(case)
+    _, _, grads = check(*args)
+    for _ in range(5):
+        again = run_both(*args)[2]
+        assert all(torch.equal(x, y) for x, y in zip(grads, again))
