@@ -325,6 +325,13 @@ __device__ __forceinline__ float4 cluster_load(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 // Writes {a, b} into (possibly remote) shared memory and counts 8
 // transaction bytes on the (same CTA's) mbarrier when the write lands.
 __device__ __forceinline__ void push_pair(uint32_t dst, float a, float b,

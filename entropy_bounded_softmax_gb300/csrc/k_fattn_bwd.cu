@@ -48,7 +48,7 @@
 //
 // Measured, both launches: 2 x 8 heads x 4096 of 128, causal, 163 us (1.05
 // PFLOP/s of the five products; bound by shared memory as the forward is, the
-// tensor pipe 63 and 69% busy); 32 x 8 heads x 512 of 64, 80 us (bound by the
+// tensor pipe 61 and 69% busy); 32 x 8 heads x 512 of 64, 76 us (bound by the
 // chain of each block's two elementwise phases and by the starts and ends of
 // the CTAs: the tensor pipe 21 and 27% busy).
 //
@@ -705,15 +705,6 @@ fattn_bwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_a1,
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
-// log2 of the CTAs that share a tile's blocks: 1 to 8, as many as the device
-// holds at once of all tiles, with at least four blocks each (8 query heads on
-// 2 x 77: 15.1 us with one CTA a tile, 13.8 with two of four blocks).
-int split_bits(int64_t tiles, int64_t blocks, int slots) {
-    int bits = 0;
-    while (bits < 3 && (tiles << (bits + 1)) <= slots && (blocks >> (bits + 1)) >= 4) ++bits;
-    return bits;
-}
-
 // One of the two launches: its tiles of `heads` heads of `length` rows, walked
 // over up to `blocks` blocks; slots: two, for the kernel without and with
 // clusters.
@@ -725,7 +716,7 @@ cudaError_t launch_one(FattnTask t, int heads, int length, int64_t blocks, bool 
     using L = BwdPlan<DP>;
     static_assert(L::kBytes <= 232448, "the shared memory of a CTA");
     const int row_tiles = (length + 127) / 128;
-    t.split_bits = split_bits(static_cast<int64_t>(heads) * t.batch * row_tiles, blocks,
+    t.split_bits = split_bits(static_cast<int64_t>(heads) * t.batch * row_tiles, blocks, 4,
                               152 * L::kCtasPerSm);
     const auto kernel = t.split_bits > 0 ? fattn_bwd_kernel<DP, KV, true>
                                          : fattn_bwd_kernel<DP, KV, false>;

@@ -14,9 +14,15 @@
 //                 write 64, 2050 of its 3000 cycles (2 x 8 heads x 4096 of
 //                 128, causal: 52 us, 1.3 PFLOP/s);
 //   d_head <= 64  blocks of 64 keys, two CTAs an SM, which four tiles keep
-//                 busier (32 x 8 heads x 512: 24.6 us; two CTAs of one tile
+//                 busier (32 x 8 heads x 512: 24.2 us; two CTAs of one tile
 //                 with two score buffers 28.5, three of one tile 28.4, one of
 //                 two tiles and blocks of 128 35).
+// Where the pairs of tiles are too few for the device (one prompt of few heads,
+// few queries over long keys), a cluster of up to eight CTAs shares a pair's
+// keys, and joins: each leaves its unnormalised outputs, maxima and sums in
+// shared memory, and works out an equal share of the rows over the cluster, in
+// the order of the ranks.  2 heads x 4096 of 128: 52 us without, 27 with; 4
+// heads, one query over 4096 keys: 47 and 12.
 // Roles, one mbarrier hand-off each:
 //   warps 0-3, 4-7  softmax of tile 0 and 1, one row a thread: the maximum of
 //                   the row's scores, 2^(s c - m c) and the sum, the weights
@@ -77,6 +83,17 @@ struct FwdPlan {
     static constexpr int kWords = (kBars + 8 * kNumBars + 15) / 16 * 16;  // [kStages][4]
     static constexpr int kFlags = kWords + kStages * 16;  // abort, tmem
     static constexpr int kBytes = kFlags + 16 + 1024;     // and alignment slack
+    // Clusters: both tiles' maxima and sums, and, in fp32 from the start on,
+    // their outputs.
+    static constexpr int kStats = kFlags + 16;            // [256] float2
+    static constexpr int kSums = 128 * DP * 4;
+    static_assert(2 * kSums <= kBars, "both tiles' outputs fit");
+    static constexpr int kSplitBytes = kBytes + 256 * 8;
+    // The blocks of keys from which on a join, about 4 us, is worth it.  D 64,
+    // whole and in clusters: 512 keys (16 heads x 512, causal) 12.7 and 13.6 us,
+    // 768 (8 heads x 64) 13.7 and 11.9.  D 128: 768 keys 12.8 and 13.2, 1024 (8
+    // heads x 256, causal) 17.4 and 16.0.
+    static constexpr int kSplitBlocks = DP == 64 ? 12 : 8;
 };
 
 // -inf for the columns whose bit is not set.
@@ -87,7 +104,8 @@ __device__ __forceinline__ void remove_columns(uint32_t (&s)[N], const uint32_t*
         if (!((kept[k >> 5] >> (k & 31)) & 1u)) s[k] = __float_as_uint(-INFINITY);
 }
 
-template <int DP>
+// SPLIT: launched in clusters that share a pair of tiles.
+template <int DP, bool SPLIT>
 __global__ void __launch_bounds__(kFwdThreads, FwdPlan<DP>::kCtasPerSm)
 fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                  const __grid_constant__ CUtensorMap map_k,
@@ -115,7 +133,8 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     // Under the causal mask later rows keep more keys: longest first.
-    const int h = blockIdx.x, b = blockIdx.y;
+    const int bits = SPLIT ? t.split_bits : 0;
+    const int h = blockIdx.x >> bits, rank = blockIdx.x & ((1 << bits) - 1), b = blockIdx.y;
     const int qt = t.causal ? static_cast<int>(gridDim.z - 1 - blockIdx.z)
                             : static_cast<int>(blockIdx.z);
     const int hk = head_of(h, t.inv_group);
@@ -151,16 +170,26 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     int key_lo = 0, key_hi = t.key_len;
     if (mask) warp_nonzero_range(mask, t.key_len, lane, key_lo, key_hi);
 
-    // Blocks j0, j0 + 1, ..: n[i] of them for tile i, none for a tile without
+    // Blocks first, first + 1, ..: n[i] of them for tile i, none for a tile without
     // rows or without kept keys.
-    const int j0 = key_lo / BLK;
+    const int first = key_lo / BLK;
     int n[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int last = min(q0 + 128 * (i + 1), t.query_len) - 1;
         const int hi = t.causal ? min(key_hi, last + off + 1) : key_hi;
-        n[i] = last >= q0 + 128 * i && hi > key_lo ? (hi + BLK - 1) / BLK - j0 : 0;
+        n[i] = last >= q0 + 128 * i && hi > key_lo ? (hi + BLK - 1) / BLK - first : 0;
     }
+    // A cluster's CTAs take equal shares of them, and join their outputs.
+    const int all = max(n[0], n[1]);
+    const bool joint = SPLIT && all > 0;
+    const int from = SPLIT ? static_cast<int>(static_cast<int64_t>(all) * rank >> bits) : 0;
+    if (SPLIT) {
+        const int to = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) >> bits);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) n[i] = max(0, min(n[i], to) - from);
+    }
+    const int j0 = first + from;
     const int blocks = max(n[0], n[1]);
     auto load_k = [&](int j) {
         const int st = j % NS;
@@ -290,6 +319,87 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
         }
         // The tile's queries are read (or, without blocks, have landed) before
         // the output is staged over them.
+        if (joint) {
+            // In fp32, over the queries, keys and values, once both tiles' are
+            // read (or have landed): rows of DP floats, their 16-byte units
+            // permuted by the row.
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (ok && n[x] > 0) ok = warp_wait(&o_done[x], 0, limit);
+                if (ok && n[x] == 0 && q0 + 128 * x < t.query_len)
+                    ok = warp_wait(&q_full[x], 0, limit);
+            }
+            float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
+            const int r = 32 * (warp & 3) + lane;
+            if (ok) {
+                tc_fence_after_sync();
+                stats[128 * tile + r] = make_float2(m == -INFINITY ? 0.0f : m * c, l);
+                unsigned char* row = smem + tile * L::kSums + r * DP * 4;
+#pragma unroll 1
+                for (int u = 0; u < DP / 32; ++u) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0u;
+                    if (nt > 0) {
+                        tmem_ld32_async(to + 32 * u, o);
+                        tmem_wait_ld<32>(o);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(row + (((8 * u + k) ^ (r & 7)) << 4)) =
+                            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            // Each CTA joins its share of the rows, rank after rank: the
+            // largest maximum M, the sums and outputs times 2^(m - M).
+            constexpr int kUnits = DP / 8;
+            const int rows = 256 >> bits;
+            for (int e = threadIdx.x; e < rows * kUnits; e += 256) {
+                const int u = e % kUnits, at = rank * rows + e / kUnits, qi = q0 + at;
+                if (qi >= t.query_len || 8 * u >= t.d_head) continue;
+                const uint32_t stat = smem_addr(smem + L::kStats) + at * 8;
+                float top = -INFINITY, sum = 0.0f;
+                for (int k = 0; k < 1 << bits; ++k) {
+                    const float2 s = cluster_load2(map_to_rank(stat, k));
+                    if (s.y != 0.0f) top = fmaxf(top, s.x);
+                }
+                const uint32_t line = smem_addr(smem) + (at >> 7) * L::kSums + (at & 127) * DP * 4;
+                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < 1 << bits; ++k) {
+                    const float2 s = cluster_load2(map_to_rank(stat, k));
+                    if (s.y == 0.0f) continue;   // no keys there
+                    const float f = ex2(s.x - top);
+                    sum = fmaf(s.y, f, sum);
+                    const uint32_t there = map_to_rank(line, k);
+                    const float4 v0 = cluster_load(there + ((2 * u ^ (at & 7)) << 4));
+                    const float4 v1 = cluster_load(there + (((2 * u + 1) ^ (at & 7)) << 4));
+                    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) acc[y] = fmaf(v[y], f, acc[y]);
+                }
+                const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+                *reinterpret_cast<uint4*>(t.out + b * t.o_stride[0] + h * t.o_stride[1] +
+                                          qi * t.o_stride[2] + 8 * u) =
+                    make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv),
+                               pack_bf16(acc[2] * inv, acc[3] * inv),
+                               pack_bf16(acc[4] * inv, acc[5] * inv),
+                               pack_bf16(acc[6] * inv, acc[7] * inv));
+                if (u == 0) {
+                    if (t.lse)
+                        t.lse[(static_cast<int64_t>(b) * t.heads + h) * t.query_len + qi] =
+                            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    if (!isfinite(sum)) raise_error(t.err, kBitNan);
+                }
+            }
+            // No CTA ends while another reads its shared memory.
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            ok = false;   // nothing is left to write
+        }
         if (ok && nt > 0) ok = warp_wait(&o_done[tile], 0, limit);
         if (ok && nt == 0 && row0 < t.query_len) ok = warp_wait(&q_full[tile], 0, limit);
         if (ok && row0 < t.query_len) {
@@ -414,6 +524,13 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
                 if (lane == 0) mbar_arrive(&v_masked[st]);
             }
         }
+        if (joint) {   // the softmax warps' two
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -421,28 +538,38 @@ fattn_fwd_kernel(const FattnTask t, const __grid_constant__ CUtensorMap map_q,
     if (threadIdx.x == 0 && flags[0]) raise_error(t.err, kBitTimeout);
 }
 
+// slots: two, for the kernel without and with clusters.
 template <int DP>
-cudaError_t launch_fwd(const FattnTask& t, int slot, cudaStream_t stream) {
+cudaError_t launch_fwd(FattnTask t, int slot, int split_slot, cudaStream_t stream) {
     using L = FwdPlan<DP>;
-    const void* kern = reinterpret_cast<const void*>(fattn_fwd_kernel<DP>);
-    cudaError_t e = ensure_smem_attribute(kern, slot, L::kBytes, false);
+    const int row_tiles = (t.query_len + 255) / 256;
+    const int64_t blocks = (t.key_len + L::kBlk - 1) / L::kBlk;
+    t.split_bits = blocks < L::kSplitBlocks
+                       ? 0
+                       : split_bits(static_cast<int64_t>(t.heads) * t.batch * row_tiles, blocks,
+                                    256 / L::kBlk, 152 * L::kCtasPerSm);
+    const bool split = t.split_bits > 0;
+    const auto kernel = split ? fattn_fwd_kernel<DP, true> : fattn_fwd_kernel<DP, false>;
+    const int bytes = split ? L::kSplitBytes : L::kBytes;
+    cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel),
+                                          split ? split_slot : slot, bytes, false);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv;
     if (!encode_heads_map(&mq, t.q, t, t.heads, t.query_len, t.q_stride, 128) ||
         !encode_heads_map(&mk, t.k, t, t.kv_heads, t.key_len, t.k_stride, L::kBlk) ||
         !encode_heads_map(&mv, t.v, t, t.kv_heads, t.key_len, t.v_stride, L::kBlk))
         return cudaErrorInvalidValue;
-    const dim3 grid(t.heads, t.batch, (t.query_len + 255) / 256);
-    fattn_fwd_kernel<DP><<<grid, kFwdThreads, L::kBytes, stream>>>(
-        t, mq, mk, mv);
-    return cudaGetLastError();
+    const dim3 grid(t.heads << t.split_bits, t.batch, row_tiles);
+    return launch_shaped(kernel,
+                         {grid, kFwdThreads, bytes, stream, false, 1 << t.split_bits}, t, mq,
+                         mk, mv);
 }
 
 }  // namespace
 
 cudaError_t launch_fattn_forward(const FattnTask& task, cudaStream_t stream) {
-    return task.d_head <= 64 ? launch_fwd<64>(task, 56, stream)
-                             : launch_fwd<128>(task, 57, stream);
+    return task.d_head <= 64 ? launch_fwd<64>(task, 56, 72, stream)
+                             : launch_fwd<128>(task, 57, 73, stream);
 }
 
 }  // namespace cs

@@ -454,3 +454,34 @@ def test_few_tiles(case):
     for _ in range(5):
         again = run_both(*args)[2]
         assert all(torch.equal(x, y) for x, y in zip(grads, again))
+
+
+@pytest.mark.parametrize("case", [
+    (1, 2, 1, 1, 5000, 128, False, "right"),   # one query, eight CTAs
+    (1, 3, 1, 140, 4100, 64, True, "left"),
+    (1, 2, 2, 600, 2500, 72, True, "holes"),
+    (2, 2, 1, 700, 600, 128, True, None),      # queries without keys
+    (1, 2, 1, 300, 2048, 8, False, "all"),
+], ids=str)
+def test_few_queries(case):
+    """Outputs of tiles whose keys several CTAs share, and join."""
+    args = inputs(case)
+    out, lse, _ = check(*args)
+    q, k, v, _, mask, causal = args
+    for _ in range(5):
+        again, lse2 = cs.fused_attention(q, k, v, mask, causal,
+                                         return_lse=True)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_nan_in_one_share_of_the_keys():
+    """Scores of keys far apart, one of them NaN: reported, and only in the
+    queries that attend it."""
+    q, k, v, _, _, _ = inputs((1, 1, 1, 70, 4096, 64, False, None))
+    k[0, 0, 4000, 3] = math.nan
+    out = cs.fused_attention(q, k, v)
+    assert out.isnan().all() and cs.get_error() == {"NAN_INPUT"}
+    keep = torch.ones(1, 4096, dtype=torch.bool, device="cuda")
+    keep[0, 4000] = False
+    assert cs.fused_attention(q, k, v, keep).isfinite().all()
+    assert cs.get_error() == set()
