@@ -1,0 +1,67 @@
+"""Calls of the attention operators that their documentation allows and that
+the tests against their definitions do not make."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import entropy_bounded_softmax_gb300 as cs
+
+pytestmark = pytest.mark.gpu
+
+
+def _best_us(call, repeats=5):
+    call()
+    torch.cuda.synchronize()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    best = math.inf
+    for _ in range(repeats):
+        start.record()
+        call()
+        end.record()
+        end.synchronize()
+        best = min(best, 1e3 * start.elapsed_time(end))
+    return best
+
+
+def _short_sequences(batch, heads=8, D=64):
+    """Sequences of one page in a table with room for 64 pages each, which
+    makes the call deal shares and join them."""
+    gen = torch.Generator(device="cuda").manual_seed(batch)
+    lengths = torch.randint(1, 17, (batch,), dtype=torch.int32, device="cuda",
+                            generator=gen)
+    k, v = (torch.randn(batch, 16, 1, D, device="cuda",
+                        generator=gen).bfloat16() for _ in range(2))
+    table = torch.zeros(batch, 64, dtype=torch.int32, device="cuda")
+    table[:, 0] = torch.randperm(batch, device="cuda", generator=gen)
+    q = torch.randn(batch, heads, D, device="cuda", generator=gen).bfloat16()
+    return q, k, v, table, lengths
+
+
+def test_paged_cost_follows_the_batch():
+    """Eight times the sequences take about eight times the time (a join that
+    walks all lengths for each of them takes 40 times)."""
+    small, large = _short_sequences(4096), _short_sequences(32768)
+    assert (_best_us(lambda: cs.paged_attention(*large))
+            < 16 * _best_us(lambda: cs.paged_attention(*small)))
+
+
+@pytest.mark.parametrize("batch", [75, 76, 77, 700, 5000])
+def test_paged_large_batches(batch):
+    """Around and far past the number of groups, whole rows against shares and
+    a join: the same sequences in a table of few pages are not cut."""
+    q, k, v, table, lengths = _short_sequences(batch, heads=16, D=128)
+    k, v = (x.repeat(1, 1, 4, 1) for x in (k, v))
+    longer = torch.arange(batch, device="cuda") % 5 == 2
+    table[longer, 1:16] = torch.randint(
+        0, batch, (int(longer.sum()), 15), dtype=torch.int32, device="cuda")
+    lengths[longer] += 200
+    wide = cs.paged_attention(q, k, v, table, lengths, return_lse=True)
+    whole = cs.paged_attention(q, k, v, table[:, :16].contiguous(), lengths,
+                               return_lse=True)
+    # Sums in another order: a rounding of the result to bf16 apart at most.
+    a, b = wide[0].float(), whole[0].float()
+    assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-5).all()
+    assert ((wide[1] - whole[1]).abs() <= 2.0 ** -16 * (1 + whole[1].abs())).all()
+    assert cs.get_error() == set()
