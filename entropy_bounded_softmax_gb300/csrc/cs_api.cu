@@ -651,11 +651,12 @@ int64_t mask_extent(const cs_attention_shape& s, const uint8_t* mask) {
 }
 
 cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
-                             unsigned int* err) {
+                             const DeviceInfo& d) {
     cs::FattnTask t{};
     t.mask = mask;
     t.mask_stride = s.mask_stride;
-    t.err = err;
+    t.err = d.err;
+    t.sm_count = d.sm_count;
     for (int i = 0; i < 3; ++i) {
         t.q_stride[i] = s.q_stride[i];
         t.k_stride[i] = s.k_stride[i];
@@ -682,6 +683,9 @@ cs::FattnTask attention_task(const cs_attention_shape& s, const uint8_t* mask,
 // ------------------------------------------------------------ paged attention
 constexpr int32_t kPagedMaxTokens = 1 << 30;
 constexpr int64_t kPagedStep = 64;      // tokens
+// The workspace, whose size is worked out without a device, is for the groups
+// of this many SMs, a GB300's; a device with fewer deals to fewer groups.
+constexpr int kPagedMaxSms = 152;
 
 cs_status check_paged_shape(const cs_paged_shape* s) {
     if (!s) return CS_ERR_INVALID_ARG;
@@ -711,20 +715,23 @@ int64_t paged_rows(const cs_paged_shape& s) {
     return static_cast<int64_t>(s.kv_heads) * paged_head_tiles(s);
 }
 
-// Groups of CTAs that the steps are dealt to: as many as 152 SMs hold at once
+// Groups of CTAs that the steps are dealt to: as many as `sms` SMs hold at once
 // (4, 2 or 1 CTAs each by the shared memory of their rings), because a CTA's
 // start and end cost it microseconds of streaming.  One sequence of 131072
-// tokens, 8 key heads, cut for 304 CTAs: 82 us, for 608: 88, for 1216: 96.
+// tokens, 8 key heads, on 152 SMs cut for 304 CTAs: 82 us, for 608: 88, for
+// 1216: 96.  Whole groups only: rows that do not divide the SMs' CTAs leave the
+// rest of them idle, up to half with just over half as many rows (d_head 256
+// and 80 key heads: 80 of 152).
 // 0: every row of a sequence is one CTA's, and there is nothing to join: where
 // no sequence can be longer than 4 steps, or than 8 with at least 128 such
 // CTAs, which keep the device busy by themselves.  Lengths up to 512 tokens,
 // from a quarter of it on: 128 CTAs 10.5 us whole and 11.5 cut (d_head 128),
 // 256 CTAs 12.3 and 15.8; 64 CTAs 10.4 and 9.7, 16 CTAs 10.1 and 7.2.  Up to
 // 1024 cut is faster with 128 CTAs, 13.6 and 17.3, and as fast with 256.
-int64_t paged_groups(const cs_paged_shape& s) {
+int64_t paged_groups(const cs_paged_shape& s, int sms) {
     const int64_t steps = paged_steps(s);
     if (steps <= 4 || (steps <= 8 && s.batch * paged_rows(s) >= 128)) return 0;
-    const int64_t ctas = 152 * (s.d_head <= 64 ? 4 : s.d_head <= 128 ? 2 : 1);
+    const int64_t ctas = sms * (s.d_head <= 64 ? 4 : s.d_head <= 128 ? 2 : 1);
     int64_t n = ctas / paged_rows(s);
     if (n < 1) n = 1;
     const int64_t total = paged_steps(s) * s.batch;
@@ -1307,7 +1314,7 @@ cs_status cs_fused_attention(const uint16_t* query, const uint16_t* keys,
     DeviceInfo* d = nullptr;
     st = device_info(&d);
     if (st != CS_OK) return st;
-    cs::FattnTask t = attention_task(*shape, mask, d->err);
+    cs::FattnTask t = attention_task(*shape, mask, *d);
     t.q = query;
     t.k = keys;
     t.v = values;
@@ -1370,7 +1377,7 @@ cs_status cs_fused_attention_backward(
     DeviceInfo* d = nullptr;
     st = device_info(&d);
     if (st != CS_OK) return st;
-    cs::FattnTask t = attention_task(*shape, mask, d->err);
+    cs::FattnTask t = attention_task(*shape, mask, *d);
     t.q = query;
     t.k = keys;
     t.v = values;
@@ -1392,7 +1399,7 @@ cs_status cs_fused_attention_backward(
 int64_t cs_paged_attention_workspace(const cs_paged_shape* shape) {
     if (check_paged_shape(shape) != CS_OK) return -1;
     // Two parts a CTA, of 16 heads: the (maximum, sum) pairs, the outputs.
-    const int64_t heads = paged_groups(*shape) * paged_rows(*shape) * 2 * 16;
+    const int64_t heads = paged_groups(*shape, kPagedMaxSms) * paged_rows(*shape) * 2 * 16;
     return heads * 8 + heads * shape->d_head * 4;
 }
 
@@ -1472,14 +1479,15 @@ cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
     t.num_pages = s.num_pages;
     t.max_pages = s.max_pages;
     t.head_tiles = paged_head_tiles(s);
-    t.groups = static_cast<int32_t>(paged_groups(s));
+    t.groups = static_cast<int32_t>(
+        paged_groups(s, d->sm_count < kPagedMaxSms ? d->sm_count : kPagedMaxSms));
     t.split = t.groups > 0;
     t.fp16 = s.fp16;
     t.scale = s.scale;
     if (t.split) {
         t.part_stats = static_cast<float2*>(workspace);
         t.part_out = reinterpret_cast<float*>(t.part_stats +
-                                              paged_groups(s) * paged_rows(s) * 2 * 16);
+                                              t.groups * paged_rows(s) * 2 * 16);
     }
     if (cs::launch_paged(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();

@@ -338,6 +338,7 @@ struct FattnTask {
     float scale;
     float inv_group;         // kv_heads / heads
     int32_t split_bits;      // 2^split_bits CTAs, a cluster, share a tile
+    int32_t sm_count;
     uint64_t wait_limit_cycles;
 };
 

@@ -717,7 +717,7 @@ cudaError_t launch_one(FattnTask t, int heads, int length, int64_t blocks, bool 
     static_assert(L::kBytes <= 232448, "the shared memory of a CTA");
     const int row_tiles = (length + 127) / 128;
     t.split_bits = split_bits(static_cast<int64_t>(heads) * t.batch * row_tiles, blocks, 4,
-                              152 * L::kCtasPerSm);
+                              t.sm_count * L::kCtasPerSm);
     const auto kernel = t.split_bits > 0 ? fattn_bwd_kernel<DP, KV, true>
                                          : fattn_bwd_kernel<DP, KV, false>;
     const cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel),

@@ -547,7 +547,7 @@ cudaError_t launch_fwd(FattnTask t, int slot, int split_slot, cudaStream_t strea
     t.split_bits = blocks < L::kSplitBlocks
                        ? 0
                        : split_bits(static_cast<int64_t>(t.heads) * t.batch * row_tiles, blocks,
-                                    256 / L::kBlk, 152 * L::kCtasPerSm);
+                                    256 / L::kBlk, t.sm_count * L::kCtasPerSm);
     const bool split = t.split_bits > 0;
     const auto kernel = split ? fattn_fwd_kernel<DP, true> : fattn_fwd_kernel<DP, false>;
     const int bytes = split ? L::kSplitBytes : L::kBytes;

@@ -1,0 +1,26 @@
+"""Fused and paged attention on the CPU: arguments at the far end of their
+ranges, and rules of the sources that no GPU here can show.  No CUDA call is
+made."""
+import glob
+import os
+import re
+
+import entropy_bounded_softmax_gb300 as cs
+
+CSRC = os.path.join(os.path.dirname(cs.__file__), "csrc")
+
+
+def _code(path):
+    """A source file without its comments."""
+    with open(path) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def test_launches_ask_the_device_for_its_sms():
+    """The number of SMs is the device's in every launch; the one literal
+    bounds a workspace whose size is worked out without a device."""
+    lines = [line.strip() for path in glob.glob(os.path.join(CSRC, "*"))
+             for line in _code(path).splitlines()
+             if re.search(r"\b152\b", line)]
+    assert lines == ["constexpr int kPagedMaxSms = 152;"]
