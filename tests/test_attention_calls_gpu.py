@@ -1,6 +1,9 @@
 """Calls of the attention operators that their documentation allows and that
 the tests against their definitions do not make."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -9,6 +12,8 @@ torch = pytest.importorskip("torch")
 import entropy_bounded_softmax_gb300 as cs
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _best_us(call, repeats=5):
@@ -65,3 +70,12 @@ def test_paged_large_batches(batch):
     assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-5).all()
     assert ((wide[1] - whole[1]).abs() <= 2.0 ** -16 * (1 + whole[1].abs())).all()
     assert cs.get_error() == set()
+
+
+def test_smoke_warns_of_nothing():
+    """In a process of its own: torch gives such a warning once."""
+    run = subprocess.run(
+        [sys.executable, "-W", "error::UserWarning", "-c",
+         "import __graft_entry__ as g; g.smoke()"], cwd=ROOT,
+        capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
