@@ -465,12 +465,25 @@ def fused_attention(query, keys, values, mask=None, causal: bool = False,
     :func:`fused_attention_backward` takes.  Asynchronous on the current
     stream; NaN or infinite scores propagate and are reported by
     :func:`get_error`.
+
+    Where autograd records and query, keys or values require a gradient, the
+    call goes through :class:`FusedAttentionFunction`: the output carries the
+    gradient, the log of the sums does not, and ``out`` is refused.
     """
     import torch
     same = () if out is None else (out,)
     if not _attention_ok(torch, query, keys, values, mask, None, same):
         _check_attention(query, keys, values, mask, scale, None,
                          {} if out is None else {"out": out})
+    if ((query.requires_grad or keys.requires_grad or values.requires_grad)
+            and torch.is_grad_enabled()):
+        if out is not None:
+            raise ValueError("out takes no gradient: call under "
+                             "torch.no_grad(), or without it")
+        # What autograd's function would copy is refused here as ever.
+        _check_attention(query, keys, values, mask, scale, None, {})
+        return _autograd_class("FusedAttentionFunction").apply(
+            query, keys, values, mask, causal, scale, return_lse)
     B, H, Sq, D = query.shape
     _, Hk, Sk, _ = keys.shape
     if out is None:
@@ -502,7 +515,8 @@ def fused_attention_backward(query, keys, values, out, lse, grad_output,
     ``lse`` (``return_lse=True``).  The probabilities are recomputed; every
     sum has a fixed order, so repeated calls give the same bits.  Returns
     bf16 gradients in the memory order of their tensors; removed keys get
-    zeros.  Asynchronous on the current stream.
+    zeros.  The gradients are not themselves differentiable.  Asynchronous on
+    the current stream.
     """
     import torch
     same = {"out": out, "grad_output": grad_output}
@@ -636,7 +650,8 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
     ``return_lse`` the log of the softmax's sums [B, H] in fp32.
     Asynchronous on the current stream; lengths and page numbers out of
     range are left out and reported by :func:`get_error`, and so are NaN or
-    infinite scores, which propagate.
+    infinite scores, which propagate.  For serving: there is no backward pass,
+    and the result carries no gradient.
     """
     import torch
     given = (query, key_pages, value_pages, page_table, lengths)
@@ -725,41 +740,58 @@ def _fused_attention_function():
 
     class FusedAttentionFunction(torch.autograd.Function):
         """Autograd wrapper of :func:`fused_attention`: ``apply(query, keys,
-        values, mask, causal, scale)``; query, keys and values receive
-        gradients.  Inputs whose strides the kernels do not take (expanded
-        ones, for example) are copied."""
+        values, mask, causal, scale, return_lse)``; query, keys and values
+        receive gradients, once (there is no second derivative, forward mode
+        or vmap rule: torch refuses them).  Inputs whose strides the kernels
+        do not take (expanded ones, for example) are copied.  The backward
+        pass computes the three gradients together, and hands on those that
+        are needed."""
 
         @staticmethod
         def forward(ctx, query, keys, values, mask=None, causal=False,
-                    scale=None):
+                    scale=None, return_lse=False):
             query, keys, values = (strided(x) for x in (query, keys, values))
             out, lse = fused_attention(query, keys, values, mask, causal,
                                        scale, return_lse=True)
             ctx.save_for_backward(query, keys, values, out, lse, mask)
             ctx.causal, ctx.scale = causal, scale
-            return out
+            ctx.set_materialize_grads(False)
+            if not return_lse:
+                return out
+            ctx.mark_non_differentiable(lse)
+            return out, lse
 
         @staticmethod
         @torch.autograd.function.once_differentiable
-        def backward(ctx, grad_output):
+        def backward(ctx, grad_output, _=None):
+            if grad_output is None:
+                return (None,) * 7
             query, keys, values, out, lse, mask = ctx.saved_tensors
             grads = fused_attention_backward(
                 query, keys, values, out, lse, strided(grad_output), mask,
                 ctx.causal, ctx.scale)
-            return (*grads, None, None, None)
+            return (*(x if needed else None
+                      for x, needed in zip(grads, ctx.needs_input_grad)),
+                    None, None, None, None)
 
     return FusedAttentionFunction
 
 
-def __getattr__(name):
-    # The autograd classes need torch; they are built on first use so that
-    # the package imports without torch (the C ABI tests run without it).
-    make = {"ConstrainedSoftmaxFunction": _autograd_function,
-            "FusedAttentionFunction": _fused_attention_function}.get(name)
-    if make is not None:
-        cls = make()
+def _autograd_class(name):
+    """An autograd class of the package.  They need torch, and are built on
+    first use so that the package imports without torch (the C ABI tests run
+    without it)."""
+    cls = globals().get(name)
+    if cls is None:
+        cls = {"ConstrainedSoftmaxFunction": _autograd_function,
+               "FusedAttentionFunction": _fused_attention_function}[name]()
         globals()[name] = cls
-        return cls
+    return cls
+
+
+def __getattr__(name):
+    if name in ("ConstrainedSoftmaxFunction", "FusedAttentionFunction"):
+        return _autograd_class(name)
     raise AttributeError(name)
 
 

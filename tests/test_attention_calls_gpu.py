@@ -10,6 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import entropy_bounded_softmax_gb300 as cs
+from test_fused_attention_gpu import inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,51 @@ def test_smoke_warns_of_nothing():
          "import __graft_entry__ as g; g.smoke()"], cwd=ROOT,
         capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_gradients_are_not_dropped():
+    """fused_attention on tensors that require gradients: those of
+    FusedAttentionFunction, for each of the three alone too."""
+    q, k, v, g, mask, causal = inputs((2, 4, 2, 90, 150, 64, True, "holes"), 9)
+    want, lse = cs.fused_attention(q, k, v, mask, causal, 0.2, return_lse=True)
+    grads = cs.fused_attention_backward(q, k, v, want, lse, g, mask, causal,
+                                        0.2)
+    for needed in ((0, 1, 2), (0,), (1,), (2,)):
+        args = [x.clone().requires_grad_(n in needed)
+                for n, x in enumerate((q, k, v))]
+        out, sums = cs.fused_attention(*args, mask, causal, 0.2,
+                                       return_lse=True)
+        assert torch.equal(out, want) and torch.equal(sums, lse)
+        assert out.requires_grad and not sums.requires_grad
+        out.backward(g)
+        for n, x in enumerate(args):
+            assert (torch.equal(x.grad, grads[n]) if n in needed
+                    else x.grad is None)
+    leaf = q.clone().requires_grad_()
+    cs.fused_attention(leaf, k, v, mask, causal, 0.2).backward(g)
+    assert torch.equal(leaf.grad, grads[0])
+    with torch.no_grad():
+        assert not cs.fused_attention(leaf, k, v).requires_grad
+        into = torch.empty_like(q)
+        assert cs.fused_attention(leaf, k, v, mask, causal, 0.2,
+                                  out=into) is into
+    assert torch.equal(into, want)
+    assert not cs.fused_attention(q, k, v).requires_grad
+
+
+def test_what_autograd_refuses():
+    q, k, v, g, _, _ = inputs((1, 2, 1, 40, 50, 64, False, None))
+    leaf = q.clone().requires_grad_()
+    with pytest.raises(ValueError):
+        cs.fused_attention(leaf, k, v, out=torch.empty_like(q))
+    with pytest.raises(ValueError):            # as without a gradient
+        cs.fused_attention(leaf, k.expand(1, 2, 50, 64), v.expand(1, 2, 50, 64))
+    with pytest.raises(TypeError):
+        cs.fused_attention(leaf, k.half(), v.half())
+    out = cs.fused_attention(leaf, k, v)
+    first, = torch.autograd.grad(out, leaf, g, create_graph=True)
+    with pytest.raises(RuntimeError):          # no second derivative
+        first.sum().backward()
+    import torch.autograd.forward_ad as fwd
+    with fwd.dual_level(), pytest.raises((RuntimeError, NotImplementedError)):
+        cs.FusedAttentionFunction.apply(fwd.make_dual(q, g), k, v)
