@@ -99,36 +99,50 @@ _PACK_ATTENTION_BACKWARD = struct.Struct("=7if25q")
 _PACK_PAGED = struct.Struct("=8ifxxxx11q")
 
 
+def _out_of_range(error) -> ValueError:
+    return ValueError(f"a size, stride or the scale is out of range: {error}")
+
+
 def pack_attention_shape(batch, heads, kv_heads, query_len, key_len, d_head,
                          causal, scale, q, k, v, o, mask_stride=0) -> bytes:
     """The bytes of a cs_attention_shape, which every function that takes one
     also takes; q .. o: element strides, the first three of each are used.
-    (Filling the ctypes struct costs more than the launch.)"""
-    return _PACK_ATTENTION.pack(
-        batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
-        q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
-        o[0], o[1], o[2], mask_stride)
+    (Filling the ctypes struct costs more than the launch.)  Raises ValueError
+    for what the struct cannot hold: a size past 32 bits, a scale past fp32."""
+    try:
+        return _PACK_ATTENTION.pack(
+            batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
+            q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
+            o[0], o[1], o[2], mask_stride)
+    except (struct.error, OverflowError) as e:
+        raise _out_of_range(e) from None
 
 
 def pack_attention_backward_shape(batch, heads, kv_heads, query_len, key_len,
                                   d_head, causal, scale, q, k, v, o, go, dq,
                                   dk, dv, mask_stride=0) -> bytes:
     """The same with the strides of the gradients."""
-    return _PACK_ATTENTION_BACKWARD.pack(
-        batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
-        q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
-        o[0], o[1], o[2], go[0], go[1], go[2], dq[0], dq[1], dq[2],
-        dk[0], dk[1], dk[2], dv[0], dv[1], dv[2], mask_stride)
+    try:
+        return _PACK_ATTENTION_BACKWARD.pack(
+            batch, heads, kv_heads, query_len, key_len, d_head, causal, scale,
+            q[0], q[1], q[2], k[0], k[1], k[2], v[0], v[1], v[2],
+            o[0], o[1], o[2], go[0], go[1], go[2], dq[0], dq[1], dq[2],
+            dk[0], dk[1], dk[2], dv[0], dv[1], dv[2], mask_stride)
+    except (struct.error, OverflowError) as e:
+        raise _out_of_range(e) from None
 
 
 def pack_paged_shape(batch, heads, kv_heads, d_head, page_size, num_pages,
                      max_pages, fp16, scale, q, o, k, v,
                      table_stride) -> bytes:
     """The bytes of a cs_paged_shape (as pack_attention_shape)."""
-    return _PACK_PAGED.pack(
-        batch, heads, kv_heads, d_head, page_size, num_pages, max_pages,
-        fp16, scale, q[0], q[1], o[0], o[1], k[0], k[1], k[2],
-        v[0], v[1], v[2], table_stride)
+    try:
+        return _PACK_PAGED.pack(
+            batch, heads, kv_heads, d_head, page_size, num_pages, max_pages,
+            fp16, scale, q[0], q[1], o[0], o[1], k[0], k[1], k[2],
+            v[0], v[1], v[2], table_stride)
+    except (struct.error, OverflowError) as e:
+        raise _out_of_range(e) from None
 
 
 def _shape_ref(shape):

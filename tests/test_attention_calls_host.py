@@ -5,7 +5,10 @@ import glob
 import os
 import re
 
+import pytest
+
 import entropy_bounded_softmax_gb300 as cs
+from entropy_bounded_softmax_gb300 import _lib
 
 CSRC = os.path.join(os.path.dirname(cs.__file__), "csrc")
 
@@ -24,3 +27,19 @@ def test_launches_ask_the_device_for_its_sms():
              for line in _code(path).splitlines()
              if re.search(r"\b152\b", line)]
     assert lines == ["constexpr int kPagedMaxSms = 152;"]
+
+
+@pytest.mark.parametrize("key_len,scale", [(1 << 31, 0.1), (5, 1e39),
+                                           (5, "0.1")])
+def test_what_the_shapes_cannot_hold_is_refused(key_len, scale):
+    """As other arguments out of range, by ValueError."""
+    st = (64, 64, 8)
+    with pytest.raises(ValueError):
+        _lib.pack_attention_shape(1, 1, 1, 4, key_len, 8, 0, scale, st, st,
+                                  st, st)
+    with pytest.raises(ValueError):
+        _lib.pack_attention_backward_shape(1, 1, 1, 4, key_len, 8, 0, scale,
+                                           *[st] * 8)
+    with pytest.raises(ValueError):
+        _lib.pack_paged_shape(1, 1, 1, 8, 16, key_len, 4, 0, scale, st, st,
+                              st, st, 4)
