@@ -372,7 +372,6 @@ def _check_attention(query, keys, values, mask, scale, lse, same) -> None:
     name.  The calls look at the properties that they need themselves, and
     leave strides, addresses and ranges to the library; only what either
     refuses comes here for its message."""
-    import math
     import torch
     for name, x in (("query", query), ("keys", keys)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -395,8 +394,8 @@ def _check_attention(query, keys, values, mask, scale, lse, same) -> None:
     _check_heads("values", values, keys.shape, dev)
     for name, x in same.items():
         _check_heads(name, x, query.shape, dev)
-    if scale is not None and not (scale > 0.0 and math.isfinite(scale)):
-        raise ValueError("scale must be positive and finite")
+    if scale is not None and not 0.0 < scale <= 2.0 ** 127:
+        raise ValueError("scale must be positive and at most 2^127")
     if mask is not None:
         if (not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool
                 or mask.device != query.device
@@ -552,7 +551,6 @@ def _check_paged(query, key_pages, value_pages, page_table, lengths, scale,
                  out) -> None:
     """Raises what is wrong with the arguments of paged attention, if
     anything is (as _check_attention)."""
-    import math
     import torch
     for name, x, dim in (("query", query, 3), ("key_pages", key_pages, 4)):
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
@@ -602,8 +600,8 @@ def _check_paged(query, key_pages, value_pages, page_table, lengths, scale,
                              "the query's device")
     if B > 1 and page_table.stride(0) < page_table.shape[1]:
         raise ValueError("page_table's rows must not overlap")
-    if scale is not None and not (scale > 0.0 and math.isfinite(scale)):
-        raise ValueError("scale must be positive and finite")
+    if scale is not None and not 0.0 < scale <= 2.0 ** 127:
+        raise ValueError("scale must be positive and at most 2^127")
 
 
 def _paged_ok(torch, query, key_pages, value_pages, page_table, lengths, out):

@@ -604,6 +604,9 @@ int64_t heads_extent(const cs_attention_shape& s, int32_t heads, int32_t length,
     return 2 * last;
 }
 
+// The kernels multiply scores by scale log2(e), which has to be finite too.
+bool good_scale(float scale) { return scale > 0.0f && scale <= 0x1p127f; }
+
 cs_status check_attention_shape(const cs_attention_shape* s) {
     if (!s) return CS_ERR_INVALID_ARG;
     if (s->batch < 0 || s->heads < 1 || s->kv_heads < 1 || s->query_len < 0 ||
@@ -612,7 +615,7 @@ cs_status check_attention_shape(const cs_attention_shape* s) {
     if (s->d_head > cs::kFattnMaxDHead) return CS_ERR_OOM;
     if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
     if (s->causal != 0 && s->causal != 1) return CS_ERR_INVALID_ARG;
-    if (!isfinite(s->scale) || !(s->scale > 0.0f)) return CS_ERR_INVALID_ARG;
+    if (!good_scale(s->scale)) return CS_ERR_INVALID_ARG;
     if (s->heads > cs::kFattnMaxHeads || s->batch > cs::kFattnMaxBatch ||
         ceil_div(s->query_len, 128) > cs::kFattnMaxTiles ||
         ceil_div(s->key_len, 128) > cs::kFattnMaxTiles)
@@ -696,7 +699,7 @@ cs_status check_paged_shape(const cs_paged_shape* s) {
     if (s->d_head > cs::kPagedMaxDHead) return CS_ERR_OOM;
     if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
     if (s->fp16 != 0 && s->fp16 != 1) return CS_ERR_INVALID_ARG;
-    if (!isfinite(s->scale) || !(s->scale > 0.0f)) return CS_ERR_INVALID_ARG;
+    if (!good_scale(s->scale)) return CS_ERR_INVALID_ARG;
     if (static_cast<int64_t>(s->max_pages) * s->page_size > kPagedMaxTokens ||
         s->batch > cs::kFattnMaxBatch || s->heads > cs::kFattnMaxHeads)
         return CS_ERR_DIM_MISMATCH;

@@ -507,7 +507,7 @@ typedef struct cs_attention_shape {
     int32_t d_head;     /* 8..128, a multiple of 8                          */
     int32_t causal;     /* 1: query i keeps keys j <= i + key_len - query_len
                            (the last query sees every key); 0: all keys     */
-    float scale;        /* of the scores; positive and finite               */
+    float scale;        /* of the scores; positive, at most 2^127           */
     int64_t q_stride[3];   /* batch, head, position; non-negative           */
     int64_t k_stride[3];   /* multiples of 8 elements (a dimension of size  */
     int64_t v_stride[3];   /* 1 may have any); an input's may not be 0      */
@@ -619,7 +619,7 @@ typedef struct cs_paged_shape {
     int32_t max_pages;  /* entries of a page-table row, >= 0; at most 2^30
                            tokens a row, 2^36 over the batch               */
     int32_t fp16;       /* 0: query, pages and out are bf16; 1: fp16        */
-    float scale;        /* of the scores; positive and finite               */
+    float scale;        /* of the scores; positive, at most 2^127           */
     int64_t q_stride[2];   /* batch, head; elements, non-negative           */
     int64_t o_stride[2];   /* multiples of 8                                */
     int64_t k_stride[3];   /* page, slot, head                              */

@@ -1,6 +1,7 @@
 """Fused and paged attention on the CPU: arguments at the far end of their
 ranges, and rules of the sources that no GPU here can show.  No CUDA call is
 made."""
+import ctypes
 import glob
 import os
 import re
@@ -43,3 +44,43 @@ def test_what_the_shapes_cannot_hold_is_refused(key_len, scale):
     with pytest.raises(ValueError):
         _lib.pack_paged_shape(1, 1, 1, 8, 16, key_len, 4, 0, scale, st, st,
                               st, st, 4)
+
+
+def _attention_shape(**kw):
+    """A shape of [B, H, S, D] tensors with these members set."""
+    s = cs.cs_attention_shape(3, 2, 2, 4, 5, 8, 0, 0.1)
+    for name, length in dict(q=4, o=4, k=5, v=5).items():
+        setattr(s, name + "_stride",
+                (ctypes.c_int64 * 3)(16 * length, 8 * length, 8))
+    s.mask_stride = 5
+    for name, value in kw.items():
+        setattr(s, name, value)
+    return s
+
+
+def _check(s):
+    """The status for far-apart fake device addresses."""
+    return cs.cs_check_fused_attention_args(
+        *(1 << (30 + i) for i in range(6)), s)
+
+
+def _paged_shape(**kw):
+    s = cs.cs_paged_shape(3, 2, 2, 8, 16, 4, 2, 0, 0.1, (16, 8), (16, 8),
+                          (256, 16, 8), (256, 16, 8), 2)
+    for name, value in kw.items():
+        setattr(s, name, value)
+    return s
+
+
+def _check_paged(s):
+    return cs.cs_check_paged_attention_args(
+        *(1 << (30 + i) for i in range(7)), s, 1 << 40, 1 << 29)
+
+
+@pytest.mark.parametrize("scale,status", [(0.1, 0), (2.0 ** 127, 0),
+                                          (2.0 ** 127.2, 8), (3e38, 8)])
+def test_scales_stay_finite_in_base_2(scale, status):
+    """A score of 0 is 0 whatever the scale; 0 times an infinite factor is
+    NaN."""
+    assert _check(_attention_shape(scale=scale)) == status
+    assert _check_paged(_paged_shape(scale=scale)) == status
