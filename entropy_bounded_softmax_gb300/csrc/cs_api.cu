@@ -647,9 +647,13 @@ cs_status check_spans(const Span* x, int n) {
     return CS_OK;
 }
 
+// The most bytes, or entries, between the rows of a mask or a page table, so
+// that their extent stays within 64 bits.
+constexpr int64_t kMaxRowStride = int64_t(1) << 40;
+
 int64_t mask_extent(const cs_attention_shape& s, const uint8_t* mask) {
     if (!mask || s.batch == 0 || s.key_len == 0) return 0;
-    if (s.batch > 1 && s.mask_stride < s.key_len) return -1;
+    if (s.batch > 1 && (s.mask_stride < s.key_len || s.mask_stride > kMaxRowStride)) return -1;
     return s.key_len + (s.batch > 1 ? (s.batch - 1) * s.mask_stride : 0);
 }
 
@@ -1421,7 +1425,8 @@ cs_status cs_check_paged_attention_args(
         return CS_ERR_DIM_MISMATCH;
     const int64_t need = cs_paged_attention_workspace(shape);
     if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
-    if (s.batch > 1 && s.table_stride < s.max_pages) return CS_ERR_INVALID_ARG;
+    if (s.batch > 1 && (s.table_stride < s.max_pages || s.table_stride > kMaxRowStride))
+        return CS_ERR_INVALID_ARG;
     const int64_t rows[2] = {s.batch, s.heads};
     const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
     const int64_t table = s.max_pages == 0 ? 0

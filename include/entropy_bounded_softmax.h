@@ -516,7 +516,8 @@ typedef struct cs_attention_shape {
     int64_t dq_stride[3];  /* backward: the gradients                       */
     int64_t dk_stride[3];
     int64_t dv_stride[3];
-    int64_t mask_stride;   /* bytes between the mask's rows, >= key_len     */
+    int64_t mask_stride;   /* bytes between the mask's rows, >= key_len, at
+                              most 2^40                                     */
 } cs_attention_shape;
 
 /*
@@ -624,7 +625,8 @@ typedef struct cs_paged_shape {
     int64_t o_stride[2];   /* multiples of 8                                */
     int64_t k_stride[3];   /* page, slot, head                              */
     int64_t v_stride[3];
-    int64_t table_stride;  /* entries between page-table rows, >= max_pages */
+    int64_t table_stride;  /* entries between page-table rows, >= max_pages,
+                              at most 2^40                                  */
 } cs_paged_shape;
 
 /*

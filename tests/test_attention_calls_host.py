@@ -84,3 +84,15 @@ def test_scales_stay_finite_in_base_2(scale, status):
     NaN."""
     assert _check(_attention_shape(scale=scale)) == status
     assert _check_paged(_paged_shape(scale=scale)) == status
+
+
+@pytest.mark.parametrize("stride", [1 << 20, 1 << 59, 1 << 61, 1 << 62,
+                                    (1 << 63) - 1, -(1 << 62)])
+def test_row_strides_do_not_wrap(stride):
+    """Strides of a mask's and a table's rows whose products pass 64 bits:
+    refused, instead of an extent that has wrapped around."""
+    want = 0 if stride == 1 << 20 else 8
+    mask = _attention_shape(mask_stride=stride)
+    assert cs.cs_check_fused_attention_args(
+        *(1 << (30 + i) for i in range(5)), 1 << 36, mask) == want
+    assert _check_paged(_paged_shape(table_stride=stride)) == want
