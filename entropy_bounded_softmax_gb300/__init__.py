@@ -740,15 +740,19 @@ def _fused_attention_function():
         """Autograd wrapper of :func:`fused_attention`: ``apply(query, keys,
         values, mask, causal, scale, return_lse)``; query, keys and values
         receive gradients, once (there is no second derivative, forward mode
-        or vmap rule: torch refuses them).  Inputs whose strides the kernels
-        do not take (expanded ones, for example) are copied.  The backward
-        pass computes the three gradients together, and hands on those that
-        are needed."""
+        or vmap rule: torch refuses them).  Inputs and masks whose strides
+        the kernels do not take (expanded ones, for example) are copied.  The
+        backward pass computes the three gradients together, and hands on
+        those that are needed."""
 
         @staticmethod
         def forward(ctx, query, keys, values, mask=None, causal=False,
                     scale=None, return_lse=False):
             query, keys, values = (strided(x) for x in (query, keys, values))
+            if (isinstance(mask, torch.Tensor) and mask.dim() == 2
+                    and (mask.stride(1) != 1
+                         or mask.stride(0) < mask.shape[1])):
+                mask = mask.contiguous()
             out, lse = fused_attention(query, keys, values, mask, causal,
                                        scale, return_lse=True)
             ctx.save_for_backward(query, keys, values, out, lse, mask)

@@ -128,3 +128,19 @@ def test_what_autograd_refuses():
     import torch.autograd.forward_ad as fwd
     with fwd.dual_level(), pytest.raises((RuntimeError, NotImplementedError)):
         cs.FusedAttentionFunction.apply(fwd.make_dual(q, g), k, v)
+
+
+def test_autograd_takes_an_expanded_mask():
+    """One sequence's mask for all of them, and a transposed one."""
+    q, k, v, g, _, _ = inputs((2, 4, 2, 60, 130, 64, False, None))
+    one = torch.arange(130, device="cuda")[None] % 3 != 1
+    tall = torch.empty(130, 2, dtype=torch.bool, device="cuda")
+    tall.copy_(one.T)
+    want, lse = cs.fused_attention(q, k, v, one.repeat(2, 1), return_lse=True)
+    dq, _, _ = cs.fused_attention_backward(q, k, v, want, lse, g,
+                                           one.repeat(2, 1))
+    for mask in (one.expand(2, 130), tall.T):
+        leaf = q.clone().requires_grad_()
+        out = cs.FusedAttentionFunction.apply(leaf, k, v, mask)
+        out.backward(g)
+        assert torch.equal(out, want) and torch.equal(leaf.grad, dq)
