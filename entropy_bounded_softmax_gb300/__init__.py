@@ -743,7 +743,10 @@ def _fused_attention_function():
         or vmap rule: torch refuses them).  Inputs and masks whose strides
         the kernels do not take (expanded ones, for example) are copied.  The
         backward pass computes the three gradients together, and hands on
-        those that are needed."""
+        those that are needed.  It can be captured into a CUDA graph after a
+        warm-up on a side stream, as any of torch's; let no eager graph of
+        the same leaves live then, whose accumulation is tied to the stream
+        of its first use."""
 
         @staticmethod
         def forward(ctx, query, keys, values, mask=None, causal=False,

@@ -10,6 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import entropy_bounded_softmax_gb300 as cs
+from fused_attention_parity import Forward, excess, gradients
 from test_fused_attention_gpu import inputs
 
 pytestmark = pytest.mark.gpu
@@ -53,7 +54,7 @@ def test_paged_cost_follows_the_batch():
             < 16 * _best_us(lambda: cs.paged_attention(*small)))
 
 
-@pytest.mark.parametrize("batch", [75, 76, 77, 700, 5000])
+@pytest.mark.parametrize("batch", [75, 303, 304, 305, 700, 5000])
 def test_paged_large_batches(batch):
     """Around and far past the number of groups, whole rows against shares and
     a join: the same sequences in a table of few pages are not cut."""
@@ -144,3 +145,140 @@ def test_autograd_takes_an_expanded_mask():
         out = cs.FusedAttentionFunction.apply(leaf, k, v, mask)
         out.backward(g)
         assert torch.equal(out, want) and torch.equal(leaf.grad, dq)
+
+
+def _attention64(q, k, v, g, scale):
+    """One head in 64 bits on the GPU: out, lse, dq, dk, dv of all keys."""
+    q, k, v, g = (x.double() for x in (q, k, v, g))
+    s = q @ k.T * scale
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse[:, None])
+    out = p @ v
+    ds = p * (g @ v.T - (g * out).sum(-1, keepdim=True))
+    return out, lse, ds @ k * scale, ds.T @ q * scale, p.T @ g
+
+
+@pytest.mark.parametrize("B,H,Hk,Sq,Sk", [
+    (65535, 1, 1, 1, 3),           # the most sequences
+    (1, 1 << 20, 1 << 18, 1, 5),   # the most heads
+    (1, 1, 1, 8388480, 9),         # the most queries
+    (1, 1, 1, 3, 8388480),         # the most keys
+])
+def test_largest_sizes(B, H, Hk, Sq, Sk):
+    """The far ends of the ranges, with heads of 8.  Few keys and queries: a
+    few heads by elements.  Long sums: by norms, where P and dS, delta's out
+    and the result are rounded by at most 2^-8 each (less on average), and an
+    accumulator that truncates loses at most 2^-24 of the sum on average at
+    each of its 2^16 steps: 2^-8."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def heads(h, n):
+        return torch.randn(B, h, n, 8, device="cuda", generator=gen).bfloat16()
+
+    q, g, k, v = heads(H, Sq), heads(H, Sq), heads(Hk, Sk), heads(Hk, Sk)
+    out, lse = cs.fused_attention(q, k, v, return_lse=True)
+    dq, dk, dv = cs.fused_attention_backward(q, k, v, out, lse, g)
+    assert cs.get_error() == set()
+    group = H // Hk
+    if Sq * Sk < 100:
+        for b, hk in ((0, 0), (B // 2, Hk // 2), (B - 1, Hk - 1)):
+            b, h = slice(b, b + 1), slice(hk * group, (hk + 1) * group)
+            hk = slice(hk, hk + 1)
+            ref = Forward(q[b, h], k[b, hk], v[b, hk], None, False, 8 ** -0.5)
+            assert excess(out[b, h], ref.out, ref.out_tol()) <= 1
+            assert excess(lse[b, h], ref.lse, ref.lse_tol()) <= 1
+            want, tol = gradients(ref, out[b, h], g[b, h])
+            for x, y, t in zip((dq[b, h], dk[b, hk], dv[b, hk]), want, tol):
+                assert excess(x, y, t) <= 1
+        return
+    ref = _attention64(q[0, 0], k[0, 0], v[0, 0], g[0, 0], 8 ** -0.5)
+    assert float((lse[0, 0].double() - ref[1]).abs().max()) < 2.0 ** -12
+    for x, y in zip((out, dq, dk, dv), (ref[0], *ref[2:])):
+        assert float((x[0, 0].double() - y).norm() / y.norm()) < 4 * 2.0 ** -8
+
+
+def test_pages_used_twice():
+    """A page that two sequences share, and one that a sequence has twice."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    k, v = (torch.randn(4, 16, 2, 64, device="cuda", generator=gen).bfloat16()
+            for _ in range(2))
+    q = torch.randn(2, 4, 64, device="cuda", generator=gen).bfloat16()
+    table = torch.tensor([[2, 0, 2, 3], [2, 2, 1, 0]], dtype=torch.int32,
+                         device="cuda")
+    lengths = torch.tensor([64, 41], dtype=torch.int32, device="cuda")
+    got = cs.paged_attention(q, k, v, table, lengths)
+    rows = table.flatten().long()
+    apart = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    want = cs.paged_attention(q, k[rows].contiguous(), v[rows].contiguous(),
+                              apart, lengths)
+    assert torch.equal(got, want) and cs.get_error() == set()
+
+
+def test_longest_cache():
+    """A row of the table with room for 2^30 tokens, in one page and in pages
+    of 2^20 slots, the tokens at the far end of it."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(1, 2, 8, device="cuda", generator=gen).bfloat16()
+    # All slots the same token: out is its value, lse the score plus ln 2^30.
+    k, v = (torch.randn(1, 1, 1, 8, device="cuda", generator=gen).bfloat16()
+            for _ in range(2))
+    many = (x.expand(1, 1 << 30, 1, 8) for x in (k, v))
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([1 << 30], dtype=torch.int32, device="cuda")
+    out, lse = cs.paged_attention(q, *many, table, lengths, return_lse=True)
+    s = (q.double() @ k[0, 0, 0].double()) * 8 ** -0.5
+    # Half a step of bf16, and at most 2^-24 on average at each of the 2^16
+    # steps of an accumulator that truncates.
+    value = v[0, 0].double()
+    assert ((out.double() - value).abs() <= 2.0 ** -7 * value.abs()).all()
+    # (The sums are of whole multiples of one weight, fewer than 2^24.)
+    assert float((lse.double() - s - 30 * math.log(2)).abs().max()) < 2.0 ** -16
+    page = 1 << 20
+    k, v = (torch.randn(2, page, 1, 8, device="cuda", generator=gen).bfloat16()
+            for _ in range(2))
+    table = torch.zeros(3, 1024, dtype=torch.int32, device="cuda")
+    table[1, 1] = 1
+    lengths = torch.tensor([5, page + 3, 0], dtype=torch.int32, device="cuda")
+    q = torch.randn(3, 2, 8, device="cuda", generator=gen).bfloat16()
+    out = cs.paged_attention(q, k, v, table, lengths)
+    for b, keys, values in ((0, k[0, :5], v[0, :5]),
+                            (1, torch.cat([k[0], k[1, :3]]),
+                             torch.cat([v[0], v[1, :3]]))):
+        want = _attention64(q[b], keys[:, 0], values[:, 0], q[b], 8 ** -0.5)[0]
+        # Half a step of bf16; the sums' fp32, cancelling, far below it.
+        assert float((out[b].double() - want).norm() / want.norm()) < 2.0 ** -8
+    assert (out[2] == 0).all() and cs.get_error() == set()
+
+
+def test_captured_training_step():
+    """Forward and backward through autograd, captured after a warm-up on a
+    side stream, and replayed on new inputs."""
+    first = inputs((2, 4, 2, 90, 150, 64, True, "right"), 20)
+    second = inputs((2, 4, 2, 90, 150, 64, True, "right"), 21)
+    leaves = [x.clone().requires_grad_() for x in first[:3]]
+    g, mask = first[3].clone(), first[4]
+
+    def step():
+        out = cs.fused_attention(*leaves, mask, True)
+        return (out.detach(), *torch.autograd.grad(out, leaves, g))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results = step()
+    for q, k, v, up, _, _ in (second, first):
+        with torch.no_grad():
+            for dst, src in zip((*leaves, g), (q, k, v, up)):
+                dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        out, lse = cs.fused_attention(q, k, v, mask, True, return_lse=True)
+        want = (out, *cs.fused_attention_backward(q, k, v, out, lse, up, mask,
+                                                  True))
+        for a, b in zip(results, want):
+            assert torch.equal(a, b)
