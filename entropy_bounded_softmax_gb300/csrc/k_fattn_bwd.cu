@@ -47,10 +47,11 @@
 //               and zeros over the removed keys' rows of K.
 //
 // Measured, both launches: 2 x 8 heads x 4096 of 128, causal, 163 us (1.05
-// PFLOP/s of the five products; bound by shared memory as the forward is, the
-// tensor pipe 61 and 69% busy); 32 x 8 heads x 512 of 64, 76 us (bound by the
-// chain of each block's two elementwise phases and by the starts and ends of
-// the CTAs: the tensor pipe 21 and 27% busy).
+// PFLOP/s of the five products, 1.47 of the seven; the tensor pipe 60 and 69%
+// busy, and what the rest goes to, as in the forward, not measured); 32 x 8
+// heads x 512 of 64, 76 us (bound by the chain of each block's two elementwise
+// phases and by the starts and ends of the CTAs: the tensor pipe 22 and 28%
+// busy).
 //
 // P and dS are rounded to bf16, the operand type next to bf16 values (a sum
 // over many rows averages those roundings); everything else stays fp32.

@@ -9,10 +9,12 @@
 // use the same K and V.  Tensor memory holds each tile's scores (a block's
 // columns) and output (DP columns); a tile's weights overwrite its scores as
 // bf16 and are the next product's A operand there.
-//   d_head > 64   blocks of 128 keys, one CTA an SM.  Shared memory bounds it:
-//                 the products read 192 KB a pair of blocks and the copies
-//                 write 64, 2050 of its 3000 cycles (2 x 8 heads x 4096 of
-//                 128, causal: 52 us, 1.3 PFLOP/s);
+//   d_head > 64   blocks of 128 keys, one CTA an SM.  A pair of blocks takes
+//                 3000 cycles: the tensor pipe needs 2048 of them for its four
+//                 products, shared memory 2050 for the 192 KB that they read
+//                 and the 64 that the copies write; what the other 950 go to
+//                 is not measured (2 x 8 heads x 4096 of 128, causal: 52 us,
+//                 1.3 PFLOP/s, tensor pipe 58% busy);
 //   d_head <= 64  blocks of 64 keys, two CTAs an SM, which four tiles keep
 //                 busier (32 x 8 heads x 512: 24.2 us; two CTAs of one tile
 //                 with two score buffers 28.5, three of one tile 28.4, one of

@@ -3,8 +3,9 @@
 // (token j in slot j % page_size of page table[b][j / page_size]):
 //   s_j = scale q . k_j,  out = sum e^(s_j - m) v_j / sum e^(s_j - m).
 //
-// Every key and value is read once and used for the query heads that share
-// its head: bound by the cache's bytes.  A sequence's tokens are steps of 64.
+// Every key and value is read once for up to 16 query heads that share its
+// head, and again for every 16 more: bound by the cache's bytes.  A sequence's
+// tokens are steps of 64.
 // The steps of the batch, one sequence after the other, are dealt to groups
 // of CTAs in equal shares, so that a batch of any lengths keeps every SM
 // streaming to the end.  A group has a CTA for every row, a key head's tile
@@ -20,12 +21,13 @@
 // empty, and the bytes take longer).  The warps' sums are joined in shared
 // memory; a sequence that lies in one share is finished there, the others'
 // parts (maximum, sum, unnormalised output) go to the workspace and a second
-// small kernel, launched to overlap the first's end, joins them.  Where no
+// small kernel, launched to overlap the first's end, joins them, with a CTA a
+// head for every sequence or place where one can be cut.  Where no
 // sequence can be longer than a few steps every CTA takes one whole row of one
 // sequence, and there is no second kernel.
 //
 // Measured with 8 key heads of 128 in bf16: 83 us for 32 query heads of 131072
-// tokens (6.5 TB/s of the cache, DRAM 84% busy), 39 us for 32 sequences of up
+// tokens (6.5 TB/s of the cache, DRAM 83% busy), 39 us for 32 sequences of up
 // to 4096 tokens (5.1 TB/s; the start of the copies, 5 us, and the join, 3,
 // do not overlap with them), 4.3 us for a call of few tokens.
 //
