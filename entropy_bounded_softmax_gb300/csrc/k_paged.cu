@@ -590,8 +590,9 @@ paged_kernel(const PagedTask t) {
 // joins the sequence that is cut there first, so that what the launch takes
 // grows with the batch and not with its square (32768 sequences of up to 32
 // tokens, 8 heads of 64 on one key head: 1015 us, with a CTA for every sequence
-// 7368; 4096 sequences: 124 and 172).
-template <int DP, class T>
+// 7368; 4096 sequences: 124 and 172).  CUTS: the latter (an instance of its own:
+// in one kernel with a branch 7 sequences of up to 1531 tokens took 1% longer).
+template <int DP, class T, bool CUTS>
 __global__ void __launch_bounds__(kPgThreads)
 paged_join_kernel(const PagedTask t) {
     constexpr int kUnits = DP / 8, kRows = kPgThreads / kUnits;
@@ -600,7 +601,7 @@ paged_join_kernel(const PagedTask t) {
     const int h = blockIdx.x;
     int b = blockIdx.y, begin = 0, share = 1;
     bool bad, cut = true;
-    if (t.batch < t.groups) {
+    if constexpr (!CUTS) {
         share = share_of(t, steps_before(t, t.batch, scan));
         begin = steps_before(t, b, scan);
     } else {
@@ -719,11 +720,11 @@ cudaError_t launch(const PagedTask& t, int slot, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.split) return e;
     if (t.groups == 1) return cudaSuccess;   // one share: nothing is cut
-    return launch_shaped(
-        paged_join_kernel<DP, T>,
-        {dim3(t.heads, t.batch < t.groups ? t.batch : t.groups - 1), kPgThreads, 0, stream, true,
-         1},
-        t);
+    const bool cuts = t.batch >= t.groups;
+    return launch_shaped(cuts ? paged_join_kernel<DP, T, true> : paged_join_kernel<DP, T, false>,
+                         {dim3(t.heads, cuts ? t.groups - 1 : t.batch), kPgThreads, 0, stream,
+                          true, 1},
+                         t);
 }
 
 template <class T>
