@@ -467,7 +467,8 @@ def fused_attention(query, keys, values, mask=None, causal: bool = False,
 
     Where autograd records and query, keys or values require a gradient, the
     call goes through :class:`FusedAttentionFunction`: the output carries the
-    gradient, the log of the sums does not, and ``out`` is refused.
+    gradient, the log of the sums does not, and ``out`` is refused.  (Tangents
+    of forward mode are not seen here; the class refuses them.)
     """
     import torch
     same = () if out is None else (out,)
