@@ -13,7 +13,11 @@ for autograd.
 Attention of language models: :func:`fused_attention` (softmax(scale q k^T) v
 without the scores in memory), :func:`fused_attention_backward`, joined for
 autograd by :class:`FusedAttentionFunction`, and :func:`paged_attention` (one
-new token per sequence over a key-value cache in pages).
+new token per sequence over a key-value cache in pages).  For several new tokens
+a sequence over such a cache: :func:`paged_extend` (pages and slots for them),
+:func:`paged_write` (their keys and values into it) and
+:func:`paged_tree_attention` (a tree of drafted tokens, or a prompt's next
+chunk).
 
 PyTorch supplies device memory and the current stream; the computation runs
 in the hand-written CUDA kernels of ``libcsoftmax.so`` behind a C ABI
@@ -35,6 +39,11 @@ from ._lib import (CONSTANTS, cs_attention_softmax, cs_attention_softmax_ex,
                    cs_check_paged_attention_args, cs_paged_attention,
                    cs_paged_attention_workspace,
                    cs_paged_shape,
+                   cs_extend_shape, cs_write_shape, cs_tree_shape,
+                   cs_paged_extend, cs_check_paged_extend_args,
+                   cs_paged_write, cs_check_paged_write_args,
+                   cs_paged_tree_attention, cs_paged_tree_attention_workspace,
+                   cs_check_paged_tree_attention_args,
                    cs_check_biencoder_args, cs_plan_biencoder_host,
                    cs_check_args, cs_check_attention_args,
                    cs_check_backward_args, cs_constrained_softmax,
@@ -74,6 +83,12 @@ __all__ = [
     "paged_attention", "cs_paged_shape", "cs_paged_attention",
     "cs_paged_attention_workspace",
     "cs_check_paged_attention_args",
+    "paged_extend", "paged_write", "paged_tree_attention",
+    "cs_extend_shape", "cs_write_shape", "cs_tree_shape",
+    "cs_paged_extend", "cs_check_paged_extend_args",
+    "cs_paged_write", "cs_check_paged_write_args",
+    "cs_paged_tree_attention", "cs_paged_tree_attention_workspace",
+    "cs_check_paged_tree_attention_args",
 ]
 
 # Defaults of section 2.1's signature.
@@ -87,7 +102,7 @@ VARIANTS = {"auto": CONSTANTS["CS_VARIANT_AUTO"],
             "cluster": CONSTANTS["CS_VARIANT_CLUSTER"]}
 ERROR_BITS = {name: 1 << CONSTANTS[f"CS_ERR_{name}"]
               for name in ("NAN_INPUT", "INF_INPUT", "ENTROPY_OVERFLOW",
-                           "TIMEOUT", "BAD_PAGE")}
+                           "TIMEOUT", "BAD_PAGE", "OUT_OF_PAGES")}
 
 
 _STAY = contextlib.nullcontext()
@@ -683,6 +698,316 @@ def paged_attention(query, key_pages, value_pages, page_table, lengths,
     if st != 0:
         _check_paged(*given, scale, out)
         raise CsError(st, "cs_paged_attention")
+    return (out, lse) if return_lse else out
+
+
+def _is_int32(torch, x, shape, dev):
+    return (isinstance(x, torch.Tensor) and x.dtype is torch.int32
+            and x.get_device() == dev and x.shape == shape
+            and x.is_contiguous())
+
+
+def _check_extend(page_table, lengths, new_lengths, free_pages, page_size,
+                  max_new, held, cursor) -> None:
+    """Raises what is wrong with the arguments of paged_extend, if anything
+    is (as _check_attention)."""
+    import torch
+    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
+        raise ValueError("page_table must be a CUDA tensor")
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)
+            or (page_table.shape[0] > 1
+                and page_table.stride(0) < page_table.shape[1])):
+        raise ValueError("page_table must be an int32 [batch, pages] tensor "
+                         "with contiguous rows that do not overlap")
+    batch = page_table.shape[0]
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a 1-D tensor")
+    for name, x, n in (("lengths", lengths, batch),
+                       ("new_lengths", new_lengths, batch),
+                       ("free_pages", free_pages, free_pages.shape[0]),
+                       ("held", held, batch), ("cursor", cursor, 1)):
+        if x is None and name in ("held", "cursor"):
+            continue
+        if not _is_int32(torch, x, (n,), page_table.get_device()):
+            raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor "
+                             "on the page table's device")
+    if page_size < 1 or max_new < 0:
+        raise ValueError("page_size must be positive and max_new not negative")
+
+
+def paged_extend(page_table, lengths, new_lengths, free_pages, page_size: int,
+                 max_new: int, held=None, cursor=None):
+    """Pages and slots for new tokens of a paged key-value cache, on the GPU.
+
+    ``page_table`` int32 [B, n], as :func:`paged_attention` reads it;
+    ``lengths`` int32 [B]: tokens in the cache; ``new_lengths`` int32 [B]: how
+    many more come, at most ``max_new``; ``held`` int32 [B]: the pages that
+    each sequence has, the first of its row (default: those of its tokens; more
+    where drafted tokens were given up).  Sequence after sequence takes the
+    pages that it is short of from ``free_pages`` (int32 [F]), in that order
+    from entry ``cursor`` (int32 [1], default 0) on.
+
+    Writes the new pages into ``page_table`` behind the held ones, and returns
+    ``(slots, totals, held, cursor)``: int64 [B, max_new], the slot
+    (page * page_size + place in the page) of each new token and -1 behind the
+    last, which :func:`paged_write` takes; int32 [B], the lengths with the new
+    tokens; int32 [B], the pages now held; int32 [1], the list's next entry.
+    Nothing else changes; the results are new tensors, to be handed to the next
+    call.  Asynchronous on the current stream.  Where the list runs out,
+    sequences get what is left in their order, tokens without a page have slot
+    -1 and are not in ``totals``; that and arguments out of range, which are
+    left out, are reported by :func:`get_error`.
+    """
+    import torch
+    given = (page_table, lengths, new_lengths, free_pages)
+    if not (isinstance(page_table, torch.Tensor)
+            and page_table.dtype is torch.int32 and page_table.is_cuda
+            and page_table.dim() == 2 and page_table.stride(1) == 1
+            and isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1
+            and page_size > 0 and max_new >= 0):
+        _check_extend(*given, page_size, max_new, held, cursor)
+    batch, width = page_table.shape
+    dev, rows = page_table.get_device(), (batch,)
+    if not (_is_int32(torch, lengths, rows, dev)
+            and _is_int32(torch, new_lengths, rows, dev)
+            and _is_int32(torch, free_pages, free_pages.shape, dev)
+            and (held is None or _is_int32(torch, held, rows, dev))
+            and (cursor is None or _is_int32(torch, cursor, (1,), dev))):
+        _check_extend(*given, page_size, max_new, held, cursor)
+    device = page_table.device
+    slots = torch.empty((batch, max_new), dtype=torch.int64, device=device)
+    totals, have, after = torch.empty(
+        2 * batch + 1, dtype=torch.int32, device=device).split(
+            (batch, batch, 1))
+    shape = _lib.pack_extend_shape(batch, max_new, width, page_size,
+                                   free_pages.shape[0], page_table.stride(0))
+    with _on_device(device):
+        st = cs_paged_extend(
+            page_table.data_ptr(), lengths.data_ptr(), new_lengths.data_ptr(),
+            None if held is None else held.data_ptr(), free_pages.data_ptr(),
+            None if cursor is None else cursor.data_ptr(), slots.data_ptr(),
+            totals.data_ptr(), have.data_ptr(), after.data_ptr(), shape,
+            _stream_handle(device))
+    if st != 0:
+        _check_extend(*given, page_size, max_new, held, cursor)
+        raise CsError(st, "cs_paged_extend")
+    return slots, totals, have, after
+
+
+def _check_rows(name, x, dtype, shape, device) -> None:
+    """Raises what is wrong with a tensor of rows over a contiguous head
+    dimension."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if x.numel() and (x.stride(-1) != 1 or x.data_ptr() & 15
+                      or any(n > 1 and s % 8
+                             for n, s in zip(shape[:-1], x.stride()))):
+        raise ValueError(f"{name}'s last dimension must be contiguous, its "
+                         "base 16-byte aligned and its other strides "
+                         "multiples of 8 elements")
+
+
+def _check_write(keys, values, slots, key_pages, value_pages) -> None:
+    """Raises what is wrong with the arguments of paged_write, if anything
+    is (as _check_attention)."""
+    import torch
+    for name, x in (("keys", keys), ("key_pages", key_pages)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.dim() != 4:
+            raise ValueError(f"{name} must have 4 dimensions")
+    dtype, dev = keys.dtype, keys.device
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("keys must be a bfloat16 or float16 tensor")
+    B, T, Hk, D = keys.shape
+    if key_pages.shape[2] != Hk or key_pages.shape[3] != D:
+        raise ValueError("key_pages must be [pages, page_size, kv_heads, "
+                         "d_head] with the keys' heads and d_head")
+    if D < 8 or D > 256 or D % 8:
+        raise ValueError("d_head must be a multiple of 8 in 8..256")
+    if Hk < 1 or key_pages.shape[1] < 1:
+        raise ValueError("there must be a head, and page_size positive")
+    for name, x, shape in (("keys", keys, keys.shape),
+                           ("values", values, keys.shape),
+                           ("key_pages", key_pages, key_pages.shape),
+                           ("value_pages", value_pages, key_pages.shape)):
+        _check_rows(name, x, dtype, shape, dev)
+    if (not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64
+            or slots.device != dev or tuple(slots.shape) != (B, T)
+            or (T > 1 and slots.stride(1) != 1)
+            or (B > 1 and slots.stride(0) < T)):
+        raise ValueError("slots must be an int64 [batch, new_tokens] tensor "
+                         "with contiguous rows that do not overlap, on the "
+                         "keys' device")
+
+
+def paged_write(keys, values, slots, key_pages, value_pages) -> None:
+    """Puts the keys and values of new tokens into a paged key-value cache.
+
+    ``keys`` and ``values`` [B, T, Hk, D], ``key_pages`` and ``value_pages``
+    [pages, page_size, Hk, D], all bf16 or all fp16 on one CUDA device, D a
+    multiple of 8 up to 256, any strides that are multiples of 8 elements over a
+    contiguous head dimension (slices of a packed projection, keys and values
+    in one buffer); ``slots`` int64 [B, T], from :func:`paged_extend`: token i
+    of sequence b goes to slot ``slots[b, i] % page_size`` of page
+    ``slots[b, i] // page_size``.  Tokens whose slot is negative are passed
+    over; so are those whose slot lies past the cache, which
+    :func:`get_error` reports.  No two tokens may have the same slot.  The
+    pages are written in place, nothing else in them changes; asynchronous on
+    the current stream.  For serving: the write is not recorded by autograd.
+    """
+    import torch
+    given = (keys, values, slots, key_pages, value_pages)
+    t = torch.Tensor
+    if not (isinstance(keys, t) and isinstance(values, t)
+            and isinstance(slots, t) and isinstance(key_pages, t)
+            and isinstance(value_pages, t) and keys.dim() == 4
+            and key_pages.dim() == 4 and slots.dim() == 2):
+        _check_write(*given)
+    dtype, dev = keys.dtype, keys.get_device()
+    ks, ps = keys.shape, key_pages.shape
+    if not ((dtype is torch.bfloat16 or dtype is torch.float16) and dev >= 0
+            and values.dtype is dtype and key_pages.dtype is dtype
+            and value_pages.dtype is dtype and slots.dtype is torch.int64
+            and values.get_device() == dev and slots.get_device() == dev
+            and key_pages.get_device() == dev
+            and value_pages.get_device() == dev and values.shape == ks
+            and value_pages.shape == ps and ps[2:] == ks[2:]
+            and slots.shape == ks[:2] and ks[3] > 1 and keys.stride(3) == 1
+            and values.stride(3) == 1 and key_pages.stride(3) == 1
+            and value_pages.stride(3) == 1 and slots.stride(1) == 1):
+        _check_write(*given)
+    shape = _lib.pack_write_shape(
+        ks[0], ks[1], ks[2], ks[3], ps[1], ps[0], keys.stride(),
+        values.stride(), key_pages.stride(), value_pages.stride(),
+        slots.stride(0))
+    with _on_device(keys.device):
+        st = cs_paged_write(
+            keys.data_ptr(), values.data_ptr(), slots.data_ptr(),
+            key_pages.data_ptr(), value_pages.data_ptr(), shape,
+            _stream_handle(keys.device))
+    if st != 0:
+        _check_write(*given)
+        raise CsError(st, "cs_paged_write")
+
+
+def _check_tree(query, key_pages, value_pages, page_table, lengths, mask,
+                new_lengths, scale, out) -> None:
+    """Raises what is wrong with the arguments of paged_tree_attention, if
+    anything is (as _check_attention)."""
+    import torch
+    if not isinstance(query, torch.Tensor) or not query.is_cuda:
+        raise ValueError("query must be a CUDA tensor")
+    if query.dim() != 4:
+        raise ValueError("query must be 4-D [batch, new_tokens, heads, d_head]")
+    B, T, H, D = query.shape
+    if T > 0:
+        # One token's arguments are those of paged_attention.
+        _check_paged(query[:, 0], key_pages, value_pages, page_table, lengths,
+                     scale, None)
+    if query.numel():
+        _check_rows("query", query, query.dtype, query.shape, query.device)
+    if out is not None:
+        _check_rows("out", out, query.dtype, query.shape, query.device)
+    if new_lengths is not None and not _is_int32(torch, new_lengths, (B,),
+                                                 query.get_device()):
+        raise ValueError("new_lengths must be a contiguous int32 [batch] "
+                         "tensor on the query's device")
+    if mask is not None:
+        if (not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool
+                or mask.device != query.device
+                or tuple(mask.shape) not in ((B, T, T), (T, T))):
+            raise ValueError("mask must be a bool [batch, new_tokens, "
+                             "new_tokens] or [new_tokens, new_tokens] tensor "
+                             "on the query's device")
+        if T > 1 and (mask.stride(-1) != 1 or mask.stride(-2) < T):
+            raise ValueError("mask's rows must be contiguous and not overlap")
+
+
+def paged_tree_attention(query, key_pages, value_pages, page_table, lengths,
+                         mask=None, new_lengths=None, scale=None, out=None,
+                         return_lse: bool = False):
+    """Attention of several new tokens per sequence over a paged key-value
+    cache: a tree of drafted tokens, or the next chunk of a prompt.
+
+    ``query`` [B, T, H, D]; the pages, ``page_table`` and ``lengths`` as
+    :func:`paged_attention` takes them, the new tokens' keys and values already
+    written (:func:`paged_write`): the last ``new_lengths[b]`` (int32 [B],
+    default T) of the ``lengths[b]`` tokens are the new ones, in their order.
+    New token i attends all tokens before the new ones, and of those the ones j
+    that ``mask``, bool [B, T, T] or [T, T] for all sequences, keeps at [i, j]
+    (for a tree: its ancestors and itself); without a mask those with j <= i.
+    ``scale`` defaults to 1/sqrt(D).  Returns [B, T, H, D] (or ``out``), zeros
+    for rows from ``new_lengths[b]`` on and for rows that attend nothing, and
+    with ``return_lse`` the log of the softmax's sums [B, T, H] in fp32.
+    Asynchronous on the current stream; lengths and page numbers out of range
+    are left out and reported by :func:`get_error`, and so are NaN or infinite
+    scores, which propagate (as does a NaN among a sequence's values, to all of
+    its rows).  For serving: there is no backward pass, and the result carries
+    no gradient.
+    """
+    import torch
+    given = (query, key_pages, value_pages, page_table, lengths)
+    t = torch.Tensor
+    bad = not (isinstance(query, t) and query.dim() == 4 and query.shape[1] > 0)
+    if not bad:
+        dev, shape = query.get_device(), query.shape
+        bad = not (
+            _paged_ok(torch, query[:, 0], *given[1:], None)
+            and query.stride(3) == 1
+            and (out is None or (
+                isinstance(out, t) and out.dtype is query.dtype
+                and out.get_device() == dev and out.shape == shape
+                and out.stride(3) == 1))
+            and (new_lengths is None
+                 or _is_int32(torch, new_lengths, shape[:1], dev))
+            and (mask is None or (
+                isinstance(mask, t) and mask.dtype is torch.bool
+                and mask.get_device() == dev and mask.stride(-1) == 1
+                and mask.shape[-2:] == (shape[1], shape[1])
+                and (mask.dim() == 2 or (mask.dim() == 3
+                                         and mask.shape[0] == shape[0])))))
+    if bad:
+        _check_tree(*given, mask, new_lengths, scale, out)
+    dtype = query.dtype
+    B, T, H, D = query.shape
+    pages, page_size, Hk, _ = key_pages.shape
+    if out is None:
+        out = torch.empty((B, T, H, D), dtype=dtype, device=query.device)
+    lse = None
+    if return_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=query.device)
+    ms = (0, 0)
+    if mask is not None:
+        ms = mask.stride()
+        ms = (0, ms[0]) if len(ms) == 2 else ms
+    shape = _lib.pack_tree_shape(
+        B, T, H, Hk, D, page_size, pages, page_table.shape[1],
+        1 if dtype is torch.float16 else 0,
+        D ** -0.5 if scale is None else scale, query.stride(), out.stride(),
+        key_pages.stride(), value_pages.stride(), page_table.stride(0), ms)
+    size = max(cs_paged_tree_attention_workspace(shape), 0)
+    work = None
+    if size:
+        work = torch.empty(size, dtype=torch.uint8, device=query.device)
+    with _on_device(query.device):
+        st = cs_paged_tree_attention(
+            query.data_ptr(), key_pages.data_ptr(), value_pages.data_ptr(),
+            page_table.data_ptr(), lengths.data_ptr(),
+            None if new_lengths is None else new_lengths.data_ptr(),
+            None if mask is None else mask.data_ptr(), out.data_ptr(),
+            lse.data_ptr() if return_lse else None, shape,
+            work.data_ptr() if size else None, size,
+            _stream_handle(query.device))
+    if st != 0:
+        _check_tree(*given, mask, new_lengths, scale, out)
+        raise CsError(st, "cs_paged_tree_attention")
     return (out, lse) if return_lse else out
 
 

@@ -94,9 +94,60 @@ class cs_paged_shape(ctypes.Structure):
     ]
 
 
+class cs_extend_shape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_free", ctypes.c_int32),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
+class cs_write_shape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("new_tokens", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("key_stride", _STRIDES),
+        ("value_stride", _STRIDES),
+        ("k_stride", _STRIDES),
+        ("v_stride", _STRIDES),
+        ("slot_stride", ctypes.c_int64),
+    ]
+
+
+class cs_tree_shape(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("new_tokens", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("d_head", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("fp16", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride", _STRIDES),
+        ("o_stride", _STRIDES),
+        ("k_stride", _STRIDES),
+        ("v_stride", _STRIDES),
+        ("table_stride", ctypes.c_int64),
+        ("mask_stride", ctypes.c_int64 * 2),
+    ]
+
+
 _PACK_ATTENTION = struct.Struct("=7if12q96xq")     # without gradients
 _PACK_ATTENTION_BACKWARD = struct.Struct("=7if25q")
 _PACK_PAGED = struct.Struct("=8ifxxxx11q")
+_PACK_EXTEND = struct.Struct("=5ixxxxq")
+_PACK_WRITE = struct.Struct("=6i13q")
+_PACK_TREE = struct.Struct("=9if15q")
 
 
 def _out_of_range(error) -> ValueError:
@@ -141,6 +192,41 @@ def pack_paged_shape(batch, heads, kv_heads, d_head, page_size, num_pages,
             batch, heads, kv_heads, d_head, page_size, num_pages, max_pages,
             fp16, scale, q[0], q[1], o[0], o[1], k[0], k[1], k[2],
             v[0], v[1], v[2], table_stride)
+    except (struct.error, OverflowError) as e:
+        raise _out_of_range(e) from None
+
+
+def pack_extend_shape(*values) -> bytes:
+    """The bytes of a cs_extend_shape, its members in their order (as
+    pack_attention_shape)."""
+    try:
+        return _PACK_EXTEND.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise _out_of_range(e) from None
+
+
+def pack_write_shape(batch, new_tokens, kv_heads, d_head, page_size,
+                     num_pages, keys, values, k, v, slot_stride) -> bytes:
+    """The bytes of a cs_write_shape; keys .. v: element strides, the first
+    three of each are used (as pack_attention_shape)."""
+    try:
+        return _PACK_WRITE.pack(
+            batch, new_tokens, kv_heads, d_head, page_size, num_pages,
+            keys[0], keys[1], keys[2], values[0], values[1], values[2],
+            k[0], k[1], k[2], v[0], v[1], v[2], slot_stride)
+    except (struct.error, OverflowError) as e:
+        raise _out_of_range(e) from None
+
+
+def pack_tree_shape(batch, new_tokens, heads, kv_heads, d_head, page_size,
+                    num_pages, max_pages, fp16, scale, q, o, k, v,
+                    table_stride, mask=(0, 0)) -> bytes:
+    """The bytes of a cs_tree_shape (as pack_write_shape)."""
+    try:
+        return _PACK_TREE.pack(
+            batch, new_tokens, heads, kv_heads, d_head, page_size, num_pages,
+            max_pages, fp16, scale, q[0], q[1], q[2], o[0], o[1], o[2],
+            k[0], k[1], k[2], v[0], v[1], v[2], table_stride, mask[0], mask[1])
     except (struct.error, OverflowError) as e:
         raise _out_of_range(e) from None
 
@@ -245,6 +331,13 @@ _SIGNATURES = {
     "cs_check_paged_attention_args": (
         _I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP,
                _VP, _VP, _I64]),
+    "cs_paged_extend": (_I32, [_VP] * 12),
+    "cs_check_paged_extend_args": (_I32, [_VP] * 11),
+    "cs_paged_write": (_I32, [_VP] * 7),
+    "cs_check_paged_write_args": (_I32, [_VP] * 6),
+    "cs_paged_tree_attention": (_I32, [_VP] * 11 + [_I64, _VP]),
+    "cs_paged_tree_attention_workspace": (_I64, [_VP]),
+    "cs_check_paged_tree_attention_args": (_I32, [_VP] * 11 + [_I64]),
     "cs_probe_ex2": (_I32, [_VP, _I32, ctypes.POINTER(_I64), _VP]),
     "cs_probe_ex2_sink_floats": (_I32, []),
     "cs_test_wait_timeout": (_I32, [_I64, _VP]),
@@ -522,6 +615,55 @@ def cs_check_paged_attention_args(query, key_pages, value_pages, page_table,
     return load().cs_check_paged_attention_args(
         query, key_pages, value_pages, page_table, lengths, out, lse,
         _shape_ref(shape), workspace, workspace_bytes)
+
+
+def cs_paged_extend(page_table, lengths, new_lengths, held, free_pages,
+                    cursor, slots, totals, held_out, cursor_out, shape,
+                    stream) -> int:
+    return load().cs_paged_extend(
+        page_table, lengths, new_lengths, held, free_pages, cursor, slots,
+        totals, held_out, cursor_out, _shape_ref(shape), stream)
+
+
+def cs_check_paged_extend_args(page_table, lengths, new_lengths, held,
+                               free_pages, cursor, slots, totals, held_out,
+                               cursor_out, shape) -> int:
+    return load().cs_check_paged_extend_args(
+        page_table, lengths, new_lengths, held, free_pages, cursor, slots,
+        totals, held_out, cursor_out, _shape_ref(shape))
+
+
+def cs_paged_write(keys, values, slots, key_pages, value_pages, shape,
+                   stream) -> int:
+    return load().cs_paged_write(keys, values, slots, key_pages, value_pages,
+                                 _shape_ref(shape), stream)
+
+
+def cs_check_paged_write_args(keys, values, slots, key_pages, value_pages,
+                              shape) -> int:
+    return load().cs_check_paged_write_args(
+        keys, values, slots, key_pages, value_pages, _shape_ref(shape))
+
+
+def cs_paged_tree_attention(query, key_pages, value_pages, page_table,
+                            lengths, new_lengths, mask, out, lse, shape,
+                            workspace, workspace_bytes, stream) -> int:
+    return load().cs_paged_tree_attention(
+        query, key_pages, value_pages, page_table, lengths, new_lengths, mask,
+        out, lse, _shape_ref(shape), workspace, workspace_bytes, stream)
+
+
+def cs_paged_tree_attention_workspace(shape) -> int:
+    return load().cs_paged_tree_attention_workspace(_shape_ref(shape))
+
+
+def cs_check_paged_tree_attention_args(query, key_pages, value_pages,
+                                       page_table, lengths, new_lengths, mask,
+                                       out, lse, shape, workspace,
+                                       workspace_bytes) -> int:
+    return load().cs_check_paged_tree_attention_args(
+        query, key_pages, value_pages, page_table, lengths, new_lengths, mask,
+        out, lse, _shape_ref(shape), workspace, workspace_bytes)
 
 
 def cs_probe_ex2(sink, iters, stream) -> tuple[int, int]:

@@ -762,6 +762,79 @@ int64_t strided_extent(const int64_t* dim, const int64_t* stride, int n, int32_t
     return 2 * last;
 }
 
+// ------------------------------------------- several new tokens over a cache
+int64_t tree_steps(const cs_tree_shape& s) {
+    return ceil_div(static_cast<int64_t>(s.max_pages) * s.page_size, cs::tree_block(s.d_head));
+}
+
+cs_status check_tree_shape(const cs_tree_shape* s) {
+    if (!s) return CS_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->new_tokens < 0 || s->heads < 1 || s->kv_heads < 1 || s->d_head < 1 ||
+        s->heads % s->kv_heads != 0 || s->page_size < 1 || s->num_pages < 0 ||
+        s->max_pages < 0)
+        return CS_ERR_DIM_MISMATCH;
+    if (s->d_head > cs::kPagedMaxDHead) return CS_ERR_OOM;
+    if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
+    if (s->fp16 != 0 && s->fp16 != 1) return CS_ERR_INVALID_ARG;
+    if (!good_scale(s->scale)) return CS_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(s->max_pages) * s->page_size > kPagedMaxTokens ||
+        s->batch > cs::kFattnMaxBatch || s->heads > cs::kFattnMaxHeads ||
+        static_cast<int64_t>(s->new_tokens) * (s->heads / s->kv_heads) > (1 << 30))
+        return CS_ERR_DIM_MISMATCH;
+    return CS_OK;
+}
+
+// How the blocks of a batch are dealt on `sms` SMs, each with room for one CTA.
+struct TreePlan {
+    int32_t unit_rows, part_rows, width, groups;
+    int64_t units;   // of a sequence
+};
+
+TreePlan tree_plan(const cs_tree_shape& s, int sms) {
+    TreePlan p;
+    const int64_t rows = static_cast<int64_t>(s.new_tokens) * (s.heads / s.kv_heads);
+    p.unit_rows = rows > 128 && s.d_head <= 128 ? 256 : 128;
+    p.part_rows = static_cast<int32_t>(rows >= p.unit_rows ? p.unit_rows : ceil_div(rows, 32) * 32);
+    p.units = s.kv_heads * ceil_div(rows, p.unit_rows);
+    // CTAs side by side on the same pages: as many as leave few SMs out.
+    int32_t w = static_cast<int32_t>(p.units < sms ? p.units : sms);
+    while (w > 1 && (p.units % w != 0 || (sms / w) * w * 20 < sms * 19)) --w;
+    p.width = w < 1 ? 1 : w;
+    // 0: a CTA for every unit, and nothing to join.
+    const int64_t steps = tree_steps(s), total = steps * s.batch * (p.units / p.width);
+    p.groups = steps <= 2 ? 0 : static_cast<int32_t>(sms / p.width < total ? sms / p.width : total);
+    return p;
+}
+
+cs_status check_write_shape(const cs_write_shape* s) {
+    if (!s) return CS_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->new_tokens < 0 || s->kv_heads < 1 || s->d_head < 1 ||
+        s->page_size < 1 || s->num_pages < 0)
+        return CS_ERR_DIM_MISMATCH;
+    if (s->d_head > cs::kPagedMaxDHead) return CS_ERR_OOM;
+    if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
+    const int64_t tokens = static_cast<int64_t>(s->batch) * s->new_tokens;
+    if (s->kv_heads > cs::kFattnMaxHeads || tokens > (1 << 30) ||
+        tokens * s->kv_heads * (s->d_head / 8) > (int64_t(1) << 40))
+        return CS_ERR_DIM_MISMATCH;
+    return CS_OK;
+}
+
+// Whether a call may write these pages: rows that share no element, and keys
+// and values that share none, also side by side in one buffer.
+bool separate_pages(const int64_t* dim, const int64_t* k_stride, const int64_t* v_stride,
+                    const uint16_t* k, const uint16_t* v, int64_t k_bytes, int64_t v_bytes,
+                    int32_t d) {
+    if (overlaps_itself(dim, k_stride, 3, d) || overlaps_itself(dim, v_stride, 3, d)) return false;
+    if (!ranges_overlap(k, k_bytes, v, v_bytes)) return true;
+    for (int i = 0; i < 3; ++i)
+        if (dim[i] > 1 && k_stride[i] != v_stride[i]) return false;
+    const int64_t apart = k < v ? v - k : k - v;
+    const int64_t dims[4] = {dim[0], dim[1], dim[2], 2};
+    const int64_t strides[4] = {k_stride[0], k_stride[1], k_stride[2], apart};
+    return !overlaps_itself(dims, strides, 4, d);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1504,6 +1577,267 @@ cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
     return CS_OK;
 }
 
+cs_status cs_check_paged_extend_args(
+    const int32_t* page_table, const int32_t* lengths, const int32_t* new_lengths,
+    const int32_t* held, const int32_t* free_pages, const int32_t* cursor, const int64_t* slots,
+    const int32_t* totals, const int32_t* held_out, const int32_t* cursor_out,
+    const cs_extend_shape* shape) {
+    if (!shape) return CS_ERR_INVALID_ARG;
+    const cs_extend_shape& s = *shape;
+    if (s.batch < 0 || s.max_new < 0 || s.max_pages < 0 || s.page_size < 1 || s.num_free < 0 ||
+        s.batch > cs::kFattnMaxBatch ||
+        static_cast<int64_t>(s.max_pages) * s.page_size > kPagedMaxTokens ||
+        static_cast<int64_t>(s.batch) * s.max_new > (int64_t(1) << 40))
+        return CS_ERR_DIM_MISMATCH;
+    if (s.batch > 1 && (s.table_stride < s.max_pages || s.table_stride > kMaxRowStride))
+        return CS_ERR_INVALID_ARG;
+    const int64_t b = s.batch;
+    const int64_t table = b == 0 || s.max_pages == 0 ? 0
+        : 4 * ((b > 1 ? (b - 1) * s.table_stride : 0) + s.max_pages);
+    const Span spans[10] = {
+        {page_table, table, 4, true},
+        {lengths, 4 * b, 4, false},
+        {new_lengths, 4 * b, 4, false},
+        {held, held ? 4 * b : 0, 4, false},
+        {free_pages, 4 * static_cast<int64_t>(s.num_free), 4, false},
+        {cursor, cursor ? 4 : 0, 4, false},
+        {slots, 8 * b * s.max_new, 8, true},
+        {totals, 4 * b, 4, true},
+        {held_out, 4 * b, 4, true},
+        {cursor_out, 4, 4, true}};
+    return check_spans(spans, 10);
+}
+
+cs_status cs_paged_extend(int32_t* page_table, const int32_t* lengths,
+                          const int32_t* new_lengths, const int32_t* held,
+                          const int32_t* free_pages, const int32_t* cursor, int64_t* slots,
+                          int32_t* totals, int32_t* held_out, int32_t* cursor_out,
+                          const cs_extend_shape* shape, void* stream) {
+    cs_status st = cs_check_paged_extend_args(page_table, lengths, new_lengths, held, free_pages,
+                                              cursor, slots, totals, held_out, cursor_out, shape);
+    if (st != CS_OK) return st;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != CS_OK) return st;
+    const cs_extend_shape& s = *shape;
+    cs::ExtendTask t{};
+    t.page_table = page_table;
+    t.lengths = lengths;
+    t.new_lengths = new_lengths;
+    t.held = held;
+    t.free_pages = free_pages;
+    t.cursor = cursor;
+    t.slots = slots;
+    t.totals = totals;
+    t.held_out = held_out;
+    t.cursor_out = cursor_out;
+    t.err = d->err;
+    t.table_stride = s.table_stride;
+    t.batch = s.batch;
+    t.max_new = s.max_new;
+    t.max_pages = s.max_pages;
+    t.page_size = s.page_size;
+    t.num_free = s.num_free;
+    if (cs::launch_extend(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return CS_ERR_CUDA;
+    }
+    return CS_OK;
+}
+
+cs_status cs_check_paged_write_args(const uint16_t* keys, const uint16_t* values,
+                                    const int64_t* slots, const uint16_t* key_pages,
+                                    const uint16_t* value_pages, const cs_write_shape* shape) {
+    const cs_status st = check_write_shape(shape);
+    if (st != CS_OK) return st;
+    const cs_write_shape& s = *shape;
+    const int64_t in[3] = {s.batch, s.new_tokens, s.kv_heads};
+    const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
+    if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
+    if (s.batch > 1 && (s.slot_stride < s.new_tokens || s.slot_stride > kMaxRowStride))
+        return CS_ERR_INVALID_ARG;
+    const int64_t slot_bytes =
+        8 * ((s.batch > 1 ? (s.batch - 1) * s.slot_stride : 0) + s.new_tokens);
+    const int64_t kb = strided_extent(pages, s.k_stride, 3, s.d_head);
+    const int64_t vb = strided_extent(pages, s.v_stride, 3, s.d_head);
+    const Span keys_of[4] = {{keys, strided_extent(in, s.key_stride, 3, s.d_head), 16, false},
+                             {values, strided_extent(in, s.value_stride, 3, s.d_head), 16, false},
+                             {slots, slot_bytes, 8, false},
+                             {key_pages, kb, 16, true}};
+    const Span values_of[4] = {keys_of[0], keys_of[1], keys_of[2], {value_pages, vb, 16, true}};
+    cs_status r = check_spans(keys_of, 4);
+    if (r == CS_OK) r = check_spans(values_of, 4);
+    if (r == CS_OK && kb > 0 &&
+        !separate_pages(pages, s.k_stride, s.v_stride, key_pages, value_pages, kb, vb, s.d_head))
+        r = CS_ERR_INVALID_ARG;
+    return r;
+}
+
+cs_status cs_paged_write(const uint16_t* keys, const uint16_t* values, const int64_t* slots,
+                         uint16_t* key_pages, uint16_t* value_pages,
+                         const cs_write_shape* shape, void* stream) {
+    cs_status st = cs_check_paged_write_args(keys, values, slots, key_pages, value_pages, shape);
+    if (st != CS_OK) return st;
+    const cs_write_shape& s = *shape;
+    if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != CS_OK) return st;
+    cs::WriteTask t{};
+    t.keys = keys;
+    t.values = values;
+    t.slots = slots;
+    t.k_pages = key_pages;
+    t.v_pages = value_pages;
+    t.err = d->err;
+    for (int i = 0; i < 3; ++i) {
+        t.key_stride[i] = s.key_stride[i];
+        t.value_stride[i] = s.value_stride[i];
+        t.k_stride[i] = s.k_stride[i];
+        t.v_stride[i] = s.v_stride[i];
+    }
+    t.slot_stride = s.slot_stride;
+    t.num_slots = static_cast<int64_t>(s.num_pages) * s.page_size;
+    t.new_tokens = s.new_tokens;
+    t.page_size = s.page_size;
+    t.head_units = s.d_head / 8;
+    t.units = s.kv_heads * t.head_units;
+    t.total = static_cast<int64_t>(s.batch) * s.new_tokens * t.units;
+    if (cs::launch_write(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return CS_ERR_CUDA;
+    }
+    return CS_OK;
+}
+
+int64_t cs_paged_tree_attention_workspace(const cs_tree_shape* shape) {
+    if (check_tree_shape(shape) != CS_OK) return -1;
+    const TreePlan p = tree_plan(*shape, kPagedMaxSms);
+    if (p.groups == 0) return 0;
+    // Two parts a CTA: the (maximum, sum) pairs, the outputs.  (However the
+    // device's SMs are grouped: at most one CTA an SM, and one a block.)
+    const int64_t blocks = tree_steps(*shape) * shape->batch;
+    const int64_t ctas =
+        blocks >= kPagedMaxSms || blocks * p.units >= kPagedMaxSms ? kPagedMaxSms : blocks * p.units;
+    const int64_t rows = ctas * 2 * p.part_rows;
+    return rows * 8 + rows * shape->d_head * 4;
+}
+
+cs_status cs_check_paged_tree_attention_args(
+    const uint16_t* query, const uint16_t* key_pages, const uint16_t* value_pages,
+    const int32_t* page_table, const int32_t* lengths, const int32_t* new_lengths,
+    const uint8_t* mask, const uint16_t* out, const float* lse, const cs_tree_shape* shape,
+    const void* workspace, int64_t workspace_bytes) {
+    const cs_status st = check_tree_shape(shape);
+    if (st != CS_OK) return st;
+    const cs_tree_shape& s = *shape;
+    if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
+    // Blocks and CTAs are counted in 32 bits.
+    const TreePlan p = tree_plan(s, kPagedMaxSms);
+    if (p.units * s.batch > (1 << 30) ||
+        tree_steps(s) > (1 << 30) / (s.batch * (p.units / p.width)))
+        return CS_ERR_DIM_MISMATCH;
+    const int64_t need = cs_paged_tree_attention_workspace(shape);
+    if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
+    if (s.batch > 1 && (s.table_stride < s.max_pages || s.table_stride > kMaxRowStride))
+        return CS_ERR_INVALID_ARG;
+    int64_t mask_bytes = 0;
+    if (mask) {
+        if ((s.new_tokens > 1 &&
+             (s.mask_stride[1] < s.new_tokens || s.mask_stride[1] > kMaxRowStride >> 10)) ||
+            (s.batch > 1 && (s.mask_stride[0] < 0 || s.mask_stride[0] > kMaxRowStride)))
+            return CS_ERR_INVALID_ARG;
+        mask_bytes = s.new_tokens +
+                     (s.new_tokens > 1 ? (s.new_tokens - 1) * s.mask_stride[1] : 0) +
+                     (s.batch > 1 ? (s.batch - 1) * s.mask_stride[0] : 0);
+    }
+    const int64_t rows[3] = {s.batch, s.new_tokens, s.heads};
+    const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
+    const int64_t table = s.max_pages == 0 ? 0
+        : 4 * ((s.batch > 1 ? (s.batch - 1) * s.table_stride : 0) + s.max_pages);
+    const int64_t b = s.batch;
+    const Span spans[10] = {
+        {query, strided_extent(rows, s.q_stride, 3, s.d_head), 16, false},
+        {key_pages, strided_extent(pages, s.k_stride, 3, s.d_head), 16, false},
+        {value_pages, strided_extent(pages, s.v_stride, 3, s.d_head), 16, false},
+        {page_table, table, 4, false},
+        {lengths, 4 * b, 4, false},
+        {new_lengths, new_lengths ? 4 * b : 0, 4, false},
+        {mask, mask_bytes, 1, false},
+        {out, strided_extent(rows, s.o_stride, 3, s.d_head), 16, true},
+        {lse, lse ? 4 * b * s.new_tokens * s.heads : 0, 4, true},
+        {workspace, need, 16, true}};
+    if (spans[7].bytes > 0 && overlaps_itself(rows, s.o_stride, 3, s.d_head))
+        return CS_ERR_INVALID_ARG;
+    return check_spans(spans, 10);
+}
+
+cs_status cs_paged_tree_attention(const uint16_t* query, const uint16_t* key_pages,
+                                  const uint16_t* value_pages, const int32_t* page_table,
+                                  const int32_t* lengths, const int32_t* new_lengths,
+                                  const uint8_t* mask, uint16_t* out, float* lse,
+                                  const cs_tree_shape* shape, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+    cs_status st = cs_check_paged_tree_attention_args(
+        query, key_pages, value_pages, page_table, lengths, new_lengths, mask, out, lse, shape,
+        workspace, workspace_bytes);
+    if (st != CS_OK) return st;
+    const cs_tree_shape& s = *shape;
+    if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
+    DeviceInfo* d = nullptr;
+    st = device_info(&d);
+    if (st != CS_OK) return st;
+    cs::TreeTask t{};
+    t.q = query;
+    t.k_pages = key_pages;
+    t.v_pages = value_pages;
+    t.page_table = page_table;
+    t.lengths = lengths;
+    t.new_lengths = new_lengths;
+    t.mask = mask;
+    t.out = out;
+    t.lse = lse;
+    t.err = d->err;
+    for (int i = 0; i < 3; ++i) {
+        t.q_stride[i] = s.q_stride[i];
+        t.o_stride[i] = s.o_stride[i];
+        t.k_stride[i] = s.k_stride[i];
+        t.v_stride[i] = s.v_stride[i];
+    }
+    t.table_stride = s.table_stride;
+    t.mask_stride[0] = s.mask_stride[0];
+    t.mask_stride[1] = s.mask_stride[1];
+    t.batch = s.batch;
+    t.new_tokens = s.new_tokens;
+    t.heads = s.heads;
+    t.kv_heads = s.kv_heads;
+    t.group = s.heads / s.kv_heads;
+    t.d_head = s.d_head;
+    t.page_size = s.page_size;
+    t.num_pages = s.num_pages;
+    t.max_pages = s.max_pages;
+    const TreePlan p = tree_plan(s, d->sm_count < kPagedMaxSms ? d->sm_count : kPagedMaxSms);
+    t.unit_rows = p.unit_rows;
+    t.part_rows = p.part_rows;
+    t.width = p.width;
+    t.bundles = static_cast<int32_t>(p.units / p.width);
+    t.groups = p.groups;
+    t.split = p.groups > 0;
+    t.fp16 = s.fp16;
+    t.scale = s.scale;
+    t.wait_limit_cycles = cs::kWaitLimitCycles;
+    if (t.split) {
+        t.part_stats = static_cast<float2*>(workspace);
+        t.part_out = reinterpret_cast<float*>(
+            t.part_stats + static_cast<int64_t>(p.groups) * p.width * 2 * p.part_rows);
+    }
+    if (cs::launch_tree(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return CS_ERR_CUDA;
+    }
+    return CS_OK;
+}
+
 int32_t cs_probe_ex2_sink_floats(void) {
     DeviceInfo* d = nullptr;
     if (device_info(&d) != CS_OK) return -1;
@@ -1559,6 +1893,7 @@ const char* cs_status_string(cs_status status) {
         case CS_ERR_CUDA: return "CUDA error";
         case CS_ERR_TIMEOUT: return "device wait timed out";
         case CS_ERR_BAD_PAGE: return "page or length out of range";
+        case CS_ERR_OUT_OF_PAGES: return "no free page left";
         default: return "unknown status";
     }
 }

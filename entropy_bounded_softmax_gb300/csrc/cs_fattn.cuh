@@ -1,8 +1,8 @@
 // Device helpers shared by the fused attention kernels (k_fattn_fwd.cu,
-// k_fattn_bwd.cu): bounded waits of a warp, operand tiles in shared memory
+// k_fattn_bwd.cu) and the one over a paged cache (k_tree.cu): bounded waits of a warp, operand tiles in shared memory
 // and the products on them, kept keys, and row stores.
 //
-// Operand tiles.  R rows of DP (64 or 128) bf16, as the tensor copies write
+// Operand tiles.  R rows of DP (64, 128 or 256) bf16 or fp16, as the tensor copies write
 // them with 128-byte swizzling: DP / 64 panels of R rows x 128 bytes, head
 // elements past D and rows past the sequence filled with zeros.  The same
 // tile serves as a K-major operand (rows along M or N, the head along K:
@@ -83,10 +83,10 @@ constexpr uint32_t kDescRows16 = 16 * 128 / 16;
 // D[128 x N] = A . B^T on a tile of 128 rows and one of N (their low descriptor
 // words), over the first 16 `steps` head elements: those past d_head are
 // zeros, and products with them would cost as much as others.
-template <int N, int DP>
+template <int N, int DP, bool FP16 = false>
 __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a, uint32_t b, int steps,
                                           bool leader) {
-    constexpr uint32_t idesc = idesc_bf16(128, N, false);
+    constexpr uint32_t idesc = idesc_half(128, N, false, FP16);
     auto one = [&](int ks) {
         mma_bf16_ss(d, a + (ks >> 2) * (128 * 128 / 16) + (ks & 3) * (32 / 16),
                     b + (ks >> 2) * (N * 128 / 16) + (ks & 3) * (32 / 16), idesc, ks > 0, leader);

@@ -16,6 +16,7 @@ constexpr unsigned int kBitInf = 1u << CS_ERR_INF_INPUT;
 constexpr unsigned int kBitOverflow = 1u << CS_ERR_ENTROPY_OVERFLOW;
 constexpr unsigned int kBitTimeout = 1u << CS_ERR_TIMEOUT;
 constexpr unsigned int kBitBadPage = 1u << CS_ERR_BAD_PAGE;
+constexpr unsigned int kBitOutOfPages = 1u << CS_ERR_OUT_OF_PAGES;
 
 // Default limit of every bounded device wait, in SM cycles: 2^31 cycles,
 // about 1 s at GB300's 2.07 GHz maximum clock.
@@ -397,6 +398,80 @@ struct PagedTask {
 constexpr int kPagedMaxDHead = 256;
 
 cudaError_t launch_paged(const PagedTask& task, cudaStream_t stream);
+
+// One paged_extend launch.
+struct ExtendTask {
+    int32_t* page_table;       // [batch, max_pages], entries from held on written
+    const int32_t* lengths;    // [batch]
+    const int32_t* new_lengths;
+    const int32_t* held;       // [batch] or null: the pages of lengths tokens
+    const int32_t* free_pages; // [num_free]
+    const int32_t* cursor;     // [1] or null: 0
+    int64_t* slots;            // [batch, max_new]
+    int32_t* totals;           // [batch]
+    int32_t* held_out;         // [batch]
+    int32_t* cursor_out;       // [1]
+    unsigned int* err;         // device error word
+    int64_t table_stride;
+    int32_t batch, max_new, max_pages, page_size, num_free;
+    int32_t span, sequences;   // of a CTA: places of a sequence, sequences
+};
+
+cudaError_t launch_extend(ExtendTask task, cudaStream_t stream);
+
+// One paged_write launch: 16-bit elements of either type.
+struct WriteTask {
+    const uint16_t* keys;      // [batch, new_tokens, kv_heads, d_head]
+    const uint16_t* values;
+    const int64_t* slots;      // [batch, new_tokens]
+    uint16_t* k_pages;         // [num_pages, page_size, kv_heads, d_head]
+    uint16_t* v_pages;
+    unsigned int* err;         // device error word
+    int64_t key_stride[3], value_stride[3], k_stride[3], v_stride[3];
+    int64_t slot_stride;
+    int64_t num_slots;         // num_pages * page_size
+    int64_t total;             // 16-byte units of all keys
+    int32_t new_tokens, page_size;
+    int32_t units, head_units; // of a token's keys, of a head
+};
+
+cudaError_t launch_write(const WriteTask& task, cudaStream_t stream);
+
+// One paged_tree_attention launch: new_tokens tokens for each of `batch`
+// sequences over the cache of PagedTask.
+struct TreeTask {
+    const uint16_t* q;         // [batch, new_tokens, heads, d_head]
+    const uint16_t* k_pages;
+    const uint16_t* v_pages;
+    const int32_t* page_table; // [batch, max_pages]
+    const int32_t* lengths;    // [batch], the new tokens included
+    const int32_t* new_lengths;// [batch] or null: all new_tokens
+    const uint8_t* mask;       // [batch, new_tokens, new_tokens] or null: j <= i
+    uint16_t* out;             // as q
+    float* lse;                // [batch, new_tokens, heads] or null
+    float2* part_stats;        // workspace: [groups, width, 2, part_rows] (max, sum)
+    float* part_out;           // [groups, width, 2, d_head / 8, part_rows, 8]
+    unsigned int* err;         // device error word
+    int64_t q_stride[3], o_stride[3], k_stride[3], v_stride[3];
+    int64_t table_stride;
+    int64_t mask_stride[2];
+    int32_t batch, new_tokens, heads, kv_heads, group, d_head;
+    int32_t page_size, num_pages, max_pages;
+    int32_t unit_rows;         // 128 or 256: rows of a unit
+    int32_t part_rows;         // rows of one that are there, whole warps
+    int32_t width;             // units that a group of CTAs walks side by side
+    int32_t bundles;           // width * bundles units to a sequence
+    int32_t split;             // 1: the blocks are dealt to groups, this many
+    int32_t groups;
+    int32_t fp16;
+    float scale;
+    uint64_t wait_limit_cycles;
+};
+
+// Tokens of a block.
+__host__ __device__ constexpr int tree_block(int d_head) { return d_head > 128 ? 64 : 128; }
+
+cudaError_t launch_tree(const TreeTask& task, cudaStream_t stream);
 
 cudaError_t launch_rowgroup(const RowTask& task, int lanes_per_row,
                             int elems_per_lane, cudaStream_t stream);

@@ -3,8 +3,9 @@
 // memory and the accumulator in tensor memory, its completion on an
 // mbarrier, loads of the accumulator into registers, and tensor copies
 // from global into shared memory.  Used by the attn . V step of
-// biencoder_attention (k_bienc_pv.cu) and by the fused attention kernels
-// (k_fattn_fwd.cu, k_fattn_bwd.cu).
+// biencoder_attention (k_bienc_pv.cu), by the fused attention kernels
+// (k_fattn_fwd.cu, k_fattn_bwd.cu) and by attention of several new tokens over
+// a paged cache (k_tree.cu).
 #pragma once
 
 #include <stdint.h>
@@ -134,15 +135,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t sbo
            (2ull << 61);
 }
 
-// Instruction descriptor of a dense kind::f16 MMA on bf16 operands with an
-// fp32 accumulator, M x N; A K-major, B K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
+// Instruction descriptor of a dense kind::f16 MMA on bf16 or fp16 operands
+// with an fp32 accumulator, M x N; A K-major, B K-major or (b_mn) MN-major.
+__host__ __device__ constexpr uint32_t idesc_half(int M, int N, bool b_mn, bool fp16) {
     return (1u << 4)                                   // D: fp32
-         | (1u << 7)                                   // A: bf16
-         | (1u << 10)                                  // B: bf16
+         | (fp16 ? 0u : 1u << 7)                       // A: fp16 or bf16
+         | (fp16 ? 0u : 1u << 10)                      // B
          | (b_mn ? 1u << 16 : 0u)
          | (static_cast<uint32_t>(N >> 3) << 17)
          | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
+    return idesc_half(M, N, b_mn, false);
 }
 
 // True in one lane of the (converged) warp.

@@ -75,7 +75,7 @@ cudaError_t launch_wait_timeout(unsigned int* err, uint64_t limit_cycles,
 
 namespace {
 constexpr int kMaxDevices = 64;
-constexpr int kSlots = 74;
+constexpr int kSlots = 90;
 // Largest MaxDynamicSharedMemorySize set so far, per device and kernel.
 std::atomic<int> g_smem_set[kMaxDevices][kSlots];
 std::mutex g_smem_mu;

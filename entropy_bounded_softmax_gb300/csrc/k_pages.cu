@@ -1,0 +1,212 @@
+// Pages and slots for new tokens of a paged key-value cache, and the write of
+// their keys and values.
+#include "cs_device.cuh"
+
+namespace cs {
+namespace {
+
+using namespace csd;
+
+// ------------------------------------------------------------------- extend
+// For sequence b with n = lengths[b] tokens, w = new_lengths[b] more and h =
+// held[b] pages:
+//   need_b = max(0, ceil((n + w) / page) - h),   first_b = sum of need before b,
+//   got_b = what of need_b the free list still has from cursor + first_b on,
+// the pages of the list's entries cursor + first_b .. go to the table's entries
+// h .., and token n + i gets slot table[(n + i) / page] * page + (n + i) % page.
+//
+// Bound by the slots that it writes, and, for few, by latency: lengths, then
+// table entries, then slots are three trips to memory.  Every CTA adds up the
+// needs of the sequences before its own, by itself (from caches: nothing waits
+// for another CTA, and one launch is enough), and takes the pages straight from
+// the free list where another CTA writes them into the table.
+constexpr int kExThreads = 256;
+
+struct Claim {
+    int len, fresh, held, need;   // as above; fresh and need 0 where `bad`
+    bool bad;
+};
+
+__device__ __forceinline__ int pages_of(uint32_t tokens, uint32_t page) {
+    return static_cast<int>(tokens / page + (tokens % page != 0));
+}
+
+__device__ __forceinline__ Claim claim_of(const ExtendTask& t, int b) {
+    Claim c;
+    c.len = t.lengths[b];
+    c.fresh = t.new_lengths[b];
+    c.bad = c.len < 0 || c.fresh < 0 || c.fresh > t.max_new;
+    c.held = t.held ? t.held[b] : c.len < 0 ? 0 : pages_of(c.len, t.page_size);
+    // Tokens without pages, or more pages than the row has entries.
+    c.bad = c.bad || c.held < 0 || c.held > t.max_pages ||
+            static_cast<int64_t>(c.held) * t.page_size < c.len;
+    if (c.bad) c.fresh = 0;
+    c.need = 0;
+    if (!c.bad) {
+        const uint32_t total = static_cast<uint32_t>(c.len) + static_cast<uint32_t>(c.fresh);
+        const int want = pages_of(total, t.page_size);
+        c.bad = want > t.max_pages;   // taken as far as the row goes
+        c.need = max(0, min(want, t.max_pages) - c.held);
+    }
+    return c;
+}
+
+__global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) {
+    constexpr int kWarps = kExThreads / 32;
+    __shared__ int64_t scan[kWarps];
+    struct Row {
+        int len, held, total;   // total: tokens with a slot after the call
+        int taken, got;         // of the free list: the entry of page `held`
+    };
+    __shared__ Row rows[kExThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b0 = blockIdx.y * t.sequences;
+    const int nb = min(t.sequences, t.batch - b0);
+
+    // The needs before sequence b0, then those of its own.
+    int64_t before = 0;
+    for (int b = threadIdx.x; b < b0; b += kExThreads) before += claim_of(t, b).need;
+    Claim c{};
+    if (threadIdx.x < nb) c = claim_of(t, b0 + threadIdx.x);
+    int64_t up = c.need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    __shared__ int64_t own[kWarps];
+    if (lane == 31) {
+        scan[warp] = before;
+        own[warp] = up;
+    }
+    __syncthreads();
+    int64_t first = up - c.need, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        first += scan[w] + (w < warp ? own[w] : 0);
+        all += scan[w] + own[w];
+    }
+    int cursor = t.cursor ? *t.cursor : 0;
+    const bool bad_cursor = cursor < 0 || cursor > t.num_free;
+    cursor = min(max(cursor, 0), t.num_free);
+    const int64_t left = t.num_free - cursor;
+    if (threadIdx.x < nb) {
+        const int64_t rest = left - first;
+        const int got = static_cast<int>(rest < 0 ? 0 : rest < c.need ? rest : c.need);
+        const int have = c.held + got;
+        const int64_t room = static_cast<int64_t>(have) * t.page_size;
+        const int64_t want = static_cast<int64_t>(c.len) + c.fresh;
+        Row r;
+        r.len = c.len;
+        r.held = c.held;
+        r.total = static_cast<int>(c.fresh == 0 ? c.len : want < room ? want : room);
+        r.taken = cursor + static_cast<int>(first < left ? first : left);
+        r.got = got;
+        rows[threadIdx.x] = r;
+        if (blockIdx.x == 0) {
+            t.totals[b0 + threadIdx.x] = r.total;
+            t.held_out[b0 + threadIdx.x] = have;
+            unsigned int bits = c.bad || bad_cursor ? kBitBadPage : 0u;
+            if (got < c.need) bits |= kBitOutOfPages;
+            raise_error(t.err, bits);
+        }
+    }
+    if (blockIdx.x == 0 && b0 + nb == t.batch && threadIdx.x == 0)
+        *t.cursor_out = cursor + static_cast<int>(all < left ? all : left);
+    __syncthreads();
+
+    // The new pages into the table: a warp a sequence, its CTAs in turn.
+    for (int y = warp; y < nb; y += kWarps) {
+        const Row r = rows[y];
+        for (int i = 32 * blockIdx.x + lane; i < r.got; i += 32 * gridDim.x)
+            t.page_table[(b0 + y) * t.table_stride + r.held + i] = t.free_pages[r.taken + i];
+    }
+    const int i0 = blockIdx.x * t.span;
+    const int span = min(t.span, t.max_new - i0);
+    for (int e = threadIdx.x; e < nb * span; e += kExThreads) {
+        const int y = e / span, i = i0 + e - y * span;
+        const Row r = rows[y];
+        int64_t slot = -1;
+        if (i < r.total - r.len) {
+            const int at = r.len + i, entry = at / t.page_size;
+            const int page = entry < r.held
+                                 ? t.page_table[(b0 + y) * t.table_stride + entry]
+                                 : t.free_pages[r.taken + entry - r.held];
+            if (page >= 0)
+                slot = static_cast<int64_t>(page) * t.page_size + (at - entry * t.page_size);
+            else
+                raise_error(t.err, kBitBadPage);
+        }
+        t.slots[static_cast<int64_t>(b0 + y) * t.max_new + i] = slot;
+    }
+}
+
+// -------------------------------------------------------------------- write
+// cache[slots[b][i]] = keys[b][i], values[b][i].  Bound by the bytes of both,
+// read and written once: a thread copies units of 16 bytes, of the key and of
+// the value at the same place, several at a time.
+constexpr int kWrThreads = 256;
+constexpr int kWrUnroll = 4;
+
+__global__ void __launch_bounds__(kWrThreads) write_kernel(const WriteTask t) {
+    const int64_t e0 = static_cast<int64_t>(blockIdx.x) * (kWrThreads * kWrUnroll) + threadIdx.x;
+    uint4 k[kWrUnroll], v[kWrUnroll];
+    int64_t dk[kWrUnroll], dv[kWrUnroll];
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kWrUnroll; ++u) {
+        const int64_t e = e0 + u * kWrThreads;
+        dk[u] = -1;
+        if (e >= t.total) continue;
+        const int64_t token = e / t.units;
+        const int unit = static_cast<int>(e - token * t.units);
+        const int b = static_cast<int>(token / t.new_tokens);
+        const int i = static_cast<int>(token - static_cast<int64_t>(b) * t.new_tokens);
+        const int64_t slot = t.slots[b * t.slot_stride + i];
+        if (slot < 0) continue;
+        if (slot >= t.num_slots) {
+            bad = true;
+            continue;
+        }
+        const int head = unit / t.head_units, d = 8 * (unit - head * t.head_units);
+        const int64_t page = slot / t.page_size, at = slot - page * t.page_size;
+        k[u] = *reinterpret_cast<const uint4*>(t.keys + b * t.key_stride[0] +
+                                               i * t.key_stride[1] + head * t.key_stride[2] + d);
+        v[u] = *reinterpret_cast<const uint4*>(t.values + b * t.value_stride[0] +
+                                               i * t.value_stride[1] +
+                                               head * t.value_stride[2] + d);
+        dk[u] = page * t.k_stride[0] + at * t.k_stride[1] + head * t.k_stride[2] + d;
+        dv[u] = page * t.v_stride[0] + at * t.v_stride[1] + head * t.v_stride[2] + d;
+    }
+#pragma unroll
+    for (int u = 0; u < kWrUnroll; ++u) {
+        if (dk[u] < 0) continue;
+        *reinterpret_cast<uint4*>(t.k_pages + dk[u]) = k[u];
+        *reinterpret_cast<uint4*>(t.v_pages + dv[u]) = v[u];
+    }
+    if (bad) raise_error(t.err, kBitBadPage);
+}
+
+}  // namespace
+
+cudaError_t launch_extend(ExtendTask t, cudaStream_t stream) {
+    // About 2048 slots a CTA.
+    t.span = t.max_new < 2048 ? (t.max_new > 0 ? t.max_new : 1) : 2048;
+    const int per = 2048 / t.span;
+    t.sequences = per < 1 ? 1 : per > kExThreads ? kExThreads : per;
+    // (One CTA at least: it passes the cursor on.)
+    const dim3 grid(t.max_new > 0 ? (t.max_new + t.span - 1) / t.span : 1,
+                    t.batch > 0 ? (t.batch + t.sequences - 1) / t.sequences : 1);
+    extend_kernel<<<grid, kExThreads, 0, stream>>>(t);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_write(const WriteTask& t, cudaStream_t stream) {
+    const int64_t ctas = (t.total + kWrThreads * kWrUnroll - 1) / (kWrThreads * kWrUnroll);
+    write_kernel<<<static_cast<unsigned>(ctas), kWrThreads, 0, stream>>>(t);
+    return cudaGetLastError();
+}
+
+}  // namespace cs

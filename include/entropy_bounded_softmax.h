@@ -59,6 +59,7 @@ typedef int32_t cs_status;
 #define CS_ERR_TIMEOUT 10         /* a bounded device wait gave up (async)  */
 #define CS_ERR_BAD_PAGE 11        /* a cache length or page number out of
                                      range (asynchronous)                   */
+#define CS_ERR_OUT_OF_PAGES 12    /* the free list had too few pages (async) */
 
 /* Kernel variants (cs_options.variant, cs_plan.variant). */
 #define CS_VARIANT_AUTO 0
@@ -227,7 +228,8 @@ cs_status cs_check_args_bf16(const uint16_t* logits, const float* out,
  * Reads and clears the calling thread's current device's error word, then
  * synchronises `stream`.  *code_mask receives a bitmask of (1 << code) for
  * every asynchronous condition since the last call: CS_ERR_NAN_INPUT,
- * CS_ERR_INF_INPUT, CS_ERR_ENTROPY_OVERFLOW, CS_ERR_TIMEOUT, CS_ERR_BAD_PAGE.  The read and
+ * CS_ERR_INF_INPUT, CS_ERR_ENTROPY_OVERFLOW, CS_ERR_TIMEOUT, CS_ERR_BAD_PAGE,
+ * CS_ERR_OUT_OF_PAGES.  The read and
  * the clear are one atomic exchange, made by a one-thread kernel on `stream`
  * after the work enqueued on it before this call.  The word is shared by
  * every launch on the device: a launch on another stream that runs
@@ -678,6 +680,194 @@ cs_status cs_check_paged_attention_args(
     const int32_t* lengths, const uint16_t* out, const float* lse,
     const cs_paged_shape* shape, const void* workspace,
     int64_t workspace_bytes);
+
+/*
+ * Several new tokens per sequence over the same cache: pages and slots for
+ * them (cs_paged_extend), the write of their keys and values (cs_paged_write)
+ * and their attention (cs_paged_tree_attention).
+ */
+typedef struct cs_extend_shape {
+    int32_t batch;      /* sequences, >= 0                                  */
+    int32_t max_new;    /* slots of a sequence, >= 0; at most 2^40 in all   */
+    int32_t max_pages;  /* entries of a page-table row, >= 0; at most 2^30
+                           tokens a row                                     */
+    int32_t page_size;  /* tokens of a page, >= 1                           */
+    int32_t num_free;   /* entries of free_pages, >= 0                      */
+    int64_t table_stride;  /* entries between page-table rows, >= max_pages,
+                              at most 2^40                                  */
+} cs_extend_shape;
+
+/*
+ * cs_paged_extend -- makes room for new tokens.  Sequence b has lengths[b]
+ * tokens in the cache, new_lengths[b] more to come, and held[b] pages, the
+ * first entries of its row of the table.  In the order of the sequences, each
+ * takes what pages it is short of from free_pages, in that list's order from
+ * entry *cursor on:
+ *
+ *   need_b = max(0, ceil((lengths[b] + new_lengths[b]) / page_size) - held[b])
+ *
+ * page_table  device pointer, [batch, max_pages] int32; the new pages are
+ *          written behind the held ones, everything else stays.
+ * lengths, new_lengths, held  device pointers, [batch] int32; held may be
+ *          NULL: ceil(lengths[b] / page_size).
+ * free_pages  device pointer, [num_free] int32; not written.
+ * cursor   device pointer to one int32, or NULL: 0.
+ * slots    device pointer, [batch, max_new] int64, contiguous, written
+ *          completely: new token i of sequence b, token j = lengths[b] + i, gets
+ *          page_table[b][j / page_size] * page_size + j % page_size; -1 where
+ *          there is no such token, or no page for it.
+ * totals   device pointer, [batch] int32: the tokens that have slots, old and
+ *          new: lengths[b] + new_lengths[b], or what its pages hold.
+ * held_out device pointer, [batch] int32: the pages of each sequence now.
+ * cursor_out  device pointer to one int32: the entry after the last one taken.
+ * What the call writes overlaps nothing else of it.
+ *
+ * Where the list runs out, sequences get what is left in their order, and
+ * CS_ERR_OUT_OF_PAGES is ORed into the error word.  A sequence whose length is
+ * negative, has no pages for its tokens, or whose new_lengths is outside
+ * 0..max_new, gets nothing; one that needs more entries than its row has is
+ * taken as far as that goes; a cursor outside 0..num_free is taken as the
+ * nearer end; a page number below 0 gives no slot; each ORs CS_ERR_BAD_PAGE.
+ * Every result is a whole number and the same for every call.  Ownership,
+ * execution and errors: as cs_constrained_softmax.
+ */
+cs_status cs_paged_extend(int32_t* page_table, const int32_t* lengths,
+                          const int32_t* new_lengths, const int32_t* held,
+                          const int32_t* free_pages, const int32_t* cursor,
+                          int64_t* slots, int32_t* totals, int32_t* held_out,
+                          int32_t* cursor_out, const cs_extend_shape* shape,
+                          void* stream);
+
+/* Host-only argument check (no CUDA call). */
+cs_status cs_check_paged_extend_args(
+    const int32_t* page_table, const int32_t* lengths,
+    const int32_t* new_lengths, const int32_t* held,
+    const int32_t* free_pages, const int32_t* cursor, const int64_t* slots,
+    const int32_t* totals, const int32_t* held_out, const int32_t* cursor_out,
+    const cs_extend_shape* shape);
+
+typedef struct cs_write_shape {
+    int32_t batch;       /* sequences, >= 0                                 */
+    int32_t new_tokens;  /* tokens of a sequence, >= 0; at most 2^30 in all,
+                            and 2^43 elements                               */
+    int32_t kv_heads;    /* >= 1                                            */
+    int32_t d_head;      /* 8..256, a multiple of 8                         */
+    int32_t page_size;   /* tokens of a page, >= 1                          */
+    int32_t num_pages;   /* pages of the cache, >= 0                        */
+    int64_t key_stride[3];    /* batch, token, head; elements, non-negative */
+    int64_t value_stride[3];  /* multiples of 8                             */
+    int64_t k_stride[3];      /* page, slot, head; positive multiples of 8  */
+    int64_t v_stride[3];
+    int64_t slot_stride;      /* between rows of slots, >= new_tokens       */
+} cs_write_shape;
+
+/*
+ * cs_paged_write -- puts the keys and values of new tokens into the cache:
+ * those of token i of sequence b into slot slots[b][i] % page_size of page
+ * slots[b][i] / page_size; the elements' 16 bits are copied as they are (bf16
+ * or fp16).
+ *
+ * keys, values  device pointers, [batch, new_tokens, kv_heads, d_head], the
+ *          head dimension contiguous, 16-byte aligned.
+ * slots    device pointer, [batch, new_tokens] int64, rows contiguous.  Below
+ *          0: the token is passed over, and its key and value are not read.
+ *          Past the cache: passed over too, and CS_ERR_BAD_PAGE is ORed into
+ *          the error word.  No two tokens may have the same slot: which of
+ *          them it then holds, element by element, is undefined.
+ * key_pages, value_pages  device pointers, 16-byte aligned.  They may lie side
+ *          by side in one buffer, but share no element, and overlap none of the
+ *          inputs.  Only the slots named are written.
+ * Ownership, execution and errors: as cs_constrained_softmax.
+ */
+cs_status cs_paged_write(const uint16_t* keys, const uint16_t* values,
+                         const int64_t* slots, uint16_t* key_pages,
+                         uint16_t* value_pages, const cs_write_shape* shape,
+                         void* stream);
+
+/* Host-only argument check (no CUDA call). */
+cs_status cs_check_paged_write_args(const uint16_t* keys,
+                                    const uint16_t* values,
+                                    const int64_t* slots,
+                                    const uint16_t* key_pages,
+                                    const uint16_t* value_pages,
+                                    const cs_write_shape* shape);
+
+typedef struct cs_tree_shape {
+    int32_t batch;       /* sequences, >= 0                                 */
+    int32_t new_tokens;  /* new tokens of a sequence, >= 0; with the heads of
+                            a key head at most 2^30 rows                    */
+    int32_t heads;       /* as in cs_paged_shape, up to                     */
+    int32_t kv_heads;
+    int32_t d_head;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages;
+    int32_t fp16;
+    float scale;
+    int64_t q_stride[3];   /* batch, token, head; elements, non-negative    */
+    int64_t o_stride[3];   /* multiples of 8                                */
+    int64_t k_stride[3];   /* page, slot, head                              */
+    int64_t v_stride[3];
+    int64_t table_stride;  /* entries between page-table rows, >= max_pages,
+                              at most 2^40                                  */
+    int64_t mask_stride[2];  /* batch (0: one mask for all), new token; bytes,
+                                the latter >= new_tokens, at most 2^40, 2^30 */
+} cs_tree_shape;
+
+/*
+ * cs_paged_tree_attention -- attention of several new tokens per sequence: a
+ * tree of drafted tokens, or the next chunk of a prompt.  Of sequence b's
+ * n = lengths[b] tokens in the cache the last w = new_lengths[b] are the new
+ * ones.  New token i attends the n - w tokens before all new ones, and new
+ * token j if mask[b][i][j] is not zero (without a mask: if j <= i):
+ *
+ *   s_j = scale * (query . key_j),  lse = ln sum_j e^(s_j)
+ *   out = sum_j e^(s_j - lse) value_j
+ *
+ * query    device pointer, [batch, new_tokens, heads, d_head]; out the same,
+ *          written completely, overlapping nothing else of the call, nor
+ *          itself.  Rows from w on, and those that attend nothing, get zeros
+ *          and lse = -inf.
+ * key_pages, value_pages, page_table, lengths  as for cs_paged_attention: the
+ *          new tokens' keys and values have been written there.
+ * new_lengths  device pointer, [batch] int32, or NULL: new_tokens each.
+ * mask     device pointer, [batch, new_tokens, new_tokens] bytes, or NULL.
+ *          Where either index is w or more it is not read.
+ * lse      optional device pointer, [batch, new_tokens, heads] fp32,
+ *          contiguous.
+ * workspace  device pointer, 16-byte aligned, at least
+ *          cs_paged_tree_attention_workspace(shape) bytes (NULL when that is
+ *          0): the caller's, used by this call only, free after it on the
+ *          stream.
+ *
+ * A length out of range, new_lengths outside 0..min(new_tokens, lengths[b])
+ * and page numbers out of range are taken as the nearest that is in range, or
+ * left out, and OR CS_ERR_BAD_PAGE into the error word.  The weights are
+ * rounded to the cache's type, their sums are fp32 in a fixed order, which
+ * depends on the batch's lengths (repeated calls give the same bits).  NaN or
+ * infinite scores propagate to their row and OR CS_ERR_NAN_INPUT; a NaN or
+ * infinite value of a token propagates to every row of its sequence and head,
+ * those that do not attend it too.  Ownership, execution and errors: as
+ * cs_constrained_softmax.
+ */
+cs_status cs_paged_tree_attention(
+    const uint16_t* query, const uint16_t* key_pages,
+    const uint16_t* value_pages, const int32_t* page_table,
+    const int32_t* lengths, const int32_t* new_lengths, const uint8_t* mask,
+    uint16_t* out, float* lse, const cs_tree_shape* shape, void* workspace,
+    int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the call needs (0 where no row of the table holds more
+ * than two blocks); negative for a malformed shape.  Host-only. */
+int64_t cs_paged_tree_attention_workspace(const cs_tree_shape* shape);
+
+/* Host-only argument check (no CUDA call). */
+cs_status cs_check_paged_tree_attention_args(
+    const uint16_t* query, const uint16_t* key_pages,
+    const uint16_t* value_pages, const int32_t* page_table,
+    const int32_t* lengths, const int32_t* new_lengths, const uint8_t* mask,
+    const uint16_t* out, const float* lse, const cs_tree_shape* shape,
+    const void* workspace, int64_t workspace_bytes);
 
 /*
  * Throughput probe of the ex2 unit, the unit this operation is bound by.
