@@ -450,7 +450,7 @@ struct TreeTask {
     uint16_t* out;             // as q
     float* lse;                // [batch, new_tokens, heads] or null
     float2* part_stats;        // workspace: [groups, width, 2, part_rows] (max, sum)
-    float* part_out;           // [groups, width, 2, d_head / 8, part_rows, 8]
+    float* part_out;           // [groups, width, 2, d_head / 4, part_rows, 4]
     unsigned int* err;         // device error word
     int64_t q_stride[3], o_stride[3], k_stride[3], v_stride[3];
     int64_t table_stride;
@@ -464,6 +464,7 @@ struct TreeTask {
     int32_t split;             // 1: the blocks are dealt to groups, this many
     int32_t groups;
     int32_t fp16;
+    int32_t box_rows;          // tokens of a tensor copy; 0: copies of 16 bytes
     float scale;
     uint64_t wait_limit_cycles;
 };

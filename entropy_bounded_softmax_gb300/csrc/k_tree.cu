@@ -36,6 +36,7 @@
 #include <math.h>
 
 #include "cs_fattn.cuh"
+#include "cs_tensormap.h"
 
 namespace cs {
 namespace {
@@ -44,10 +45,15 @@ using namespace csd;
 
 constexpr int kTrThreads = 512;
 constexpr int kTrMmaWarp = 8;
+constexpr int kTrPartWarp = 9;
 constexpr int kTrCopyWarp = 12;
+constexpr int kTrWarpBatch = 256;      // sequences whose lengths one warp adds up
 constexpr float kTrWeightBits = 8.0f;  // log2 of the weights' common factor
 constexpr float kTrLagBits = 6.0f;     // how far the maximum may lag
 constexpr int kTrWords = 8;            // blocks whose kept tokens are noted
+constexpr int kTrParts = 4;            // parts that are known ahead
+constexpr int kTrPartWarps = 13;       // that read them
+constexpr int kTrPartCost = 2;         // blocks that take as long as a part's start and end
 
 struct TrBF16 {
     static constexpr bool kFp16 = false;
@@ -84,9 +90,10 @@ struct TreePlan {
     static constexpr int kK = kQ + NQ * kTile;
     static constexpr int kV = kK + kStages * kBlock;
     static constexpr int kBars = kV + kStages * kBlock;
-    static constexpr int kNumBars = 4 * kStages + 11;
+    static constexpr int kNumBars = 4 * kStages + 11 + 2 * kTrParts;
     static constexpr int kWords = kBars + (8 * kNumBars + 15) / 16 * 16;  // [kTrWords][4]
-    static constexpr int kScan = kWords + kTrWords * 16;   // [18] ints
+    static constexpr int kParts = kWords + kTrWords * 16;
+    static constexpr int kScan = kParts + kTrParts * 48;   // [18] ints
     static constexpr int kFlags = kScan + 80;              // abort, tmem
     static constexpr int kStats = kFlags + 16;             // [2][128] float2 (one tile)
     static constexpr int kBytes = kStats + (NQ == 1 ? 2 * 128 * 8 : 0);
@@ -109,6 +116,10 @@ __device__ __forceinline__ TreeLens tree_lens(const TreeTask& t, int b, bool& ba
     return x;
 }
 
+__device__ __forceinline__ int tree_places(int steps) {
+    return steps > 0 ? steps + kTrPartCost : 0;
+}
+
 // Blocks of a unit of sequence b.
 template <int BLK>
 __device__ __forceinline__ int tree_steps(const TreeLens& x) {
@@ -116,8 +127,8 @@ __device__ __forceinline__ int tree_steps(const TreeLens& x) {
 }
 
 // The sum of n over the threads before this one and over all of the CTA of
-// 32 WARPS threads; scan: WARPS shared ints, free again after the caller's next
-// __syncthreads.
+// 32 WARPS threads, or of the calling warp (WARPS 1); scan: WARPS shared ints,
+// free again after the caller's next barrier.
 template <int WARPS>
 __device__ __forceinline__ void tree_scan(int n, int* scan, int& before, int& all) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -127,9 +138,13 @@ __device__ __forceinline__ void tree_scan(int n, int* scan, int& before, int& al
         const int x = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up += x;
     }
+    before = up - n;
+    if (WARPS == 1) {
+        all = __shfl_sync(0xffffffffu, up, 31);
+        return;
+    }
     if (lane == 31) scan[warp] = up;
     __syncthreads();
-    before = up - n;
     all = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
@@ -137,34 +152,43 @@ __device__ __forceinline__ void tree_scan(int n, int* scan, int& before, int& al
         all += scan[w];
     }
 }
+template <int WARPS>
+__device__ __forceinline__ void tree_sync() {
+    if (WARPS == 1) __syncwarp();
+    else __syncthreads();
+}
 
-// What a group of CTAs has of the list of the batch's blocks: for each sequence,
-// for each of its bundles of `width` rows (units side by side), the blocks.
-// Blocks g0 .. g1 - 1, the first in sequence b whose first is `base`.
+// What a group of CTAs has of the batch's list: for each sequence, for each of
+// its bundles of `width` units side by side, kTrPartCost places for a part's
+// start and end and then its blocks.  Places g0 .. g1 - 1, the first in sequence
+// b whose first is `base`.
 struct TreeDeal {
     int g0, g1, b, base, share;
 };
 
-// By a whole CTA; false without blocks.  scan: WARPS + 2 shared ints.
+// By a whole CTA of 32 WARPS threads, or one warp; false without places.  scan:
+// WARPS + 2 shared ints.
 template <int WARPS, int BLK>
 __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan, TreeDeal& d) {
     constexpr int kThreads = 32 * WARPS;
+    const int thread = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
     bool bad;
-    auto blocks = [&](int i) {
-        return i < t.batch ? tree_steps<BLK>(tree_lens(t, i, bad)) * t.bundles : 0;
+    auto places = [&](int i) {
+        return i < t.batch ? tree_places(tree_steps<BLK>(tree_lens(t, i, bad))) * t.bundles : 0;
     };
     int total = 0, before;
     const bool once = t.batch <= kThreads;   // one walk over the lengths is enough
     if (!once) {
         int n = 0;
-        for (int i = threadIdx.x; i < t.batch; i += kThreads) n += blocks(i);
+#pragma unroll 4
+        for (int i = thread; i < t.batch; i += kThreads) n += places(i);
         tree_scan<WARPS>(n, scan, before, total);
-        __syncthreads();
+        tree_sync<WARPS>();
     }
     int done = 0;
     for (int b0 = 0; b0 < t.batch; b0 += kThreads) {
-        const int i = b0 + threadIdx.x;
-        const int n = blocks(i);
+        const int i = b0 + thread;
+        const int n = places(i);
         int first, all;
         tree_scan<WARPS>(n, scan, first, all);
         if (once) total = all;
@@ -178,7 +202,7 @@ __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan,
             scan[WARPS + 1] = first;
         }
         done += all;
-        __syncthreads();
+        tree_sync<WARPS>();
         if (done > d.g0) break;
     }
     // (In range even where the lengths were changed under the call.)
@@ -187,75 +211,41 @@ __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan,
     return true;
 }
 
-// Blocks s0 .. s1 - 1 of a unit of sequence b: all of them, or part `place` of
-// the workspace.
-struct TreePart {
-    int b, row, s0, s1;
-    TreeLens n;
-    bool whole;
-    int place;
+// Blocks of a unit that a CTA takes, all of them or a part of them, as one warp
+// works them out for the others.  Rows are token by token, `group` heads each.
+struct alignas(16) TreePart {
+    int n;         // blocks, which may be none; -1: no part is left
+    int key0;      // the first one's first token
+    int b, hk;
+    int r0, rows;  // first row of the unit, and rows there
+    int valid;     // of those: rows of new tokens, may be negative
+    int len;       // tokens of the sequence,
+    int context;   // those before all new ones
+    int place;     // of the workspace; -1: finished here
+    int pad[2];
 };
 
-// A CTA's parts, one after the other; every role walks its own copy.
-template <int BLK>
-struct TreeWalk {
-    int g, g0, g1, b, bundle, s, steps, x;
-    TreeLens n;
-    bool any;
-    __device__ __forceinline__ bool next(const TreeTask& t, TreePart& p) {
-        if (!any || g >= g1) return false;
-        bool bad;
-        while (steps == 0 || bundle == t.bundles) {
-            if (b + 1 >= t.batch) return false;
-            n = tree_lens(t, ++b, bad);
-            steps = tree_steps<BLK>(n);
-            bundle = 0;
-        }
-        p.b = b;
-        p.row = bundle * t.width + x;
-        p.s0 = s;
-        p.s1 = min(steps, s + g1 - g);
-        p.n = n;
-        p.whole = p.s0 == 0 && p.s1 == steps;
-        p.place = 2 * static_cast<int>(blockIdx.x) + (g > g0);
-        g += p.s1 - p.s0;
-        s = p.s1;
-        if (s == steps) {
-            s = 0;
-            ++bundle;
-        }
-        return true;
-    }
-};
-
-// The rows of a unit: first row, rows there and rows whose token is new (rows
-// are token by token, `group` heads each).
-struct TreeRows {
-    int hk, r0, rows, valid;
-};
-template <int NQ>
-__device__ __forceinline__ TreeRows tree_rows(const TreeTask& t, int row, const TreeLens& n) {
-    TreeRows u;
-    const int tile = row / t.kv_heads;
-    u.hk = row - tile * t.kv_heads;
-    u.r0 = 128 * NQ * tile;
-    u.rows = min(128 * NQ, t.new_tokens * t.group - u.r0);
-    u.valid = min(128 * NQ, n.fresh * t.group - u.r0);   // may be negative
-    return u;
-}
-
-// Blocks s0 .. s1 - 1 that some row of the unit attends: none without rows, and
-// none past the last row's token where each attends those before it.
-template <int BLK>
-__device__ __forceinline__ int tree_blocks(const TreeTask& t, const TreePart& p,
-                                           const TreeRows& u) {
-    if (u.valid <= 0) return 0;
-    int last = p.s1;
-    if (!t.mask) {
-        const int token = (u.r0 + u.valid - 1) / t.group;
-        last = min(last, (p.n.len - p.n.fresh + token + BLK) / BLK);
-    }
-    return max(0, last - p.s0);
+template <int BLK, int NQ>
+__device__ __forceinline__ TreePart tree_part(const TreeTask& t, int b, const TreeLens& n,
+                                              int unit, int s0, int s1, int steps) {
+    TreePart p{};
+    const int tile = unit / t.kv_heads;
+    p.b = b;
+    p.hk = unit - tile * t.kv_heads;
+    p.r0 = 128 * NQ * tile;
+    p.rows = min(128 * NQ, t.new_tokens * t.group - p.r0);
+    p.valid = min(128 * NQ, n.fresh * t.group - p.r0);
+    p.key0 = s0 * BLK;
+    p.len = n.len;
+    p.context = n.len - n.fresh;
+    // A part at a share's end begins its unit, one at the start does not.
+    p.place = s0 == 0 && s1 == steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (s0 == 0);
+    // None without rows, and none past the last row's token where each row
+    // attends those before it.
+    int last = s1;
+    if (!t.mask) last = min(last, (p.context + (p.r0 + p.valid - 1) / t.group + BLK) / BLK);
+    p.n = p.valid <= 0 ? 0 : max(0, last - s0);
+    return p;
 }
 
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -286,7 +276,9 @@ __device__ __forceinline__ void tree_lse(const TreeTask& t, int b, int i, int h,
 }
 
 template <int DP, int NQ, class E>
-__global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
+__global__ void __launch_bounds__(kTrThreads, 1)
+tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
+            const __grid_constant__ CUtensorMap map_v) {
     using L = TreePlan<DP, NQ>;
     constexpr int NS = L::kStages, BLK = L::kBlk, NT = L::kTiles;
     // (No room is left to align it here: the swizzled tiles want 1024 bytes.)
@@ -308,61 +300,56 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
     uint64_t* o_done = q_empty + 1;           // the part's last P V completed
     uint64_t* drained = o_done + 1;
     uint64_t* joined = drained + 1;           // eight softmax warps
+    uint64_t* part_full = joined + 1;         // [kTrParts]
+    uint64_t* part_empty = part_full + kTrParts;
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kWords);
+    TreePart* ahead_of = reinterpret_cast<TreePart*>(smem + L::kParts);
+    int* scan = reinterpret_cast<int*>(smem + L::kScan);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
     allow_next_kernel();
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const bool tensor_copies = t.box_rows > 0;
     if (warp == kTrCopyWarp) {
         for (int i = lane; i < L::kNumBars; i += 32) {
             uint64_t* bar = bars + i;
-            mbar_init(bar, bar < k_empty ? 128u + 4u
-                           : (bar >= v_full && bar < v_empty) || bar == q_full ? 128u
+            mbar_init(bar, bar < k_empty ? (tensor_copies ? 1u : 128u + 4u)
+                           : bar >= v_full && bar < v_empty ? (tensor_copies ? 1u : 128u)
+                           : bar == q_full ? (tensor_copies ? 64u : 128u)
                            : bar >= p_full && bar < q_full ? 4u
-                           : bar == joined ? 8u : 1u);
+                           : bar == joined ? 8u
+                           : bar >= part_empty ? static_cast<uint32_t>(kTrPartWarps) : 1u);
         }
         if (lane == 0) flags[0] = 0u;
         fence_mbar_init();
     } else if (warp == kTrMmaWarp) {
         tmem_alloc(const_cast<uint32_t*>(flags) + 1, L::kTmemCols);
+    } else if (warp == kTrCopyWarp + 1 && lane == 0 && tensor_copies) {
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
     }
-    TreeWalk<BLK> walk{};
-    {
-        const int grp = static_cast<int>(blockIdx.x) / t.width;
-        walk.x = static_cast<int>(blockIdx.x) - grp * t.width;
-        bool bad;
-        if (t.split) {
-            TreeDeal d;
-            walk.any = tree_deal<kTrThreads / 32, BLK>(
-                t, grp, reinterpret_cast<int*>(smem + L::kScan), d);
-            if (walk.any) {
-                walk.g = walk.g0 = d.g0;
-                walk.g1 = d.g1;
-                walk.b = d.b;
-                walk.n = tree_lens(t, d.b, bad);
-                walk.steps = tree_steps<BLK>(walk.n);
-                if (walk.steps > 0) {
-                    walk.bundle = min((d.g0 - d.base) / walk.steps, t.bundles);
-                    walk.s = (d.g0 - d.base) % walk.steps;
-                }
-            }
-        } else {
-            // Each group one bundle of one sequence, blocks or not.
-            walk.b = grp / t.bundles;
-            walk.bundle = grp - walk.b * t.bundles;
-            walk.n = tree_lens(t, walk.b, bad);
-            walk.steps = max(1, tree_steps<BLK>(walk.n));
-            walk.g1 = walk.steps;
-            walk.any = true;
-        }
-    }
+    const int grp = static_cast<int>(blockIdx.x) / t.width;
+    TreeDeal deal{};
+    bool any = false;
+    // A large batch's lengths are added up by the whole CTA.
+    const bool large = t.split && t.batch > kTrWarpBatch;
+    if (large) any = tree_deal<kTrThreads / 32, BLK>(t, grp, scan, deal);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = flags[1];
     const int group = t.group;
+    // Part i, to be given back after its last use by one arrival of the warp.
+    auto part = [&](int i, bool& ok) {
+        ok = warp_wait(&part_full[i % kTrParts], i / kTrParts, limit);
+        return &ahead_of[i % kTrParts];
+    };
+    auto done_with = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&part_empty[i % kTrParts]);
+    };
 
     if (warp < 8) {
         // -------------------------------------------------------- softmax
@@ -370,143 +357,152 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
         const int wg = warp >> 2;              // warpgroup
         const int tile = NT == 2 ? wg : 0;
         const int tr = 32 * (warp & 3) + lane; // row of the tile
+        const int warp_r = (NQ == 2 ? 128 * wg : 0) + 32 * (warp & 3);   // of the unit
+        const int r = warp_r + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + BLK * tile;
         const uint32_t out0 = tmem + lanes + L::kOut;
         const uint32_t to = out0 + DP * tile;
         const float c = t.scale * kLog2e;
-        float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
+        // This warpgroup's blocks: all of them, or every other one.
+        constexpr int kStep = NQ == 1 && NT == 2 ? 2 : 1;
+        const int first = kStep == 2 ? wg : 0;
         int visit = 0;      // blocks of this warpgroup so far, over all parts
-        int parts = 0;      // parts with blocks
+        int with_blocks = 0;   // parts so far that have some
         int block0 = 0;     // blocks of the parts before
         int joins = 0;
-        bool ok = true;
-        TreePart p;
-        while (ok && walk.next(t, p)) {
-            const TreeRows u = tree_rows<NQ>(t, p.row, p.n);
-            const int n = tree_blocks<BLK>(t, p, u);
-            // This warpgroup's blocks: all of them, or every other one.
-            const int first = NQ == 1 && NT == 2 ? wg : 0, step = NQ == 1 && NT == 2 ? 2 : 1;
-            const int mine = NT == 1 && wg > 0 ? 0 : n > first ? (n - first + step - 1) / step : 0;
-            const int r = (NQ == 2 ? 128 * wg : 0) + tr;      // row of the unit
-            const int warp_r = (NQ == 2 ? 128 * wg : 0) + 32 * (warp & 3);
-            const int token = (u.r0 + r) / group;             // new token
-            const bool valid = r < u.valid;
-            const bool warp_valid = warp_r < u.valid;
-            const int context = p.n.len - p.n.fresh;
-            // Rows keep the tokens below this, and of them those the mask keeps.
-            const int row_limit = !valid ? 0 : t.mask ? p.n.len : context + token + 1;
+        for (int ip = 0;; ++ip) {
+            bool ok;
+            const TreePart* p = part(ip, ok);
+            if (!ok) break;
+            const int n = p->n;
+            if (n < 0) break;
+            const int mine = NT == 1 && wg > 0 ? 0 : (n - first + kStep - 1) / kStep;
             float m = -INFINITY, l = 0.0f;
-            for (int k = 0; k < mine; ++k, ++visit) {
-                const int block = first + step * k;
-                const int key = (p.s0 + block) * BLK;
-                uint32_t kept[BLK / 32];
-#pragma unroll
-                for (int w = 0; w < BLK / 32; ++w) kept[w] = bits_below(row_limit, key + 32 * w);
-                if (t.mask && warp_valid && key + BLK > context) {
-                    // The mask's rows of this warp's tokens, 32 bytes at a time.
-                    const uint8_t* rows = t.mask + p.b * t.mask_stride[0];
-                    const int i0 = (u.r0 + warp_r) / group;
-                    const int i1 = min((u.r0 + warp_r + 31) / group, p.n.fresh - 1);
-#pragma unroll 2
-                    for (int i = i0; i <= i1; ++i) {
-#pragma unroll
-                        for (int w = 0; w < BLK / 32; ++w) {
-                            const int j = key + 32 * w + lane - context;
-                            bool keep = j < 0;
-                            if (j >= 0 && j < p.n.fresh)
-                                keep = rows[i * t.mask_stride[1] + j] != 0;
-                            const uint32_t bits = __ballot_sync(0xffffffffu, keep);
-                            if (i == token) kept[w] &= bits;
-                        }
-                    }
-                }
-                ok = warp_wait(&s_full[tile], visit, limit);
-                if (!ok) break;
-                tc_fence_after_sync();
-                if (warp_valid) {
-                    bool edge = false;
-#pragma unroll
-                    for (int w = 0; w < BLK / 32; ++w) {
-                        kept[w] &= words[4 * ((block0 + block) % kTrWords) + w];
-                        edge = edge || kept[w] != ~0u;
-                    }
-                    edge = __any_sync(0xffffffffu, edge);
-                    uint32_t s[BLK];
-#pragma unroll
-                    for (int x = 0; x < BLK / 32; ++x) tmem_ld32_async(ts + 32 * x, s + 32 * x);
-                    tmem_wait_ld<BLK>(s);
+            if (mine > 0) {
+                const int context = p->context, token = (p->r0 + r) / group;
+                const bool warp_valid = warp_r < p->valid;
+                // The row keeps the tokens below this, and of them those the
+                // mask keeps; every row of the warp those below `all_below`.
+                // (Rows past the new tokens count for nothing in the end.)
+                const int row_limit = t.mask || r >= p->valid ? p->len : context + token + 1;
+                const int all_below =
+                    __reduce_min_sync(0xffffffffu, t.mask ? min(row_limit, context) : row_limit);
+                int key = p->key0 + first * BLK;
+                for (int k = 0; k < mine; ++k, ++visit, key += kStep * BLK) {
+                    uint32_t kept[BLK / 32];
+                    bool edge = key + BLK > all_below;
                     if (edge) {
 #pragma unroll
-                        for (int x = 0; x < BLK; ++x)
-                            if (!((kept[x >> 5] >> (x & 31)) & 1u))
-                                s[x] = __float_as_uint(-INFINITY);
-                    }
-                    float mx[4] = {m, m, m, m};
+                        for (int w = 0; w < BLK / 32; ++w)
+                            kept[w] = bits_below(row_limit, key + 32 * w);
+                        if (t.mask && warp_valid && key + BLK > context) {
+                            // The mask's rows of this warp's tokens, 32 bytes
+                            // at a time.
+                            const int fresh = p->len - context;
+                            const int i0 = (p->r0 + warp_r) / group;
+                            const int i1 = min((p->r0 + warp_r + 31) / group, fresh - 1);
+                            const uint8_t* row = t.mask + p->b * t.mask_stride[0] +
+                                                 i0 * t.mask_stride[1] + key - context + lane;
+#pragma unroll 2
+                            for (int i = i0; i <= i1; ++i, row += t.mask_stride[1]) {
 #pragma unroll
-                    for (int x = 0; x < BLK; x += 8)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            mx[y] = max3(mx[y], __uint_as_float(s[x + 2 * y]),
-                                         __uint_as_float(s[x + 2 * y + 1]));
-                    const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                    if (k == 0) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, (top - m) * c > kTrLagBits)) {
-                        const float f = m == -INFINITY ? 0.0f : ex2((m - top) * c);
-                        m = top;
-                        l *= f;
-                        ok = warp_wait(&o_full[tile], visit - 1, limit);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll 1
-                        for (int x = 0; x < DP / 32; ++x) {
-                            uint32_t o[32];
-                            tmem_ld32_async(to + 32 * x, o);
-                            tmem_wait_ld<32>(o);
-#pragma unroll
-                            for (int y = 0; y < 32; ++y)
-                                o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                            tmem_st32(to + 32 * x, o);
+                                for (int w = 0; w < BLK / 32; ++w) {
+                                    const int j = key + 32 * w + lane - context;
+                                    bool keep = j < 0;
+                                    if (j >= 0 && j < fresh) keep = row[32 * w] != 0;
+                                    const uint32_t bits = __ballot_sync(0xffffffffu, keep);
+                                    if (i == token) kept[w] &= bits;
+                                }
+                            }
                         }
                     }
-                    const float mc = (m == -INFINITY ? 0.0f : m * c) - kTrWeightBits;
-                    const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    ok = warp_wait(&s_full[tile], visit, limit);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (warp_valid) {
+                        // (Tokens that are not in the cache, too.)
+                        const uint4 there = *reinterpret_cast<const uint4*>(
+                            words + 4 * ((block0 + first + kStep * k) % kTrWords));
+                        const uint32_t in[4] = {there.x, there.y, there.z, there.w};
+                        uint32_t every = ~0u;
 #pragma unroll
-                    for (int x = 0; x < BLK / 2; ++x) {
-                        const float2 y = fma2(make_float2(__uint_as_float(s[2 * x]),
-                                                          __uint_as_float(s[2 * x + 1])),
-                                              c2, mc2);
-                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                        sum[x & 1] = add2(sum[x & 1], e);
-                        s[x] = E::pack(e.x, e.y);
+                        for (int w = 0; w < BLK / 32; ++w) every &= in[w];
+                        if (every != ~0u || edge) {
+#pragma unroll
+                            for (int w = 0; w < BLK / 32; ++w) kept[w] = edge ? kept[w] & in[w] : in[w];
+                            edge = true;
+                        }
+                        uint32_t s[BLK];
+#pragma unroll
+                        for (int x = 0; x < BLK / 32; ++x) tmem_ld32_async(ts + 32 * x, s + 32 * x);
+                        tmem_wait_ld<BLK>(s);
+                        if (edge) {
+#pragma unroll
+                            for (int x = 0; x < BLK; ++x)
+                                if (!((kept[x >> 5] >> (x & 31)) & 1u))
+                                    s[x] = __float_as_uint(-INFINITY);
+                        }
+                        float mx[4] = {m, m, m, m};
+#pragma unroll
+                        for (int x = 0; x < BLK; x += 8)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                mx[y] = max3(mx[y], __uint_as_float(s[x + 2 * y]),
+                                             __uint_as_float(s[x + 2 * y + 1]));
+                        const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                        if (k == 0) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, (top - m) * c > kTrLagBits)) {
+                            const float f = m == -INFINITY ? 0.0f : ex2((m - top) * c);
+                            m = top;
+                            l *= f;
+                            ok = warp_wait(&o_full[tile], visit - 1, limit);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int x = 0; x < DP; x += 16) {
+                                float o[16];
+                                tmem_ld16(to + x, o);
+                                uint32_t w[16];
+#pragma unroll
+                                for (int y = 0; y < 16; ++y) w[y] = __float_as_uint(o[y] * f);
+                                tmem_st16(to + x, w);
+                            }
+                        }
+                        const float mc = (m == -INFINITY ? 0.0f : m * c) - kTrWeightBits;
+                        const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int x = 0; x < BLK / 2; ++x) {
+                            const float2 y = fma2(make_float2(__uint_as_float(s[2 * x]),
+                                                              __uint_as_float(s[2 * x + 1])),
+                                                  c2, mc2);
+                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                            sum[x & 1] = add2(sum[x & 1], e);
+                            s[x] = E::pack(e.x, e.y);
+                        }
+#pragma unroll
+                        for (int x = 0; x < BLK / 64; ++x) tmem_st32(ts + 32 * x, s + 32 * x);
+                        tmem_wait_st();
+                        sum[0] = add2(sum[0], sum[1]);
+                        l += sum[0].x + sum[0].y;
                     }
-#pragma unroll
-                    for (int x = 0; x < BLK / 64; ++x) tmem_st32(ts + 32 * x, s + 32 * x);
-                    tmem_wait_st();
-                    sum[0] = add2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
+                    // (Of a warp without rows the weights are what was there.)
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[tile]);
                 }
-                // (Of a warp without rows the weights are what was there.)
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[tile]);
-            }
-            if (!ok) break;
-            block0 += n;
-            if (n > 0) {
-                ok = warp_wait(o_done, parts++, limit);
                 if (!ok) break;
-                tc_fence_after_sync();
             }
+            block0 += n;
+            if (r >= p->valid) l = 0.0f;
             // The row's maximum (base 2) and sum, and the factors of the outputs
             // in tensor memory: with one tile, both warpgroups' parts.
             float top = m == -INFINITY ? 0.0f : m * c, sum = l;
-            float f[2] = {1.0f, 1.0f};
-            bool has[2] = {mine > 0, false};
-            int d0 = 0, d1 = DP;
+            float f0 = l == 0.0f ? 0.0f : 1.0f, f1 = 0.0f;
             if (NQ == 1) {
+                float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
                 stats[128 * wg + tr] = make_float2(top, l);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(joined);
@@ -514,77 +510,81 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
                 if (!ok) break;
                 const float2 a = stats[tr], z = stats[128 + tr];
                 top = a.y == 0.0f ? z.x : z.y == 0.0f ? a.x : fmaxf(a.x, z.x);
-                f[0] = a.y == 0.0f ? 0.0f : ex2(a.x - top);
-                f[1] = z.y == 0.0f ? 0.0f : ex2(z.x - top);
-                sum = fmaf(a.y, f[0], z.y * f[1]);
-                has[0] = n > 0;
-                has[1] = NT == 2 && n > 1;
-                d0 = wg * (DP / 2);
-                d1 = d0 + DP / 2;
+                f0 = a.y == 0.0f ? 0.0f : ex2(a.x - top);
+                f1 = z.y == 0.0f ? 0.0f : ex2(z.x - top);
+                sum = fmaf(a.y, f0, z.y * f1);
             }
-            const uint32_t from0 = NQ == 1 ? out0 : to;
-            const int h = u.hk * group + (u.r0 + r) - token * group;
-            const bool here = r < u.rows;
-            const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
-            uint16_t* row = here ? tree_out(t, p.b, token, h) : nullptr;
-            float* part = nullptr;
-            if (!p.whole) {
-                const int64_t at = static_cast<int64_t>(p.place) * t.part_rows;
-                part = t.part_out + at * t.d_head + r * 8;
-                if (here && (NQ == 2 || wg == 0)) t.part_stats[at + r] = make_float2(top, sum);
-            } else if (here && (NQ == 2 || wg == 0)) {
-                tree_lse(t, p.b, token, h, top, sum);
+            if (n > 0) {
+                ok = warp_wait(o_done, with_blocks++, limit);
+                if (!ok) break;
+                tc_fence_after_sync();
             }
-            if (warp_r < u.rows) {
+            const int rows = p->rows;
+            if (warp_r < rows) {
+                const bool here = r < rows;
+                const int token = (p->r0 + r) / group;
+                const int h = p->hk * group + (p->r0 + r) - token * group;
+                const int place = p->place;
+                // Whose columns: with one tile each warpgroup half of them.
+                const int d0 = NQ == 1 ? wg * (DP / 2) : 0;
+                const int d1 = min(t.d_head, NQ == 1 ? d0 + DP / 2 : DP);
+                const uint32_t from = NQ == 1 ? out0 : to;
+                const bool mine_first = here && (NQ == 2 || wg == 0);
+                uint16_t* row = nullptr;
+                float4* part_row = nullptr;
+                if (place < 0) {
+                    if (here) row = tree_out(t, p->b, token, h);
+                    if (mine_first) tree_lse(t, p->b, token, h, top, sum);
+                    const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+                    f0 *= inv;
+                    f1 *= inv;
+                } else {
+                    const int64_t at = static_cast<int64_t>(place) * t.part_rows;
+                    part_row = reinterpret_cast<float4*>(t.part_out + at * t.d_head) + r;
+                    if (mine_first) t.part_stats[at + r] = make_float2(top, sum);
+                }
 #pragma unroll 1
-                for (int d = d0; d < d1 && d < t.d_head; d += 32) {
-                    uint32_t o[32];
+                for (int d = d0; d < d1; d += 16) {
+                    float o[16];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = 0u;
-                    if (has[0]) {
-                        tmem_ld32_async(from0 + d, o);
-                        tmem_wait_ld<32>(o);
-                    }
+                    for (int x = 0; x < 16; ++x) o[x] = 0.0f;
                     // (Exactly 0 of what has no kept token: 0 times a NaN is not.)
+                    if (n > 0) {
+                        float v[16];
+                        tmem_ld16(from + d, v);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        o[x] = f[0] == 0.0f || (NQ == 2 && sum == 0.0f)
-                                   ? 0u : __float_as_uint(__uint_as_float(o[x]) * f[0]);
-                    if (NQ == 1 && has[1]) {
-                        uint32_t z[32];
-                        tmem_ld32_async(out0 + DP + d, z);
-                        tmem_wait_ld<32>(z);
-                        if (f[1] != 0.0f) {
+                        for (int x = 0; x < 16; ++x) o[x] = f0 == 0.0f ? 0.0f : v[x] * f0;
+                    }
+                    if (NQ == 1 && NT == 2 && n > 1) {
+                        float v[16];
+                        tmem_ld16(out0 + DP + d, v);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                o[x] = __float_as_uint(fmaf(__uint_as_float(z[x]), f[1],
-                                                            __uint_as_float(o[x])));
-                        }
+                        for (int x = 0; x < 16; ++x) o[x] = f1 == 0.0f ? o[x] : fmaf(v[x], f1, o[x]);
                     }
                     if (!here) continue;
+                    if (place < 0) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        if (d + 8 * y >= t.d_head) break;
-                        float v[8];
+                        for (int y = 0; y < 16; y += 8)
+                            if (d + y < t.d_head)
+                                *reinterpret_cast<uint4*>(row + d + y) = make_uint4(
+                                    E::pack(o[y], o[y + 1]), E::pack(o[y + 2], o[y + 3]),
+                                    E::pack(o[y + 4], o[y + 5]), E::pack(o[y + 6], o[y + 7]));
+                    } else {
+                        float4* w = part_row + (d / 4) * t.part_rows;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[8 * y + x]);
-                        if (p.whole) {
-                            tree_store8<E>(row, d + 8 * y, v, inv);
-                        } else {
-                            float4* w = reinterpret_cast<float4*>(
-                                part + static_cast<int64_t>(d / 8 + y) * t.part_rows * 8);
-                            w[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            w[1] = make_float4(v[4], v[5], v[6], v[7]);
-                        }
+                        for (int y = 0; y < 16; y += 4, w += t.part_rows)
+                            if (d + y < t.d_head) *w = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
                     }
                 }
             }
+            done_with(ip);
             // The next part's products write over what was read here.
             if (NQ == 1) {
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(joined);
                 ok = warp_wait(joined, joins++, limit);
+                if (!ok) break;
                 tc_fence_after_sync();
             }
         }
@@ -601,20 +601,22 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
             const int steps = (t.d_head + 15) / 16;
             const uint32_t idesc = idesc_half(128, 16 * steps, true, E::kFp16);
             constexpr int kPerBlock = NQ;      // visits of a block
-            int block0 = 0, parts = 0, visits[2] = {0, 0};
-            bool ok = true;
-            TreePart p;
-            while (ok && walk.next(t, p)) {
-                const TreeRows u = tree_rows<NQ>(t, p.row, p.n);
-                const int n = tree_blocks<BLK>(t, p, u);
+            int block0 = 0, with_blocks = 0, visits[2] = {0, 0};
+            for (int ip = 0;; ++ip) {
+                bool ok;
+                const TreePart* p = part(ip, ok);
+                if (!ok) break;
+                const int n = p->n, past = p->len - p->key0;
+                done_with(ip);
+                if (n < 0) break;
                 if (n == 0) continue;
                 const int all = n * kPerBlock;
                 auto scores = [&](int v) {
                     const int i = NT == 2 ? v & 1 : 0;
                     const int kb = block0 + v / kPerBlock, st = kb % NS;
                     if (!warp_wait(&k_full[st], kb / NS, limit)) return false;
-                    if (v == 0 && !warp_wait(q_full, parts, limit)) return false;
-                    fence_proxy_async_smem();
+                    if (v == 0 && !warp_wait(q_full, with_blocks, limit)) return false;
+                    if (!tensor_copies || v == 0) fence_proxy_async_smem();
                     tc_fence_after_sync();
                     mma_tiles<BLK, DP, E::kFp16>(tmem + BLK * i, q + i * tile_step,
                                                  kd + st * stage_step, steps, leader);
@@ -630,7 +632,26 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
                     ok = warp_wait(&v_full[st], kb / NS, limit) &&
                          warp_wait(&p_full[i], visits[i], limit);
                     if (!ok) break;
-                    fence_proxy_async_smem();
+                    if (!tensor_copies) {
+                        fence_proxy_async_smem();
+                    } else if (v % kPerBlock == 0) {
+                        // Values past the length, which a tensor copy brings in
+                        // with the last ones before: 0 times them has to be 0.
+                        const int there = past - (v / kPerBlock) * BLK;
+                        if (there < BLK && there % t.box_rows != 0) {
+                            const int rows = t.box_rows - there % t.box_rows;
+                            unsigned char* tile = smem + L::kV + st * L::kBlock + there * 128;
+#pragma unroll 1
+                            for (int e = lane; e < rows * (DP / 8); e += 32) {
+                                const int r = e / (DP / 8), unit = e % (DP / 8);
+                                *reinterpret_cast<uint4*>(tile + (unit >> 3) * BLK * 128 +
+                                                          r * 128 + (unit & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
                     tc_fence_after_sync();
                     mma_weights<BLK>(tmem + L::kOut + DP * i, tmem + BLK * i, vd + st * stage_step,
                                      idesc, v >= NT, leader);
@@ -640,26 +661,88 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
                     if (v + 1 == all) mma_commit(o_done, leader);
                     if (v + NT < all) ok = scores(v + NT);
                 }
+                if (!ok) break;
                 block0 += n;
-                ++parts;
+                ++with_blocks;
             }
             // No product may be in flight when the tensor memory is freed.
             mma_commit(drained, leader);
             mbar_wait<false>(drained, 0u, t.wait_limit_cycles);
             __syncwarp();
+        } else if (warp == kTrPartWarp) {
+            // ------------------------------------------------------ parts
+            int ip = 0;
+            bool ok = true, bad;
+            auto give = [&](const TreePart& p) {
+                if (ip >= kTrParts)
+                    ok = warp_wait(&part_empty[ip % kTrParts], ip / kTrParts - 1, limit);
+                if (!ok) return;
+                if (lane == 0) {
+                    ahead_of[ip % kTrParts] = p;
+                    mbar_arrive(&part_full[ip % kTrParts]);
+                }
+                ++ip;
+                __syncwarp();
+            };
+            if (t.split) {
+                if (!large) any = tree_deal<1, BLK>(t, grp, scan, deal);
+                int g = deal.g0, b = deal.b - 1, bundle = t.bundles, at = 0, steps = 0;
+                TreeLens n{};
+                if (any) {
+                    n = tree_lens(t, ++b, bad);
+                    steps = tree_steps<BLK>(n);
+                    const int places = max(1, tree_places(steps));
+                    bundle = min((g - deal.base) / places, t.bundles);
+                    at = (g - deal.base) % places;
+                }
+                while (any && ok && g < deal.g1) {
+                    while (b < t.batch && (steps == 0 || bundle == t.bundles)) {
+                        if (++b == t.batch) break;
+                        n = tree_lens(t, b, bad);
+                        steps = tree_steps<BLK>(n);
+                        bundle = 0;
+                    }
+                    if (b >= t.batch) break;
+                    const int places = tree_places(steps);
+                    const int to = min(places, at + deal.g1 - g);
+                    const int s0 = max(0, at - kTrPartCost), s1 = to - kTrPartCost;
+                    if (s1 > s0)
+                        give(tree_part<BLK, NQ>(
+                            t, b, n, bundle * t.width + static_cast<int>(blockIdx.x) - grp * t.width,
+                            s0, s1, steps));
+                    g += to - at;
+                    at = to;
+                    if (at == places) {
+                        at = 0;
+                        ++bundle;
+                    }
+                }
+            } else {
+                // Each group one bundle of one sequence, blocks or not.
+                const int b = grp / t.bundles;
+                const TreeLens n = tree_lens(t, b, bad);
+                const int steps = tree_steps<BLK>(n);
+                give(tree_part<BLK, NQ>(t, b, n,
+                                        (grp - b * t.bundles) * t.width +
+                                            static_cast<int>(blockIdx.x) - grp * t.width,
+                                        0, steps, steps));
+            }
+            TreePart none{};
+            none.n = -1;
+            if (ok) give(none);
         } else if (warp >= kTrCopyWarp) {
             // ----------------------------------------------------- copies
             constexpr int kUnits = DP / 8;         // 16-byte units of a row
             constexpr int kRows = BLK / 4;         // of a block, of this warp
             constexpr int kAtOnce = 32 / kUnits;   // rows an instruction copies
             const int cw = warp - kTrCopyWarp;
-            const int unit = lane % kUnits;
-            const bool in_head = 8 * unit < t.d_head;
-            const uint32_t at_unit = in_head ? 8 * unit : 0;
             // Rows r0 + kAtOnce x + lane / kUnits of a tile of ROWS rows, from
             // the addresses that lanes 0, 1, .. hold of them.
             auto copy_rows = [&](unsigned char* tile, int tile_rows, int r0, int count,
                                  const uint16_t* address, uint32_t there) {
+                const int unit = lane % kUnits;
+                const bool in_head = 8 * unit < t.d_head;
+                const uint32_t at_unit = in_head ? 8 * unit : 0;
 #pragma unroll 4
                 for (int x = 0; x < count / kAtOnce; ++x) {
                     const int y = kAtOnce * x + lane / kUnits, r = r0 + y;
@@ -672,92 +755,177 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
                 }
             };
             const int skip = BLK / t.page_size, rest = BLK - skip * t.page_size;
-            int block0 = 0, parts = 0;
-            bool ok = true;
-            TreePart p;
-            while (ok && walk.next(t, p)) {
-                const TreeRows u = tree_rows<NQ>(t, p.row, p.n);
-                const int n = tree_blocks<BLK>(t, p, u);
-                if (n == 0) continue;
-                // This lane's token of a block (lanes past the rows as others),
-                // its entry of the table, its slot; looked up three blocks
-                // ahead, a table's entry takes a microsecond to come when it is
-                // not in a cache.
-                int tok = p.s0 * BLK + cw * kRows + lane % kRows;
-                int entry = tok / t.page_size, slot = tok - entry * t.page_size;
-                struct Place {
-                    int page, slot;   // slot -1: no token
-                };
-                auto locate = [&]() {
-                    Place at{0, -1};
-                    if (tok < p.n.len) {
-                        at.slot = slot;
-                        at.page = t.page_table[p.b * t.table_stride + entry];
-                    }
-                    tok += BLK;
-                    entry += skip;
-                    slot += rest;
-                    if (slot >= t.page_size) {
-                        slot -= t.page_size;
-                        ++entry;
-                    }
-                    return at;
-                };
-                Place ahead[3];
+            // A lane's token of every block, its entry of the table and its
+            // slot; looked up three blocks ahead: a table's entry takes a
+            // microsecond to come when it is not in a cache.
+            struct Place {
+                int page, slot;   // slot -1: no token
+            };
+            const int32_t* table = nullptr;
+            int tok = 0, len = 0, entry = 0, slot = 0;
+            Place ahead[3];
+            auto locate = [&]() {
+                Place at{0, -1};
+                if (tok < len) {
+                    at.slot = slot;
+                    at.page = table[entry];
+                }
+                tok += BLK;
+                entry += skip;
+                slot += rest;
+                if (slot >= t.page_size) {
+                    slot -= t.page_size;
+                    ++entry;
+                }
+                return at;
+            };
+            auto begin = [&](const TreePart* p, int first) {
+                table = t.page_table + p->b * t.table_stride;
+                len = p->len;
+                tok = p->key0 + first;
+                entry = tok / t.page_size;
+                slot = tok - entry * t.page_size;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) ahead[x] = locate();
-                auto load_q = [&]() {
-                    if (parts > 0 && !warp_wait(q_empty, parts - 1, limit)) return false;
+            };
+            auto next_place = [&]() {
+                const Place at = ahead[0];
+                ahead[0] = ahead[1];
+                ahead[1] = ahead[2];
+                ahead[2] = locate();
+                return at;
+            };
+            // A part's queries, by `warps` warps of which this is number w.
+            auto load_q = [&](const TreePart* p, int w, int warps, int with_blocks) {
+                if (with_blocks > 0 && !warp_wait(q_empty, with_blocks - 1, limit)) return false;
 #pragma unroll 1
-                    for (int i = 0; i < NQ; ++i) {
-                        const int r = 128 * i + 32 * cw + lane;
-                        const int token = (u.r0 + r) / group;
-                        const bool valid = r < u.valid;
-                        const uint16_t* a = t.q;
-                        if (valid)
-                            a = t.q + p.b * t.q_stride[0] + token * t.q_stride[1] +
-                                (u.hk * group + (u.r0 + r) - token * group) * t.q_stride[2];
-                        copy_rows(smem + L::kQ + i * L::kTile, 128, 32 * cw, 32, a,
-                                  __ballot_sync(0xffffffffu, valid));
-                    }
-                    cp_async_arrive(q_full);
-                    return true;
-                };
-                const uint16_t* kbase = t.k_pages + u.hk * t.k_stride[2];
-                const uint16_t* vbase = t.v_pages + u.hk * t.v_stride[2];
-                for (int j = 0; j < n && ok; ++j) {
-                    const Place at = ahead[0];
-                    ahead[0] = ahead[1];
-                    ahead[1] = ahead[2];
-                    ahead[2] = locate();
-                    const bool valid = at.slot >= 0 && at.page >= 0 && at.page < t.num_pages;
-                    if (at.slot >= 0 && !valid) raise_error(t.err, kBitBadPage);
-                    const uint16_t *k = t.q, *v = t.q;
-                    if (valid) {
-                        k = kbase + at.page * t.k_stride[0] + at.slot * t.k_stride[1];
-                        v = vbase + at.page * t.v_stride[0] + at.slot * t.v_stride[1];
-                    }
-                    const uint32_t there = __ballot_sync(0xffffffffu, valid);
-                    const int kb = block0 + j, st = kb % NS;
-                    if (kb >= NS) ok = warp_wait(&k_empty[st], kb / NS - 1, limit);
-                    if (!ok) break;
-                    copy_rows(smem + L::kK + st * L::kBlock, BLK, kRows * cw, kRows, k, there);
-                    cp_async_arrive(&k_full[st]);
-                    if (lane == 0) {
-                        // The tokens that are there, one bit each.
-                        uint32_t* w = words + 4 * (kb % kTrWords);
-                        if (kRows == 32) w[cw] = there;
-                        else reinterpret_cast<uint16_t*>(w)[cw] = static_cast<uint16_t>(there);
-                        mbar_arrive(&k_full[st]);
-                    }
-                    if (kb >= NS) ok = warp_wait(&v_empty[st], kb / NS - 1, limit);
-                    if (!ok) break;
-                    copy_rows(smem + L::kV + st * L::kBlock, BLK, kRows * cw, kRows, v, there);
-                    cp_async_arrive(&v_full[st]);
-                    if (j == 0) ok = load_q();
+                for (int r0 = 32 * w; r0 < 128 * NQ; r0 += 32 * warps) {
+                    const int r = r0 + lane;
+                    const int token = (p->r0 + r) / group;
+                    const bool valid = r < p->valid;
+                    const uint16_t* a = t.q;
+                    if (valid)
+                        a = t.q + p->b * t.q_stride[0] + token * t.q_stride[1] +
+                            (p->hk * group + (p->r0 + r) - token * group) * t.q_stride[2];
+                    copy_rows(smem + L::kQ + (r0 >> 7) * L::kTile, 128, r0 & 127, 32, a,
+                              __ballot_sync(0xffffffffu, valid));
                 }
-                block0 += n;
-                ++parts;
+                cp_async_arrive(q_full);
+                return true;
+            };
+            int block0 = 0, with_blocks = 0;
+            if (tensor_copies && cw >= 2) {
+                // Two warps for the queries,
+                for (int ip = 0;; ++ip) {
+                    bool ok;
+                    const TreePart* p = part(ip, ok);
+                    if (!ok || p->n < 0) break;
+                    if (p->n > 0) ok = load_q(p, cw - 2, 2, with_blocks++);
+                    if (!ok) break;
+                    done_with(ip);
+                }
+            } else if (tensor_copies) {
+                // one for the keys and one for the values: a lane a box.
+                const bool keys = cw == 0;
+                const CUtensorMap* map = keys ? &map_k : &map_v;
+                uint64_t* full = keys ? k_full : v_full;
+                uint64_t* empty = keys ? k_empty : v_empty;
+                unsigned char* ring = smem + (keys ? L::kK : L::kV);
+                const int boxes = BLK / t.box_rows;
+                for (int ip = 0;; ++ip) {
+                    bool ok;
+                    const TreePart* p = part(ip, ok);
+                    if (!ok || p->n < 0) break;
+                    const int n = p->n, hk = p->hk;
+                    if (n > 0) begin(p, (lane % boxes) * t.box_rows);
+                    done_with(ip);
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j) {
+                        const Place at = next_place();
+                        const bool valid = at.page >= 0 && at.page < t.num_pages;
+                        const int kb = block0 + j, st = kb % NS;
+                        if (kb >= NS) ok = warp_wait(&empty[st], kb / NS - 1, limit);
+                        if (!ok) break;
+                        if (keys) {
+                            // Boxes whose page is in the cache, and their tokens.
+                            const bool lost = at.slot >= 0 && !valid;
+                            if (lost && lane < boxes) raise_error(t.err, kBitBadPage);
+                            const uint32_t good = __ballot_sync(0xffffffffu, !lost);
+                            uint32_t bits = ~0u;
+                            if (good != ~0u) {   // rare
+                                bits = 0;
+#pragma unroll 1
+                                for (int x = 0; x < 32; ++x)
+                                    bits |= (good >> ((32 * lane + x) / t.box_rows & 31) & 1u) << x;
+                            }
+                            if (lane < BLK / 32) words[4 * (kb % kTrWords) + lane] = bits;
+                            __syncwarp();
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kBlock);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            // (Outside the cache: zeros.)
+                            const int page = at.slot >= 0 && valid ? at.page : t.num_pages;
+                            unsigned char* dst = ring + st * L::kBlock + lane * t.box_rows * 128;
+#pragma unroll
+                            for (int x = 0; x < DP / 64; ++x)
+                                tma_load_4d(dst + x * BLK * 128, map, 64 * x, hk,
+                                            max(at.slot, 0), page, &full[st]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    block0 += n;
+                }
+                // None may land in shared memory after the CTA has ended.
+                if (*limit.abort_flag) {
+                    for (int st = 0; st < NS; ++st)
+                        for (int phase = 0; phase < 2; ++phase)
+                            mbar_wait<false>(&full[st], phase, t.wait_limit_cycles / 8);
+                }
+                __syncwarp();
+            } else {
+                for (int ip = 0;; ++ip) {
+                    bool ok;
+                    const TreePart* p = part(ip, ok);
+                    if (!ok || p->n < 0) break;
+                    const int n = p->n;
+                    if (n > 0) begin(p, cw * kRows + lane % kRows);
+                    const uint16_t* kbase = t.k_pages + p->hk * t.k_stride[2];
+                    const uint16_t* vbase = t.v_pages + p->hk * t.v_stride[2];
+#pragma unroll 1
+                    for (int j = 0; j < n && ok; ++j) {
+                        const Place at = next_place();
+                        const bool valid = at.slot >= 0 && at.page >= 0 && at.page < t.num_pages;
+                        if (at.slot >= 0 && !valid) raise_error(t.err, kBitBadPage);
+                        const uint16_t *k = t.q, *v = t.q;
+                        if (valid) {
+                            k = kbase + at.page * t.k_stride[0] + at.slot * t.k_stride[1];
+                            v = vbase + at.page * t.v_stride[0] + at.slot * t.v_stride[1];
+                        }
+                        const uint32_t there = __ballot_sync(0xffffffffu, valid);
+                        const int kb = block0 + j, st = kb % NS;
+                        if (kb >= NS) ok = warp_wait(&k_empty[st], kb / NS - 1, limit);
+                        if (!ok) break;
+                        copy_rows(smem + L::kK + st * L::kBlock, BLK, kRows * cw, kRows, k, there);
+                        cp_async_arrive(&k_full[st]);
+                        if (lane == 0) {
+                            // The tokens that are there, one bit each.
+                            uint32_t* w = words + 4 * (kb % kTrWords);
+                            if (kRows == 32) w[cw] = there;
+                            else reinterpret_cast<uint16_t*>(w)[cw] = static_cast<uint16_t>(there);
+                            mbar_arrive(&k_full[st]);
+                        }
+                        if (kb >= NS) ok = warp_wait(&v_empty[st], kb / NS - 1, limit);
+                        if (!ok) break;
+                        copy_rows(smem + L::kV + st * L::kBlock, BLK, kRows * cw, kRows, v, there);
+                        cp_async_arrive(&v_full[st]);
+                        if (j == 0) ok = load_q(p, cw, 4, with_blocks++);
+                    }
+                    if (!ok) break;
+                    done_with(ip);
+                    block0 += n;
+                }
             }
             cp_async_wait_all();
         }
@@ -765,22 +933,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) tree_kernel(const TreeTask t) {
 
     // Sequences without blocks in a dealt batch: zeros, by the CTAs in turn;
     // what is wrong with a length is reported here too.
-    for (int b = t.split ? static_cast<int>(blockIdx.x)
-                         : static_cast<int>(blockIdx.x) / (t.width * t.bundles);
-         b < t.batch; b += t.split ? static_cast<int>(gridDim.x) : t.batch) {
+    for (int b = t.split ? static_cast<int>(blockIdx.x) : grp / t.bundles; b < t.batch;
+         b += t.split ? static_cast<int>(gridDim.x) : t.batch) {
         bool bad;
         const TreeLens n = tree_lens(t, b, bad);
         if (bad && threadIdx.x == 0) raise_error(t.err, kBitBadPage);
         if (t.split && tree_steps<BLK>(n) == 0) {
-            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const int units = t.d_head / 8;
+#pragma unroll 1
             for (int64_t e = threadIdx.x;
                  e < static_cast<int64_t>(t.new_tokens) * t.heads * units; e += kTrThreads) {
                 const int64_t row = e / units;
                 const int i = static_cast<int>(row / t.heads);
                 const int h = static_cast<int>(row - static_cast<int64_t>(i) * t.heads);
                 const int d = 8 * static_cast<int>(e - row * units);
-                tree_store8<E>(tree_out(t, b, i, h), d, zero, 0.0f);
+                *reinterpret_cast<uint4*>(tree_out(t, b, i, h) + d) = make_uint4(0u, 0u, 0u, 0u);
                 if (d == 0) tree_lse(t, b, i, h, 0.0f, 0.0f);
             }
         }
@@ -810,7 +977,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
         bundle = blockIdx.y - b * t.bundles;
         int before = 0, total = 0;
         for (int i = threadIdx.x; i < t.batch; i += kTrJoinThreads) {
-            const int n = tree_steps<BLK>(tree_lens(t, i, bad)) * t.bundles;
+            const int n = tree_places(tree_steps<BLK>(tree_lens(t, i, bad))) * t.bundles;
             total += n;
             if (i < b) before += n;
         }
@@ -820,7 +987,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
         share = max(1, (all + t.groups - 1) / t.groups);
         tree_scan<kWarps>(before, scan, skip, all);
         steps = tree_steps<BLK>(tree_lens(t, b, bad));
-        begin = all + bundle * steps;
+        begin = all + bundle * tree_places(steps) + kTrPartCost;
     } else {
         TreeDeal d;
         const int later = blockIdx.y + 1;
@@ -829,8 +996,9 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
             b = d.b;
             share = d.share;
             steps = tree_steps<BLK>(tree_lens(t, b, bad));
-            bundle = steps > 0 ? min((d.g0 - d.base) / steps, t.bundles - 1) : 0;
-            begin = d.base + bundle * steps;
+            const int places = max(1, tree_places(steps));
+            bundle = min((d.g0 - d.base) / places, t.bundles - 1);
+            begin = d.base + bundle * places + kTrPartCost;
             cut = begin < d.g0 && begin / share == later - 1;
         }
     }
@@ -847,12 +1015,9 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
     const int col = 4 * (chunk / tiles) + warp;                // of 8 elements
     const int r_all = tile * t.unit_rows + r;
     if (8 * col >= t.d_head || r_all >= t.new_tokens * t.group || r >= t.unit_rows) return;
-    // Part i: group c0 + i's first, but group c0's last where it had others
-    // before.
-    const int late = begin > c0 * share ? 1 : 0;
+    // Part i: the first begins the unit (see TreePart).
     auto place = [&](int i) {
-        return static_cast<int64_t>(2 * ((c0 + i) * t.width + x) + (i == 0 ? late : 0)) *
-               t.part_rows;
+        return static_cast<int64_t>(2 * ((c0 + i) * t.width + x) + (i == 0)) * t.part_rows;
     };
     const int n = c1 - c0 + 1;
     float top = -INFINITY, sum = 0.0f;
@@ -867,10 +1032,10 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
             if (i0 + k < n) {
                 const int64_t at = place(i0 + k);
                 st[k] = t.part_stats[at + r];
-                const float4* w = reinterpret_cast<const float4*>(
-                    t.part_out + at * t.d_head + (static_cast<int64_t>(col) * t.part_rows + r) * 8);
+                const float4* w = reinterpret_cast<const float4*>(t.part_out + at * t.d_head) +
+                                  2 * col * t.part_rows + r;
                 v[k][0] = w[0];
-                v[k][1] = w[1];
+                v[k][1] = w[t.part_rows];
             }
         }
         float m = top;
@@ -900,14 +1065,23 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
 }
 
 template <int DP, int NQ, class E>
-cudaError_t launch(const TreeTask& t, int slot, cudaStream_t stream) {
+cudaError_t launch(TreeTask t, int slot, cudaStream_t stream) {
     using L = TreePlan<DP, NQ>;
     const auto kernel = tree_kernel<DP, NQ, E>;
     cudaError_t e = ensure_smem_attribute(reinterpret_cast<const void*>(kernel), slot, L::kBytes,
                                           false);
     if (e != cudaSuccess) return e;
+    // Tensor copies take boxes of one page: the rows of the largest power of two
+    // that divides the page and the block, 8 (a swizzled atom) at least.
+    CUtensorMap map_k{}, map_v{};
+    t.box_rows = t.page_size & -t.page_size;
+    if (t.box_rows > L::kBlk) t.box_rows = L::kBlk;
+    if (t.box_rows < 8 || t.num_pages == 0 ||
+        !encode_pages_map(&map_k, t.k_pages, t, t.k_stride, t.box_rows) ||
+        !encode_pages_map(&map_v, t.v_pages, t, t.v_stride, t.box_rows))
+        t.box_rows = 0;
     const int grid = (t.split ? t.groups : t.batch * t.bundles) * t.width;
-    kernel<<<grid, kTrThreads, L::kBytes, stream>>>(t);
+    kernel<<<grid, kTrThreads, L::kBytes, stream>>>(t, map_k, map_v);
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.split || t.groups == 1) return e;
     const int64_t units = static_cast<int64_t>(t.batch) * t.bundles;
