@@ -814,9 +814,7 @@ cs_status check_write_shape(const cs_write_shape* s) {
     if (s->d_head > cs::kPagedMaxDHead) return CS_ERR_OOM;
     if (s->d_head % 8 != 0) return CS_ERR_INVALID_ARG;
     const int64_t tokens = static_cast<int64_t>(s->batch) * s->new_tokens;
-    if (s->kv_heads > cs::kFattnMaxHeads || tokens > (1 << 30) ||
-        tokens * s->kv_heads * (s->d_head / 8) > (int64_t(1) << 40))
-        return CS_ERR_DIM_MISMATCH;
+    if (s->kv_heads > cs::kFattnMaxHeads || tokens > (1 << 30)) return CS_ERR_DIM_MISMATCH;
     return CS_OK;
 }
 
@@ -1702,7 +1700,7 @@ cs_status cs_paged_write(const uint16_t* keys, const uint16_t* values, const int
     t.page_size = s.page_size;
     t.head_units = s.d_head / 8;
     t.units = s.kv_heads * t.head_units;
-    t.total = static_cast<int64_t>(s.batch) * s.new_tokens * t.units;
+    t.tokens = s.batch * s.new_tokens;
     if (cs::launch_write(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return CS_ERR_CUDA;

@@ -430,12 +430,12 @@ struct WriteTask {
     int64_t key_stride[3], value_stride[3], k_stride[3], v_stride[3];
     int64_t slot_stride;
     int64_t num_slots;         // num_pages * page_size
-    int64_t total;             // 16-byte units of all keys
-    int32_t new_tokens, page_size;
-    int32_t units, head_units; // of a token's keys, of a head
+    int32_t tokens, new_tokens, page_size;
+    int32_t units, head_units; // of 16 bytes: a token's keys', a head's
+    int32_t cta_tokens, cta_units;
 };
 
-cudaError_t launch_write(const WriteTask& task, cudaStream_t stream);
+cudaError_t launch_write(WriteTask task, cudaStream_t stream);
 
 // One paged_tree_attention launch: new_tokens tokens for each of `batch`
 // sequences over the cache of PagedTask.

@@ -145,48 +145,77 @@ __global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) 
 
 // -------------------------------------------------------------------- write
 // cache[slots[b][i]] = keys[b][i], values[b][i].  Bound by the bytes of both,
-// read and written once: a thread copies units of 16 bytes, of the key and of
-// the value at the same place, several at a time.
+// read and written once.  A CTA takes some tokens, whose rows it looks up first,
+// a thread each, and then copies units of 16 bytes, of the key and the value at
+// the same place, several at a time.
 constexpr int kWrThreads = 256;
 constexpr int kWrUnroll = 4;
+constexpr int kWrUnits = kWrThreads * kWrUnroll;   // of a CTA, about
 
 __global__ void __launch_bounds__(kWrThreads) write_kernel(const WriteTask t) {
-    const int64_t e0 = static_cast<int64_t>(blockIdx.x) * (kWrThreads * kWrUnroll) + threadIdx.x;
-    uint4 k[kWrUnroll], v[kWrUnroll];
-    int64_t dk[kWrUnroll], dv[kWrUnroll];
-    bool bad = false;
-#pragma unroll
-    for (int u = 0; u < kWrUnroll; ++u) {
-        const int64_t e = e0 + u * kWrThreads;
-        dk[u] = -1;
-        if (e >= t.total) continue;
-        const int64_t token = e / t.units;
-        const int unit = static_cast<int>(e - token * t.units);
-        const int b = static_cast<int>(token / t.new_tokens);
-        const int i = static_cast<int>(token - static_cast<int64_t>(b) * t.new_tokens);
+    // Where a token's rows begin, in elements; dst_k -1: passed over.
+    struct Rows {
+        int64_t src_k, src_v, dst_k, dst_v;
+    };
+    __shared__ Rows rows[kWrThreads];
+    const int token0 = blockIdx.x * t.cta_tokens;
+    const int n = min(t.cta_tokens, t.tokens - token0);
+    if (threadIdx.x < n) {
+        const int token = token0 + threadIdx.x;
+        const int b = token / t.new_tokens, i = token - b * t.new_tokens;
         const int64_t slot = t.slots[b * t.slot_stride + i];
-        if (slot < 0) continue;
-        if (slot >= t.num_slots) {
-            bad = true;
-            continue;
+        Rows r;
+        r.dst_k = -1;
+        if (slot >= 0 && slot < t.num_slots) {
+            int64_t page, at;
+            if (t.num_slots <= 0xffffffffll) {   // a division of 32 bits
+                const uint32_t x = static_cast<uint32_t>(slot) / static_cast<uint32_t>(t.page_size);
+                page = x;
+                at = static_cast<uint32_t>(slot) - x * static_cast<uint32_t>(t.page_size);
+            } else {
+                page = slot / t.page_size;
+                at = slot - page * t.page_size;
+            }
+            r.src_k = b * t.key_stride[0] + i * t.key_stride[1];
+            r.src_v = b * t.value_stride[0] + i * t.value_stride[1];
+            r.dst_k = page * t.k_stride[0] + at * t.k_stride[1];
+            r.dst_v = page * t.v_stride[0] + at * t.v_stride[1];
+        } else if (slot >= 0 && blockIdx.y == 0) {
+            raise_error(t.err, kBitBadPage);
         }
-        const int head = unit / t.head_units, d = 8 * (unit - head * t.head_units);
-        const int64_t page = slot / t.page_size, at = slot - page * t.page_size;
-        k[u] = *reinterpret_cast<const uint4*>(t.keys + b * t.key_stride[0] +
-                                               i * t.key_stride[1] + head * t.key_stride[2] + d);
-        v[u] = *reinterpret_cast<const uint4*>(t.values + b * t.value_stride[0] +
-                                               i * t.value_stride[1] +
-                                               head * t.value_stride[2] + d);
-        dk[u] = page * t.k_stride[0] + at * t.k_stride[1] + head * t.k_stride[2] + d;
-        dv[u] = page * t.v_stride[0] + at * t.v_stride[1] + head * t.v_stride[2] + d;
+        rows[threadIdx.x] = r;
     }
+    __syncthreads();
+    // A token's units, all or (long ones) a slice of them.
+    const int u0 = blockIdx.y * t.cta_units;
+    const int units = min(t.cta_units, t.units - u0);
+    const int total = n * units;
+    for (int e0 = threadIdx.x; e0 < total; e0 += kWrUnits) {
+        uint4 k[kWrUnroll], v[kWrUnroll];
+        int64_t dk[kWrUnroll], dv[kWrUnroll];
 #pragma unroll
-    for (int u = 0; u < kWrUnroll; ++u) {
-        if (dk[u] < 0) continue;
-        *reinterpret_cast<uint4*>(t.k_pages + dk[u]) = k[u];
-        *reinterpret_cast<uint4*>(t.v_pages + dv[u]) = v[u];
+        for (int x = 0; x < kWrUnroll; ++x) {
+            const int e = e0 + x * kWrThreads;
+            dk[x] = -1;
+            if (e >= total) continue;
+            const int y = e / units, unit = u0 + e - y * units;
+            const Rows r = rows[y];
+            if (r.dst_k < 0) continue;
+            const int head = unit / t.head_units, d = 8 * (unit - head * t.head_units);
+            k[x] = __ldcs(reinterpret_cast<const uint4*>(t.keys + r.src_k +
+                                                         head * t.key_stride[2] + d));
+            v[x] = __ldcs(reinterpret_cast<const uint4*>(t.values + r.src_v +
+                                                         head * t.value_stride[2] + d));
+            dk[x] = r.dst_k + head * t.k_stride[2] + d;
+            dv[x] = r.dst_v + head * t.v_stride[2] + d;
+        }
+#pragma unroll
+        for (int x = 0; x < kWrUnroll; ++x) {
+            if (dk[x] < 0) continue;
+            *reinterpret_cast<uint4*>(t.k_pages + dk[x]) = k[x];
+            *reinterpret_cast<uint4*>(t.v_pages + dv[x]) = v[x];
+        }
     }
-    if (bad) raise_error(t.err, kBitBadPage);
 }
 
 }  // namespace
@@ -203,9 +232,13 @@ cudaError_t launch_extend(ExtendTask t, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_write(const WriteTask& t, cudaStream_t stream) {
-    const int64_t ctas = (t.total + kWrThreads * kWrUnroll - 1) / (kWrThreads * kWrUnroll);
-    write_kernel<<<static_cast<unsigned>(ctas), kWrThreads, 0, stream>>>(t);
+cudaError_t launch_write(WriteTask t, cudaStream_t stream) {
+    t.cta_units = t.units < kWrUnits ? t.units : kWrUnits;
+    t.cta_tokens = kWrUnits / t.cta_units;
+    if (t.cta_tokens > kWrThreads) t.cta_tokens = kWrThreads;
+    const dim3 grid((t.tokens + t.cta_tokens - 1) / t.cta_tokens,
+                    (t.units + t.cta_units - 1) / t.cta_units);
+    write_kernel<<<grid, kWrThreads, 0, stream>>>(t);
     return cudaGetLastError();
 }
 

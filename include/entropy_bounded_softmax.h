@@ -748,9 +748,8 @@ cs_status cs_check_paged_extend_args(
 
 typedef struct cs_write_shape {
     int32_t batch;       /* sequences, >= 0                                 */
-    int32_t new_tokens;  /* tokens of a sequence, >= 0; at most 2^30 in all,
-                            and 2^43 elements                               */
-    int32_t kv_heads;    /* >= 1                                            */
+    int32_t new_tokens;  /* tokens of a sequence, >= 0; at most 2^30 in all */
+    int32_t kv_heads;    /* 1..2^20                                         */
     int32_t d_head;      /* 8..256, a multiple of 8                         */
     int32_t page_size;   /* tokens of a page, >= 1                          */
     int32_t num_pages;   /* pages of the cache, >= 0                        */
