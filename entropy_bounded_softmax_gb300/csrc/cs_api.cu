@@ -1583,7 +1583,7 @@ cs_status cs_check_paged_extend_args(
     if (!shape) return CS_ERR_INVALID_ARG;
     const cs_extend_shape& s = *shape;
     if (s.batch < 0 || s.max_new < 0 || s.max_pages < 0 || s.page_size < 1 || s.num_free < 0 ||
-        s.batch > cs::kFattnMaxBatch ||
+        s.batch > cs::kFattnMaxBatch || s.max_new > kPagedMaxTokens ||
         static_cast<int64_t>(s.max_pages) * s.page_size > kPagedMaxTokens ||
         static_cast<int64_t>(s.batch) * s.max_new > (int64_t(1) << 40))
         return CS_ERR_DIM_MISMATCH;
@@ -1625,7 +1625,8 @@ cs_status cs_paged_extend(int32_t* page_table, const int32_t* lengths,
     t.held = held;
     t.free_pages = free_pages;
     t.cursor = cursor;
-    t.slots = slots;
+    t.slots = reinterpret_cast<long long*>(slots);
+    t.sm_count = d->sm_count;
     t.totals = totals;
     t.held_out = held_out;
     t.cursor_out = cursor_out;
@@ -1701,6 +1702,7 @@ cs_status cs_paged_write(const uint16_t* keys, const uint16_t* values, const int
     t.head_units = s.d_head / 8;
     t.units = s.kv_heads * t.head_units;
     t.tokens = s.batch * s.new_tokens;
+    t.sm_count = d->sm_count;
     if (cs::launch_write(t, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return CS_ERR_CUDA;

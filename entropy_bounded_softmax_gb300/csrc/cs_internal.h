@@ -407,7 +407,7 @@ struct ExtendTask {
     const int32_t* held;       // [batch] or null: the pages of lengths tokens
     const int32_t* free_pages; // [num_free]
     const int32_t* cursor;     // [1] or null: 0
-    int64_t* slots;            // [batch, max_new]
+    long long* slots;          // [batch, max_new]
     int32_t* totals;           // [batch]
     int32_t* held_out;         // [batch]
     int32_t* cursor_out;       // [1]
@@ -415,6 +415,8 @@ struct ExtendTask {
     int64_t table_stride;
     int32_t batch, max_new, max_pages, page_size, num_free;
     int32_t span, sequences;   // of a CTA: places of a sequence, sequences
+    int32_t lane_bits;         // log2 of the threads that share a sequence
+    int32_t sm_count;
 };
 
 cudaError_t launch_extend(ExtendTask task, cudaStream_t stream);
@@ -433,6 +435,7 @@ struct WriteTask {
     int32_t tokens, new_tokens, page_size;
     int32_t units, head_units; // of 16 bytes: a token's keys', a head's
     int32_t cta_tokens, cta_units;
+    int32_t sm_count;
 };
 
 cudaError_t launch_write(WriteTask task, cudaStream_t stream);

@@ -21,6 +21,8 @@ using namespace csd;
 // for another CTA, and one launch is enough), and takes the pages straight from
 // the free list where another CTA writes them into the table.
 constexpr int kExThreads = 256;
+constexpr int kExSlots = 2048;
+constexpr int kExCtasPerSm = 4;
 
 struct Claim {
     int len, fresh, held, need;   // as above; fresh and need 0 where `bad`
@@ -125,21 +127,43 @@ __global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) 
     }
     const int i0 = blockIdx.x * t.span;
     const int span = min(t.span, t.max_new - i0);
-    for (int e = threadIdx.x; e < nb * span; e += kExThreads) {
-        const int y = e / span, i = i0 + e - y * span;
+    // 2^bits threads to a sequence, which step through its places by additions;
+    // four places at a time: their pages are all under way before one is used.
+    const int step = 1 << t.lane_bits;
+    const int skip = step / t.page_size, rest = step - skip * t.page_size;
+    for (int y = threadIdx.x >> t.lane_bits; y < nb; y += kExThreads >> t.lane_bits) {
         const Row r = rows[y];
-        int64_t slot = -1;
-        if (i < r.total - r.len) {
-            const int at = r.len + i, entry = at / t.page_size;
-            const int page = entry < r.held
-                                 ? t.page_table[(b0 + y) * t.table_stride + entry]
-                                 : t.free_pages[r.taken + entry - r.held];
-            if (page >= 0)
-                slot = static_cast<int64_t>(page) * t.page_size + (at - entry * t.page_size);
-            else
-                raise_error(t.err, kBitBadPage);
+        const int32_t* table = t.page_table + (b0 + y) * t.table_stride;
+        const int32_t* fresh = t.free_pages + r.taken;
+        long long* out = t.slots + static_cast<int64_t>(b0 + y) * t.max_new + i0;
+        const int there = min(r.total - r.len - i0, span);   // places with a slot
+        int i = threadIdx.x & (step - 1);
+        int entry = (r.len + i0 + i) / t.page_size;
+        int at = r.len + i0 + i - entry * t.page_size;
+        while (i < span) {
+            int page[4], slot[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                page[x] = -1;
+                slot[x] = at;
+                if (i + x * step < there)
+                    page[x] = entry < r.held ? table[entry] : fresh[entry - r.held];
+                entry += skip;
+                at += rest;
+                if (at >= t.page_size) {
+                    at -= t.page_size;
+                    ++entry;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x, i += step) {
+                if (i >= span) break;
+                if (i < there && page[x] < 0) raise_error(t.err, kBitBadPage);
+                __stcs(out + i, page[x] < 0 ? -1ll
+                                            : static_cast<long long>(page[x]) * t.page_size +
+                                                  slot[x]);
+            }
         }
-        t.slots[static_cast<int64_t>(b0 + y) * t.max_new + i] = slot;
     }
 }
 
@@ -147,10 +171,16 @@ __global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) 
 // cache[slots[b][i]] = keys[b][i], values[b][i].  Bound by the bytes of both,
 // read and written once.  A CTA takes some tokens, whose rows it looks up first,
 // a thread each, and then copies units of 16 bytes, of the key and the value at
-// the same place, several at a time.
-constexpr int kWrThreads = 256;
-constexpr int kWrUnroll = 4;
-constexpr int kWrUnits = kWrThreads * kWrUnroll;   // of a CTA, about
+// the same place, two at a time, past the caches (nothing is read again here).
+// Small CTAs of several rounds: 32 prompts of up to 4096 tokens, 8 heads of 128,
+// 403 MB, take 64 us (6.3 TB/s, 93% of a plain copy); one round of 1024 units 74,
+// through the caches 81.  A small call has no CTAs to spare for rounds (7 x 333
+// tokens of 12 heads of 80, 11 MB: 4.2 us, with four rounds 6.8).
+constexpr int kWrThreads = 128;
+constexpr int kWrUnroll = 2;
+constexpr int kWrUnits = kWrThreads * kWrUnroll;
+constexpr int kWrRounds = 4;
+constexpr int kWrCtasPerSm = 16;   // from which on rounds are taken
 
 __global__ void __launch_bounds__(kWrThreads) write_kernel(const WriteTask t) {
     // Where a token's rows begin, in elements; dst_k -1: passed over.
@@ -212,8 +242,8 @@ __global__ void __launch_bounds__(kWrThreads) write_kernel(const WriteTask t) {
 #pragma unroll
         for (int x = 0; x < kWrUnroll; ++x) {
             if (dk[x] < 0) continue;
-            *reinterpret_cast<uint4*>(t.k_pages + dk[x]) = k[x];
-            *reinterpret_cast<uint4*>(t.v_pages + dv[x]) = v[x];
+            __stcs(reinterpret_cast<uint4*>(t.k_pages + dk[x]), k[x]);
+            __stcs(reinterpret_cast<uint4*>(t.v_pages + dv[x]), v[x]);
         }
     }
 }
@@ -221,9 +251,15 @@ __global__ void __launch_bounds__(kWrThreads) write_kernel(const WriteTask t) {
 }  // namespace
 
 cudaError_t launch_extend(ExtendTask t, cudaStream_t stream) {
-    // About 2048 slots a CTA.
-    t.span = t.max_new < 2048 ? (t.max_new > 0 ? t.max_new : 1) : 2048;
-    const int per = 2048 / t.span;
+    // The slots of a CTA: one a thread, and more only where the device is full of
+    // CTAs (each adds up the needs before it).
+    int64_t slots = static_cast<int64_t>(t.batch) * t.max_new / (kExCtasPerSm * t.sm_count);
+    slots = slots < kExThreads ? kExThreads : slots > kExSlots ? kExSlots : slots;
+    const int most = static_cast<int>(slots);
+    t.span = t.max_new < most ? (t.max_new > 0 ? t.max_new : 1) : most;
+    t.lane_bits = 0;
+    while ((1 << t.lane_bits) < t.span && (1 << t.lane_bits) < kExThreads) ++t.lane_bits;
+    const int per = most / t.span;
     t.sequences = per < 1 ? 1 : per > kExThreads ? kExThreads : per;
     // (One CTA at least: it passes the cursor on.)
     const dim3 grid(t.max_new > 0 ? (t.max_new + t.span - 1) / t.span : 1,
@@ -233,9 +269,15 @@ cudaError_t launch_extend(ExtendTask t, cudaStream_t stream) {
 }
 
 cudaError_t launch_write(WriteTask t, cudaStream_t stream) {
-    t.cta_units = t.units < kWrUnits ? t.units : kWrUnits;
-    t.cta_tokens = kWrUnits / t.cta_units;
+    // (A launch has at most 65535 slices of a token.)
+    const int slice = (t.units + 65534) / 65535;
+    t.cta_units = slice > kWrUnits ? slice : t.units < kWrUnits ? t.units : kWrUnits;
+    const int64_t once = static_cast<int64_t>(t.tokens) * t.units / kWrUnits;
+    const int rounds = once >= static_cast<int64_t>(kWrRounds) * kWrCtasPerSm * t.sm_count
+                           ? kWrRounds : 1;
+    t.cta_tokens = rounds * kWrUnits / t.cta_units;
     if (t.cta_tokens > kWrThreads) t.cta_tokens = kWrThreads;
+    if (t.cta_tokens < 1) t.cta_tokens = 1;
     const dim3 grid((t.tokens + t.cta_tokens - 1) / t.cta_tokens,
                     (t.units + t.cta_units - 1) / t.cta_units);
     write_kernel<<<grid, kWrThreads, 0, stream>>>(t);

@@ -688,7 +688,7 @@ cs_status cs_check_paged_attention_args(
  */
 typedef struct cs_extend_shape {
     int32_t batch;      /* sequences, >= 0                                  */
-    int32_t max_new;    /* slots of a sequence, >= 0; at most 2^40 in all   */
+    int32_t max_new;    /* slots of a sequence, 0..2^30; at most 2^40 in all */
     int32_t max_pages;  /* entries of a page-table row, >= 0; at most 2^30
                            tokens a row                                     */
     int32_t page_size;  /* tokens of a page, >= 1                           */
