@@ -24,6 +24,7 @@
 //   warps 0-3, 4-7  softmax, one row a thread;
 //   warp 8          issues the products (tcgen05, operands in shared memory,
 //                   weights in tensor memory);
+//   warp 9          works out the CTA's parts, a few ahead;
 //   warps 12-15     look pages up and keep the rings of K and V full by
 //                   asynchronous copies of 16 bytes, whatever a page's size and
 //                   its strides are; queries too.
@@ -253,6 +254,32 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
                  :: "r"(smem_addr(bar)) : "memory");
 }
 
+// warp_wait for two barriers at once.  (Every lane polls both: lanes that poll
+// different ones leave the warp in two halves, each of which would run what
+// follows, and the products want a whole warp.)
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, int phase_a, uint64_t* b, int phase_b,
+                                           const WaitLimit& w) {
+    const uint32_t bar_a = smem_addr(a), bar_b = smem_addr(b);
+    const uint32_t parity_a = phase_a & 1, parity_b = phase_b & 1;
+    auto both = [&] {
+        const bool x = mbar_try_wait<false>(bar_a, parity_a);
+        const bool y = mbar_try_wait<false>(bar_b, parity_b);
+        return __all_sync(0xffffffffu, x && y);
+    };
+    bool ok = both();
+    if (!ok) {
+        const long long c0 = clock64();
+        for (uint32_t i = 0; i < (1u << 31); ++i) {
+            ok = both();
+            const bool over = *w.abort_flag || clock64() - c0 > static_cast<long long>(w.cycles);
+            if (ok || __any_sync(0xffffffffu, over)) break;
+        }
+        if (!ok) *w.abort_flag = 1u;
+    }
+    __syncwarp();
+    return ok;
+}
+
 // Elements d .. d + 7 of one row of the output, from unnormalised sums.
 template <class E>
 __device__ __forceinline__ void tree_store8(uint16_t* row, int d, const float (&acc)[8],
@@ -315,12 +342,12 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
     if (warp == kTrCopyWarp) {
         for (int i = lane; i < L::kNumBars; i += 32) {
             uint64_t* bar = bars + i;
-            mbar_init(bar, bar < k_empty ? (tensor_copies ? 1u : 128u + 4u)
-                           : bar >= v_full && bar < v_empty ? (tensor_copies ? 1u : 128u)
-                           : bar == q_full ? (tensor_copies ? 64u : 128u)
-                           : bar >= p_full && bar < q_full ? 4u
-                           : bar == joined ? 8u
-                           : bar >= part_empty ? static_cast<uint32_t>(kTrPartWarps) : 1u);
+            mbar_init(bar, bar < k_empty ? (tensor_copies ? 1 : 128 + 4)
+                           : bar >= v_full && bar < v_empty ? (tensor_copies ? 1 : 128)
+                           : bar == q_full ? (tensor_copies ? 64 : 128)
+                           : bar >= p_full && bar < q_full ? 4
+                           : bar == joined ? 8
+                           : bar >= part_empty ? kTrPartWarps : 1);
         }
         if (lane == 0) flags[0] = 0u;
         fence_mbar_init();
@@ -592,6 +619,12 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
         give_registers<L::kRegsOther>();
         if (warp == kTrMmaWarp) {
             // ------------------------------------------------- MMA issuer
+            // (One warp for both accumulators: with one for each, whose products
+            // mix in the tensor pipe, two prompts' chunks of 512 over 8192
+            // tokens took 132 us, and 121 so.  Nor could two warps take one
+            // tile's blocks in turn: a ring's barriers are told apart by the
+            // parity of their phase alone, so who waits for one has to wait for
+            // all.)
             const bool leader = elect_lane();
             const uint32_t q = tile_desc(smem_addr(smem + L::kQ));
             const uint32_t kd = tile_desc(smem_addr(smem + L::kK));
@@ -600,7 +633,6 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             constexpr uint32_t stage_step = L::kBlock / 16;
             const int steps = (t.d_head + 15) / 16;
             const uint32_t idesc = idesc_half(128, 16 * steps, true, E::kFp16);
-            constexpr int kPerBlock = NQ;      // visits of a block
             int block0 = 0, with_blocks = 0, visits[2] = {0, 0};
             for (int ip = 0;; ++ip) {
                 bool ok;
@@ -610,34 +642,38 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 done_with(ip);
                 if (n < 0) break;
                 if (n == 0) continue;
-                const int all = n * kPerBlock;
+                // Visits: block v with accumulator v mod 2, or of a pair block
+                // v / 2 with each tile.
+                const int all = n * NQ;
                 auto scores = [&](int v) {
                     const int i = NT == 2 ? v & 1 : 0;
-                    const int kb = block0 + v / kPerBlock, st = kb % NS;
-                    if (!warp_wait(&k_full[st], kb / NS, limit)) return false;
-                    if (v == 0 && !warp_wait(q_full, with_blocks, limit)) return false;
-                    if (!tensor_copies || v == 0) fence_proxy_async_smem();
-                    tc_fence_after_sync();
+                    const int kb = block0 + v / NQ, st = kb % NS;
+                    if (v % NQ == 0) {
+                        if (!warp_wait2(&k_full[st], kb / NS, q_full, with_blocks, limit))
+                            return false;
+                        if (!tensor_copies || v == 0) fence_proxy_async_smem();
+                        tc_fence_after_sync();
+                    }
                     mma_tiles<BLK, DP, E::kFp16>(tmem + BLK * i, q + i * tile_step,
                                                  kd + st * stage_step, steps, leader);
                     mma_commit(&s_full[i], leader);
-                    if ((v + 1) % kPerBlock == 0) mma_commit(&k_empty[st], leader);
+                    if ((v + 1) % NQ == 0) mma_commit(&k_empty[st], leader);
                     if (v + 1 == all) mma_commit(q_empty, leader);
                     return true;
                 };
                 for (int v = 0; v < NT && v < all && ok; ++v) ok = scores(v);
                 for (int v = 0; v < all && ok; ++v) {
                     const int i = NT == 2 ? v & 1 : 0;
-                    const int kb = block0 + v / kPerBlock, st = kb % NS;
-                    ok = warp_wait(&v_full[st], kb / NS, limit) &&
-                         warp_wait(&p_full[i], visits[i], limit);
+                    const int kb = block0 + v / NQ, st = kb % NS;
+                    ok = warp_wait2(&v_full[st], kb / NS, &p_full[i], visits[i], limit);
                     if (!ok) break;
+                    ++visits[i];
                     if (!tensor_copies) {
                         fence_proxy_async_smem();
-                    } else if (v % kPerBlock == 0) {
+                    } else if (v % NQ == 0) {
                         // Values past the length, which a tensor copy brings in
                         // with the last ones before: 0 times them has to be 0.
-                        const int there = past - (v / kPerBlock) * BLK;
+                        const int there = past - v / NQ * BLK;
                         if (there < BLK && there % t.box_rows != 0) {
                             const int rows = t.box_rows - there % t.box_rows;
                             unsigned char* tile = smem + L::kV + st * L::kBlock + there * 128;
@@ -656,8 +692,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                     mma_weights<BLK>(tmem + L::kOut + DP * i, tmem + BLK * i, vd + st * stage_step,
                                      idesc, v >= NT, leader);
                     mma_commit(&o_full[i], leader);
-                    ++visits[i];
-                    if ((v + 1) % kPerBlock == 0) mma_commit(&v_empty[st], leader);
+                    if ((v + 1) % NQ == 0) mma_commit(&v_empty[st], leader);
                     if (v + 1 == all) mma_commit(o_done, leader);
                     if (v + NT < all) ok = scores(v + NT);
                 }
@@ -796,8 +831,10 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 return at;
             };
             // A part's queries, by `warps` warps of which this is number w.
-            auto load_q = [&](const TreePart* p, int w, int warps, int with_blocks) {
+            int with_blocks = 0;
+            auto load_q = [&](const TreePart* p, int w, int warps) {
                 if (with_blocks > 0 && !warp_wait(q_empty, with_blocks - 1, limit)) return false;
+                ++with_blocks;
 #pragma unroll 1
                 for (int r0 = 32 * w; r0 < 128 * NQ; r0 += 32 * warps) {
                     const int r = r0 + lane;
@@ -813,14 +850,14 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 cp_async_arrive(q_full);
                 return true;
             };
-            int block0 = 0, with_blocks = 0;
+            int block0 = 0;
             if (tensor_copies && cw >= 2) {
                 // Two warps for the queries,
                 for (int ip = 0;; ++ip) {
                     bool ok;
                     const TreePart* p = part(ip, ok);
                     if (!ok || p->n < 0) break;
-                    if (p->n > 0) ok = load_q(p, cw - 2, 2, with_blocks++);
+                    if (p->n > 0) ok = load_q(p, cw - 2, 2);
                     if (!ok) break;
                     done_with(ip);
                 }
@@ -920,7 +957,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         if (!ok) break;
                         copy_rows(smem + L::kV + st * L::kBlock, BLK, kRows * cw, kRows, v, there);
                         cp_async_arrive(&v_full[st]);
-                        if (j == 0) ok = load_q(p, cw, 4, with_blocks++);
+                        if (j == 0) ok = load_q(p, cw, 4);
                     }
                     if (!ok) break;
                     done_with(ip);
