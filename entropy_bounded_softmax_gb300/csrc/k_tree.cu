@@ -91,7 +91,7 @@ struct TreePlan {
     static constexpr int kK = kQ + NQ * kTile;
     static constexpr int kV = kK + kStages * kBlock;
     static constexpr int kBars = kV + kStages * kBlock;
-    static constexpr int kNumBars = 4 * kStages + 11 + 2 * kTrParts;
+    static constexpr int kNumBars = 4 * kStages + 9 + 2 * kTrParts;
     static constexpr int kWords = kBars + (8 * kNumBars + 15) / 16 * 16;  // [kTrWords][4]
     static constexpr int kParts = kWords + kTrWords * 16;
     static constexpr int kScan = kParts + kTrParts * 48;   // [18] ints
@@ -319,9 +319,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
     uint64_t* k_empty = k_full + NS;          // [NS] products that read it completed
     uint64_t* v_full = k_empty + NS;
     uint64_t* v_empty = v_full + NS;
-    uint64_t* s_full = v_empty + NS;          // [2] scores of a block
-    uint64_t* o_full = s_full + 2;            // [2] its P V completed
-    uint64_t* p_full = o_full + 2;            // [2] its weights, from four warps
+    uint64_t* s_full = v_empty + NS;          // [2] scores of a block, and the P V before
+    uint64_t* p_full = s_full + 2;            // [2] its weights, from four warps
     uint64_t* q_full = p_full + 2;
     uint64_t* q_empty = q_full + 1;           // the part's last scores completed
     uint64_t* o_done = q_empty + 1;           // the part's last P V completed
@@ -484,9 +483,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                             const float f = m == -INFINITY ? 0.0f : ex2((m - top) * c);
                             m = top;
                             l *= f;
-                            ok = warp_wait(&o_full[tile], visit - 1, limit);
-                            if (!ok) break;
-                            tc_fence_after_sync();
+                            // (The P V before has completed: the scores came
+                            // after it from the same thread.)
 #pragma unroll 1
                             for (int x = 0; x < DP; x += 16) {
                                 float o[16];
@@ -691,7 +689,6 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                     tc_fence_after_sync();
                     mma_weights<BLK>(tmem + L::kOut + DP * i, tmem + BLK * i, vd + st * stage_step,
                                      idesc, v >= NT, leader);
-                    mma_commit(&o_full[i], leader);
                     if ((v + 1) % NQ == 0) mma_commit(&v_empty[st], leader);
                     if (v + 1 == all) mma_commit(o_done, leader);
                     if (v + NT < all) ok = scores(v + NT);
