@@ -362,6 +362,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
     // A large batch's lengths are added up by the whole CTA.
     const bool large = t.split && t.batch > kTrWarpBatch;
     if (large) any = tree_deal<kTrThreads / 32, BLK>(t, grp, scan, deal);
+    else if (t.split && warp == kTrPartWarp) any = tree_deal<1, BLK>(t, grp, scan, deal);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -539,70 +540,76 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 f1 = z.y == 0.0f ? 0.0f : ex2(z.x - top);
                 sum = fmaf(a.y, f0, z.y * f1);
             }
+            // Where the row goes, worked out while the last products run.
+            const int rows = p->rows, place = p->place;
+            const bool here = r < rows;
+            const int token = (p->r0 + r) / group;
+            const int h = p->hk * group + (p->r0 + r) - token * group;
+            // Whose columns: with one tile each warpgroup half of them.
+            const int d0 = NQ == 1 ? wg * (DP / 2) : 0;
+            const int d1 = min(t.d_head, NQ == 1 ? d0 + DP / 2 : DP);
+            const uint32_t from = NQ == 1 ? out0 : to;
+            uint16_t* row = nullptr;
+            float4* part_row = nullptr;
+            if (place < 0) {
+                if (here) row = tree_out(t, p->b, token, h);
+                if (here && (NQ == 2 || wg == 0)) tree_lse(t, p->b, token, h, top, sum);
+                const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+                f0 *= inv;
+                f1 *= inv;
+            } else {
+                const int64_t at = static_cast<int64_t>(place) * t.part_rows;
+                part_row = reinterpret_cast<float4*>(t.part_out + at * t.d_head) + r;
+                if (here && (NQ == 2 || wg == 0)) t.part_stats[at + r] = make_float2(top, sum);
+            }
+            done_with(ip);
             if (n > 0) {
                 ok = warp_wait(o_done, with_blocks++, limit);
                 if (!ok) break;
                 tc_fence_after_sync();
             }
-            const int rows = p->rows;
             if (warp_r < rows) {
-                const bool here = r < rows;
-                const int token = (p->r0 + r) / group;
-                const int h = p->hk * group + (p->r0 + r) - token * group;
-                const int place = p->place;
-                // Whose columns: with one tile each warpgroup half of them.
-                const int d0 = NQ == 1 ? wg * (DP / 2) : 0;
-                const int d1 = min(t.d_head, NQ == 1 ? d0 + DP / 2 : DP);
-                const uint32_t from = NQ == 1 ? out0 : to;
-                const bool mine_first = here && (NQ == 2 || wg == 0);
-                uint16_t* row = nullptr;
-                float4* part_row = nullptr;
-                if (place < 0) {
-                    if (here) row = tree_out(t, p->b, token, h);
-                    if (mine_first) tree_lse(t, p->b, token, h, top, sum);
-                    const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
-                    f0 *= inv;
-                    f1 *= inv;
-                } else {
-                    const int64_t at = static_cast<int64_t>(place) * t.part_rows;
-                    part_row = reinterpret_cast<float4*>(t.part_out + at * t.d_head) + r;
-                    if (mine_first) t.part_stats[at + r] = make_float2(top, sum);
-                }
+                const bool second = NQ == 1 && NT == 2 && n > 1;
 #pragma unroll 1
-                for (int d = d0; d < d1; d += 16) {
-                    float o[16];
+                for (int d = d0; d < d1; d += 32) {
+                    uint32_t o[32], z[32];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) o[x] = 0.0f;
-                    // (Exactly 0 of what has no kept token: 0 times a NaN is not.)
+                    for (int x = 0; x < 32; ++x) o[x] = z[x] = 0u;
                     if (n > 0) {
-                        float v[16];
-                        tmem_ld16(from + d, v);
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) o[x] = f0 == 0.0f ? 0.0f : v[x] * f0;
+                        tmem_ld16_async(from + d, o);
+                        tmem_ld16_async(from + d + 16, o + 16);
                     }
-                    if (NQ == 1 && NT == 2 && n > 1) {
-                        float v[16];
-                        tmem_ld16(out0 + DP + d, v);
+                    if (second) {
+                        tmem_ld16_async(out0 + DP + d, z);
+                        tmem_ld16_async(out0 + DP + d + 16, z + 16);
+                    }
+                    tmem_wait_ld<32>(o);
+                    tmem_wait_ld<32>(z);
+                    float v[32];
+                    // (Exactly 0 of what has no kept token: 0 times a NaN is not.)
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) o[x] = f1 == 0.0f ? o[x] : fmaf(v[x], f1, o[x]);
+                    for (int x = 0; x < 32; ++x) {
+                        v[x] = f0 == 0.0f ? 0.0f : __uint_as_float(o[x]) * f0;
+                        if (NQ == 1 && NT == 2)
+                            v[x] = f1 == 0.0f ? v[x] : fmaf(__uint_as_float(z[x]), f1, v[x]);
                     }
                     if (!here) continue;
                     if (place < 0) {
 #pragma unroll
-                        for (int y = 0; y < 16; y += 8)
+                        for (int y = 0; y < 32; y += 8)
                             if (d + y < t.d_head)
                                 *reinterpret_cast<uint4*>(row + d + y) = make_uint4(
-                                    E::pack(o[y], o[y + 1]), E::pack(o[y + 2], o[y + 3]),
-                                    E::pack(o[y + 4], o[y + 5]), E::pack(o[y + 6], o[y + 7]));
+                                    E::pack(v[y], v[y + 1]), E::pack(v[y + 2], v[y + 3]),
+                                    E::pack(v[y + 4], v[y + 5]), E::pack(v[y + 6], v[y + 7]));
                     } else {
                         float4* w = part_row + (d / 4) * t.part_rows;
 #pragma unroll
-                        for (int y = 0; y < 16; y += 4, w += t.part_rows)
-                            if (d + y < t.d_head) *w = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                        for (int y = 0; y < 32; y += 4, w += t.part_rows)
+                            if (d + y < t.d_head)
+                                *w = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
                     }
                 }
             }
-            done_with(ip);
             // The next part's products write over what was read here.
             if (NQ == 1) {
                 tc_fence_before_sync();
@@ -717,7 +724,6 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 __syncwarp();
             };
             if (t.split) {
-                if (!large) any = tree_deal<1, BLK>(t, grp, scan, deal);
                 int g = deal.g0, b = deal.b - 1, bundle = t.bundles, at = 0, steps = 0;
                 TreeLens n{};
                 if (any) {
