@@ -638,7 +638,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             constexpr uint32_t stage_step = L::kBlock / 16;
             const int steps = (t.d_head + 15) / 16;
             const uint32_t idesc = idesc_half(128, 16 * steps, true, E::kFp16);
-            int block0 = 0, with_blocks = 0, visits[2] = {0, 0};
+            int block0 = 0, with_blocks = 0;
+            int before[2] = {0, 0};   // visits of the parts before
             for (int ip = 0;; ++ip) {
                 bool ok;
                 const TreePart* p = part(ip, ok);
@@ -648,12 +649,11 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 if (n < 0) break;
                 if (n == 0) continue;
                 // Visits: block v with accumulator v mod 2, or of a pair block
-                // v / 2 with each tile.
+                // v / 2 with each tile.  i: the accumulator of v.
                 const int all = n * NQ;
-                auto scores = [&](int v) {
-                    const int i = NT == 2 ? v & 1 : 0;
+                auto scores = [&](int v, int i) {
                     const int kb = block0 + v / NQ, st = kb % NS;
-                    if (v % NQ == 0) {
+                    if (NQ == 1 || i == 0) {
                         if (!warp_wait2(&k_full[st], kb / NS, q_full, with_blocks, limit))
                             return false;
                         if (!tensor_copies || v == 0) fence_proxy_async_smem();
@@ -662,20 +662,17 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                     mma_tiles<BLK, DP, E::kFp16>(tmem + BLK * i, q + i * tile_step,
                                                  kd + st * stage_step, steps, leader);
                     mma_commit(&s_full[i], leader);
-                    if ((v + 1) % NQ == 0) mma_commit(&k_empty[st], leader);
+                    if (NQ == 1 || i == 1) mma_commit(&k_empty[st], leader);
                     if (v + 1 == all) mma_commit(q_empty, leader);
                     return true;
                 };
-                for (int v = 0; v < NT && v < all && ok; ++v) ok = scores(v);
-                for (int v = 0; v < all && ok; ++v) {
-                    const int i = NT == 2 ? v & 1 : 0;
+                auto weights = [&](int v, int i) {
                     const int kb = block0 + v / NQ, st = kb % NS;
-                    ok = warp_wait2(&v_full[st], kb / NS, &p_full[i], visits[i], limit);
-                    if (!ok) break;
-                    ++visits[i];
+                    if (!warp_wait2(&v_full[st], kb / NS, &p_full[i], before[i] + v / NT, limit))
+                        return false;
                     if (!tensor_copies) {
                         fence_proxy_async_smem();
-                    } else if (v % NQ == 0) {
+                    } else if (NQ == 1 || i == 0) {
                         // Values past the length, which a tensor copy brings in
                         // with the last ones before: 0 times them has to be 0.
                         const int there = past - v / NQ * BLK;
@@ -696,12 +693,24 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                     tc_fence_after_sync();
                     mma_weights<BLK>(tmem + L::kOut + DP * i, tmem + BLK * i, vd + st * stage_step,
                                      idesc, v >= NT, leader);
-                    if ((v + 1) % NQ == 0) mma_commit(&v_empty[st], leader);
+                    if (NQ == 1 || i == 1) mma_commit(&v_empty[st], leader);
                     if (v + 1 == all) mma_commit(o_done, leader);
-                    if (v + NT < all) ok = scores(v + NT);
+                    return true;
+                };
+                ok = scores(0, 0);
+                if (NT == 2 && all > 1 && ok) ok = scores(1, 1);
+                for (int v = 0; v < all && ok; v += NT) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        if (!ok || v + i >= all) break;
+                        ok = weights(v + i, i);
+                        if (ok && v + i + NT < all) ok = scores(v + i + NT, i);
+                    }
                 }
                 if (!ok) break;
                 block0 += n;
+                before[0] += (all + NT - 1) / NT;
+                before[1] += all / 2;
                 ++with_blocks;
             }
             // No product may be in flight when the tensor memory is freed.
