@@ -857,7 +857,8 @@ cs_status cs_paged_tree_attention(
     int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace the call needs (0 where no row of the table holds more
- * than two blocks); negative for a malformed shape.  Host-only. */
+ * than 512 tokens, 1024 in some batches; half of that for d_head above 128);
+ * negative for a malformed shape.  Host-only. */
 int64_t cs_paged_tree_attention_workspace(const cs_tree_shape* shape);
 
 /* Host-only argument check (no CUDA call). */

@@ -6,7 +6,9 @@ Allowances of the attention, per element: half a step of the result's type;
 half a step of the cache's for each weight; a score's dot product errs by
 (D + 8) 2^-23 of the sum of its terms' magnitudes, 2^x by 2^-21; the sums of
 n <= 6000 terms by 2^-17 of the sum of magnitudes (each step rounds by 2^-23,
-mostly cancelling)."""
+mostly cancelling).  In fp16, whose steps are never below 2^-24: results err by
+up to 2^-25, and weights, which carry a factor 2^8 or more and have a sum of at
+least as much, by up to 2^-33 of that sum each."""
 import math
 
 import torch
@@ -102,6 +104,9 @@ def definition(q, k, v, table, lengths, mask=None, new_lengths=None,
                   + 2.0 ** -21 + 2.0 ** -17)[:, None]
             tol[b, some, h] += (half * out[b, some, h].abs()
                                 + (2 * es + half) * (p @ vv.abs()))
+            if q.dtype == torch.float16:
+                tol[b, some, h] += (2.0 ** -25 + 2.0 ** -33 *
+                                    (sees[some].double() @ vv.abs()))
             tol_lse[b, some, h] = es[:, 0] + 4 * F32 * lse[b, some, h].abs()
     return out, tol, lse, tol_lse
 
