@@ -115,22 +115,38 @@ class CsError(RuntimeError):
                          f"({_lib.cs_status_string(status)})")
 
 
+# torch's functions for the current stream and device of the calling thread,
+# looked up once: every call asks for both.
+_raw_stream = _current_device = None
+
+
+def _look_up() -> None:
+    global _raw_stream, _current_device
+    import torch
+    _raw_stream = getattr(
+        torch._C, "_cuda_getCurrentRawStream",
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice",
+                              torch.cuda.current_device)
+
+
 def _stream_handle(device) -> int:
     """The raw cudaStream_t of the current stream of a CUDA device."""
-    import torch
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(idx)
-    return torch.cuda.current_stream(device).cuda_stream
+    if _raw_stream is None:
+        _look_up()
+    index = device.index
+    return _raw_stream(_current_device() if index is None else index)
 
 
 def _on_device(device):
     """A context that makes `device` current: none when it already is (the
     common case, and the cheapest: the call is on every step's path)."""
-    import torch
-    if device.index is None or device.index == torch.cuda.current_device():
+    if _raw_stream is None:
+        _look_up()
+    index = device.index
+    if index is None or index == _current_device():
         return _STAY
+    import torch
     return torch.cuda.device(device)
 
 

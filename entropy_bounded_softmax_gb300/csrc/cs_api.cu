@@ -816,6 +816,67 @@ TreePlan tree_plan(const cs_tree_shape& s, int sms) {
     return p;
 }
 
+int64_t tree_workspace(const cs_tree_shape& s, const TreePlan& p) {
+    if (p.groups == 0) return 0;
+    // Two parts a CTA: the (maximum, sum) pairs, the outputs.  (However the
+    // device's SMs are grouped: at most one CTA an SM, and one a block.)
+    const int64_t blocks = tree_steps(s) * s.batch;
+    const int64_t ctas =
+        blocks >= kPagedMaxSms || blocks * p.units >= kPagedMaxSms ? kPagedMaxSms : blocks * p.units;
+    const int64_t rows = ctas * 2 * p.part_rows;
+    return rows * 8 + rows * s.d_head * 4;
+}
+
+// cs_check_paged_tree_attention_args, which leaves the plan for a GB300's SMs.
+cs_status check_tree(const uint16_t* query, const uint16_t* key_pages,
+                     const uint16_t* value_pages, const int32_t* page_table,
+                     const int32_t* lengths, const int32_t* new_lengths, const uint8_t* mask,
+                     const uint16_t* out, const float* lse, const cs_tree_shape* shape,
+                     const void* workspace, int64_t workspace_bytes, TreePlan& p) {
+    const cs_status st = check_tree_shape(shape);
+    if (st != CS_OK) return st;
+    const cs_tree_shape& s = *shape;
+    if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
+    // Blocks and CTAs are counted in 32 bits.
+    p = tree_plan(s, kPagedMaxSms);
+    if (p.units * s.batch > (1 << 30) ||
+        tree_steps(s) > (1 << 30) / (s.batch * (p.units / p.width)))
+        return CS_ERR_DIM_MISMATCH;
+    const int64_t need = tree_workspace(s, p);
+    if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
+    if (s.batch > 1 && (s.table_stride < s.max_pages || s.table_stride > kMaxRowStride))
+        return CS_ERR_INVALID_ARG;
+    int64_t mask_bytes = 0;
+    if (mask) {
+        if ((s.new_tokens > 1 &&
+             (s.mask_stride[1] < s.new_tokens || s.mask_stride[1] > kMaxRowStride >> 10)) ||
+            (s.batch > 1 && (s.mask_stride[0] < 0 || s.mask_stride[0] > kMaxRowStride)))
+            return CS_ERR_INVALID_ARG;
+        mask_bytes = s.new_tokens +
+                     (s.new_tokens > 1 ? (s.new_tokens - 1) * s.mask_stride[1] : 0) +
+                     (s.batch > 1 ? (s.batch - 1) * s.mask_stride[0] : 0);
+    }
+    const int64_t rows[3] = {s.batch, s.new_tokens, s.heads};
+    const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
+    const int64_t table = s.max_pages == 0 ? 0
+        : 4 * ((s.batch > 1 ? (s.batch - 1) * s.table_stride : 0) + s.max_pages);
+    const int64_t b = s.batch;
+    const Span spans[10] = {
+        {query, strided_extent(rows, s.q_stride, 3, s.d_head), 16, false},
+        {key_pages, strided_extent(pages, s.k_stride, 3, s.d_head), 16, false},
+        {value_pages, strided_extent(pages, s.v_stride, 3, s.d_head), 16, false},
+        {page_table, table, 4, false},
+        {lengths, 4 * b, 4, false},
+        {new_lengths, new_lengths ? 4 * b : 0, 4, false},
+        {mask, mask_bytes, 1, false},
+        {out, strided_extent(rows, s.o_stride, 3, s.d_head), 16, true},
+        {lse, lse ? 4 * b * s.new_tokens * s.heads : 0, 4, true},
+        {workspace, need, 16, true}};
+    if (spans[7].bytes > 0 && overlaps_itself(rows, s.o_stride, 3, s.d_head))
+        return CS_ERR_INVALID_ARG;
+    return check_spans(spans, 10);
+}
+
 cs_status check_write_shape(const cs_write_shape* s) {
     if (!s) return CS_ERR_INVALID_ARG;
     if (s->batch < 0 || s->new_tokens < 0 || s->kv_heads < 1 || s->d_head < 1 ||
@@ -1722,15 +1783,7 @@ cs_status cs_paged_write(const uint16_t* keys, const uint16_t* values, const int
 
 int64_t cs_paged_tree_attention_workspace(const cs_tree_shape* shape) {
     if (check_tree_shape(shape) != CS_OK) return -1;
-    const TreePlan p = tree_plan(*shape, kPagedMaxSms);
-    if (p.groups == 0) return 0;
-    // Two parts a CTA: the (maximum, sum) pairs, the outputs.  (However the
-    // device's SMs are grouped: at most one CTA an SM, and one a block.)
-    const int64_t blocks = tree_steps(*shape) * shape->batch;
-    const int64_t ctas =
-        blocks >= kPagedMaxSms || blocks * p.units >= kPagedMaxSms ? kPagedMaxSms : blocks * p.units;
-    const int64_t rows = ctas * 2 * p.part_rows;
-    return rows * 8 + rows * shape->d_head * 4;
+    return tree_workspace(*shape, tree_plan(*shape, kPagedMaxSms));
 }
 
 cs_status cs_check_paged_tree_attention_args(
@@ -1738,48 +1791,9 @@ cs_status cs_check_paged_tree_attention_args(
     const int32_t* page_table, const int32_t* lengths, const int32_t* new_lengths,
     const uint8_t* mask, const uint16_t* out, const float* lse, const cs_tree_shape* shape,
     const void* workspace, int64_t workspace_bytes) {
-    const cs_status st = check_tree_shape(shape);
-    if (st != CS_OK) return st;
-    const cs_tree_shape& s = *shape;
-    if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
-    // Blocks and CTAs are counted in 32 bits.
-    const TreePlan p = tree_plan(s, kPagedMaxSms);
-    if (p.units * s.batch > (1 << 30) ||
-        tree_steps(s) > (1 << 30) / (s.batch * (p.units / p.width)))
-        return CS_ERR_DIM_MISMATCH;
-    const int64_t need = cs_paged_tree_attention_workspace(shape);
-    if (workspace_bytes < need) return CS_ERR_INVALID_ARG;
-    if (s.batch > 1 && (s.table_stride < s.max_pages || s.table_stride > kMaxRowStride))
-        return CS_ERR_INVALID_ARG;
-    int64_t mask_bytes = 0;
-    if (mask) {
-        if ((s.new_tokens > 1 &&
-             (s.mask_stride[1] < s.new_tokens || s.mask_stride[1] > kMaxRowStride >> 10)) ||
-            (s.batch > 1 && (s.mask_stride[0] < 0 || s.mask_stride[0] > kMaxRowStride)))
-            return CS_ERR_INVALID_ARG;
-        mask_bytes = s.new_tokens +
-                     (s.new_tokens > 1 ? (s.new_tokens - 1) * s.mask_stride[1] : 0) +
-                     (s.batch > 1 ? (s.batch - 1) * s.mask_stride[0] : 0);
-    }
-    const int64_t rows[3] = {s.batch, s.new_tokens, s.heads};
-    const int64_t pages[3] = {s.num_pages, s.page_size, s.kv_heads};
-    const int64_t table = s.max_pages == 0 ? 0
-        : 4 * ((s.batch > 1 ? (s.batch - 1) * s.table_stride : 0) + s.max_pages);
-    const int64_t b = s.batch;
-    const Span spans[10] = {
-        {query, strided_extent(rows, s.q_stride, 3, s.d_head), 16, false},
-        {key_pages, strided_extent(pages, s.k_stride, 3, s.d_head), 16, false},
-        {value_pages, strided_extent(pages, s.v_stride, 3, s.d_head), 16, false},
-        {page_table, table, 4, false},
-        {lengths, 4 * b, 4, false},
-        {new_lengths, new_lengths ? 4 * b : 0, 4, false},
-        {mask, mask_bytes, 1, false},
-        {out, strided_extent(rows, s.o_stride, 3, s.d_head), 16, true},
-        {lse, lse ? 4 * b * s.new_tokens * s.heads : 0, 4, true},
-        {workspace, need, 16, true}};
-    if (spans[7].bytes > 0 && overlaps_itself(rows, s.o_stride, 3, s.d_head))
-        return CS_ERR_INVALID_ARG;
-    return check_spans(spans, 10);
+    TreePlan p;
+    return check_tree(query, key_pages, value_pages, page_table, lengths, new_lengths, mask, out,
+                      lse, shape, workspace, workspace_bytes, p);
 }
 
 cs_status cs_paged_tree_attention(const uint16_t* query, const uint16_t* key_pages,
@@ -1788,9 +1802,9 @@ cs_status cs_paged_tree_attention(const uint16_t* query, const uint16_t* key_pag
                                   const uint8_t* mask, uint16_t* out, float* lse,
                                   const cs_tree_shape* shape, void* workspace,
                                   int64_t workspace_bytes, void* stream) {
-    cs_status st = cs_check_paged_tree_attention_args(
-        query, key_pages, value_pages, page_table, lengths, new_lengths, mask, out, lse, shape,
-        workspace, workspace_bytes);
+    TreePlan p;
+    cs_status st = check_tree(query, key_pages, value_pages, page_table, lengths, new_lengths, mask,
+                              out, lse, shape, workspace, workspace_bytes, p);
     if (st != CS_OK) return st;
     const cs_tree_shape& s = *shape;
     if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
@@ -1826,7 +1840,7 @@ cs_status cs_paged_tree_attention(const uint16_t* query, const uint16_t* key_pag
     t.page_size = s.page_size;
     t.num_pages = s.num_pages;
     t.max_pages = s.max_pages;
-    const TreePlan p = tree_plan(s, d->sm_count < kPagedMaxSms ? d->sm_count : kPagedMaxSms);
+    if (d->sm_count < kPagedMaxSms) p = tree_plan(s, d->sm_count);
     t.unit_rows = p.unit_rows;
     t.part_rows = p.part_rows;
     t.width = p.width;
