@@ -61,6 +61,9 @@ __global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) 
         int taken, got;         // of the free list: the entry of page `held`
     };
     __shared__ Row rows[kExThreads];
+    // Launched while the kernel before ends, as the next one may be.
+    allow_next_kernel();
+    wait_for_previous_kernel();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b0 = blockIdx.y * t.sequences;
     const int nb = min(t.sequences, t.batch - b0);
@@ -188,6 +191,8 @@ __global__ void __launch_bounds__(kWrThreads) write_kernel(const WriteTask t) {
         int64_t src_k, src_v, dst_k, dst_v;
     };
     __shared__ Rows rows[kWrThreads];
+    allow_next_kernel();
+    wait_for_previous_kernel();
     const int token0 = blockIdx.x * t.cta_tokens;
     const int n = min(t.cta_tokens, t.tokens - token0);
     if (threadIdx.x < n) {
@@ -264,8 +269,7 @@ cudaError_t launch_extend(ExtendTask t, cudaStream_t stream) {
     // (One CTA at least: it passes the cursor on.)
     const dim3 grid(t.max_new > 0 ? (t.max_new + t.span - 1) / t.span : 1,
                     t.batch > 0 ? (t.batch + t.sequences - 1) / t.sequences : 1);
-    extend_kernel<<<grid, kExThreads, 0, stream>>>(t);
-    return cudaGetLastError();
+    return launch_shaped(extend_kernel, {grid, kExThreads, 0, stream, true, 1}, t);
 }
 
 cudaError_t launch_write(WriteTask t, cudaStream_t stream) {
@@ -280,8 +284,7 @@ cudaError_t launch_write(WriteTask t, cudaStream_t stream) {
     if (t.cta_tokens < 1) t.cta_tokens = 1;
     const dim3 grid((t.tokens + t.cta_tokens - 1) / t.cta_tokens,
                     (t.units + t.cta_units - 1) / t.cta_units);
-    write_kernel<<<grid, kWrThreads, 0, stream>>>(t);
-    return cudaGetLastError();
+    return launch_shaped(write_kernel, {grid, kWrThreads, 0, stream, true, 1}, t);
 }
 
 }  // namespace cs

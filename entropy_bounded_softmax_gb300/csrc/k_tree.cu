@@ -356,6 +356,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
         prefetch_tmap(&map_k);
         prefetch_tmap(&map_v);
     }
+    // Launched while the kernel before ends; nothing of memory is touched above.
+    wait_for_previous_kernel();
     const int grp = static_cast<int>(blockIdx.x) / t.width;
     TreeDeal deal{};
     bool any = false;
@@ -1130,8 +1132,8 @@ cudaError_t launch(TreeTask t, int slot, cudaStream_t stream) {
         !encode_pages_map(&map_v, t.v_pages, t, t.v_stride, t.box_rows))
         t.box_rows = 0;
     const int grid = (t.split ? t.groups : t.batch * t.bundles) * t.width;
-    kernel<<<grid, kTrThreads, L::kBytes, stream>>>(t, map_k, map_v);
-    e = cudaGetLastError();
+    e = launch_shaped(kernel, {dim3(grid), kTrThreads, L::kBytes, stream, true, 1}, t, map_k,
+                      map_v);
     if (e != cudaSuccess || !t.split || t.groups == 1) return e;
     const int64_t units = static_cast<int64_t>(t.batch) * t.bundles;
     const bool cuts = units >= t.groups;
