@@ -800,18 +800,18 @@ TreePlan tree_plan(const cs_tree_shape& s, int sms) {
     int32_t w = static_cast<int32_t>(p.units < sms ? p.units : sms);
     while (w > 1 && (p.units % w != 0 || (sms / w) * w * 20 < sms * 19)) --w;
     p.width = w < 1 ? 1 : w;
-    // 0: a CTA for every unit, and nothing to join: where no sequence can be
-    // longer than 4 blocks, or than 8 with units for at least three quarters of
-    // the SMs and no more than there are.  Blocks of 128, cut and whole, on the
-    // GPU (a call from the host takes 5 us less whole): 1 x 512 tokens, 8 units,
-    // 10.6 and 10.6 us, 32 x 512 18.4 and 18.9; 16 x 1024, 128 units, 16.4 and
-    // 15.2, 4 x 1024 12.7 and 14.5, 64 x 1024 34.6 and 42.3; 7 x 1531, 84 units,
-    // 15.5 and 19.4.  (The workspace's size goes by this too, and knows no
-    // device: so the SMs are a GB300's.)
+    // 0: a CTA for every unit, and nothing to join: with no more units than SMs,
+    // where no sequence can be longer than 4 blocks, or than 8 with units for at
+    // least three quarters of the SMs.  Blocks of 128, cut and whole, on the GPU
+    // (a call from the host takes 5 us less whole): 1 x 512 tokens, 8 units, 10.6
+    // and 10.6 us; 16 x 1024, 128 units, 16.4 and 15.2, 4 x 1024 12.7 and 14.5;
+    // 7 x 1531, 84 units, 15.5 and 19.4; 256 x 512, 2048 units, 56 and 115.
+    // (The workspace's size goes by this too, and knows no device: so the SMs
+    // are a GB300's.)
     const int64_t steps = tree_steps(s), total = steps * s.batch * (p.units / p.width);
     const int64_t all = s.batch * p.units;
-    const bool whole =
-        steps <= 4 || (steps <= 8 && 4 * all >= 3 * kPagedMaxSms && all <= kPagedMaxSms);
+    const bool whole = all <= kPagedMaxSms &&
+                       (steps <= 4 || (steps <= 8 && 4 * all >= 3 * kPagedMaxSms));
     p.groups = whole ? 0 : static_cast<int32_t>(sms / p.width < total ? sms / p.width : total);
     return p;
 }

@@ -440,6 +440,30 @@ struct WriteTask {
 
 cudaError_t launch_write(WriteTask task, cudaStream_t stream);
 
+// Division of 0 <= n < 2^31 by a number d > 0 that a launch knows, as a product
+// and a shift: with 2^(s-1) < d <= 2^s and m = ceil(2^(31+s) / d) < 2^32, m n =
+// 2^(31+s) n / d + e n / d with 0 <= e < d, and the last term, below n < 2^31,
+// is too small to carry n / d, whose fraction is at most (d - 1) / d, past the
+// next integer, 2^(31+s) / d >= 2^31 away.
+struct FastDiv {
+    uint32_t mul = 0;   // 0: d is 1
+    int32_t shift = 0;
+    FastDiv() = default;
+    explicit FastDiv(int32_t d) {
+        if (d <= 1) return;
+        int s = 0;
+        while ((int64_t(1) << s) < d) ++s;
+        mul = static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d);
+        shift = s - 1;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int n) const {
+        return mul == 0 ? n
+                        : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+    }
+#endif
+};
+
 // One paged_tree_attention launch: new_tokens tokens for each of `batch`
 // sequences over the cache of PagedTask.
 struct TreeTask {
@@ -467,7 +491,10 @@ struct TreeTask {
     int32_t split;             // 1: the blocks are dealt to groups, this many
     int32_t groups;
     int32_t fp16;
-    int32_t box_rows;          // tokens of a tensor copy; 0: copies of 16 bytes
+    int32_t box_bits;          // log2 of the tokens of a tensor copy; -1: copies
+                               // of 16 bytes
+    int32_t skip, rest;        // a block's tokens: whole pages, and the rest
+    FastDiv by_page, by_group, by_kv_heads, by_groups, by_width;
     float scale;
     uint64_t wait_limit_cycles;
 };

@@ -193,7 +193,7 @@ __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan,
         int first, all;
         tree_scan<WARPS>(n, scan, first, all);
         if (once) total = all;
-        d.share = max(1, (total + t.groups - 1) / t.groups);
+        d.share = max(1, t.by_groups(total + t.groups - 1));
         d.g0 = grp * d.share;
         d.g1 = min(total, d.g0 + d.share);
         if (d.g0 >= d.g1) return false;
@@ -230,7 +230,7 @@ template <int BLK, int NQ>
 __device__ __forceinline__ TreePart tree_part(const TreeTask& t, int b, const TreeLens& n,
                                               int unit, int s0, int s1, int steps) {
     TreePart p{};
-    const int tile = unit / t.kv_heads;
+    const int tile = t.by_kv_heads(unit);
     p.b = b;
     p.hk = unit - tile * t.kv_heads;
     p.r0 = 128 * NQ * tile;
@@ -243,10 +243,23 @@ __device__ __forceinline__ TreePart tree_part(const TreeTask& t, int b, const Tr
     p.place = s0 == 0 && s1 == steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (s0 == 0);
     // None without rows, and none past the last row's token where each row
     // attends those before it.
-    int last = s1;
-    if (!t.mask) last = min(last, (p.context + (p.r0 + p.valid - 1) / t.group + BLK) / BLK);
-    p.n = p.valid <= 0 ? 0 : max(0, last - s0);
+    int last = p.valid > 0 ? s1 : s0;
+    if (!t.mask && p.valid > 0)
+        last = min(last, (p.context + t.by_group(p.r0 + p.valid - 1) + BLK) / BLK);
+    p.n = max(0, last - s0);
     return p;
+}
+
+// Of a block whose boxes with bit 0 lie on pages outside the cache: reports
+// that, and gives lane w the tokens 32 w to 32 w + 31 that are there.
+__device__ __forceinline__ uint32_t tree_lost(const TreeTask& t, uint32_t good) {
+    const int lane = threadIdx.x & 31;
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (int x = 0; x < 32; ++x)
+        bits |= (good >> (((32 * lane + x) >> t.box_bits) & 31) & 1u) << x;
+    if (lane == 0) raise_error(t.err, kBitBadPage);
+    return bits;
 }
 
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -337,7 +350,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const bool tensor_copies = t.box_rows > 0;
+    const bool tensor_copies = t.box_bits >= 0;
     if (warp == kTrCopyWarp) {
         for (int i = lane; i < L::kNumBars; i += 32) {
             uint64_t* bar = bars + i;
@@ -358,7 +371,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
     }
     // Launched while the kernel before ends; nothing of memory is touched above.
     wait_for_previous_kernel();
-    const int grp = static_cast<int>(blockIdx.x) / t.width;
+    const int grp = t.by_width(static_cast<int>(blockIdx.x));
     TreeDeal deal{};
     bool any = false;
     // A large batch's lengths are added up by the whole CTA.
@@ -409,7 +422,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             const int mine = NT == 1 && wg > 0 ? 0 : (n - first + kStep - 1) / kStep;
             float m = -INFINITY, l = 0.0f;
             if (mine > 0) {
-                const int context = p->context, token = (p->r0 + r) / group;
+                const int context = p->context, token = t.by_group(p->r0 + r);
                 const bool warp_valid = warp_r < p->valid;
                 // The row keeps the tokens below this, and of them those the
                 // mask keeps; every row of the warp those below `all_below`.
@@ -429,20 +442,32 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                             // The mask's rows of this warp's tokens, 32 bytes
                             // at a time.
                             const int fresh = p->len - context;
-                            const int i0 = (p->r0 + warp_r) / group;
-                            const int i1 = min((p->r0 + warp_r + 31) / group, fresh - 1);
+                            const int i0 = t.by_group(p->r0 + warp_r);
+                            const int i1 = min(t.by_group(p->r0 + warp_r + 31), fresh - 1);
                             const uint8_t* row = t.mask + p->b * t.mask_stride[0] +
                                                  i0 * t.mask_stride[1] + key - context + lane;
-#pragma unroll 2
-                            for (int i = i0; i <= i1; ++i, row += t.mask_stride[1]) {
+                            // (Four tokens' loads under way at once.)
+#pragma unroll 1
+                            for (int i = i0; i <= i1; i += 4, row += 4 * t.mask_stride[1]) {
+                                bool keep[4][BLK / 32];
 #pragma unroll
-                                for (int w = 0; w < BLK / 32; ++w) {
-                                    const int j = key + 32 * w + lane - context;
-                                    bool keep = j < 0;
-                                    if (j >= 0 && j < fresh) keep = row[32 * w] != 0;
-                                    const uint32_t bits = __ballot_sync(0xffffffffu, keep);
-                                    if (i == token) kept[w] &= bits;
-                                }
+                                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                    for (int w = 0; w < BLK / 32; ++w) {
+                                        const int j = key + 32 * w + lane - context;
+                                        keep[x][w] = j < 0;
+                                        if (j >= 0 && j < fresh && i + x <= i1)
+                                            keep[x][w] =
+                                                row[x * t.mask_stride[1] + 32 * w] != 0;
+                                    }
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                    for (int w = 0; w < BLK / 32; ++w) {
+                                        const uint32_t bits =
+                                            __ballot_sync(0xffffffffu, keep[x][w]);
+                                        if (i + x == token) kept[w] &= bits;
+                                    }
                             }
                         }
                     }
@@ -545,7 +570,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             // Where the row goes, worked out while the last products run.
             const int rows = p->rows, place = p->place;
             const bool here = r < rows;
-            const int token = (p->r0 + r) / group;
+            const int token = t.by_group(p->r0 + r);
             const int h = p->hk * group + (p->r0 + r) - token * group;
             // Whose columns: with one tile each warpgroup half of them.
             const int d0 = NQ == 1 ? wg * (DP / 2) : 0;
@@ -678,8 +703,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         // Values past the length, which a tensor copy brings in
                         // with the last ones before: 0 times them has to be 0.
                         const int there = past - v / NQ * BLK;
-                        if (there < BLK && there % t.box_rows != 0) {
-                            const int rows = t.box_rows - there % t.box_rows;
+                        const int rows = -there & ((1 << t.box_bits) - 1);
+                        if (there < BLK && rows != 0) {
                             unsigned char* tile = smem + L::kV + st * L::kBlock + there * 128;
 #pragma unroll 1
                             for (int e = lane; e < rows * (DP / 8); e += 32) {
@@ -803,7 +828,6 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                                      reinterpret_cast<const uint16_t*>(a) + at_unit, bytes);
                 }
             };
-            const int skip = BLK / t.page_size, rest = BLK - skip * t.page_size;
             // A lane's token of every block, its entry of the table and its
             // slot; looked up three blocks ahead: a table's entry takes a
             // microsecond to come when it is not in a cache.
@@ -820,8 +844,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                     at.page = table[entry];
                 }
                 tok += BLK;
-                entry += skip;
-                slot += rest;
+                entry += t.skip;
+                slot += t.rest;
                 if (slot >= t.page_size) {
                     slot -= t.page_size;
                     ++entry;
@@ -832,7 +856,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 table = t.page_table + p->b * t.table_stride;
                 len = p->len;
                 tok = p->key0 + first;
-                entry = tok / t.page_size;
+                entry = t.by_page(tok);
                 slot = tok - entry * t.page_size;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) ahead[x] = locate();
@@ -852,7 +876,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
 #pragma unroll 1
                 for (int r0 = 32 * w; r0 < 128 * NQ; r0 += 32 * warps) {
                     const int r = r0 + lane;
-                    const int token = (p->r0 + r) / group;
+                    const int token = t.by_group(p->r0 + r);
                     const bool valid = r < p->valid;
                     const uint16_t* a = t.q;
                     if (valid)
@@ -882,13 +906,13 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 uint64_t* full = keys ? k_full : v_full;
                 uint64_t* empty = keys ? k_empty : v_empty;
                 unsigned char* ring = smem + (keys ? L::kK : L::kV);
-                const int boxes = BLK / t.box_rows;
+                const int boxes = BLK >> t.box_bits;
                 for (int ip = 0;; ++ip) {
                     bool ok;
                     const TreePart* p = part(ip, ok);
                     if (!ok || p->n < 0) break;
                     const int n = p->n, hk = p->hk;
-                    if (n > 0) begin(p, (lane % boxes) * t.box_rows);
+                    if (n > 0) begin(p, (lane & (boxes - 1)) << t.box_bits);
                     done_with(ip);
 #pragma unroll 1
                     for (int j = 0; j < n; ++j) {
@@ -900,15 +924,9 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         if (keys) {
                             // Boxes whose page is in the cache, and their tokens.
                             const bool lost = at.slot >= 0 && !valid;
-                            if (lost && lane < boxes) raise_error(t.err, kBitBadPage);
                             const uint32_t good = __ballot_sync(0xffffffffu, !lost);
                             uint32_t bits = ~0u;
-                            if (good != ~0u) {   // rare
-                                bits = 0;
-#pragma unroll 1
-                                for (int x = 0; x < 32; ++x)
-                                    bits |= (good >> ((32 * lane + x) / t.box_rows & 31) & 1u) << x;
-                            }
+                            if (good != ~0u) bits = tree_lost(t, good);   // rare
                             if (lane < BLK / 32) words[4 * (kb % kTrWords) + lane] = bits;
                             __syncwarp();
                         }
@@ -917,7 +935,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         if (lane < boxes) {
                             // (Outside the cache: zeros.)
                             const int page = at.slot >= 0 && valid ? at.page : t.num_pages;
-                            unsigned char* dst = ring + st * L::kBlock + lane * t.box_rows * 128;
+                            unsigned char* dst = ring + st * L::kBlock + (lane << t.box_bits) * 128;
 #pragma unroll
                             for (int x = 0; x < DP / 64; ++x)
                                 tma_load_4d(dst + x * BLK * 128, map, 64 * x, hk,
@@ -1020,7 +1038,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
     constexpr int kWarps = kTrJoinThreads / 32;
     __shared__ int scan[kWarps + 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int x = blockIdx.x % t.width, chunk = blockIdx.x / t.width;
+    const int chunk = t.by_width(blockIdx.x), x = blockIdx.x - chunk * t.width;
     int b, bundle = 0, begin = 0, steps = 0, share = 1;
     bool bad, cut = true;
     if constexpr (!CUTS) {
@@ -1035,7 +1053,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
         int skip, all;
         tree_scan<kWarps>(total, scan, skip, all);
         __syncthreads();
-        share = max(1, (all + t.groups - 1) / t.groups);
+        share = max(1, t.by_groups(all + t.groups - 1));
         tree_scan<kWarps>(before, scan, skip, all);
         steps = tree_steps<BLK>(tree_lens(t, b, bad));
         begin = all + bundle * tree_places(steps) + kTrPartCost;
@@ -1125,12 +1143,19 @@ cudaError_t launch(TreeTask t, int slot, cudaStream_t stream) {
     // Tensor copies take boxes of one page: the rows of the largest power of two
     // that divides the page and the block, 8 (a swizzled atom) at least.
     CUtensorMap map_k{}, map_v{};
-    t.box_rows = t.page_size & -t.page_size;
-    if (t.box_rows > L::kBlk) t.box_rows = L::kBlk;
-    if (t.box_rows < 8 || t.num_pages == 0 ||
-        !encode_pages_map(&map_k, t.k_pages, t, t.k_stride, t.box_rows) ||
-        !encode_pages_map(&map_v, t.v_pages, t, t.v_stride, t.box_rows))
-        t.box_rows = 0;
+    t.box_bits = 0;
+    while ((t.page_size >> t.box_bits & 1) == 0 && (1 << t.box_bits) < L::kBlk) ++t.box_bits;
+    if (t.box_bits < 3 || t.num_pages == 0 ||
+        !encode_pages_map(&map_k, t.k_pages, t, t.k_stride, 1 << t.box_bits) ||
+        !encode_pages_map(&map_v, t.v_pages, t, t.v_stride, 1 << t.box_bits))
+        t.box_bits = -1;
+    t.skip = L::kBlk / t.page_size;
+    t.rest = L::kBlk - t.skip * t.page_size;
+    t.by_page = FastDiv(t.page_size);
+    t.by_group = FastDiv(t.group);
+    t.by_kv_heads = FastDiv(t.kv_heads);
+    t.by_groups = FastDiv(t.groups);
+    t.by_width = FastDiv(t.width);
     const int grid = (t.split ? t.groups : t.batch * t.bundles) * t.width;
     e = launch_shaped(kernel, {dim3(grid), kTrThreads, L::kBytes, stream, true, 1}, t, map_k,
                       map_v);
