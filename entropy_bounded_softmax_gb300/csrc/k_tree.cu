@@ -250,6 +250,54 @@ __device__ __forceinline__ TreePart tree_part(const TreeTask& t, int b, const Tr
     return p;
 }
 
+// A row's kept tokens of a block: token x is new token j0 + x, of the row's
+// `fresh`, where that is not negative, and a token before the new ones, which
+// all rows keep, where it is.  Clears the bits of what the row, `fresh` bytes,
+// does not keep.  A thread a row, words of 4 bytes all under way at once, single
+// bytes at the row's ends.  (Whole warps a row, 32 bytes at a time, took ten
+// microseconds for 64 rows of 64 in a CTA of its own.)
+template <int BLK>
+__device__ __forceinline__ void tree_mask_row(const uint8_t* row, int j0, int fresh,
+                                              uint32_t (&kept)[BLK / 32]) {
+    const int lo = max(0, -j0), hi = min(BLK, fresh - j0);   // x of the row's bytes
+    const int64_t at = reinterpret_cast<int64_t>(row) + j0;  // of x = 0
+    const int head = static_cast<int>(at & 3);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(at - head);
+    uint32_t bits[BLK / 32 + 1];   // of x = -head ..
+#pragma unroll
+    for (int w = 0; w <= BLK / 32; ++w) bits[w] = 0u;
+    uint32_t v[BLK / 4 + 1];
+#pragma unroll
+    for (int k = 0; k <= BLK / 4; ++k) {
+        const int x = 4 * k - head;
+        v[k] = x >= lo && x + 4 <= hi ? __ldg(words + k) : 0u;
+    }
+    const int first = (lo + head + 3) / 4 * 4 - head, last = (hi + head) / 4 * 4 - head;
+    bool edge[6];
+    int edge_x[6];
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+        edge_x[e] = lo + e;
+        edge_x[3 + e] = max(first, last) + e;
+        edge[e] = edge_x[e] < min(first, hi) && row[j0 + edge_x[e]] != 0;
+        edge[3 + e] = edge_x[3 + e] < hi && row[j0 + edge_x[3 + e]] != 0;
+    }
+#pragma unroll
+    for (int k = 0; k <= BLK / 4; ++k) {
+        // Bytes that are not 0, to their lowest bits, and these side by side.
+        const uint32_t m = ((((v[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v[k]) >> 7) & 0x01010101u;
+        bits[k / 8] |= (m * 0x01020408u >> 24 & 15u) << (4 * k % 32);
+    }
+#pragma unroll
+    for (int w = 0; w < BLK / 32; ++w) {
+        uint32_t keep = __funnelshift_r(bits[w], bits[w + 1], head) | bits_below(-j0, 32 * w);
+#pragma unroll
+        for (int e = 0; e < 6; ++e)
+            if (edge[e] && edge_x[e] >> 5 == w) keep |= 1u << (edge_x[e] & 31);
+        kept[w] &= keep;
+    }
+}
+
 // Of a block whose boxes with bit 0 lie on pages outside the cache: reports
 // that, and gives lane w the tokens 32 w to 32 w + 31 that are there.
 __device__ __forceinline__ uint32_t tree_lost(const TreeTask& t, uint32_t good) {
@@ -438,38 +486,10 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                         for (int w = 0; w < BLK / 32; ++w)
                             kept[w] = bits_below(row_limit, key + 32 * w);
-                        if (t.mask && warp_valid && key + BLK > context) {
-                            // The mask's rows of this warp's tokens, 32 bytes
-                            // at a time.
-                            const int fresh = p->len - context;
-                            const int i0 = t.by_group(p->r0 + warp_r);
-                            const int i1 = min(t.by_group(p->r0 + warp_r + 31), fresh - 1);
-                            const uint8_t* row = t.mask + p->b * t.mask_stride[0] +
-                                                 i0 * t.mask_stride[1] + key - context + lane;
-                            // (Four tokens' loads under way at once.)
-#pragma unroll 1
-                            for (int i = i0; i <= i1; i += 4, row += 4 * t.mask_stride[1]) {
-                                bool keep[4][BLK / 32];
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                                    for (int w = 0; w < BLK / 32; ++w) {
-                                        const int j = key + 32 * w + lane - context;
-                                        keep[x][w] = j < 0;
-                                        if (j >= 0 && j < fresh && i + x <= i1)
-                                            keep[x][w] =
-                                                row[x * t.mask_stride[1] + 32 * w] != 0;
-                                    }
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                                    for (int w = 0; w < BLK / 32; ++w) {
-                                        const uint32_t bits =
-                                            __ballot_sync(0xffffffffu, keep[x][w]);
-                                        if (i + x == token) kept[w] &= bits;
-                                    }
-                            }
-                        }
+                        if (t.mask && warp_valid && key + BLK > context)
+                            tree_mask_row<BLK>(
+                                t.mask + p->b * t.mask_stride[0] + token * t.mask_stride[1],
+                                key - context, r < p->valid ? p->len - context : 0, kept);
                     }
                     ok = warp_wait(&s_full[tile], visit, limit);
                     if (!ok) break;
