@@ -94,7 +94,7 @@ struct TreePlan {
     static constexpr int kNumBars = 4 * kStages + 9 + 2 * kTrParts;
     static constexpr int kWords = kBars + (8 * kNumBars + 15) / 16 * 16;  // [kTrWords][4]
     static constexpr int kParts = kWords + kTrWords * 16;
-    static constexpr int kScan = kParts + kTrParts * 48;   // [18] ints
+    static constexpr int kScan = kParts + kTrParts * 48;   // [20] ints
     static constexpr int kFlags = kScan + 80;              // abort, tmem
     static constexpr int kStats = kFlags + 16;             // [2][128] float2 (one tile)
     static constexpr int kBytes = kStats + (NQ == 1 ? 2 * 128 * 8 : 0);
@@ -165,17 +165,20 @@ __device__ __forceinline__ void tree_sync() {
 // b whose first is `base`.
 struct TreeDeal {
     int g0, g1, b, base, share;
+    TreeLens n;
 };
 
 // By a whole CTA of 32 WARPS threads, or one warp; false without places.  scan:
-// WARPS + 2 shared ints.
+// WARPS + 4 shared ints.
 template <int WARPS, int BLK>
 __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan, TreeDeal& d) {
     constexpr int kThreads = 32 * WARPS;
     const int thread = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x;
     bool bad;
+    TreeLens mine{};
     auto places = [&](int i) {
-        return i < t.batch ? tree_places(tree_steps<BLK>(tree_lens(t, i, bad))) * t.bundles : 0;
+        if (i < t.batch) mine = tree_lens(t, i, bad);
+        return i < t.batch ? tree_places(tree_steps<BLK>(mine)) * t.bundles : 0;
     };
     int total = 0, before;
     const bool once = t.batch <= kThreads;   // one walk over the lengths is enough
@@ -201,6 +204,8 @@ __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan,
         if (first <= d.g0 && d.g0 < first + n) {
             scan[WARPS] = i;
             scan[WARPS + 1] = first;
+            scan[WARPS + 2] = mine.len;
+            scan[WARPS + 3] = mine.fresh;
         }
         done += all;
         tree_sync<WARPS>();
@@ -209,6 +214,7 @@ __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan,
     // (In range even where the lengths were changed under the call.)
     d.b = max(0, min(scan[WARPS], t.batch - 1));
     d.base = min(scan[WARPS + 1], d.g0);
+    d.n = TreeLens{scan[WARPS + 2], scan[WARPS + 3]};
     return true;
 }
 
@@ -783,7 +789,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 int g = deal.g0, b = deal.b - 1, bundle = t.bundles, at = 0, steps = 0;
                 TreeLens n{};
                 if (any) {
-                    n = tree_lens(t, ++b, bad);
+                    n = deal.n;
+                    ++b;
                     steps = tree_steps<BLK>(n);
                     const int places = max(1, tree_places(steps));
                     bundle = min((g - deal.base) / places, t.bundles);
@@ -1056,7 +1063,7 @@ constexpr int kTrJoinThreads = 128;
 template <int BLK, class E, bool CUTS>
 __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTask t) {
     constexpr int kWarps = kTrJoinThreads / 32;
-    __shared__ int scan[kWarps + 2];
+    __shared__ int scan[kWarps + 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int chunk = t.by_width(blockIdx.x), x = blockIdx.x - chunk * t.width;
     int b, bundle = 0, begin = 0, steps = 0, share = 1;
