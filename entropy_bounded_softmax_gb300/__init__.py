@@ -1010,7 +1010,7 @@ def paged_tree_attention(query, key_pages, value_pages, page_table, lengths,
     with ``return_lse`` the log of the softmax's sums [B, T, H] in fp32.
     Asynchronous on the current stream; lengths and page numbers out of range
     are left out and reported by :func:`get_error`, and so are NaN or infinite
-    scores, which propagate (as does a NaN among a sequence's values, to all of
+    scores, which propagate (a NaN among a sequence's values may reach all of
     its rows).  For serving: there is no backward pass, and the result carries
     no gradient.
     """

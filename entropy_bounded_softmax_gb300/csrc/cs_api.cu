@@ -837,10 +837,11 @@ cs_status check_tree(const uint16_t* query, const uint16_t* key_pages,
     if (st != CS_OK) return st;
     const cs_tree_shape& s = *shape;
     if (s.batch == 0 || s.new_tokens == 0) return CS_OK;
-    // Blocks and CTAs are counted in 32 bits.
+    // Blocks, with what a part's start and end count, and CTAs are counted in 32
+    // bits.
     p = tree_plan(s, kPagedMaxSms);
     if (p.units * s.batch > (1 << 30) ||
-        tree_steps(s) > (1 << 30) / (s.batch * (p.units / p.width)))
+        tree_steps(s) + cs::kTreePartCost > (1 << 30) / (s.batch * (p.units / p.width)))
         return CS_ERR_DIM_MISMATCH;
     const int64_t need = tree_workspace(s, p);
     if (workspace_bytes < need) return CS_ERR_INVALID_ARG;

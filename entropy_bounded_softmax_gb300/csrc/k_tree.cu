@@ -54,7 +54,6 @@ constexpr float kTrLagBits = 6.0f;     // how far the maximum may lag
 constexpr int kTrWords = 8;            // blocks whose kept tokens are noted
 constexpr int kTrParts = 4;            // parts that are known ahead
 constexpr int kTrPartWarps = 13;       // that read them
-constexpr int kTrPartCost = 2;         // blocks that take as long as a part's start and end
 
 struct TrBF16 {
     static constexpr bool kFp16 = false;
@@ -118,7 +117,7 @@ __device__ __forceinline__ TreeLens tree_lens(const TreeTask& t, int b, bool& ba
 }
 
 __device__ __forceinline__ int tree_places(int steps) {
-    return steps > 0 ? steps + kTrPartCost : 0;
+    return steps > 0 ? steps + kTreePartCost : 0;
 }
 
 // Blocks of a unit of sequence b.
@@ -160,7 +159,7 @@ __device__ __forceinline__ void tree_sync() {
 }
 
 // What a group of CTAs has of the batch's list: for each sequence, for each of
-// its bundles of `width` units side by side, kTrPartCost places for a part's
+// its bundles of `width` units side by side, kTreePartCost places for a part's
 // start and end and then its blocks.  Places g0 .. g1 - 1, the first in sequence
 // b whose first is `base`.
 struct TreeDeal {
@@ -259,11 +258,12 @@ __device__ __forceinline__ TreePart tree_part(const TreeTask& t, int b, const Tr
 // A row's kept tokens of a block: token x is new token j0 + x, of the row's
 // `fresh`, where that is not negative, and a token before the new ones, which
 // all rows keep, where it is.  Clears the bits of what the row, `fresh` bytes,
-// does not keep.  A thread a row, words of 4 bytes all under way at once, single
-// bytes at the row's ends.  (Whole warps a row, 32 bytes at a time, took ten
-// microseconds for 64 rows of 64 in a CTA of its own.)
+// does not keep.  A thread a row: words of 4 bytes, eight under way at once,
+// single bytes at the row's ends; words that no row of the warp, which have up to
+// `most` bytes, reaches into are passed over.  (Whole warps a row, 32 bytes at a
+// time, took ten microseconds for 64 rows of 64 in a CTA of its own.)
 template <int BLK>
-__device__ __forceinline__ void tree_mask_row(const uint8_t* row, int j0, int fresh,
+__device__ __forceinline__ void tree_mask_row(const uint8_t* row, int j0, int fresh, int most,
                                               uint32_t (&kept)[BLK / 32]) {
     const int lo = max(0, -j0), hi = min(BLK, fresh - j0);   // x of the row's bytes
     const int64_t at = reinterpret_cast<int64_t>(row) + j0;  // of x = 0
@@ -272,12 +272,6 @@ __device__ __forceinline__ void tree_mask_row(const uint8_t* row, int j0, int fr
     uint32_t bits[BLK / 32 + 1];   // of x = -head ..
 #pragma unroll
     for (int w = 0; w <= BLK / 32; ++w) bits[w] = 0u;
-    uint32_t v[BLK / 4 + 1];
-#pragma unroll
-    for (int k = 0; k <= BLK / 4; ++k) {
-        const int x = 4 * k - head;
-        v[k] = x >= lo && x + 4 <= hi ? __ldg(words + k) : 0u;
-    }
     const int first = (lo + head + 3) / 4 * 4 - head, last = (hi + head) / 4 * 4 - head;
     bool edge[6];
     int edge_x[6];
@@ -288,11 +282,23 @@ __device__ __forceinline__ void tree_mask_row(const uint8_t* row, int j0, int fr
         edge[e] = edge_x[e] < min(first, hi) && row[j0 + edge_x[e]] != 0;
         edge[3 + e] = edge_x[3 + e] < hi && row[j0 + edge_x[3 + e]] != 0;
     }
+#pragma unroll 1
+    for (int g = 0; g <= BLK / 32; ++g) {
+        if (-j0 >= 32 * g + 32 || most - j0 <= 32 * g - 3) continue;
+        uint32_t v[8], sum = 0;
 #pragma unroll
-    for (int k = 0; k <= BLK / 4; ++k) {
-        // Bytes that are not 0, to their lowest bits, and these side by side.
-        const uint32_t m = ((((v[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v[k]) >> 7) & 0x01010101u;
-        bits[k / 8] |= (m * 0x01020408u >> 24 & 15u) << (4 * k % 32);
+        for (int k = 0; k < 8; ++k) {
+            const int x = 32 * g + 4 * k - head;
+            v[k] = x >= lo && x + 4 <= hi ? __ldg(words + 8 * g + k) : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            // Bytes that are not 0, to their lowest bits, and these side by side.
+            const uint32_t m = ((((v[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v[k]) >> 7) & 0x01010101u;
+            sum |= (m * 0x01020408u >> 24 & 15u) << (4 * k);
+        }
+#pragma unroll
+        for (int y = 0; y <= BLK / 32; ++y) bits[y] = y == g ? sum : bits[y];
     }
 #pragma unroll
     for (int w = 0; w < BLK / 32; ++w) {
@@ -495,7 +501,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         if (t.mask && warp_valid && key + BLK > context)
                             tree_mask_row<BLK>(
                                 t.mask + p->b * t.mask_stride[0] + token * t.mask_stride[1],
-                                key - context, r < p->valid ? p->len - context : 0, kept);
+                                key - context, r < p->valid ? p->len - context : 0, p->len - context, kept);
                     }
                     ok = warp_wait(&s_full[tile], visit, limit);
                     if (!ok) break;
@@ -806,7 +812,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                     if (b >= t.batch) break;
                     const int places = tree_places(steps);
                     const int to = min(places, at + deal.g1 - g);
-                    const int s0 = max(0, at - kTrPartCost), s1 = to - kTrPartCost;
+                    const int s0 = max(0, at - kTreePartCost), s1 = to - kTreePartCost;
                     if (s1 > s0)
                         give(tree_part<BLK, NQ>(
                             t, b, n, bundle * t.width + static_cast<int>(blockIdx.x) - grp * t.width,
@@ -1083,7 +1089,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
         share = max(1, t.by_groups(all + t.groups - 1));
         tree_scan<kWarps>(before, scan, skip, all);
         steps = tree_steps<BLK>(tree_lens(t, b, bad));
-        begin = all + bundle * tree_places(steps) + kTrPartCost;
+        begin = all + bundle * tree_places(steps) + kTreePartCost;
     } else {
         TreeDeal d;
         const int later = blockIdx.y + 1;
@@ -1094,7 +1100,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
             steps = tree_steps<BLK>(tree_lens(t, b, bad));
             const int places = max(1, tree_places(steps));
             bundle = min((d.g0 - d.base) / places, t.bundles - 1);
-            begin = d.base + bundle * places + kTrPartCost;
+            begin = d.base + bundle * places + kTreePartCost;
             cut = begin < d.g0 && begin / share == later - 1;
         }
     }

@@ -845,8 +845,8 @@ typedef struct cs_tree_shape {
  * rounded to the cache's type, their sums are fp32 in a fixed order, which
  * depends on the batch's lengths (repeated calls give the same bits).  NaN or
  * infinite scores propagate to their row and OR CS_ERR_NAN_INPUT; a NaN or
- * infinite value of a token propagates to every row of its sequence and head,
- * those that do not attend it too.  Ownership, execution and errors: as
+ * infinite value of a token may reach every row of its sequence and key head,
+ * those that do not attend it too (0 times it is added).  Ownership, execution and errors: as
  * cs_constrained_softmax.
  */
 cs_status cs_paged_tree_attention(

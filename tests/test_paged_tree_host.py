@@ -178,6 +178,9 @@ def check_tree(s, q=A[0], k=A[1], v=A[2], table=A[3], lengths=A[4], new=A[5],
     (dict(scale=2.0 ** 127), OK), (dict(scale=2.0 ** 127.2), BAD),
     (dict(most=1 << 27), DIM),                # more than 2^30 tokens a row
     (dict(T=1 << 29), DIM),                   # more than 2^30 rows
+    # More than 2^30 blocks with their starts and ends: 16381 key heads, one by
+    # one, of 65535 sequences.
+    (dict(B=65535, H=16381, Hk=16381, D=8, most=1, page=1, pages=1), DIM),
     (dict(q=(2560, 512, 60)), BAD), (dict(q=(-2560, 512, 64)), BAD),
     (dict(q=(0, 0, 0)), OK),
     (dict(o=(2560, 512, 32)), BAD), (dict(o=(2560, 0, 64)), BAD),
