@@ -406,7 +406,6 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
     int* scan = reinterpret_cast<int*>(smem + L::kScan);
     volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + L::kFlags);
     const WaitLimit limit{flags, t.wait_limit_cycles};
-    allow_next_kernel();
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -430,7 +429,10 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
         prefetch_tmap(&map_v);
     }
     // Launched while the kernel before ends; nothing of memory is touched above.
+    // The join may start only after this wait, since it reads the lengths, which
+    // a kernel before this one (paged_extend's) may have written, before its own.
     wait_for_previous_kernel();
+    allow_next_kernel();
     const int grp = t.by_width(static_cast<int>(blockIdx.x));
     TreeDeal deal{};
     bool any = false;

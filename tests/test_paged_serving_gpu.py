@@ -158,3 +158,46 @@ def test_pool_runs_dry():
     assert (out[2] == 0).all() and cs.get_error() == set()
     # Two roundings of results and weights.
     assert (out[:2].float() - want[:2].float()).abs().max() < 4 * 2.0 ** -8 * 4.5
+
+
+@pytest.mark.parametrize("B,most", [(3, 4096), (40, 512), (300, 16)])
+def test_lengths_of_the_call_before(B, most):
+    """paged_tree_attention with the lengths that paged_extend just wrote: what
+    its kernels look up ahead may not be of the lengths before.  One captured
+    run, replayed with lengths that grow and shrink."""
+    T, D, page, dtype = 4, 64, 16, torch.bfloat16
+    gen = torch.Generator().manual_seed(B)
+    longest = 3000 if B < 10 else 600
+    entries = (longest + most) // page + 1
+    pages = [torch.randn(2048, page, HK, D, generator=gen).to(dtype).cuda()
+             for _ in range(2)]
+    table = torch.randint(0, 2048, (B, entries), generator=gen).int().cuda()
+    free = torch.arange(2048, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, T, H, D, generator=gen).to(dtype).cuda()
+    count = torch.randint(0, T + 1, (B,), generator=gen).int().cuda()
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+
+    def run():
+        totals = cs.paged_extend(table, lengths, count, free, page, most)[1]
+        return cs.paged_tree_attention(q, *pages, table, totals,
+                                       new_lengths=count)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for i in range(12):
+        top = longest if i % 2 else 1 + longest // 50
+        now = torch.randint(0, top, (B,), generator=gen).int().cuda()
+        lengths.copy_(now)
+        torch.cuda.synchronize()
+        graph.replay()
+        got = out.clone()
+        want = cs.paged_tree_attention(q, *pages, table, now + count,
+                                       new_lengths=count)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert cs.get_error() <= {"OUT_OF_PAGES"}
