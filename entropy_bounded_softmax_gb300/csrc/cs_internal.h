@@ -493,6 +493,7 @@ struct TreeTask {
     int32_t fp16;
     int32_t box_bits;          // log2 of the tokens of a tensor copy; -1: copies
                                // of 16 bytes
+    int32_t tensor_q;          // 1: tensor copies for the queries, too
     int32_t skip, rest;        // a block's tokens: whole pages, and the rest
     FastDiv by_page, by_group, by_kv_heads, by_groups, by_width;
     float scale;

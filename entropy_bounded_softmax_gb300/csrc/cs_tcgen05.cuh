@@ -288,6 +288,12 @@ __device__ __forceinline__ void tma_load_4d(void* sdst, const void* tmap, int x,
            "r"(smem_addr(bar)) : "memory");
 }
 
+// Fetches a box into L2 alone.
+__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
+                 :: "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // Fetches a tensor map ahead of its first use.
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(tmap) : "memory");

@@ -96,4 +96,28 @@ inline bool encode_pages_map(CUtensorMap* map, const void* data, const TreeTask&
                       dim, bytes, box, step);
 }
 
+// The map of the queries of those pages' call, in boxes of 64 elements of the
+// heads of one key head x as many tokens as make 128 rows; tokens past the last
+// read as zeros.  False where they make none, or the strides are none that
+// tensor copies take.
+inline bool encode_queries_map(CUtensorMap* map, const TreeTask& t) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc || 128 % t.group != 0) return false;
+    const cuuint64_t dim[4] = {static_cast<cuuint64_t>(t.d_head),
+                               static_cast<cuuint64_t>(t.heads),
+                               static_cast<cuuint64_t>(t.new_tokens),
+                               static_cast<cuuint64_t>(t.batch)};
+    cuuint64_t bytes[3];
+    for (int i = 0; i < 3; ++i) {   // head, token, sequence
+        bytes[i] = dim[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(t.q_stride[2 - i]) * 2;
+        if (bytes[i] == 0 || bytes[i] >> 40) return false;
+    }
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(t.group),
+                               static_cast<cuuint32_t>(128 / t.group), 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return encode_map(enc, map, t.q,
+                      t.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      dim, bytes, box, step);
+}
+
 }  // namespace cs

@@ -378,7 +378,7 @@ __device__ __forceinline__ void tree_lse(const TreeTask& t, int b, int i, int h,
 template <int DP, int NQ, class E>
 __global__ void __launch_bounds__(kTrThreads, 1)
 tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
-            const __grid_constant__ CUtensorMap map_v) {
+            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q) {
     using L = TreePlan<DP, NQ>;
     constexpr int NS = L::kStages, BLK = L::kBlk, NT = L::kTiles;
     // (No room is left to align it here: the swizzled tiles want 1024 bytes.)
@@ -415,7 +415,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             uint64_t* bar = bars + i;
             mbar_init(bar, bar < k_empty ? (tensor_copies ? 1 : 128 + 4)
                            : bar >= v_full && bar < v_empty ? (tensor_copies ? 1 : 128)
-                           : bar == q_full ? (tensor_copies ? 64 : 128)
+                           : bar == q_full ? (t.tensor_q ? 1 : tensor_copies ? 64 : 128)
                            : bar >= p_full && bar < q_full ? 4
                            : bar == joined ? 8
                            : bar >= part_empty ? kTrPartWarps : 1);
@@ -427,6 +427,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
     } else if (warp == kTrCopyWarp + 1 && lane == 0 && tensor_copies) {
         prefetch_tmap(&map_k);
         prefetch_tmap(&map_v);
+        if (t.tensor_q) prefetch_tmap(&map_q);
     }
     // Launched while the kernel before ends; nothing of memory is touched above.
     // The join may start only after this wait, since it reads the lengths, which
@@ -923,16 +924,53 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                 cp_async_arrive(q_full);
                 return true;
             };
+            // The same by tensor copies, a box of 128 rows each; into L2 before
+            // the last part's products have left the room for them.
+            auto fetch_q = [&](const TreePart* p) {
+                const int head = p->hk * group, token = t.by_group(p->r0);
+                auto each = [&](auto copy) {
+#pragma unroll
+                    for (int y = 0; y < NQ; ++y)
+#pragma unroll
+                        for (int x = 0; x < DP / 64; ++x)
+                            copy(L::kQ + y * L::kTile + x * 128 * 128, 64 * x,
+                                 token + y * t.by_group(128));
+                };
+                if (with_blocks > 0) {
+                    if (lane == 0)
+                        each([&](int, int x, int z) { tma_prefetch_4d(&map_q, x, head, z, p->b); });
+                    __syncwarp();
+                    if (!warp_wait(q_empty, with_blocks - 1, limit)) return false;
+                }
+                ++with_blocks;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, NQ * L::kTile);
+                    each([&](int to, int x, int z) {
+                        tma_load_4d(smem + to, &map_q, x, head, z, p->b, q_full);
+                    });
+                }
+                __syncwarp();
+                return true;
+            };
             int block0 = 0;
             if (tensor_copies && cw >= 2) {
-                // Two warps for the queries,
+                // Two warps for the queries, or one thread where a tile's rows
+                // are a box of whole tokens,
                 for (int ip = 0;; ++ip) {
                     bool ok;
                     const TreePart* p = part(ip, ok);
                     if (!ok || p->n < 0) break;
-                    if (p->n > 0) ok = load_q(p, cw - 2, 2);
+                    if (p->n > 0) {
+                        if (!t.tensor_q) ok = load_q(p, cw - 2, 2);
+                        else if (cw == 2) ok = fetch_q(p);
+                    }
                     if (!ok) break;
                     done_with(ip);
+                }
+                if (t.tensor_q && cw == 2 && *limit.abort_flag) {
+                    for (int phase = 0; phase < 2; ++phase)
+                        mbar_wait<false>(q_full, phase, t.wait_limit_cycles / 8);
+                    __syncwarp();
                 }
             } else if (tensor_copies) {
                 // one for the keys and one for the values: a lane a box.
@@ -1177,13 +1215,14 @@ cudaError_t launch(TreeTask t, int slot, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Tensor copies take boxes of one page: the rows of the largest power of two
     // that divides the page and the block, 8 (a swizzled atom) at least.
-    CUtensorMap map_k{}, map_v{};
+    CUtensorMap map_k{}, map_v{}, map_q{};
     t.box_bits = 0;
     while ((t.page_size >> t.box_bits & 1) == 0 && (1 << t.box_bits) < L::kBlk) ++t.box_bits;
     if (t.box_bits < 3 || t.num_pages == 0 ||
         !encode_pages_map(&map_k, t.k_pages, t, t.k_stride, 1 << t.box_bits) ||
         !encode_pages_map(&map_v, t.v_pages, t, t.v_stride, 1 << t.box_bits))
         t.box_bits = -1;
+    t.tensor_q = t.box_bits >= 0 && encode_queries_map(&map_q, t);
     t.skip = L::kBlk / t.page_size;
     t.rest = L::kBlk - t.skip * t.page_size;
     t.by_page = FastDiv(t.page_size);
@@ -1193,7 +1232,7 @@ cudaError_t launch(TreeTask t, int slot, cudaStream_t stream) {
     t.by_width = FastDiv(t.width);
     const int grid = (t.split ? t.groups : t.batch * t.bundles) * t.width;
     e = launch_shaped(kernel, {dim3(grid), kTrThreads, L::kBytes, stream, true, 1}, t, map_k,
-                      map_v);
+                      map_v, map_q);
     if (e != cudaSuccess || !t.split || t.groups == 1) return e;
     const int64_t units = static_cast<int64_t>(t.batch) * t.bundles;
     const bool cuts = units >= t.groups;

@@ -185,6 +185,31 @@ def test_strided_caches_queries_and_outputs():
     assert cs.get_error() == set()
 
 
+@pytest.mark.parametrize("H,Hk", [(8, 2), (6, 2), (128, 1), (4, 4)])
+def test_queries_in_other_layouts(H, Hk):
+    """Queries that tensor copies take (key heads of a power of two of query
+    heads) and others; expanded, token-major, one token or one head of more."""
+    q, k, v, table, lengths = cache([300, 77, 150], 5, H, Hk, 64, 16, seed=11)
+    args = (k, v, table, lengths)
+    want = check((q, *args))
+    q = q.cuda()     # (a copy to the device would straighten the strides)
+    for other in (
+            q.transpose(0, 1).contiguous().transpose(0, 1),
+            q.transpose(1, 2).contiguous().transpose(1, 2),
+            torch.nn.functional.pad(q, (8, 16, 1, 2, 3, 0))[:, 3:, 1:-2, 8:-16]):
+        assert not other.is_contiguous()
+        got = run((other, *args), return_lse=True)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    one = q[:1].expand(3, 5, H, 64)
+    got = run((one, *args), return_lse=True)
+    check((one.cpu().contiguous(), *args))
+    want = run((one.contiguous(), *args), return_lse=True)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    want = run((q[:, 4:].contiguous(), *args), return_lse=True)
+    got = run((q[:, 4:], *args), return_lse=True)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_offsets_past_32_bits():
     """Pages more than 2^32 elements apart, in both kinds of copies."""
     for page in (16, 3):
