@@ -353,15 +353,6 @@ __device__ __forceinline__ bool warp_wait2(uint64_t* a, int phase_a, uint64_t* b
     return ok;
 }
 
-// Elements d .. d + 7 of one row of the output, from unnormalised sums.
-template <class E>
-__device__ __forceinline__ void tree_store8(uint16_t* row, int d, const float (&acc)[8],
-                                            float inv) {
-    *reinterpret_cast<uint4*>(row + d) =
-        make_uint4(E::pack(acc[0] * inv, acc[1] * inv), E::pack(acc[2] * inv, acc[3] * inv),
-                   E::pack(acc[4] * inv, acc[5] * inv), E::pack(acc[6] * inv, acc[7] * inv));
-}
-
 __device__ __forceinline__ uint16_t* tree_out(const TreeTask& t, int b, int i, int h) {
     return t.out + b * t.o_stride[0] + i * t.o_stride[1] + h * t.o_stride[2];
 }
@@ -1101,12 +1092,19 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
 }
 
 constexpr int kTrJoinThreads = 128;
+constexpr int kTrJoinFew = 2;    // CTAs an SM with C 2, up to which it is 1
+constexpr int kTrJoinFull = 8;   // CTAs an SM with C 4, from which on it is 4
 
-// Joins a unit's parts: a CTA takes 32 rows, a lane each, and 32 columns.  A
-// small batch has CTAs for every unit, a larger one for every place between two
-// groups, where alone a unit can be cut, which join the unit that is cut there
-// first (CUTS).
-template <int BLK, class E, bool CUTS>
+// Joins a unit's parts: a CTA takes 32 rows, a lane each, and 16 C columns, 4 C a
+// thread.  A small batch has CTAs for every unit, a larger one for every place
+// between two groups, where alone a unit can be cut, which join the unit that is
+// cut there first (CUTS).  Bound by latency: eight loads of 16 bytes are under
+// way in a thread, of eight parts where there are few CTAs (C 1: 131072 tokens in
+// 19 parts, 91.5 us with the kernel before, with C 2 95, with 4 99), of four
+// columns where there are enough (C 4: two prompts' chunks of 512 over 8192
+// tokens, 2048 CTAs of 2 or 3 parts, 107.5, with C 2 110, with 1 120).  C 2 in
+// between: 8 x 64 over 8192, 65.0, with 1 71, with 4 65.4.
+template <int BLK, class E, bool CUTS, int C>
 __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTask t) {
     constexpr int kWarps = kTrJoinThreads / 32;
     __shared__ int scan[kWarps + 4];
@@ -1154,55 +1152,76 @@ __global__ void __launch_bounds__(kTrJoinThreads) tree_join_kernel(const TreeTas
     const int row = bundle * t.width + x;
     const int tile = row / t.kv_heads, hk = row - tile * t.kv_heads;
     const int r = 32 * (chunk % tiles) + lane;                 // of the unit
-    const int col = 4 * (chunk / tiles) + warp;                // of 8 elements
+    const int col = C * (kWarps * (chunk / tiles) + warp);     // of 4 elements
     const int r_all = tile * t.unit_rows + r;
-    if (8 * col >= t.d_head || r_all >= t.new_tokens * t.group || r >= t.unit_rows) return;
+    if (4 * col >= t.d_head || r_all >= t.new_tokens * t.group || r >= t.unit_rows) return;
     // Part i: the first begins the unit (see TreePart).
     auto place = [&](int i) {
         return static_cast<int64_t>(2 * ((c0 + i) * t.width + x) + (i == 0)) * t.part_rows;
     };
+    constexpr int kAtOnce = 8 / C;
     const int n = c1 - c0 + 1;
     float top = -INFINITY, sum = 0.0f;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < n; i0 += 4) {
-        float2 st[4];
-        float4 v[4][2];
+    float acc[C][4] = {};
+    for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+        float2 st[kAtOnce];
+        float4 v[kAtOnce][C];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kAtOnce; ++k) {
             st[k] = make_float2(0.0f, 0.0f);
-            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int y = 0; y < C; ++y) v[k][y] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i0 + k < n) {
                 const int64_t at = place(i0 + k);
                 st[k] = t.part_stats[at + r];
                 const float4* w = reinterpret_cast<const float4*>(t.part_out + at * t.d_head) +
-                                  2 * col * t.part_rows + r;
-                v[k][0] = w[0];
-                v[k][1] = w[t.part_rows];
+                                  col * t.part_rows + r;
+#pragma unroll
+                for (int y = 0; y < C; ++y)
+                    if (4 * (col + y) < t.d_head) v[k][y] = w[y * t.part_rows];
             }
         }
         float m = top;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kAtOnce; ++k)
             if (st[k].y != 0.0f) m = fmaxf(m, st[k].x);
         const float f = top == -INFINITY ? 0.0f : ex2(top - m);
         sum *= f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] *= f;
+        for (int y = 0; y < C; ++y)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+            for (int e = 0; e < 4; ++e) acc[y][e] *= f;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
             if (st[k].y == 0.0f) continue;   // no kept tokens there
             const float g = ex2(st[k].x - m);
             sum = fmaf(st[k].y, g, sum);
-            const float y[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
-                                v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(y[e], g, acc[e]);
+            for (int y = 0; y < C; ++y) {
+                acc[y][0] = fmaf(v[k][y].x, g, acc[y][0]);
+                acc[y][1] = fmaf(v[k][y].y, g, acc[y][1]);
+                acc[y][2] = fmaf(v[k][y].z, g, acc[y][2]);
+                acc[y][3] = fmaf(v[k][y].w, g, acc[y][3]);
+            }
         }
         top = m;
     }
     const int token = r_all / t.group, h = hk * t.group + r_all - token * t.group;
-    tree_store8<E>(tree_out(t, b, token, h), 8 * col, acc,
-                   sum == 0.0f ? 0.0f : __frcp_rn(sum));
+    uint16_t* to = tree_out(t, b, token, h) + 4 * col;
+    const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+    if constexpr (C == 1) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(E::pack(acc[0][0] * inv, acc[0][1] * inv),
+                                                    E::pack(acc[0][2] * inv, acc[0][3] * inv));
+    } else {
+#pragma unroll
+        for (int y = 0; y < C; y += 2)
+            if (4 * (col + y) < t.d_head)
+                *reinterpret_cast<uint4*>(to + 4 * y) = make_uint4(
+                    E::pack(acc[y][0] * inv, acc[y][1] * inv),
+                    E::pack(acc[y][2] * inv, acc[y][3] * inv),
+                    E::pack(acc[y + 1][0] * inv, acc[y + 1][1] * inv),
+                    E::pack(acc[y + 1][2] * inv, acc[y + 1][3] * inv));
+    }
     if (col == 0) tree_lse(t, b, token, h, top, sum);
 }
 
@@ -1236,12 +1255,23 @@ cudaError_t launch(TreeTask t, int slot, cudaStream_t stream) {
     if (e != cudaSuccess || !t.split || t.groups == 1) return e;
     const int64_t units = static_cast<int64_t>(t.batch) * t.bundles;
     const bool cuts = units >= t.groups;
-    const int chunks = t.part_rows / 32 * ((t.d_head + 31) / 32);
-    return launch_shaped(
-        cuts ? tree_join_kernel<L::kBlk, E, true> : tree_join_kernel<L::kBlk, E, false>,
-        {dim3(t.width * chunks, cuts ? t.groups - 1 : static_cast<unsigned>(units)),
-         kTrJoinThreads, 0, stream, true, 1},
-        t);
+    const unsigned joins = static_cast<unsigned>(cuts ? t.groups - 1 : units);
+    const int sms = t.groups * t.width;
+    auto ctas = [&](int c) {   // of a join
+        return t.width * (t.part_rows / 32) * ((t.d_head + 16 * c - 1) / (16 * c));
+    };
+    auto join = [&](auto kernel, int c) {
+        return launch_shaped(kernel, {dim3(ctas(c), joins), kTrJoinThreads, 0, stream, true, 1},
+                             t);
+    };
+    if (static_cast<int64_t>(joins) * ctas(2) <= kTrJoinFew * sms)
+        return join(cuts ? tree_join_kernel<L::kBlk, E, true, 1>
+                         : tree_join_kernel<L::kBlk, E, false, 1>, 1);
+    if (static_cast<int64_t>(joins) * ctas(4) >= kTrJoinFull * sms)
+        return join(cuts ? tree_join_kernel<L::kBlk, E, true, 4>
+                         : tree_join_kernel<L::kBlk, E, false, 4>, 4);
+    return join(cuts ? tree_join_kernel<L::kBlk, E, true, 2>
+                     : tree_join_kernel<L::kBlk, E, false, 2>, 2);
 }
 
 template <class E>

@@ -373,6 +373,23 @@ def test_many_sequences(batch):
                        lengths[some].cpu(), mask.cpu(), new[some].cpu()))
 
 
+@pytest.mark.parametrize("B,T,H,Hk,D,longest", [
+    (10, 256, 8, 8, 128, 1300),   # a join for each sequence, many rows,
+    (3, 40, 16, 4, 64, 2600),     # some,
+    (1, 5, 8, 4, 80, 5900),       # and few, of many parts;
+    (20, 256, 8, 8, 128, 1100),   # one for each place between two groups
+    (40, 9, 8, 2, 96, 1500),
+    (170, 1, 1, 1, 64, 900),
+])
+def test_joins(B, T, H, Hk, D, longest):
+    """Units that are cut, joined in each of the ways there are."""
+    gen = torch.Generator().manual_seed(B)
+    lengths = torch.randint(T, longest, (B,), generator=gen).tolist()
+    args = cache(lengths, T, H, Hk, D, 16, seed=B)
+    table = torch.nn.functional.pad(args[3], (0, 64))   # rows for 1024 more
+    check((*args[:3], table, args[4]), tree_mask(1, T, seed=B)[0])
+
+
 def test_repeated_calls_give_the_same_bits():
     for case in CASES:
         args = [x.cuda() for x in cache(*case, seed=9)]
