@@ -1,11 +1,12 @@
 // Device helpers shared by the fused attention kernels (k_fattn_fwd.cu,
-// k_fattn_bwd.cu) and the one over a paged cache (k_tree.cu): bounded waits of a warp, operand tiles in shared memory
-// and the products on them, kept keys, and row stores.
+// k_fattn_bwd.cu) and the one of several new tokens over a paged cache
+// (k_tree.cu): bounded waits of a warp, operand tiles in shared memory and the
+// products on them, kept keys, and row stores.
 //
-// Operand tiles.  R rows of DP (64, 128 or 256) bf16 or fp16, as the tensor copies write
-// them with 128-byte swizzling: DP / 64 panels of R rows x 128 bytes, head
-// elements past D and rows past the sequence filled with zeros.  The same
-// tile serves as a K-major operand (rows along M or N, the head along K:
+// Operand tiles.  R rows of DP (64, 128 or 256) bf16 or fp16, as the tensor
+// copies write them with 128-byte swizzling: DP / 64 panels of R rows x 128
+// bytes, head elements past D and rows past the sequence filled with zeros.  The
+// same tile serves as a K-major operand (rows along M or N, the head along K:
 // Q K^T) and, by its descriptor alone, as an MN-major one (the head along N,
 // rows along K: P V), so nothing is ever transposed.
 #pragma once

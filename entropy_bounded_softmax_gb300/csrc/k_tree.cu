@@ -25,9 +25,28 @@
 //   warp 8          issues the products (tcgen05, operands in shared memory,
 //                   weights in tensor memory);
 //   warp 9          works out the CTA's parts, a few ahead;
-//   warps 12-15     look pages up and keep the rings of K and V full by
-//                   asynchronous copies of 16 bytes, whatever a page's size and
-//                   its strides are; queries too.
+//   warps 12, 13    look pages up and keep the rings of K and V full by tensor
+//                   copies, a lane a box: the tokens of one page, 8 or more;
+//   warps 14, 15    queries, by a tensor copy of whole tokens where the query
+//                   heads of a key head divide 128, or 16 bytes at a time;
+//   warps 12-15     all of it 16 bytes at a time, where pages are not of a
+//                   multiple of 8 tokens or strides are none of a tensor map's
+//                   (131072 tokens: 122 us so, 99 by tensor copies).
+//
+// Measured, bf16, heads of 128, 32 on 8 key heads, GPU time of a call in a graph:
+//   1 x 32 tokens over 131072   91.5 us, 5.9 TB/s (87% of a plain copy), 0.75
+//                               PFLOP/s: DRAM, a block of 64 KB in 2750 cycles;
+//   32 x 16 over 256 .. 4096    39.2 us, 4.5 TB/s: as above, and 8 us until
+//                               the first pages are there (lengths, table and
+//                               copies one after the other), 3 us of join;
+//   8 x 64 over 8192            65.0 us, 4.3 TB/s and 1.05 PFLOP/s: a pair's block
+//                               takes 3120 cycles, of which the tensor pipe works
+//                               2048: a tile's chain (products, softmax, products)
+//                               is longer than the other tile's products, and its
+//                               256 columns leave no room for a second score tile;
+//   2 x 512 of 8192 (a chunk)   107.3 us, 1.24 PFLOP/s (65% of a library product):
+//                               the same; start and join take 15 us.
+// (Both chains are also fused_attention's.)
 //
 // The weights are rounded to the cache's type, the one the tensor cores take
 // beside its values; their sum is taken in fp32 before that.  They carry a
@@ -495,7 +514,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         if (t.mask && warp_valid && key + BLK > context)
                             tree_mask_row<BLK>(
                                 t.mask + p->b * t.mask_stride[0] + token * t.mask_stride[1],
-                                key - context, r < p->valid ? p->len - context : 0, p->len - context, kept);
+                                key - context, r < p->valid ? p->len - context : 0,
+                                p->len - context, kept);
                     }
                     ok = warp_wait(&s_full[tile], visit, limit);
                     if (!ok) break;
@@ -510,7 +530,8 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                         for (int w = 0; w < BLK / 32; ++w) every &= in[w];
                         if (every != ~0u || edge) {
 #pragma unroll
-                            for (int w = 0; w < BLK / 32; ++w) kept[w] = edge ? kept[w] & in[w] : in[w];
+                            for (int w = 0; w < BLK / 32; ++w)
+                                kept[w] = edge ? kept[w] & in[w] : in[w];
                             edge = true;
                         }
                         uint32_t s[BLK];

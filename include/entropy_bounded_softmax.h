@@ -846,8 +846,8 @@ typedef struct cs_tree_shape {
  * depends on the batch's lengths (repeated calls give the same bits).  NaN or
  * infinite scores propagate to their row and OR CS_ERR_NAN_INPUT; a NaN or
  * infinite value of a token may reach every row of its sequence and key head,
- * those that do not attend it too (0 times it is added).  Ownership, execution and errors: as
- * cs_constrained_softmax.
+ * those that do not attend it too (0 times it is added).  Ownership, execution
+ * and errors: as cs_constrained_softmax.
  */
 cs_status cs_paged_tree_attention(
     const uint16_t* query, const uint16_t* key_pages,
