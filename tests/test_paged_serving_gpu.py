@@ -201,3 +201,66 @@ def test_lengths_of_the_call_before(B, most):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         assert cs.get_error() <= {"OUT_OF_PAGES"}
+
+
+@pytest.mark.parametrize("B,T,page", [(3, 5, 16), (24, 4, 64), (2, 64, 5)])
+def test_captured_step(B, T, page):
+    """A step of drafts as one captured graph, its state updated in place, over
+    steps that take new pages; each as the same calls made one by one."""
+    D, dtype, steps = 128, torch.bfloat16, 12
+    gen = torch.Generator().manual_seed(B)
+    entries = (600 + steps * T) // page + 2
+    num = B * entries
+    start = torch.randint(0, 600, (B,), generator=gen).int()
+    pages = torch.randn(2, num, page, HK, D, generator=gen).to(dtype).cuda()
+    free = torch.randperm(num, generator=gen).int().cuda()
+    table = torch.full((B, entries), -1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    _, lengths, held, cursor = cs.paged_extend(table, zero, start.cuda(), free,
+                                               page, 600)
+    count = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, T, H, D, dtype=dtype, device="cuda")
+    k, v = (torch.zeros(B, T, HK, D, dtype=dtype, device="cuda")
+            for _ in range(2))
+    mask = torch.zeros(B, T, T, dtype=torch.bool, device="cuda")
+
+    def step(table, lengths, held, cursor, pages, wait=False):
+        def settle():
+            if wait:
+                torch.cuda.synchronize()
+        slots, totals, have, after = cs.paged_extend(
+            table, lengths, count, free, page, T, held=held, cursor=cursor)
+        settle()
+        cs.paged_write(k, v, slots, *pages)
+        settle()
+        out, lse = cs.paged_tree_attention(q, *pages, table, totals, mask,
+                                           count, return_lse=True)
+        settle()
+        return out, lse, totals, have, after
+
+    copies = [x.clone() for x in (table, lengths, held, cursor, pages)]
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step(*[x.clone() for x in copies])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse, totals, have, after = step(table, lengths, held, cursor,
+                                             pages)
+        lengths.copy_(totals)
+        held.copy_(have)
+        cursor.copy_(after)
+    for i in range(steps):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=gen))
+        mask.copy_(tree_mask(B, T, seed=i))
+        count.copy_(torch.randint(0, T + 1, (B,), generator=gen))
+        graph.replay()
+        want = step(*copies, wait=True)
+        for x, y in zip(copies[1:4], want[2:]):
+            x.copy_(y)
+        torch.cuda.synchronize()
+        for x, y in zip((out, lse, totals, have, after), want):
+            assert torch.equal(x, y)
+        assert torch.equal(table, copies[0]) and torch.equal(pages, copies[4])
+        assert cs.get_error() == set()
