@@ -501,8 +501,8 @@ struct TreeTask {
 };
 
 // What a part's start and end take, in blocks: counted when blocks are dealt (32
-// sequences of 256 to 4096 tokens, trees of 16: 43.2 us with 1, 41.5 with 2, 41.4
-// with 3, 41.9 with 4).
+// sequences of 256 to 4096 tokens, trees of 16: 40.2 us with 1, 39.3 with 2, 40.5
+// with 3; 8 x 64 over 8192: 66.4, 65.0, 64.8; 2 x 512 of 8192: 109.0, 109.2, 110.5).
 constexpr int kTreePartCost = 2;
 
 // Tokens of a block.
