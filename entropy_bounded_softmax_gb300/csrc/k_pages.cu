@@ -1,6 +1,7 @@
 // Pages and slots for new tokens of a paged key-value cache, and the write of
 // their keys and values.
 #include "cs_device.cuh"
+#include "cs_pages.h"
 
 namespace cs {
 namespace {
@@ -27,33 +28,9 @@ constexpr int kExThreads = 256;
 constexpr int kExSlots = 2048;
 constexpr int kExCtasPerSm = 4;
 
-struct Claim {
-    int len, fresh, held, need;   // as above; fresh and need 0 where `bad`
-    bool bad;
-};
-
-__device__ __forceinline__ int pages_of(uint32_t tokens, uint32_t page) {
-    return static_cast<int>(tokens / page + (tokens % page != 0));
-}
-
 __device__ __forceinline__ Claim claim_of(const ExtendTask& t, int b) {
-    Claim c;
-    c.len = t.lengths[b];
-    c.fresh = t.new_lengths[b];
-    c.bad = c.len < 0 || c.fresh < 0 || c.fresh > t.max_new;
-    c.held = t.held ? t.held[b] : c.len < 0 ? 0 : pages_of(c.len, t.page_size);
-    // Tokens without pages, or more pages than the row has entries.
-    c.bad = c.bad || c.held < 0 || c.held > t.max_pages ||
-            static_cast<int64_t>(c.held) * t.page_size < c.len;
-    if (c.bad) c.fresh = 0;
-    c.need = 0;
-    if (!c.bad) {
-        const uint32_t total = static_cast<uint32_t>(c.len) + static_cast<uint32_t>(c.fresh);
-        const int want = pages_of(total, t.page_size);
-        c.bad = want > t.max_pages;   // taken as far as the row goes
-        c.need = max(0, min(want, t.max_pages) - c.held);
-    }
-    return c;
+    return cs::claim_of(t.lengths[b], t.new_lengths[b], t.held != nullptr,
+                        t.held ? t.held[b] : 0, t.max_new, t.max_pages, t.page_size);
 }
 
 __global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) {
@@ -144,20 +121,26 @@ __global__ void __launch_bounds__(kExThreads) extend_kernel(const ExtendTask t) 
         long long* out = t.slots + static_cast<int64_t>(b0 + y) * t.max_new + i0;
         const int there = min(r.total - r.len - i0, span);   // places with a slot
         int i = threadIdx.x & (step - 1);
-        int entry = (r.len + i0 + i) / t.page_size;
-        int at = r.len + i0 + i - entry * t.page_size;
+        // (Places past the last slot may lie past 2^31; nothing is read there.)
+        const uint32_t place = static_cast<uint32_t>(r.len) + static_cast<uint32_t>(i0 + i);
+        const uint32_t size = t.page_size;
+        uint32_t entry = place / size;
+        uint32_t at = place - entry * size;
         while (i < span) {
-            int page[4], slot[4];
+            int page[4];
+            uint32_t slot[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 page[x] = -1;
                 slot[x] = at;
-                if (i + x * step < there)
-                    page[x] = entry < r.held ? table[entry] : fresh[entry - r.held];
+                if (i + x * step < there) {
+                    const int e = static_cast<int>(entry);
+                    page[x] = e < r.held ? table[e] : fresh[e - r.held];
+                }
                 entry += skip;
                 at += rest;
-                if (at >= t.page_size) {
-                    at -= t.page_size;
+                if (at >= size) {
+                    at -= size;
                     ++entry;
                 }
             }

@@ -1,0 +1,65 @@
+"""The whole-number arithmetic by which the operators around a paged cache find
+where they read and write, on the CPU, at the ends of what they accept."""
+import ctypes
+import itertools
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+
+CSRC = os.path.join(ROOT, "entropy_bounded_softmax_gb300", "csrc")
+MOST = 1 << 30       # tokens of a table's row, and new tokens of a sequence
+
+SHIM = """
+#include "cs_pages.h"
+extern "C" void claim(const int32_t* in, int32_t* out) {
+    const cs::Claim c = cs::claim_of(in[0], in[1], in[2] != 0, in[3], in[4], in[5], in[6]);
+    out[0] = c.len; out[1] = c.fresh; out[2] = c.held; out[3] = c.need; out[4] = c.bad;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def claim(tmp_path_factory):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    folder = tmp_path_factory.mktemp("pages")
+    source, library = folder / "shim.cpp", folder / "shim.so"
+    source.write_text(SHIM)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared",
+                    "-fPIC", "-I", CSRC, str(source), "-o", str(library)],
+                   check=True)
+    lib = ctypes.CDLL(str(library))
+
+    def call(*values):
+        given = (ctypes.c_int32 * 7)(*values)
+        out = (ctypes.c_int32 * 5)()
+        lib.claim(given, out)
+        return list(out)
+    return call
+
+
+@pytest.mark.parametrize("page,max_pages", [
+    (1, MOST), (1, MOST - 1), (2, MOST // 2), (16, MOST // 16), (3, 1000),
+    (MOST, 1), (1 << 20, 1024), (7, 0), (2 ** 31 - 1, 0)])
+def test_claims(claim, page, max_pages):
+    """The pages that a sequence is short of: never past its row."""
+    ends = [-2 ** 31, -1, 0, 1, 2, 15, 16, 17, MOST - 1, MOST, MOST + 1,
+            2 ** 31 - 1]
+    pages = sorted({-2 ** 31, -1, 0, 1, max_pages - 1, max_pages,
+                    max_pages + 1, 2 ** 31 - 1})
+    for n, w, held, max_new in itertools.product(
+            ends, ends, [None, *pages], (0, 16, MOST)):
+        got = claim(n, w, held is not None, held or 0, max_new, max_pages,
+                    page)
+        have = held if held is not None else -(-max(n, 0) // page)
+        out = (n < 0 or w < 0 or w > max_new or not 0 <= have <= max_pages
+               or have * page < n)
+        want = 0 if out else -(-(n + w) // page)
+        need = 0 if out else max(0, min(want, max_pages) - have)
+        assert got == [n, 0 if out else w, have, need,
+                       int(out or want > max_pages)], (n, w, held, max_new)
+        assert out or 0 <= have + need <= max_pages
