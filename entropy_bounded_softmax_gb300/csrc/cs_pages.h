@@ -49,4 +49,37 @@ CS_HOST_DEVICE Claim claim_of(int32_t len, int32_t fresh, bool given, int32_t he
     return c;
 }
 
+// A sequence's tokens, and how many of them are new.
+struct TreeLens {
+    int32_t len, fresh;
+};
+
+// The nearest in range of any two numbers; most: the tokens of a table's row.
+CS_HOST_DEVICE TreeLens tree_lens_of(int32_t len, int32_t fresh, int32_t most,
+                                     int32_t new_tokens) {
+    TreeLens x;
+    x.len = len < 0 ? 0 : len < most ? len : most;
+    const int32_t top = new_tokens < x.len ? new_tokens : x.len;
+    x.fresh = fresh < 0 ? 0 : fresh < top ? fresh : top;
+    return x;
+}
+
+// Where a group's share of a batch's list begins: place g0 lies in sequence b,
+// whose first place is base.
+struct TreeStart {
+    int32_t b, base;
+    TreeLens n;
+};
+
+// From what the walk that looks for it left in memory, which is anything where
+// the lengths were changed under the call and it found none.
+CS_HOST_DEVICE TreeStart tree_start_of(const int32_t* found, int32_t g0, int32_t batch,
+                                       int32_t most, int32_t new_tokens) {
+    TreeStart x;
+    x.b = found[0] < 0 ? 0 : found[0] < batch ? found[0] : batch - 1;
+    x.base = found[1] < 0 ? 0 : found[1] < g0 ? found[1] : g0;
+    x.n = tree_lens_of(found[2], found[3], most, new_tokens);
+    return x;
+}
+
 }  // namespace cs

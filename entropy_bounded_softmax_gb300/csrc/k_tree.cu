@@ -56,6 +56,7 @@
 #include <math.h>
 
 #include "cs_fattn.cuh"
+#include "cs_pages.h"
 #include "cs_tensormap.h"
 
 namespace cs {
@@ -120,17 +121,11 @@ struct TreePlan {
     static_assert(kStages + 2 <= kTrWords, "a block's words outlive its keys' stage");
 };
 
-// A sequence's tokens, and how many of them are new.
-struct TreeLens {
-    int len, fresh;
-};
 __device__ __forceinline__ TreeLens tree_lens(const TreeTask& t, int b, bool& bad) {
     const int n = t.lengths[b];
     const int most = t.max_pages * t.page_size;
     const int w = t.new_lengths ? t.new_lengths[b] : t.new_tokens;
-    TreeLens x;
-    x.len = n < 0 ? 0 : min(n, most);
-    x.fresh = min(max(w, 0), min(t.new_tokens, x.len));
+    const TreeLens x = tree_lens_of(n, w, most, t.new_tokens);
     bad = n < 0 || n > most || w != x.fresh;
     return x;
 }
@@ -229,10 +224,13 @@ __device__ __forceinline__ bool tree_deal(const TreeTask& t, int grp, int* scan,
         tree_sync<WARPS>();
         if (done > d.g0) break;
     }
-    // (In range even where the lengths were changed under the call.)
-    d.b = max(0, min(scan[WARPS], t.batch - 1));
-    d.base = min(scan[WARPS + 1], d.g0);
-    d.n = TreeLens{scan[WARPS + 2], scan[WARPS + 3]};
+    // (In range even where the lengths were changed under the call: what comes of
+    // them is then wrong, but no page table, row or part is left.)
+    const TreeStart x = tree_start_of(scan + WARPS, d.g0, t.batch, t.max_pages * t.page_size,
+                                      t.new_tokens);
+    d.b = x.b;
+    d.base = x.base;
+    d.n = x.n;
     return true;
 }
 

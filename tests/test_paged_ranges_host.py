@@ -19,11 +19,15 @@ extern "C" void claim(const int32_t* in, int32_t* out) {
     const cs::Claim c = cs::claim_of(in[0], in[1], in[2] != 0, in[3], in[4], in[5], in[6]);
     out[0] = c.len; out[1] = c.fresh; out[2] = c.held; out[3] = c.need; out[4] = c.bad;
 }
+extern "C" void start(const int32_t* in, int32_t* out) {
+    const cs::TreeStart x = cs::tree_start_of(in, in[4], in[5], in[6], in[7]);
+    out[0] = x.b; out[1] = x.base; out[2] = x.n.len; out[3] = x.n.fresh;
+}
 """
 
 
 @pytest.fixture(scope="module")
-def claim(tmp_path_factory):
+def library(tmp_path_factory):
     if shutil.which("g++") is None:
         pytest.skip("g++ not available")
     folder = tmp_path_factory.mktemp("pages")
@@ -32,20 +36,19 @@ def claim(tmp_path_factory):
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared",
                     "-fPIC", "-I", CSRC, str(source), "-o", str(library)],
                    check=True)
-    lib = ctypes.CDLL(str(library))
+    return ctypes.CDLL(str(library))
 
-    def call(*values):
-        given = (ctypes.c_int32 * 7)(*values)
-        out = (ctypes.c_int32 * 5)()
-        lib.claim(given, out)
-        return list(out)
-    return call
+
+def call(function, given, results):
+    out = (ctypes.c_int32 * results)()
+    function((ctypes.c_int32 * len(given))(*given), out)
+    return list(out)
 
 
 @pytest.mark.parametrize("page,max_pages", [
     (1, MOST), (1, MOST - 1), (2, MOST // 2), (16, MOST // 16), (3, 1000),
     (MOST, 1), (1 << 20, 1024), (7, 0), (2 ** 31 - 1, 0)])
-def test_claims(claim, page, max_pages):
+def test_claims(library, page, max_pages):
     """The pages that a sequence is short of: never past its row."""
     ends = [-2 ** 31, -1, 0, 1, 2, 15, 16, 17, MOST - 1, MOST, MOST + 1,
             2 ** 31 - 1]
@@ -53,8 +56,8 @@ def test_claims(claim, page, max_pages):
                     max_pages + 1, 2 ** 31 - 1})
     for n, w, held, max_new in itertools.product(
             ends, ends, [None, *pages], (0, 16, MOST)):
-        got = claim(n, w, held is not None, held or 0, max_new, max_pages,
-                    page)
+        got = call(library.claim, (n, w, held is not None, held or 0, max_new,
+                                   max_pages, page), 5)
         have = held if held is not None else -(-max(n, 0) // page)
         out = (n < 0 or w < 0 or w > max_new or not 0 <= have <= max_pages
                or have * page < n)
@@ -63,3 +66,20 @@ def test_claims(claim, page, max_pages):
         assert got == [n, 0 if out else w, have, need,
                        int(out or want > max_pages)], (n, w, held, max_new)
         assert out or 0 <= have + need <= max_pages
+
+
+@pytest.mark.parametrize("batch,most,T", [(33, 1280, 5), (65535, MOST, 1 << 20),
+                                          (513, 0, 4), (1, 16, 64)])
+def test_where_a_share_begins(library, batch, most, T):
+    """What paged_tree_attention's walk over the lengths left, which may be any
+    numbers where they were changed under it, in range; as it is where it is."""
+    ends = [-2 ** 31, -1, 0, 1, 2 ** 31 - 1]
+    for b, base, n, w, g0 in itertools.product(
+            [*ends, batch - 1, batch], [*ends, 1000], [*ends, most - 1, most],
+            [*ends, T, T + 1], (0, 1, 1000, MOST)):
+        got = call(library.start, (b, base, n, w, g0, batch, most, T), 4)
+        assert 0 <= got[0] < batch and 0 <= got[1] <= g0
+        assert 0 <= got[2] <= most and 0 <= got[3] <= min(T, got[2])
+        if (0 <= b < batch and 0 <= base <= g0 and 0 <= n <= most
+                and 0 <= w <= min(T, n)):
+            assert got == [b, base, n, w]
