@@ -123,11 +123,12 @@ _raw_stream = _current_device = None
 def _look_up() -> None:
     global _raw_stream, _current_device
     import torch
-    _raw_stream = getattr(
-        torch._C, "_cuda_getCurrentRawStream",
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _current_device = getattr(torch._C, "_cuda_getDevice",
-                              torch.cuda.current_device)
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                  lambda index: torch.cuda.current_stream(index).cuda_stream)
+    # The one that callers test comes last: other threads may be in them.
+    _current_device = device
+    _raw_stream = raw
 
 
 def _stream_handle(device) -> int:
