@@ -49,9 +49,13 @@
 // (Both chains are also fused_attention's.)
 //
 // The weights are rounded to the cache's type, the one the tensor cores take
-// beside its values; their sum is taken in fp32 before that.  They carry a
-// factor 2^8, and their maximum may lag by 2^6: fp16 has no exponents below
-// 2^-24, and the largest weight, 2^8 to 2^14, leaves 2^-32 of it.
+// beside its values; their sum is taken in fp32 before that.  Their maximum may
+// lag by 2^6.  In fp16, which has no exponents below 2^-24, they carry a factor
+// 2^8: the largest, 2^8 to 2^14, leaves 2^-32 of it.  In bf16, whose values reach
+// as far as fp32, they carry 2^-6 / n, n the sequence's tokens, up to a power of
+// two: the weights of any of them have a sum of at most 1, and no sum of weights
+// and finite values overflows (with 2^8, values from about 2^114 on could; a value
+// keeps bf16's bits down to n 2^-134).
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -69,20 +73,24 @@ constexpr int kTrMmaWarp = 8;
 constexpr int kTrPartWarp = 9;
 constexpr int kTrCopyWarp = 12;
 constexpr int kTrWarpBatch = 256;      // sequences whose lengths one warp adds up
-constexpr float kTrWeightBits = 8.0f;  // log2 of the weights' common factor
 constexpr float kTrLagBits = 6.0f;     // how far the maximum may lag
 constexpr int kTrWords = 8;            // blocks whose kept tokens are noted
 constexpr int kTrParts = 4;            // parts that are known ahead
 constexpr int kTrPartWarps = 13;       // that read them
 
+// weight_bits: log2 of the common factor of the weights of a sequence's tokens.
 struct TrBF16 {
     static constexpr bool kFp16 = false;
+    static __device__ __forceinline__ float weight_bits(int tokens) {
+        return -kTrLagBits - static_cast<float>(32 - __clz(tokens - 1));
+    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         return pack_bf16(lo, hi);
     }
 };
 struct TrFP16 {
     static constexpr bool kFp16 = true;
+    static __device__ __forceinline__ float weight_bits(int) { return 8.0f; }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -374,12 +382,12 @@ __device__ __forceinline__ uint16_t* tree_out(const TreeTask& t, int b, int i, i
     return t.out + b * t.o_stride[0] + i * t.o_stride[1] + h * t.o_stride[2];
 }
 
-// A row's lse, and whether its sum is finite, from the maximum in base 2.
+// A row's lse, and whether its sum is finite: weights are 2^(score - top).
 __device__ __forceinline__ void tree_lse(const TreeTask& t, int b, int i, int h, float top,
                                          float sum) {
     if (t.lse)
         t.lse[(static_cast<int64_t>(b) * t.new_tokens + i) * t.heads + h] =
-            sum == 0.0f ? -INFINITY : (top + log2f(sum) - kTrWeightBits) * kLn2;
+            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     if (!isfinite(sum)) raise_error(t.err, kBitNan);
 }
 
@@ -491,6 +499,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             const int n = p->n;
             if (n < 0) break;
             const int mine = NT == 1 && wg > 0 ? 0 : (n - first + kStep - 1) / kStep;
+            const float bits = E::weight_bits(p->len);
             float m = -INFINITY, l = 0.0f;
             if (mine > 0) {
                 const int context = p->context, token = t.by_group(p->r0 + r);
@@ -568,7 +577,7 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
                                 tmem_st16(to + x, w);
                             }
                         }
-                        const float mc = (m == -INFINITY ? 0.0f : m * c) - kTrWeightBits;
+                        const float mc = (m == -INFINITY ? 0.0f : m * c) - bits;
                         const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -595,9 +604,10 @@ tree_kernel(const TreeTask t, const __grid_constant__ CUtensorMap map_k,
             }
             block0 += n;
             if (r >= p->valid) l = 0.0f;
-            // The row's maximum (base 2) and sum, and the factors of the outputs
-            // in tensor memory: with one tile, both warpgroups' parts.
-            float top = m == -INFINITY ? 0.0f : m * c, sum = l;
+            // What the row's weights are relative to (base 2; mc above) and their
+            // sum, and the factors of the outputs in tensor memory: with one tile,
+            // both warpgroups' parts.
+            float top = (m == -INFINITY ? 0.0f : m * c) - bits, sum = l;
             float f0 = l == 0.0f ? 0.0f : 1.0f, f1 = 0.0f;
             if (NQ == 1) {
                 float2* stats = reinterpret_cast<float2*>(smem + L::kStats);

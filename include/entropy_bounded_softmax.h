@@ -843,10 +843,11 @@ typedef struct cs_tree_shape {
  * and page numbers out of range are taken as the nearest that is in range, or
  * left out, and OR CS_ERR_BAD_PAGE into the error word.  The weights are
  * rounded to the cache's type, their sums are fp32 in a fixed order, which
- * depends on the batch's lengths (repeated calls give the same bits).  NaN or
- * infinite scores propagate to their row and OR CS_ERR_NAN_INPUT; a NaN or
- * infinite value of a token may reach every row of its sequence and key head,
- * those that do not attend it too (0 times it is added).  Ownership, execution
+ * depends on the batch's lengths (repeated calls give the same bits).  Finite
+ * values of any magnitude give finite results.  NaN or infinite scores propagate
+ * to their row and OR CS_ERR_NAN_INPUT; a NaN or infinite value of a token may
+ * reach every row of its sequence and key head, those that do not attend it too
+ * (0 times it is added).  Ownership, execution
  * and errors: as cs_constrained_softmax.
  */
 cs_status cs_paged_tree_attention(
