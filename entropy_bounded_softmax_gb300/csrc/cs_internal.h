@@ -393,6 +393,7 @@ struct PagedTask {
     int32_t groups;            // kv_heads * head_tiles CTAs, this many
     int32_t fp16;
     float scale;
+    float weight_bits;         // log2 of the weights' common factor
 };
 
 constexpr int kPagedMaxDHead = 256;

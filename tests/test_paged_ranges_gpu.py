@@ -103,3 +103,38 @@ def test_tree_values_as_small_as_bf16_has(case):
     # The result's rounding, the weights', and as much again for the rest.
     assert ((out.cpu().double() - ref).abs() <= 4 * 2.0 ** -8 * ref.abs()).all()
     assert cs.get_error() == set()
+
+
+def one_token(q, k, v, table, lengths, scale):
+    """paged_attention of each sequence's last query, beside the definition of
+    a tree of one token."""
+    q = q[:, -1].contiguous()
+    out, lse = cs.paged_attention(
+        *(x.cuda() for x in (q, k, v, table, lengths)), scale=scale,
+        return_lse=True)
+    want = definition(q[:, None], k, v, table, lengths, scale=scale)
+    return (out[:, None], lse[:, None]), want
+
+
+@pytest.mark.parametrize("kind", ["flat", "peak"])
+@pytest.mark.parametrize("case", SPREAD, ids=str)
+def test_paged_attention_values_as_large_as_bf16_has(case, kind):
+    *args, scale = spread(case, kind)
+    top = torch.finfo(torch.bfloat16).max
+    args[2] = ((0.5 + 0.5 * args[2].float().abs().clamp(max=1))
+               * top).bfloat16()
+    within(*one_token(*args, scale))
+    assert cs.get_error() == set()
+
+
+@pytest.mark.parametrize("case", SPREAD, ids=str)
+def test_paged_attention_values_as_small_as_bf16_has(case):
+    """As for trees, n the 2^13 tokens of a table's row at most: an fp32 step is
+    2^-13 of the smallest products."""
+    *args, scale = spread(case, "flat")
+    args[2] = ((1 + args[2].float().abs().clamp(max=1))
+               * 2.0 ** -117).bfloat16()
+    (out, _), want = one_token(*args, scale)
+    assert ((out.cpu().double() - want[0]).abs()
+            <= 4 * 2.0 ** -8 * want[0].abs()).all()
+    assert cs.get_error() == set()
