@@ -845,10 +845,11 @@ typedef struct cs_tree_shape {
  * left out, and OR CS_ERR_BAD_PAGE into the error word.  The weights are
  * rounded to the cache's type, their sums are fp32 in a fixed order, which
  * depends on the batch's lengths (repeated calls give the same bits).  Finite
- * values of any magnitude give finite results.  NaN or infinite scores propagate
- * to their row and OR CS_ERR_NAN_INPUT; a NaN or infinite value of a token may
- * reach every row of its sequence and key head, those that do not attend it too
- * (0 times it is added).  Ownership, execution
+ * values of any magnitude give finite results.  An lse beyond
+ * 2^128 / log2(e) = 2.36e38 of either sign is given as that.  NaN or infinite
+ * products query . key propagate to their row and OR CS_ERR_NAN_INPUT; a NaN or
+ * infinite value of a token may reach every row of its sequence and key head,
+ * those that do not attend it too (0 times it is added).  Ownership, execution
  * and errors: as cs_constrained_softmax.
  */
 cs_status cs_paged_tree_attention(

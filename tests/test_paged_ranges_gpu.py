@@ -1,4 +1,6 @@
 """The operators around a paged cache at the ends of what they accept."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -138,3 +140,71 @@ def test_paged_attention_values_as_small_as_bf16_has(case):
     assert ((out.cpu().double() - want[0]).abs()
             <= 4 * 2.0 ** -8 * want[0].abs()).all()
     assert cs.get_error() == set()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -119, 2.0 ** -104, 2.0 ** -95,
+                                   2.0 ** -40, 1.0, 1.9, 4.0])
+@pytest.mark.parametrize("case", [
+    ([5], 3, 4, 4, 8, 16, 0), ([300, 9], 3, 4, 2, 8, 16, 0),
+    ([2000, 40], 3, 4, 2, 72, 16, 64), ([2000], 40, 16, 4, 8, 5, 64),
+    ([900], 3, 2, 1, 136, 16, 64)], ids=str)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_tree_large_scores(case, scale, sign):
+    """One score of 1.875 * 2^126 * scale, the row's others 0, or one of 0, the
+    others that far below it: it takes the row; lse stays in fp32.  Other rows
+    are as ever."""
+    *sizes, more = case
+    q, k, v, table, lengths = cache(*sizes, seed=6)
+    table = torch.nn.functional.pad(table, (0, more))
+    T, H, Hk = sizes[1:4]
+    j, i = int(lengths[0]) // 2, T - 1
+    q[:], k[:] = 0, 0
+    q[0, i, 1, 0] = 1.5 * 2.0 ** 63
+    at = int(table[0, j // k.shape[1]]), j % k.shape[1], Hk // H   # of head 1
+    if sign < 0:
+        k[..., 0] = -1.25 * 2.0 ** 63
+        k[at][0] = 0
+    else:
+        k[at][0] = 1.25 * 2.0 ** 63
+    out, lse = (x.cpu() for x in cs.paged_tree_attention(
+        *(x.cuda() for x in (q, k, v, table, lengths)), scale=scale,
+        return_lse=True))
+    hit = torch.zeros(lse.shape, dtype=torch.bool)
+    hit[0, i, 1] = True
+    assert cs.get_error() == set()
+    # One weight, which its sum takes away again, to fp32 (the others, 240 or
+    # more below the maximum, are less than 2^-126).
+    assert torch.equal(out[0, i, 1], v[at])
+    score = min(1.875 * 2.0 ** 126 * scale, 2.0 ** 128 * math.log(2))
+    score = score if sign > 0 else 0.0
+    assert abs(float(lse[0, i, 1]) - score) <= 2.0 ** -21 * max(1, score)
+    ref, tol, wlse, tlse = definition(q * 0, k * 0, v, table, lengths)
+    assert ((out.double() - ref).abs() <= tol)[~hit].all()
+    assert ((lse.double() - wlse).abs() <= tlse)[~hit].all()
+
+
+@pytest.mark.parametrize("T,D,page", [(3, 64, 16), (40, 128, 5), (2, 200, 16)])
+def test_tree_all_scores_far_below_zero(T, D, page):
+    """Rows whose scores are all about -2^40, one of them the largest: the same
+    as without what all have in common."""
+    q, k, v, table, lengths = cache([1500, 90], T, 8, 2, D, page, seed=7)
+    table = torch.nn.functional.pad(table, (0, 64))
+    q[:], k[:] = 0, 0
+    q[..., 0], k[..., 0] = 2.0 ** 20, -2.0 ** 20
+    for b, n in enumerate(lengths.tolist()):
+        for j in (0, n // 2):
+            at = int(table[b, j // page]), j % page
+            k[at][..., 0] = -2.0 ** 20 + 2.0 ** 12
+    out, lse = cs.paged_tree_attention(
+        *(x.cuda() for x in (q, k, v, table, lengths)), scale=1.0,
+        return_lse=True)
+    assert cs.get_error() == set()
+    for b, n in enumerate(lengths.tolist()):
+        rows = [v[int(table[b, j // page]), j % page] for j in (0, n // 2)]
+        want = (rows[0].double() + rows[1].double()) / 2
+        want = want.repeat_interleave(4, 0)
+        # (Half a step of the result, and as much for fp32's.)
+        assert ((out[b].cpu().double() - want).abs()
+                <= 2.0 ** -8 * want.abs() + 2.0 ** -16).all()
+    score = -2.0 ** 40 + 2.0 ** 32
+    assert ((lse.cpu().double() - score).abs() <= 2.0 ** -21 * 2.0 ** 40).all()
