@@ -977,10 +977,11 @@ def _tree_ok(torch, query, key_pages, value_pages, page_table, lengths, mask,
         return False
     if mask is not None:
         if not (isinstance(mask, t) and mask.dtype is torch.bool
-                and mask.get_device() == dev and mask.stride(-1) == 1):
+                and mask.get_device() == dev):
             return False
         ms, n = mask.shape, qs[1]
-        if ms != (qs[0], n, n) and ms != (n, n):
+        if ((ms != (qs[0], n, n) and ms != (n, n))
+                or mask.stride(-1) != 1):
             return False
     return ((new_lengths is None or (
                 isinstance(new_lengths, t) and new_lengths.dtype is i32
