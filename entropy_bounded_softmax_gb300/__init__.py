@@ -927,10 +927,9 @@ def _check_tree(query, key_pages, value_pages, page_table, lengths, mask,
     if query.dim() != 4:
         raise ValueError("query must be 4-D [batch, new_tokens, heads, d_head]")
     B, T, H, D = query.shape
-    if T > 0:
-        # One token's arguments are those of paged_attention.
-        _check_paged(query[:, 0], key_pages, value_pages, page_table, lengths,
-                     scale, None)
+    # One token's arguments are those of paged_attention.
+    _check_paged(query[:, 0] if T > 0 else query.new_empty((B, H, D)),
+                 key_pages, value_pages, page_table, lengths, scale, None)
     if query.numel():
         _check_rows("query", query, query.dtype, query.shape, query.device)
     if out is not None:

@@ -31,3 +31,14 @@ def test_masks_of_other_shapes(args, shape):
     mask = torch.ones(shape, dtype=torch.bool, device="cuda")
     with pytest.raises(ValueError, match="mask must be"):
         cs.paged_tree_attention(**args, mask=mask)
+
+
+@pytest.mark.parametrize("T", [0, 3])
+@pytest.mark.parametrize("bad", [
+    dict(key_pages=None), dict(key_pages=3), dict(value_pages=[1]),
+    dict(page_table=None), dict(lengths=None), dict(lengths=7)], ids=str)
+def test_arguments_of_other_types(args, T, bad):
+    """Also where there is no new token, so that nothing is looked at."""
+    args["query"] = args["query"][:, :T]
+    with pytest.raises(ValueError):
+        cs.paged_tree_attention(**{**args, **bad})
