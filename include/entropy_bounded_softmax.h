@@ -859,9 +859,11 @@ cs_status cs_paged_tree_attention(
     uint16_t* out, float* lse, const cs_tree_shape* shape, void* workspace,
     int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace the call needs (0 where no row of the table holds more
- * than 512 tokens, 1024 in some batches; half of that for d_head above 128);
- * negative for a malformed shape.  Host-only. */
+/* Bytes of workspace the call needs; negative for a malformed shape.  Host-only.
+ * The rows (new token, query head) of a key head make units of 128, or of 256
+ * where they are more than 128 and d_head is at most 128.  0 where the batch has
+ * at most 152 units and no row of the table holds more than 512 tokens, or than
+ * 1024 where it has at least 114 (256 and 512 for d_head above 128). */
 int64_t cs_paged_tree_attention_workspace(const cs_tree_shape* shape);
 
 /* Host-only argument check (no CUDA call). */

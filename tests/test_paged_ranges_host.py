@@ -8,6 +8,7 @@ import subprocess
 
 import pytest
 
+import entropy_bounded_softmax_gb300 as cs
 from conftest import ROOT
 
 CSRC = os.path.join(ROOT, "entropy_bounded_softmax_gb300", "csrc")
@@ -83,3 +84,26 @@ def test_where_a_share_begins(library, batch, most, T):
         if (0 <= b < batch and 0 <= base <= g0 and 0 <= n <= most
                 and 0 <= w <= min(T, n)):
             assert got == [b, base, n, w]
+
+
+@pytest.mark.parametrize("D", [64, 128, 136])
+@pytest.mark.parametrize("T,H,Hk", [(1, 1, 1), (5, 8, 2), (32, 32, 8),
+                                    (33, 32, 8), (65, 32, 8), (100, 6, 3)])
+def test_what_needs_no_workspace(D, T, H, Hk):
+    """The header's rule: units of the batch against the tokens of a row."""
+    rows = T * (H // Hk)
+    size = 256 if rows > 128 and D <= 128 else 128
+    strides = (ctypes.c_int64 * 3)(T * H * D, H * D, D)
+    full = 512 if D <= 128 else 256
+    for B, most in itertools.product(
+            (1, 2, 3, 13, 18, 19, 37, 38, 56, 57, 76, 77, 113, 114, 152, 153,
+             300),
+            (1, full // 16, full // 16 + 1, full // 8, full // 8 + 1, 1000)):
+        units = B * Hk * -(-rows // size)
+        shape = cs.cs_tree_shape(B, T, H, Hk, D, 16, 100, most, 0, 0.125,
+                                 strides, strides, strides, strides, most,
+                                 (0, T))
+        whole = units <= 152 and 16 * most <= (2 * full if units >= 114
+                                               else full)
+        assert (cs.cs_paged_tree_attention_workspace(shape) == 0) == whole, \
+            (B, most)
