@@ -1010,10 +1010,10 @@ def paged_tree_attention(query, key_pages, value_pages, page_table, lengths,
     for rows from ``new_lengths[b]`` on and for rows that attend nothing, and
     with ``return_lse`` the log of the softmax's sums [B, T, H] in fp32.
     Asynchronous on the current stream; lengths and page numbers out of range
-    are left out and reported by :func:`get_error`, and so are NaN or infinite
-    scores, which propagate (a NaN among a sequence's values may reach all of
-    its rows).  For serving: there is no backward pass, and the result carries
-    no gradient.
+    are left out and reported by :func:`get_error`; NaN and +infinite scores
+    propagate and are reported too, tokens with a score of -infinity count as
+    removed, and a NaN or infinite value may reach all rows of its sequence.
+    For serving: there is no backward pass, and the result carries no gradient.
     """
     import torch
     given = (query, key_pages, value_pages, page_table, lengths, mask,

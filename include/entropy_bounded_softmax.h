@@ -846,10 +846,12 @@ typedef struct cs_tree_shape {
  * rounded to the cache's type, their sums are fp32 in a fixed order, which
  * depends on the batch's lengths (repeated calls give the same bits).  Finite
  * values of any magnitude give finite results.  An lse beyond
- * 2^128 / log2(e) = 2.36e38 of either sign is given as that.  NaN or infinite
- * products query . key propagate to their row and OR CS_ERR_NAN_INPUT; a NaN or
- * infinite value of a token may reach every row of its sequence and key head,
- * those that do not attend it too (0 times it is added).  Ownership, execution
+ * 2^128 / log2(e) = 2.36e38 of either sign is given as that.  A product
+ * query . key of a kept token that is NaN or +infinite propagates to its row and
+ * ORs CS_ERR_NAN_INPUT; a token with one of -infinity counts as removed (a row of
+ * no others gets zeros and lse = -inf).  A NaN or infinite value of a token may
+ * reach every row of its sequence and key head, those that do not attend it too
+ * (0 times it is added).  Ownership, execution
  * and errors: as cs_constrained_softmax.
  */
 cs_status cs_paged_tree_attention(

@@ -208,3 +208,51 @@ def test_tree_all_scores_far_below_zero(T, D, page):
                 <= 2.0 ** -8 * want.abs() + 2.0 ** -16).all()
     score = -2.0 ** 40 + 2.0 ** 32
     assert ((lse.cpu().double() - score).abs() <= 2.0 ** -21 * 2.0 ** 40).all()
+
+
+@pytest.mark.parametrize("wide", [0, 64])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 5), (256, 64)])
+def test_tree_infinite_scores(D, page, wide):
+    """A score of +infinity makes its row NaN and is reported; a token with one
+    of -infinity counts as removed, also where a row has no other."""
+    T, j = 6, 700 - 6 + 4
+    args = cache([700, 6], T, 4, 2, D, page, seed=8)
+    q, k, v, table, lengths = args
+    table = torch.nn.functional.pad(table, (0, wide))
+    mask = tree_mask(2, T, seed=3)
+    mask[0, :, 4] = False
+    mask[0, 4, 4] = True                      # new token 4: row 4 alone
+    mask[1] = torch.eye(T, dtype=torch.bool)  # each itself alone
+    q[..., 5] = q[..., 5].abs() + 0.5
+    for b, at in ((0, j), (1, 4)):
+        k[int(table[b, at // page]), at % page, 1, 5] = math.inf
+    hit = torch.zeros(2, T, 4, dtype=torch.bool)
+    hit[:, 4, 2:] = True
+    for sign in (1, -1):
+        out, lse = cs.paged_tree_attention(
+            *(x.cuda() for x in (sign * q, k, v, table, lengths)),
+            mask=mask.cuda(), return_lse=True)
+        out, lse = out.cpu(), lse.cpu()
+        assert cs.get_error() == ({"NAN_INPUT"} if sign > 0 else set())
+        # What the rows would be without the token, which in `k` is out of
+        # reach of a product with 0.
+        kk = k.clone()
+        kk[kk.isinf()] = 0
+        gone = mask.clone()
+        gone[:, 4, 4] = False
+        a = definition(sign * q, kk, v, table, lengths, mask)
+        z = definition(sign * q, kk, v, table, lengths, gone)
+        ref, tol, wlse, tlse = (torch.where(
+            hit if x.dim() == 3 else hit[..., None], y, x)
+            for x, y in zip(a, z))
+        sound = ~hit if sign > 0 else torch.ones_like(hit)
+        assert ((out.double() - ref).abs() <= tol)[sound].all()
+        empty = wlse == -math.inf
+        assert empty[1, 4, 2:].all() and empty.sum() == 2
+        assert torch.equal(lse[sound] == -math.inf, empty[sound])
+        some = sound & ~empty
+        assert ((lse.double() - wlse).abs() <= tlse)[some].all()
+        if sign > 0:
+            assert out[hit].isnan().all() and lse[hit].isnan().all()
+        else:
+            assert (out[1, 4, 2:] == 0).all()
