@@ -773,8 +773,10 @@ def paged_extend(page_table, lengths, new_lengths, free_pages, page_size: int,
     Nothing else changes; the results are new tensors, to be handed to the next
     call.  Asynchronous on the current stream.  Where the list runs out,
     sequences get what is left in their order, tokens without a page have slot
-    -1 and are not in ``totals``; that and arguments out of range, which are
-    left out, are reported by :func:`get_error`.
+    -1 and are not in ``totals`` (``totals - lengths`` are the new tokens that
+    :func:`paged_tree_attention` finds there, its ``new_lengths``); that and
+    arguments out of range, which are left out, are reported by
+    :func:`get_error`.
     """
     import torch
     t, i32 = torch.Tensor, torch.int32
@@ -1008,7 +1010,10 @@ def paged_tree_attention(query, key_pages, value_pages, page_table, lengths,
     (for a tree: its ancestors and itself); without a mask those with j <= i.
     ``scale`` defaults to 1/sqrt(D).  Returns [B, T, H, D] (or ``out``), zeros
     for rows from ``new_lengths[b]`` on and for rows that attend nothing, and
-    with ``return_lse`` the log of the softmax's sums [B, T, H] in fp32.
+    with ``return_lse`` the log of the softmax's sums [B, T, H] in fp32.  The
+    weights are rounded to the cache's type (:func:`paged_attention` holds them
+    in two halves: its errors are about two thirds of these); their sums are
+    fp32.
     Asynchronous on the current stream; lengths and page numbers out of range
     are left out and reported by :func:`get_error`; NaN and +infinite scores
     propagate and are reported too, tokens with a score of -infinity count as
