@@ -805,7 +805,7 @@ TreePlan tree_plan(const cs_tree_shape& s, int sms) {
     // least three quarters of the SMs.  Blocks of 128, cut and whole, on the GPU
     // (a call from the host takes 5 us less whole): 1 x 512 tokens, 8 units, 10.6
     // and 10.6 us; 16 x 1024, 128 units, 16.4 and 15.2, 4 x 1024 12.7 and 14.5;
-    // 7 x 1531, 84 units, 15.5 and 19.4; 256 x 512, 2048 units, 83 and 115.
+    // 7 x 1531, 84 units, 15.5 and 19.4; 256 x 512, 2048 units, 85 and 115.
     // (The workspace's size goes by this too, and knows no device: so the SMs
     // are a GB300's.)
     const int64_t steps = tree_steps(s), total = steps * s.batch * (p.units / p.width);

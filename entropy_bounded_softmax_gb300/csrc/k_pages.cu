@@ -23,7 +23,8 @@ using namespace csd;
 // the free list where another CTA writes them into the table.  On the GPU: one
 // token for each of 32 sequences 2.7 us, trees of up to 61 for 256 of them 3.1,
 // 512 prompts of up to 4096 tokens, 17 MB of slots, 9.3 (1.8 TB/s: the needs
-// before a CTA and the three trips, then the slots).
+// before a CTA and the three trips, about 3, and then the instructions of a slot, a
+// lookup, a wide multiplication and a store of 8 bytes: the ALU pipe is 51% busy).
 constexpr int kExThreads = 256;
 constexpr int kExSlots = 2048;
 constexpr int kExCtasPerSm = 4;

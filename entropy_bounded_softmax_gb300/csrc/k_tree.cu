@@ -36,15 +36,15 @@
 // Measured, bf16, heads of 128, 32 on 8 key heads, GPU time of a call in a graph:
 //   1 x 32 tokens over 131072   91.5 us, 5.9 TB/s (87% of a plain copy), 0.75
 //                               PFLOP/s: DRAM, a block of 64 KB in 2750 cycles;
-//   32 x 16 over 256 .. 4096    39.2 us, 4.5 TB/s: as above, and 8 us until
+//   32 x 16 over 256 .. 4096    40.0 us, 4.4 TB/s: as above, and 8 us until
 //                               the first pages are there (lengths, table and
 //                               copies one after the other), 3 us of join;
-//   8 x 64 over 8192            65.0 us, 4.3 TB/s and 1.05 PFLOP/s: a pair's block
+//   8 x 64 over 8192            65.2 us, 4.2 TB/s and 1.05 PFLOP/s: a pair's block
 //                               takes 3120 cycles, of which the tensor pipe works
 //                               2048: a tile's chain (products, softmax, products)
 //                               is longer than the other tile's products, and its
 //                               256 columns leave no room for a second score tile;
-//   2 x 512 of 8192 (a chunk)   107.3 us, 1.24 PFLOP/s (65% of a library product):
+//   2 x 512 of 8192 (a chunk)   106.5 us, 1.25 PFLOP/s (66% of a library product):
 //                               the same; start and join take 15 us.
 // (Both chains are also fused_attention's.)
 //
@@ -78,7 +78,7 @@ constexpr float kTrLagBits = 6.0f;     // how far the maximum may lag
 // Above this, fma(s, c, -m c) of the maximum itself, which is what rounding m c
 // took off, is no longer a small number (from 2^31 on 2^x overflows, or leaves no
 // weight): the maximum is taken off the scores first.  (256 x 512 tokens in trees of
-// 4: 102 us without that code, 105 with it; others within 1%.)
+// 4: 82.5 us without that code, 85.0 with it; others within 1%.)
 constexpr float kTrLarge = 0x1p22f;
 constexpr int kTrWords = 8;            // blocks whose kept tokens are noted
 constexpr int kTrParts = 4;            // parts that are known ahead
