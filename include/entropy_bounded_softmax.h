@@ -657,8 +657,9 @@ typedef struct cs_paged_shape {
  * left out; both OR CS_ERR_BAD_PAGE into the error word.  Sums are fp32 in a
  * fixed order, which depends on the batch's lengths (repeated calls give the
  * same bits, whatever else runs).  Finite values of any magnitude give finite
- * results.  NaN or infinite scores propagate by IEEE arithmetic and OR
- * CS_ERR_NAN_INPUT into the error word.  Ownership, execution and errors: as
+ * results (where scores are below 2^20: beyond, values from 2^122 / n on may
+ * overflow, n the tokens).  NaN or infinite scores propagate by IEEE arithmetic
+ * and OR CS_ERR_NAN_INPUT into the error word.  Ownership, execution and errors: as
  * cs_constrained_softmax.
  */
 cs_status cs_paged_attention(const uint16_t* query, const uint16_t* key_pages,
